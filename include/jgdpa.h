@@ -85,7 +85,9 @@ typedef enum {
     JGDPA_ERR_WORKSPACE_TOO_SMALL = 4,  /* workspace (or the no-alloc array) too small for the sizes */
     JGDPA_ERR_CUDA = 5,               /* a CUDA runtime call or launch failed */
     JGDPA_ERR_BAD_OFFSETS = 6,        /* device-detected: offsets not monotone / wrong ends */
-    JGDPA_ERR_DEVICE_TIMEOUT = 7      /* device-detected: an internal wait gave up */
+    JGDPA_ERR_DEVICE_TIMEOUT = 7,     /* device-detected: an internal wait gave up */
+    JGDPA_ERR_OUT_OF_PAGES = 8,       /* device-detected: the pool has too few free pages */
+    JGDPA_ERR_BAD_PAGE = 9            /* device-detected: a block table entry outside the cache */
 } jgdpa_status;
 
 /*
@@ -271,6 +273,120 @@ JGDPA_API jgdpa_status jgdpa_bwd_shared_q(const void* q, int32_t n_shared, const
                                           void* workspace, size_t workspace_bytes,
                                           void* ds_scratch, size_t ds_scratch_bytes, jgdpa_stream_t stream,
                                           void* const* pass_events);
+
+/*
+ * Paged key/value cache: attention from a few new tokens per request over the
+ * keys and values that earlier calls left in GPU memory (serving, without
+ * gradients).  The computation is that of jgdpa_fwd_ex -- the same act, scale,
+ * bias table, window and softmax mode -- with these segments:
+ *
+ *  - A page holds page_size (a power of two, 16 to 1024) consecutive tokens of
+ *    one request, bf16 [page_size][kv_heads][head_dim]; the cache is num_pages
+ *    of them, page_stride elements apart (at least a page, a multiple of 8:
+ *    the cache may be one layer's or one half's slice of a larger pool).
+ *    Token j of request b lies in page block_table[b][j / page_size], place
+ *    j % page_size; slot = page * page_size + place.
+ *  - Request b has kv_lens[b] tokens.  The last T_b = q_offsets[b + 1] -
+ *    q_offsets[b] of them are this step's new tokens (their keys and values
+ *    already in the cache), the C_b = kv_lens[b] - T_b before them its context.
+ *  - Requests per call: at most 16384.  Rows of q, slots and outputs behind
+ *    q_offsets[batch] (a padded batch) are allowed and left as they were.
+ */
+
+/*
+ * Hands out pages and slots for a step's tokens, on the GPU.  For request b:
+ *   ctx_lens[b]    tokens it keeps (what earlier steps left, or fewer: drafted
+ *                  tokens that were not accepted; 0 for a new or ended request)
+ *   new_lens[b]    tokens it adds
+ *   held_pages[b]  pages it holds, the first entries of its table row
+ * It comes to want_b = ceil((ctx + new) / page_size) pages: the pages
+ * block_table[b][want .. held) go back to the pool, or block_table[b][held ..
+ * want) are taken from it.  free_pages[0 .. free_count[0]) is the stack of free
+ * pages (capacity num_pages).  All returned pages go onto it first, in (request,
+ * page) order, then pages are taken off its top in the same order; the result
+ * is the same on every run.
+ *   block_table    int32 [batch][table_width], updated in place (the entries
+ *                  taken; the others are left as they were)
+ *   free_pages     int32 [num_pages], updated in place (the entries above the
+ *                  old count that hold returned pages)
+ *   free_count     int32 [1]; the new count goes to free_count_out [1]
+ *   held_out       int32 [batch], the new page counts want_b
+ *   q_offsets      int32 [batch + 1], kv_lens int32 [batch]: for
+ *                  jgdpa_cache_fwd
+ *   slots          int32 [total_new], the slot of each new token in request
+ *                  order; -1 in rows behind the last
+ * held_out, kv_lens and free_count_out must not overlap the inputs.  The same
+ * call on the same inputs may be repeated: it writes the same values.
+ * Device-detected errors: BAD_OFFSETS (negative lengths, more tokens than
+ * table_width pages or total_new rows hold, counts beyond num_pages),
+ * OUT_OF_PAGES.  Such a call hands out nothing: table and stack are not
+ * touched, held_out, free_count_out and kv_lens are the old counts and
+ * ctx_lens, q_offsets is all 0 and slots all -1, so that an append and an
+ * attention call that follow on the stream do nothing.  A page id outside
+ * [0, num_pages) gives slot -1.
+ * The workspace (jgdpa_cache_plan_workspace_bytes()) holds the status word.
+ */
+JGDPA_API size_t jgdpa_cache_plan_workspace_bytes(void);
+JGDPA_API jgdpa_status jgdpa_cache_plan(const int32_t* ctx_lens, const int32_t* new_lens, const int32_t* held_pages,
+                                        int32_t batch, int32_t page_size, int32_t* block_table, int32_t table_width,
+                                        int32_t* free_pages, int32_t num_pages, const int32_t* free_count,
+                                        int32_t total_new, int32_t* held_out, int32_t* free_count_out,
+                                        int32_t* q_offsets, int32_t* kv_lens, int32_t* slots,
+                                        void* workspace, size_t workspace_bytes, jgdpa_stream_t stream);
+
+/*
+ * Writes new keys and values into the cache: row r of k_new and v_new (bf16,
+ * [kv_heads][head_dim], rows k_stride / v_stride elements apart, multiples of
+ * 8) to slot slots[r]; rows whose slot is negative or beyond the cache are
+ * skipped.  Rows of one call must have different slots, and k_new / v_new must
+ * not overlap the cache.  After a tree of drafted tokens was checked, the same
+ * call moves the accepted ones to their places: k_new and v_new once more, with
+ * the accepted rows' new slots and -1 for the others.
+ */
+JGDPA_API jgdpa_status jgdpa_cache_append(const void* k_new, const void* v_new, int64_t k_stride, int64_t v_stride,
+                                          const int32_t* slots, int32_t total_new, void* k_cache, void* v_cache,
+                                          int64_t k_page_stride, int64_t v_page_stride, int32_t num_pages,
+                                          int32_t page_size, int32_t kv_heads, int32_t head_dim,
+                                          jgdpa_stream_t stream);
+
+/*
+ * Attention from the new tokens over each request's pages.
+ *   q            bf16 rows [heads][head_dim], q_stride elements apart (a
+ *                multiple of 8); row q_offsets[b] + t is new token t of request
+ *                b.  heads is a multiple of kv_heads; query head h reads
+ *                key/value head h / (heads / kv_heads)
+ *   max_q        an upper bound of every T_b, known to the host
+ *   tree_mask    NULL: new token t sees new tokens u <= t.  Otherwise int32
+ *                [total_q][mask_words]: bit u % 32 of word u / 32 of its row
+ *                says whether it sees new token u of its request (itself
+ *                included); T_b must be at most 32 mask_words
+ *   depths       NULL or int32 [total_q], >= 0: new token t is at position
+ *                C + depths (C + t without), and context token j at j; the bias
+ *                index is clamp(pos_i - pos_j, -R, R) + R and a window w > 0
+ *                keeps pairs with |pos_i - pos_j| < w
+ *   act, scale, bias_table, bias_len   as in jgdpa_fwd, bias_table [heads]
+ *   out          bf16 [total_q][heads][head_dim]
+ *   lse          fp32 [heads][total_q] in SOFTMAX mode, or NULL; NULL otherwise
+ * Every token sees the whole context (within the window).  A token that sees
+ * nothing gets O = 0 (LSE = -inf).  Infinities and NaN in the cache reach only
+ * the rows that see their token; places of a page behind kv_lens[b] may hold
+ * anything.  Same bits on every run, whatever else runs beside it.
+ * Device-detected errors: BAD_OFFSETS (offsets not monotone from 0, beyond
+ * total_q, T_b > max_q, kv_lens[b] < T_b or beyond the table), in which case
+ * nothing is written; BAD_PAGE (a table entry of a live token outside
+ * [0, num_pages)): no such page is read, and its request's outputs are
+ * unspecified.
+ */
+JGDPA_API size_t jgdpa_cache_fwd_workspace_bytes(int32_t heads, int32_t kv_heads, int32_t head_dim, int32_t max_q);
+JGDPA_API jgdpa_status jgdpa_cache_fwd(const void* q, int64_t q_stride, const void* k_cache, const void* v_cache,
+                                       int64_t k_page_stride, int64_t v_page_stride, int32_t num_pages,
+                                       int32_t page_size, const int32_t* block_table, int32_t table_width,
+                                       const int32_t* q_offsets, const int32_t* kv_lens, int32_t batch,
+                                       int64_t total_q, int32_t max_q, int32_t heads, int32_t kv_heads,
+                                       int32_t head_dim, jgdpa_act act, float scale, const float* bias_table,
+                                       int32_t bias_len, int32_t window, const int32_t* tree_mask, int32_t mask_words,
+                                       const int32_t* depths, void* out, float* lse,
+                                       void* workspace, size_t workspace_bytes, jgdpa_stream_t stream);
 
 /*
  * Forward pass without a caller-provided workspace: the same computation and

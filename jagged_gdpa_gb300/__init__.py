@@ -12,6 +12,11 @@ from ._lib import (  # noqa: F401
     JgdpaError,
     jgdpa_bwd,
     jgdpa_bwd_shared_q,
+    jgdpa_cache_append,
+    jgdpa_cache_fwd,
+    jgdpa_cache_fwd_workspace_bytes,
+    jgdpa_cache_plan,
+    jgdpa_cache_plan_workspace_bytes,
     jgdpa_fwd_shared_q,
     jgdpa_shared_q_workspace_bytes,
     jgdpa_ds_scratch_bytes,

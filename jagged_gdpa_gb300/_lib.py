@@ -9,6 +9,7 @@ import fails loudly -- there is no fallback implementation.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from typing import Optional
 
@@ -23,12 +24,15 @@ ACT = {"gelu": 0, "silu": 1, "softmax": 2}
 STATUS = {
     0: "JGDPA_OK", 1: "JGDPA_ERR_INVALID_ARGUMENT", 2: "JGDPA_ERR_UNSUPPORTED",
     3: "JGDPA_ERR_MISALIGNED", 4: "JGDPA_ERR_WORKSPACE_TOO_SMALL", 5: "JGDPA_ERR_CUDA",
-    6: "JGDPA_ERR_BAD_OFFSETS", 7: "JGDPA_ERR_DEVICE_TIMEOUT",
+    6: "JGDPA_ERR_BAD_OFFSETS", 7: "JGDPA_ERR_DEVICE_TIMEOUT", 8: "JGDPA_ERR_OUT_OF_PAGES",
+    9: "JGDPA_ERR_BAD_PAGE",
 }
 EXPORTS = ("jgdpa_workspace_bytes", "jgdpa_fwd", "jgdpa_fwd_ex", "jgdpa_bwd", "jgdpa_bwd_ex",
            "jgdpa_ds_scratch_bytes",
            "jgdpa_read_device_status", "jgdpa_status_string", "jgdpa_eval_activation", "jgdpa_fwd_noalloc",
-           "jgdpa_set_wait_limit_ns", "jgdpa_shared_q_workspace_bytes", "jgdpa_fwd_shared_q", "jgdpa_bwd_shared_q")
+           "jgdpa_set_wait_limit_ns", "jgdpa_shared_q_workspace_bytes", "jgdpa_fwd_shared_q", "jgdpa_bwd_shared_q",
+           "jgdpa_cache_plan_workspace_bytes", "jgdpa_cache_plan", "jgdpa_cache_append",
+           "jgdpa_cache_fwd_workspace_bytes", "jgdpa_cache_fwd")
 
 
 class JgdpaError(RuntimeError):
@@ -83,6 +87,17 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.jgdpa_bwd_shared_q.argtypes = [P, i32, P, P, P, P, P, P, i32, i64, i32, i32, ctypes.c_int, f32, P, i32,
                                        i32, i32, P, P, P, P, P, sz, P, sz, P, P]
     lib.jgdpa_bwd_shared_q.restype = ctypes.c_int
+    lib.jgdpa_cache_plan_workspace_bytes.argtypes = []
+    lib.jgdpa_cache_plan_workspace_bytes.restype = sz
+    lib.jgdpa_cache_plan.argtypes = [P, P, P, i32, i32, P, i32, P, i32, P, i32, P, P, P, P, P, P, sz, P]
+    lib.jgdpa_cache_plan.restype = ctypes.c_int
+    lib.jgdpa_cache_append.argtypes = [P, P, i64, i64, P, i32, P, P, i64, i64, i32, i32, i32, i32, P]
+    lib.jgdpa_cache_append.restype = ctypes.c_int
+    lib.jgdpa_cache_fwd_workspace_bytes.argtypes = [i32, i32, i32, i32]
+    lib.jgdpa_cache_fwd_workspace_bytes.restype = sz
+    lib.jgdpa_cache_fwd.argtypes = [P, i64, P, P, i64, i64, i32, i32, P, i32, P, P, i32, i64, i32, i32, i32, i32,
+                                    ctypes.c_int, f32, P, i32, i32, P, i32, P, P, P, P, sz, P]
+    lib.jgdpa_cache_fwd.restype = ctypes.c_int
     _libs[path] = lib
     return lib
 
@@ -408,3 +423,196 @@ def jgdpa_bwd_shared_q(q, k, v, out, lse, dout, kv_offsets, act, scale: float, b
                                 _events(pass_events))
     _rc(rc, "jgdpa_bwd_shared_q")
     return dq, dk, dv, dbias
+
+
+# ------------------------------------------------- paged key/value cache (serving)
+def _on_device(fn):
+    """Runs a cache wrapper with its tensors' device as the current one."""
+    @functools.wraps(fn)
+    def call(*args, **kw):
+        first = args[0] if args else next(iter(kw.values()), None)
+        if isinstance(first, torch.Tensor) and first.is_cuda and first.device.index != torch.cuda.current_device():
+            with torch.cuda.device(first.device):
+                return fn(*args, **kw)
+        return fn(*args, **kw)
+    return call
+
+
+class _Alloc:
+    """Memory for results and scratch of a call on `stream` (None: the current
+    stream, whose allocations need nothing more).  Scratch comes from the
+    stream's own pool, so that it is not handed out again before the call's
+    kernels have run; results are known to the current stream too."""
+
+    def __init__(self, device, stream):
+        self.device = device
+        self.other = stream if stream is not None and stream != torch.cuda.current_stream(device) else None
+
+    def __call__(self, shape, dtype, result=True):
+        if self.other is None:
+            return torch.empty(shape, dtype=dtype, device=self.device)
+        with torch.cuda.stream(self.other):
+            t = torch.empty(shape, dtype=dtype, device=self.device)
+        if result:
+            t.record_stream(torch.cuda.current_stream(self.device))
+        return t
+
+
+def _need_cuda(t: torch.Tensor):
+    if not t.is_cuda:
+        raise ValueError("tensors passed to libjgdpa must be on a CUDA device")
+
+
+def _check_cache(k_cache, v_cache):
+    """(num_pages, page_size, kv_heads, head_dim) of a cache whose pages are
+    contiguous (their distance may be any multiple of 8 elements)."""
+    if not isinstance(k_cache, torch.Tensor) or k_cache.dim() != 4:
+        raise ValueError("k_cache must be a bf16 tensor [num_pages, page_size, kv_heads, head_dim]")
+    _check(k_cache, "k_cache", torch.bfloat16, (None, None, None, None))
+    _check(v_cache, "v_cache", torch.bfloat16, k_cache.shape, k_cache.device)
+    n, page, heads, d = k_cache.shape
+    for t, name in ((k_cache, "k_cache"), (v_cache, "v_cache")):
+        if t.stride()[1:] != (heads * d, d, 1):
+            raise ValueError(f"{name}: the tokens, heads and columns of a page must be contiguous")
+        if n > 1 and (t.stride(0) < page * heads * d or t.stride(0) % 8):
+            raise ValueError(f"{name}: pages must not overlap and lie a multiple of 8 elements apart")
+    return n, page, heads, d
+
+
+def _page_stride(t: torch.Tensor) -> int:
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2] * t.shape[3]
+
+
+def _row_stride(t: torch.Tensor, name: str) -> int:
+    """Elements between rows [heads][head_dim] of t (contiguous inside a row)."""
+    rows, heads, d = t.shape
+    if rows <= 1:
+        if rows and (t.stride(2) != 1 or (heads > 1 and t.stride(1) != d)):
+            raise ValueError(f"{name}: the heads and columns of a row must be contiguous")
+        return heads * d
+    if t.stride(2) != 1 or (heads > 1 and t.stride(1) != d) or t.stride(0) < heads * d or t.stride(0) % 8:
+        raise ValueError(f"{name}: rows must be contiguous inside and lie a multiple of 8 elements apart")
+    return t.stride(0)
+
+
+def _addr(t: Optional[torch.Tensor]):
+    return None if t is None else t.data_ptr()
+
+
+def _contiguous(**tensors):
+    for name, t in tensors.items():
+        if t is not None and not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+
+
+def jgdpa_cache_plan_workspace_bytes(lib=None) -> int:
+    return int((lib or load()).jgdpa_cache_plan_workspace_bytes())
+
+
+@_on_device
+def jgdpa_cache_plan(ctx_lens, new_lens, held_pages, block_table, free_pages, free_count, page_size: int,
+                     total_new: int, workspace=None, stream=None, lib=None):
+    """Pages and slots for a step's tokens (jgdpa_cache_plan); returns (slots,
+    q_offsets, kv_lens, held_pages, free_count), the last two being the new
+    counts to pass to the next plan.  block_table and free_pages are updated in
+    place.  total_new: rows of slots, at least the sum of new_lens."""
+    lib = lib or load()
+    _check(ctx_lens, "ctx_lens", torch.int32, (None,))
+    device, batch = ctx_lens.device, ctx_lens.shape[0]
+    _check(new_lens, "new_lens", torch.int32, (batch,), device)
+    _check(held_pages, "held_pages", torch.int32, (batch,), device)
+    _check(block_table, "block_table", torch.int32, (batch, None), device)
+    _check(free_pages, "free_pages", torch.int32, (None,), device)
+    _check(free_count, "free_count", torch.int32, (1,), device)
+    _check_bytes(workspace, "workspace", device)
+    total_new = int(total_new)
+    if total_new < 0:
+        raise ValueError("total_new must not be negative")
+    _contiguous(ctx_lens=ctx_lens, new_lens=new_lens, held_pages=held_pages, block_table=block_table,
+                free_pages=free_pages, workspace=workspace)
+    _need_cuda(ctx_lens)
+    alloc = _Alloc(device, stream)
+    ws = alloc(jgdpa_cache_plan_workspace_bytes(lib), torch.uint8, result=False) if workspace is None else workspace
+    ints = alloc(total_new + 3 * batch + 2, torch.int32)
+    slots, q_offsets, kv_lens, held, count = ints.split((total_new, batch + 1, batch, batch, 1))
+    rc = lib.jgdpa_cache_plan(_addr(ctx_lens), _addr(new_lens), _addr(held_pages), batch, int(page_size),
+                              _addr(block_table), block_table.shape[1], _addr(free_pages), free_pages.shape[0],
+                              _addr(free_count), total_new, _addr(held), _addr(count), _addr(q_offsets),
+                              _addr(kv_lens), _addr(slots), _addr(ws), ws.numel(), _stream(stream))
+    _rc(rc, "jgdpa_cache_plan")
+    return slots, q_offsets, kv_lens, held, count
+
+
+@_on_device
+def jgdpa_cache_append(k_new, v_new, slots, k_cache, v_cache, stream=None, lib=None):
+    """Writes rows of k_new / v_new [total_new, kv_heads, head_dim] (rows may be
+    slices of wider ones) to their slots; returns (k_cache, v_cache)."""
+    lib = lib or load()
+    n, page, heads, d = _check_cache(k_cache, v_cache)
+    device = k_cache.device
+    _check(k_new, "k_new", torch.bfloat16, (None, heads, d), device)
+    rows = k_new.shape[0]
+    _check(v_new, "v_new", torch.bfloat16, (rows, heads, d), device)
+    _check(slots, "slots", torch.int32, (rows,), device)
+    ks, vs = _row_stride(k_new, "k_new"), _row_stride(v_new, "v_new")
+    _contiguous(slots=slots)
+    _need_cuda(k_cache)
+    rc = lib.jgdpa_cache_append(_addr(k_new), _addr(v_new), ks, vs, _addr(slots), rows, _addr(k_cache),
+                                _addr(v_cache), _page_stride(k_cache), _page_stride(v_cache), n, page, heads, d,
+                                _stream(stream))
+    _rc(rc, "jgdpa_cache_append")
+    return k_cache, v_cache
+
+
+def jgdpa_cache_fwd_workspace_bytes(heads: int, kv_heads: int, head_dim: int, max_q: int, lib=None) -> int:
+    return int((lib or load()).jgdpa_cache_fwd_workspace_bytes(heads, kv_heads, head_dim, max_q))
+
+
+@_on_device
+def jgdpa_cache_fwd(q, k_cache, v_cache, block_table, q_offsets, kv_lens, act, scale: float, max_q: int,
+                    bias_table=None, window: int = 0, tree_mask=None, depths=None, out=None, lse=None,
+                    workspace=None, stream=None, lib=None):
+    """Attention from new tokens q [total_q, heads, head_dim] over each
+    request's pages (jgdpa_cache_fwd); returns (out, lse) with lse None unless
+    act == 'softmax'.  max_q: an upper bound of the new tokens per request."""
+    lib = lib or load()
+    n, page, kv_heads, d = _check_cache(k_cache, v_cache)
+    device = k_cache.device
+    _check(q, "q", torch.bfloat16, (None, None, d), device)
+    total_q, heads = q.shape[0], q.shape[1]
+    _check(kv_lens, "kv_lens", torch.int32, (None,), device)
+    batch = kv_lens.shape[0]
+    _check(q_offsets, "q_offsets", torch.int32, (batch + 1,), device)
+    _check(block_table, "block_table", torch.int32, (batch, None), device)
+    _check(bias_table, "bias_table", torch.float32, (heads, None), device, optional=True)
+    _check(tree_mask, "tree_mask", torch.int32, (total_q, None), device, optional=True)
+    _check(depths, "depths", torch.int32, (total_q,), device, optional=True)
+    a = _act(act)
+    softmax = a == ACT["softmax"]
+    _check(out, "out", torch.bfloat16, (total_q, heads, d), device, optional=True)
+    if lse is not None and not softmax:
+        raise ValueError("lse is written in softmax mode only; pass None")
+    _check(lse, "lse", torch.float32, (heads, total_q), device, optional=True)
+    _check_bytes(workspace, "workspace", device)
+    qs = _row_stride(q, "q")
+    _contiguous(block_table=block_table, q_offsets=q_offsets, kv_lens=kv_lens, bias_table=bias_table,
+                tree_mask=tree_mask, depths=depths, out=out, lse=lse, workspace=workspace)
+    _need_cuda(k_cache)
+    max_q, window = int(max_q), int(window)
+    alloc = _Alloc(device, stream)
+    if out is None:
+        out = alloc((total_q, heads, d), torch.bfloat16)
+    if lse is None and softmax:
+        lse = alloc((heads, total_q), torch.float32)
+    if workspace is None:
+        nbytes = lib.jgdpa_cache_fwd_workspace_bytes(heads, kv_heads, d, max_q)
+        workspace = alloc(max(nbytes, 256), torch.uint8, result=False)
+    rc = lib.jgdpa_cache_fwd(_addr(q), qs, _addr(k_cache), _addr(v_cache), _page_stride(k_cache),
+                             _page_stride(v_cache), n, page, _addr(block_table), block_table.shape[1],
+                             _addr(q_offsets), _addr(kv_lens), batch, total_q, max_q, heads, kv_heads, d, a,
+                             float(scale), _addr(bias_table), 0 if bias_table is None else bias_table.shape[1],
+                             window, _addr(tree_mask), 0 if tree_mask is None else tree_mask.shape[1],
+                             _addr(depths), _addr(out), _addr(lse), _addr(workspace), workspace.numel(),
+                             _stream(stream))
+    _rc(rc, "jgdpa_cache_fwd")
+    return out, lse

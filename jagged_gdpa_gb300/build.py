@@ -1,7 +1,7 @@
 """Builds libjgdpa.so in-tree (jagged_gdpa_gb300/_build/) with nvcc for sm_103a.
 
-The forward and backward sources are compiled once per head dimension
-(-DJGDPA_HEAD_DIM=32/64/128), and every object is compiled in parallel, then
+The forward, backward and cache attention sources are compiled once per head
+dimension (-DJGDPA_HEAD_DIM=32/64/128), and every object is compiled in parallel, then
 linked into one shared library with the CUDA runtime linked statically, so
 the library loads on a machine without a GPU driver (the CUDA calls fail
 there, the symbols are still present).
@@ -28,9 +28,11 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(BUILD, "libjgdpa.so")
 HEAD_DIMS = (32, 64, 128)
-SOURCES = ["api.cu", "sched.cu"]                 # compiled once
-PER_DIM_SOURCES = ["fwd.cu", "fwd_shortq.cu", "bwd.cu", "bwd_shortq.cu"]  # compiled once per head dimension
-HEADERS = ["act.cuh", "common.cuh", "ptx.cuh"]
+SOURCES = ["api.cu", "sched.cu", "cache_api.cu", "cache_plan.cu"]  # compiled once
+# compiled once per head dimension, shared by both libraries
+PER_DIM_SHARED_SOURCES = ["cache_fwd.cu"]
+PER_DIM_SOURCES = ["fwd.cu", "fwd_shortq.cu", "bwd.cu", "bwd_shortq.cu"]  # compiled once per head dimension and library
+HEADERS = ["act.cuh", "cache.cuh", "common.cuh", "host.h", "ptx.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
          "--expt-relaxed-constexpr"]
@@ -70,6 +72,14 @@ def _compile_jobs(cc: str, force: bool):
             objs[v].append(obj)
         if force or _stale(obj, src):
             jobs.append([cc, *ARCH, *FLAGS, "-c", src, "-o", obj])
+    for s in PER_DIM_SHARED_SOURCES:
+        src = os.path.join(CSRC, s)
+        for d in HEAD_DIMS:
+            obj = os.path.join(BUILD, s.replace(".cu", f"_d{d}.o"))
+            for v in VARIANTS:
+                objs[v].append(obj)
+            if force or _stale(obj, src):
+                jobs.append([cc, *ARCH, *FLAGS, f"-DJGDPA_HEAD_DIM={d}", "-c", src, "-o", obj])
     for v, vflags in VARIANTS.items():
         out_dir = BUILD if v is None else os.path.join(BUILD, v)
         os.makedirs(out_dir, exist_ok=True)

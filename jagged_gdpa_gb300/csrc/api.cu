@@ -13,6 +13,7 @@
 #include "../../include/jgdpa.h"
 #include "act.cuh"
 #include "common.cuh"
+#include "host.h"
 #include "ptx.cuh"
 
 namespace jg {
@@ -120,9 +121,7 @@ int sm_count() {
 
 // cuTensorMapEncodeTiled through the runtime's driver entry point (no link
 // dependency on libcuda).
-using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                              const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                              CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+using jg::EncodeFn;
 EncodeFn encode_fn() {
   static std::once_flag once;
   static EncodeFn fn = nullptr;
@@ -428,6 +427,12 @@ jgdpa_status run_sched(const int32_t* q_off, const int32_t* kv_off, int32_t batc
 }
 
 }  // namespace
+
+namespace jg {
+int host_sm_count() { return sm_count(); }
+unsigned long long host_wait_limit_ns() { return wait_limit_ns(); }
+EncodeFn host_encode_fn() { return encode_fn(); }
+}  // namespace jg
 
 extern "C" {
 
@@ -811,6 +816,8 @@ const char* jgdpa_status_string(jgdpa_status s) {
     case JGDPA_ERR_CUDA: return "CUDA error";
     case JGDPA_ERR_BAD_OFFSETS: return "bad offsets (device-detected)";
     case JGDPA_ERR_DEVICE_TIMEOUT: return "device wait timed out";
+    case JGDPA_ERR_OUT_OF_PAGES: return "out of pages (device-detected)";
+    case JGDPA_ERR_BAD_PAGE: return "bad page in the block table (device-detected)";
   }
   return "unknown status";
 }

@@ -1,0 +1,259 @@
+// Parameters, work division and small helpers of the paged key/value cache
+// kernels (cache_plan.cu, cache_fwd.cu, cache_fwd_wide.cu, cache_api.cu).
+#pragma once
+
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "common.cuh"
+#include "ptx.cuh"
+
+namespace jg {
+
+// Status codes of the cache calls (same values as jgdpa_status).
+enum : int { kErrOutOfPages = 8, kErrBadPage = 9 };
+
+constexpr int kCacheMaxBatch = 16384;  // requests per call (the plan's prefix sums live in shared memory)
+
+struct CachePlanParams {
+  const int32_t* ctx;
+  const int32_t* add;
+  const int32_t* held;
+  int32_t batch, page_shift, width, pool, total;
+  int32_t* table;
+  int32_t* free_pages;
+  const int32_t* free_count;
+  int32_t* held_out;
+  int32_t* free_count_out;
+  int32_t* q_off;
+  int32_t* kv_lens;
+  int32_t* slots;
+  int* status;
+};
+
+struct CacheAppendParams {
+  const __nv_bfloat16* k;
+  const __nv_bfloat16* v;
+  int64_t k_stride, v_stride;  // elements from one new row to the next
+  const int32_t* slots;
+  int32_t rows, chunks;        // chunks: 16-byte pieces of a row
+  __nv_bfloat16* k_cache;
+  __nv_bfloat16* v_cache;
+  int64_t k_page_stride, v_page_stride;  // elements from one page to the next
+  int32_t page_shift;
+  int32_t slot_end;            // num_pages * page_size
+};
+
+// The item that a CTA's range of key tiles starts inside of, written for the
+// joining kernel: valid only from the first CTA that continues an item.
+struct CacheJoin {
+  int32_t valid, b, h, rt;
+  int64_t t0, t1;  // the item's tiles in the global order
+  int64_t per;     // tiles per CTA
+};
+
+struct CacheFwdParams {
+  CUtensorMap tm_k;
+  CUtensorMap tm_v;
+  const __nv_bfloat16* q;
+  int64_t q_stride;          // elements from one query row to the next
+  const int32_t* table;      // [batch][width]
+  const int32_t* q_off;
+  const int32_t* kv_lens;
+  const float* bias;         // [heads][bias_len] or nullptr
+  const int32_t* mask;       // [total_q][mask_words] or nullptr
+  const int32_t* depth;      // [total_q] or nullptr
+  __nv_bfloat16* out;        // [total_q][heads][D]
+  float* lse;                // [heads][total_q] or nullptr
+  float* part_o;             // [2 grid][rows per tile][D]
+  float2* part_ml;           // [2 grid][rows per tile]: running maximum (log2 units) and sum
+  CacheJoin* join;           // [grid]
+  int* err;                  // [grid]: one status word per CTA, joined into `status`
+  int* status;
+  int64_t total_q;
+  int32_t batch, max_q, heads, kv_heads, group;
+  int32_t page_shift, width, num_pages;
+  int32_t mask_words, bias_len, window;
+  int32_t rows_per_tile;     // query rows (token, head of the group) of one item
+  float scale;               // s (GELU / SiLU) or s log2(e) (softmax)
+  unsigned long long wait_limit_ns;
+};
+
+// One request: its tokens, cached context and the key tiles its items visit.
+struct CacheReq {
+  int q0, T, L, C;
+  int kt0, n;  // first key tile and tiles of every item
+  int rt;      // row tiles
+};
+
+template <int KT>
+__device__ __forceinline__ CacheReq cache_req(const CacheFwdParams& p, int b) {
+  CacheReq r;
+  r.q0 = __ldg(p.q_off + b);
+  r.T = __ldg(p.q_off + b + 1) - r.q0;
+  r.L = __ldg(p.kv_lens + b);
+  r.C = r.L - r.T;
+  // new tokens sit at positions >= C, so no cached key at or below C - window is seen
+  r.kt0 = p.window > 0 ? max(0, r.C - p.window + 1) / KT : 0;
+  r.n = static_cast<int>((static_cast<int64_t>(r.L) + KT - 1) / KT) - r.kt0;
+  r.rt = static_cast<int>((static_cast<int64_t>(r.T) * p.group + p.rows_per_tile - 1) / p.rows_per_tile);
+  return r;
+}
+__device__ __forceinline__ int64_t cache_cost(const CacheFwdParams& p, const CacheReq& r) {
+  return r.T <= 0 ? 0 : static_cast<int64_t>(p.kv_heads) * r.rt * r.n;
+}
+__device__ __forceinline__ bool cache_req_ok(const CacheFwdParams& p, const CacheReq& r) {
+  return r.T >= 0 && r.T <= p.max_q && r.L >= r.T &&
+         static_cast<int64_t>(r.L) <= static_cast<int64_t>(p.width) << p.page_shift &&
+         (p.mask == nullptr || r.T <= 32 * p.mask_words);
+}
+
+// Work division.  The items are (request, kv head, row tile), each of n key
+// tiles; laid end to end (request by request, row tiles of one head next to
+// each other so that they meet in L2) their tiles form one line that is cut
+// into equal ranges, one per CTA, whatever the lengths.  An item cut by a
+// range border is finished by the joining kernel.
+struct CacheRange {
+  int64_t total, per, begin, end;
+  int b;        // request that `begin` lies in
+  int64_t rem;  // begin minus the request's first tile
+  bool ok;
+};
+struct CacheRangeShared {
+  int64_t warp_sum[32];
+  int64_t rem;
+  int b;
+};
+
+// Run by every thread of the CTA (a whole number of warps, at most 1024).
+template <int KT>
+__device__ CacheRange cache_range(const CacheFwdParams& p, CacheRangeShared* sh, int min_tiles) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nt = blockDim.x, nw = nt >> 5;
+  const int each = (p.batch + nt - 1) / nt;
+  const int b0 = min(tid * each, p.batch), b1 = min(b0 + each, p.batch);
+  int64_t sum = 0;
+  bool ok = true;
+  if (tid == 0) ok = __ldg(p.q_off) == 0 && static_cast<int64_t>(__ldg(p.q_off + p.batch)) <= p.total_q;
+  for (int b = b0; b < b1; ++b) {
+    const CacheReq r = cache_req<KT>(p, b);
+    ok = ok && cache_req_ok(p, r);
+    sum += cache_cost(p, r);
+  }
+  int64_t incl = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t v = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += v;
+  }
+  if (lane == 31) sh->warp_sum[warp] = incl;
+  const bool all_ok = __syncthreads_and(ok) != 0;
+  int64_t base = 0, total = 0;
+  for (int w = 0; w < nw; ++w) {
+    const int64_t v = sh->warp_sum[w];
+    if (w < warp) base += v;
+    total += v;
+  }
+  CacheRange R;
+  R.ok = all_ok;
+  R.total = total;
+  const int64_t g = gridDim.x;
+  R.per = max((total + g - 1) / g, static_cast<int64_t>(min_tiles));
+  R.begin = min(R.per * blockIdx.x, total);
+  R.end = min(R.begin + R.per, total);
+  int64_t at = base + incl - sum;
+  if (all_ok && R.begin < total && at <= R.begin && R.begin < at + sum) {
+    int b = b0;
+    for (;; ++b) {
+      const int64_t c = cache_cost(p, cache_req<KT>(p, b));
+      if (R.begin < at + c) break;
+      at += c;
+    }
+    sh->b = b;
+    sh->rem = R.begin - at;
+  }
+  __syncthreads();
+  R.b = sh->b;
+  R.rem = sh->rem;
+  return R;
+}
+
+// Walks the parts of items in a CTA's range, in order; every role of the CTA
+// walks the same parts.
+struct CacheWalk {
+  int64_t left;  // tiles left in the range
+  int64_t rem;   // place in the request's tiles
+  int b;
+  bool first;    // the part starts at the range's start
+  // the current part
+  CacheReq r;
+  int h, row_tile, tile0, count;  // count tiles from the item's tile0
+  bool whole;                     // the part is the whole item
+
+  __device__ __forceinline__ void init(const CacheRange& R) {
+    left = R.ok ? R.end - R.begin : 0;
+    rem = R.rem;
+    b = R.b;
+    first = true;
+  }
+  template <int KT>
+  __device__ __forceinline__ bool next(const CacheFwdParams& p) {
+    if (left <= 0) return false;
+    int64_t cost;
+    for (;; ++b, rem = 0) {
+      r = cache_req<KT>(p, b);
+      cost = cache_cost(p, r);
+      if (rem < cost) break;
+    }
+    const int64_t item = rem / r.n;
+    tile0 = static_cast<int>(rem - item * r.n);
+    h = static_cast<int>(item / r.rt);
+    row_tile = static_cast<int>(item - static_cast<int64_t>(h) * r.rt);
+    count = static_cast<int>(min(static_cast<int64_t>(r.n - tile0), left));
+    whole = count == r.n;
+    return true;
+  }
+  __device__ __forceinline__ void advance() {
+    rem += count;
+    left -= count;
+    first = false;
+  }
+  // Keys of tiles [lo, hi) (of the request's) in this part that any row of the
+  // row tile can see: without a mask, rows of tokens up to t see keys up to
+  // C + t, so later tiles are neither loaded nor computed.
+  template <int KT>
+  __device__ __forceinline__ void tiles(const CacheFwdParams& p, int& lo, int& hi) const {
+    lo = r.kt0 + tile0;
+    hi = lo + count;
+    if (p.mask == nullptr) {
+      const int64_t last_row = min(static_cast<int64_t>(r.T) * p.group,
+                                   static_cast<int64_t>(row_tile + 1) * p.rows_per_tile) - 1;
+      const int64_t keys = static_cast<int64_t>(r.C) + last_row / p.group + 1;
+      hi = max(lo, static_cast<int>(min(static_cast<int64_t>(hi), (keys + KT - 1) / KT)));
+    }
+  }
+};
+
+// Writes this CTA's join record and clears its status word (one thread).
+template <int KT>
+__device__ __forceinline__ void cache_open(const CacheFwdParams& p, const CacheRange& R) {
+  const int c = blockIdx.x;
+  p.err[c] = R.ok ? kOk : kErrBadOffsets;
+  CacheJoin j{};
+  if (R.ok && R.begin < R.end) {
+    const CacheReq r = cache_req<KT>(p, R.b);
+    const int64_t item = R.rem / r.n;
+    j.t0 = R.begin - (R.rem - item * r.n);
+    j.t1 = j.t0 + r.n;
+    j.per = R.per;
+    j.b = R.b;
+    j.h = static_cast<int>(item / r.rt);
+    j.rt = static_cast<int>(item - static_cast<int64_t>(j.h) * r.rt);
+    j.valid = j.t0 < R.begin && j.t0 / R.per + 1 == c;
+  }
+  p.join[c] = j;
+}
+
+}  // namespace jg

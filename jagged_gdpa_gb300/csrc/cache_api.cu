@@ -1,0 +1,289 @@
+// Entry points of the paged key/value cache: argument checks, tensor maps,
+// workspace layout and launches.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+#include <cstring>
+
+#include "../../include/jgdpa.h"
+#include "act.cuh"
+#include "cache.cuh"
+#include "host.h"
+
+namespace jg {
+template <int D>
+cudaError_t launch_cache_fwd_d(const CacheFwdParams& p, int act, int grid, cudaStream_t stream);
+template <int D>
+cudaError_t launch_cache_join_d(const CacheFwdParams& p, int act, int n_ctas, int max_rows, cudaStream_t stream);
+cudaError_t launch_cache_plan(const CachePlanParams& p, int sms, cudaStream_t stream);
+cudaError_t launch_cache_append(const CacheAppendParams& p, cudaStream_t stream);
+}  // namespace jg
+
+namespace {
+
+constexpr size_t kAlign = 256;
+size_t up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
+bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+
+// log2 of an accepted page size (a power of two, 16 to 1024 tokens), or -1.
+int page_shift_of(int32_t page_size) {
+  for (int s = 4; s <= 10; ++s)
+    if (page_size == 1 << s) return s;
+  return -1;
+}
+
+jgdpa_status check_cache(const void* k_cache, const void* v_cache, int64_t k_page_stride, int64_t v_page_stride,
+                         int32_t num_pages, int32_t page_size, int32_t kv_heads, int32_t head_dim) {
+  if (num_pages < 1 || page_size < 1 || kv_heads < 1) return JGDPA_ERR_INVALID_ARGUMENT;
+  if (head_dim != 32 && head_dim != 64 && head_dim != 128) return JGDPA_ERR_UNSUPPORTED;
+  if (page_shift_of(page_size) < 0 || kv_heads > 65535) return JGDPA_ERR_UNSUPPORTED;
+  if (static_cast<int64_t>(num_pages) * page_size > INT32_MAX) return JGDPA_ERR_UNSUPPORTED;
+  if (k_cache == nullptr || v_cache == nullptr) return JGDPA_ERR_INVALID_ARGUMENT;
+  const int64_t page = static_cast<int64_t>(page_size) * kv_heads * head_dim;
+  if (k_page_stride < page || v_page_stride < page) return JGDPA_ERR_INVALID_ARGUMENT;
+  if (k_page_stride >= (int64_t{1} << 39) || v_page_stride >= (int64_t{1} << 39)) return JGDPA_ERR_UNSUPPORTED;
+  if (!aligned(k_cache, 16) || !aligned(v_cache, 16) || k_page_stride % 8 || v_page_stride % 8)
+    return JGDPA_ERR_MISALIGNED;
+  return JGDPA_OK;
+}
+
+// Query rows of one item, from the most rows a key/value head can have.
+int rows_per_tile(int64_t max_rows) { return max_rows <= 16 ? 16 : 32; }
+
+struct CacheLayout {
+  size_t err, join, part_ml, part_o, total;
+  int rows, grid;
+};
+bool cache_layout(int32_t heads, int32_t kv_heads, int32_t head_dim, int32_t max_q, CacheLayout* L) {
+  const int sms = jg::host_sm_count();
+  if (sms <= 0) return false;
+  L->grid = sms;
+  L->rows = rows_per_tile(static_cast<int64_t>(max_q) * (heads / kv_heads));
+  const size_t parts = 2 * static_cast<size_t>(L->grid) * L->rows;
+  size_t off = kAlign;  // the status word
+  L->err = off;
+  off += up(L->grid * sizeof(int));
+  L->join = off;
+  off += up(L->grid * sizeof(jg::CacheJoin));
+  L->part_ml = off;
+  off += up(parts * sizeof(float2));
+  L->part_o = off;
+  off += up(parts * head_dim * sizeof(float));
+  L->total = off;
+  return true;
+}
+
+// The cache as one tensor map: (column of a 64-column half, token of the page,
+// half, head, page); a box is one head of up to 64 tokens of a page.
+bool cache_map(CUtensorMap* m, const void* ptr, int64_t page_stride, int32_t num_pages, int32_t page_size,
+               int32_t kv_heads, int32_t head_dim) {
+  std::memset(m, 0, sizeof(*m));
+  const jg::EncodeFn enc = jg::host_encode_fn();
+  if (!enc) return false;
+  const cuuint64_t cols = std::min(head_dim, 64), halves = head_dim / cols;
+  cuuint64_t dims[5] = {cols, static_cast<cuuint64_t>(page_size), halves, static_cast<cuuint64_t>(kv_heads),
+                        static_cast<cuuint64_t>(num_pages)};
+  cuuint64_t strides[4] = {static_cast<cuuint64_t>(kv_heads) * head_dim * 2, cols * 2,
+                           static_cast<cuuint64_t>(head_dim) * 2, static_cast<cuuint64_t>(page_stride) * 2};
+  cuuint32_t box[5] = {static_cast<cuuint32_t>(cols), static_cast<cuuint32_t>(std::min(page_size, 64)),
+                       static_cast<cuuint32_t>(halves), 1, 1};
+  cuuint32_t es[5] = {1, 1, 1, 1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<void*>(ptr), dims, strides, box, es,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, cols == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+#define JG_CUDA(x)                              \
+  do {                                          \
+    if ((x) != cudaSuccess) return JGDPA_ERR_CUDA; \
+  } while (0)
+
+}  // namespace
+
+extern "C" {
+
+size_t jgdpa_cache_plan_workspace_bytes(void) { return kAlign; }
+
+jgdpa_status jgdpa_cache_plan(const int32_t* ctx_lens, const int32_t* new_lens, const int32_t* held_pages,
+                              int32_t batch, int32_t page_size, int32_t* block_table, int32_t table_width,
+                              int32_t* free_pages, int32_t num_pages, const int32_t* free_count, int32_t total_new,
+                              int32_t* held_out, int32_t* free_count_out, int32_t* q_offsets, int32_t* kv_lens,
+                              int32_t* slots, void* workspace, size_t workspace_bytes, jgdpa_stream_t stream_) {
+  if (batch < 0 || table_width < 0 || num_pages < 0 || total_new < 0 || page_size < 1)
+    return JGDPA_ERR_INVALID_ARGUMENT;
+  const int shift = page_shift_of(page_size);
+  if (shift < 0 || batch > jg::kCacheMaxBatch) return JGDPA_ERR_UNSUPPORTED;
+  if (static_cast<int64_t>(num_pages) * page_size > INT32_MAX ||
+      static_cast<int64_t>(table_width) * page_size > INT32_MAX)
+    return JGDPA_ERR_UNSUPPORTED;
+  if (free_count == nullptr || free_count_out == nullptr || q_offsets == nullptr) return JGDPA_ERR_INVALID_ARGUMENT;
+  if (batch > 0 && (ctx_lens == nullptr || new_lens == nullptr || held_pages == nullptr || held_out == nullptr ||
+                    kv_lens == nullptr || (table_width > 0 && block_table == nullptr)))
+    return JGDPA_ERR_INVALID_ARGUMENT;
+  if ((num_pages > 0 && free_pages == nullptr) || (total_new > 0 && slots == nullptr)) return JGDPA_ERR_INVALID_ARGUMENT;
+  // results are written while other parts of the call still read their inputs
+  if ((batch > 0 && (held_out == held_pages || kv_lens == ctx_lens || kv_lens == held_pages || held_out == ctx_lens ||
+                     held_out == new_lens || kv_lens == new_lens)) || free_count_out == free_count)
+    return JGDPA_ERR_INVALID_ARGUMENT;
+  for (const void* a : {static_cast<const void*>(ctx_lens), static_cast<const void*>(new_lens),
+                        static_cast<const void*>(held_pages), static_cast<const void*>(block_table),
+                        static_cast<const void*>(free_pages), static_cast<const void*>(free_count),
+                        static_cast<const void*>(held_out), static_cast<const void*>(free_count_out),
+                        static_cast<const void*>(q_offsets), static_cast<const void*>(kv_lens),
+                        static_cast<const void*>(slots)})
+    if (!aligned(a, 4)) return JGDPA_ERR_MISALIGNED;
+  if (workspace == nullptr || workspace_bytes < kAlign) return JGDPA_ERR_WORKSPACE_TOO_SMALL;
+  if (!aligned(workspace, kAlign)) return JGDPA_ERR_MISALIGNED;
+  const int sms = jg::host_sm_count();
+  if (sms <= 0) return JGDPA_ERR_CUDA;
+  jg::CachePlanParams p{};
+  p.ctx = ctx_lens;
+  p.add = new_lens;
+  p.held = held_pages;
+  p.batch = batch;
+  p.page_shift = shift;
+  p.width = table_width;
+  p.pool = num_pages;
+  p.total = total_new;
+  p.table = block_table;
+  p.free_pages = free_pages;
+  p.free_count = free_count;
+  p.held_out = held_out;
+  p.free_count_out = free_count_out;
+  p.q_off = q_offsets;
+  p.kv_lens = kv_lens;
+  p.slots = slots;
+  p.status = static_cast<int*>(workspace);
+  JG_CUDA(jg::launch_cache_plan(p, sms, reinterpret_cast<cudaStream_t>(stream_)));
+  return JGDPA_OK;
+}
+
+jgdpa_status jgdpa_cache_append(const void* k_new, const void* v_new, int64_t k_stride, int64_t v_stride,
+                                const int32_t* slots, int32_t total_new, void* k_cache, void* v_cache,
+                                int64_t k_page_stride, int64_t v_page_stride, int32_t num_pages, int32_t page_size,
+                                int32_t kv_heads, int32_t head_dim, jgdpa_stream_t stream_) {
+  if (total_new < 0) return JGDPA_ERR_INVALID_ARGUMENT;
+  jgdpa_status st = check_cache(k_cache, v_cache, k_page_stride, v_page_stride, num_pages, page_size, kv_heads, head_dim);
+  if (st != JGDPA_OK) return st;
+  if (total_new == 0) return JGDPA_OK;
+  if (k_new == nullptr || v_new == nullptr || slots == nullptr) return JGDPA_ERR_INVALID_ARGUMENT;
+  const int64_t row = static_cast<int64_t>(kv_heads) * head_dim;
+  if (k_stride < row || v_stride < row) return JGDPA_ERR_INVALID_ARGUMENT;
+  if (!aligned(k_new, 16) || !aligned(v_new, 16) || !aligned(slots, 4) || k_stride % 8 || v_stride % 8)
+    return JGDPA_ERR_MISALIGNED;
+  jg::CacheAppendParams p{};
+  p.k = static_cast<const __nv_bfloat16*>(k_new);
+  p.v = static_cast<const __nv_bfloat16*>(v_new);
+  p.k_stride = k_stride;
+  p.v_stride = v_stride;
+  p.slots = slots;
+  p.rows = total_new;
+  p.chunks = static_cast<int32_t>(row / 8);
+  p.k_cache = static_cast<__nv_bfloat16*>(k_cache);
+  p.v_cache = static_cast<__nv_bfloat16*>(v_cache);
+  p.k_page_stride = k_page_stride;
+  p.v_page_stride = v_page_stride;
+  p.page_shift = page_shift_of(page_size);
+  p.slot_end = num_pages * page_size;
+  JG_CUDA(jg::launch_cache_append(p, reinterpret_cast<cudaStream_t>(stream_)));
+  return JGDPA_OK;
+}
+
+size_t jgdpa_cache_fwd_workspace_bytes(int32_t heads, int32_t kv_heads, int32_t head_dim, int32_t max_q) {
+  if (heads < 1 || kv_heads < 1 || heads % kv_heads || max_q < 0) return 0;
+  if (head_dim != 32 && head_dim != 64 && head_dim != 128) return 0;
+  CacheLayout L;
+  return cache_layout(heads, kv_heads, head_dim, max_q, &L) ? L.total : 0;
+}
+
+jgdpa_status jgdpa_cache_fwd(const void* q, int64_t q_stride, const void* k_cache, const void* v_cache,
+                             int64_t k_page_stride, int64_t v_page_stride, int32_t num_pages, int32_t page_size,
+                             const int32_t* block_table, int32_t table_width, const int32_t* q_offsets,
+                             const int32_t* kv_lens, int32_t batch, int64_t total_q, int32_t max_q, int32_t heads,
+                             int32_t kv_heads, int32_t head_dim, jgdpa_act act, float scale, const float* bias_table,
+                             int32_t bias_len, int32_t window, const int32_t* tree_mask, int32_t mask_words,
+                             const int32_t* depths, void* out, float* lse, void* workspace, size_t workspace_bytes,
+                             jgdpa_stream_t stream_) {
+  cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
+  if (batch < 0 || total_q < 0 || max_q < 0 || heads < 1 || table_width < 0 || window < 0 || mask_words < 0)
+    return JGDPA_ERR_INVALID_ARGUMENT;
+  jgdpa_status st = check_cache(k_cache, v_cache, k_page_stride, v_page_stride, num_pages, page_size, kv_heads, head_dim);
+  if (st != JGDPA_OK) return st;
+  if (heads % kv_heads || heads > 65535) return heads % kv_heads ? JGDPA_ERR_INVALID_ARGUMENT : JGDPA_ERR_UNSUPPORTED;
+  if (act < JGDPA_ACT_GELU || act > JGDPA_ACT_SOFTMAX || !std::isfinite(scale)) return JGDPA_ERR_INVALID_ARGUMENT;
+  if (bias_len < 0 || (bias_len > 0) != (bias_table != nullptr) || (bias_len > 0 && bias_len % 2 == 0))
+    return JGDPA_ERR_INVALID_ARGUMENT;
+  if (bias_len > jg::kMaxBiasLen) return JGDPA_ERR_UNSUPPORTED;
+  if ((mask_words > 0) != (tree_mask != nullptr)) return JGDPA_ERR_INVALID_ARGUMENT;
+  if (act != JGDPA_ACT_SOFTMAX && lse != nullptr) return JGDPA_ERR_INVALID_ARGUMENT;
+  const int64_t max_rows = static_cast<int64_t>(max_q) * (heads / kv_heads);
+  if (total_q > INT32_MAX || batch > jg::kCacheMaxBatch || max_rows > INT32_MAX / 2 ||
+      static_cast<int64_t>(table_width) * page_size > INT32_MAX || static_cast<int64_t>(mask_words) * 32 > INT32_MAX)
+    return JGDPA_ERR_UNSUPPORTED;
+  if (batch > 0 && (q_offsets == nullptr || kv_lens == nullptr || (table_width > 0 && block_table == nullptr)))
+    return JGDPA_ERR_INVALID_ARGUMENT;
+  if (total_q > 0 && (q == nullptr || out == nullptr)) return JGDPA_ERR_INVALID_ARGUMENT;
+  if (q_stride < static_cast<int64_t>(heads) * head_dim) return JGDPA_ERR_INVALID_ARGUMENT;
+  if (!aligned(q, 16) || q_stride % 8 || !aligned(out, 16) || !aligned(lse, 4) || !aligned(bias_table, 4) ||
+      !aligned(q_offsets, 4) || !aligned(kv_lens, 4) || !aligned(block_table, 4) || !aligned(tree_mask, 4) ||
+      !aligned(depths, 4))
+    return JGDPA_ERR_MISALIGNED;
+  CacheLayout L;
+  if (!cache_layout(heads, kv_heads, head_dim, max_q, &L)) return JGDPA_ERR_CUDA;
+  if (workspace == nullptr || workspace_bytes < L.total) return JGDPA_ERR_WORKSPACE_TOO_SMALL;
+  if (!aligned(workspace, kAlign)) return JGDPA_ERR_MISALIGNED;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  if (batch == 0 || total_q == 0 || max_q == 0) {
+    JG_CUDA(cudaMemsetAsync(ws, 0, sizeof(int), stream));
+    return JGDPA_OK;
+  }
+  jg::CacheFwdParams p{};
+  if (!cache_map(&p.tm_k, k_cache, k_page_stride, num_pages, page_size, kv_heads, head_dim) ||
+      !cache_map(&p.tm_v, v_cache, v_page_stride, num_pages, page_size, kv_heads, head_dim))
+    return JGDPA_ERR_CUDA;
+  p.q = static_cast<const __nv_bfloat16*>(q);
+  p.q_stride = q_stride;
+  p.table = block_table;
+  p.q_off = q_offsets;
+  p.kv_lens = kv_lens;
+  p.bias = bias_table;
+  p.mask = tree_mask;
+  p.depth = depths;
+  p.out = static_cast<__nv_bfloat16*>(out);
+  p.lse = lse;
+  p.part_o = reinterpret_cast<float*>(ws + L.part_o);
+  p.part_ml = reinterpret_cast<float2*>(ws + L.part_ml);
+  p.join = reinterpret_cast<jg::CacheJoin*>(ws + L.join);
+  p.err = reinterpret_cast<int*>(ws + L.err);
+  p.status = reinterpret_cast<int*>(ws);
+  p.total_q = total_q;
+  p.batch = batch;
+  p.max_q = max_q;
+  p.heads = heads;
+  p.kv_heads = kv_heads;
+  p.group = heads / kv_heads;
+  p.page_shift = page_shift_of(page_size);
+  p.width = table_width;
+  p.num_pages = num_pages;
+  p.mask_words = mask_words;
+  p.bias_len = bias_len;
+  p.window = window;
+  p.rows_per_tile = L.rows;
+  p.scale = act == JGDPA_ACT_SOFTMAX ? scale * jg::kLog2e : scale;
+  p.wait_limit_ns = jg::host_wait_limit_ns();
+  const int max_tile_rows = static_cast<int>(std::min<int64_t>(L.rows, max_rows));
+  auto launch = [&](auto dim) -> cudaError_t {
+    constexpr int D = decltype(dim)::value;
+    cudaError_t e = jg::launch_cache_fwd_d<D>(p, act, L.grid, stream);
+    return e != cudaSuccess ? e : jg::launch_cache_join_d<D>(p, act, L.grid, max_tile_rows, stream);
+  };
+  JG_CUDA(head_dim == 128  ? launch(std::integral_constant<int, 128>{})
+          : head_dim == 64 ? launch(std::integral_constant<int, 64>{})
+                           : launch(std::integral_constant<int, 32>{}));
+  return JGDPA_OK;
+}
+
+}  // extern "C"
