@@ -15,7 +15,7 @@
 // O; they meet once per item.  With 16-row tiles a second group of four warps
 // takes every other tile, with 32-row tiles the second 16 rows.
 //
-// The TMA producer runs up to 160 KB ahead, across items, so that an item's
+// The TMA producer runs up to 160 KB ahead (128 KB at d = 128), across items, so that an item's
 // end (the warps' exchange) does not stop the loads.
 #include "act.cuh"
 #include "cache.cuh"
@@ -36,7 +36,12 @@ struct CcCfg {
   static constexpr int kRowBytes = kBlockCols * 2;
   static constexpr int kHalves = D / kBlockCols;
   static constexpr int kTileBytes = kCKeys * D * 2;            // K or V of one tile
-  static constexpr int kStages = D == 128 ? 5 : (D == 64 ? 10 : 16);
+  // Even, so that with 16-row tiles a stage always serves the same group of
+  // warps: a group that met a stage only every other round could take the
+  // other group's unfinished round for its own (a parity tells two rounds
+  // apart, not three).
+  static constexpr int kStages = D == 128 ? 4 : (D == 64 ? 10 : 16);
+  static_assert(kStages % 2 == 0, "stages alternate between two groups");
   static constexpr int kSlotBytes = 16 * D * 4;                // one warp's O
   static constexpr int kOOff = kStages * 2 * kTileBytes;
   static constexpr int kBarOff = kOOff + kCWarps * kSlotBytes;
