@@ -30,7 +30,7 @@ LIB = os.path.join(BUILD, "libjgdpa.so")
 HEAD_DIMS = (32, 64, 128)
 SOURCES = ["api.cu", "sched.cu", "cache_api.cu", "cache_plan.cu"]  # compiled once
 # compiled once per head dimension, shared by both libraries
-PER_DIM_SHARED_SOURCES = ["cache_fwd.cu"]
+PER_DIM_SHARED_SOURCES = ["cache_fwd.cu", "cache_fwd_wide.cu"]
 PER_DIM_SOURCES = ["fwd.cu", "fwd_shortq.cu", "bwd.cu", "bwd_shortq.cu"]  # compiled once per head dimension and library
 HEADERS = ["act.cuh", "cache.cuh", "common.cuh", "host.h", "ptx.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

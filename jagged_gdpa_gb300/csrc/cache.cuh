@@ -8,6 +8,7 @@
 
 #include <cstdint>
 
+#include "act.cuh"
 #include "common.cuh"
 #include "ptx.cuh"
 
@@ -58,8 +59,12 @@ struct CacheJoin {
 struct CacheFwdParams {
   CUtensorMap tm_k;
   CUtensorMap tm_v;
+  CUtensorMap tm_q;          // (column, head, token), boxes of one 128-row tile (128-row kernel)
   const __nv_bfloat16* q;
   int64_t q_stride;          // elements from one query row to the next
+  const __nv_bfloat16* k_cache;
+  const __nv_bfloat16* v_cache;
+  int64_t k_page_stride, v_page_stride;  // elements from one page to the next
   const int32_t* table;      // [batch][width]
   const int32_t* q_off;
   const int32_t* kv_lens;
@@ -254,6 +259,72 @@ __device__ __forceinline__ void cache_open(const CacheFwdParams& p, const CacheR
     j.valid = j.t0 < R.begin && j.t0 / R.per + 1 == c;
   }
   p.join[c] = j;
+}
+
+// What the kernels keep of a query row.
+struct CcRow {
+  int t;            // token, or -1: no row
+  int pos;          // C + depth
+  int head;
+  float far_bias;   // bias of keys at least R behind every new token
+};
+
+template <int ACT>
+__device__ __forceinline__ float cc_act(float x) {
+  if constexpr (ACT == 0) return 0.5f * x * (1.0f + erff(x * 0.70710678118654752f));
+  else return __fdividef(x, 1.0f + __expf(-x));
+}
+
+template <int ACT>
+__device__ __forceinline__ float cc_bias_unit() { return ACT == 2 ? kLog2e : 1.0f; }
+
+// The halves of a packed bf16 pair that are infinite or NaN, as a mask.
+__device__ __forceinline__ uint32_t cc_nonfinite(uint32_t v) {
+  return ((v & 0x7F80u) == 0x7F80u ? 0xFFFFu : 0u) | ((v & 0x7F800000u) == 0x7F800000u ? 0xFFFF0000u : 0u);
+}
+
+// Whether a row sees key j.
+__device__ __forceinline__ bool cc_sees(const CacheFwdParams& p, const CacheReq& r, const CcRow& q, int j, int depth_j) {
+  if (q.t < 0 || j >= r.L) return false;
+  const int u = j - r.C;
+  if (u >= 0) {
+    if (p.mask != nullptr) {
+      const uint32_t word = __ldg(p.mask + static_cast<int64_t>(r.q0 + q.t) * p.mask_words + (u >> 5));
+      if (!((word >> (u & 31)) & 1)) return false;
+    } else if (u > q.t) {
+      return false;
+    }
+  }
+  if (p.window > 0) {
+    const int64_t apart = static_cast<int64_t>(q.pos) - (u >= 0 ? static_cast<int64_t>(r.C) + depth_j : j);
+    if (apart >= p.window || -apart >= p.window) return false;
+  }
+  return true;
+}
+
+// The bias table's entry for a row and key j.
+__device__ __forceinline__ float cc_bias(const CacheFwdParams& p, const CacheReq& r, const CcRow& q, int j, int depth_j) {
+  const int64_t reach = (p.bias_len - 1) / 2;
+  const int64_t apart = static_cast<int64_t>(q.pos) - (j >= r.C ? static_cast<int64_t>(r.C) + depth_j : j);
+  const int at = static_cast<int>(min(max(apart, -reach), reach) + reach);
+  return __ldg(p.bias + static_cast<int64_t>(q.head) * p.bias_len + at);
+}
+
+// The depth of key j's token (0 for the context).
+__device__ __forceinline__ int cc_depth(const CacheFwdParams& p, const CacheReq& r, int j) {
+  const int u = j - r.C;
+  if (u < 0 || j >= r.L) return 0;
+  return p.depth != nullptr ? __ldg(p.depth + r.q0 + u) : u;
+}
+
+// x innermost: columns, rows of the page, column halves, heads, pages
+__device__ __forceinline__ void tma_load_5d(uint32_t dst, const CUtensorMap* map, uint64_t* bar, int x, int y, int z,
+                                            int u, int w) {
+  asm volatile(
+      "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5, %6, %7}], [%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z), "r"(u), "r"(w)
+      : "memory");
 }
 
 }  // namespace jg

@@ -17,6 +17,8 @@ namespace jg {
 template <int D>
 cudaError_t launch_cache_fwd_d(const CacheFwdParams& p, int act, int grid, cudaStream_t stream);
 template <int D>
+cudaError_t launch_cache_fwd_wide_d(const CacheFwdParams& p, int act, int grid, cudaStream_t stream);
+template <int D>
 cudaError_t launch_cache_join_d(const CacheFwdParams& p, int act, int n_ctas, int max_rows, cudaStream_t stream);
 cudaError_t launch_cache_plan(const CachePlanParams& p, int sms, cudaStream_t stream);
 cudaError_t launch_cache_append(const CacheAppendParams& p, cudaStream_t stream);
@@ -50,18 +52,25 @@ jgdpa_status check_cache(const void* k_cache, const void* v_cache, int64_t k_pag
   return JGDPA_OK;
 }
 
-// Query rows of one item, from the most rows a key/value head can have.
-int rows_per_tile(int64_t max_rows) { return max_rows <= 16 ? 16 : 32; }
-
 struct CacheLayout {
   size_t err, join, part_ml, part_o, total;
-  int rows, grid;
+  int rows, grid;  // query rows of one item, CTAs
+  bool wide;       // 128-row tiles through tensor memory
 };
 bool cache_layout(int32_t heads, int32_t kv_heads, int32_t head_dim, int32_t max_q, CacheLayout* L) {
   const int sms = jg::host_sm_count();
   if (sms <= 0) return false;
   L->grid = sms;
-  L->rows = rows_per_tile(static_cast<int64_t>(max_q) * (heads / kv_heads));
+  const int group = heads / kv_heads;
+  const int64_t max_rows = static_cast<int64_t>(max_q) * group;
+  // (a tile of the wide kernel holds whole tokens, so at most 128 heads share a key/value head there)
+  L->wide = max_rows > 32 && group <= jg::kTile;
+  if (L->wide) {
+    const int tile = jg::kTile / group * group;
+    L->rows = max_rows > tile ? 2 * tile : tile;
+  } else {
+    L->rows = max_rows <= 16 ? 16 : 32;
+  }
   const size_t parts = 2 * static_cast<size_t>(L->grid) * L->rows;
   size_t off = kAlign;  // the status word
   L->err = off;
@@ -77,9 +86,10 @@ bool cache_layout(int32_t heads, int32_t kv_heads, int32_t head_dim, int32_t max
 }
 
 // The cache as one tensor map: (column of a 64-column half, token of the page,
-// half, head, page); a box is one head of up to 64 tokens of a page.
+// half, head, page).  A box is one head of up to box_tokens tokens of a page,
+// both halves or one.
 bool cache_map(CUtensorMap* m, const void* ptr, int64_t page_stride, int32_t num_pages, int32_t page_size,
-               int32_t kv_heads, int32_t head_dim) {
+               int32_t kv_heads, int32_t head_dim, int32_t box_tokens, bool both_halves) {
   std::memset(m, 0, sizeof(*m));
   const jg::EncodeFn enc = jg::host_encode_fn();
   if (!enc) return false;
@@ -88,10 +98,28 @@ bool cache_map(CUtensorMap* m, const void* ptr, int64_t page_stride, int32_t num
                         static_cast<cuuint64_t>(num_pages)};
   cuuint64_t strides[4] = {static_cast<cuuint64_t>(kv_heads) * head_dim * 2, cols * 2,
                            static_cast<cuuint64_t>(head_dim) * 2, static_cast<cuuint64_t>(page_stride) * 2};
-  cuuint32_t box[5] = {static_cast<cuuint32_t>(cols), static_cast<cuuint32_t>(std::min(page_size, 64)),
-                       static_cast<cuuint32_t>(halves), 1, 1};
+  cuuint32_t box[5] = {static_cast<cuuint32_t>(cols), static_cast<cuuint32_t>(std::min(page_size, box_tokens)),
+                       static_cast<cuuint32_t>(both_halves ? halves : 1), 1, 1};
   cuuint32_t es[5] = {1, 1, 1, 1, 1};
   return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<void*>(ptr), dims, strides, box, es,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, cols == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// The queries: (column, head, token), a box one 64-column half of a tile's
+// tokens and the heads of one group.
+bool query_map(CUtensorMap* m, const void* ptr, int64_t q_stride, int64_t total_q, int32_t heads, int32_t head_dim,
+               int32_t group) {
+  std::memset(m, 0, sizeof(*m));
+  const jg::EncodeFn enc = jg::host_encode_fn();
+  if (!enc) return false;
+  const cuuint32_t cols = std::min(head_dim, 64);
+  cuuint64_t dims[3] = {static_cast<cuuint64_t>(head_dim), static_cast<cuuint64_t>(heads),
+                        static_cast<cuuint64_t>(total_q)};
+  cuuint64_t strides[2] = {static_cast<cuuint64_t>(head_dim) * 2, static_cast<cuuint64_t>(q_stride) * 2};
+  cuuint32_t box[3] = {cols, static_cast<cuuint32_t>(group), static_cast<cuuint32_t>(jg::kTile / group)};
+  cuuint32_t es[3] = {1, 1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(ptr), dims, strides, box, es,
              CU_TENSOR_MAP_INTERLEAVE_NONE, cols == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
@@ -231,6 +259,7 @@ jgdpa_status jgdpa_cache_fwd(const void* q, int64_t q_stride, const void* k_cach
       !aligned(q_offsets, 4) || !aligned(kv_lens, 4) || !aligned(block_table, 4) || !aligned(tree_mask, 4) ||
       !aligned(depths, 4))
     return JGDPA_ERR_MISALIGNED;
+  if (q_stride >= (int64_t{1} << 39)) return JGDPA_ERR_UNSUPPORTED;
   CacheLayout L;
   if (!cache_layout(heads, kv_heads, head_dim, max_q, &L)) return JGDPA_ERR_CUDA;
   if (workspace == nullptr || workspace_bytes < L.total) return JGDPA_ERR_WORKSPACE_TOO_SMALL;
@@ -241,9 +270,15 @@ jgdpa_status jgdpa_cache_fwd(const void* q, int64_t q_stride, const void* k_cach
     return JGDPA_OK;
   }
   jg::CacheFwdParams p{};
-  if (!cache_map(&p.tm_k, k_cache, k_page_stride, num_pages, page_size, kv_heads, head_dim) ||
-      !cache_map(&p.tm_v, v_cache, v_page_stride, num_pages, page_size, kv_heads, head_dim))
+  const int32_t box = L.wide ? jg::kTile : 64;
+  if (!cache_map(&p.tm_k, k_cache, k_page_stride, num_pages, page_size, kv_heads, head_dim, box, !L.wide) ||
+      !cache_map(&p.tm_v, v_cache, v_page_stride, num_pages, page_size, kv_heads, head_dim, box, !L.wide) ||
+      (L.wide && !query_map(&p.tm_q, q, q_stride, total_q, heads, head_dim, heads / kv_heads)))
     return JGDPA_ERR_CUDA;
+  p.k_cache = static_cast<const __nv_bfloat16*>(k_cache);
+  p.v_cache = static_cast<const __nv_bfloat16*>(v_cache);
+  p.k_page_stride = k_page_stride;
+  p.v_page_stride = v_page_stride;
   p.q = static_cast<const __nv_bfloat16*>(q);
   p.q_stride = q_stride;
   p.table = block_table;
@@ -277,7 +312,8 @@ jgdpa_status jgdpa_cache_fwd(const void* q, int64_t q_stride, const void* k_cach
   const int max_tile_rows = static_cast<int>(std::min<int64_t>(L.rows, max_rows));
   auto launch = [&](auto dim) -> cudaError_t {
     constexpr int D = decltype(dim)::value;
-    cudaError_t e = jg::launch_cache_fwd_d<D>(p, act, L.grid, stream);
+    cudaError_t e = L.wide ? jg::launch_cache_fwd_wide_d<D>(p, act, L.grid, stream)
+                           : jg::launch_cache_fwd_d<D>(p, act, L.grid, stream);
     return e != cudaSuccess ? e : jg::launch_cache_join_d<D>(p, act, L.grid, max_tile_rows, stream);
   };
   JG_CUDA(head_dim == 128  ? launch(std::integral_constant<int, 128>{})

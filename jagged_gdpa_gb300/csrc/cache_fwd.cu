@@ -75,16 +75,6 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-// x innermost: columns, rows of the page, column halves, heads, pages
-__device__ __forceinline__ void tma_load_5d(uint32_t dst, const CUtensorMap* map, uint64_t* bar, int x, int y, int z,
-                                            int u, int w) {
-  asm volatile(
-      "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%3, %4, %5, %6, %7}], [%2];" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z), "r"(u), "r"(w)
-      : "memory");
-}
-
 // Byte offset of 16-byte piece c of key n in a K or V tile: the tile is a row
 // of TMA boxes of `pr` = min(page size, 64) tokens, each [halves][pr][row],
 // its pieces swizzled over the bytes of a row by the row's place in 8.
@@ -148,47 +138,6 @@ __device__ void cc_producer(const CacheFwdParams& p, uint8_t* smem, CcShared* sh
 }
 
 // ------------------------------------------------------------- consumers
-// What one lane needs of its two rows (lane / 4 and lane / 4 + 8 of the warp's 16).
-struct CcRow {
-  int t;            // token, or -1: no row
-  int pos;          // C + depth
-  int head;
-  float far_bias;   // bias of keys at least R behind every new token
-};
-
-template <int ACT>
-__device__ __forceinline__ float cc_act(float x) {
-  if constexpr (ACT == 0) return 0.5f * x * (1.0f + erff(x * 0.70710678118654752f));
-  else return __fdividef(x, 1.0f + __expf(-x));
-}
-
-template <int ACT>
-__device__ __forceinline__ float cc_bias_unit() { return ACT == 2 ? kLog2e : 1.0f; }
-
-// The halves of a packed bf16 pair that are infinite or NaN, as a mask.
-__device__ __forceinline__ uint32_t cc_nonfinite(uint32_t v) {
-  return ((v & 0x7F80u) == 0x7F80u ? 0xFFFFu : 0u) | ((v & 0x7F800000u) == 0x7F800000u ? 0xFFFF0000u : 0u);
-}
-
-// Whether a row sees key j.
-__device__ __forceinline__ bool cc_sees(const CacheFwdParams& p, const CacheReq& r, const CcRow& q, int j, int depth_j) {
-  if (q.t < 0 || j >= r.L) return false;
-  const int u = j - r.C;
-  if (u >= 0) {
-    if (p.mask != nullptr) {
-      const uint32_t word = __ldg(p.mask + static_cast<int64_t>(r.q0 + q.t) * p.mask_words + (u >> 5));
-      if (!((word >> (u & 31)) & 1)) return false;
-    } else if (u > q.t) {
-      return false;
-    }
-  }
-  if (p.window > 0) {
-    const int64_t apart = static_cast<int64_t>(q.pos) - (u >= 0 ? static_cast<int64_t>(r.C) + depth_j : j);
-    if (apart >= p.window || -apart >= p.window) return false;
-  }
-  return true;
-}
-
 template <int D, int ACT, int MT>
 __device__ void cc_consumer(const CacheFwdParams& p, uint8_t* smem, CcShared* sh, const CacheRange& R, Fail fail) {
   using C = CcCfg<D>;
@@ -294,16 +243,10 @@ __device__ void cc_consumer(const CacheFwdParams& p, uint8_t* smem, CcShared* sh
             for (int e = 0; e < 4; ++e) {
               const CcRow& q = rows[e >> 1];
               const int j = key0 + 8 * i + 2 * (lane & 3) + (e & 1);
-              const int u = j - r.C;
-              const int depth_j = u < 0 || j >= r.L ? 0 : (p.depth != nullptr ? __ldg(p.depth + r.q0 + u) : u);
+              const int depth_j = cc_depth(p, r, j);
               const bool sees = cc_sees(p, r, q, j, depth_j);
               float x = s[i][e] * p.scale;
-              if (p.bias_len && sees) {
-                const int64_t apart = static_cast<int64_t>(q.pos) - (u >= 0 ? static_cast<int64_t>(r.C) + depth_j : j);
-                const int at = static_cast<int>(min(max(apart, static_cast<int64_t>(-bias_reach)),
-                                                    static_cast<int64_t>(bias_reach))) + bias_reach;
-                x = __fmaf_rn(__ldg(p.bias + static_cast<int64_t>(q.head) * p.bias_len + at), cc_bias_unit<ACT>(), x);
-              }
+              if (p.bias_len && sees) x = __fmaf_rn(cc_bias(p, r, q, j, depth_j), cc_bias_unit<ACT>(), x);
               s[i][e] = sees ? x : (ACT == 2 ? -INFINITY : 0.f);  // act(0) = 0
               vis |= (sees ? 1u : 0u) << (4 * i + e);
             }

@@ -1,0 +1,657 @@
+// Attention over a paged key/value cache, many query rows per key/value head.
+//
+// One item is (request, key/value head, block of query rows); a row is (new
+// token, query head of the group).  Tiles of 128 rows and 128 keys run on the
+// tensor cores through tensor memory:
+//
+//   S = Q K^T (128 x 128), P = act(S) or exp2(S - m) as bf16 over S's columns,
+//   O += P V (128 x d)
+//
+// From 33 rows on the register form (cache_fwd.cu) would be bound by its
+// matrix and special-function work; here a tile's two products take about
+// 1,500 cycles at d = 128 (110 per 128 x 128 x 16 with both operands in shared
+// memory, 80 with P in tensor memory) against the 2,700 in which HBM delivers
+// its K and V, so up to 128 rows the kernel is bound by HBM and above by the
+// products.
+//
+// Two streams, each with its S, O and a warpgroup of activation threads, keep
+// the tensor core fed: while one stream's S is turned into P, the other's
+// products run.  A part with more than 128 rows gives each stream its own rows
+// and uses every K and V tile twice (half the shared-memory fills and L2 reads
+// per product); a part with fewer gives both streams the same rows and every
+// other key tile, and joins their O, maxima and sums at its end.
+//
+// Warps: 0 TMA producer, 1 MMA issuer (owns tensor memory), 4-7 and 8-11 the
+// streams' activation and epilogue (one row per thread).
+// TMEM: S_s at 128 s, O_s at 256 + 128 s.
+#include "act.cuh"
+#include "cache.cuh"
+#include "common.cuh"
+#include "ptx.cuh"
+
+namespace jg {
+
+constexpr int kWideMinTiles = 2;  // a range below this many tiles is not worth its own CTA
+constexpr int kWideThreads = 384;
+
+template <int D>
+struct CwCfg {
+  static constexpr int kBlockCols = D < 64 ? D : 64;
+  static constexpr int kRowBytes = kBlockCols * 2;
+  static constexpr int kBlockBytes = kTile * kRowBytes;  // 128 rows of one column block
+  static constexpr int kBlocks = D / kBlockCols;
+  static constexpr int kTileBytes = kTile * D * 2;
+  static constexpr int kStages = D == 128 ? 2 : (D == 64 ? 4 : 8);
+  static constexpr uint32_t kSwizzle = kRowBytes == 128 ? 2u : 4u;
+  static constexpr int kSBO = 8 * kRowBytes;
+  static constexpr int kQOff = 0;  // two Q tiles
+  static constexpr int kKOff = kQOff + 2 * kTileBytes;
+  static constexpr int kVOff = kKOff + kStages * kTileBytes;
+  static constexpr int kBarOff = kVOff + kStages * kTileBytes;
+  static constexpr int kSmemBytes = kBarOff + 8192 + 1024;
+  static_assert(kSmemBytes <= 232448, "shared memory per CTA");
+};
+
+struct CwShared {
+  uint64_t q_full[2], q_empty[2];
+  uint64_t k_full[8], k_empty[8], v_full[8], v_empty[8];
+  uint64_t s_full[2], p_full[2], o_full[2];
+  uint64_t o_empty, drain;
+  CacheRangeShared range;
+  float2 ml[2][2][kTile];  // [part parity][stream][row]: maximum and sum
+  uint32_t tmem_base;
+  int abort;
+  int odd[2];              // by parity: number of the last part whose masked tiles hold a V that is not finite
+};
+static_assert(sizeof(CwShared) <= 8192, "shared block");
+
+// What every role works out about a part.
+struct CwPart {
+  int lo, n;        // key tiles [lo, lo + n)
+  int tile_rows;    // rows of one 128-row tile: a whole number of tokens
+  int rows;         // rows of the part
+  bool pair;        // two tiles of rows; otherwise the streams share one
+  int count[2];     // tiles of each stream
+
+  __device__ __forceinline__ CwPart(const CacheFwdParams& p, const CacheWalk& w) {
+    int hi;
+    w.tiles<kTile>(p, lo, hi);
+    n = hi - lo;
+    tile_rows = kTile / p.group * p.group;
+    rows = static_cast<int>(min(static_cast<int64_t>(p.rows_per_tile),
+                                static_cast<int64_t>(w.r.T) * p.group -
+                                    static_cast<int64_t>(w.row_tile) * p.rows_per_tile));
+    pair = rows > tile_rows;
+    count[0] = pair ? n : (n + 1) / 2;
+    count[1] = pair ? n : n / 2;
+  }
+  // the part's tile that stream s takes as its i-th
+  __device__ __forceinline__ int at(int s, int i) const { return pair ? i : 2 * i + s; }
+};
+
+// ------------------------------------------------------------- producer
+template <int D>
+__device__ void cw_producer(const CacheFwdParams& p, uint8_t* smem, CwShared* sh, const CacheRange& R, Fail fail) {
+  using C = CwCfg<D>;
+  const int lane = threadIdx.x & 31;
+  const int pr = min(1 << p.page_shift, kTile), pieces = kTile / pr;  // pieces: 1, 2, 4 or 8
+  const int piece = lane & 7, cb = lane >> 3;
+  const uint32_t base = smem_u32(smem);
+  uint32_t q_n = 0, k_n = 0, v_n = 0;
+  bool ok = true;
+  CacheWalk w;
+  w.init(R);
+  for (; ok && w.next<kTile>(p); w.advance()) {
+    const CwPart part(p, w);
+    if (part.n == 0) continue;
+    for (int s = 0; s < (part.pair ? 2 : 1) && ok; ++s, ++q_n) {
+      const int slot = q_n & 1;
+      if (!(ok = mbar_wait_warp(&sh->q_empty[slot], ((q_n >> 1) & 1) ^ 1, fail))) break;
+      if (lane == 0) {
+        mbar_arrive_tx(&sh->q_full[slot], part.tile_rows * D * 2);
+        const int token = w.r.q0 + w.row_tile * (p.rows_per_tile / p.group) + s * (part.tile_rows / p.group);
+#pragma unroll
+        for (int b = 0; b < C::kBlocks; ++b)
+          tma_load_3d(smem + C::kQOff + slot * C::kTileBytes + b * C::kBlockBytes, &p.tm_q, &sh->q_full[slot],
+                      b * C::kBlockCols, w.h * p.group, token);
+      }
+      __syncwarp();
+    }
+    const int32_t* row = p.table + static_cast<int64_t>(w.b) * p.width;
+    for (int t = part.lo; t < part.lo + part.n && ok; ++t) {
+      // lane: piece lane % 8 (min(page size, 128) tokens) of column block lane / 8
+      const int key = t * kTile + piece * pr;
+      const bool mine = cb < C::kBlocks && piece < pieces && key < w.r.L;
+      int page = p.num_pages;
+      if (mine) {
+        page = __ldg(row + (key >> p.page_shift));
+        if (static_cast<uint32_t>(page) >= static_cast<uint32_t>(p.num_pages)) {
+          atomicCAS(fail.status, kOk, kErrBadPage);
+          page = p.num_pages;  // outside the map: the copy writes zeros and reads nothing
+        }
+      }
+      const uint32_t bytes = min(pieces, (w.r.L - t * kTile + pr - 1) / pr) * pr * D * 2;
+      const uint32_t dst = base + cb * C::kBlockBytes + piece * pr * C::kRowBytes;
+      const int y = key & ((1 << p.page_shift) - 1);
+      int st = k_n % C::kStages;
+      if (!(ok = mbar_wait_warp(&sh->k_empty[st], ((k_n / C::kStages) & 1) ^ 1, fail))) break;
+      if (lane == 0) mbar_arrive_tx(&sh->k_full[st], bytes);
+      __syncwarp();
+      if (mine) tma_load_5d(dst + C::kKOff + st * C::kTileBytes, &p.tm_k, &sh->k_full[st], 0, y, cb, w.h, page);
+      ++k_n;
+      st = v_n % C::kStages;
+      if (!(ok = mbar_wait_warp(&sh->v_empty[st], ((v_n / C::kStages) & 1) ^ 1, fail))) break;
+      if (lane == 0) mbar_arrive_tx(&sh->v_full[st], bytes);
+      __syncwarp();
+      if (mine) tma_load_5d(dst + C::kVOff + st * C::kTileBytes, &p.tm_v, &sh->v_full[st], 0, y, cb, w.h, page);
+      ++v_n;
+    }
+  }
+  if (!ok) {  // let the copies already issued land before the CTA exits
+    for (uint32_t i = q_n > 2 ? q_n - 2 : 0; i < q_n; ++i) mbar_wait_drain(&sh->q_full[i & 1], (i >> 1) & 1);
+    for (uint32_t i = k_n > C::kStages ? k_n - C::kStages : 0; i < k_n; ++i)
+      mbar_wait_drain(&sh->k_full[i % C::kStages], (i / C::kStages) & 1);
+    for (uint32_t i = v_n > C::kStages ? v_n - C::kStages : 0; i < v_n; ++i)
+      mbar_wait_drain(&sh->v_full[i % C::kStages], (i / C::kStages) & 1);
+  }
+}
+
+// ------------------------------------------------------------- MMA issuer
+template <int D>
+__device__ __forceinline__ void cw_issue_qk(uint32_t t_s, uint32_t q_addr, uint32_t k_addr, bool leader) {
+  using C = CwCfg<D>;
+  constexpr uint32_t idesc = idesc_bf16(kTile, kTile, 0, 0);
+  const uint64_t a0 = sdesc(q_addr, 16, C::kSBO, C::kSwizzle), b0 = sdesc(k_addr, 16, C::kSBO, C::kSwizzle);
+#pragma unroll
+  for (int kk = 0; kk < D / 16; ++kk) {
+    const uint64_t off = static_cast<uint64_t>((kk * 16 / C::kBlockCols) * C::kBlockBytes + (kk * 16 % C::kBlockCols) * 2) >> 4;
+    if (leader) mma_ss(t_s, a0 + off, b0 + off, idesc, kk > 0 ? 1u : 0u);
+  }
+}
+template <int D>
+__device__ __forceinline__ void cw_issue_pv(uint32_t t_o, uint32_t t_p, uint32_t v_addr, bool accumulate, bool leader) {
+  using C = CwCfg<D>;
+  constexpr uint32_t idesc = idesc_bf16(kTile, D, 0, 1);  // V is MN-major
+  const uint64_t b0 = sdesc(v_addr, C::kBlockBytes, C::kSBO, C::kSwizzle);
+#pragma unroll
+  for (int kk = 0; kk < kTile / 16; ++kk) {
+    const uint64_t off = static_cast<uint64_t>(kk * 16 * C::kRowBytes) >> 4;
+    if (leader) mma_ts(t_o, t_p + kk * 8, b0 + off, idesc, (accumulate || kk > 0) ? 1u : 0u);
+  }
+}
+
+// Per pair of tiles: O_0 += P_0 V, S_0 of the stream's next tile, O_1 += P_1 V,
+// S_1 of its next.  A stream's S overwrites the columns of its P; it is issued
+// after the product that reads them, and MMAs execute in issue order.  For the
+// same reason a stream's S being complete says that its O is, too.
+template <int D>
+__device__ void cw_mma(const CacheFwdParams& p, uint8_t* smem, CwShared* sh, uint32_t tmem, const CacheRange& R,
+                       Fail fail) {
+  using C = CwCfg<D>;
+  const uint32_t q_base = smem_u32(smem + C::kQOff), k_base = smem_u32(smem + C::kKOff),
+                 v_base = smem_u32(smem + C::kVOff);
+  const bool leader = elect_one();
+  uint32_t q_n = 0, kv_n = 0, o_n = 0, p_n[2] = {0, 0};
+  bool ok = true;
+  CacheWalk w;
+  w.init(R);
+  for (; ok && w.next<kTile>(p); w.advance()) {
+    const CwPart part(p, w);
+    if (part.n == 0) continue;
+    const uint32_t slot[2] = {q_n & 1, part.pair ? (q_n + 1) & 1 : q_n & 1};
+    for (int s = 0; s < (part.pair ? 2 : 1) && ok; ++s, ++q_n) ok = mbar_wait_warp(&sh->q_full[q_n & 1], (q_n >> 1) & 1, fail);
+    if (!ok) break;
+    // S of stream s's i-th tile; frees what no later product of the part reads
+    auto issue_s = [&](int s, int i) -> bool {
+      const uint32_t it = kv_n + part.at(s, i);
+      const int st = it % C::kStages;
+      if (!mbar_wait_warp(&sh->k_full[st], (it / C::kStages) & 1, fail)) return false;
+      tc_fence_after();
+      cw_issue_qk<D>(tmem + 128 * s, q_base + slot[s] * C::kTileBytes, k_base + st * C::kTileBytes, leader);
+      if (leader) {
+        mma_commit(&sh->s_full[s]);
+        if (!part.pair || s == 1) mma_commit(&sh->k_empty[st]);
+        if (part.pair ? i == part.n - 1 : part.at(s, i) == part.n - 1) mma_commit(&sh->q_empty[slot[s]]);
+      }
+      return true;
+    };
+    for (int s = 0; s < 2 && ok; ++s)
+      if (part.count[s] > 0) ok = issue_s(s, 0);
+    for (int i = 0; i < part.count[0] && ok; ++i) {
+      for (int s = 0; s < 2 && ok; ++s) {
+        if (i >= part.count[s]) continue;
+        const uint32_t it = kv_n + part.at(s, i);
+        const int st = it % C::kStages;
+        if (!(ok = mbar_wait_warp(&sh->v_full[st], (it / C::kStages) & 1, fail))) break;
+        if (i == 0 && s == 0) {  // the part before has read its O
+          if (!(ok = mbar_wait_warp(&sh->o_empty, (o_n & 1) ^ 1, fail))) break;
+          ++o_n;
+        }
+        if (!(ok = mbar_wait_warp(&sh->p_full[s], p_n[s] & 1, fail))) break;
+        ++p_n[s];
+        tc_fence_after();
+        cw_issue_pv<D>(tmem + 256 + 128 * s, tmem + 128 * s, v_base + st * C::kTileBytes, i > 0, leader);
+        if (leader) {
+          if (!part.pair || s == 1) mma_commit(&sh->v_empty[st]);
+          if (i == part.count[s] - 1) mma_commit(&sh->o_full[s]);
+        }
+        if (i + 1 < part.count[s]) ok = issue_s(s, i + 1);
+      }
+    }
+    kv_n += part.n;
+  }
+  if (leader) mma_commit(&sh->drain);
+  mbar_wait_drain(&sh->drain, 0);
+}
+
+// ------------------------------------------------------ activation warps
+// S -> x for the tiles where some rows do not see some keys or the bias varies
+// (a few per item): S's columns become s S + bias (in log2 units for softmax),
+// -inf (softmax) or 0 (act(0) = 0) where the row does not see the key.
+template <int ACT>
+__device__ void cw_mask(const CacheFwdParams& p, const CacheReq& r, const CcRow& q, bool far, int key0, uint32_t t_s) {
+#pragma unroll 1
+  for (int c0 = 0; c0 < kTile; c0 += 32) {
+    uint32_t v[32];
+    tmem_ld32(t_s + c0, v);
+    tmem_ld_wait(v);
+#pragma unroll
+    for (int c = 0; c < 32; ++c) {
+      const int j = key0 + c0 + c;
+      const int depth_j = (p.window > 0 || !far) ? cc_depth(p, r, j) : 0;
+      float x = ACT == 2 ? -INFINITY : 0.f;
+      if (cc_sees(p, r, q, j, depth_j)) {
+        const float bias = far ? q.far_bias : cc_bias(p, r, q, j, depth_j) * cc_bias_unit<ACT>();
+        x = __fmaf_rn(__uint_as_float(v[c]), p.scale, bias);
+      }
+      v[c] = __float_as_uint(x);
+    }
+    tmem_st32(t_s + c0, v);
+  }
+  tmem_st_wait();
+}
+
+// P = act(s S + bias) over S's columns, two elements per packed instruction;
+// the TMEM load of the next 32 columns is in flight while these are computed.
+template <int ACT>
+__device__ __forceinline__ void cw_act_tile(uint32_t t_s, float scale, float bias) {
+  const float2 hs = f2(0.5f * scale), hb = f2(0.5f * bias);
+  uint32_t buf0[32], buf1[32];
+  tmem_ld32(t_s, buf0);
+  tmem_ld_wait(buf0);
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    uint32_t(&cur)[32] = (q & 1) ? buf1 : buf0;
+    uint32_t(&nxt)[32] = (q & 1) ? buf0 : buf1;
+    if (q < 3) tmem_ld32(t_s + 32 * (q + 1), nxt);
+    uint32_t pk[16];
+#pragma unroll
+    for (int c = 0; c < 16; ++c) {
+      const float2 hx = __ffma2_rn(make_float2(__uint_as_float(cur[2 * c]), __uint_as_float(cur[2 * c + 1])), hs, hb);
+      const float2 y = act2_route<ACT, 0>(hx);
+      pk[c] = pack_bf16(y.x, y.y);
+    }
+    tmem_st16(t_s + 16 * q, pk);  // columns [16 q, 16 q + 16) are read already
+    if (q < 3) tmem_ld_wait(nxt);
+  }
+}
+
+// P = 2^(x - m) with a running maximum that moves only when it grows by more
+// than 8 (P stays below 2^8, O and l in fp32): O is rescaled then.
+template <int D>
+__device__ __forceinline__ void cw_softmax_tile(uint32_t t_s, uint32_t t_o, float scale, float bias, bool first,
+                                                float& m, float& l) {
+  uint32_t a[32], b[32], c3[32], d4[32];
+  tmem_ld32(t_s, a);
+  tmem_ld32(t_s + 32, b);
+  tmem_ld_wait2(a, b);
+  tmem_ld32(t_s + 64, c3);
+  tmem_ld32(t_s + 96, d4);
+  tmem_ld_wait2(c3, d4);
+  float mx = -INFINITY;
+#pragma unroll
+  for (int c = 0; c < 128; c += 2) {
+    uint32_t& r0 = c < 32 ? a[c] : c < 64 ? b[c - 32] : c < 96 ? c3[c - 64] : d4[c - 96];
+    uint32_t& r1 = c < 32 ? a[c + 1] : c < 64 ? b[c - 31] : c < 96 ? c3[c - 63] : d4[c - 95];
+    const float2 x = __ffma2_rn(make_float2(__uint_as_float(r0), __uint_as_float(r1)), f2(scale), f2(bias));
+    r0 = __float_as_uint(x.x);
+    r1 = __float_as_uint(x.y);
+    mx = fmaxf(mx, fmaxf(x.x, x.y));
+  }
+  const bool grow = mx > m + 8.0f;
+  const float factor = grow ? ex2_sfu(m - mx) : 1.0f;  // 0 on the first tile
+  if (grow) m = mx;
+  l *= factor;
+  const float2 neg = f2(m == -INFINITY ? 0.f : -m);  // no key seen so far: every x is -inf and P is 0
+  float2 sum = f2(0.f);
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    uint32_t(&src)[32] = q == 0 ? a : q == 1 ? b : q == 2 ? c3 : d4;
+    uint32_t pk[16];
+#pragma unroll
+    for (int c = 0; c < 16; ++c) {
+      const float2 z = __fadd2_rn(make_float2(__uint_as_float(src[2 * c]), __uint_as_float(src[2 * c + 1])), neg);
+      const float2 e = make_float2(ex2_sfu(z.x), ex2_sfu(z.y));
+      sum = __fadd2_rn(sum, e);
+      pk[c] = pack_bf16(e.x, e.y);
+    }
+    tmem_st16(t_s + 16 * q, pk);
+  }
+  l += sum.x + sum.y;
+  if (!first && __any_sync(0xffffffffu, grow)) {
+#pragma unroll
+    for (int c0 = 0; c0 < D; c0 += 32) {
+      uint32_t o[32];
+      tmem_ld32(t_o + c0, o);
+      tmem_ld_wait(o);
+#pragma unroll
+      for (int i = 0; i < 32; i += 2) {
+        const float2 v = __fmul2_rn(make_float2(__uint_as_float(o[i]), __uint_as_float(o[i + 1])), f2(factor));
+        o[i] = __float_as_uint(v.x);
+        o[i + 1] = __float_as_uint(v.y);
+      }
+      tmem_st32(t_o + c0, o);
+    }
+  }
+}
+
+// Adds what the product left out: infinities and NaN in V of keys in the
+// part's masked tiles, for the rows that see them, to columns [c0, c0 + 16) of
+// a row.  Rare, so it works from global memory.
+template <int D, int ACT>
+__device__ __noinline__ void cw_add_odd(const CacheFwdParams& p, const CacheReq& r, const CcRow& q, const __nv_bfloat16* kc,
+                                        const __nv_bfloat16* vc, const int32_t* pages, int64_t k_stride, int64_t v_stride,
+                                        int key, int c0, float* o) {
+  const int page = __ldg(pages + (key >> p.page_shift));
+  if (static_cast<uint32_t>(page) >= static_cast<uint32_t>(p.num_pages)) return;
+  const int depth_j = cc_depth(p, r, key);
+  if (!cc_sees(p, r, q, key, depth_j)) return;
+  const int64_t place = static_cast<int64_t>(key & ((1 << p.page_shift) - 1)) * p.kv_heads * D;
+  const __nv_bfloat16* v = vc + page * v_stride + place;
+  bool any = false;
+  for (int c = 0; c < 16; ++c) any = any || !isfinite(__bfloat162float(v[c0 + c]));
+  if (!any) return;
+  float weight = 1.f;  // softmax weights are positive
+  if constexpr (ACT != 2) {
+    const __nv_bfloat16* k = kc + page * k_stride + place;
+    const __nv_bfloat16* qr = p.q + static_cast<int64_t>(r.q0 + q.t) * p.q_stride + static_cast<int64_t>(q.head) * D;
+    float x = 0.f;
+    for (int c = 0; c < D; ++c) x = __fmaf_rn(__bfloat162float(k[c]), __bfloat162float(qr[c]), x);
+    x *= p.scale;
+    if (p.bias_len) x += cc_bias(p, r, q, key, depth_j);
+    weight = cc_act<ACT>(x);
+  }
+  for (int c = 0; c < 16; ++c) {
+    const float x = __bfloat162float(v[c0 + c]);
+    if (!isfinite(x)) o[c] += weight * x;
+  }
+}
+
+template <int D, int ACT>
+__device__ void cw_consumer(const CacheFwdParams& p, uint8_t* smem, CwShared* sh, uint32_t tmem, int stream,
+                            const CacheRange& R, Fail fail) {
+  using C = CwCfg<D>;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int row = (warp & 3) * 32 + lane;  // row of the tile, and key row of V for the zeroing
+  const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
+  const uint32_t t_s = tmem + lane_off + 128 * stream, t_o = tmem + lane_off + 256;
+  const uint32_t v_base = smem_u32(smem + C::kVOff);
+  const int reach = (p.bias_len - 1) / 2;
+  uint32_t kv_n = 0, s_n = 0, o_n[2] = {0, 0};
+  int number = 0;  // of the part with tiles, from 1
+  int ml_at = 0;
+  bool dead = false;
+  CacheWalk w;
+  w.init(R);
+  for (; w.next<kTile>(p); w.advance()) {
+    const CwPart part(p, w);
+    const CacheReq& r = w.r;
+    if (part.n > 0) ++number;  // (a warpgroup is at most one such part ahead of the other: O is shared)
+    const int block_row0 = w.row_tile * p.rows_per_tile;
+    const int my_rows = part.pair ? (stream == 0 ? part.tile_rows : part.rows - part.tile_rows) : part.rows;
+    const bool row_ok = row < my_rows;
+    const int flat = block_row0 + (part.pair ? stream * part.tile_rows : 0) + row;
+    CcRow q;
+    q.t = row_ok ? flat / p.group : -1;
+    q.head = w.h * p.group + (row_ok ? flat % p.group : 0);
+    q.pos = r.C + (row_ok ? (p.depth != nullptr ? __ldg(p.depth + r.q0 + q.t) : q.t) : 0);
+    q.far_bias = 0.f;
+    if (row_ok && p.bias_len)
+      q.far_bias = __ldg(p.bias + static_cast<int64_t>(q.head) * p.bias_len + 2 * reach) * cc_bias_unit<ACT>();
+    // over all rows of the part, the same in every warp
+    const int first_token = block_row0 / p.group, last_token = (block_row0 + part.rows - 1) / p.group;
+    int far_depth = last_token;
+    if (p.window > 0 && p.depth != nullptr) {
+      far_depth = 0;
+      for (int t = first_token + lane; t <= last_token; t += 32) far_depth = max(far_depth, __ldg(p.depth + r.q0 + t));
+      far_depth = __reduce_max_sync(0xffffffffu, far_depth);
+    }
+    // A tile is plain when every row sees all of its keys.  (The same answer
+    // for both streams: they take V from one tile.)
+    auto plain_tile = [&](int key0) {
+      const int last = key0 + kTile - 1;
+      if (p.window > 0) return last < r.C && static_cast<int64_t>(r.C) + far_depth - key0 < p.window;
+      return p.mask != nullptr ? last < r.C : last <= r.C + first_token && last < r.L;
+    };
+    const bool warp_live = (warp & 3) * 32 < my_rows;
+    float m = -INFINITY, l = 0.f;
+    for (int i = 0; i < part.count[stream]; ++i) {
+      const uint32_t it = kv_n + part.at(stream, i);
+      const int key0 = (part.lo + part.at(stream, i)) * kTile;
+      if (!dead && !mbar_wait(&sh->s_full[stream], s_n & 1, fail)) dead = true;
+      dead = __any_sync(0xffffffffu, dead);
+      ++s_n;
+      if (dead) continue;
+      tc_fence_after();
+      const bool plain = plain_tile(key0);
+      float scale = p.scale, bias = q.far_bias;
+      if (warp_live) {
+        const bool far = p.bias_len == 0 || (key0 + kTile - 1 < r.C && r.C - (key0 + kTile - 1) >= reach);
+        if (!plain || !far) {
+          cw_mask<ACT>(p, r, q, far, key0, t_s);
+          scale = 1.f;
+          bias = 0.f;
+        }
+        if constexpr (ACT == 2) cw_softmax_tile<D>(t_s, t_o + 128 * stream, scale, bias, i == 0, m, l);
+        else cw_act_tile<ACT>(t_s, scale, bias);
+        tmem_st_wait();
+      }
+      if (!plain) {
+        // 0 * NaN = NaN: V rows past the request's end are zeroed (the page
+        // or an earlier tile may have left anything there), and infinities and
+        // NaN of the others are taken out; the epilogue adds them to the rows
+        // that see them.
+        const int st = it % C::kStages;
+        if (!mbar_wait(&sh->v_full[st], (it / C::kStages) & 1, fail)) dead = true;
+        dead = __any_sync(0xffffffffu, dead);
+        if (dead) continue;
+        const uint32_t vr = v_base + st * C::kTileBytes + row * C::kRowBytes;
+        const bool past = key0 + row >= r.L;
+#pragma unroll 4
+        for (int c = 0; c < D / 8; ++c) {  // (the order of the swizzled pieces does not matter)
+          const uint32_t a = vr + (c / (C::kBlockCols / 8)) * C::kBlockBytes + (c % (C::kBlockCols / 8)) * 16;
+          uint32_t x[4];
+          ld_shared_v4(a, x[0], x[1], x[2], x[3]);
+          uint32_t bad = 0;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const uint32_t f = past ? 0xFFFFFFFFu : cc_nonfinite(x[e]);
+            bad |= f;
+            x[e] &= ~f;
+          }
+          if (bad) {
+            if (!past) {
+              *const_cast<volatile int*>(&sh->odd[number & 1]) = number;
+              __threadfence_block();
+            }
+            st_shared_v4(a, x[0], x[1], x[2], x[3]);
+          }
+        }
+        fence_proxy_async_smem();
+      }
+      tc_fence_before();
+      mbar_arrive_warp(&sh->p_full[stream]);
+    }
+    kv_n += part.n;
+
+    // the part's end
+    int o_col = 0, o_cols = D;  // columns this warpgroup writes
+    float f[2] = {1.f, 1.f};    // factors of the streams' O
+    bool use[2] = {false, false};
+    if (part.n > 0) {
+      use[0] = !part.pair || stream == 0;
+      use[1] = part.pair ? stream == 1 : part.count[1] > 0;
+      if (!part.pair) {  // both streams' rows are the same: each warpgroup joins and writes half the columns
+        o_col = stream * (D / 2);
+        o_cols = D / 2;
+        if constexpr (ACT == 2) {
+          sh->ml[ml_at][stream][row] = make_float2(m, l);
+          named_bar(1, 256);
+          const float2 other = sh->ml[ml_at][stream ^ 1][row];
+          ml_at ^= 1;
+          const float top = fmaxf(m, other.x), ref = top == -INFINITY ? 0.f : top;
+          f[stream] = ex2_sfu(m - ref);
+          f[stream ^ 1] = ex2_sfu(other.x - ref);
+          // (in stream order, so that both warpgroups get the same bits)
+          const float l0 = stream == 0 ? l : other.y, l1 = stream == 0 ? other.y : l;
+          l = __fmaf_rn(l0, f[0], l1 * f[1]);
+          m = top;
+        }
+      }
+      for (int s = 0; s < 2; ++s) {
+        if (part.count[s] == 0) continue;
+        if (use[s] && !dead && !mbar_wait(&sh->o_full[s], o_n[s] & 1, fail)) dead = true;
+        ++o_n[s];
+      }
+      dead = __any_sync(0xffffffffu, dead);
+    }
+    if (!dead) {
+      tc_fence_after();
+      const bool odd = part.n > 0 && *const_cast<volatile int*>(&sh->odd[number & 1]) == number;
+      const float inv = ACT != 2 || !w.whole ? 1.f : (l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l));
+      const int64_t token = r.q0 + (row_ok ? q.t : 0);
+      __nv_bfloat16* dst = p.out + (token * p.heads + q.head) * D;
+      const int64_t prow = (2 * static_cast<int64_t>(blockIdx.x) + (w.first ? 0 : 1)) * p.rows_per_tile + (flat - block_row0);
+      for (int c0 = o_col; c0 < o_col + o_cols; c0 += 16) {
+        float o[16];
+        uint32_t x[16];
+#pragma unroll
+        for (int c = 0; c < 16; ++c) o[c] = 0.f;
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+          if (!use[s]) continue;
+          tmem_ld16(t_o + 128 * s + c0, x);
+          tmem_ld_wait16(x);
+#pragma unroll
+          for (int c = 0; c < 16; ++c) o[c] = __fmaf_rn(__uint_as_float(x[c]), f[s], o[c]);
+        }
+        if (odd && row_ok) {
+          const int32_t* pages = p.table + static_cast<int64_t>(w.b) * p.width;
+          for (int t = part.lo; t < part.lo + part.n; ++t) {
+            if (plain_tile(t * kTile)) continue;
+            for (int j = t * kTile; j < min(r.L, (t + 1) * kTile); ++j)
+              cw_add_odd<D, ACT>(p, r, q, p.k_cache + w.h * D, p.v_cache + w.h * D, pages, p.k_page_stride,
+                                 p.v_page_stride, j, c0, o);
+          }
+        }
+        if (row_ok) {
+          if (w.whole) {
+            uint32_t pk[8];
+#pragma unroll
+            for (int c = 0; c < 8; ++c) pk[c] = pack_bf16(o[2 * c] * inv, o[2 * c + 1] * inv);
+            st_global_v4(dst + c0, pk[0], pk[1], pk[2], pk[3]);
+            st_global_v4(dst + c0 + 8, pk[4], pk[5], pk[6], pk[7]);
+          } else {
+#pragma unroll
+            for (int c = 0; c < 16; c += 4)
+              *reinterpret_cast<float4*>(p.part_o + prow * D + c0 + c) = make_float4(o[c], o[c + 1], o[c + 2], o[c + 3]);
+          }
+        }
+        __syncwarp();
+      }
+      if (ACT == 2 && row_ok && o_col == 0) {
+        if (!w.whole) p.part_ml[prow] = make_float2(m, l);
+        else if (p.lse != nullptr)
+          p.lse[static_cast<int64_t>(q.head) * p.total_q + token] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+      }
+    }
+    if (part.n > 0) {
+      tc_fence_before();
+      mbar_arrive_warp(&sh->o_empty);
+    }
+  }
+}
+
+template <int D, int ACT>
+__global__ void __launch_bounds__(kWideThreads, 1) cache_fwd_wide_kernel(const __grid_constant__ CacheFwdParams p) {
+  using C = CwCfg<D>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  CwShared* sh = reinterpret_cast<CwShared*>(smem + C::kBarOff);
+  const int warp = threadIdx.x >> 5;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&sh->q_full[s], 1);
+      mbar_init(&sh->q_empty[s], 1);
+      mbar_init(&sh->s_full[s], 1);
+      mbar_init(&sh->p_full[s], 4);
+      mbar_init(&sh->o_full[s], 1);
+    }
+    for (int s = 0; s < C::kStages; ++s) {
+      mbar_init(&sh->k_full[s], 1);
+      mbar_init(&sh->k_empty[s], 1);
+      mbar_init(&sh->v_full[s], 1);
+      mbar_init(&sh->v_empty[s], 1);
+    }
+    mbar_init(&sh->o_empty, 8);
+    mbar_init(&sh->drain, 1);
+    sh->abort = 0;
+    sh->odd[0] = sh->odd[1] = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(&sh->tmem_base, 512);
+    tmem_relinquish();
+  }
+  const CacheRange R = cache_range<kTile>(p, &sh->range, kWideMinTiles);
+  if (threadIdx.x == 0) cache_open<kTile>(p, R);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sh->tmem_base;
+  Fail fail{&sh->abort, p.err + blockIdx.x, p.wait_limit_ns};
+  if (warp == 0) cw_producer<D>(p, smem, sh, R, fail);
+  else if (warp == 1) cw_mma<D>(p, smem, sh, tmem, R, fail);
+  else if (warp >= 4) cw_consumer<D, ACT>(p, smem, sh, tmem, (warp - 4) >> 2, R, fail);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc(tmem, 512);
+}
+
+// ------------------------------------------------------------------ launch
+#ifndef JGDPA_HEAD_DIM
+#error "compile cache_fwd_wide.cu with -DJGDPA_HEAD_DIM=32, 64 or 128"
+#endif
+
+template <int D, int ACT>
+static cudaError_t launch_cw(const CacheFwdParams& p, int grid, cudaStream_t stream) {
+  auto kern = cache_fwd_wide_kernel<D, ACT>;
+  constexpr int kSmem = CwCfg<D>::kSmemBytes;
+  static DeviceFlags attr_set = {};
+  cudaError_t e = smem_attr_once(kern, kSmem, attr_set);
+  if (e != cudaSuccess) return e;
+  kern<<<grid, kWideThreads, kSmem, stream>>>(p);
+  return cudaGetLastError();
+}
+
+template <int D>
+cudaError_t launch_cache_fwd_wide_d(const CacheFwdParams& p, int act, int grid, cudaStream_t stream) {
+  if (act == 0) return launch_cw<D, 0>(p, grid, stream);
+  if (act == 1) return launch_cw<D, 1>(p, grid, stream);
+  return launch_cw<D, 2>(p, grid, stream);
+}
+template cudaError_t launch_cache_fwd_wide_d<JGDPA_HEAD_DIM>(const CacheFwdParams&, int, int, cudaStream_t);
+
+}  // namespace jg
