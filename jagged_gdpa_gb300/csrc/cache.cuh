@@ -283,38 +283,44 @@ __device__ __forceinline__ uint32_t cc_nonfinite(uint32_t v) {
   return ((v & 0x7F80u) == 0x7F80u ? 0xFFFFu : 0u) | ((v & 0x7F800000u) == 0x7F800000u ? 0xFFFF0000u : 0u);
 }
 
-// Whether a row sees key j.
-__device__ __forceinline__ bool cc_sees(const CacheFwdParams& p, const CacheReq& r, const CcRow& q, int j, int depth_j) {
-  if (q.t < 0 || j >= r.L) return false;
-  const int u = j - r.C;
-  if (u >= 0) {
-    if (p.mask != nullptr) {
-      const uint32_t word = __ldg(p.mask + static_cast<int64_t>(r.q0 + q.t) * p.mask_words + (u >> 5));
-      if (!((word >> (u & 31)) & 1)) return false;
-    } else if (u > q.t) {
-      return false;
-    }
-  }
-  if (p.window > 0) {
-    const int64_t apart = static_cast<int64_t>(q.pos) - (u >= 0 ? static_cast<int64_t>(r.C) + depth_j : j);
-    if (apart >= p.window || -apart >= p.window) return false;
-  }
-  return true;
-}
-
-// The bias table's entry for a row and key j.
-__device__ __forceinline__ float cc_bias(const CacheFwdParams& p, const CacheReq& r, const CcRow& q, int j, int depth_j) {
-  const int64_t reach = (p.bias_len - 1) / 2;
-  const int64_t apart = static_cast<int64_t>(q.pos) - (j >= r.C ? static_cast<int64_t>(r.C) + depth_j : j);
-  const int at = static_cast<int>(min(max(apart, -reach), reach) + reach);
-  return __ldg(p.bias + static_cast<int64_t>(q.head) * p.bias_len + at);
-}
-
 // The depth of key j's token (0 for the context).
 __device__ __forceinline__ int cc_depth(const CacheFwdParams& p, const CacheReq& r, int j) {
   const int u = j - r.C;
   if (u < 0 || j >= r.L) return 0;
   return p.depth != nullptr ? __ldg(p.depth + r.q0 + u) : u;
+}
+// Its position.
+__device__ __forceinline__ int cc_pos(const CacheFwdParams& p, const CacheReq& r, int j) {
+  return j < r.C ? j : r.C + cc_depth(p, r, j);
+}
+
+__device__ __forceinline__ uint32_t cc_ones(int n) { return n >= 32 ? 0xFFFFFFFFu : (n <= 0 ? 0u : (1u << n) - 1u); }
+
+// Which of the keys key0 .. key0 + 31 a row sees by length and mask (bit c:
+// key0 + c), whatever the window.
+__device__ __forceinline__ uint32_t cc_vis32(const CacheFwdParams& p, const CacheReq& r, const CcRow& q, int key0) {
+  if (q.t < 0) return 0u;
+  if (p.mask == nullptr) return cc_ones(min(r.L, r.C + q.t + 1) - key0);
+  const int u0 = key0 - r.C;
+  uint32_t bits = 0xFFFFFFFFu;
+  if (u0 > -32) {  // words i and i + 1 of the row's mask, the context's ones before the first
+    const int32_t* words = p.mask + static_cast<int64_t>(r.q0 + q.t) * p.mask_words;
+    const int i = u0 >> 5;
+    const uint32_t lo = i < 0 ? 0xFFFFFFFFu : (i < p.mask_words ? static_cast<uint32_t>(__ldg(words + i)) : 0u);
+    const uint32_t hi = i + 1 < p.mask_words ? static_cast<uint32_t>(__ldg(words + i + 1)) : 0u;
+    bits = __funnelshift_r(lo, hi, u0 & 31);
+  }
+  return bits & cc_ones(r.L - key0);
+}
+// Whether the window joins a row and a key, by their positions.
+__device__ __forceinline__ bool cc_near(const CacheFwdParams& p, int pos, int key_pos) {
+  const int apart = pos - key_pos;
+  return p.window <= 0 || (apart < p.window && apart > -p.window);
+}
+// The bias table's entry of a row for a key position (any position: the index is clamped).
+__device__ __forceinline__ float cc_bias(const CacheFwdParams& p, const CcRow& q, int reach, int key_pos) {
+  const int at = min(max(q.pos - key_pos, -reach), reach) + reach;
+  return __ldg(p.bias + static_cast<int64_t>(q.head) * p.bias_len + at);
 }
 
 // x innermost: columns, rows of the page, column halves, heads, pages

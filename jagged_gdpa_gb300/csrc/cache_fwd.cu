@@ -237,18 +237,24 @@ __device__ void cc_consumer(const CacheFwdParams& p, uint8_t* smem, CcShared* sh
 #pragma unroll
             for (int e = 0; e < 4; ++e) s[i][e] = __fmaf_rn(s[i][e], p.scale, rows[e >> 1].far_bias);
         } else {
+          // (written without branches, so that the loads run side by side)
+          const uint32_t see[2] = {cc_vis32(p, r, rows[0], key0), cc_vis32(p, r, rows[1], key0)};
 #pragma unroll
           for (int i = 0; i < 2; ++i)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const CcRow& q = rows[e >> 1];
-              const int j = key0 + 8 * i + 2 * (lane & 3) + (e & 1);
-              const int depth_j = cc_depth(p, r, j);
-              const bool sees = cc_sees(p, r, q, j, depth_j);
-              float x = s[i][e] * p.scale;
-              if (p.bias_len && sees) x = __fmaf_rn(cc_bias(p, r, q, j, depth_j), cc_bias_unit<ACT>(), x);
-              s[i][e] = sees ? x : (ACT == 2 ? -INFINITY : 0.f);  // act(0) = 0
-              vis |= (sees ? 1u : 0u) << (4 * i + e);
+            for (int c = 0; c < 2; ++c) {
+              const int col = 8 * i + 2 * (lane & 3) + c;
+              const int key_pos = cc_pos(p, r, key0 + col);
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                const CcRow& q = rows[h];
+                const bool sees = ((see[h] >> col) & 1) && cc_near(p, q.pos, key_pos);
+                float bias = q.far_bias;
+                if (!far) bias = cc_bias(p, q, bias_reach, key_pos) * cc_bias_unit<ACT>();
+                const float x = __fmaf_rn(s[i][2 * h + c], p.scale, bias);
+                s[i][2 * h + c] = sees ? x : (ACT == 2 ? -INFINITY : 0.f);  // act(0) = 0
+                vis |= (sees ? 1u : 0u) << (4 * i + 2 * h + c);
+              }
             }
         }
         if constexpr (ACT == 2) {

@@ -248,24 +248,39 @@ __device__ void cw_mma(const CacheFwdParams& p, uint8_t* smem, CwShared* sh, uin
 // S -> x for the tiles where some rows do not see some keys or the bias varies
 // (a few per item): S's columns become s S + bias (in log2 units for softmax),
 // -inf (softmax) or 0 (act(0) = 0) where the row does not see the key.
+// (Without branches per element: 128 of them, each with its loads in a row,
+// took some 40 us a tile.)
 template <int ACT>
-__device__ void cw_mask(const CacheFwdParams& p, const CacheReq& r, const CcRow& q, bool far, int key0, uint32_t t_s) {
+__device__ void cw_mask(const CacheFwdParams& p, const CacheReq& r, const CcRow& q, bool far, int reach, int key0,
+                        uint32_t t_s) {
+  const int lane = threadIdx.x & 31;
 #pragma unroll 1
   for (int c0 = 0; c0 < kTile; c0 += 32) {
     uint32_t v[32];
     tmem_ld32(t_s + c0, v);
-    tmem_ld_wait(v);
+    uint32_t see = cc_vis32(p, r, q, key0 + c0);
+    // lane c: the position of key c0 + c
+    const int my_pos = (p.window > 0 || !far) ? cc_pos(p, r, key0 + c0 + lane) : 0;
+    if (p.window > 0) {
+      uint32_t near = 0;
 #pragma unroll
-    for (int c = 0; c < 32; ++c) {
-      const int j = key0 + c0 + c;
-      const int depth_j = (p.window > 0 || !far) ? cc_depth(p, r, j) : 0;
-      float x = ACT == 2 ? -INFINITY : 0.f;
-      if (cc_sees(p, r, q, j, depth_j)) {
-        const float bias = far ? q.far_bias : cc_bias(p, r, q, j, depth_j) * cc_bias_unit<ACT>();
-        x = __fmaf_rn(__uint_as_float(v[c]), p.scale, bias);
-      }
-      v[c] = __float_as_uint(x);
+      for (int c = 0; c < 32; ++c) near |= (cc_near(p, q.pos, __shfl_sync(0xffffffffu, my_pos, c)) ? 1u : 0u) << c;
+      see &= near;
     }
+    tmem_ld_wait(v);
+    if (far) {
+#pragma unroll
+      for (int c = 0; c < 32; ++c) v[c] = __float_as_uint(__fmaf_rn(__uint_as_float(v[c]), p.scale, q.far_bias));
+    } else {
+#pragma unroll
+      for (int c = 0; c < 32; ++c) {
+        const float bias = cc_bias(p, q, reach, __shfl_sync(0xffffffffu, my_pos, c)) * cc_bias_unit<ACT>();
+        v[c] = __float_as_uint(__fmaf_rn(__uint_as_float(v[c]), p.scale, bias));
+      }
+    }
+#pragma unroll
+    for (int c = 0; c < 32; ++c)
+      if (!((see >> c) & 1)) v[c] = ACT == 2 ? 0xFF800000u : 0u;  // -inf, or act(0) = 0
     tmem_st32(t_s + c0, v);
   }
   tmem_st_wait();
@@ -364,8 +379,8 @@ __device__ __noinline__ void cw_add_odd(const CacheFwdParams& p, const CacheReq&
                                         int key, int c0, float* o) {
   const int page = __ldg(pages + (key >> p.page_shift));
   if (static_cast<uint32_t>(page) >= static_cast<uint32_t>(p.num_pages)) return;
-  const int depth_j = cc_depth(p, r, key);
-  if (!cc_sees(p, r, q, key, depth_j)) return;
+  const int key_pos = cc_pos(p, r, key);
+  if (!(cc_vis32(p, r, q, key) & 1) || !cc_near(p, q.pos, key_pos)) return;
   const int64_t place = static_cast<int64_t>(key & ((1 << p.page_shift) - 1)) * p.kv_heads * D;
   const __nv_bfloat16* v = vc + page * v_stride + place;
   bool any = false;
@@ -378,7 +393,7 @@ __device__ __noinline__ void cw_add_odd(const CacheFwdParams& p, const CacheReq&
     float x = 0.f;
     for (int c = 0; c < D; ++c) x = __fmaf_rn(__bfloat162float(k[c]), __bfloat162float(qr[c]), x);
     x *= p.scale;
-    if (p.bias_len) x += cc_bias(p, r, q, key, depth_j);
+    if (p.bias_len) x += cc_bias(p, q, (p.bias_len - 1) / 2, key_pos);
     weight = cc_act<ACT>(x);
   }
   for (int c = 0; c < 16; ++c) {
@@ -448,7 +463,7 @@ __device__ void cw_consumer(const CacheFwdParams& p, uint8_t* smem, CwShared* sh
       if (warp_live) {
         const bool far = p.bias_len == 0 || (key0 + kTile - 1 < r.C && r.C - (key0 + kTile - 1) >= reach);
         if (!plain || !far) {
-          cw_mask<ACT>(p, r, q, far, key0, t_s);
+          cw_mask<ACT>(p, r, q, far, reach, key0, t_s);
           scale = 1.f;
           bias = 0.f;
         }
