@@ -473,11 +473,11 @@ __global__ void __launch_bounds__(kCThreads, 1) cache_fwd_kernel(const __grid_co
       mbar_init(&sh->empty[s], MT == 2 ? kCWarps : kCGroupWarps);
     }
     sh->abort = 0;
+    p.err[blockIdx.x] = kOk;
     fence_mbar_init();
   }
-  const CacheRange R = cache_range<kCKeys>(p, &sh->range, kCMinTiles);
-  if (threadIdx.x == 0) cache_open<kCKeys>(p, R);
-  __syncthreads();
+  const CacheRange R = cache_range<kCKeys>(p, &sh->range, kCMinTiles);  // (ends in a barrier)
+  if (threadIdx.x == (kCWarps - 1) * 32) cache_open<kCKeys>(p, R);
   Fail fail{&sh->abort, p.err + blockIdx.x, p.wait_limit_ns};
   if (threadIdx.x >= kCWarps * 32) cc_producer<D>(p, smem, sh, R, fail);
   else cc_consumer<D, ACT, MT>(p, smem, sh, R, fail);

@@ -21,8 +21,9 @@
 // per product); a part with fewer gives both streams the same rows and every
 // other key tile, and joins their O, maxima and sums at its end.
 //
-// Warps: 0 TMA producer, 1 MMA issuer (owns tensor memory), 4-7 and 8-11 the
-// streams' activation and epilogue (one row per thread).
+// Warps: 0 TMA producer, 1 MMA issuer (owns tensor memory), 2-3 the masked
+// tiles' V, 4-7 and 8-11 the streams' activation and epilogue (one row per
+// thread).
 // TMEM: S_s at 128 s, O_s at 256 + 128 s.
 #include "act.cuh"
 #include "cache.cuh"
@@ -56,12 +57,13 @@ struct CwShared {
   uint64_t q_full[2], q_empty[2];
   uint64_t k_full[8], k_empty[8], v_full[8], v_empty[8];
   uint64_t s_full[2], p_full[2], o_full[2];
+  uint64_t v_fixed[8];     // masked tiles only: a stage's next one comes after its product
   uint64_t o_empty, drain;
   CacheRangeShared range;
   float2 ml[2][2][kTile];  // [part parity][stream][row]: maximum and sum
   uint32_t tmem_base;
   int abort;
-  int odd[2];              // by parity: number of the last part whose masked tiles hold a V that is not finite
+  int odd[16];             // number of the last part (mod 16) whose masked tiles hold a V that is not finite
 };
 static_assert(sizeof(CwShared) <= 8192, "shared block");
 
@@ -84,6 +86,22 @@ struct CwPart {
     pair = rows > tile_rows;
     count[0] = pair ? n : (n + 1) / 2;
     count[1] = pair ? n : n / 2;
+  }
+  // The largest depth of the part's rows (whole warp).
+  __device__ __forceinline__ int far_depth(const CacheFwdParams& p, const CacheWalk& w) const {
+    const int64_t row0 = static_cast<int64_t>(w.row_tile) * p.rows_per_tile;
+    const int first = static_cast<int>(row0 / p.group), last = static_cast<int>((row0 + rows - 1) / p.group);
+    if (p.window <= 0 || p.depth == nullptr) return last;
+    int d = 0;
+    for (int t = first + (threadIdx.x & 31); t <= last; t += 32) d = max(d, __ldg(p.depth + w.r.q0 + t));
+    return __reduce_max_sync(0xffffffffu, d);
+  }
+  // A tile is plain when every row of the part sees all of its keys.
+  __device__ __forceinline__ bool plain(const CacheFwdParams& p, const CacheWalk& w, int far_depth, int key0) const {
+    const int last = key0 + kTile - 1;
+    if (p.window > 0) return last < w.r.C && static_cast<int64_t>(w.r.C) + far_depth - key0 < p.window;
+    if (p.mask != nullptr) return last < w.r.C;
+    return last < w.r.L && last <= w.r.C + static_cast<int>(static_cast<int64_t>(w.row_tile) * p.rows_per_tile / p.group);
   }
   // the part's tile that stream s takes as its i-th
   __device__ __forceinline__ int at(int s, int i) const { return pair ? i : 2 * i + s; }
@@ -191,6 +209,7 @@ __device__ void cw_mma(const CacheFwdParams& p, uint8_t* smem, CwShared* sh, uin
   const uint32_t q_base = smem_u32(smem + C::kQOff), k_base = smem_u32(smem + C::kKOff),
                  v_base = smem_u32(smem + C::kVOff);
   const bool leader = elect_one();
+  uint32_t fixed = 0;  // bit st: parity of stage st's masked tiles so far
   uint32_t q_n = 0, kv_n = 0, o_n = 0, p_n[2] = {0, 0};
   bool ok = true;
   CacheWalk w;
@@ -198,6 +217,7 @@ __device__ void cw_mma(const CacheFwdParams& p, uint8_t* smem, CwShared* sh, uin
   for (; ok && w.next<kTile>(p); w.advance()) {
     const CwPart part(p, w);
     if (part.n == 0) continue;
+    const int far_depth = part.far_depth(p, w);
     const uint32_t slot[2] = {q_n & 1, part.pair ? (q_n + 1) & 1 : q_n & 1};
     for (int s = 0; s < (part.pair ? 2 : 1) && ok; ++s, ++q_n) ok = mbar_wait_warp(&sh->q_full[q_n & 1], (q_n >> 1) & 1, fail);
     if (!ok) break;
@@ -229,6 +249,11 @@ __device__ void cw_mma(const CacheFwdParams& p, uint8_t* smem, CwShared* sh, uin
         }
         if (!(ok = mbar_wait_warp(&sh->p_full[s], p_n[s] & 1, fail))) break;
         ++p_n[s];
+        // V of a masked tile, once for both streams
+        if ((!part.pair || s == 0) && !part.plain(p, w, far_depth, (part.lo + part.at(s, i)) * kTile)) {
+          if (!(ok = mbar_wait_warp(&sh->v_fixed[st], (fixed >> st) & 1, fail))) break;
+          fixed ^= 1u << st;
+        }
         tc_fence_after();
         cw_issue_pv<D>(tmem + 256 + 128 * s, tmem + 128 * s, v_base + st * C::kTileBytes, i > 0, leader);
         if (leader) {
@@ -245,42 +270,41 @@ __device__ void cw_mma(const CacheFwdParams& p, uint8_t* smem, CwShared* sh, uin
 }
 
 // ------------------------------------------------------ activation warps
-// S -> x for the tiles where some rows do not see some keys or the bias varies
-// (a few per item): S's columns become s S + bias (in log2 units for softmax),
-// -inf (softmax) or 0 (act(0) = 0) where the row does not see the key.
-// (Without branches per element: 128 of them, each with its loads in a row,
-// took some 40 us a tile.)
+// Which of a tile's 128 keys a row sees (bit c of word q: key0 + 32 q + c).
+__device__ __forceinline__ void cw_visible(const CacheFwdParams& p, const CacheReq& r, const CcRow& q, int key0,
+                                           uint32_t (&see)[4]) {
+#pragma unroll
+  for (int k = 0; k < 4; ++k) see[k] = cc_vis32(p, r, q, key0 + 32 * k);
+  if (p.window > 0) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int my_pos = cc_pos(p, r, key0 + 32 * k + lane);  // lane c: of key c
+      uint32_t near = 0;
+#pragma unroll
+      for (int c = 0; c < 32; ++c) near |= (cc_near(p, q.pos, __shfl_sync(0xffffffffu, my_pos, c)) ? 1u : 0u) << c;
+      see[k] &= near;
+    }
+  }
+}
+
+// S -> s S + bias (in log2 units for softmax) for the tiles near the new
+// tokens, where the bias varies from key to key.
 template <int ACT>
-__device__ void cw_mask(const CacheFwdParams& p, const CacheReq& r, const CcRow& q, bool far, int reach, int key0,
-                        uint32_t t_s) {
+__device__ __forceinline__ void cw_bias_tile(const CacheFwdParams& p, const CacheReq& r, const CcRow& q, int reach,
+                                             int key0, uint32_t t_s) {
   const int lane = threadIdx.x & 31;
 #pragma unroll 1
   for (int c0 = 0; c0 < kTile; c0 += 32) {
     uint32_t v[32];
     tmem_ld32(t_s + c0, v);
-    uint32_t see = cc_vis32(p, r, q, key0 + c0);
-    // lane c: the position of key c0 + c
-    const int my_pos = (p.window > 0 || !far) ? cc_pos(p, r, key0 + c0 + lane) : 0;
-    if (p.window > 0) {
-      uint32_t near = 0;
+    const int my_pos = cc_pos(p, r, key0 + c0 + lane);  // lane c: of key c0 + c
+    float bias[32];
 #pragma unroll
-      for (int c = 0; c < 32; ++c) near |= (cc_near(p, q.pos, __shfl_sync(0xffffffffu, my_pos, c)) ? 1u : 0u) << c;
-      see &= near;
-    }
+    for (int c = 0; c < 32; ++c) bias[c] = cc_bias(p, q, reach, __shfl_sync(0xffffffffu, my_pos, c)) * cc_bias_unit<ACT>();
     tmem_ld_wait(v);
-    if (far) {
 #pragma unroll
-      for (int c = 0; c < 32; ++c) v[c] = __float_as_uint(__fmaf_rn(__uint_as_float(v[c]), p.scale, q.far_bias));
-    } else {
-#pragma unroll
-      for (int c = 0; c < 32; ++c) {
-        const float bias = cc_bias(p, q, reach, __shfl_sync(0xffffffffu, my_pos, c)) * cc_bias_unit<ACT>();
-        v[c] = __float_as_uint(__fmaf_rn(__uint_as_float(v[c]), p.scale, bias));
-      }
-    }
-#pragma unroll
-    for (int c = 0; c < 32; ++c)
-      if (!((see >> c) & 1)) v[c] = ACT == 2 ? 0xFF800000u : 0u;  // -inf, or act(0) = 0
+    for (int c = 0; c < 32; ++c) v[c] = __float_as_uint(__fmaf_rn(__uint_as_float(v[c]), p.scale, bias[c]));
     tmem_st32(t_s + c0, v);
   }
   tmem_st_wait();
@@ -288,8 +312,9 @@ __device__ void cw_mask(const CacheFwdParams& p, const CacheReq& r, const CcRow&
 
 // P = act(s S + bias) over S's columns, two elements per packed instruction;
 // the TMEM load of the next 32 columns is in flight while these are computed.
-template <int ACT>
-__device__ __forceinline__ void cw_act_tile(uint32_t t_s, float scale, float bias) {
+// MASKED: keys a row does not see get P = act(0) = 0.
+template <int ACT, bool MASKED>
+__device__ __forceinline__ void cw_act_tile(uint32_t t_s, float scale, float bias, const uint32_t (&see)[4]) {
   const float2 hs = f2(0.5f * scale), hb = f2(0.5f * bias);
   uint32_t buf0[32], buf1[32];
   tmem_ld32(t_s, buf0);
@@ -302,7 +327,11 @@ __device__ __forceinline__ void cw_act_tile(uint32_t t_s, float scale, float bia
     uint32_t pk[16];
 #pragma unroll
     for (int c = 0; c < 16; ++c) {
-      const float2 hx = __ffma2_rn(make_float2(__uint_as_float(cur[2 * c]), __uint_as_float(cur[2 * c + 1])), hs, hb);
+      float2 hx = __ffma2_rn(make_float2(__uint_as_float(cur[2 * c]), __uint_as_float(cur[2 * c + 1])), hs, hb);
+      if (MASKED) {
+        if (!((see[q] >> (2 * c)) & 1)) hx.x = 0.f;
+        if (!((see[q] >> (2 * c + 1)) & 1)) hx.y = 0.f;
+      }
       const float2 y = act2_route<ACT, 0>(hx);
       pk[c] = pack_bf16(y.x, y.y);
     }
@@ -312,10 +341,11 @@ __device__ __forceinline__ void cw_act_tile(uint32_t t_s, float scale, float bia
 }
 
 // P = 2^(x - m) with a running maximum that moves only when it grows by more
-// than 8 (P stays below 2^8, O and l in fp32): O is rescaled then.
-template <int D>
-__device__ __forceinline__ void cw_softmax_tile(uint32_t t_s, uint32_t t_o, float scale, float bias, bool first,
-                                                float& m, float& l) {
+// than 8 (P stays below 2^8, O and l in fp32): O is rescaled then.  MASKED:
+// keys a row does not see have x = -inf.
+template <int D, bool MASKED>
+__device__ __forceinline__ void cw_softmax_tile(uint32_t t_s, uint32_t t_o, float scale, float bias,
+                                                const uint32_t (&see)[4], bool first, float& m, float& l) {
   uint32_t a[32], b[32], c3[32], d4[32];
   tmem_ld32(t_s, a);
   tmem_ld32(t_s + 32, b);
@@ -328,7 +358,11 @@ __device__ __forceinline__ void cw_softmax_tile(uint32_t t_s, uint32_t t_o, floa
   for (int c = 0; c < 128; c += 2) {
     uint32_t& r0 = c < 32 ? a[c] : c < 64 ? b[c - 32] : c < 96 ? c3[c - 64] : d4[c - 96];
     uint32_t& r1 = c < 32 ? a[c + 1] : c < 64 ? b[c - 31] : c < 96 ? c3[c - 63] : d4[c - 95];
-    const float2 x = __ffma2_rn(make_float2(__uint_as_float(r0), __uint_as_float(r1)), f2(scale), f2(bias));
+    float2 x = __ffma2_rn(make_float2(__uint_as_float(r0), __uint_as_float(r1)), f2(scale), f2(bias));
+    if (MASKED) {
+      if (!((see[c / 32] >> (c % 32)) & 1)) x.x = -INFINITY;
+      if (!((see[c / 32] >> (c % 32 + 1)) & 1)) x.y = -INFINITY;
+    }
     r0 = __float_as_uint(x.x);
     r1 = __float_as_uint(x.y);
     mx = fmaxf(mx, fmaxf(x.x, x.y));
@@ -371,48 +405,137 @@ __device__ __forceinline__ void cw_softmax_tile(uint32_t t_s, uint32_t t_o, floa
 }
 
 // Adds what the product left out: infinities and NaN in V of keys in the
-// part's masked tiles, for the rows that see them, to columns [c0, c0 + 16) of
-// a row.  Rare, so it works from global memory.
+// part's masked tiles, for a row that sees them, to columns [c0, c0 + n) of the
+// row's result (bf16 `out` or fp32 `part`), which this thread has written.
+// Rare, so it works from global memory.
 template <int D, int ACT>
-__device__ __noinline__ void cw_add_odd(const CacheFwdParams& p, const CacheReq& r, const CcRow& q, const __nv_bfloat16* kc,
-                                        const __nv_bfloat16* vc, const int32_t* pages, int64_t k_stride, int64_t v_stride,
-                                        int key, int c0, float* o) {
-  const int page = __ldg(pages + (key >> p.page_shift));
-  if (static_cast<uint32_t>(page) >= static_cast<uint32_t>(p.num_pages)) return;
-  const int key_pos = cc_pos(p, r, key);
-  if (!(cc_vis32(p, r, q, key) & 1) || !cc_near(p, q.pos, key_pos)) return;
-  const int64_t place = static_cast<int64_t>(key & ((1 << p.page_shift) - 1)) * p.kv_heads * D;
-  const __nv_bfloat16* v = vc + page * v_stride + place;
-  bool any = false;
-  for (int c = 0; c < 16; ++c) any = any || !isfinite(__bfloat162float(v[c0 + c]));
-  if (!any) return;
-  float weight = 1.f;  // softmax weights are positive
-  if constexpr (ACT != 2) {
-    const __nv_bfloat16* k = kc + page * k_stride + place;
-    const __nv_bfloat16* qr = p.q + static_cast<int64_t>(r.q0 + q.t) * p.q_stride + static_cast<int64_t>(q.head) * D;
-    float x = 0.f;
-    for (int c = 0; c < D; ++c) x = __fmaf_rn(__bfloat162float(k[c]), __bfloat162float(qr[c]), x);
-    x *= p.scale;
-    if (p.bias_len) x += cc_bias(p, q, (p.bias_len - 1) / 2, key_pos);
-    weight = cc_act<ACT>(x);
+__device__ __noinline__ void cw_add_odd(const CacheFwdParams& p, CacheWalk w, CwPart part, CcRow q, int far_depth,
+                                        int c0, int n, __nv_bfloat16* out, float* part_o) {
+  const CacheReq& r = w.r;
+  const int32_t* pages = p.table + static_cast<int64_t>(w.b) * p.width;
+  for (int t = part.lo; t < part.lo + part.n; ++t) {
+    if (part.plain(p, w, far_depth, t * kTile)) continue;
+    for (int key = t * kTile; key < min(r.L, (t + 1) * kTile); ++key) {
+      const int page = __ldg(pages + (key >> p.page_shift));
+      if (static_cast<uint32_t>(page) >= static_cast<uint32_t>(p.num_pages)) continue;
+      const int key_pos = cc_pos(p, r, key);
+      if (!(cc_vis32(p, r, q, key) & 1) || !cc_near(p, q.pos, key_pos)) continue;
+      const int64_t place = static_cast<int64_t>(key & ((1 << p.page_shift) - 1)) * p.kv_heads * D + w.h * D;
+      const __nv_bfloat16* v = p.v_cache + page * p.v_page_stride + place;
+      bool any = false;
+      for (int c = 0; c < n; ++c) any = any || !isfinite(__bfloat162float(v[c0 + c]));
+      if (!any) continue;
+      float weight = 1.f;  // softmax weights are positive
+      if constexpr (ACT != 2) {
+        const __nv_bfloat16* k = p.k_cache + page * p.k_page_stride + place;
+        const __nv_bfloat16* qr = p.q + static_cast<int64_t>(r.q0 + q.t) * p.q_stride + static_cast<int64_t>(q.head) * D;
+        float x = 0.f;
+        for (int c = 0; c < D; ++c) x = __fmaf_rn(__bfloat162float(k[c]), __bfloat162float(qr[c]), x);
+        x *= p.scale;
+        if (p.bias_len) x += cc_bias(p, q, (p.bias_len - 1) / 2, key_pos);
+        weight = cc_act<ACT>(x);
+      }
+      for (int c = 0; c < n; ++c) {
+        const float x = __bfloat162float(v[c0 + c]);
+        if (isfinite(x)) continue;
+        if (out != nullptr) out[c0 + c] = __float2bfloat16_rn(__bfloat162float(out[c0 + c]) + weight * x);
+        else part_o[c0 + c] += weight * x;
+      }
+    }
   }
-  for (int c = 0; c < 16; ++c) {
-    const float x = __bfloat162float(v[c0 + c]);
-    if (!isfinite(x)) o[c] += weight * x;
+}
+
+// Two spare warps make V of the masked tiles safe for the product: 0 * NaN =
+// NaN, so V rows past the request's end (the page or an earlier tile may have
+// left anything there) are zeroed, and infinities and NaN of the others taken
+// out; the epilogue adds those to the rows that see them.
+template <int D>
+__device__ void cw_fixer(const CacheFwdParams& p, uint8_t* smem, CwShared* sh, const CacheRange& R, Fail fail) {
+  using C = CwCfg<D>;
+  constexpr int kPieces = C::kBlockCols / 8;
+  const int lane = threadIdx.x & 31;
+  const uint32_t v_base = smem_u32(smem + C::kVOff);
+  uint32_t kv_n = 0;
+  int number = 0;
+  CacheWalk w;
+  w.init(R);
+  for (; w.next<kTile>(p); w.advance()) {
+    const CwPart part(p, w);
+    if (part.n == 0) continue;
+    ++number;
+    const int far_depth = part.far_depth(p, w);
+    for (int i = 0; i < part.n; ++i) {
+      // (every tile is waited for and released, so that no round of a stage
+      // is mistaken for another)
+      const int key0 = (part.lo + i) * kTile;
+      const uint32_t it = kv_n + i;
+      const int st = it % C::kStages;
+      if (!mbar_wait_warp(&sh->v_full[st], (it / C::kStages) & 1, fail)) return;
+      if (part.plain(p, w, far_depth, key0)) {
+        mbar_arrive_warp(&sh->v_empty[st]);
+        continue;
+      }
+      for (int row = threadIdx.x & 63; row < kTile; row += 64) {
+        const bool past = key0 + row >= w.r.L;
+        const uint32_t vr = v_base + st * C::kTileBytes + row * C::kRowBytes;
+        // (pieces in any order, whatever the swizzle: from the lane's on, so
+        // that the lanes, a row apart, meet different banks)
+#pragma unroll
+        for (int c = 0; c < D / 8; ++c) {
+          const uint32_t a = vr + (c / kPieces) * C::kBlockBytes + ((c + lane * kPieces / 8) % kPieces) * 16;
+          uint32_t x[4];
+          ld_shared_v4(a, x[0], x[1], x[2], x[3]);
+          uint32_t bad = 0;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const uint32_t f = past ? 0xFFFFFFFFu : cc_nonfinite(x[e]);
+            bad |= f;
+            x[e] &= ~f;
+          }
+          if (bad) {
+            if (!past) *const_cast<volatile int*>(&sh->odd[number & 15]) = number;
+            st_shared_v4(a, x[0], x[1], x[2], x[3]);
+          }
+        }
+      }
+      fence_proxy_async_smem();
+      mbar_arrive_warp(&sh->v_fixed[st]);
+      mbar_arrive_warp(&sh->v_empty[st]);
+    }
+    kv_n += part.n;
+  }
+}
+
+// 16 columns of a row: bf16 to `out`, or fp32 to `part` where the item goes on elsewhere.
+__device__ __forceinline__ void cw_store16(const uint32_t (&x)[16], float inv, __nv_bfloat16* out, float* part, int c0) {
+  if (out != nullptr) {
+    uint32_t pk[8];
+#pragma unroll
+    for (int c = 0; c < 8; ++c) pk[c] = pack_bf16(__uint_as_float(x[2 * c]) * inv, __uint_as_float(x[2 * c + 1]) * inv);
+    if (reinterpret_cast<uintptr_t>(out) % 32 == 0) {
+      st_global_v8(out + c0, pk);
+    } else {
+      st_global_v4(out + c0, pk[0], pk[1], pk[2], pk[3]);
+      st_global_v4(out + c0 + 8, pk[4], pk[5], pk[6], pk[7]);
+    }
+  } else {
+#pragma unroll
+    for (int c = 0; c < 16; c += 8) {
+      const uint32_t w[8] = {x[c], x[c + 1], x[c + 2], x[c + 3], x[c + 4], x[c + 5], x[c + 6], x[c + 7]};
+      st_global_v8(part + c0 + c, w);
+    }
   }
 }
 
 template <int D, int ACT>
-__device__ void cw_consumer(const CacheFwdParams& p, uint8_t* smem, CwShared* sh, uint32_t tmem, int stream,
-                            const CacheRange& R, Fail fail) {
-  using C = CwCfg<D>;
+__device__ void cw_consumer(const CacheFwdParams& p, CwShared* sh, uint32_t tmem, int stream, const CacheRange& R,
+                            Fail fail) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int row = (warp & 3) * 32 + lane;  // row of the tile, and key row of V for the zeroing
+  const int row = (warp & 3) * 32 + lane;
   const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
   const uint32_t t_s = tmem + lane_off + 128 * stream, t_o = tmem + lane_off + 256;
-  const uint32_t v_base = smem_u32(smem + C::kVOff);
   const int reach = (p.bias_len - 1) / 2;
-  uint32_t kv_n = 0, s_n = 0, o_n[2] = {0, 0};
+  uint32_t s_n = 0, o_n[2] = {0, 0};
   int number = 0;  // of the part with tiles, from 1
   int ml_at = 0;
   bool dead = false;
@@ -421,7 +544,8 @@ __device__ void cw_consumer(const CacheFwdParams& p, uint8_t* smem, CwShared* sh
   for (; w.next<kTile>(p); w.advance()) {
     const CwPart part(p, w);
     const CacheReq& r = w.r;
-    if (part.n > 0) ++number;  // (a warpgroup is at most one such part ahead of the other: O is shared)
+    if (part.n > 0) ++number;  // (the V ring lets no more than 8 later parts be loaded, let alone checked)
+    __syncwarp();
     const int block_row0 = w.row_tile * p.rows_per_tile;
     const int my_rows = part.pair ? (stream == 0 ? part.tile_rows : part.rows - part.tile_rows) : part.rows;
     const bool row_ok = row < my_rows;
@@ -433,84 +557,42 @@ __device__ void cw_consumer(const CacheFwdParams& p, uint8_t* smem, CwShared* sh
     q.far_bias = 0.f;
     if (row_ok && p.bias_len)
       q.far_bias = __ldg(p.bias + static_cast<int64_t>(q.head) * p.bias_len + 2 * reach) * cc_bias_unit<ACT>();
-    // over all rows of the part, the same in every warp
-    const int first_token = block_row0 / p.group, last_token = (block_row0 + part.rows - 1) / p.group;
-    int far_depth = last_token;
-    if (p.window > 0 && p.depth != nullptr) {
-      far_depth = 0;
-      for (int t = first_token + lane; t <= last_token; t += 32) far_depth = max(far_depth, __ldg(p.depth + r.q0 + t));
-      far_depth = __reduce_max_sync(0xffffffffu, far_depth);
-    }
-    // A tile is plain when every row sees all of its keys.  (The same answer
-    // for both streams: they take V from one tile.)
-    auto plain_tile = [&](int key0) {
-      const int last = key0 + kTile - 1;
-      if (p.window > 0) return last < r.C && static_cast<int64_t>(r.C) + far_depth - key0 < p.window;
-      return p.mask != nullptr ? last < r.C : last <= r.C + first_token && last < r.L;
-    };
+    const int far_depth = part.far_depth(p, w);
     const bool warp_live = (warp & 3) * 32 < my_rows;
     float m = -INFINITY, l = 0.f;
     for (int i = 0; i < part.count[stream]; ++i) {
-      const uint32_t it = kv_n + part.at(stream, i);
       const int key0 = (part.lo + part.at(stream, i)) * kTile;
       if (!dead && !mbar_wait(&sh->s_full[stream], s_n & 1, fail)) dead = true;
       dead = __any_sync(0xffffffffu, dead);
       ++s_n;
       if (dead) continue;
       tc_fence_after();
-      const bool plain = plain_tile(key0);
-      float scale = p.scale, bias = q.far_bias;
       if (warp_live) {
+        const bool plain = part.plain(p, w, far_depth, key0);
         const bool far = p.bias_len == 0 || (key0 + kTile - 1 < r.C && r.C - (key0 + kTile - 1) >= reach);
-        if (!plain || !far) {
-          cw_mask<ACT>(p, r, q, far, reach, key0, t_s);
+        float scale = p.scale, bias = q.far_bias;
+        if (!far) {
+          cw_bias_tile<ACT>(p, r, q, reach, key0, t_s);
           scale = 1.f;
           bias = 0.f;
         }
-        if constexpr (ACT == 2) cw_softmax_tile<D>(t_s, t_o + 128 * stream, scale, bias, i == 0, m, l);
-        else cw_act_tile<ACT>(t_s, scale, bias);
-        tmem_st_wait();
-      }
-      if (!plain) {
-        // 0 * NaN = NaN: V rows past the request's end are zeroed (the page
-        // or an earlier tile may have left anything there), and infinities and
-        // NaN of the others are taken out; the epilogue adds them to the rows
-        // that see them.
-        const int st = it % C::kStages;
-        if (!mbar_wait(&sh->v_full[st], (it / C::kStages) & 1, fail)) dead = true;
-        dead = __any_sync(0xffffffffu, dead);
-        if (dead) continue;
-        const uint32_t vr = v_base + st * C::kTileBytes + row * C::kRowBytes;
-        const bool past = key0 + row >= r.L;
-#pragma unroll 4
-        for (int c = 0; c < D / 8; ++c) {  // (the order of the swizzled pieces does not matter)
-          const uint32_t a = vr + (c / (C::kBlockCols / 8)) * C::kBlockBytes + (c % (C::kBlockCols / 8)) * 16;
-          uint32_t x[4];
-          ld_shared_v4(a, x[0], x[1], x[2], x[3]);
-          uint32_t bad = 0;
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const uint32_t f = past ? 0xFFFFFFFFu : cc_nonfinite(x[e]);
-            bad |= f;
-            x[e] &= ~f;
-          }
-          if (bad) {
-            if (!past) {
-              *const_cast<volatile int*>(&sh->odd[number & 1]) = number;
-              __threadfence_block();
-            }
-            st_shared_v4(a, x[0], x[1], x[2], x[3]);
-          }
+        uint32_t see[4] = {0u, 0u, 0u, 0u};
+        if (plain) {
+          if constexpr (ACT == 2) cw_softmax_tile<D, false>(t_s, t_o + 128 * stream, scale, bias, see, i == 0, m, l);
+          else cw_act_tile<ACT, false>(t_s, scale, bias, see);
+        } else {
+          cw_visible(p, r, q, key0, see);
+          if constexpr (ACT == 2) cw_softmax_tile<D, true>(t_s, t_o + 128 * stream, scale, bias, see, i == 0, m, l);
+          else cw_act_tile<ACT, true>(t_s, scale, bias, see);
         }
-        fence_proxy_async_smem();
+        tmem_st_wait();
       }
       tc_fence_before();
       mbar_arrive_warp(&sh->p_full[stream]);
     }
-    kv_n += part.n;
 
     // the part's end
-    int o_col = 0, o_cols = D;  // columns this warpgroup writes
+    int o_col = 0;              // first column this warpgroup writes
     float f[2] = {1.f, 1.f};    // factors of the streams' O
     bool use[2] = {false, false};
     if (part.n > 0) {
@@ -518,7 +600,6 @@ __device__ void cw_consumer(const CacheFwdParams& p, uint8_t* smem, CwShared* sh
       use[1] = part.pair ? stream == 1 : part.count[1] > 0;
       if (!part.pair) {  // both streams' rows are the same: each warpgroup joins and writes half the columns
         o_col = stream * (D / 2);
-        o_cols = D / 2;
         if constexpr (ACT == 2) {
           sh->ml[ml_at][stream][row] = make_float2(m, l);
           named_bar(1, 256);
@@ -540,59 +621,52 @@ __device__ void cw_consumer(const CacheFwdParams& p, uint8_t* smem, CwShared* sh
       }
       dead = __any_sync(0xffffffffu, dead);
     }
-    if (!dead) {
-      tc_fence_after();
-      const bool odd = part.n > 0 && *const_cast<volatile int*>(&sh->odd[number & 1]) == number;
-      const float inv = ACT != 2 || !w.whole ? 1.f : (l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l));
-      const int64_t token = r.q0 + (row_ok ? q.t : 0);
-      __nv_bfloat16* dst = p.out + (token * p.heads + q.head) * D;
-      const int64_t prow = (2 * static_cast<int64_t>(blockIdx.x) + (w.first ? 0 : 1)) * p.rows_per_tile + (flat - block_row0);
-      for (int c0 = o_col; c0 < o_col + o_cols; c0 += 16) {
-        float o[16];
-        uint32_t x[16];
+    // O leaves tensor memory at once (all columns of one stream, or half the
+    // columns of both), so that the next part's products may start
+    uint32_t x[D / 16][16];
+    tc_fence_after();
 #pragma unroll
-        for (int c = 0; c < 16; ++c) o[c] = 0.f;
+    for (int k = 0; k < D / 16; ++k) {
+      const int s = part.pair ? stream : (k >= D / 32 ? 1 : 0);
+      const int col = part.pair ? 16 * k : o_col + 16 * (k % (D / 32));
+      if (!dead && use[s]) {
+        tmem_ld16(t_o + 128 * s + col, x[k]);
+      } else {
 #pragma unroll
-        for (int s = 0; s < 2; ++s) {
-          if (!use[s]) continue;
-          tmem_ld16(t_o + 128 * s + c0, x);
-          tmem_ld_wait16(x);
-#pragma unroll
-          for (int c = 0; c < 16; ++c) o[c] = __fmaf_rn(__uint_as_float(x[c]), f[s], o[c]);
-        }
-        if (odd && row_ok) {
-          const int32_t* pages = p.table + static_cast<int64_t>(w.b) * p.width;
-          for (int t = part.lo; t < part.lo + part.n; ++t) {
-            if (plain_tile(t * kTile)) continue;
-            for (int j = t * kTile; j < min(r.L, (t + 1) * kTile); ++j)
-              cw_add_odd<D, ACT>(p, r, q, p.k_cache + w.h * D, p.v_cache + w.h * D, pages, p.k_page_stride,
-                                 p.v_page_stride, j, c0, o);
-          }
-        }
-        if (row_ok) {
-          if (w.whole) {
-            uint32_t pk[8];
-#pragma unroll
-            for (int c = 0; c < 8; ++c) pk[c] = pack_bf16(o[2 * c] * inv, o[2 * c + 1] * inv);
-            st_global_v4(dst + c0, pk[0], pk[1], pk[2], pk[3]);
-            st_global_v4(dst + c0 + 8, pk[4], pk[5], pk[6], pk[7]);
-          } else {
-#pragma unroll
-            for (int c = 0; c < 16; c += 4)
-              *reinterpret_cast<float4*>(p.part_o + prow * D + c0 + c) = make_float4(o[c], o[c + 1], o[c + 2], o[c + 3]);
-          }
-        }
-        __syncwarp();
-      }
-      if (ACT == 2 && row_ok && o_col == 0) {
-        if (!w.whole) p.part_ml[prow] = make_float2(m, l);
-        else if (p.lse != nullptr)
-          p.lse[static_cast<int64_t>(q.head) * p.total_q + token] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+        for (int c = 0; c < 16; ++c) x[k][c] = 0u;
       }
     }
+#pragma unroll
+    for (int k = 0; k < D / 16; ++k) tmem_ld_wait16(x[k]);
+    const bool odd = part.n > 0 && *const_cast<volatile int*>(&sh->odd[number & 15]) == number;
     if (part.n > 0) {
       tc_fence_before();
       mbar_arrive_warp(&sh->o_empty);
+    }
+    if (!row_ok || dead) continue;
+    const float inv = ACT != 2 || !w.whole ? 1.f : (l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l));
+    const int64_t token = r.q0 + q.t;
+    const int64_t prow = (2 * static_cast<int64_t>(blockIdx.x) + (w.first ? 0 : 1)) * p.rows_per_tile + (flat - block_row0);
+    __nv_bfloat16* out = w.whole ? p.out + (token * p.heads + q.head) * D : nullptr;
+    float* part_o = p.part_o + prow * D;
+    // (the columns of a part without tiles are written by both warpgroups, as zeros)
+    if (part.pair || part.n == 0) {
+#pragma unroll
+      for (int k = 0; k < D / 16; ++k) cw_store16(x[k], inv, out, part_o, 16 * k);
+    } else {
+#pragma unroll
+      for (int k = 0; k < D / 32; ++k) {
+#pragma unroll
+        for (int c = 0; c < 16; ++c)
+          x[k][c] = __float_as_uint(__fmaf_rn(__uint_as_float(x[k][c]), f[0], __uint_as_float(x[k + D / 32][c]) * f[1]));
+        cw_store16(x[k], inv, out, part_o, o_col + 16 * k);
+      }
+    }
+    if (odd) cw_add_odd<D, ACT>(p, w, part, q, far_depth, o_col, part.pair ? D : D / 2, out, part_o);
+    if (ACT == 2 && o_col == 0) {
+      if (!w.whole) p.part_ml[prow] = make_float2(m, l);
+      else if (p.lse != nullptr)
+        p.lse[static_cast<int64_t>(q.head) * p.total_q + token] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
     }
   }
 }
@@ -617,12 +691,14 @@ __global__ void __launch_bounds__(kWideThreads, 1) cache_fwd_wide_kernel(const _
       mbar_init(&sh->k_full[s], 1);
       mbar_init(&sh->k_empty[s], 1);
       mbar_init(&sh->v_full[s], 1);
-      mbar_init(&sh->v_empty[s], 1);
+      mbar_init(&sh->v_empty[s], 3);  // the last product that reads it, and the two fixing warps
+      mbar_init(&sh->v_fixed[s], 2);
     }
     mbar_init(&sh->o_empty, 8);
     mbar_init(&sh->drain, 1);
     sh->abort = 0;
-    sh->odd[0] = sh->odd[1] = 0;
+    p.err[blockIdx.x] = kOk;
+    for (int i = 0; i < 16; ++i) sh->odd[i] = 0;
     fence_mbar_init();
   }
   if (warp == 1) {
@@ -630,15 +706,16 @@ __global__ void __launch_bounds__(kWideThreads, 1) cache_fwd_wide_kernel(const _
     tmem_relinquish();
   }
   const CacheRange R = cache_range<kTile>(p, &sh->range, kWideMinTiles);
-  if (threadIdx.x == 0) cache_open<kTile>(p, R);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  if (threadIdx.x == 96) cache_open<kTile>(p, R);
   const uint32_t tmem = sh->tmem_base;
   Fail fail{&sh->abort, p.err + blockIdx.x, p.wait_limit_ns};
   if (warp == 0) cw_producer<D>(p, smem, sh, R, fail);
   else if (warp == 1) cw_mma<D>(p, smem, sh, tmem, R, fail);
-  else if (warp >= 4) cw_consumer<D, ACT>(p, smem, sh, tmem, (warp - 4) >> 2, R, fail);
+  else if (warp >= 4) cw_consumer<D, ACT>(p, sh, tmem, (warp - 4) >> 2, R, fail);
+  else cw_fixer<D>(p, smem, sh, R, fail);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();

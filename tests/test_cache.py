@@ -349,7 +349,7 @@ def test_attention(jg, act, d, group, new):
 @pytest.mark.parametrize("act", ["silu", "softmax"])
 @pytest.mark.parametrize("new,group,bias,window,page", [
     (1, 1, 257, 0, 16), (9, 2, 33, 0, 64), (33, 1, 5, 100, 32), (64, 4, 0, 1, 128), (20, 3, 1, 64, 256), (40, 1, 129, 7, 1024),
-    (5, 1, 4095, 0, 16), (65, 2, 9, 300, 16),
+    (5, 1, 4095, 0, 16), (65, 2, 9, 300, 16), (70, 3, 0, 50, 32), (50, 7, 65, 0, 16),
 ])
 def test_trees_bias_and_window(jg, act, new, group, bias, window, page):
     rng = np.random.default_rng(new + bias)
@@ -391,6 +391,29 @@ def test_long_contexts_are_cut_between_ctas(jg, act, new):
 
 @gpu
 @pytest.mark.parametrize("act", ["gelu", "softmax"])
+@pytest.mark.parametrize("d", [32, 128])
+@pytest.mark.parametrize("new,group,window", [(1, 3, 0), (9, 2, 0), (40, 2, 0), (40, 5, 70)])
+def test_many_requests_per_cta(jg, act, d, new, group, window):
+    """Six requests, each there 200 times: every CTA walks several items."""
+    rng = np.random.default_rng(new)
+    c = Case(d + new, sizes(rng, 6, 500), rng.integers(1, new + 1, 6), 2, group, d, 16, act, bias=33, window=window, mask=True)
+    want = c.oracle()
+    kw = c.kwargs()
+    n, times = int(c.off[-1]), 200
+    order = rng.permutation(np.repeat(np.arange(6), times))
+    rows = np.concatenate([np.arange(c.off[b], c.off[b + 1]) for b in order])
+    off = np.concatenate([[0], np.cumsum(c.new[order])])
+    for k in ("q", "tree_mask", "depths"):
+        kw[k] = kw[k][torch.from_numpy(rows).cuda()].contiguous()
+    kw["block_table"] = kw["block_table"][torch.from_numpy(order).cuda()].contiguous()
+    out, lse = jg.jgdpa_cache_fwd(**{**kw, "q_offsets": i32(off, "cuda"), "kv_lens": i32(c.kv[order], "cuda")})
+    c.off = off
+    assert len(rows) == n * times
+    compare(c, out, lse, (want[0][rows], want[1][:, rows], want[2][rows], want[3][:, rows], want[4][rows]))
+
+
+@gpu
+@pytest.mark.parametrize("act", ["gelu", "softmax"])
 @pytest.mark.parametrize("new", [4, 40])
 def test_rows_that_see_nothing(jg, act, new):
     c = Case(3, [0, 50], [new, new], 1, 2, 64, 16, act, window=3, mask=True)
@@ -405,7 +428,7 @@ def test_rows_that_see_nothing(jg, act, new):
 
 @gpu
 @pytest.mark.parametrize("act", ["gelu", "silu", "softmax"])
-@pytest.mark.parametrize("new,group", [(6, 2), (30, 4)])
+@pytest.mark.parametrize("new,group", [(6, 2), (30, 4), (40, 8)])
 def test_infinities_reach_only_the_rows_that_see_them(jg, act, new, group):
     """NaN and infinities in one drafted token's key and value, and in a context
     token out of the window: rows that do not see it are as without it."""
