@@ -19,6 +19,9 @@ enum : int { kErrOutOfPages = 8, kErrBadPage = 9 };
 
 constexpr int kCacheMaxBatch = 16384;  // requests per call (the plan's prefix sums live in shared memory)
 
+// CTAs per SM of the attention kernel for up to 16 rows (cache_fwd.cu).
+__host__ __device__ constexpr int cache_ctas_narrow(int d) { return d == 128 ? 2 : (d == 64 ? 3 : 4); }
+
 struct CachePlanParams {
   const int32_t* ctx;
   const int32_t* add;
@@ -52,8 +55,8 @@ struct CacheAppendParams {
 // joining kernel: valid only from the first CTA that continues an item.
 struct CacheJoin {
   int32_t valid, b, h, rt;
-  int64_t t0, t1;  // the item's tiles in the global order
-  int64_t per;     // tiles per CTA
+  int64_t t0, t1;  // the item's place in the global order
+  int64_t per;     // length of a CTA's range
 };
 
 struct CacheFwdParams {
@@ -83,6 +86,7 @@ struct CacheFwdParams {
   int32_t page_shift, width, num_pages;
   int32_t mask_words, bias_len, window;
   int32_t rows_per_tile;     // query rows (token, head of the group) of one item
+  int32_t item_cost;         // tiles that an item's start and end are worth
   float scale;               // s (GELU / SiLU) or s log2(e) (softmax)
   unsigned long long wait_limit_ns;
 };
@@ -108,7 +112,7 @@ __device__ __forceinline__ CacheReq cache_req(const CacheFwdParams& p, int b) {
   return r;
 }
 __device__ __forceinline__ int64_t cache_cost(const CacheFwdParams& p, const CacheReq& r) {
-  return r.T <= 0 ? 0 : static_cast<int64_t>(p.kv_heads) * r.rt * r.n;
+  return r.T <= 0 ? 0 : static_cast<int64_t>(p.kv_heads) * r.rt * (r.n + p.item_cost);
 }
 __device__ __forceinline__ bool cache_req_ok(const CacheFwdParams& p, const CacheReq& r) {
   return r.T >= 0 && r.T <= p.max_q && r.L >= r.T &&
@@ -117,10 +121,12 @@ __device__ __forceinline__ bool cache_req_ok(const CacheFwdParams& p, const Cach
 }
 
 // Work division.  The items are (request, kv head, row tile), each of n key
-// tiles; laid end to end (request by request, row tiles of one head next to
-// each other so that they meet in L2) their tiles form one line that is cut
-// into equal ranges, one per CTA, whatever the lengths.  An item cut by a
-// range border is finished by the joining kernel.
+// tiles and a lead of item_cost tiles' length, what its start and end take
+// beside them; laid end to end (request by request, row tiles of one head next
+// to each other so that they meet in L2) they form one line that is cut into
+// equal ranges, one per CTA, whatever the lengths.  (Without the lead, ranges
+// that fall on many short requests took half as long again as the others.)  An
+// item cut by a range border is finished by the joining kernel.
 struct CacheRange {
   int64_t total, per, begin, end;
   int b;        // request that `begin` lies in
@@ -135,7 +141,7 @@ struct CacheRangeShared {
 
 // Run by every thread of the CTA (a whole number of warps, at most 1024).
 template <int KT>
-__device__ CacheRange cache_range(const CacheFwdParams& p, CacheRangeShared* sh, int min_tiles) {
+__device__ CacheRange cache_range(const CacheFwdParams& p, CacheRangeShared* sh, int min_range) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nt = blockDim.x, nw = nt >> 5;
   const int each = (p.batch + nt - 1) / nt;
   const int b0 = min(tid * each, p.batch), b1 = min(b0 + each, p.batch);
@@ -165,7 +171,7 @@ __device__ CacheRange cache_range(const CacheFwdParams& p, CacheRangeShared* sh,
   R.ok = all_ok;
   R.total = total;
   const int64_t g = gridDim.x;
-  R.per = max((total + g - 1) / g, static_cast<int64_t>(min_tiles));
+  R.per = max((total + g - 1) / g, static_cast<int64_t>(min_range));
   R.begin = min(R.per * blockIdx.x, total);
   R.end = min(R.begin + R.per, total);
   int64_t at = base + incl - sum;
@@ -193,13 +199,14 @@ __device__ __forceinline__ int64_t cache_div(int64_t a, int b) {
 // Walks the parts of items in a CTA's range, in order; every role of the CTA
 // walks the same parts.
 struct CacheWalk {
-  int64_t left;  // tiles left in the range
-  int64_t rem;   // place in the request's tiles
+  int64_t left;  // length left in the range
+  int64_t rem;   // place in the request's length
   int b;
   bool first;    // the part starts at the range's start
   // the current part
   CacheReq r;
   int h, row_tile, tile0, count;  // count tiles from the item's tile0
+  int step;                       // its length
   bool whole;                     // the part is the whole item
 
   __device__ __forceinline__ void init(const CacheRange& R) {
@@ -217,17 +224,21 @@ struct CacheWalk {
       cost = cache_cost(p, r);
       if (rem < cost) break;
     }
-    const int64_t item = cache_div(rem, r.n);
-    tile0 = static_cast<int>(rem - item * r.n);
+    const int len = r.n + p.item_cost;
+    const int64_t item = cache_div(rem, len);
+    const int from = static_cast<int>(rem - item * len);
+    step = static_cast<int>(min(static_cast<int64_t>(len - from), left));
+    tile0 = max(0, from - p.item_cost);
+    count = max(0, from + step - p.item_cost) - tile0;
+    if (count == 0) return false;  // the range ends inside the lead
     h = static_cast<int>(cache_div(item, r.rt));
     row_tile = static_cast<int>(item - static_cast<int64_t>(h) * r.rt);
-    count = static_cast<int>(min(static_cast<int64_t>(r.n - tile0), left));
     whole = count == r.n;
     return true;
   }
   __device__ __forceinline__ void advance() {
-    rem += count;
-    left -= count;
+    rem += step;
+    left -= step;
     first = false;
   }
   // Keys of tiles [lo, hi) (of the request's) in this part that any row of the
@@ -254,14 +265,17 @@ __device__ __forceinline__ void cache_open(const CacheFwdParams& p, const CacheR
   CacheJoin j{};
   if (R.ok && R.begin < R.end) {
     const CacheReq r = cache_req<KT>(p, R.b);
-    const int64_t item = R.rem / r.n;
-    j.t0 = R.begin - (R.rem - item * r.n);
-    j.t1 = j.t0 + r.n;
+    const int len = r.n + p.item_cost;
+    const int64_t item = cache_div(R.rem, len);
+    j.t0 = R.begin - (R.rem - item * len);
+    j.t1 = j.t0 + len;
     j.per = R.per;
     j.b = R.b;
-    j.h = static_cast<int>(item / r.rt);
+    j.h = static_cast<int>(cache_div(item, r.rt));
     j.rt = static_cast<int>(item - static_cast<int64_t>(j.h) * r.rt);
-    j.valid = j.t0 < R.begin && j.t0 / R.per + 1 == c;
+    // tiles in several ranges, and this is the second of them
+    const int64_t c0 = (j.t0 + p.item_cost) / R.per;
+    j.valid = c0 + 1 == c && (j.t1 - 1) / R.per > c0;
   }
   p.join[c] = j;
 }

@@ -12,11 +12,12 @@
 // keep S, P and O in registers: no tensor-memory round trip and no block-wide
 // step per tile.  (The 128-row tensor-memory form is cache_fwd_wide.cu.)  Each
 // of four warps takes 16 of a tile's keys with its own running maximum, sum and
-// O; they meet once per item.  With 16-row tiles a second group of four warps
-// takes every other tile, with 32-row tiles the second 16 rows.
+// O; they meet once per item.  With 32-row tiles a second group of four warps
+// takes the second 16 rows of the same keys.
 //
-// The TMA producer runs up to 160 KB ahead (128 KB at d = 128), across items, so that an item's
-// end (the warps' exchange) does not stop the loads.
+// A TMA producer runs up to 96 KB ahead, across items, and several CTAs share
+// an SM, so that neither an item's end (the warps' exchange) nor its start
+// stops the loads.
 #include "act.cuh"
 #include "cache.cuh"
 #include "common.cuh"
@@ -26,32 +27,31 @@ namespace jg {
 
 constexpr int kCKeys = 64;        // tokens per tile
 constexpr int kCGroupWarps = 4;   // warps that share a tile's keys
-constexpr int kCWarps = 8;        // consumer warps
-constexpr int kCThreads = (kCWarps + 1) * 32;
-constexpr int kCMinTiles = 4;     // a range below this many tiles is not worth its own CTA
+constexpr int kCMinRange = 6;     // a range below this many tiles is not worth its own CTA
+constexpr int kCChunk = 32;       // columns of O that meet at a time at an item's end
 
-template <int D>
+template <int D, int MT>
 struct CcCfg {
+  static constexpr int kWarps = kCGroupWarps * MT;  // consumer warps
+  static constexpr int kThreads = (kWarps + 1) * 32;
   static constexpr int kBlockCols = D < 64 ? D : 64;
   static constexpr int kRowBytes = kBlockCols * 2;
-  static constexpr int kHalves = D / kBlockCols;
-  static constexpr int kTileBytes = kCKeys * D * 2;            // K or V of one tile
-  // Even, so that with 16-row tiles a stage always serves the same group of
-  // warps: a group that met a stage only every other round could take the
-  // other group's unfinished round for its own (a parity tells two rounds
-  // apart, not three).
-  static constexpr int kStages = D == 128 ? 4 : (D == 64 ? 10 : 16);
-  static_assert(kStages % 2 == 0, "stages alternate between two groups");
-  static constexpr int kSlotBytes = 16 * D * 4;                // one warp's O
+  static constexpr int kTileBytes = kCKeys * D * 2;  // K or V of one tile
+  // CTAs per SM and stages of K and V: 130 to 190 KB of loads in flight on an
+  // SM (at d = 128, 64 KB reached 0.67 of the copy bandwidth on one long
+  // request, 128 KB 0.82)
+  static constexpr int kCtas = MT == 1 ? cache_ctas_narrow(D) : (D == 128 ? 1 : 2);
+  static constexpr int kStages = MT == 1 ? (D == 128 ? 3 : D == 64 ? 4 : 5) : (D == 128 ? 6 : D == 64 ? 5 : 10);
+  static constexpr int kSlotBytes = 16 * kCChunk * 4;  // one warp's chunk of O
   static constexpr int kOOff = kStages * 2 * kTileBytes;
-  static constexpr int kBarOff = kOOff + kCWarps * kSlotBytes;
+  static constexpr int kBarOff = kOOff + kWarps * kSlotBytes;
   static constexpr int kSmemBytes = kBarOff + 2048 + 1024;
-  static_assert(kSmemBytes <= 232448, "shared memory per CTA");
+  static_assert(kSmemBytes <= 233472 / kCtas - 1024, "shared memory per CTA");
 };
 
 struct CcShared {
   uint64_t full[16], empty[16];
-  float ml[kCWarps][16][2];
+  float ml[2 * kCGroupWarps][16][2];
   CacheRangeShared range;
   int abort;
 };
@@ -80,7 +80,7 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
 // its pieces swizzled over the bytes of a row by the row's place in 8.
 template <int D>
 __device__ __forceinline__ uint32_t cc_offset(int n, int c, int pr) {
-  using C = CcCfg<D>;
+  using C = CcCfg<D, 1>;
   const int r = n & (pr - 1);
   uint32_t off = (n - r) * (D * 2) + r * C::kRowBytes;
   if constexpr (C::kRowBytes == 128) {
@@ -92,9 +92,9 @@ __device__ __forceinline__ uint32_t cc_offset(int n, int c, int pr) {
 }
 
 // ------------------------------------------------------------- producer
-template <int D>
+template <int D, int MT>
 __device__ void cc_producer(const CacheFwdParams& p, uint8_t* smem, CcShared* sh, const CacheRange& R, Fail fail) {
-  using C = CcCfg<D>;
+  using C = CcCfg<D, MT>;
   const int lane = threadIdx.x & 31;
   const uint32_t base = smem_u32(smem);
   const int pr = min(1 << p.page_shift, kCKeys), pieces = kCKeys / pr;  // pieces: 1, 2 or 4
@@ -140,13 +140,13 @@ __device__ void cc_producer(const CacheFwdParams& p, uint8_t* smem, CcShared* sh
 // ------------------------------------------------------------- consumers
 template <int D, int ACT, int MT>
 __device__ void cc_consumer(const CacheFwdParams& p, uint8_t* smem, CcShared* sh, const CacheRange& R, Fail fail) {
-  using C = CcCfg<D>;
+  using C = CcCfg<D, MT>;
   constexpr int KS = D / 16;  // k steps of S = Q K^T
   constexpr int NT = D / 8;   // n tiles of O
   constexpr int kRows = 16 * MT;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int grp = warp / kCGroupWarps, kw = warp % kCGroupWarps;
-  const int row0 = MT == 2 ? 16 * grp : 0;
+  const int row0 = 16 * grp;
   const int pr = min(1 << p.page_shift, kCKeys);
   const uint32_t base = smem_u32(smem);
   // this warp's 16 keys: piece addresses for ldmatrix (the four 8x8 blocks of
@@ -154,7 +154,6 @@ __device__ void cc_consumer(const CacheFwdParams& p, uint8_t* smem, CcShared* sh
   const int kn = 16 * kw + (lane & 7) + ((lane & 16) ? 8 : 0), kc = (lane >> 3) & 1;
   const int vn = 16 * kw + (lane & 7) + ((lane & 8) ? 8 : 0), vc = lane >> 4;
   const int bias_reach = (p.bias_len - 1) / 2;
-  const float* ml = &sh->ml[0][0][0];
   uint32_t it = 0;
   bool dead = false;
   CacheWalk w;
@@ -206,7 +205,6 @@ __device__ void cc_consumer(const CacheFwdParams& p, uint8_t* smem, CcShared* sh
     float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
 
     for (int t = lo; t < hi; ++t, ++it) {
-      if (MT == 1 && static_cast<int>(it & 1) != grp) continue;
       const int st = it % C::kStages;
       if (!dead && !mbar_wait(&sh->full[st], (it / C::kStages) & 1, fail)) dead = true;
       dead = __any_sync(0xffffffffu, dead);
@@ -375,94 +373,72 @@ __device__ void cc_consumer(const CacheFwdParams& p, uint8_t* smem, CcShared* sh
         sh->ml[warp][(lane >> 2) + 8 * i][1] = l[i];
       }
     }
-    // row g, column pair c at pair c ^ 4 (g % 4) of the row: no bank conflicts
+    // O by chunks of 32 columns: a warp's slot holds its 16 rows, row g's
+    // column pair c at pair c ^ 4 (g % 4) (no bank conflicts); a thread sums 4
+    // columns of a row over the group's four slots
+    constexpr int kPerRow = kCChunk / 4;  // threads per row
+    const int lr = tid / kPerRow, cc = (tid % kPerRow) * 4;
+    const int g = lr & 15, w0 = (lr >> 4) * kCGroupWarps;
+    const bool live = lr < n_rows;
+    const int flat = w.row_tile * kRows + lr;
+    const int64_t token = r.q0 + (live ? flat / p.group : 0);
+    const int head = w.h * p.group + (live ? flat % p.group : 0);
+    const int64_t prow = (2 * static_cast<int64_t>(blockIdx.x) + (w.first ? 0 : 1)) * kRows + lr;
+    float M = -INFINITY, L = 0.f, inv = 1.f, f[kCGroupWarps] = {1.f, 1.f, 1.f, 1.f};
     float* slot = reinterpret_cast<float*>(smem + C::kOOff + warp * C::kSlotBytes);
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
+    for (int c0 = 0; c0 < D; c0 += kCChunk) {
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int g = (lane >> 2) + 8 * i, c2 = (4 * nt + (lane & 3)) ^ ((g & 3) << 2);
-        *reinterpret_cast<float2*>(slot + g * D + 2 * c2) = make_float2(o[nt][2 * i], o[nt][2 * i + 1]);
-      }
-    named_bar(1, kCWarps * 32);
-    {
-      constexpr int kPerRow = kCWarps * 32 / kRows;  // threads per row
-      constexpr int kCols = D / kPerRow;             // columns per thread (2, 4, 8 or 16)
-      constexpr int kParts = kCWarps / MT;           // warps that hold parts of a row
-      const int lr = tid / kPerRow, c0 = (tid % kPerRow) * kCols;
-      const int g = lr & 15, w0 = MT == 2 ? (lr >> 4) * kCGroupWarps : 0;
-      if (lr < n_rows) {
-        float M = -INFINITY, L = 0.f, f[kParts];
-        if constexpr (ACT == 2) {
+      for (int nt = 0; nt < kCChunk / 8; ++nt)
 #pragma unroll
-          for (int i = 0; i < kParts; ++i) M = fmaxf(M, ml[((w0 + i) * 16 + g) * 2]);
+        for (int i = 0; i < 2; ++i) {
+          const int gr = (lane >> 2) + 8 * i, c2 = (4 * nt + (lane & 3)) ^ ((gr & 3) << 2);
+          *reinterpret_cast<float2*>(slot + gr * kCChunk + 2 * c2) =
+              make_float2(o[c0 / 8 + nt][2 * i], o[c0 / 8 + nt][2 * i + 1]);
+        }
+      named_bar(1, C::kWarps * 32);
+      if (live) {
+        if (ACT == 2 && c0 == 0) {
+#pragma unroll
+          for (int i = 0; i < kCGroupWarps; ++i) M = fmaxf(M, sh->ml[w0 + i][g][0]);
           const float ref = M == -INFINITY ? 0.f : M;
 #pragma unroll
-          for (int i = 0; i < kParts; ++i) {
-            f[i] = ex2_sfu(ml[((w0 + i) * 16 + g) * 2] - ref);
-            L = __fmaf_rn(ml[((w0 + i) * 16 + g) * 2 + 1], f[i], L);
+          for (int i = 0; i < kCGroupWarps; ++i) {
+            f[i] = ex2_sfu(sh->ml[w0 + i][g][0] - ref);
+            L = __fmaf_rn(sh->ml[w0 + i][g][1], f[i], L);
           }
+          if (w.whole) inv = L > 0.f ? 1.f / L : (L == 0.f ? 0.f : L);  // no key seen: 0 (a NaN sum stays NaN)
         }
-        float acc[kCols];
+        float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-        for (int c = 0; c < kCols; c += 2) {
-          const int c2 = ((c0 + c) >> 1) ^ ((g & 3) << 2);
-          float2 a = make_float2(0.f, 0.f);
-#pragma unroll
-          for (int i = 0; i < kParts; ++i) {
-            const float2 v = *reinterpret_cast<const float2*>(smem + C::kOOff + (w0 + i) * C::kSlotBytes +
-                                                              (g * D + 2 * c2) * 4);
-            if constexpr (ACT == 2) {
-              a.x = __fmaf_rn(v.x, f[i], a.x);
-              a.y = __fmaf_rn(v.y, f[i], a.y);
-            } else {
-              a.x += v.x;
-              a.y += v.y;
-            }
-          }
-          acc[c] = a.x;
-          acc[c + 1] = a.y;
+        for (int i = 0; i < kCGroupWarps; ++i) {
+          const float4 v = *reinterpret_cast<const float4*>(smem + C::kOOff + (w0 + i) * C::kSlotBytes +
+                                                            (g * kCChunk + (cc ^ ((g & 3) << 3))) * 4);
+          a.x = __fmaf_rn(v.x, f[i], a.x);
+          a.y = __fmaf_rn(v.y, f[i], a.y);
+          a.z = __fmaf_rn(v.z, f[i], a.z);
+          a.w = __fmaf_rn(v.w, f[i], a.w);
         }
-        if (w.whole) {
-          const int flat = w.row_tile * kRows + lr;
-          const int64_t token = r.q0 + flat / p.group;
-          const int head = w.h * p.group + flat % p.group;
-          if constexpr (ACT == 2) {
-            const float inv = L > 0.f ? 1.f / L : (L == 0.f ? 0.f : L);  // no key seen: 0 (a NaN sum stays NaN)
-#pragma unroll
-            for (int c = 0; c < kCols; ++c) acc[c] *= inv;
-            if (c0 == 0 && p.lse != nullptr)
-              p.lse[static_cast<int64_t>(head) * p.total_q + token] = L == 0.f ? -INFINITY : (M + log2f(L)) * kLn2;
-          }
-          __nv_bfloat16* dst = p.out + (token * p.heads + head) * D + c0;
-          uint32_t pk[kCols / 2];
-#pragma unroll
-          for (int c = 0; c < kCols / 2; ++c) pk[c] = pack_bf16(acc[2 * c], acc[2 * c + 1]);
-          if constexpr (kCols >= 8) {
-#pragma unroll
-            for (int c = 0; c < kCols / 8; ++c)
-              st_global_v4(dst + 8 * c, pk[4 * c], pk[4 * c + 1], pk[4 * c + 2], pk[4 * c + 3]);
-          } else if constexpr (kCols == 4) {
-            *reinterpret_cast<uint2*>(dst) = make_uint2(pk[0], pk[1]);
-          } else {
-            *reinterpret_cast<uint32_t*>(dst) = pk[0];
-          }
-        } else {
-          const int64_t prow = (2 * static_cast<int64_t>(blockIdx.x) + (w.first ? 0 : 1)) * kRows + lr;
-#pragma unroll
-          for (int c = 0; c < kCols; c += 2)
-            *reinterpret_cast<float2*>(p.part_o + prow * D + c0 + c) = make_float2(acc[c], acc[c + 1]);
-          if (ACT == 2 && c0 == 0) p.part_ml[prow] = make_float2(M, L);
-        }
+        if (w.whole)
+          *reinterpret_cast<uint2*>(p.out + (token * p.heads + head) * D + c0 + cc) =
+              make_uint2(pack_bf16(a.x * inv, a.y * inv), pack_bf16(a.z * inv, a.w * inv));
+        else
+          *reinterpret_cast<float4*>(p.part_o + prow * D + c0 + cc) = a;
       }
+      named_bar(1, C::kWarps * 32);  // the slots are free again
     }
-    named_bar(1, kCWarps * 32);  // the slots are free again
+    if (ACT == 2 && live && cc == 0) {
+      if (!w.whole) p.part_ml[prow] = make_float2(M, L);
+      else if (p.lse != nullptr)
+        p.lse[static_cast<int64_t>(head) * p.total_q + token] = L == 0.f ? -INFINITY : (M + log2f(L)) * kLn2;
+    }
   }
 }
 
 template <int D, int ACT, int MT>
-__global__ void __launch_bounds__(kCThreads, 1) cache_fwd_kernel(const __grid_constant__ CacheFwdParams p) {
-  using C = CcCfg<D>;
+__global__ void __launch_bounds__((CcCfg<D, MT>::kThreads), (CcCfg<D, MT>::kCtas))
+    cache_fwd_kernel(const __grid_constant__ CacheFwdParams p) {
+  using C = CcCfg<D, MT>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   CcShared* sh = reinterpret_cast<CcShared*>(smem + C::kBarOff);
@@ -470,16 +446,16 @@ __global__ void __launch_bounds__(kCThreads, 1) cache_fwd_kernel(const __grid_co
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::kStages; ++s) {
       mbar_init(&sh->full[s], 1);
-      mbar_init(&sh->empty[s], MT == 2 ? kCWarps : kCGroupWarps);
+      mbar_init(&sh->empty[s], C::kWarps);
     }
     sh->abort = 0;
     p.err[blockIdx.x] = kOk;
     fence_mbar_init();
   }
-  const CacheRange R = cache_range<kCKeys>(p, &sh->range, kCMinTiles);  // (ends in a barrier)
-  if (threadIdx.x == (kCWarps - 1) * 32) cache_open<kCKeys>(p, R);
+  const CacheRange R = cache_range<kCKeys>(p, &sh->range, kCMinRange);  // (ends in a barrier)
+  if (threadIdx.x == (C::kWarps - 1) * 32) cache_open<kCKeys>(p, R);
   Fail fail{&sh->abort, p.err + blockIdx.x, p.wait_limit_ns};
-  if (threadIdx.x >= kCWarps * 32) cc_producer<D>(p, smem, sh, R, fail);
+  if (threadIdx.x >= C::kWarps * 32) cc_producer<D, MT>(p, smem, sh, R, fail);
   else cc_consumer<D, ACT, MT>(p, smem, sh, R, fail);
 }
 
@@ -509,7 +485,8 @@ __global__ void __launch_bounds__(128) cache_join_kernel(const __grid_constant__
   const int64_t flat = static_cast<int64_t>(j.rt) * R + 4 * blockIdx.y + warp;
   if (4 * static_cast<int>(blockIdx.y) + warp >= R || flat >= static_cast<int64_t>(T) * p.group) return;
   const int lr = 4 * blockIdx.y + warp;
-  const int c0 = static_cast<int>(j.t0 / j.per), c1 = static_cast<int>((j.t1 - 1) / j.per);
+  // (the first range that holds one of its tiles, the last)
+  const int c0 = static_cast<int>((j.t0 + p.item_cost) / j.per), c1 = static_cast<int>((j.t1 - 1) / j.per);
   // CTA c's part lies in its first slot when its range starts inside the item (or at its start)
   auto row_of = [&](int c) { return (2 * static_cast<int64_t>(c) + (c * j.per < j.t0 ? 1 : 0)) * R + lr; };
   float M = -INFINITY, L = 0.f;
@@ -558,11 +535,11 @@ __global__ void __launch_bounds__(128) cache_join_kernel(const __grid_constant__
 template <int D, int ACT, int MT>
 static cudaError_t launch_cc(const CacheFwdParams& p, int grid, cudaStream_t stream) {
   auto kern = cache_fwd_kernel<D, ACT, MT>;
-  constexpr int kSmem = CcCfg<D>::kSmemBytes;
+  constexpr int kSmem = CcCfg<D, MT>::kSmemBytes;
   static DeviceFlags attr_set = {};
   cudaError_t e = smem_attr_once(kern, kSmem, attr_set);
   if (e != cudaSuccess) return e;
-  kern<<<grid, kCThreads, kSmem, stream>>>(p);
+  kern<<<grid, CcCfg<D, MT>::kThreads, kSmem, stream>>>(p);
   return cudaGetLastError();
 }
 

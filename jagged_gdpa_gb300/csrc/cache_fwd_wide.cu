@@ -32,7 +32,7 @@
 
 namespace jg {
 
-constexpr int kWideMinTiles = 2;  // a range below this many tiles is not worth its own CTA
+constexpr int kWideMinRange = 6;  // a range below this many tiles is not worth its own CTA
 constexpr int kWideThreads = 384;
 
 template <int D>
@@ -705,7 +705,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) cache_fwd_wide_kernel(const _
     tmem_alloc(&sh->tmem_base, 512);
     tmem_relinquish();
   }
-  const CacheRange R = cache_range<kTile>(p, &sh->range, kWideMinTiles);
+  const CacheRange R = cache_range<kTile>(p, &sh->range, kWideMinRange);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
