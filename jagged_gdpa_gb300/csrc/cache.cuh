@@ -19,8 +19,11 @@ enum : int { kErrOutOfPages = 8, kErrBadPage = 9 };
 
 constexpr int kCacheMaxBatch = 16384;  // requests per call (the plan's prefix sums live in shared memory)
 
-// CTAs per SM of the attention kernel for up to 16 rows (cache_fwd.cu).
-__host__ __device__ constexpr int cache_ctas_narrow(int d) { return d == 128 ? 2 : (d == 64 ? 3 : 4); }
+// CTAs per SM of the attention kernel for up to 16 mt rows and w columns of K
+// and V per item (cache_fwd.cu).
+__host__ __device__ constexpr int cache_ctas(int w, int mt) {
+  return mt == 1 ? (w == 128 ? 2 : w == 64 ? 3 : 4) : (w == 128 ? 1 : 2);
+}
 
 struct CachePlanParams {
   const int32_t* ctx;
@@ -86,6 +89,7 @@ struct CacheFwdParams {
   int32_t page_shift, width, num_pages;
   int32_t mask_words, bias_len, window;
   int32_t rows_per_tile;     // query rows (token, head of the group) of one item
+  int32_t heads_per_item;    // key/value heads of one item
   int32_t item_cost;         // tiles that an item's start and end are worth
   float scale;               // s (GELU / SiLU) or s log2(e) (softmax)
   unsigned long long wait_limit_ns;
@@ -112,7 +116,7 @@ __device__ __forceinline__ CacheReq cache_req(const CacheFwdParams& p, int b) {
   return r;
 }
 __device__ __forceinline__ int64_t cache_cost(const CacheFwdParams& p, const CacheReq& r) {
-  return r.T <= 0 ? 0 : static_cast<int64_t>(p.kv_heads) * r.rt * (r.n + p.item_cost);
+  return r.T <= 0 ? 0 : static_cast<int64_t>(p.kv_heads / p.heads_per_item) * r.rt * (r.n + p.item_cost);
 }
 __device__ __forceinline__ bool cache_req_ok(const CacheFwdParams& p, const CacheReq& r) {
   return r.T >= 0 && r.T <= p.max_q && r.L >= r.T &&

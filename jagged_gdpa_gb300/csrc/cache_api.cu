@@ -19,7 +19,7 @@ cudaError_t launch_cache_fwd_d(const CacheFwdParams& p, int act, int grid, cudaS
 template <int D>
 cudaError_t launch_cache_fwd_wide_d(const CacheFwdParams& p, int act, int grid, cudaStream_t stream);
 template <int D>
-cudaError_t launch_cache_join_d(const CacheFwdParams& p, int act, int n_ctas, int max_rows, cudaStream_t stream);
+cudaError_t launch_cache_join_d(const CacheFwdParams& p, int act, int n_ctas, int item_rows, cudaStream_t stream);
 cudaError_t launch_cache_plan(const CachePlanParams& p, int sms, cudaStream_t stream);
 cudaError_t launch_cache_append(const CacheAppendParams& p, cudaStream_t stream);
 }  // namespace jg
@@ -54,7 +54,8 @@ jgdpa_status check_cache(const void* k_cache, const void* v_cache, int64_t k_pag
 
 struct CacheLayout {
   size_t err, join, part_ml, part_o, total;
-  int rows, grid;  // query rows of one item, CTAs
+  int rows, grid;  // query rows of one item per key/value head, CTAs
+  int heads;       // key/value heads of one item
   bool wide;       // 128-row tiles through tensor memory
 };
 bool cache_layout(int32_t heads, int32_t kv_heads, int32_t head_dim, int32_t max_q, CacheLayout* L) {
@@ -68,11 +69,14 @@ bool cache_layout(int32_t heads, int32_t kv_heads, int32_t head_dim, int32_t max
     const int tile = jg::kTile / group * group;
     L->rows = max_rows > tile ? 2 * tile : tile;
     L->grid = sms;
+    L->heads = 1;
   } else {
+    // small heads side by side; measured at d = 32, 16 heads, 8 tokens: see the kernel
+    L->heads = kv_heads % (128 / head_dim) == 0 ? 128 / head_dim : 1;
     L->rows = max_rows <= 16 ? 16 : 32;
-    L->grid = sms * (max_rows <= 16 ? jg::cache_ctas_narrow(head_dim) : head_dim == 128 ? 1 : 2);
+    L->grid = sms * jg::cache_ctas(head_dim * L->heads, L->rows / 16);
   }
-  const size_t parts = 2 * static_cast<size_t>(L->grid) * L->rows;
+  const size_t parts = 2 * static_cast<size_t>(L->grid) * L->rows * L->heads;
   size_t off = kAlign;  // the status word
   L->err = off;
   off += up(L->grid * sizeof(int));
@@ -272,8 +276,9 @@ jgdpa_status jgdpa_cache_fwd(const void* q, int64_t q_stride, const void* k_cach
   }
   jg::CacheFwdParams p{};
   const int32_t box = L.wide ? jg::kTile : 64;
-  if (!cache_map(&p.tm_k, k_cache, k_page_stride, num_pages, page_size, kv_heads, head_dim, box, !L.wide) ||
-      !cache_map(&p.tm_v, v_cache, v_page_stride, num_pages, page_size, kv_heads, head_dim, box, !L.wide) ||
+  const int32_t map_heads = kv_heads / L.heads, map_dim = head_dim * L.heads;  // heads that go together as one
+  if (!cache_map(&p.tm_k, k_cache, k_page_stride, num_pages, page_size, map_heads, map_dim, box, !L.wide) ||
+      !cache_map(&p.tm_v, v_cache, v_page_stride, num_pages, page_size, map_heads, map_dim, box, !L.wide) ||
       (L.wide && !query_map(&p.tm_q, q, q_stride, total_q, heads, head_dim, heads / kv_heads)))
     return JGDPA_ERR_CUDA;
   p.k_cache = static_cast<const __nv_bfloat16*>(k_cache);
@@ -308,15 +313,16 @@ jgdpa_status jgdpa_cache_fwd(const void* q, int64_t q_stride, const void* k_cach
   p.bias_len = bias_len;
   p.window = window;
   p.rows_per_tile = L.rows;
-  p.item_cost = 4;  // measured: 3 to 5 tiles (64 or 128 keys) of time
+  p.heads_per_item = L.heads;
+  p.item_cost = L.wide ? 12 : 4;
   p.scale = act == JGDPA_ACT_SOFTMAX ? scale * jg::kLog2e : scale;
   p.wait_limit_ns = jg::host_wait_limit_ns();
-  const int max_tile_rows = static_cast<int>(std::min<int64_t>(L.rows, max_rows));
+  const int item_rows = L.heads > 1 ? L.rows * L.heads : static_cast<int>(std::min<int64_t>(L.rows, max_rows));
   auto launch = [&](auto dim) -> cudaError_t {
     constexpr int D = decltype(dim)::value;
     cudaError_t e = L.wide ? jg::launch_cache_fwd_wide_d<D>(p, act, L.grid, stream)
                            : jg::launch_cache_fwd_d<D>(p, act, L.grid, stream);
-    return e != cudaSuccess ? e : jg::launch_cache_join_d<D>(p, act, L.grid, max_tile_rows, stream);
+    return e != cudaSuccess ? e : jg::launch_cache_join_d<D>(p, act, L.grid, item_rows, stream);
   };
   JG_CUDA(head_dim == 128  ? launch(std::integral_constant<int, 128>{})
           : head_dim == 64 ? launch(std::integral_constant<int, 64>{})

@@ -480,22 +480,33 @@ __device__ void cw_fixer(const CacheFwdParams& p, uint8_t* smem, CwShared* sh, c
         const uint32_t vr = v_base + st * C::kTileBytes + row * C::kRowBytes;
         // (pieces in any order, whatever the swizzle: from the lane's on, so
         // that the lanes, a row apart, meet different banks)
+        auto piece = [&](int c) {
+          return vr + (c / kPieces) * C::kBlockBytes + ((c + lane * kPieces / 8) % kPieces) * 16;
+        };
+        if (past) {
+#pragma unroll
+          for (int c = 0; c < D / 8; ++c) st_shared_v4(piece(c), 0u, 0u, 0u, 0u);
+          continue;
+        }
+        // 0 * x summed over the row is NaN when one of its values is not finite
+        const __nv_bfloat162 zero = __float2bfloat162_rn(0.f);
+        __nv_bfloat162 sum = zero;
 #pragma unroll
         for (int c = 0; c < D / 8; ++c) {
-          const uint32_t a = vr + (c / kPieces) * C::kBlockBytes + ((c + lane * kPieces / 8) % kPieces) * 16;
           uint32_t x[4];
-          ld_shared_v4(a, x[0], x[1], x[2], x[3]);
-          uint32_t bad = 0;
+          ld_shared_v4(piece(c), x[0], x[1], x[2], x[3]);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const uint32_t f = past ? 0xFFFFFFFFu : cc_nonfinite(x[e]);
-            bad |= f;
-            x[e] &= ~f;
-          }
-          if (bad) {
-            if (!past) *const_cast<volatile int*>(&sh->odd[number & 15]) = number;
-            st_shared_v4(a, x[0], x[1], x[2], x[3]);
-          }
+          for (int e = 0; e < 4; ++e) sum = __hfma2(*reinterpret_cast<__nv_bfloat162*>(&x[e]), zero, sum);
+        }
+        if (__low2float(sum) == 0.f && __high2float(sum) == 0.f) continue;
+        *const_cast<volatile int*>(&sh->odd[number & 15]) = number;
+#pragma unroll 1
+        for (int c = 0; c < D / 8; ++c) {
+          uint32_t x[4];
+          ld_shared_v4(piece(c), x[0], x[1], x[2], x[3]);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) x[e] &= ~cc_nonfinite(x[e]);
+          st_shared_v4(piece(c), x[0], x[1], x[2], x[3]);
         }
       }
       fence_proxy_async_smem();
