@@ -54,12 +54,12 @@ struct CacheAppendParams {
   int32_t slot_end;            // num_pages * page_size
 };
 
-// The item that a CTA's range of key tiles starts inside of, written for the
-// joining kernel: valid only from the first CTA that continues an item.
+// The item that a range of key tiles starts inside of, written for the joining
+// kernel: valid only from the first range that continues an item.
 struct CacheJoin {
   int32_t valid, b, h, rt;
   int64_t t0, t1;  // the item's place in the global order
-  int64_t per;     // length of a CTA's range
+  int64_t per;     // length of a range
 };
 
 struct CacheFwdParams {
@@ -79,9 +79,11 @@ struct CacheFwdParams {
   const int32_t* depth;      // [total_q] or nullptr
   __nv_bfloat16* out;        // [total_q][heads][D]
   float* lse;                // [heads][total_q] or nullptr
-  float* part_o;             // [2 grid][rows per tile][D]
-  float2* part_ml;           // [2 grid][rows per tile]: running maximum (log2 units) and sum
-  CacheJoin* join;           // [grid]
+  // parts of items that other ranges share, two per range: the one its range
+  // starts with, and its last
+  float* part_o;             // [2 ranges][heads per item][rows per tile][D]
+  float2* part_ml;           // [2 ranges][heads per item][rows per tile]: maximum (log2 units) and sum
+  CacheJoin* join;           // [ranges]
   int* err;                  // [grid]: one status word per CTA, joined into `status`
   int* status;
   int64_t total_q;
@@ -128,24 +130,26 @@ __device__ __forceinline__ bool cache_req_ok(const CacheFwdParams& p, const Cach
 // tiles and a lead of item_cost tiles' length, what its start and end take
 // beside them; laid end to end (request by request, row tiles of one head next
 // to each other so that they meet in L2) they form one line that is cut into
-// equal ranges, one per CTA, whatever the lengths.  (Without the lead, ranges
+// equal ranges, one or two per CTA, whatever the lengths.  (Without the lead, ranges
 // that fall on many short requests took half as long again as the others.)  An
 // item cut by a range border is finished by the joining kernel.
 struct CacheRange {
   int64_t total, per, begin, end;
+  int index;    // of the range
   int b;        // request that `begin` lies in
-  int64_t rem;  // begin minus the request's first tile
+  int64_t rem;  // begin minus the request's start
   bool ok;
 };
 struct CacheRangeShared {
-  int64_t warp_sum[32];
+  int64_t warp_sum[16];
   int64_t rem;
   int b;
 };
 
-// Run by every thread of the CTA (a whole number of warps, at most 1024).
-template <int KT>
-__device__ CacheRange cache_range(const CacheFwdParams& p, CacheRangeShared* sh, int min_range) {
+// This CTA's N ranges (of N gridDim.x).  Run by every thread of the CTA (a whole
+// number of warps, at most 512); ends in a barrier.
+template <int KT, int N>
+__device__ void cache_ranges(const CacheFwdParams& p, CacheRangeShared* sh, int min_range, CacheRange (&R)[N]) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nt = blockDim.x, nw = nt >> 5;
   const int each = (p.batch + nt - 1) / nt;
   const int b0 = min(tid * each, p.batch), b1 = min(b0 + each, p.batch);
@@ -163,36 +167,42 @@ __device__ CacheRange cache_range(const CacheFwdParams& p, CacheRangeShared* sh,
     const int64_t v = __shfl_up_sync(0xffffffffu, incl, o);
     if (lane >= o) incl += v;
   }
-  if (lane == 31) sh->warp_sum[warp] = incl;
+  if (lane == 31) sh[0].warp_sum[warp] = incl;
   const bool all_ok = __syncthreads_and(ok) != 0;
   int64_t base = 0, total = 0;
   for (int w = 0; w < nw; ++w) {
-    const int64_t v = sh->warp_sum[w];
+    const int64_t v = sh[0].warp_sum[w];
     if (w < warp) base += v;
     total += v;
   }
-  CacheRange R;
-  R.ok = all_ok;
-  R.total = total;
-  const int64_t g = gridDim.x;
-  R.per = max((total + g - 1) / g, static_cast<int64_t>(min_range));
-  R.begin = min(R.per * blockIdx.x, total);
-  R.end = min(R.begin + R.per, total);
-  int64_t at = base + incl - sum;
-  if (all_ok && R.begin < total && at <= R.begin && R.begin < at + sum) {
-    int b = b0;
-    for (;; ++b) {
-      const int64_t c = cache_cost(p, cache_req<KT>(p, b));
-      if (R.begin < at + c) break;
-      at += c;
+  const int64_t g = static_cast<int64_t>(gridDim.x) * N;
+  const int64_t per = max((total + g - 1) / g, static_cast<int64_t>(min_range));
+#pragma unroll
+  for (int s = 0; s < N; ++s) {
+    R[s].ok = all_ok;
+    R[s].total = total;
+    R[s].per = per;
+    R[s].index = N * blockIdx.x + s;
+    R[s].begin = min(per * R[s].index, total);
+    R[s].end = min(R[s].begin + per, total);
+    int64_t at = base + incl - sum;
+    if (all_ok && R[s].begin < total && at <= R[s].begin && R[s].begin < at + sum) {
+      int b = b0;
+      for (;; ++b) {
+        const int64_t c = cache_cost(p, cache_req<KT>(p, b));
+        if (R[s].begin < at + c) break;
+        at += c;
+      }
+      sh[s].b = b;
+      sh[s].rem = R[s].begin - at;
     }
-    sh->b = b;
-    sh->rem = R.begin - at;
   }
   __syncthreads();
-  R.b = sh->b;
-  R.rem = sh->rem;
-  return R;
+#pragma unroll
+  for (int s = 0; s < N; ++s) {
+    R[s].b = sh[s].b;
+    R[s].rem = sh[s].rem;
+  }
 }
 
 // a / b for a >= 0: the 64-bit division, some 100 instructions, only where it is needed.
@@ -261,11 +271,11 @@ struct CacheWalk {
   }
 };
 
-// Writes this CTA's join record (one thread).
+// Writes a range's join record (one thread).
 template <int KT>
 __device__ __forceinline__ void cache_open(const CacheFwdParams& p, const CacheRange& R) {
-  const int c = blockIdx.x;
-  if (!R.ok) p.err[c] = kErrBadOffsets;
+  const int c = R.index;
+  if (!R.ok) p.err[blockIdx.x] = kErrBadOffsets;
   CacheJoin j{};
   if (R.ok && R.begin < R.end) {
     const CacheReq r = cache_req<KT>(p, R.b);

@@ -35,46 +35,61 @@ namespace jg {
 constexpr int kWideMinRange = 6;  // a range below this many tiles is not worth its own CTA
 constexpr int kWideThreads = 384;
 
-template <int D>
+template <int D, bool PAIR>
 struct CwCfg {
   static constexpr int kBlockCols = D < 64 ? D : 64;
   static constexpr int kRowBytes = kBlockCols * 2;
   static constexpr int kBlockBytes = kTile * kRowBytes;  // 128 rows of one column block
   static constexpr int kBlocks = D / kBlockCols;
   static constexpr int kTileBytes = kTile * D * 2;
-  static constexpr int kStages = D == 128 ? 2 : (D == 64 ? 4 : 8);
+  // K and V go through one ring of `kStages` tiles in the order K0 K1 V0 K2 V1
+  // ..: a V is not needed before its P, more than a tile's time after its K, and
+  // would only hold its stage meanwhile
+  static constexpr int kStages = D == 128 ? (PAIR ? 4 : 5) : (D == 64 ? 11 : 16);
   static constexpr uint32_t kSwizzle = kRowBytes == 128 ? 2u : 4u;
   static constexpr int kSBO = 8 * kRowBytes;
   static constexpr int kQOff = 0;  // two Q tiles
-  static constexpr int kKOff = kQOff + 2 * kTileBytes;
-  static constexpr int kVOff = kKOff + kStages * kTileBytes;
-  static constexpr int kBarOff = kVOff + kStages * kTileBytes;
-  static constexpr int kSmemBytes = kBarOff + 8192 + 1024;
+  static constexpr int kRingOff = kQOff + 2 * kTileBytes;
+  static constexpr int kBarOff = kRingOff + kStages * kTileBytes;
+  static constexpr int kSmemBytes = kBarOff + 2048 + (PAIR ? 2 * 2 * kTile * 8 : 0) + 1024;
   static_assert(kSmemBytes <= 232448, "shared memory per CTA");
+  // Ring entries of the CTA's tile `it`.  (The K entry before the very last V
+  // is skipped; the ring does not come round to it.)
+  static __device__ __forceinline__ uint32_t entry_k(uint32_t it) { return it == 0 ? 0 : 2 * it - 1; }
+  static __device__ __forceinline__ uint32_t entry_v(uint32_t it) { return 2 * it + 2; }
+  static __device__ __forceinline__ int stage(uint32_t entry) { return entry % kStages; }
+  static __device__ __forceinline__ uint32_t parity(uint32_t entry) { return (entry / kStages) & 1; }
 };
 
 struct CwShared {
   uint64_t q_full[2], q_empty[2];
-  uint64_t k_full[8], k_empty[8], v_full[8], v_empty[8];
-  uint64_t s_full[2], p_full[2], o_full[2];
-  uint64_t v_fixed[8];     // masked tiles only: a stage's next one comes after its product
-  uint64_t o_empty, drain;
-  CacheRangeShared range;
-  float2 ml[2][2][kTile];  // [part parity][stream][row]: maximum and sum
+  uint64_t full[16], empty[16];
+  // The CTA's n-th masked tile, at n % 2: asked for when its S is issued, its V
+  // safe.  (Each stream has at most one tile whose S is issued and P V is not.)
+  uint64_t fix_ask[2], fixed[2];
+  uint64_t s_full[2], p_full[2], o_full[2], o_empty[2];
+  uint64_t drain;
+  CacheRangeShared range[2];
   uint32_t tmem_base;
   int abort;
-  int odd[16];             // number of the last part (mod 16) whose masked tiles hold a V that is not finite
+  int odd[2][16];          // by stream (0 for both of a pair): number of the last part (mod 16) whose
+                           // masked tiles hold a V that is not finite
+  float2 ml[];             // pairs only, [part parity][stream][row]: maximum and sum
 };
-static_assert(sizeof(CwShared) <= 8192, "shared block");
+static_assert(sizeof(CwShared) <= 2048, "shared block");
 
 // What every role works out about a part.
 struct CwPart {
   int lo, n;        // key tiles [lo, lo + n)
   int tile_rows;    // rows of one 128-row tile: a whole number of tokens
   int rows;         // rows of the part
-  bool pair;        // two tiles of rows; otherwise the streams share one
-  int count[2];     // tiles of each stream
+  bool pair;        // two tiles of rows; otherwise one
+  int first_token;  // of the part's rows
+  int plain_lo, plain_hi;  // tiles in which every row sees every key
+  int far_hi;              // tiles below it are plain in the bias: R or more behind every row
 
+  __device__ __forceinline__ CwPart() {}
+  // (whole warp)
   __device__ __forceinline__ CwPart(const CacheFwdParams& p, const CacheWalk& w) {
     int hi;
     w.tiles<kTile>(p, lo, hi);
@@ -84,100 +99,176 @@ struct CwPart {
                                 static_cast<int64_t>(w.r.T) * p.group -
                                     static_cast<int64_t>(w.row_tile) * p.rows_per_tile));
     pair = rows > tile_rows;
-    count[0] = pair ? n : (n + 1) / 2;
-    count[1] = pair ? n : n / 2;
+    first_token = w.row_tile * (p.rows_per_tile / p.group);
+    const int C = w.r.C, last_token = first_token + (rows - 1) / p.group;
+    plain_lo = 0;
+    plain_hi = (p.window <= 0 && p.mask == nullptr ? min(w.r.L, C + first_token + 1) : C) / kTile;
+    if (p.window > 0) {
+      int depth = last_token;  // the rows' largest
+      if (p.depth != nullptr) {
+        depth = 0;
+        for (int t = first_token + (threadIdx.x & 31); t <= last_token; t += 32) depth = max(depth, __ldg(p.depth + w.r.q0 + t));
+        depth = __reduce_max_sync(0xffffffffu, depth);
+      }
+      const int64_t behind = static_cast<int64_t>(C) + depth - p.window;  // keys up to here are out of some row's window
+      if (behind >= 0) plain_lo = static_cast<int>(min(behind / kTile + 1, static_cast<int64_t>(INT32_MAX)));
+    }
+    const int reach = max((p.bias_len - 1) / 2, 1);
+    far_hi = p.bias_len == 0 ? INT32_MAX : (C >= reach ? (C - reach + 1) / kTile : 0);
   }
-  // The largest depth of the part's rows (whole warp).
-  __device__ __forceinline__ int far_depth(const CacheFwdParams& p, const CacheWalk& w) const {
-    const int64_t row0 = static_cast<int64_t>(w.row_tile) * p.rows_per_tile;
-    const int first = static_cast<int>(row0 / p.group), last = static_cast<int>((row0 + rows - 1) / p.group);
-    if (p.window <= 0 || p.depth == nullptr) return last;
-    int d = 0;
-    for (int t = first + (threadIdx.x & 31); t <= last; t += 32) d = max(d, __ldg(p.depth + w.r.q0 + t));
-    return __reduce_max_sync(0xffffffffu, d);
-  }
-  // A tile is plain when every row of the part sees all of its keys.
-  __device__ __forceinline__ bool plain(const CacheFwdParams& p, const CacheWalk& w, int far_depth, int key0) const {
-    const int last = key0 + kTile - 1;
-    if (p.window > 0) return last < w.r.C && static_cast<int64_t>(w.r.C) + far_depth - key0 < p.window;
-    if (p.mask != nullptr) return last < w.r.C;
-    return last < w.r.L && last <= w.r.C + static_cast<int>(static_cast<int64_t>(w.row_tile) * p.rows_per_tile / p.group);
-  }
-  // the part's tile that stream s takes as its i-th
+  __device__ __forceinline__ bool plain(int tile) const { return tile >= plain_lo && tile < plain_hi; }
+  // Of a CTA whose streams share their parts: the tiles of stream s, and the one it takes as its i-th.
+  __device__ __forceinline__ int count(int s) const { return pair ? n : (n + 1 - s) / 2; }
   __device__ __forceinline__ int at(int s, int i) const { return pair ? i : 2 * i + s; }
 };
 
-// ------------------------------------------------------------- producer
-template <int D>
-__device__ void cw_producer(const CacheFwdParams& p, uint8_t* smem, CwShared* sh, const CacheRange& R, Fail fail) {
-  using C = CwCfg<D>;
-  const int lane = threadIdx.x & 31;
-  const int pr = min(1 << p.page_shift, kTile), pieces = kTile / pr;  // pieces: 1, 2, 4 or 8
-  const int piece = lane & 7, cb = lane >> 3;
-  const uint32_t base = smem_u32(smem);
-  uint32_t q_n = 0, k_n = 0, v_n = 0;
-  bool ok = true;
-  CacheWalk w;
-  w.init(R);
-  for (; ok && w.next<kTile>(p); w.advance()) {
-    const CwPart part(p, w);
-    if (part.n == 0) continue;
-    for (int s = 0; s < (part.pair ? 2 : 1) && ok; ++s, ++q_n) {
-      const int slot = q_n & 1;
-      if (!(ok = mbar_wait_warp(&sh->q_empty[slot], ((q_n >> 1) & 1) ^ 1, fail))) break;
-      if (lane == 0) {
-        mbar_arrive_tx(&sh->q_full[slot], part.tile_rows * D * 2);
-        const int token = w.r.q0 + w.row_tile * (p.rows_per_tile / p.group) + s * (part.tile_rows / p.group);
+// The tiles of a CTA with lone streams in the order in which every role takes
+// them: by turns, one tile of each stream that has any left.
+struct CwTurns {
+  CacheWalk w[2];
+  CwPart part[2];
+  int i[2];  // tile of the part
+  bool more[2];
+
+  // (a part without tiles, all behind what its rows see, is passed over)
+  __device__ __forceinline__ void part_from(const CacheFwdParams& p, int s) {
+    i[s] = 0;
+    for (;; w[s].advance()) {
+      more[s] = w[s].next<kTile>(p);
+      if (!more[s]) return;
+      part[s] = CwPart(p, w[s]);
+      if (part[s].n > 0) return;
+    }
+  }
+  __device__ __forceinline__ CwTurns(const CacheFwdParams& p, const CacheRange (&R)[2]) {
 #pragma unroll
-        for (int b = 0; b < C::kBlocks; ++b)
-          tma_load_3d(smem + C::kQOff + slot * C::kTileBytes + b * C::kBlockBytes, &p.tm_q, &sh->q_full[slot],
-                      b * C::kBlockCols, w.h * p.group, token);
-      }
-      __syncwarp();
-    }
-    const int32_t* row = p.table + static_cast<int64_t>(w.b) * p.width;
-    for (int t = part.lo; t < part.lo + part.n && ok; ++t) {
-      // lane: piece lane % 8 (min(page size, 128) tokens) of column block lane / 8
-      const int key = t * kTile + piece * pr;
-      const bool mine = cb < C::kBlocks && piece < pieces && key < w.r.L;
-      int page = p.num_pages;
-      if (mine) {
-        page = __ldg(row + (key >> p.page_shift));
-        if (static_cast<uint32_t>(page) >= static_cast<uint32_t>(p.num_pages)) {
-          atomicCAS(fail.status, kOk, kErrBadPage);
-          page = p.num_pages;  // outside the map: the copy writes zeros and reads nothing
-        }
-      }
-      const uint32_t bytes = min(pieces, (w.r.L - t * kTile + pr - 1) / pr) * pr * D * 2;
-      const uint32_t dst = base + cb * C::kBlockBytes + piece * pr * C::kRowBytes;
-      const int y = key & ((1 << p.page_shift) - 1);
-      int st = k_n % C::kStages;
-      if (!(ok = mbar_wait_warp(&sh->k_empty[st], ((k_n / C::kStages) & 1) ^ 1, fail))) break;
-      if (lane == 0) mbar_arrive_tx(&sh->k_full[st], bytes);
-      __syncwarp();
-      if (mine) tma_load_5d(dst + C::kKOff + st * C::kTileBytes, &p.tm_k, &sh->k_full[st], 0, y, cb, w.h, page);
-      ++k_n;
-      st = v_n % C::kStages;
-      if (!(ok = mbar_wait_warp(&sh->v_empty[st], ((v_n / C::kStages) & 1) ^ 1, fail))) break;
-      if (lane == 0) mbar_arrive_tx(&sh->v_full[st], bytes);
-      __syncwarp();
-      if (mine) tma_load_5d(dst + C::kVOff + st * C::kTileBytes, &p.tm_v, &sh->v_full[st], 0, y, cb, w.h, page);
-      ++v_n;
+    for (int s = 0; s < 2; ++s) {
+      w[s].init(R[s]);
+      part_from(p, s);
     }
   }
-  if (!ok) {  // let the copies already issued land before the CTA exits
-    for (uint32_t i = q_n > 2 ? q_n - 2 : 0; i < q_n; ++i) mbar_wait_drain(&sh->q_full[i & 1], (i >> 1) & 1);
-    for (uint32_t i = k_n > C::kStages ? k_n - C::kStages : 0; i < k_n; ++i)
-      mbar_wait_drain(&sh->k_full[i % C::kStages], (i / C::kStages) & 1);
-    for (uint32_t i = v_n > C::kStages ? v_n - C::kStages : 0; i < v_n; ++i)
-      mbar_wait_drain(&sh->v_full[i % C::kStages], (i / C::kStages) & 1);
+  __device__ __forceinline__ int tile(int s) const { return part[s].lo + i[s]; }
+  __device__ __forceinline__ void step(const CacheFwdParams& p, int s) {
+    if (++i[s] == part[s].n) {
+      w[s].advance();
+      part_from(p, s);
+    }
   }
+};
+
+// ------------------------------------------------------------- producer
+template <int D, bool PAIR>
+struct CwProducer {
+  using C = CwCfg<D, PAIR>;
+  const CacheFwdParams& p;
+  uint8_t* smem;
+  CwShared* sh;
+  Fail fail;
+  uint32_t q_n[2] = {0, 0};  // Q loads issued, by slot
+  uint32_t it = 0;           // tiles taken
+  uint32_t entries = 0;      // ring entries issued, or one more (the skipped one)
+  // the last tile, whose V is to come
+  struct {
+    int h, y, page;
+    uint32_t bytes;
+    bool mine;
+  } held;
+
+  // Rows of the tile from `token` on into a Q slot (whole warp).
+  __device__ __forceinline__ bool query(int slot, const CacheWalk& w, int token) {
+    if (!mbar_wait_warp(&sh->q_empty[slot], (q_n[slot] & 1) ^ 1, fail)) return false;
+    if ((threadIdx.x & 31) == 0) {
+      mbar_arrive_tx(&sh->q_full[slot], kTile / p.group * p.group * D * 2);
+#pragma unroll
+      for (int b = 0; b < C::kBlocks; ++b)
+        tma_load_3d(smem + C::kQOff + slot * C::kTileBytes + b * C::kBlockBytes, &p.tm_q, &sh->q_full[slot],
+                    b * C::kBlockCols, w.h * p.group, w.r.q0 + token);
+    }
+    __syncwarp();
+    ++q_n[slot];
+    return true;
+  }
+  // Lane: piece lane % 8 (min(page size, 128) tokens) of column block lane / 8.
+  __device__ __forceinline__ bool load(uint32_t entry, const CUtensorMap* map, bool mine, uint32_t bytes, int y, int h,
+                                       int page) {
+    const int lane = threadIdx.x & 31, piece = lane & 7, cb = lane >> 3, st = C::stage(entry);
+    if (!mbar_wait_warp(&sh->empty[st], C::parity(entry) ^ 1, fail)) return false;
+    if (lane == 0) mbar_arrive_tx(&sh->full[st], bytes);
+    __syncwarp();
+    if (mine)
+      tma_load_5d(smem_u32(smem) + C::kRingOff + st * C::kTileBytes + cb * C::kBlockBytes +
+                      piece * min(1 << p.page_shift, kTile) * C::kRowBytes,
+                  map, &sh->full[st], 0, y, cb, h, page);
+    entries = entry + 1;
+    return true;
+  }
+  // K of the next tile, then V of the tile before.
+  __device__ __forceinline__ bool tile(const CacheWalk& w, int t) {
+    const int lane = threadIdx.x & 31, piece = lane & 7;
+    const int pr = min(1 << p.page_shift, kTile), pieces = kTile / pr;  // pieces: 1, 2, 4 or 8
+    const int key = t * kTile + piece * pr, y = key & ((1 << p.page_shift) - 1);
+    const bool mine = (lane >> 3) < C::kBlocks && piece < pieces && key < w.r.L;
+    int page = p.num_pages;
+    if (mine) {
+      page = __ldg(p.table + static_cast<int64_t>(w.b) * p.width + (key >> p.page_shift));
+      if (static_cast<uint32_t>(page) >= static_cast<uint32_t>(p.num_pages)) {
+        atomicCAS(fail.status, kOk, kErrBadPage);
+        page = p.num_pages;  // outside the map: the copy writes zeros and reads nothing
+      }
+    }
+    const uint32_t bytes = min(pieces, (w.r.L - t * kTile + pr - 1) / pr) * pr * D * 2;
+    if (!load(C::entry_k(it), &p.tm_k, mine, bytes, y, w.h, page) || !value()) return false;
+    held = {w.h, y, page, bytes, mine};
+    ++it;
+    return true;
+  }
+  // V of the last tile taken, if any.
+  __device__ __forceinline__ bool value() {
+    return it == 0 || load(C::entry_v(it - 1), &p.tm_v, held.mine, held.bytes, held.y, held.h, held.page);
+  }
+  // After a failure: lets the copies already issued land before the CTA exits.
+  __device__ void drain() {
+    for (int s = 0; s < 2; ++s)
+      if (q_n[s]) mbar_wait_drain(&sh->q_full[s], (q_n[s] - 1) & 1);
+    for (uint32_t e = entries > C::kStages ? entries - C::kStages : 0; e < entries; ++e)
+      mbar_wait_drain(&sh->full[C::stage(e)], C::parity(e));
+  }
+};
+
+template <int D, bool PAIR>
+__device__ void cw_producer(const CacheFwdParams& p, uint8_t* smem, CwShared* sh, const CacheRange (&R)[2], Fail fail) {
+  CwProducer<D, PAIR> load{p, smem, sh, fail};
+  bool ok = true;
+  if constexpr (PAIR) {
+    uint32_t q_slot = 0;
+    CacheWalk w;
+    w.init(R[0]);
+    for (; ok && w.next<kTile>(p); w.advance()) {
+      const CwPart part(p, w);
+      if (part.n == 0) continue;
+      for (int s = 0; s < (part.pair ? 2 : 1) && ok; ++s, ++q_slot)
+        ok = load.query(q_slot & 1, w, part.first_token + s * (part.tile_rows / p.group));
+      for (int t = part.lo; t < part.lo + part.n && ok; ++t) ok = load.tile(w, t);
+    }
+  } else {
+    CwTurns turns(p, R);
+    while (ok && (turns.more[0] || turns.more[1])) {
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        if (!ok || !turns.more[s]) continue;
+        if (turns.i[s] == 0) ok = load.query(s, turns.w[s], turns.part[s].first_token);
+        if (ok) ok = load.tile(turns.w[s], turns.tile(s));
+        if (ok) turns.step(p, s);
+      }
+    }
+  }
+  if (!ok || !load.value()) load.drain();
 }
 
 // ------------------------------------------------------------- MMA issuer
 template <int D>
 __device__ __forceinline__ void cw_issue_qk(uint32_t t_s, uint32_t q_addr, uint32_t k_addr, bool leader) {
-  using C = CwCfg<D>;
+  using C = CwCfg<D, false>;  // (the layouts are the same)
   constexpr uint32_t idesc = idesc_bf16(kTile, kTile, 0, 0);
   const uint64_t a0 = sdesc(q_addr, 16, C::kSBO, C::kSwizzle), b0 = sdesc(k_addr, 16, C::kSBO, C::kSwizzle);
 #pragma unroll
@@ -188,7 +279,7 @@ __device__ __forceinline__ void cw_issue_qk(uint32_t t_s, uint32_t q_addr, uint3
 }
 template <int D>
 __device__ __forceinline__ void cw_issue_pv(uint32_t t_o, uint32_t t_p, uint32_t v_addr, bool accumulate, bool leader) {
-  using C = CwCfg<D>;
+  using C = CwCfg<D, false>;
   constexpr uint32_t idesc = idesc_bf16(kTile, D, 0, 1);  // V is MN-major
   const uint64_t b0 = sdesc(v_addr, C::kBlockBytes, C::kSBO, C::kSwizzle);
 #pragma unroll
@@ -202,70 +293,135 @@ __device__ __forceinline__ void cw_issue_pv(uint32_t t_o, uint32_t t_p, uint32_t
 // S_1 of its next.  A stream's S overwrites the columns of its P; it is issued
 // after the product that reads them, and MMAs execute in issue order.  For the
 // same reason a stream's S being complete says that its O is, too.
-template <int D>
-__device__ void cw_mma(const CacheFwdParams& p, uint8_t* smem, CwShared* sh, uint32_t tmem, const CacheRange& R,
+template <int D, bool PAIR>
+struct CwIssuer {
+  using C = CwCfg<D, PAIR>;
+  CwShared* sh;
+  uint32_t tmem, q_base, ring;
+  bool leader;
+  Fail fail;
+  uint32_t p_n[2] = {0, 0}, o_n[2] = {0, 0}, q_n[2] = {0, 0};
+  uint32_t asked = 0, fixed = 0;  // masked tiles
+
+  __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity) { return mbar_wait_warp(bar, parity, fail); }
+  __device__ __forceinline__ void commit(uint64_t* bar) {
+    if (leader) mma_commit(bar);
+  }
+  // S of stream s from a Q slot and the K of tile `it`; `masked`: has its V made safe meanwhile.
+  __device__ __forceinline__ bool issue_s(int s, int slot, uint32_t it, bool masked) {
+    const uint32_t e = C::entry_k(it);
+    if (!wait(&sh->full[C::stage(e)], C::parity(e))) return false;
+    tc_fence_after();
+    cw_issue_qk<D>(tmem + 128 * s, q_base + slot * C::kTileBytes, ring + C::stage(e) * C::kTileBytes, leader);
+    commit(&sh->s_full[s]);
+    if (masked) {
+      if (leader) mbar_arrive(&sh->fix_ask[asked & 1]);
+      ++asked;
+    }
+    return true;
+  }
+  // O of stream s from its P and the V of tile `it`.
+  __device__ __forceinline__ bool issue_o(int s, uint32_t it, bool first, bool masked) {
+    const uint32_t e = C::entry_v(it);
+    if (!wait(&sh->full[C::stage(e)], C::parity(e)) || !wait(&sh->p_full[s], p_n[s] & 1)) return false;
+    ++p_n[s];
+    if (masked) {
+      if (!wait(&sh->fixed[fixed & 1], (fixed >> 1) & 1)) return false;
+      ++fixed;
+    }
+    tc_fence_after();
+    cw_issue_pv<D>(tmem + 256 + 128 * s, tmem + 128 * s, ring + C::stage(e) * C::kTileBytes, !first, leader);
+    return true;
+  }
+  __device__ __forceinline__ void free_k(uint32_t it) { commit(&sh->empty[C::stage(C::entry_k(it))]); }
+  __device__ __forceinline__ void free_v(uint32_t it) { commit(&sh->empty[C::stage(C::entry_v(it))]); }
+};
+
+template <int D, bool PAIR>
+__device__ void cw_mma(const CacheFwdParams& p, uint8_t* smem, CwShared* sh, uint32_t tmem, const CacheRange (&R)[2],
                        Fail fail) {
-  using C = CwCfg<D>;
-  const uint32_t q_base = smem_u32(smem + C::kQOff), k_base = smem_u32(smem + C::kKOff),
-                 v_base = smem_u32(smem + C::kVOff);
-  const bool leader = elect_one();
-  uint32_t fixed = 0;  // bit st: parity of stage st's masked tiles so far
-  uint32_t q_n = 0, kv_n = 0, o_n = 0, p_n[2] = {0, 0};
+  using C = CwCfg<D, PAIR>;
+  CwIssuer<D, PAIR> mma{sh, tmem, smem_u32(smem + C::kQOff), smem_u32(smem + C::kRingOff), elect_one(), fail};
   bool ok = true;
-  CacheWalk w;
-  w.init(R);
-  for (; ok && w.next<kTile>(p); w.advance()) {
-    const CwPart part(p, w);
-    if (part.n == 0) continue;
-    const int far_depth = part.far_depth(p, w);
-    const uint32_t slot[2] = {q_n & 1, part.pair ? (q_n + 1) & 1 : q_n & 1};
-    for (int s = 0; s < (part.pair ? 2 : 1) && ok; ++s, ++q_n) ok = mbar_wait_warp(&sh->q_full[q_n & 1], (q_n >> 1) & 1, fail);
-    if (!ok) break;
-    // S of stream s's i-th tile; frees what no later product of the part reads
-    auto issue_s = [&](int s, int i) -> bool {
-      const uint32_t it = kv_n + part.at(s, i);
-      const int st = it % C::kStages;
-      if (!mbar_wait_warp(&sh->k_full[st], (it / C::kStages) & 1, fail)) return false;
-      tc_fence_after();
-      cw_issue_qk<D>(tmem + 128 * s, q_base + slot[s] * C::kTileBytes, k_base + st * C::kTileBytes, leader);
-      if (leader) {
-        mma_commit(&sh->s_full[s]);
-        if (!part.pair || s == 1) mma_commit(&sh->k_empty[st]);
-        if (part.pair ? i == part.n - 1 : part.at(s, i) == part.n - 1) mma_commit(&sh->q_empty[slot[s]]);
+  if constexpr (PAIR) {
+    uint32_t q_n = 0, it0 = 0;
+    CacheWalk w;
+    w.init(R[0]);
+    for (; ok && w.next<kTile>(p); w.advance()) {
+      const CwPart part(p, w);
+      if (part.n == 0) continue;
+      const uint32_t slot[2] = {q_n & 1, part.pair ? (q_n + 1) & 1 : q_n & 1};
+      for (int s = 0; s < (part.pair ? 2 : 1) && ok; ++s, ++q_n) ok = mma.wait(&sh->q_full[q_n & 1], (q_n >> 1) & 1);
+      // (a pair has a masked V made safe once)
+      auto masked = [&](int s, int t) { return (!part.pair || s == 0) && !part.plain(part.lo + t); };
+      // S of stream s's i-th tile; frees what no later product of the part reads
+      auto part_s = [&](int s, int i) -> bool {
+        const int t = part.at(s, i);
+        if (!mma.issue_s(s, slot[s], it0 + t, masked(s, t))) return false;
+        if (!part.pair || s == 1) mma.free_k(it0 + t);
+        if (t == part.n - 1) mma.commit(&sh->q_empty[slot[s]]);
+        return true;
+      };
+#pragma unroll
+      for (int s = 0; s < 2; ++s)
+        if (ok && part.count(s) > 0) ok = part_s(s, 0);
+      if (ok) ok = mma.wait(&sh->o_empty[0], (mma.o_n[0] & 1) ^ 1);  // the part before has read its O
+      ++mma.o_n[0];
+      for (int i = 0; i < part.count(0) && ok; ++i) {
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+          if (!ok || i >= part.count(s)) continue;
+          const int t = part.at(s, i);
+          if (!(ok = mma.issue_o(s, it0 + t, i == 0, masked(s, t)))) continue;
+          if (!part.pair || s == 1) mma.free_v(it0 + t);
+          if (i == part.count(s) - 1) mma.commit(&sh->o_full[s]);
+          if (i + 1 < part.count(s)) ok = part_s(s, i + 1);
+        }
       }
+      it0 += part.n;
+    }
+  } else {
+    // the tile of each stream whose S is issued and whose P V is not
+    struct {
+      bool any, first, last, masked;
+      uint32_t it;
+    } held[2] = {};
+    auto finish = [&](int s) -> bool {
+      if (!held[s].any) return true;
+      held[s].any = false;
+      if (held[s].first) {  // the part before has read its O
+        if (!mma.wait(&sh->o_empty[s], (mma.o_n[s] & 1) ^ 1)) return false;
+        ++mma.o_n[s];
+      }
+      if (!mma.issue_o(s, held[s].it, held[s].first, held[s].masked)) return false;
+      mma.free_v(held[s].it);
+      if (held[s].last) mma.commit(&sh->o_full[s]);
       return true;
     };
-    for (int s = 0; s < 2 && ok; ++s)
-      if (part.count[s] > 0) ok = issue_s(s, 0);
-    for (int i = 0; i < part.count[0] && ok; ++i) {
-      for (int s = 0; s < 2 && ok; ++s) {
-        if (i >= part.count[s]) continue;
-        const uint32_t it = kv_n + part.at(s, i);
-        const int st = it % C::kStages;
-        if (!(ok = mbar_wait_warp(&sh->v_full[st], (it / C::kStages) & 1, fail))) break;
-        if (i == 0 && s == 0) {  // the part before has read its O
-          if (!(ok = mbar_wait_warp(&sh->o_empty, (o_n & 1) ^ 1, fail))) break;
-          ++o_n;
+    uint32_t it = 0;
+    CwTurns turns(p, R);
+    while (ok && (turns.more[0] || turns.more[1])) {
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        // (a stream that is done must not hold a stage back, either)
+        if (!ok || !(ok = finish(s)) || !turns.more[s]) continue;
+        const CwPart& part = turns.part[s];
+        const bool first = turns.i[s] == 0, last = turns.i[s] == part.n - 1, masked = !part.plain(turns.tile(s));
+        if (first) {
+          if (!(ok = mma.wait(&sh->q_full[s], mma.q_n[s] & 1))) continue;
+          ++mma.q_n[s];
         }
-        if (!(ok = mbar_wait_warp(&sh->p_full[s], p_n[s] & 1, fail))) break;
-        ++p_n[s];
-        // V of a masked tile, once for both streams
-        if ((!part.pair || s == 0) && !part.plain(p, w, far_depth, (part.lo + part.at(s, i)) * kTile)) {
-          if (!(ok = mbar_wait_warp(&sh->v_fixed[st], (fixed >> st) & 1, fail))) break;
-          fixed ^= 1u << st;
-        }
-        tc_fence_after();
-        cw_issue_pv<D>(tmem + 256 + 128 * s, tmem + 128 * s, v_base + st * C::kTileBytes, i > 0, leader);
-        if (leader) {
-          if (!part.pair || s == 1) mma_commit(&sh->v_empty[st]);
-          if (i == part.count[s] - 1) mma_commit(&sh->o_full[s]);
-        }
-        if (i + 1 < part.count[s]) ok = issue_s(s, i + 1);
+        if (!(ok = mma.issue_s(s, s, it, masked))) continue;
+        mma.free_k(it);
+        if (last) mma.commit(&sh->q_empty[s]);
+        held[s] = {true, first, last, masked, it};
+        ++it;
+        turns.step(p, s);
       }
     }
-    kv_n += part.n;
+    if (ok && finish(0)) finish(1);
   }
-  if (leader) mma_commit(&sh->drain);
+  mma.commit(&sh->drain);
   mbar_wait_drain(&sh->drain, 0);
 }
 
@@ -409,12 +565,12 @@ __device__ __forceinline__ void cw_softmax_tile(uint32_t t_s, uint32_t t_o, floa
 // row's result (bf16 `out` or fp32 `part`), which this thread has written.
 // Rare, so it works from global memory.
 template <int D, int ACT>
-__device__ __noinline__ void cw_add_odd(const CacheFwdParams& p, CacheWalk w, CwPart part, CcRow q, int far_depth,
-                                        int c0, int n, __nv_bfloat16* out, float* part_o) {
+__device__ __noinline__ void cw_add_odd(const CacheFwdParams& p, CacheWalk w, CwPart part, CcRow q, int c0,
+                                        int n, __nv_bfloat16* out, float* part_o) {
   const CacheReq& r = w.r;
   const int32_t* pages = p.table + static_cast<int64_t>(w.b) * p.width;
   for (int t = part.lo; t < part.lo + part.n; ++t) {
-    if (part.plain(p, w, far_depth, t * kTile)) continue;
+    if (part.plain(t)) continue;
     for (int key = t * kTile; key < min(r.L, (t + 1) * kTile); ++key) {
       const int page = __ldg(pages + (key >> p.page_shift));
       if (static_cast<uint32_t>(page) >= static_cast<uint32_t>(p.num_pages)) continue;
@@ -449,71 +605,82 @@ __device__ __noinline__ void cw_add_odd(const CacheFwdParams& p, CacheWalk w, Cw
 // NaN, so V rows past the request's end (the page or an earlier tile may have
 // left anything there) are zeroed, and infinities and NaN of the others taken
 // out; the epilogue adds those to the rows that see them.
-template <int D>
-__device__ void cw_fixer(const CacheFwdParams& p, uint8_t* smem, CwShared* sh, const CacheRange& R, Fail fail) {
-  using C = CwCfg<D>;
+template <int D, bool PAIR>
+__device__ void cw_fixer(const CacheFwdParams& p, uint8_t* smem, CwShared* sh, const CacheRange (&R)[2], Fail fail) {
+  using C = CwCfg<D, PAIR>;
   constexpr int kPieces = C::kBlockCols / 8;
   const int lane = threadIdx.x & 31;
-  const uint32_t v_base = smem_u32(smem + C::kVOff);
-  uint32_t kv_n = 0;
-  int number = 0;
-  CacheWalk w;
-  w.init(R);
-  for (; w.next<kTile>(p); w.advance()) {
-    const CwPart part(p, w);
-    if (part.n == 0) continue;
-    ++number;
-    const int far_depth = part.far_depth(p, w);
-    for (int i = 0; i < part.n; ++i) {
-      // (every tile is waited for and released, so that no round of a stage
-      // is mistaken for another)
-      const int key0 = (part.lo + i) * kTile;
-      const uint32_t it = kv_n + i;
-      const int st = it % C::kStages;
-      if (!mbar_wait_warp(&sh->v_full[st], (it / C::kStages) & 1, fail)) return;
-      if (part.plain(p, w, far_depth, key0)) {
-        mbar_arrive_warp(&sh->v_empty[st]);
+  const uint32_t ring = smem_u32(smem + C::kRingOff);
+  uint32_t it = 0, asked = 0;
+  int number[2] = {0, 0};
+  auto tile = [&](int s, const CacheWalk& w, const CwPart& part, int t) -> bool {
+    const uint32_t e = C::entry_v(it);
+    const int st = C::stage(e), key0 = t * kTile;
+    ++it;
+    if (part.plain(t)) return true;
+    // (once its S is issued, the stage's round before this V is over)
+    if (!mbar_wait_warp(&sh->fix_ask[asked & 1], (asked >> 1) & 1, fail)) return false;
+    if (!mbar_wait_warp(&sh->full[st], C::parity(e), fail)) return false;
+    for (int row = threadIdx.x & 63; row < kTile; row += 64) {
+      const bool past = key0 + row >= w.r.L;
+      const uint32_t vr = ring + st * C::kTileBytes + row * C::kRowBytes;
+      // (pieces in any order, whatever the swizzle: from the lane's on, so
+      // that the lanes, a row apart, meet different banks)
+      auto piece = [&](int c) {
+        return vr + (c / kPieces) * C::kBlockBytes + ((c + lane * kPieces / 8) % kPieces) * 16;
+      };
+      if (past) {
+#pragma unroll
+        for (int c = 0; c < D / 8; ++c) st_shared_v4(piece(c), 0u, 0u, 0u, 0u);
         continue;
       }
-      for (int row = threadIdx.x & 63; row < kTile; row += 64) {
-        const bool past = key0 + row >= w.r.L;
-        const uint32_t vr = v_base + st * C::kTileBytes + row * C::kRowBytes;
-        // (pieces in any order, whatever the swizzle: from the lane's on, so
-        // that the lanes, a row apart, meet different banks)
-        auto piece = [&](int c) {
-          return vr + (c / kPieces) * C::kBlockBytes + ((c + lane * kPieces / 8) % kPieces) * 16;
-        };
-        if (past) {
+      // 0 * x summed over the row is NaN when one of its values is not finite
+      const __nv_bfloat162 zero = __float2bfloat162_rn(0.f);
+      __nv_bfloat162 sum = zero;
 #pragma unroll
-          for (int c = 0; c < D / 8; ++c) st_shared_v4(piece(c), 0u, 0u, 0u, 0u);
-          continue;
-        }
-        // 0 * x summed over the row is NaN when one of its values is not finite
-        const __nv_bfloat162 zero = __float2bfloat162_rn(0.f);
-        __nv_bfloat162 sum = zero;
+      for (int c = 0; c < D / 8; ++c) {
+        uint32_t x[4];
+        ld_shared_v4(piece(c), x[0], x[1], x[2], x[3]);
 #pragma unroll
-        for (int c = 0; c < D / 8; ++c) {
-          uint32_t x[4];
-          ld_shared_v4(piece(c), x[0], x[1], x[2], x[3]);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) sum = __hfma2(*reinterpret_cast<__nv_bfloat162*>(&x[e]), zero, sum);
-        }
-        if (__low2float(sum) == 0.f && __high2float(sum) == 0.f) continue;
-        *const_cast<volatile int*>(&sh->odd[number & 15]) = number;
-#pragma unroll 1
-        for (int c = 0; c < D / 8; ++c) {
-          uint32_t x[4];
-          ld_shared_v4(piece(c), x[0], x[1], x[2], x[3]);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) x[e] &= ~cc_nonfinite(x[e]);
-          st_shared_v4(piece(c), x[0], x[1], x[2], x[3]);
-        }
+        for (int e = 0; e < 4; ++e) sum = __hfma2(*reinterpret_cast<__nv_bfloat162*>(&x[e]), zero, sum);
       }
-      fence_proxy_async_smem();
-      mbar_arrive_warp(&sh->v_fixed[st]);
-      mbar_arrive_warp(&sh->v_empty[st]);
+      if (__low2float(sum) == 0.f && __high2float(sum) == 0.f) continue;
+      *const_cast<volatile int*>(&sh->odd[s][number[s] & 15]) = number[s];
+#pragma unroll 1
+      for (int c = 0; c < D / 8; ++c) {
+        uint32_t x[4];
+        ld_shared_v4(piece(c), x[0], x[1], x[2], x[3]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[e] &= ~cc_nonfinite(x[e]);
+        st_shared_v4(piece(c), x[0], x[1], x[2], x[3]);
+      }
     }
-    kv_n += part.n;
+    fence_proxy_async_smem();
+    mbar_arrive_warp(&sh->fixed[asked & 1]);
+    ++asked;
+    return true;
+  };
+  if constexpr (PAIR) {
+    CacheWalk w;
+    w.init(R[0]);
+    for (; w.next<kTile>(p); w.advance()) {
+      const CwPart part(p, w);
+      if (part.n == 0) continue;
+      ++number[0];
+      for (int t = part.lo; t < part.lo + part.n; ++t)
+        if (!tile(0, w, part, t)) return;
+    }
+  } else {
+    CwTurns turns(p, R);
+    while (turns.more[0] || turns.more[1]) {
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        if (!turns.more[s]) continue;
+        if (turns.i[s] == 0) ++number[s];
+        if (!tile(s, turns.w[s], turns.part[s], turns.tile(s))) return;
+        turns.step(p, s);
+      }
+    }
   }
 }
 
@@ -538,8 +705,8 @@ __device__ __forceinline__ void cw_store16(const uint32_t (&x)[16], float inv, _
   }
 }
 
-template <int D, int ACT>
-__device__ void cw_consumer(const CacheFwdParams& p, CwShared* sh, uint32_t tmem, int stream, const CacheRange& R,
+template <int D, int ACT, bool PAIR>
+__device__ void cw_consumer(const CacheFwdParams& p, CwShared* sh, uint32_t tmem, int stream, const CacheRange R,
                             Fail fail) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int row = (warp & 3) * 32 + lane;
@@ -555,12 +722,13 @@ __device__ void cw_consumer(const CacheFwdParams& p, CwShared* sh, uint32_t tmem
   for (; w.next<kTile>(p); w.advance()) {
     const CwPart part(p, w);
     const CacheReq& r = w.r;
-    if (part.n > 0) ++number;  // (the V ring lets no more than 8 later parts be loaded, let alone checked)
+    if (part.n > 0) ++number;  // (the ring lets no more than 8 later parts be loaded, let alone checked)
     __syncwarp();
     const int block_row0 = w.row_tile * p.rows_per_tile;
-    const int my_rows = part.pair ? (stream == 0 ? part.tile_rows : part.rows - part.tile_rows) : part.rows;
+    const bool pair = PAIR && part.pair;
+    const int my_rows = pair ? (stream == 0 ? part.tile_rows : part.rows - part.tile_rows) : part.rows;
     const bool row_ok = row < my_rows;
-    const int flat = block_row0 + (part.pair ? stream * part.tile_rows : 0) + row;
+    const int flat = block_row0 + (pair ? stream * part.tile_rows : 0) + row;
     CcRow q;
     q.t = row_ok ? flat / p.group : -1;
     q.head = w.h * p.group + (row_ok ? flat % p.group : 0);
@@ -568,31 +736,29 @@ __device__ void cw_consumer(const CacheFwdParams& p, CwShared* sh, uint32_t tmem
     q.far_bias = 0.f;
     if (row_ok && p.bias_len)
       q.far_bias = __ldg(p.bias + static_cast<int64_t>(q.head) * p.bias_len + 2 * reach) * cc_bias_unit<ACT>();
-    const int far_depth = part.far_depth(p, w);
     const bool warp_live = (warp & 3) * 32 < my_rows;
+    const int count = PAIR ? part.count(stream) : part.n;
     float m = -INFINITY, l = 0.f;
-    for (int i = 0; i < part.count[stream]; ++i) {
-      const int key0 = (part.lo + part.at(stream, i)) * kTile;
+    for (int i = 0; i < count; ++i) {
+      const int tile = part.lo + (PAIR ? part.at(stream, i) : i);
       if (!dead && !mbar_wait(&sh->s_full[stream], s_n & 1, fail)) dead = true;
       dead = __any_sync(0xffffffffu, dead);
       ++s_n;
       if (dead) continue;
       tc_fence_after();
       if (warp_live) {
-        const bool plain = part.plain(p, w, far_depth, key0);
-        const bool far = p.bias_len == 0 || (key0 + kTile - 1 < r.C && r.C - (key0 + kTile - 1) >= reach);
         float scale = p.scale, bias = q.far_bias;
-        if (!far) {
-          cw_bias_tile<ACT>(p, r, q, reach, key0, t_s);
+        if (tile >= part.far_hi) {
+          cw_bias_tile<ACT>(p, r, q, reach, tile * kTile, t_s);
           scale = 1.f;
           bias = 0.f;
         }
         uint32_t see[4] = {0u, 0u, 0u, 0u};
-        if (plain) {
+        if (part.plain(tile)) {
           if constexpr (ACT == 2) cw_softmax_tile<D, false>(t_s, t_o + 128 * stream, scale, bias, see, i == 0, m, l);
           else cw_act_tile<ACT, false>(t_s, scale, bias, see);
         } else {
-          cw_visible(p, r, q, key0, see);
+          cw_visible(p, r, q, tile * kTile, see);
           if constexpr (ACT == 2) cw_softmax_tile<D, true>(t_s, t_o + 128 * stream, scale, bias, see, i == 0, m, l);
           else cw_act_tile<ACT, true>(t_s, scale, bias, see);
         }
@@ -603,43 +769,43 @@ __device__ void cw_consumer(const CacheFwdParams& p, CwShared* sh, uint32_t tmem
     }
 
     // the part's end
-    int o_col = 0;              // first column this warpgroup writes
-    float f[2] = {1.f, 1.f};    // factors of the streams' O
-    bool use[2] = {false, false};
-    if (part.n > 0) {
-      use[0] = !part.pair || stream == 0;
-      use[1] = part.pair ? stream == 1 : part.count[1] > 0;
-      if (!part.pair) {  // both streams' rows are the same: each warpgroup joins and writes half the columns
-        o_col = stream * (D / 2);
-        if constexpr (ACT == 2) {
-          sh->ml[ml_at][stream][row] = make_float2(m, l);
-          named_bar(1, 256);
-          const float2 other = sh->ml[ml_at][stream ^ 1][row];
-          ml_at ^= 1;
-          const float top = fmaxf(m, other.x), ref = top == -INFINITY ? 0.f : top;
-          f[stream] = ex2_sfu(m - ref);
-          f[stream ^ 1] = ex2_sfu(other.x - ref);
-          // (in stream order, so that both warpgroups get the same bits)
-          const float l0 = stream == 0 ? l : other.y, l1 = stream == 0 ? other.y : l;
-          l = __fmaf_rn(l0, f[0], l1 * f[1]);
-          m = top;
-        }
+    const bool share = PAIR && !part.pair && part.n > 0;  // both streams hold parts of the same rows
+    int o_col = 0;            // first column this warpgroup writes
+    float f[2] = {1.f, 1.f};  // factors of the streams' O
+    bool use[2] = {stream == 0 && part.n > 0, stream == 1 && part.n > 0};
+    if (share) {  // each warpgroup joins and writes half the columns
+      use[0] = true;
+      use[1] = part.count(1) > 0;
+      o_col = stream * (D / 2);
+      if constexpr (ACT == 2) {
+        float2* ml = sh->ml + ml_at * 2 * kTile;
+        ml[stream * kTile + row] = make_float2(m, l);
+        named_bar(1, 256);
+        const float2 other = ml[(stream ^ 1) * kTile + row];
+        ml_at ^= 1;
+        const float top = fmaxf(m, other.x), ref = top == -INFINITY ? 0.f : top;
+        f[stream] = ex2_sfu(m - ref);
+        f[stream ^ 1] = ex2_sfu(other.x - ref);
+        // (in stream order, so that both warpgroups get the same bits)
+        const float l0 = stream == 0 ? l : other.y, l1 = stream == 0 ? other.y : l;
+        l = __fmaf_rn(l0, f[0], l1 * f[1]);
+        m = top;
       }
-      for (int s = 0; s < 2; ++s) {
-        if (part.count[s] == 0) continue;
-        if (use[s] && !dead && !mbar_wait(&sh->o_full[s], o_n[s] & 1, fail)) dead = true;
-        ++o_n[s];
-      }
-      dead = __any_sync(0xffffffffu, dead);
     }
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      if (use[s] && !dead && !mbar_wait(&sh->o_full[s], o_n[s] & 1, fail)) dead = true;
+      if (PAIR ? part.count(s) > 0 && part.n > 0 : use[s]) ++o_n[s];
+    }
+    dead = __any_sync(0xffffffffu, dead);
     // O leaves tensor memory at once (all columns of one stream, or half the
     // columns of both), so that the next part's products may start
     uint32_t x[D / 16][16];
     tc_fence_after();
 #pragma unroll
     for (int k = 0; k < D / 16; ++k) {
-      const int s = part.pair ? stream : (k >= D / 32 ? 1 : 0);
-      const int col = part.pair ? 16 * k : o_col + 16 * (k % (D / 32));
+      const int s = share ? (k >= D / 32 ? 1 : 0) : stream;
+      const int col = share ? o_col + 16 * (k % (D / 32)) : 16 * k;
       if (!dead && use[s]) {
         tmem_ld16(t_o + 128 * s + col, x[k]);
       } else {
@@ -649,19 +815,19 @@ __device__ void cw_consumer(const CacheFwdParams& p, CwShared* sh, uint32_t tmem
     }
 #pragma unroll
     for (int k = 0; k < D / 16; ++k) tmem_ld_wait16(x[k]);
-    const bool odd = part.n > 0 && *const_cast<volatile int*>(&sh->odd[number & 15]) == number;
+    const bool odd = part.n > 0 && *const_cast<volatile int*>(&sh->odd[PAIR ? 0 : stream][number & 15]) == number;
     if (part.n > 0) {
       tc_fence_before();
-      mbar_arrive_warp(&sh->o_empty);
+      mbar_arrive_warp(&sh->o_empty[PAIR ? 0 : stream]);
     }
     if (!row_ok || dead) continue;
     const float inv = ACT != 2 || !w.whole ? 1.f : (l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l));
     const int64_t token = r.q0 + q.t;
-    const int64_t prow = (2 * static_cast<int64_t>(blockIdx.x) + (w.first ? 0 : 1)) * p.rows_per_tile + (flat - block_row0);
+    const int64_t prow = (2 * static_cast<int64_t>(R.index) + (w.first ? 0 : 1)) * p.rows_per_tile + (flat - block_row0);
     __nv_bfloat16* out = w.whole ? p.out + (token * p.heads + q.head) * D : nullptr;
     float* part_o = p.part_o + prow * D;
-    // (the columns of a part without tiles are written by both warpgroups, as zeros)
-    if (part.pair || part.n == 0) {
+    // (a part without tiles leaves zeros; where the streams share it, both write them)
+    if (!share) {
 #pragma unroll
       for (int k = 0; k < D / 16; ++k) cw_store16(x[k], inv, out, part_o, 16 * k);
     } else {
@@ -673,7 +839,7 @@ __device__ void cw_consumer(const CacheFwdParams& p, CwShared* sh, uint32_t tmem
         cw_store16(x[k], inv, out, part_o, o_col + 16 * k);
       }
     }
-    if (odd) cw_add_odd<D, ACT>(p, w, part, q, far_depth, o_col, part.pair ? D : D / 2, out, part_o);
+    if (odd) cw_add_odd<D, ACT>(p, w, part, q, o_col, share ? D / 2 : D, out, part_o);
     if (ACT == 2 && o_col == 0) {
       if (!w.whole) p.part_ml[prow] = make_float2(m, l);
       else if (p.lse != nullptr)
@@ -682,9 +848,9 @@ __device__ void cw_consumer(const CacheFwdParams& p, CwShared* sh, uint32_t tmem
   }
 }
 
-template <int D, int ACT>
+template <int D, int ACT, bool PAIR>
 __global__ void __launch_bounds__(kWideThreads, 1) cache_fwd_wide_kernel(const __grid_constant__ CacheFwdParams p) {
-  using C = CwCfg<D>;
+  using C = CwCfg<D, PAIR>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   CwShared* sh = reinterpret_cast<CwShared*>(smem + C::kBarOff);
@@ -697,36 +863,47 @@ __global__ void __launch_bounds__(kWideThreads, 1) cache_fwd_wide_kernel(const _
       mbar_init(&sh->s_full[s], 1);
       mbar_init(&sh->p_full[s], 4);
       mbar_init(&sh->o_full[s], 1);
+      mbar_init(&sh->o_empty[s], PAIR ? 8 : 4);
+    }
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&sh->fix_ask[s], 1);
+      mbar_init(&sh->fixed[s], 2);
     }
     for (int s = 0; s < C::kStages; ++s) {
-      mbar_init(&sh->k_full[s], 1);
-      mbar_init(&sh->k_empty[s], 1);
-      mbar_init(&sh->v_full[s], 1);
-      mbar_init(&sh->v_empty[s], 3);  // the last product that reads it, and the two fixing warps
-      mbar_init(&sh->v_fixed[s], 2);
+      mbar_init(&sh->full[s], 1);
+      mbar_init(&sh->empty[s], 1);
     }
-    mbar_init(&sh->o_empty, 8);
     mbar_init(&sh->drain, 1);
     sh->abort = 0;
     p.err[blockIdx.x] = kOk;
-    for (int i = 0; i < 16; ++i) sh->odd[i] = 0;
+    for (int i = 0; i < 32; ++i) sh->odd[i >> 4][i & 15] = 0;
     fence_mbar_init();
   }
   if (warp == 1) {
     tmem_alloc(&sh->tmem_base, 512);
     tmem_relinquish();
   }
-  const CacheRange R = cache_range<kTile>(p, &sh->range, kWideMinRange);
+  CacheRange R[2];
+  if constexpr (PAIR) {
+    CacheRange one[1];
+    cache_ranges<kTile>(p, sh->range, kWideMinRange, one);
+    R[0] = R[1] = one[0];
+  } else {
+    cache_ranges<kTile>(p, sh->range, kWideMinRange, R);
+  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (threadIdx.x == 96) cache_open<kTile>(p, R);
+  if (threadIdx.x == 96) {
+    cache_open<kTile>(p, R[0]);
+    if constexpr (!PAIR) cache_open<kTile>(p, R[1]);
+  }
   const uint32_t tmem = sh->tmem_base;
   Fail fail{&sh->abort, p.err + blockIdx.x, p.wait_limit_ns};
-  if (warp == 0) cw_producer<D>(p, smem, sh, R, fail);
-  else if (warp == 1) cw_mma<D>(p, smem, sh, tmem, R, fail);
-  else if (warp >= 4) cw_consumer<D, ACT>(p, sh, tmem, (warp - 4) >> 2, R, fail);
-  else cw_fixer<D>(p, smem, sh, R, fail);
+  if (warp == 0) cw_producer<D, PAIR>(p, smem, sh, R, fail);
+  else if (warp == 1) cw_mma<D, PAIR>(p, smem, sh, tmem, R, fail);
+  else if (warp < 4) cw_fixer<D, PAIR>(p, smem, sh, R, fail);
+  else cw_consumer<D, ACT, PAIR>(p, sh, tmem, (warp - 4) >> 2, warp < 8 ? R[0] : R[1], fail);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -738,10 +915,10 @@ __global__ void __launch_bounds__(kWideThreads, 1) cache_fwd_wide_kernel(const _
 #error "compile cache_fwd_wide.cu with -DJGDPA_HEAD_DIM=32, 64 or 128"
 #endif
 
-template <int D, int ACT>
+template <int D, int ACT, bool PAIR>
 static cudaError_t launch_cw(const CacheFwdParams& p, int grid, cudaStream_t stream) {
-  auto kern = cache_fwd_wide_kernel<D, ACT>;
-  constexpr int kSmem = CwCfg<D>::kSmemBytes;
+  auto kern = cache_fwd_wide_kernel<D, ACT, PAIR>;
+  constexpr int kSmem = CwCfg<D, PAIR>::kSmemBytes;
   static DeviceFlags attr_set = {};
   cudaError_t e = smem_attr_once(kern, kSmem, attr_set);
   if (e != cudaSuccess) return e;
@@ -749,12 +926,13 @@ static cudaError_t launch_cw(const CacheFwdParams& p, int grid, cudaStream_t str
   return cudaGetLastError();
 }
 
+// pairs: items of two 128-row tiles (the streams share their parts).
 template <int D>
-cudaError_t launch_cache_fwd_wide_d(const CacheFwdParams& p, int act, int grid, cudaStream_t stream) {
-  if (act == 0) return launch_cw<D, 0>(p, grid, stream);
-  if (act == 1) return launch_cw<D, 1>(p, grid, stream);
-  return launch_cw<D, 2>(p, grid, stream);
+cudaError_t launch_cache_fwd_wide_d(const CacheFwdParams& p, int act, bool pairs, int grid, cudaStream_t stream) {
+  if (act == 0) return pairs ? launch_cw<D, 0, true>(p, grid, stream) : launch_cw<D, 0, false>(p, grid, stream);
+  if (act == 1) return pairs ? launch_cw<D, 1, true>(p, grid, stream) : launch_cw<D, 1, false>(p, grid, stream);
+  return pairs ? launch_cw<D, 2, true>(p, grid, stream) : launch_cw<D, 2, false>(p, grid, stream);
 }
-template cudaError_t launch_cache_fwd_wide_d<JGDPA_HEAD_DIM>(const CacheFwdParams&, int, int, cudaStream_t);
+template cudaError_t launch_cache_fwd_wide_d<JGDPA_HEAD_DIM>(const CacheFwdParams&, int, bool, int, cudaStream_t);
 
 }  // namespace jg
