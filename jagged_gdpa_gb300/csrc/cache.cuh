@@ -130,12 +130,11 @@ __device__ __forceinline__ bool cache_req_ok(const CacheFwdParams& p, const Cach
 // tiles and a lead of item_cost tiles' length, what its start and end take
 // beside them; laid end to end (request by request, row tiles of one head next
 // to each other so that they meet in L2) they form one line that is cut into
-// equal ranges, one or two per CTA, whatever the lengths.  (Without the lead, ranges
+// equal ranges, one per CTA, whatever the lengths.  (Without the lead, ranges
 // that fall on many short requests took half as long again as the others.)  An
 // item cut by a range border is finished by the joining kernel.
 struct CacheRange {
-  int64_t total, per, begin, end;
-  int index;    // of the range
+  int64_t per, begin, end;
   int b;        // request that `begin` lies in
   int64_t rem;  // begin minus the request's start
   bool ok;
@@ -146,10 +145,15 @@ struct CacheRangeShared {
   int b;
 };
 
-// This CTA's N ranges (of N gridDim.x).  Run by every thread of the CTA (a whole
-// number of warps, at most 512); ends in a barrier.
-template <int KT, int N>
-__device__ void cache_ranges(const CacheFwdParams& p, CacheRangeShared* sh, int min_range, CacheRange (&R)[N]) {
+// a / b for a >= 0: the 64-bit division, some 100 instructions, only where it is needed.
+__device__ __forceinline__ int64_t cache_div(int64_t a, int b) {
+  return a <= 0xFFFFFFFFll ? static_cast<int64_t>(static_cast<uint32_t>(a) / static_cast<uint32_t>(b)) : a / b;
+}
+
+// This CTA's range.  Run by every thread of the CTA (a whole number of warps, at
+// most 512); ends in a barrier.
+template <int KT>
+__device__ CacheRange cache_range(const CacheFwdParams& p, CacheRangeShared* sh, int min_range) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nt = blockDim.x, nw = nt >> 5;
   const int each = (p.batch + nt - 1) / nt;
   const int b0 = min(tid * each, p.batch), b1 = min(b0 + each, p.batch);
@@ -167,47 +171,35 @@ __device__ void cache_ranges(const CacheFwdParams& p, CacheRangeShared* sh, int 
     const int64_t v = __shfl_up_sync(0xffffffffu, incl, o);
     if (lane >= o) incl += v;
   }
-  if (lane == 31) sh[0].warp_sum[warp] = incl;
+  if (lane == 31) sh->warp_sum[warp] = incl;
   const bool all_ok = __syncthreads_and(ok) != 0;
   int64_t base = 0, total = 0;
   for (int w = 0; w < nw; ++w) {
-    const int64_t v = sh[0].warp_sum[w];
+    const int64_t v = sh->warp_sum[w];
     if (w < warp) base += v;
     total += v;
   }
-  const int64_t g = static_cast<int64_t>(gridDim.x) * N;
-  const int64_t per = max((total + g - 1) / g, static_cast<int64_t>(min_range));
-#pragma unroll
-  for (int s = 0; s < N; ++s) {
-    R[s].ok = all_ok;
-    R[s].total = total;
-    R[s].per = per;
-    R[s].index = N * blockIdx.x + s;
-    R[s].begin = min(per * R[s].index, total);
-    R[s].end = min(R[s].begin + per, total);
-    int64_t at = base + incl - sum;
-    if (all_ok && R[s].begin < total && at <= R[s].begin && R[s].begin < at + sum) {
-      int b = b0;
-      for (;; ++b) {
-        const int64_t c = cache_cost(p, cache_req<KT>(p, b));
-        if (R[s].begin < at + c) break;
-        at += c;
-      }
-      sh[s].b = b;
-      sh[s].rem = R[s].begin - at;
+  CacheRange R;
+  R.ok = all_ok;
+  const int g = gridDim.x;
+  R.per = max(cache_div(total + g - 1, g), static_cast<int64_t>(min_range));
+  R.begin = min(R.per * blockIdx.x, total);
+  R.end = min(R.begin + R.per, total);
+  int64_t at = base + incl - sum;
+  if (all_ok && R.begin < total && at <= R.begin && R.begin < at + sum) {
+    int b = b0;
+    for (;; ++b) {
+      const int64_t c = cache_cost(p, cache_req<KT>(p, b));
+      if (R.begin < at + c) break;
+      at += c;
     }
+    sh->b = b;
+    sh->rem = R.begin - at;
   }
   __syncthreads();
-#pragma unroll
-  for (int s = 0; s < N; ++s) {
-    R[s].b = sh[s].b;
-    R[s].rem = sh[s].rem;
-  }
-}
-
-// a / b for a >= 0: the 64-bit division, some 100 instructions, only where it is needed.
-__device__ __forceinline__ int64_t cache_div(int64_t a, int b) {
-  return a <= 0xFFFFFFFFll ? static_cast<int64_t>(static_cast<uint32_t>(a) / static_cast<uint32_t>(b)) : a / b;
+  R.b = sh->b;
+  R.rem = sh->rem;
+  return R;
 }
 
 // Walks the parts of items in a CTA's range, in order; every role of the CTA
@@ -271,11 +263,16 @@ struct CacheWalk {
   }
 };
 
+// The range that a place on the line lies in.
+__device__ __forceinline__ int64_t cache_range_of(int64_t at, int64_t per) {
+  return (at | per) <= 0xFFFFFFFFll ? static_cast<uint32_t>(at) / static_cast<uint32_t>(per) : at / per;
+}
+
 // Writes a range's join record (one thread).
 template <int KT>
 __device__ __forceinline__ void cache_open(const CacheFwdParams& p, const CacheRange& R) {
-  const int c = R.index;
-  if (!R.ok) p.err[blockIdx.x] = kErrBadOffsets;
+  const int c = blockIdx.x;
+  if (!R.ok) p.err[c] = kErrBadOffsets;
   CacheJoin j{};
   if (R.ok && R.begin < R.end) {
     const CacheReq r = cache_req<KT>(p, R.b);
@@ -288,8 +285,8 @@ __device__ __forceinline__ void cache_open(const CacheFwdParams& p, const CacheR
     j.h = static_cast<int>(cache_div(item, r.rt));
     j.rt = static_cast<int>(item - static_cast<int64_t>(j.h) * r.rt);
     // tiles in several ranges, and this is the second of them
-    const int64_t c0 = (j.t0 + p.item_cost) / R.per;
-    j.valid = c0 + 1 == c && (j.t1 - 1) / R.per > c0;
+    const int64_t c0 = cache_range_of(j.t0 + p.item_cost, R.per);
+    j.valid = c0 + 1 == c && cache_range_of(j.t1 - 1, R.per) > c0;
   }
   p.join[c] = j;
 }

@@ -19,8 +19,7 @@ cudaError_t launch_cache_fwd_d(const CacheFwdParams& p, int act, int grid, cudaS
 template <int D>
 cudaError_t launch_cache_fwd_wide_d(const CacheFwdParams& p, int act, bool pairs, int grid, cudaStream_t stream);
 template <int D>
-cudaError_t launch_cache_join_d(const CacheFwdParams& p, int act, int n_ctas, int n_ranges, int item_rows,
-                                cudaStream_t stream);
+cudaError_t launch_cache_join_d(const CacheFwdParams& p, int act, int n_ctas, int item_rows, cudaStream_t stream);
 cudaError_t launch_cache_plan(const CachePlanParams& p, int sms, cudaStream_t stream);
 cudaError_t launch_cache_append(const CacheAppendParams& p, cudaStream_t stream);
 }  // namespace jg
@@ -57,7 +56,6 @@ struct CacheLayout {
   size_t err, join, part_ml, part_o, total;
   int rows, grid;  // query rows of one item per key/value head, CTAs
   int heads;       // key/value heads of one item
-  int ranges;      // of the work division
   bool wide;       // 128-row tiles through tensor memory
   bool pairs;      // of them, two at a time
 };
@@ -70,25 +68,23 @@ bool cache_layout(int32_t heads, int32_t kv_heads, int32_t head_dim, int32_t max
   L->wide = max_rows > 32 && group <= jg::kTile;
   if (L->wide) {
     const int tile = jg::kTile / group * group;
-    static const char* ev = getenv("JG_PAIR");
-    L->pairs = max_rows > (ev ? atoi(ev) : 1) * tile;
+    L->pairs = max_rows > tile;
     L->rows = L->pairs ? 2 * tile : tile;
     L->grid = sms;
-    L->ranges = L->pairs ? sms : 2 * sms;
     L->heads = 1;
   } else {
     // small heads side by side; measured at d = 32, 16 heads, 8 tokens: see the kernel
     L->heads = kv_heads % (128 / head_dim) == 0 ? 128 / head_dim : 1;
     L->rows = max_rows <= 16 ? 16 : 32;
     L->pairs = false;
-    L->grid = L->ranges = sms * jg::cache_ctas(head_dim * L->heads, L->rows / 16);
+    L->grid = sms * jg::cache_ctas(head_dim * L->heads, L->rows / 16);
   }
-  const size_t parts = 2 * static_cast<size_t>(L->ranges) * L->rows * L->heads;
+  const size_t parts = 2 * static_cast<size_t>(L->grid) * L->rows * L->heads;
   size_t off = kAlign;  // the status word
   L->err = off;
   off += up(L->grid * sizeof(int));
   L->join = off;
-  off += up(L->ranges * sizeof(jg::CacheJoin));
+  off += up(L->grid * sizeof(jg::CacheJoin));
   L->part_ml = off;
   off += up(parts * sizeof(float2));
   L->part_o = off;
@@ -321,8 +317,7 @@ jgdpa_status jgdpa_cache_fwd(const void* q, int64_t q_stride, const void* k_cach
   p.window = window;
   p.rows_per_tile = L.rows;
   p.heads_per_item = L.heads;
-  static const char* ev = getenv("JG_COST");
-  p.item_cost = L.wide ? (ev ? atoi(ev) : (L.pairs ? 12 : 4)) : 4;
+  p.item_cost = L.wide ? (L.pairs ? 10 : 8) : 4;
   p.scale = act == JGDPA_ACT_SOFTMAX ? scale * jg::kLog2e : scale;
   p.wait_limit_ns = jg::host_wait_limit_ns();
   const int item_rows = L.heads > 1 ? L.rows * L.heads : static_cast<int>(std::min<int64_t>(L.rows, max_rows));
@@ -330,7 +325,7 @@ jgdpa_status jgdpa_cache_fwd(const void* q, int64_t q_stride, const void* k_cach
     constexpr int D = decltype(dim)::value;
     cudaError_t e = L.wide ? jg::launch_cache_fwd_wide_d<D>(p, act, L.pairs, L.grid, stream)
                            : jg::launch_cache_fwd_d<D>(p, act, L.grid, stream);
-    return e != cudaSuccess ? e : jg::launch_cache_join_d<D>(p, act, L.grid, L.ranges, item_rows, stream);
+    return e != cudaSuccess ? e : jg::launch_cache_join_d<D>(p, act, L.grid, item_rows, stream);
   };
   JG_CUDA(head_dim == 128  ? launch(std::integral_constant<int, 128>{})
           : head_dim == 64 ? launch(std::integral_constant<int, 64>{})

@@ -484,9 +484,7 @@ __global__ void __launch_bounds__((CcCfg<D * HP, MT, HP>::kThreads), (CcCfg<D * 
     p.err[blockIdx.x] = kOk;
     fence_mbar_init();
   }
-  CacheRange ranges[1];
-  cache_ranges<kCKeys>(p, &sh->range, kCMinRange, ranges);
-  const CacheRange& R = ranges[0];
+  const CacheRange R = cache_range<kCKeys>(p, &sh->range, kCMinRange);
   if (threadIdx.x == (C::kWarps - 1) * 32) cache_open<kCKeys>(p, R);
   Fail fail{&sh->abort, p.err + blockIdx.x, p.wait_limit_ns};
   if (threadIdx.x >= C::kWarps * 32) cc_producer<D * HP, MT, HP>(p, smem, sh, R, fail);
@@ -501,8 +499,7 @@ __global__ void __launch_bounds__((CcCfg<D * HP, MT, HP>::kThreads), (CcCfg<D * 
 constexpr int kJoinRows = 2;
 
 template <int D, bool SOFTMAX>
-__global__ void __launch_bounds__(kJoinRows * 128) cache_join_kernel(const __grid_constant__ CacheFwdParams p, int n_ctas,
-                                                                     int n_ranges) {
+__global__ void __launch_bounds__(kJoinRows * 128) cache_join_kernel(const __grid_constant__ CacheFwdParams p, int n_ctas) {
   constexpr int V = D / 32;
   __shared__ int worst[kJoinRows * 4];
   __shared__ float sums[kJoinRows][4][D];
@@ -521,7 +518,7 @@ __global__ void __launch_bounds__(kJoinRows * 128) cache_join_kernel(const __gri
     }
   }
   const int border = blockIdx.x + 1;
-  if (border >= n_ranges) return;
+  if (border >= n_ctas) return;
   const CacheJoin j = p.join[border];
   if (!j.valid) return;
   const int q0 = __ldg(p.q_off + j.b), T = __ldg(p.q_off + j.b + 1) - q0;
@@ -530,7 +527,7 @@ __global__ void __launch_bounds__(kJoinRows * 128) cache_join_kernel(const __gri
   const int64_t flat = static_cast<int64_t>(j.rt) * R + lr;
   const bool live = hh < p.heads_per_item && flat < static_cast<int64_t>(T) * p.group;
   // (the first range that holds one of the item's tiles, the last)
-  const int c0 = static_cast<int>((j.t0 + p.item_cost) / j.per), c1 = static_cast<int>((j.t1 - 1) / j.per);
+  const int c0 = static_cast<int>(cache_range_of(j.t0 + p.item_cost, j.per)), c1 = static_cast<int>(cache_range_of(j.t1 - 1, j.per));
   // range c's part lies in its first slot when the range starts inside the item (or at its start)
   auto row_of = [&](int c) {
     return (2 * static_cast<int64_t>(c) + (c * j.per < j.t0 ? 1 : 0)) * (p.heads_per_item * R) + row;
@@ -621,10 +618,9 @@ cudaError_t launch_cache_fwd_d(const CacheFwdParams& p, int act, int grid, cudaS
 // Launched so that its blocks may be set up while the attention still runs
 // (programmatic dependent launch); they wait for its end before they read.
 template <int D>
-cudaError_t launch_cache_join_d(const CacheFwdParams& p, int act, int n_ctas, int n_ranges, int item_rows,
-                                cudaStream_t stream) {
+cudaError_t launch_cache_join_d(const CacheFwdParams& p, int act, int n_ctas, int item_rows, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(n_ranges > 1 ? n_ranges - 1 : 1, (item_rows + kJoinRows - 1) / kJoinRows, 1);
+  cfg.gridDim = dim3(n_ctas > 1 ? n_ctas - 1 : 1, (item_rows + kJoinRows - 1) / kJoinRows, 1);
   cfg.blockDim = dim3(kJoinRows * 128, 1, 1);
   cfg.stream = stream;
   cudaLaunchAttribute at[1];
@@ -632,11 +628,11 @@ cudaError_t launch_cache_join_d(const CacheFwdParams& p, int act, int n_ctas, in
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return act == 2 ? cudaLaunchKernelEx(&cfg, cache_join_kernel<D, true>, p, n_ctas, n_ranges)
-                  : cudaLaunchKernelEx(&cfg, cache_join_kernel<D, false>, p, n_ctas, n_ranges);
+  return act == 2 ? cudaLaunchKernelEx(&cfg, cache_join_kernel<D, true>, p, n_ctas)
+                  : cudaLaunchKernelEx(&cfg, cache_join_kernel<D, false>, p, n_ctas);
 }
 
 template cudaError_t launch_cache_fwd_d<JGDPA_HEAD_DIM>(const CacheFwdParams&, int, int, cudaStream_t);
-template cudaError_t launch_cache_join_d<JGDPA_HEAD_DIM>(const CacheFwdParams&, int, int, int, int, cudaStream_t);
+template cudaError_t launch_cache_join_d<JGDPA_HEAD_DIM>(const CacheFwdParams&, int, int, int, cudaStream_t);
 
 }  // namespace jg

@@ -35,6 +35,7 @@ namespace jg {
 constexpr int kWideMinRange = 6;  // a range below this many tiles is not worth its own CTA
 constexpr int kWideThreads = 384;
 
+// PAIR: items of more than 128 rows.
 template <int D, bool PAIR>
 struct CwCfg {
   static constexpr int kBlockCols = D < 64 ? D : 64;
@@ -45,13 +46,14 @@ struct CwCfg {
   // K and V go through one ring of `kStages` tiles in the order K0 K1 V0 K2 V1
   // ..: a V is not needed before its P, more than a tile's time after its K, and
   // would only hold its stage meanwhile
-  static constexpr int kStages = D == 128 ? (PAIR ? 4 : 5) : (D == 64 ? 11 : 16);
+  static constexpr int kSlots = PAIR ? 2 : 1;  // Q tiles
+  static constexpr int kStages = D == 128 ? 7 - kSlots : (D == 64 ? 14 - kSlots : 16);
   static constexpr uint32_t kSwizzle = kRowBytes == 128 ? 2u : 4u;
   static constexpr int kSBO = 8 * kRowBytes;
-  static constexpr int kQOff = 0;  // two Q tiles
-  static constexpr int kRingOff = kQOff + 2 * kTileBytes;
+  static constexpr int kQOff = 0;
+  static constexpr int kRingOff = kQOff + kSlots * kTileBytes;
   static constexpr int kBarOff = kRingOff + kStages * kTileBytes;
-  static constexpr int kSmemBytes = kBarOff + 2048 + (PAIR ? 2 * 2 * kTile * 8 : 0) + 1024;
+  static constexpr int kSmemBytes = kBarOff + 2048 + 1024;
   static_assert(kSmemBytes <= 232448, "shared memory per CTA");
   // Ring entries of the CTA's tile `it`.  (The K entry before the very last V
   // is skipped; the ring does not come round to it.)
@@ -67,14 +69,13 @@ struct CwShared {
   // The CTA's n-th masked tile, at n % 2: asked for when its S is issued, its V
   // safe.  (Each stream has at most one tile whose S is issued and P V is not.)
   uint64_t fix_ask[2], fixed[2];
-  uint64_t s_full[2], p_full[2], o_full[2], o_empty[2];
-  uint64_t drain;
-  CacheRangeShared range[2];
+  uint64_t s_full[2], p_full[2], o_full[2];
+  uint64_t o_empty, drain;
+  CacheRangeShared range;
   uint32_t tmem_base;
   int abort;
-  int odd[2][16];          // by stream (0 for both of a pair): number of the last part (mod 16) whose
-                           // masked tiles hold a V that is not finite
-  float2 ml[];             // pairs only, [part parity][stream][row]: maximum and sum
+  int odd[16];       // number of the last part (mod 16) whose masked tiles hold a V that is not finite
+  float2 ml[kTile];  // the streams' maxima and sums at the end of a part that they share
 };
 static_assert(sizeof(CwShared) <= 2048, "shared block");
 
@@ -117,43 +118,9 @@ struct CwPart {
     far_hi = p.bias_len == 0 ? INT32_MAX : (C >= reach ? (C - reach + 1) / kTile : 0);
   }
   __device__ __forceinline__ bool plain(int tile) const { return tile >= plain_lo && tile < plain_hi; }
-  // Of a CTA whose streams share their parts: the tiles of stream s, and the one it takes as its i-th.
+  // The tiles of stream s, and the one it takes as its i-th.
   __device__ __forceinline__ int count(int s) const { return pair ? n : (n + 1 - s) / 2; }
   __device__ __forceinline__ int at(int s, int i) const { return pair ? i : 2 * i + s; }
-};
-
-// The tiles of a CTA with lone streams in the order in which every role takes
-// them: by turns, one tile of each stream that has any left.
-struct CwTurns {
-  CacheWalk w[2];
-  CwPart part[2];
-  int i[2];  // tile of the part
-  bool more[2];
-
-  // (a part without tiles, all behind what its rows see, is passed over)
-  __device__ __forceinline__ void part_from(const CacheFwdParams& p, int s) {
-    i[s] = 0;
-    for (;; w[s].advance()) {
-      more[s] = w[s].next<kTile>(p);
-      if (!more[s]) return;
-      part[s] = CwPart(p, w[s]);
-      if (part[s].n > 0) return;
-    }
-  }
-  __device__ __forceinline__ CwTurns(const CacheFwdParams& p, const CacheRange (&R)[2]) {
-#pragma unroll
-    for (int s = 0; s < 2; ++s) {
-      w[s].init(R[s]);
-      part_from(p, s);
-    }
-  }
-  __device__ __forceinline__ int tile(int s) const { return part[s].lo + i[s]; }
-  __device__ __forceinline__ void step(const CacheFwdParams& p, int s) {
-    if (++i[s] == part[s].n) {
-      w[s].advance();
-      part_from(p, s);
-    }
-  }
 };
 
 // ------------------------------------------------------------- producer
@@ -164,7 +131,7 @@ struct CwProducer {
   uint8_t* smem;
   CwShared* sh;
   Fail fail;
-  uint32_t q_n[2] = {0, 0};  // Q loads issued, by slot
+  uint32_t q_n = 0;          // Q loads issued
   uint32_t it = 0;           // tiles taken
   uint32_t entries = 0;      // ring entries issued, or one more (the skipped one)
   // the last tile, whose V is to come
@@ -174,9 +141,10 @@ struct CwProducer {
     bool mine;
   } held;
 
-  // Rows of the tile from `token` on into a Q slot (whole warp).
-  __device__ __forceinline__ bool query(int slot, const CacheWalk& w, int token) {
-    if (!mbar_wait_warp(&sh->q_empty[slot], (q_n[slot] & 1) ^ 1, fail)) return false;
+  // Rows of the tile from `token` on into the next Q slot (whole warp).
+  __device__ __forceinline__ bool query(const CacheWalk& w, int token) {
+    const int slot = q_n % C::kSlots;
+    if (!mbar_wait_warp(&sh->q_empty[slot], ((q_n / C::kSlots) & 1) ^ 1, fail)) return false;
     if ((threadIdx.x & 31) == 0) {
       mbar_arrive_tx(&sh->q_full[slot], kTile / p.group * p.group * D * 2);
 #pragma unroll
@@ -185,7 +153,7 @@ struct CwProducer {
                     b * C::kBlockCols, w.h * p.group, w.r.q0 + token);
     }
     __syncwarp();
-    ++q_n[slot];
+    ++q_n;
     return true;
   }
   // Lane: piece lane % 8 (min(page size, 128) tokens) of column block lane / 8.
@@ -228,39 +196,25 @@ struct CwProducer {
   }
   // After a failure: lets the copies already issued land before the CTA exits.
   __device__ void drain() {
-    for (int s = 0; s < 2; ++s)
-      if (q_n[s]) mbar_wait_drain(&sh->q_full[s], (q_n[s] - 1) & 1);
+    for (uint32_t i = q_n > C::kSlots ? q_n - C::kSlots : 0; i < q_n; ++i)
+      mbar_wait_drain(&sh->q_full[i % C::kSlots], (i / C::kSlots) & 1);
     for (uint32_t e = entries > C::kStages ? entries - C::kStages : 0; e < entries; ++e)
       mbar_wait_drain(&sh->full[C::stage(e)], C::parity(e));
   }
 };
 
 template <int D, bool PAIR>
-__device__ void cw_producer(const CacheFwdParams& p, uint8_t* smem, CwShared* sh, const CacheRange (&R)[2], Fail fail) {
+__device__ void cw_producer(const CacheFwdParams& p, uint8_t* smem, CwShared* sh, const CacheRange& R, Fail fail) {
   CwProducer<D, PAIR> load{p, smem, sh, fail};
   bool ok = true;
-  if constexpr (PAIR) {
-    uint32_t q_slot = 0;
-    CacheWalk w;
-    w.init(R[0]);
-    for (; ok && w.next<kTile>(p); w.advance()) {
-      const CwPart part(p, w);
-      if (part.n == 0) continue;
-      for (int s = 0; s < (part.pair ? 2 : 1) && ok; ++s, ++q_slot)
-        ok = load.query(q_slot & 1, w, part.first_token + s * (part.tile_rows / p.group));
-      for (int t = part.lo; t < part.lo + part.n && ok; ++t) ok = load.tile(w, t);
-    }
-  } else {
-    CwTurns turns(p, R);
-    while (ok && (turns.more[0] || turns.more[1])) {
-#pragma unroll
-      for (int s = 0; s < 2; ++s) {
-        if (!ok || !turns.more[s]) continue;
-        if (turns.i[s] == 0) ok = load.query(s, turns.w[s], turns.part[s].first_token);
-        if (ok) ok = load.tile(turns.w[s], turns.tile(s));
-        if (ok) turns.step(p, s);
-      }
-    }
+  CacheWalk w;
+  w.init(R);
+  for (; ok && w.next<kTile>(p); w.advance()) {
+    const CwPart part(p, w);
+    if (part.n == 0) continue;
+    ok = load.query(w, part.first_token);
+    if (PAIR && part.pair && ok) ok = load.query(w, part.first_token + part.tile_rows / p.group);
+    for (int t = part.lo; t < part.lo + part.n && ok; ++t) ok = load.tile(w, t);
   }
   if (!ok || !load.value()) load.drain();
 }
@@ -300,7 +254,7 @@ struct CwIssuer {
   uint32_t tmem, q_base, ring;
   bool leader;
   Fail fail;
-  uint32_t p_n[2] = {0, 0}, o_n[2] = {0, 0}, q_n[2] = {0, 0};
+  uint32_t p_n[2] = {0, 0};
   uint32_t asked = 0, fixed = 0;  // masked tiles
 
   __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity) { return mbar_wait_warp(bar, parity, fail); }
@@ -338,97 +292,60 @@ struct CwIssuer {
 };
 
 template <int D, bool PAIR>
-__device__ void cw_mma(const CacheFwdParams& p, uint8_t* smem, CwShared* sh, uint32_t tmem, const CacheRange (&R)[2],
+__device__ void cw_mma(const CacheFwdParams& p, uint8_t* smem, CwShared* sh, uint32_t tmem, const CacheRange& R,
                        Fail fail) {
   using C = CwCfg<D, PAIR>;
   CwIssuer<D, PAIR> mma{sh, tmem, smem_u32(smem + C::kQOff), smem_u32(smem + C::kRingOff), elect_one(), fail};
   bool ok = true;
-  if constexpr (PAIR) {
-    uint32_t q_n = 0, it0 = 0;
-    CacheWalk w;
-    w.init(R[0]);
-    for (; ok && w.next<kTile>(p); w.advance()) {
-      const CwPart part(p, w);
-      if (part.n == 0) continue;
-      const uint32_t slot[2] = {q_n & 1, part.pair ? (q_n + 1) & 1 : q_n & 1};
-      for (int s = 0; s < (part.pair ? 2 : 1) && ok; ++s, ++q_n) ok = mma.wait(&sh->q_full[q_n & 1], (q_n >> 1) & 1);
-      // (a pair has a masked V made safe once)
-      auto masked = [&](int s, int t) { return (!part.pair || s == 0) && !part.plain(part.lo + t); };
-      // S of stream s's i-th tile; frees what no later product of the part reads
-      auto part_s = [&](int s, int i) -> bool {
-        const int t = part.at(s, i);
-        if (!mma.issue_s(s, slot[s], it0 + t, masked(s, t))) return false;
-        if (!part.pair || s == 1) mma.free_k(it0 + t);
-        if (t == part.n - 1) mma.commit(&sh->q_empty[slot[s]]);
-        return true;
-      };
-#pragma unroll
-      for (int s = 0; s < 2; ++s)
-        if (ok && part.count(s) > 0) ok = part_s(s, 0);
-      if (ok) ok = mma.wait(&sh->o_empty[0], (mma.o_n[0] & 1) ^ 1);  // the part before has read its O
-      ++mma.o_n[0];
-      for (int i = 0; i < part.count(0) && ok; ++i) {
-#pragma unroll
-        for (int s = 0; s < 2; ++s) {
-          if (!ok || i >= part.count(s)) continue;
-          const int t = part.at(s, i);
-          if (!(ok = mma.issue_o(s, it0 + t, i == 0, masked(s, t)))) continue;
-          if (!part.pair || s == 1) mma.free_v(it0 + t);
-          if (i == part.count(s) - 1) mma.commit(&sh->o_full[s]);
-          if (i + 1 < part.count(s)) ok = part_s(s, i + 1);
-        }
-      }
-      it0 += part.n;
-    }
-  } else {
-    // the tile of each stream whose S is issued and whose P V is not
-    struct {
-      bool any, first, last, masked;
-      uint32_t it;
-    } held[2] = {};
-    auto finish = [&](int s) -> bool {
-      if (!held[s].any) return true;
-      held[s].any = false;
-      if (held[s].first) {  // the part before has read its O
-        if (!mma.wait(&sh->o_empty[s], (mma.o_n[s] & 1) ^ 1)) return false;
-        ++mma.o_n[s];
-      }
-      if (!mma.issue_o(s, held[s].it, held[s].first, held[s].masked)) return false;
-      mma.free_v(held[s].it);
-      if (held[s].last) mma.commit(&sh->o_full[s]);
+  uint32_t q_n = 0, it0 = 0, o_n = 0;
+  CacheWalk w;
+  w.init(R);
+  for (; ok && w.next<kTile>(p); w.advance()) {
+    const CwPart part(p, w);
+    if (part.n == 0) continue;
+    const bool pair = PAIR && part.pair;
+    const int slot[2] = {static_cast<int>(q_n % C::kSlots), static_cast<int>(pair ? (q_n + 1) % C::kSlots : q_n % C::kSlots)};
+    for (int s = 0; s < (pair ? 2 : 1) && ok; ++s, ++q_n)
+      ok = mma.wait(&sh->q_full[q_n % C::kSlots], (q_n / C::kSlots) & 1);
+    // (a pair has a masked V made safe once)
+    auto masked = [&](int s, int t) { return (!pair || s == 0) && !part.plain(part.lo + t); };
+    // S of stream s's i-th tile; frees what no later product of the part reads
+    auto part_s = [&](int s, int i) -> bool {
+      const int t = part.at(s, i);
+      if (!mma.issue_s(s, slot[s], it0 + t, masked(s, t))) return false;
+      if (!pair || s == 1) mma.free_k(it0 + t);
+      if (t == part.n - 1) mma.commit(&sh->q_empty[slot[s]]);
       return true;
     };
-    uint32_t it = 0;
-    CwTurns turns(p, R);
-    while (ok && (turns.more[0] || turns.more[1])) {
+    if (ok) ok = part_s(0, 0);
+    if (ok && part.count(1) > 0) ok = part_s(1, 0);
+    if (ok) ok = mma.wait(&sh->o_empty, (o_n & 1) ^ 1);  // the part before has read its O
+    ++o_n;
+    for (int i = 0; i < part.count(0) && ok; ++i) {
 #pragma unroll
       for (int s = 0; s < 2; ++s) {
-        // (a stream that is done must not hold a stage back, either)
-        if (!ok || !(ok = finish(s)) || !turns.more[s]) continue;
-        const CwPart& part = turns.part[s];
-        const bool first = turns.i[s] == 0, last = turns.i[s] == part.n - 1, masked = !part.plain(turns.tile(s));
-        if (first) {
-          if (!(ok = mma.wait(&sh->q_full[s], mma.q_n[s] & 1))) continue;
-          ++mma.q_n[s];
-        }
-        if (!(ok = mma.issue_s(s, s, it, masked))) continue;
-        mma.free_k(it);
-        if (last) mma.commit(&sh->q_empty[s]);
-        held[s] = {true, first, last, masked, it};
-        ++it;
-        turns.step(p, s);
+        if (!ok || i >= part.count(s)) continue;
+        const int t = part.at(s, i);
+        if (!(ok = mma.issue_o(s, it0 + t, i == 0, masked(s, t)))) continue;
+        if (!pair || s == 1) mma.free_v(it0 + t);
+        if (i == part.count(s) - 1) mma.commit(&sh->o_full[s]);
+        if (i + 1 < part.count(s)) ok = part_s(s, i + 1);
       }
     }
-    if (ok && finish(0)) finish(1);
+    it0 += part.n;
   }
   mma.commit(&sh->drain);
   mbar_wait_drain(&sh->drain, 0);
 }
 
 // ------------------------------------------------------ activation warps
-// Which of a tile's 128 keys a row sees (bit c of word q: key0 + 32 q + c).
-__device__ __forceinline__ void cw_visible(const CacheFwdParams& p, const CacheReq& r, const CcRow& q, int key0,
-                                           uint32_t (&see)[4]) {
+// The code of a tile is kept small, in loops over 32 columns: most of it runs a
+// few times per item, and instructions fetched for the first time cost more
+// than the work (a fully unrolled tile took 2.1 us on its first run, 0.9 after).
+
+// Which of a tile's 128 keys a row sees (bit c of word k: key0 + 32 k + c).
+static __device__ __noinline__ uint4 cw_visible(const CacheFwdParams& p, CacheReq r, CcRow q, int key0) {
+  uint32_t see[4];
 #pragma unroll
   for (int k = 0; k < 4; ++k) see[k] = cc_vis32(p, r, q, key0 + 32 * k);
   if (p.window > 0) {
@@ -437,124 +354,120 @@ __device__ __forceinline__ void cw_visible(const CacheFwdParams& p, const CacheR
     for (int k = 0; k < 4; ++k) {
       const int my_pos = cc_pos(p, r, key0 + 32 * k + lane);  // lane c: of key c
       uint32_t near = 0;
-#pragma unroll
+#pragma unroll 4
       for (int c = 0; c < 32; ++c) near |= (cc_near(p, q.pos, __shfl_sync(0xffffffffu, my_pos, c)) ? 1u : 0u) << c;
       see[k] &= near;
     }
   }
+  return make_uint4(see[0], see[1], see[2], see[3]);
 }
 
-// S -> s S + bias (in log2 units for softmax) for the tiles near the new
-// tokens, where the bias varies from key to key.
+// S -> s S + bias (in log2 units for softmax) in place, for the tiles near the
+// new tokens, where the bias varies from key to key or some rows do not see
+// some keys (-inf for softmax, else 0, as act(0) = 0).
 template <int ACT>
-__device__ __forceinline__ void cw_bias_tile(const CacheFwdParams& p, const CacheReq& r, const CcRow& q, int reach,
-                                             int key0, uint32_t t_s) {
-  const int lane = threadIdx.x & 31;
+__device__ __noinline__ void cw_near_tile(const CacheFwdParams& p, CacheReq r, CcRow q, bool far, uint4 see, int key0,
+                                          uint32_t t_s) {
+  const int lane = threadIdx.x & 31, reach = (p.bias_len - 1) / 2;
 #pragma unroll 1
   for (int c0 = 0; c0 < kTile; c0 += 32) {
     uint32_t v[32];
     tmem_ld32(t_s + c0, v);
-    const int my_pos = cc_pos(p, r, key0 + c0 + lane);  // lane c: of key c0 + c
-    float bias[32];
-#pragma unroll
-    for (int c = 0; c < 32; ++c) bias[c] = cc_bias(p, q, reach, __shfl_sync(0xffffffffu, my_pos, c)) * cc_bias_unit<ACT>();
+    const int my_pos = far ? 0 : cc_pos(p, r, key0 + c0 + lane);  // lane c: the position of key c0 + c
     tmem_ld_wait(v);
+    if (far) {
 #pragma unroll
-    for (int c = 0; c < 32; ++c) v[c] = __float_as_uint(__fmaf_rn(__uint_as_float(v[c]), p.scale, bias[c]));
+      for (int c = 0; c < 32; ++c) v[c] = __float_as_uint(__fmaf_rn(__uint_as_float(v[c]), p.scale, q.far_bias));
+    } else {
+#pragma unroll
+      for (int c = 0; c < 32; ++c) {
+        const float bias = cc_bias(p, q, reach, __shfl_sync(0xffffffffu, my_pos, c)) * cc_bias_unit<ACT>();
+        v[c] = __float_as_uint(__fmaf_rn(__uint_as_float(v[c]), p.scale, bias));
+      }
+    }
+#pragma unroll
+    for (int c = 0; c < 32; ++c)
+      if (!((see.x >> c) & 1)) v[c] = ACT == 2 ? 0xFF800000u : 0u;
+    see = make_uint4(see.y, see.z, see.w, 0u);
     tmem_st32(t_s + c0, v);
   }
   tmem_st_wait();
 }
 
-// P = act(s S + bias) over S's columns, two elements per packed instruction;
-// the TMEM load of the next 32 columns is in flight while these are computed.
-// MASKED: keys a row does not see get P = act(0) = 0.
-template <int ACT, bool MASKED>
-__device__ __forceinline__ void cw_act_tile(uint32_t t_s, float scale, float bias, const uint32_t (&see)[4]) {
+// P = act(s S + bias) over S's columns, two elements per packed instruction.
+template <int ACT>
+__device__ __forceinline__ void cw_act_tile(uint32_t t_s, float scale, float bias) {
   const float2 hs = f2(0.5f * scale), hb = f2(0.5f * bias);
-  uint32_t buf0[32], buf1[32];
-  tmem_ld32(t_s, buf0);
-  tmem_ld_wait(buf0);
+#pragma unroll 1
+  for (int q = 0; q < 4; q += 2) {
+    uint32_t a[32], b[32];
+    tmem_ld32(t_s + 32 * q, a);
+    tmem_ld32(t_s + 32 * q + 32, b);
+    tmem_ld_wait2(a, b);
+    uint32_t pk[32];
 #pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    uint32_t(&cur)[32] = (q & 1) ? buf1 : buf0;
-    uint32_t(&nxt)[32] = (q & 1) ? buf0 : buf1;
-    if (q < 3) tmem_ld32(t_s + 32 * (q + 1), nxt);
-    uint32_t pk[16];
-#pragma unroll
-    for (int c = 0; c < 16; ++c) {
-      float2 hx = __ffma2_rn(make_float2(__uint_as_float(cur[2 * c]), __uint_as_float(cur[2 * c + 1])), hs, hb);
-      if (MASKED) {
-        if (!((see[q] >> (2 * c)) & 1)) hx.x = 0.f;
-        if (!((see[q] >> (2 * c + 1)) & 1)) hx.y = 0.f;
-      }
+    for (int c = 0; c < 32; ++c) {
+      const uint32_t(&v)[32] = c < 16 ? a : b;
+      const float2 hx = __ffma2_rn(make_float2(__uint_as_float(v[2 * (c % 16)]), __uint_as_float(v[2 * (c % 16) + 1])), hs, hb);
       const float2 y = act2_route<ACT, 0>(hx);
       pk[c] = pack_bf16(y.x, y.y);
     }
-    tmem_st16(t_s + 16 * q, pk);  // columns [16 q, 16 q + 16) are read already
-    if (q < 3) tmem_ld_wait(nxt);
+    tmem_st32(t_s + 16 * q, pk);  // columns [16 q, 16 q + 32) are read already
   }
 }
 
 // P = 2^(x - m) with a running maximum that moves only when it grows by more
-// than 8 (P stays below 2^8, O and l in fp32): O is rescaled then.  MASKED:
-// keys a row does not see have x = -inf.
-template <int D, bool MASKED>
-__device__ __forceinline__ void cw_softmax_tile(uint32_t t_s, uint32_t t_o, float scale, float bias,
-                                                const uint32_t (&see)[4], bool first, float& m, float& l) {
-  uint32_t a[32], b[32], c3[32], d4[32];
-  tmem_ld32(t_s, a);
-  tmem_ld32(t_s + 32, b);
-  tmem_ld_wait2(a, b);
-  tmem_ld32(t_s + 64, c3);
-  tmem_ld32(t_s + 96, d4);
-  tmem_ld_wait2(c3, d4);
+// than 8 (P stays below 2^8, O and l in fp32): O is rescaled then.
+template <int D>
+__device__ __forceinline__ void cw_softmax_tile(uint32_t t_s, uint32_t t_o, float scale, float bias, bool first,
+                                                float& m, float& l) {
   float mx = -INFINITY;
+#pragma unroll 1
+  for (int q = 0; q < 4; q += 2) {
+    uint32_t a[32], b[32];
+    tmem_ld32(t_s + 32 * q, a);
+    tmem_ld32(t_s + 32 * q + 32, b);
+    tmem_ld_wait2(a, b);
 #pragma unroll
-  for (int c = 0; c < 128; c += 2) {
-    uint32_t& r0 = c < 32 ? a[c] : c < 64 ? b[c - 32] : c < 96 ? c3[c - 64] : d4[c - 96];
-    uint32_t& r1 = c < 32 ? a[c + 1] : c < 64 ? b[c - 31] : c < 96 ? c3[c - 63] : d4[c - 95];
-    float2 x = __ffma2_rn(make_float2(__uint_as_float(r0), __uint_as_float(r1)), f2(scale), f2(bias));
-    if (MASKED) {
-      if (!((see[c / 32] >> (c % 32)) & 1)) x.x = -INFINITY;
-      if (!((see[c / 32] >> (c % 32 + 1)) & 1)) x.y = -INFINITY;
+    for (int c = 0; c < 32; c += 2) {
+      const float2 x = __ffma2_rn(make_float2(__uint_as_float(a[c]), __uint_as_float(a[c + 1])), f2(scale), f2(bias));
+      const float2 y = __ffma2_rn(make_float2(__uint_as_float(b[c]), __uint_as_float(b[c + 1])), f2(scale), f2(bias));
+      mx = fmaxf(fmaxf(mx, fmaxf(x.x, x.y)), fmaxf(y.x, y.y));
     }
-    r0 = __float_as_uint(x.x);
-    r1 = __float_as_uint(x.y);
-    mx = fmaxf(mx, fmaxf(x.x, x.y));
   }
   const bool grow = mx > m + 8.0f;
   const float factor = grow ? ex2_sfu(m - mx) : 1.0f;  // 0 on the first tile
   if (grow) m = mx;
   l *= factor;
-  const float2 neg = f2(m == -INFINITY ? 0.f : -m);  // no key seen so far: every x is -inf and P is 0
+  // x - m, with m = 0 while no key was seen: then every x is -inf and P is 0
+  const float2 off = f2(m == -INFINITY ? bias : bias - m);
   float2 sum = f2(0.f);
+#pragma unroll 1
+  for (int q = 0; q < 4; q += 2) {
+    uint32_t a[32], b[32];
+    tmem_ld32(t_s + 32 * q, a);
+    tmem_ld32(t_s + 32 * q + 32, b);
+    tmem_ld_wait2(a, b);
+    uint32_t pk[32];
 #pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    uint32_t(&src)[32] = q == 0 ? a : q == 1 ? b : q == 2 ? c3 : d4;
-    uint32_t pk[16];
-#pragma unroll
-    for (int c = 0; c < 16; ++c) {
-      const float2 z = __fadd2_rn(make_float2(__uint_as_float(src[2 * c]), __uint_as_float(src[2 * c + 1])), neg);
+    for (int c = 0; c < 32; ++c) {
+      const uint32_t(&v)[32] = c < 16 ? a : b;
+      const float2 z = __ffma2_rn(make_float2(__uint_as_float(v[2 * (c % 16)]), __uint_as_float(v[2 * (c % 16) + 1])), f2(scale), off);
       const float2 e = make_float2(ex2_sfu(z.x), ex2_sfu(z.y));
       sum = __fadd2_rn(sum, e);
       pk[c] = pack_bf16(e.x, e.y);
     }
-    tmem_st16(t_s + 16 * q, pk);
+    tmem_st32(t_s + 16 * q, pk);  // columns [16 q, 16 q + 32) are read already
   }
   l += sum.x + sum.y;
   if (!first && __any_sync(0xffffffffu, grow)) {
-#pragma unroll
+#pragma unroll 1
     for (int c0 = 0; c0 < D; c0 += 32) {
       uint32_t o[32];
       tmem_ld32(t_o + c0, o);
       tmem_ld_wait(o);
 #pragma unroll
-      for (int i = 0; i < 32; i += 2) {
-        const float2 v = __fmul2_rn(make_float2(__uint_as_float(o[i]), __uint_as_float(o[i + 1])), f2(factor));
-        o[i] = __float_as_uint(v.x);
-        o[i + 1] = __float_as_uint(v.y);
-      }
+      for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * factor);
       tmem_st32(t_o + c0, o);
     }
   }
@@ -606,80 +519,63 @@ __device__ __noinline__ void cw_add_odd(const CacheFwdParams& p, CacheWalk w, Cw
 // left anything there) are zeroed, and infinities and NaN of the others taken
 // out; the epilogue adds those to the rows that see them.
 template <int D, bool PAIR>
-__device__ void cw_fixer(const CacheFwdParams& p, uint8_t* smem, CwShared* sh, const CacheRange (&R)[2], Fail fail) {
+__device__ void cw_fixer(const CacheFwdParams& p, uint8_t* smem, CwShared* sh, const CacheRange& R, Fail fail) {
   using C = CwCfg<D, PAIR>;
   constexpr int kPieces = C::kBlockCols / 8;
   const int lane = threadIdx.x & 31;
   const uint32_t ring = smem_u32(smem + C::kRingOff);
   uint32_t it = 0, asked = 0;
-  int number[2] = {0, 0};
-  auto tile = [&](int s, const CacheWalk& w, const CwPart& part, int t) -> bool {
-    const uint32_t e = C::entry_v(it);
-    const int st = C::stage(e), key0 = t * kTile;
-    ++it;
-    if (part.plain(t)) return true;
-    // (once its S is issued, the stage's round before this V is over)
-    if (!mbar_wait_warp(&sh->fix_ask[asked & 1], (asked >> 1) & 1, fail)) return false;
-    if (!mbar_wait_warp(&sh->full[st], C::parity(e), fail)) return false;
-    for (int row = threadIdx.x & 63; row < kTile; row += 64) {
-      const bool past = key0 + row >= w.r.L;
-      const uint32_t vr = ring + st * C::kTileBytes + row * C::kRowBytes;
-      // (pieces in any order, whatever the swizzle: from the lane's on, so
-      // that the lanes, a row apart, meet different banks)
-      auto piece = [&](int c) {
-        return vr + (c / kPieces) * C::kBlockBytes + ((c + lane * kPieces / 8) % kPieces) * 16;
-      };
-      if (past) {
-#pragma unroll
-        for (int c = 0; c < D / 8; ++c) st_shared_v4(piece(c), 0u, 0u, 0u, 0u);
-        continue;
+  int number = 0;
+  CacheWalk w;
+  w.init(R);
+  for (; w.next<kTile>(p); w.advance()) {
+    const CwPart part(p, w);
+    if (part.n == 0) continue;
+    ++number;
+    for (int t = part.lo; t < part.lo + part.n; ++t, ++it) {
+      if (part.plain(t)) continue;
+      const uint32_t e = C::entry_v(it);
+      const int st = C::stage(e), key0 = t * kTile;
+      // (once its S is issued, the stage's round before this V is over)
+      if (!mbar_wait_warp(&sh->fix_ask[asked & 1], (asked >> 1) & 1, fail)) return;
+      if (!mbar_wait_warp(&sh->full[st], C::parity(e), fail)) return;
+      for (int row = threadIdx.x & 63; row < kTile; row += 64) {
+        const bool past = key0 + row >= w.r.L;
+        const uint32_t vr = ring + st * C::kTileBytes + row * C::kRowBytes;
+        // (pieces in any order, whatever the swizzle: from the lane's on, so
+        // that the lanes, a row apart, meet different banks)
+        auto piece = [&](int c) {
+          return vr + (c / kPieces) * C::kBlockBytes + ((c + lane * kPieces / 8) % kPieces) * 16;
+        };
+        if (past) {
+  #pragma unroll
+          for (int c = 0; c < D / 8; ++c) st_shared_v4(piece(c), 0u, 0u, 0u, 0u);
+          continue;
+        }
+        // 0 * x summed over the row is NaN when one of its values is not finite
+        const __nv_bfloat162 zero = __float2bfloat162_rn(0.f);
+        __nv_bfloat162 sum = zero;
+  #pragma unroll
+        for (int c = 0; c < D / 8; ++c) {
+          uint32_t x[4];
+          ld_shared_v4(piece(c), x[0], x[1], x[2], x[3]);
+  #pragma unroll
+          for (int e = 0; e < 4; ++e) sum = __hfma2(*reinterpret_cast<__nv_bfloat162*>(&x[e]), zero, sum);
+        }
+        if (__low2float(sum) == 0.f && __high2float(sum) == 0.f) continue;
+        *const_cast<volatile int*>(&sh->odd[number & 15]) = number;
+  #pragma unroll 1
+        for (int c = 0; c < D / 8; ++c) {
+          uint32_t x[4];
+          ld_shared_v4(piece(c), x[0], x[1], x[2], x[3]);
+  #pragma unroll
+          for (int e = 0; e < 4; ++e) x[e] &= ~cc_nonfinite(x[e]);
+          st_shared_v4(piece(c), x[0], x[1], x[2], x[3]);
+        }
       }
-      // 0 * x summed over the row is NaN when one of its values is not finite
-      const __nv_bfloat162 zero = __float2bfloat162_rn(0.f);
-      __nv_bfloat162 sum = zero;
-#pragma unroll
-      for (int c = 0; c < D / 8; ++c) {
-        uint32_t x[4];
-        ld_shared_v4(piece(c), x[0], x[1], x[2], x[3]);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) sum = __hfma2(*reinterpret_cast<__nv_bfloat162*>(&x[e]), zero, sum);
-      }
-      if (__low2float(sum) == 0.f && __high2float(sum) == 0.f) continue;
-      *const_cast<volatile int*>(&sh->odd[s][number[s] & 15]) = number[s];
-#pragma unroll 1
-      for (int c = 0; c < D / 8; ++c) {
-        uint32_t x[4];
-        ld_shared_v4(piece(c), x[0], x[1], x[2], x[3]);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) x[e] &= ~cc_nonfinite(x[e]);
-        st_shared_v4(piece(c), x[0], x[1], x[2], x[3]);
-      }
-    }
-    fence_proxy_async_smem();
-    mbar_arrive_warp(&sh->fixed[asked & 1]);
-    ++asked;
-    return true;
-  };
-  if constexpr (PAIR) {
-    CacheWalk w;
-    w.init(R[0]);
-    for (; w.next<kTile>(p); w.advance()) {
-      const CwPart part(p, w);
-      if (part.n == 0) continue;
-      ++number[0];
-      for (int t = part.lo; t < part.lo + part.n; ++t)
-        if (!tile(0, w, part, t)) return;
-    }
-  } else {
-    CwTurns turns(p, R);
-    while (turns.more[0] || turns.more[1]) {
-#pragma unroll
-      for (int s = 0; s < 2; ++s) {
-        if (!turns.more[s]) continue;
-        if (turns.i[s] == 0) ++number[s];
-        if (!tile(s, turns.w[s], turns.part[s], turns.tile(s))) return;
-        turns.step(p, s);
-      }
+      fence_proxy_async_smem();
+      mbar_arrive_warp(&sh->fixed[asked & 1]);
+      ++asked;
     }
   }
 }
@@ -706,7 +602,7 @@ __device__ __forceinline__ void cw_store16(const uint32_t (&x)[16], float inv, _
 }
 
 template <int D, int ACT, bool PAIR>
-__device__ void cw_consumer(const CacheFwdParams& p, CwShared* sh, uint32_t tmem, int stream, const CacheRange R,
+__device__ void cw_consumer(const CacheFwdParams& p, CwShared* sh, uint32_t tmem, int stream, const CacheRange& R,
                             Fail fail) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int row = (warp & 3) * 32 + lane;
@@ -715,14 +611,13 @@ __device__ void cw_consumer(const CacheFwdParams& p, CwShared* sh, uint32_t tmem
   const int reach = (p.bias_len - 1) / 2;
   uint32_t s_n = 0, o_n[2] = {0, 0};
   int number = 0;  // of the part with tiles, from 1
-  int ml_at = 0;
   bool dead = false;
   CacheWalk w;
   w.init(R);
   for (; w.next<kTile>(p); w.advance()) {
     const CwPart part(p, w);
     const CacheReq& r = w.r;
-    if (part.n > 0) ++number;  // (the ring lets no more than 8 later parts be loaded, let alone checked)
+    if (part.n > 0) ++number;  // (the ring lets no more than 8 later parts be loaded, let alone made safe)
     __syncwarp();
     const int block_row0 = w.row_tile * p.rows_per_tile;
     const bool pair = PAIR && part.pair;
@@ -737,10 +632,13 @@ __device__ void cw_consumer(const CacheFwdParams& p, CwShared* sh, uint32_t tmem
     if (row_ok && p.bias_len)
       q.far_bias = __ldg(p.bias + static_cast<int64_t>(q.head) * p.bias_len + 2 * reach) * cc_bias_unit<ACT>();
     const bool warp_live = (warp & 3) * 32 < my_rows;
-    const int count = PAIR ? part.count(stream) : part.n;
+    const int count = part.count(stream);
     float m = -INFINITY, l = 0.f;
     for (int i = 0; i < count; ++i) {
-      const int tile = part.lo + (PAIR ? part.at(stream, i) : i);
+      const int tile = part.lo + part.at(stream, i);
+      const bool far = tile < part.far_hi, plain = part.plain(tile);
+      uint4 see = make_uint4(0xFFFFFFFFu, 0xFFFFFFFFu, 0xFFFFFFFFu, 0xFFFFFFFFu);
+      if (!plain && warp_live) see = cw_visible(p, r, q, tile * kTile);  // (its loads before S is waited for)
       if (!dead && !mbar_wait(&sh->s_full[stream], s_n & 1, fail)) dead = true;
       dead = __any_sync(0xffffffffu, dead);
       ++s_n;
@@ -748,20 +646,13 @@ __device__ void cw_consumer(const CacheFwdParams& p, CwShared* sh, uint32_t tmem
       tc_fence_after();
       if (warp_live) {
         float scale = p.scale, bias = q.far_bias;
-        if (tile >= part.far_hi) {
-          cw_bias_tile<ACT>(p, r, q, reach, tile * kTile, t_s);
+        if (!far || !plain) {
+          cw_near_tile<ACT>(p, r, q, far, see, tile * kTile, t_s);
           scale = 1.f;
           bias = 0.f;
         }
-        uint32_t see[4] = {0u, 0u, 0u, 0u};
-        if (part.plain(tile)) {
-          if constexpr (ACT == 2) cw_softmax_tile<D, false>(t_s, t_o + 128 * stream, scale, bias, see, i == 0, m, l);
-          else cw_act_tile<ACT, false>(t_s, scale, bias, see);
-        } else {
-          cw_visible(p, r, q, tile * kTile, see);
-          if constexpr (ACT == 2) cw_softmax_tile<D, true>(t_s, t_o + 128 * stream, scale, bias, see, i == 0, m, l);
-          else cw_act_tile<ACT, true>(t_s, scale, bias, see);
-        }
+        if constexpr (ACT == 2) cw_softmax_tile<D>(t_s, t_o + 128 * stream, scale, bias, i == 0, m, l);
+        else cw_act_tile<ACT>(t_s, scale, bias);
         tmem_st_wait();
       }
       tc_fence_before();
@@ -769,7 +660,7 @@ __device__ void cw_consumer(const CacheFwdParams& p, CwShared* sh, uint32_t tmem
     }
 
     // the part's end
-    const bool share = PAIR && !part.pair && part.n > 0;  // both streams hold parts of the same rows
+    const bool share = !pair && part.n > 0;  // both streams hold parts of the same rows
     int o_col = 0;            // first column this warpgroup writes
     float f[2] = {1.f, 1.f};  // factors of the streams' O
     bool use[2] = {stream == 0 && part.n > 0, stream == 1 && part.n > 0};
@@ -778,11 +669,16 @@ __device__ void cw_consumer(const CacheFwdParams& p, CwShared* sh, uint32_t tmem
       use[1] = part.count(1) > 0;
       o_col = stream * (D / 2);
       if constexpr (ACT == 2) {
-        float2* ml = sh->ml + ml_at * 2 * kTile;
-        ml[stream * kTile + row] = make_float2(m, l);
+        // the two threads of a row exchange through one place, there and back
+        float2 other = make_float2(m, l);
+        if (stream == 1) sh->ml[row] = other;
         named_bar(1, 256);
-        const float2 other = ml[(stream ^ 1) * kTile + row];
-        ml_at ^= 1;
+        if (stream == 0) {
+          other = sh->ml[row];
+          sh->ml[row] = make_float2(m, l);
+        }
+        named_bar(1, 256);
+        if (stream == 1) other = sh->ml[row];
         const float top = fmaxf(m, other.x), ref = top == -INFINITY ? 0.f : top;
         f[stream] = ex2_sfu(m - ref);
         f[stream ^ 1] = ex2_sfu(other.x - ref);
@@ -795,50 +691,39 @@ __device__ void cw_consumer(const CacheFwdParams& p, CwShared* sh, uint32_t tmem
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
       if (use[s] && !dead && !mbar_wait(&sh->o_full[s], o_n[s] & 1, fail)) dead = true;
-      if (PAIR ? part.count(s) > 0 && part.n > 0 : use[s]) ++o_n[s];
+      if (part.n > 0 && part.count(s) > 0) ++o_n[s];
     }
     dead = __any_sync(0xffffffffu, dead);
-    // O leaves tensor memory at once (all columns of one stream, or half the
-    // columns of both), so that the next part's products may start
-    uint32_t x[D / 16][16];
-    tc_fence_after();
-#pragma unroll
-    for (int k = 0; k < D / 16; ++k) {
-      const int s = share ? (k >= D / 32 ? 1 : 0) : stream;
-      const int col = share ? o_col + 16 * (k % (D / 32)) : 16 * k;
-      if (!dead && use[s]) {
-        tmem_ld16(t_o + 128 * s + col, x[k]);
-      } else {
-#pragma unroll
-        for (int c = 0; c < 16; ++c) x[k][c] = 0u;
-      }
-    }
-#pragma unroll
-    for (int k = 0; k < D / 16; ++k) tmem_ld_wait16(x[k]);
-    const bool odd = part.n > 0 && *const_cast<volatile int*>(&sh->odd[PAIR ? 0 : stream][number & 15]) == number;
-    if (part.n > 0) {
-      tc_fence_before();
-      mbar_arrive_warp(&sh->o_empty[PAIR ? 0 : stream]);
-    }
-    if (!row_ok || dead) continue;
+    const bool odd = part.n > 0 && *const_cast<volatile int*>(&sh->odd[number & 15]) == number;
     const float inv = ACT != 2 || !w.whole ? 1.f : (l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l));
-    const int64_t token = r.q0 + q.t;
-    const int64_t prow = (2 * static_cast<int64_t>(R.index) + (w.first ? 0 : 1)) * p.rows_per_tile + (flat - block_row0);
+    const int64_t token = r.q0 + (row_ok ? q.t : 0);
+    const int64_t prow = (2 * static_cast<int64_t>(blockIdx.x) + (w.first ? 0 : 1)) * p.rows_per_tile + (flat - block_row0);
     __nv_bfloat16* out = w.whole ? p.out + (token * p.heads + q.head) * D : nullptr;
     float* part_o = p.part_o + prow * D;
+    tc_fence_after();
     // (a part without tiles leaves zeros; where the streams share it, both write them)
-    if (!share) {
+#pragma unroll 1
+    for (int c0 = o_col; c0 < o_col + (share ? D / 2 : D); c0 += 16) {
+      uint32_t x[16], y[16];
 #pragma unroll
-      for (int k = 0; k < D / 16; ++k) cw_store16(x[k], inv, out, part_o, 16 * k);
-    } else {
-#pragma unroll
-      for (int k = 0; k < D / 32; ++k) {
-#pragma unroll
-        for (int c = 0; c < 16; ++c)
-          x[k][c] = __float_as_uint(__fmaf_rn(__uint_as_float(x[k][c]), f[0], __uint_as_float(x[k + D / 32][c]) * f[1]));
-        cw_store16(x[k], inv, out, part_o, o_col + 16 * k);
+      for (int c = 0; c < 16; ++c) x[c] = y[c] = 0u;
+      if (!dead) {
+        if (use[0]) tmem_ld16(t_o + c0, x);
+        if (use[1]) tmem_ld16(t_o + 128 + c0, y);
+        tmem_ld_wait16(x);
+        tmem_ld_wait16(y);
       }
+#pragma unroll
+      for (int c = 0; c < 16; ++c)
+        x[c] = __float_as_uint(__fmaf_rn(__uint_as_float(x[c]), f[0], __uint_as_float(y[c]) * f[1]));
+      if (row_ok && !dead) cw_store16(x, inv, out, part_o, c0);
+      __syncwarp();
     }
+    if (part.n > 0) {
+      tc_fence_before();
+      mbar_arrive_warp(&sh->o_empty);
+    }
+    if (!row_ok || dead) continue;
     if (odd) cw_add_odd<D, ACT>(p, w, part, q, o_col, share ? D / 2 : D, out, part_o);
     if (ACT == 2 && o_col == 0) {
       if (!w.whole) p.part_ml[prow] = make_float2(m, l);
@@ -863,9 +748,6 @@ __global__ void __launch_bounds__(kWideThreads, 1) cache_fwd_wide_kernel(const _
       mbar_init(&sh->s_full[s], 1);
       mbar_init(&sh->p_full[s], 4);
       mbar_init(&sh->o_full[s], 1);
-      mbar_init(&sh->o_empty[s], PAIR ? 8 : 4);
-    }
-    for (int s = 0; s < 2; ++s) {
       mbar_init(&sh->fix_ask[s], 1);
       mbar_init(&sh->fixed[s], 2);
     }
@@ -873,37 +755,28 @@ __global__ void __launch_bounds__(kWideThreads, 1) cache_fwd_wide_kernel(const _
       mbar_init(&sh->full[s], 1);
       mbar_init(&sh->empty[s], 1);
     }
+    mbar_init(&sh->o_empty, 8);
     mbar_init(&sh->drain, 1);
     sh->abort = 0;
     p.err[blockIdx.x] = kOk;
-    for (int i = 0; i < 32; ++i) sh->odd[i >> 4][i & 15] = 0;
+    for (int i = 0; i < 16; ++i) sh->odd[i] = 0;
     fence_mbar_init();
   }
   if (warp == 1) {
     tmem_alloc(&sh->tmem_base, 512);
     tmem_relinquish();
   }
-  CacheRange R[2];
-  if constexpr (PAIR) {
-    CacheRange one[1];
-    cache_ranges<kTile>(p, sh->range, kWideMinRange, one);
-    R[0] = R[1] = one[0];
-  } else {
-    cache_ranges<kTile>(p, sh->range, kWideMinRange, R);
-  }
+  const CacheRange R = cache_range<kTile>(p, &sh->range, kWideMinRange);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (threadIdx.x == 96) {
-    cache_open<kTile>(p, R[0]);
-    if constexpr (!PAIR) cache_open<kTile>(p, R[1]);
-  }
+  if (threadIdx.x == 96) cache_open<kTile>(p, R);
   const uint32_t tmem = sh->tmem_base;
   Fail fail{&sh->abort, p.err + blockIdx.x, p.wait_limit_ns};
   if (warp == 0) cw_producer<D, PAIR>(p, smem, sh, R, fail);
   else if (warp == 1) cw_mma<D, PAIR>(p, smem, sh, tmem, R, fail);
   else if (warp < 4) cw_fixer<D, PAIR>(p, smem, sh, R, fail);
-  else cw_consumer<D, ACT, PAIR>(p, sh, tmem, (warp - 4) >> 2, warp < 8 ? R[0] : R[1], fail);
+  else cw_consumer<D, ACT, PAIR>(p, sh, tmem, (warp - 4) >> 2, R, fail);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -926,7 +799,7 @@ static cudaError_t launch_cw(const CacheFwdParams& p, int grid, cudaStream_t str
   return cudaGetLastError();
 }
 
-// pairs: items of two 128-row tiles (the streams share their parts).
+// pairs: items of two 128-row tiles.
 template <int D>
 cudaError_t launch_cache_fwd_wide_d(const CacheFwdParams& p, int act, bool pairs, int grid, cudaStream_t stream) {
   if (act == 0) return pairs ? launch_cw<D, 0, true>(p, grid, stream) : launch_cw<D, 0, false>(p, grid, stream);
