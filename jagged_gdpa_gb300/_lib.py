@@ -9,7 +9,6 @@ import fails loudly -- there is no fallback implementation.
 from __future__ import annotations
 
 import ctypes
-import functools
 import os
 from typing import Optional
 
@@ -426,77 +425,54 @@ def jgdpa_bwd_shared_q(q, k, v, out, lse, dout, kv_offsets, act, scale: float, b
 
 
 # ------------------------------------------------- paged key/value cache (serving)
-def _on_device(fn):
-    """Runs a cache wrapper with its tensors' device as the current one."""
-    @functools.wraps(fn)
-    def call(*args, **kw):
-        first = args[0] if args else next(iter(kw.values()), None)
-        if isinstance(first, torch.Tensor) and first.is_cuda and first.device.index != torch.cuda.current_device():
-            with torch.cuda.device(first.device):
-                return fn(*args, **kw)
-        return fn(*args, **kw)
-    return call
+# These calls belong to a serving step, where some tens of microseconds of
+# Python per call would be what the step waits for: each wrapper first tests
+# everything in one pass, and names what is wrong (`_refuse_*`) only if a test fails.
+_i32, _f32, _bf16, _u8 = torch.int32, torch.float32, torch.bfloat16, torch.uint8
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _current_raw_stream(index: int) -> int:
+    if _raw_stream is not None:
+        return _raw_stream(index)
+    return torch.cuda.current_stream(index).cuda_stream
 
 
 class _Alloc:
-    """Memory for results and scratch of a call on `stream` (None: the current
-    stream, whose allocations need nothing more).  Scratch comes from the
-    stream's own pool, so that it is not handed out again before the call's
-    kernels have run; results are known to the current stream too."""
+    """Memory for results and scratch of a call on another stream than the
+    current one.  Scratch comes from that stream's own pool, so that it is not
+    handed out again before the call's kernels have run; results are known to
+    the current stream too."""
 
     def __init__(self, device, stream):
-        self.device = device
-        self.other = stream if stream is not None and stream != torch.cuda.current_stream(device) else None
+        self.device, self.stream = device, stream
 
     def __call__(self, shape, dtype, result=True):
-        if self.other is None:
-            return torch.empty(shape, dtype=dtype, device=self.device)
-        with torch.cuda.stream(self.other):
+        with torch.cuda.stream(self.stream):
             t = torch.empty(shape, dtype=dtype, device=self.device)
         if result:
             t.record_stream(torch.cuda.current_stream(self.device))
         return t
 
 
-def _need_cuda(t: torch.Tensor):
-    if not t.is_cuda:
-        raise ValueError("tensors passed to libjgdpa must be on a CUDA device")
+def _launch_on(stream, device):
+    """(cudaStream_t, allocator or None for torch's own) of a call."""
+    if stream is None:
+        return _current_raw_stream(device.index), None
+    if stream == torch.cuda.current_stream(device):
+        return stream.cuda_stream, None
+    return stream.cuda_stream, _Alloc(device, stream)
 
 
-def _check_cache(k_cache, v_cache):
-    """(num_pages, page_size, kv_heads, head_dim) of a cache whose pages are
-    contiguous (their distance may be any multiple of 8 elements)."""
-    if not isinstance(k_cache, torch.Tensor) or k_cache.dim() != 4:
-        raise ValueError("k_cache must be a bf16 tensor [num_pages, page_size, kv_heads, head_dim]")
-    _check(k_cache, "k_cache", torch.bfloat16, (None, None, None, None))
-    _check(v_cache, "v_cache", torch.bfloat16, k_cache.shape, k_cache.device)
-    n, page, heads, d = k_cache.shape
-    for t, name in ((k_cache, "k_cache"), (v_cache, "v_cache")):
-        if t.stride()[1:] != (heads * d, d, 1):
-            raise ValueError(f"{name}: the tokens, heads and columns of a page must be contiguous")
-        if n > 1 and (t.stride(0) < page * heads * d or t.stride(0) % 8):
-            raise ValueError(f"{name}: pages must not overlap and lie a multiple of 8 elements apart")
-    return n, page, heads, d
+def _on_other_device(fn, device, args, kw):
+    """Runs a wrapper again with its tensors' device as the current one."""
+    with torch.cuda.device(device):
+        return fn(*args, **kw)
 
 
-def _page_stride(t: torch.Tensor) -> int:
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2] * t.shape[3]
-
-
-def _row_stride(t: torch.Tensor, name: str) -> int:
-    """Elements between rows [heads][head_dim] of t (contiguous inside a row)."""
-    rows, heads, d = t.shape
-    if rows <= 1:
-        if rows and (t.stride(2) != 1 or (heads > 1 and t.stride(1) != d)):
-            raise ValueError(f"{name}: the heads and columns of a row must be contiguous")
-        return heads * d
-    if t.stride(2) != 1 or (heads > 1 and t.stride(1) != d) or t.stride(0) < heads * d or t.stride(0) % 8:
-        raise ValueError(f"{name}: rows must be contiguous inside and lie a multiple of 8 elements apart")
-    return t.stride(0)
-
-
-def _addr(t: Optional[torch.Tensor]):
-    return None if t is None else t.data_ptr()
+def _is(t, dtype, shape, index) -> bool:
+    """Whether t is a contiguous tensor of this dtype and shape on this CUDA device."""
+    return t.dtype is dtype and t.shape == shape and t.get_device() == index and t.is_contiguous()
 
 
 def _contiguous(**tensors):
@@ -505,18 +481,56 @@ def _contiguous(**tensors):
             raise ValueError(f"{name} must be contiguous")
 
 
+def _need_cuda(t: torch.Tensor):
+    if not t.is_cuda:
+        raise ValueError("tensors passed to libjgdpa must be on a CUDA device")
+
+
+def _page_stride(t: torch.Tensor, page: int, heads: int, d: int) -> int:
+    """Elements between the pages of a cache (any multiple of 8 from a page's
+    size on), or 0 if its pages are not contiguous inside or overlap."""
+    n, stride = t.shape[0], t.stride()
+    size = page * heads * d
+    if stride[1:] != (heads * d, d, 1) and any(
+            k > 1 and a != b for k, a, b in zip((page, heads, d), stride[1:], (heads * d, d, 1))):
+        return 0
+    if n <= 1:
+        return size
+    return stride[0] if stride[0] >= size and stride[0] % 8 == 0 else 0
+
+
+def _row_stride(t: torch.Tensor, heads: int, d: int) -> int:
+    """Elements between rows [heads][d] of t (any multiple of 8 from a row's
+    size on), or 0 if a row is not contiguous inside or rows overlap."""
+    stride = t.stride()
+    if t.numel() and (stride[2] != 1 or (heads > 1 and stride[1] != d)):
+        return 0
+    if t.shape[0] <= 1:
+        return heads * d
+    return stride[0] if stride[0] >= heads * d and stride[0] % 8 == 0 else 0
+
+
+def _refuse_cache(k_cache, v_cache):
+    if not isinstance(k_cache, torch.Tensor) or k_cache.dim() != 4:
+        raise ValueError("k_cache must be a bf16 tensor [num_pages, page_size, kv_heads, head_dim]")
+    _check(k_cache, "k_cache", torch.bfloat16, (None, None, None, None))
+    _check(v_cache, "v_cache", torch.bfloat16, k_cache.shape, k_cache.device)
+    for t, name in ((k_cache, "k_cache"), (v_cache, "v_cache")):
+        if not _page_stride(t, *t.shape[1:]):
+            raise ValueError(f"{name}: pages must be contiguous inside, must not overlap and lie a multiple of 8 "
+                             "elements apart")
+
+
+def _refuse_rows(t, name, heads, d):
+    if not _row_stride(t, heads, d):
+        raise ValueError(f"{name}: rows must be contiguous inside, must not overlap and lie a multiple of 8 elements apart")
+
+
 def jgdpa_cache_plan_workspace_bytes(lib=None) -> int:
     return int((lib or load()).jgdpa_cache_plan_workspace_bytes())
 
 
-@_on_device
-def jgdpa_cache_plan(ctx_lens, new_lens, held_pages, block_table, free_pages, free_count, page_size: int,
-                     total_new: int, workspace=None, stream=None, lib=None):
-    """Pages and slots for a step's tokens (jgdpa_cache_plan); returns (slots,
-    q_offsets, kv_lens, held_pages, free_count), the last two being the new
-    counts to pass to the next plan.  block_table and free_pages are updated in
-    place.  total_new: rows of slots, at least the sum of new_lens."""
-    lib = lib or load()
+def _refuse_plan(ctx_lens, new_lens, held_pages, block_table, free_pages, free_count, workspace):
     _check(ctx_lens, "ctx_lens", torch.int32, (None,))
     device, batch = ctx_lens.device, ctx_lens.shape[0]
     _check(new_lens, "new_lens", torch.int32, (batch,), device)
@@ -525,42 +539,97 @@ def jgdpa_cache_plan(ctx_lens, new_lens, held_pages, block_table, free_pages, fr
     _check(free_pages, "free_pages", torch.int32, (None,), device)
     _check(free_count, "free_count", torch.int32, (1,), device)
     _check_bytes(workspace, "workspace", device)
-    total_new = int(total_new)
-    if total_new < 0:
-        raise ValueError("total_new must not be negative")
     _contiguous(ctx_lens=ctx_lens, new_lens=new_lens, held_pages=held_pages, block_table=block_table,
                 free_pages=free_pages, workspace=workspace)
     _need_cuda(ctx_lens)
-    alloc = _Alloc(device, stream)
-    ws = alloc(jgdpa_cache_plan_workspace_bytes(lib), torch.uint8, result=False) if workspace is None else workspace
-    ints = alloc(total_new + 3 * batch + 2, torch.int32)
-    slots, q_offsets, kv_lens, held, count = ints.split((total_new, batch + 1, batch, batch, 1))
-    rc = lib.jgdpa_cache_plan(_addr(ctx_lens), _addr(new_lens), _addr(held_pages), batch, int(page_size),
-                              _addr(block_table), block_table.shape[1], _addr(free_pages), free_pages.shape[0],
-                              _addr(free_count), total_new, _addr(held), _addr(count), _addr(q_offsets),
-                              _addr(kv_lens), _addr(slots), _addr(ws), ws.numel(), _stream(stream))
-    _rc(rc, "jgdpa_cache_plan")
+
+
+def jgdpa_cache_plan(ctx_lens, new_lens, held_pages, block_table, free_pages, free_count, page_size: int,
+                     total_new: int, workspace=None, stream=None, lib=None):
+    """Pages and slots for a step's tokens (jgdpa_cache_plan); returns (slots,
+    q_offsets, kv_lens, held_pages, free_count), the last two being the new
+    counts to pass to the next plan.  block_table and free_pages are updated in
+    place.  total_new: rows of slots, at least the sum of new_lens."""
+    lib = lib or load()
+    try:
+        index, shape = ctx_lens.get_device(), ctx_lens.shape
+        batch, width = block_table.shape
+        pages = free_pages.shape[0]
+        ok = (index >= 0 and _is(ctx_lens, _i32, (batch,), index) and _is(new_lens, _i32, shape, index)
+              and _is(held_pages, _i32, shape, index) and _is(block_table, _i32, (batch, width), index)
+              and _is(free_pages, _i32, (pages,), index) and _is(free_count, _i32, (1,), index)
+              and (workspace is None or _is(workspace, _u8, (workspace.numel(),), index)))
+    except (AttributeError, ValueError, IndexError, TypeError):
+        ok = False
+    if not ok:
+        _refuse_plan(ctx_lens, new_lens, held_pages, block_table, free_pages, free_count, workspace)
+        raise ValueError("jgdpa_cache_plan: unusable tensors")
+    total_new = int(total_new)
+    if total_new < 0:
+        raise ValueError("total_new must not be negative")
+    if index != torch.cuda.current_device():
+        return _on_other_device(jgdpa_cache_plan, ctx_lens.device, (ctx_lens, new_lens, held_pages, block_table, free_pages,
+                                free_count, page_size, total_new, workspace, stream, lib), {})
+    raw, alloc = _launch_on(stream, ctx_lens.device)
+    # one allocation: 256 bytes of workspace (unless the caller has one), then the results
+    n = 64 + total_new + 3 * batch + 2
+    ints = torch.empty(n, dtype=_i32, device=ctx_lens.device) if alloc is None else alloc(n, _i32)
+    _, slots, q_offsets, kv_lens, held, count = torch.split_with_sizes(ints, (64, total_new, batch + 1, batch, batch, 1))
+    base = ints.data_ptr()
+    at = base + 256
+    off, kv = at + 4 * total_new, at + 4 * (total_new + batch + 1)
+    held_at = kv + 4 * batch
+    ws, ws_bytes = (base, 256) if workspace is None else (workspace.data_ptr(), workspace.numel())
+    rc = lib.jgdpa_cache_plan(ctx_lens.data_ptr(), new_lens.data_ptr(), held_pages.data_ptr(), batch, int(page_size),
+                              block_table.data_ptr(), width, free_pages.data_ptr(), pages, free_count.data_ptr(),
+                              total_new, held_at, held_at + 4 * batch, off, kv, at, ws, ws_bytes, raw)
+    if rc:
+        raise JgdpaError(rc, "jgdpa_cache_plan")
     return slots, q_offsets, kv_lens, held, count
 
 
-@_on_device
-def jgdpa_cache_append(k_new, v_new, slots, k_cache, v_cache, stream=None, lib=None):
-    """Writes rows of k_new / v_new [total_new, kv_heads, head_dim] (rows may be
-    slices of wider ones) to their slots; returns (k_cache, v_cache)."""
-    lib = lib or load()
-    n, page, heads, d = _check_cache(k_cache, v_cache)
+def _refuse_append(k_new, v_new, slots, k_cache, v_cache):
+    _refuse_cache(k_cache, v_cache)
+    heads, d = k_cache.shape[2:]
     device = k_cache.device
     _check(k_new, "k_new", torch.bfloat16, (None, heads, d), device)
     rows = k_new.shape[0]
     _check(v_new, "v_new", torch.bfloat16, (rows, heads, d), device)
     _check(slots, "slots", torch.int32, (rows,), device)
-    ks, vs = _row_stride(k_new, "k_new"), _row_stride(v_new, "v_new")
+    _refuse_rows(k_new, "k_new", heads, d)
+    _refuse_rows(v_new, "v_new", heads, d)
     _contiguous(slots=slots)
     _need_cuda(k_cache)
-    rc = lib.jgdpa_cache_append(_addr(k_new), _addr(v_new), ks, vs, _addr(slots), rows, _addr(k_cache),
-                                _addr(v_cache), _page_stride(k_cache), _page_stride(v_cache), n, page, heads, d,
-                                _stream(stream))
-    _rc(rc, "jgdpa_cache_append")
+
+
+def jgdpa_cache_append(k_new, v_new, slots, k_cache, v_cache, stream=None, lib=None):
+    """Writes rows of k_new / v_new [total_new, kv_heads, head_dim] (rows may be
+    slices of wider ones) to their slots; returns (k_cache, v_cache)."""
+    lib = lib or load()
+    ks = vs = kps = vps = 0
+    try:
+        index = k_cache.get_device()
+        n, page, heads, d = k_cache.shape
+        rows = k_new.shape[0]
+        shape = (rows, heads, d)
+        if (index >= 0 and k_cache.dtype is _bf16 and v_cache.dtype is _bf16 and v_cache.shape == k_cache.shape
+                and v_cache.get_device() == index and k_new.dtype is _bf16 and v_new.dtype is _bf16
+                and k_new.shape == shape and v_new.shape == shape and k_new.get_device() == index
+                and v_new.get_device() == index and _is(slots, _i32, (rows,), index)):
+            kps, vps = _page_stride(k_cache, page, heads, d), _page_stride(v_cache, page, heads, d)
+            ks, vs = _row_stride(k_new, heads, d), _row_stride(v_new, heads, d)
+    except (AttributeError, ValueError, IndexError, TypeError):
+        pass
+    if not (ks and vs and kps and vps):
+        _refuse_append(k_new, v_new, slots, k_cache, v_cache)
+        raise ValueError("jgdpa_cache_append: unusable tensors")
+    if index != torch.cuda.current_device():
+        return _on_other_device(jgdpa_cache_append, k_cache.device, (k_new, v_new, slots, k_cache, v_cache, stream, lib), {})
+    rc = lib.jgdpa_cache_append(k_new.data_ptr(), v_new.data_ptr(), ks, vs, slots.data_ptr(), rows, k_cache.data_ptr(),
+                                v_cache.data_ptr(), kps, vps, n, page, heads, d,
+                                _current_raw_stream(index) if stream is None else stream.cuda_stream)
+    if rc:
+        raise JgdpaError(rc, "jgdpa_cache_append")
     return k_cache, v_cache
 
 
@@ -568,16 +637,10 @@ def jgdpa_cache_fwd_workspace_bytes(heads: int, kv_heads: int, head_dim: int, ma
     return int((lib or load()).jgdpa_cache_fwd_workspace_bytes(heads, kv_heads, head_dim, max_q))
 
 
-@_on_device
-def jgdpa_cache_fwd(q, k_cache, v_cache, block_table, q_offsets, kv_lens, act, scale: float, max_q: int,
-                    bias_table=None, window: int = 0, tree_mask=None, depths=None, out=None, lse=None,
-                    workspace=None, stream=None, lib=None):
-    """Attention from new tokens q [total_q, heads, head_dim] over each
-    request's pages (jgdpa_cache_fwd); returns (out, lse) with lse None unless
-    act == 'softmax'.  max_q: an upper bound of the new tokens per request."""
-    lib = lib or load()
-    n, page, kv_heads, d = _check_cache(k_cache, v_cache)
-    device = k_cache.device
+def _refuse_fwd(q, k_cache, v_cache, block_table, q_offsets, kv_lens, softmax, bias_table, tree_mask, depths, out, lse,
+                workspace):
+    _refuse_cache(k_cache, v_cache)
+    d, device = k_cache.shape[3], k_cache.device
     _check(q, "q", torch.bfloat16, (None, None, d), device)
     total_q, heads = q.shape[0], q.shape[1]
     _check(kv_lens, "kv_lens", torch.int32, (None,), device)
@@ -587,32 +650,88 @@ def jgdpa_cache_fwd(q, k_cache, v_cache, block_table, q_offsets, kv_lens, act, s
     _check(bias_table, "bias_table", torch.float32, (heads, None), device, optional=True)
     _check(tree_mask, "tree_mask", torch.int32, (total_q, None), device, optional=True)
     _check(depths, "depths", torch.int32, (total_q,), device, optional=True)
-    a = _act(act)
-    softmax = a == ACT["softmax"]
     _check(out, "out", torch.bfloat16, (total_q, heads, d), device, optional=True)
     if lse is not None and not softmax:
         raise ValueError("lse is written in softmax mode only; pass None")
     _check(lse, "lse", torch.float32, (heads, total_q), device, optional=True)
     _check_bytes(workspace, "workspace", device)
-    qs = _row_stride(q, "q")
+    _refuse_rows(q, "q", heads, d)
     _contiguous(block_table=block_table, q_offsets=q_offsets, kv_lens=kv_lens, bias_table=bias_table,
                 tree_mask=tree_mask, depths=depths, out=out, lse=lse, workspace=workspace)
     _need_cuda(k_cache)
+
+
+def jgdpa_cache_fwd(q, k_cache, v_cache, block_table, q_offsets, kv_lens, act, scale: float, max_q: int,
+                    bias_table=None, window: int = 0, tree_mask=None, depths=None, out=None, lse=None,
+                    workspace=None, stream=None, lib=None):
+    """Attention from new tokens q [total_q, heads, head_dim] over each
+    request's pages (jgdpa_cache_fwd); returns (out, lse) with lse None unless
+    act == 'softmax'.  max_q: an upper bound of the new tokens per request."""
+    lib = lib or load()
+    a = _act(act)
+    softmax = a == 2
+    qs = kps = vps = 0
+    bias = mask = depth = None
+    bias_len = words = 0
+    try:
+        index = k_cache.get_device()
+        n, page, kv_heads, d = k_cache.shape
+        total_q, heads, _ = shape = q.shape
+        batch, width = block_table.shape
+        ok = (index >= 0 and k_cache.dtype is _bf16 and v_cache.dtype is _bf16 and v_cache.shape == k_cache.shape
+              and v_cache.get_device() == index and q.dtype is _bf16 and shape[2] == d and q.get_device() == index
+              and _is(block_table, _i32, (batch, width), index) and _is(q_offsets, _i32, (batch + 1,), index)
+              and _is(kv_lens, _i32, (batch,), index))
+        if ok and bias_table is not None:
+            bias, bias_len = bias_table.data_ptr(), bias_table.shape[1]
+            ok = _is(bias_table, _f32, (heads, bias_len), index)
+        if ok and tree_mask is not None:
+            mask, words = tree_mask.data_ptr(), tree_mask.shape[1]
+            ok = _is(tree_mask, _i32, (total_q, words), index)
+        if ok and depths is not None:
+            depth = depths.data_ptr()
+            ok = _is(depths, _i32, (total_q,), index)
+        if ok and out is not None:
+            ok = _is(out, _bf16, shape, index)
+        if ok and lse is not None:
+            ok = softmax and _is(lse, _f32, (heads, total_q), index)
+        if ok and workspace is not None:
+            ok = _is(workspace, _u8, (workspace.numel(),), index)
+        if ok:
+            kps, vps = _page_stride(k_cache, page, kv_heads, d), _page_stride(v_cache, page, kv_heads, d)
+            qs = _row_stride(q, heads, d)
+    except (AttributeError, ValueError, IndexError, TypeError):
+        pass
+    if not (qs and kps and vps):
+        _refuse_fwd(q, k_cache, v_cache, block_table, q_offsets, kv_lens, softmax, bias_table, tree_mask, depths, out, lse,
+                    workspace)
+        raise ValueError("jgdpa_cache_fwd: unusable tensors")
     max_q, window = int(max_q), int(window)
-    alloc = _Alloc(device, stream)
-    if out is None:
-        out = alloc((total_q, heads, d), torch.bfloat16)
-    if lse is None and softmax:
-        lse = alloc((heads, total_q), torch.float32)
-    if workspace is None:
-        nbytes = lib.jgdpa_cache_fwd_workspace_bytes(heads, kv_heads, d, max_q)
-        workspace = alloc(max(nbytes, 256), torch.uint8, result=False)
-    rc = lib.jgdpa_cache_fwd(_addr(q), qs, _addr(k_cache), _addr(v_cache), _page_stride(k_cache),
-                             _page_stride(v_cache), n, page, _addr(block_table), block_table.shape[1],
-                             _addr(q_offsets), _addr(kv_lens), batch, total_q, max_q, heads, kv_heads, d, a,
-                             float(scale), _addr(bias_table), 0 if bias_table is None else bias_table.shape[1],
-                             window, _addr(tree_mask), 0 if tree_mask is None else tree_mask.shape[1],
-                             _addr(depths), _addr(out), _addr(lse), _addr(workspace), workspace.numel(),
-                             _stream(stream))
-    _rc(rc, "jgdpa_cache_fwd")
+    if index != torch.cuda.current_device():
+        return _on_other_device(jgdpa_cache_fwd, k_cache.device, (q, k_cache, v_cache, block_table, q_offsets, kv_lens, act,
+                                scale, max_q, bias_table, window, tree_mask, depths, out, lse, workspace, stream, lib), {})
+    device = k_cache.device
+    raw, alloc = _launch_on(stream, device)
+    if alloc is None:
+        if out is None:
+            out = torch.empty(shape, dtype=_bf16, device=device)
+        if softmax and lse is None:
+            lse = torch.empty((heads, total_q), dtype=_f32, device=device)
+        if workspace is None:
+            workspace = torch.empty(max(256, lib.jgdpa_cache_fwd_workspace_bytes(heads, kv_heads, d, max_q)), dtype=_u8,
+                                    device=device)
+    else:
+        if out is None:
+            out = alloc(shape, _bf16)
+        if softmax and lse is None:
+            lse = alloc((heads, total_q), _f32)
+        if workspace is None:
+            workspace = alloc(max(256, lib.jgdpa_cache_fwd_workspace_bytes(heads, kv_heads, d, max_q)), _u8, result=False)
+    rc = lib.jgdpa_cache_fwd(q.data_ptr(), qs, k_cache.data_ptr(), v_cache.data_ptr(), kps, vps, n, page,
+                             block_table.data_ptr(), width, q_offsets.data_ptr(), kv_lens.data_ptr(), batch, total_q,
+                             max_q, heads, kv_heads, d, a, float(scale), bias, bias_len, window, mask, words, depth,
+                             out.data_ptr(), lse.data_ptr() if lse is not None else None, workspace.data_ptr(),
+                             workspace.numel(), raw)
+    if rc:
+        raise JgdpaError(rc, "jgdpa_cache_fwd")
     return out, lse

@@ -184,7 +184,7 @@ def test_workspace_query(jg):
     ("q", lambda t: t.transpose(0, 1).contiguous().transpose(0, 1), "contiguous inside"),
     ("k_cache", lambda t: t[0], "k_cache must be"),
     ("v_cache", lambda t: t[:-1], "v_cache must have shape"),
-    ("k_cache", lambda t: t.transpose(1, 2).contiguous().transpose(1, 2), "must be contiguous"),
+    ("k_cache", lambda t: t.transpose(1, 2).contiguous().transpose(1, 2), "contiguous inside"),
     ("v_cache", lambda t: t[:1].expand(t.shape), "must not overlap"),
     ("block_table", lambda t: t.long(), "block_table must have dtype"),
     ("block_table", lambda t: t[:1], "block_table must have shape"),
