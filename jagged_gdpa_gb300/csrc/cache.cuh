@@ -263,6 +263,28 @@ struct CacheWalk {
   }
 };
 
+// The attention and joining kernels are launched so that a kernel's blocks may
+// be set up while the kernel before it on the stream still runs (programmatic
+// dependent launch).  Each block waits for that kernel's end before it touches
+// global memory, and none ends without having waited.
+__device__ __forceinline__ void cache_wait_before() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void cache_let_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+template <typename... Params, typename... Args>
+inline cudaError_t cache_launch(void (*kern)(Params...), dim3 grid, int threads, int smem, cudaStream_t stream,
+                                const Args&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads, 1, 1);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
 // The range that a place on the line lies in.
 __device__ __forceinline__ int64_t cache_range_of(int64_t at, int64_t per) {
   return (at | per) <= 0xFFFFFFFFll ? static_cast<uint32_t>(at) / static_cast<uint32_t>(per) : at / per;
@@ -328,7 +350,7 @@ __device__ __forceinline__ uint32_t cc_ones(int n) { return n >= 32 ? 0xFFFFFFFF
 
 // Which of the keys key0 .. key0 + 31 a row sees by length and mask (bit c:
 // key0 + c), whatever the window.
-__device__ __forceinline__ uint32_t cc_vis32(const CacheFwdParams& p, const CacheReq& r, const CcRow& q, int key0) {
+static __device__ __noinline__ uint32_t cc_vis32(const CacheFwdParams& p, CacheReq r, CcRow q, int key0) {
   if (q.t < 0) return 0u;
   if (p.mask == nullptr) return cc_ones(min(r.L, r.C + q.t + 1) - key0);
   const int u0 = key0 - r.C;

@@ -19,7 +19,7 @@ cudaError_t launch_cache_fwd_d(const CacheFwdParams& p, int act, int grid, cudaS
 template <int D>
 cudaError_t launch_cache_fwd_wide_d(const CacheFwdParams& p, int act, bool pairs, int grid, cudaStream_t stream);
 template <int D>
-cudaError_t launch_cache_join_d(const CacheFwdParams& p, int act, int n_ctas, int item_rows, cudaStream_t stream);
+cudaError_t launch_cache_join_d(const CacheFwdParams& p, int act, int n_ctas, int tile_rows, cudaStream_t stream);
 cudaError_t launch_cache_plan(const CachePlanParams& p, int sms, cudaStream_t stream);
 cudaError_t launch_cache_append(const CacheAppendParams& p, cudaStream_t stream);
 }  // namespace jg
@@ -320,12 +320,12 @@ jgdpa_status jgdpa_cache_fwd(const void* q, int64_t q_stride, const void* k_cach
   p.item_cost = L.wide ? (L.pairs ? 10 : 8) : 4;
   p.scale = act == JGDPA_ACT_SOFTMAX ? scale * jg::kLog2e : scale;
   p.wait_limit_ns = jg::host_wait_limit_ns();
-  const int item_rows = L.heads > 1 ? L.rows * L.heads : static_cast<int>(std::min<int64_t>(L.rows, max_rows));
+  const int tile_rows = static_cast<int>(std::min<int64_t>(L.rows, max_rows));
   auto launch = [&](auto dim) -> cudaError_t {
     constexpr int D = decltype(dim)::value;
     cudaError_t e = L.wide ? jg::launch_cache_fwd_wide_d<D>(p, act, L.pairs, L.grid, stream)
                            : jg::launch_cache_fwd_d<D>(p, act, L.grid, stream);
-    return e != cudaSuccess ? e : jg::launch_cache_join_d<D>(p, act, L.grid, item_rows, stream);
+    return e != cudaSuccess ? e : jg::launch_cache_join_d<D>(p, act, L.grid, tile_rows, stream);
   };
   JG_CUDA(head_dim == 128  ? launch(std::integral_constant<int, 128>{})
           : head_dim == 64 ? launch(std::integral_constant<int, 64>{})

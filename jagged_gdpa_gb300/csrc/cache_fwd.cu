@@ -146,9 +146,14 @@ __device__ void cc_consumer(const CacheFwdParams& p, uint8_t* smem, CcShared<MT,
   const int pr = min(1 << p.page_shift, kCKeys);
   const uint32_t base = smem_u32(smem);
   // this warp's 16 keys: piece addresses for ldmatrix (the four 8x8 blocks of
-  // a load are keys 0-7 / 8-15 by 16-byte piece for K, and transposed for V)
-  const int kn = 16 * kw + (lane & 7) + ((lane & 16) ? 8 : 0), kc = (lane >> 3) & 1;
-  const int vn = 16 * kw + (lane & 7) + ((lane & 8) ? 8 : 0), vc = lane >> 4;
+  // a load are keys 0-7 / 8-15 by 16-byte piece for K, and transposed for V);
+  // the lane's part of an address is fixed, a piece comes in by exclusive or
+  const int half = W >= 64 ? pr * 128 : 0;  // bytes of a box's column half
+  const uint32_t kl = cc_offset<W>(16 * kw + (lane & 7) + ((lane & 16) ? 8 : 0), (lane >> 3) & 1, pr);
+  const uint32_t vl = cc_offset<W>(16 * kw + (lane & 7) + ((lane & 8) ? 8 : 0), lane >> 4, pr);
+  auto piece = [&](uint32_t at, int c) {  // of the even piece c
+    return (at ^ ((c & (W >= 64 ? 6 : 2)) << 4)) + (W >= 64 && c >= 8 ? half : 0);
+  };
   const int reach = (p.bias_len - 1) / 2;
   uint32_t it = 0;
   bool dead = false;
@@ -222,21 +227,45 @@ __device__ void cc_consumer(const CacheFwdParams& p, uint8_t* smem, CcShared<MT,
         const int last = key0 + 15;
         const bool plain = last < r.C && (p.window <= 0 || pos_max - key0 < p.window);
         const bool far = p.bias_len == 0 || (last < r.C && pos_min - last >= reach);
-        uint32_t see[2] = {0u, 0u};
+        uint32_t see[2] = {0xFFFFu, 0xFFFFu}, keep[2] = {0xFFFFFFFFu, 0xFFFFFFFFu};
+        bool odd = false;
         if (!plain) {
-#pragma unroll
+          // Some rows do not see some of these keys, and 0 * NaN = NaN: rows of
+          // V past the request's end (whatever the page held) count as zeros
+          // (`keep`), and where others hold an infinity or NaN (`odd`) those
+          // are left out of the product and added to the rows that see them.
+#pragma unroll 1
           for (int h = 0; h < 2; ++h) {
-            see[h] = cc_vis32(p, r, rows[h], key0);
+            uint32_t bits = cc_vis32(p, r, h == 0 ? rows[0] : rows[1], key0);
             if (p.window > 0) {
               uint32_t near = 0;
-#pragma unroll
+#pragma unroll 1
               for (int c = 0; c < 4; ++c) {
                 const int col = 8 * (c >> 1) + 2 * (lane & 3) + (c & 1);
-                near |= (cc_near(p, rows[h].pos, cc_pos(p, r, key0 + col)) ? 1u : 0u) << col;
+                near |= (cc_near(p, h == 0 ? rows[0].pos : rows[1].pos, cc_pos(p, r, key0 + col)) ? 1u : 0u) << col;
               }
-              see[h] &= near;  // (only this lane's columns are kept)
+              bits &= near;  // (only this lane's columns are kept)
+            }
+            if (h == 0) see[0] = bits;
+            else see[1] = bits;
+          }
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const int j = key0 + 8 * i + 2 * (lane & 3);
+            keep[i] = j + 1 < r.L ? 0xFFFFFFFFu : (j < r.L ? 0xFFFFu : 0u);
+          }
+          const __nv_bfloat162 zero = __float2bfloat162_rn(0.f);
+          __nv_bfloat162 sum = zero;  // of 0 * v
+          if (key0 + (lane & 15) < r.L) {
+#pragma unroll 1
+            for (int c = lane >> 4; c < W / 8; c += 2) {
+              uint32_t x[4];
+              ld_shared_v4(vb + cc_offset<W>(16 * kw + (lane & 15), c, pr), x[0], x[1], x[2], x[3]);
+#pragma unroll
+              for (int e = 0; e < 4; ++e) sum = __hfma2(*reinterpret_cast<__nv_bfloat162*>(&x[e]), zero, sum);
             }
           }
+          odd = __any_sync(0xffffffffu, !(__low2float(sum) == 0.f && __high2float(sum) == 0.f));
         }
 #pragma unroll
         for (int hh = 0; hh < HP; ++hh) {
@@ -248,7 +277,7 @@ __device__ void cc_consumer(const CacheFwdParams& p, uint8_t* smem, CcShared<MT,
 #pragma unroll
           for (int ks = 0; ks < KS; ++ks) {
             uint32_t b[4];
-            ldsm4(kb + cc_offset<W>(kn, hh * (D / 8) + 2 * ks + kc, pr), b);
+            ldsm4(piece(kb + kl, hh * (D / 8) + 2 * ks), b);
             mma16816(s[0], qa[hh][ks], b[0], b[1]);
             mma16816(s[1], qa[hh][ks], b[2], b[3]);
           }
@@ -318,68 +347,46 @@ __device__ void cc_consumer(const CacheFwdParams& p, uint8_t* smem, CcShared<MT,
           // P rounds to bf16 as the A operand (half a step, 2^-8 of each weight at most)
           uint32_t pa[4] = {pack_bf16(pv[0][0], pv[0][1]), pack_bf16(pv[0][2], pv[0][3]), pack_bf16(pv[1][0], pv[1][1]),
                             pack_bf16(pv[1][2], pv[1][3])};
-          if (plain) {
 #pragma unroll
-            for (int n2 = 0; n2 < NT / 2; ++n2) {
-              uint32_t b[4];
-              ldsm4_t(vb + cc_offset<W>(vn, hh * (D / 8) + 2 * n2 + vc, pr), b);
-              mma16816(o[hh][2 * n2], pa, b[0], b[1]);
-              mma16816(o[hh][2 * n2 + 1], pa, b[2], b[3]);
+          for (int n2 = 0; n2 < NT / 2; ++n2) {
+            uint32_t b[4];
+            ldsm4_t(piece(vb + vl, hh * (D / 8) + 2 * n2), b);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) b[e] &= keep[e & 1];
+            if (odd) {
+#pragma unroll
+              for (int e = 0; e < 4; ++e) b[e] &= ~cc_nonfinite(b[e]);
             }
-          } else {
-            // Some rows do not see some of these keys, and 0 * NaN = NaN: rows
-            // of V past the request's end (whatever the page held) count as
-            // zeros, and infinities or NaN of the others are left out of the
-            // product and added below to the rows that see them.
-            uint32_t keep[2];
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              const int j = key0 + 8 * i + 2 * (lane & 3);
-              keep[i] = j + 1 < r.L ? 0xFFFFFFFFu : (j < r.L ? 0xFFFFu : 0u);
-            }
-            bool odd = false;
-#pragma unroll
-            for (int n2 = 0; n2 < NT / 2; ++n2) {
-              uint32_t b[4];
-              ldsm4_t(vb + cc_offset<W>(vn, hh * (D / 8) + 2 * n2 + vc, pr), b);
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                b[e] &= keep[e & 1];
-                const uint32_t bad = cc_nonfinite(b[e]);
-                odd = odd || bad != 0;
-                b[e] &= ~bad;
-              }
-              mma16816(o[hh][2 * n2], pa, b[0], b[1]);
-              mma16816(o[hh][2 * n2 + 1], pa, b[2], b[3]);
-            }
-            if (__any_sync(0xffffffffu, odd)) {
+            mma16816(o[hh][2 * n2], pa, b[0], b[1]);
+            mma16816(o[hh][2 * n2 + 1], pa, b[2], b[3]);
+          }
+          if (odd) {
 #pragma unroll 1
-              for (int kk = 0; kk < 16 && key0 + kk < r.L; ++kk) {
-                // the lane with this key's weights for the same rows, and what the rows see
-                const int from = (lane & ~3) | ((kk & 7) >> 1);
-                const uint32_t see0 = __shfl_sync(0xffffffffu, see[0], from) >> kk, see1 = __shfl_sync(0xffffffffu, see[1], from) >> kk;
-                const float w0 = __shfl_sync(0xffffffffu, kk < 8 ? ((kk & 1) ? pv[0][1] : pv[0][0])
-                                                                 : ((kk & 1) ? pv[1][1] : pv[1][0]), from);
-                const float w1 = __shfl_sync(0xffffffffu, kk < 8 ? ((kk & 1) ? pv[0][3] : pv[0][2])
-                                                                 : ((kk & 1) ? pv[1][3] : pv[1][2]), from);
+            for (int kk = 0; kk < 16 && key0 + kk < r.L; ++kk) {
+              // the lane with this key's weights for the same rows, and what the rows see
+              const int from = (lane & ~3) | ((kk & 7) >> 1);
+              const uint32_t see0 = __shfl_sync(0xffffffffu, see[0], from) >> kk, see1 = __shfl_sync(0xffffffffu, see[1], from) >> kk;
+              const float w0 = __shfl_sync(0xffffffffu, kk < 8 ? ((kk & 1) ? pv[0][1] : pv[0][0])
+                                                               : ((kk & 1) ? pv[1][1] : pv[1][0]), from);
+              const float w1 = __shfl_sync(0xffffffffu, kk < 8 ? ((kk & 1) ? pv[0][3] : pv[0][2])
+                                                               : ((kk & 1) ? pv[1][3] : pv[1][2]), from);
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                  uint32_t v;
-                  asm volatile("ld.shared.b32 %0, [%1];"
-                               : "=r"(v)
-                               : "r"(vb + cc_offset<W>(16 * kw + kk, hh * (D / 8) + nt, pr) + 4 * (lane & 3))
-                               : "memory");
-                  v &= cc_nonfinite(v);
-                  if (v == 0) continue;
-                  const float x = __uint_as_float(v << 16), y = __uint_as_float(v & 0xFFFF0000u);
-                  if (see0 & 1) {
-                    if (x != 0.f) o[hh][nt][0] += w0 * x;
-                    if (y != 0.f) o[hh][nt][1] += w0 * y;
-                  }
-                  if (see1 & 1) {
-                    if (x != 0.f) o[hh][nt][2] += w1 * x;
-                    if (y != 0.f) o[hh][nt][3] += w1 * y;
-                  }
+              for (int nt = 0; nt < NT; ++nt) {
+                uint32_t v;
+                asm volatile("ld.shared.b32 %0, [%1];"
+                             : "=r"(v)
+                             : "r"(vb + cc_offset<W>(16 * kw + kk, hh * (D / 8) + nt, pr) + 4 * (lane & 3))
+                             : "memory");
+                v &= cc_nonfinite(v);
+                if (v == 0) continue;
+                const float x = __uint_as_float(v << 16), y = __uint_as_float(v & 0xFFFF0000u);
+                if (see0 & 1) {
+                  if (x != 0.f) o[hh][nt][0] += w0 * x;
+                  if (y != 0.f) o[hh][nt][1] += w0 * y;
+                }
+                if (see1 & 1) {
+                  if (x != 0.f) o[hh][nt][2] += w1 * x;
+                  if (y != 0.f) o[hh][nt][3] += w1 * y;
                 }
               }
             }
@@ -474,16 +481,17 @@ __global__ void __launch_bounds__((CcCfg<D * HP, MT, HP>::kThreads), (CcCfg<D * 
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   CcShared<MT, HP>* sh = reinterpret_cast<CcShared<MT, HP>*>(smem + C::kBarOff);
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  cache_let_next();
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::kStages; ++s) {
       mbar_init(&sh->full[s], 1);
       mbar_init(&sh->empty[s], C::kWarps);
     }
     sh->abort = 0;
-    p.err[blockIdx.x] = kOk;
     fence_mbar_init();
   }
+  cache_wait_before();
+  if (threadIdx.x == 0) p.err[blockIdx.x] = kOk;
   const CacheRange R = cache_range<kCKeys>(p, &sh->range, kCMinRange);
   if (threadIdx.x == (C::kWarps - 1) * 32) cache_open<kCKeys>(p, R);
   Fail fail{&sh->abort, p.err + blockIdx.x, p.wait_limit_ns};
@@ -493,18 +501,20 @@ __global__ void __launch_bounds__((CcCfg<D * HP, MT, HP>::kThreads), (CcCfg<D * 
 
 // ------------------------------------------------------------------ joining
 // Joins the parts of the items that range borders cut, and the CTAs' status
-// words.  Block (i, y): border i + 1, rows 2 y and 2 y + 1 of the item; four
-// warps share a row's parts (every fourth part each, then the four sums in
+// words.  Block (i, y): border i + 1, rows 2 y and 2 y + 1 of the item, whose
+// heads have at most tile_rows live rows each; four warps share a row's parts (every fourth part each, then the four sums in
 // order: the same bits on every run).
 constexpr int kJoinRows = 2;
 
 template <int D, bool SOFTMAX>
-__global__ void __launch_bounds__(kJoinRows * 128) cache_join_kernel(const __grid_constant__ CacheFwdParams p, int n_ctas) {
+__global__ void __launch_bounds__(kJoinRows * 128) cache_join_kernel(const __grid_constant__ CacheFwdParams p, int n_ctas,
+                                                                     int tile_rows) {
   constexpr int V = D / 32;
   __shared__ int worst[kJoinRows * 4];
   __shared__ float sums[kJoinRows][4][D];
   __shared__ float2 ml[kJoinRows][4];
-  asm volatile("griddepcontrol.wait;" ::: "memory");  // every block waits: none may end before the attention has
+  cache_let_next();
+  cache_wait_before();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   if (blockIdx.x == 0 && blockIdx.y == 0) {
     int e = kOk;
@@ -522,15 +532,16 @@ __global__ void __launch_bounds__(kJoinRows * 128) cache_join_kernel(const __gri
   const CacheJoin j = p.join[border];
   if (!j.valid) return;
   const int q0 = __ldg(p.q_off + j.b), T = __ldg(p.q_off + j.b + 1) - q0;
-  const int R = p.rows_per_tile, row = kJoinRows * blockIdx.y + (warp >> 2), quarter = warp & 3;
-  const int hh = row / R, lr = row - hh * R;  // head of the item's, row of the tile
+  const int R = p.rows_per_tile, quarter = warp & 3;
+  const int row = kJoinRows * blockIdx.y + (warp >> 2);
+  const int hh = row / tile_rows, lr = row - hh * tile_rows;  // head of the item's, row of its tile
   const int64_t flat = static_cast<int64_t>(j.rt) * R + lr;
   const bool live = hh < p.heads_per_item && flat < static_cast<int64_t>(T) * p.group;
   // (the first range that holds one of the item's tiles, the last)
   const int c0 = static_cast<int>(cache_range_of(j.t0 + p.item_cost, j.per)), c1 = static_cast<int>(cache_range_of(j.t1 - 1, j.per));
   // range c's part lies in its first slot when the range starts inside the item (or at its start)
   auto row_of = [&](int c) {
-    return (2 * static_cast<int64_t>(c) + (c * j.per < j.t0 ? 1 : 0)) * (p.heads_per_item * R) + row;
+    return (2 * static_cast<int64_t>(c) + (c * j.per < j.t0 ? 1 : 0)) * (p.heads_per_item * R) + hh * R + lr;
   };
   float M = -INFINITY, L = 0.f;
   float acc[V];
@@ -594,8 +605,7 @@ static cudaError_t launch_cc(const CacheFwdParams& p, int grid, cudaStream_t str
   static DeviceFlags attr_set = {};
   cudaError_t e = smem_attr_once(kern, C::kSmemBytes, attr_set);
   if (e != cudaSuccess) return e;
-  kern<<<grid, C::kThreads, C::kSmemBytes, stream>>>(p);
-  return cudaGetLastError();
+  return cache_launch(kern, dim3(grid), C::kThreads, C::kSmemBytes, stream, p);
 }
 
 template <int D, int ACT>
@@ -615,21 +625,11 @@ cudaError_t launch_cache_fwd_d(const CacheFwdParams& p, int act, int grid, cudaS
   return launch_cc_act<D, 2>(p, grid, stream);
 }
 
-// Launched so that its blocks may be set up while the attention still runs
-// (programmatic dependent launch); they wait for its end before they read.
 template <int D>
-cudaError_t launch_cache_join_d(const CacheFwdParams& p, int act, int n_ctas, int item_rows, cudaStream_t stream) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(n_ctas > 1 ? n_ctas - 1 : 1, (item_rows + kJoinRows - 1) / kJoinRows, 1);
-  cfg.blockDim = dim3(kJoinRows * 128, 1, 1);
-  cfg.stream = stream;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  return act == 2 ? cudaLaunchKernelEx(&cfg, cache_join_kernel<D, true>, p, n_ctas)
-                  : cudaLaunchKernelEx(&cfg, cache_join_kernel<D, false>, p, n_ctas);
+cudaError_t launch_cache_join_d(const CacheFwdParams& p, int act, int n_ctas, int tile_rows, cudaStream_t stream) {
+  const dim3 grid(n_ctas > 1 ? n_ctas - 1 : 1, (p.heads_per_item * tile_rows + kJoinRows - 1) / kJoinRows, 1);
+  return cache_launch(act == 2 ? cache_join_kernel<D, true> : cache_join_kernel<D, false>, grid, kJoinRows * 128, 0, stream,
+                      p, n_ctas, tile_rows);
 }
 
 template cudaError_t launch_cache_fwd_d<JGDPA_HEAD_DIM>(const CacheFwdParams&, int, int, cudaStream_t);

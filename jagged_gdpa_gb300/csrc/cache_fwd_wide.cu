@@ -740,7 +740,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) cache_fwd_wide_kernel(const _
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   CwShared* sh = reinterpret_cast<CwShared*>(smem + C::kBarOff);
   const int warp = threadIdx.x >> 5;
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  cache_let_next();
   if (threadIdx.x == 0) {
     for (int s = 0; s < 2; ++s) {
       mbar_init(&sh->q_full[s], 1);
@@ -758,7 +758,6 @@ __global__ void __launch_bounds__(kWideThreads, 1) cache_fwd_wide_kernel(const _
     mbar_init(&sh->o_empty, 8);
     mbar_init(&sh->drain, 1);
     sh->abort = 0;
-    p.err[blockIdx.x] = kOk;
     for (int i = 0; i < 16; ++i) sh->odd[i] = 0;
     fence_mbar_init();
   }
@@ -766,6 +765,8 @@ __global__ void __launch_bounds__(kWideThreads, 1) cache_fwd_wide_kernel(const _
     tmem_alloc(&sh->tmem_base, 512);
     tmem_relinquish();
   }
+  cache_wait_before();
+  if (threadIdx.x == 0) p.err[blockIdx.x] = kOk;
   const CacheRange R = cache_range<kTile>(p, &sh->range, kWideMinRange);
   tc_fence_before();
   __syncthreads();
@@ -795,8 +796,7 @@ static cudaError_t launch_cw(const CacheFwdParams& p, int grid, cudaStream_t str
   static DeviceFlags attr_set = {};
   cudaError_t e = smem_attr_once(kern, kSmem, attr_set);
   if (e != cudaSuccess) return e;
-  kern<<<grid, kWideThreads, kSmem, stream>>>(p);
-  return cudaGetLastError();
+  return cache_launch(kern, dim3(grid), kWideThreads, kSmem, stream, p);
 }
 
 // pairs: items of two 128-row tiles.
