@@ -112,9 +112,10 @@ __device__ __forceinline__ CacheReq cache_req(const CacheFwdParams& p, int b) {
   r.L = __ldg(p.kv_lens + b);
   r.C = r.L - r.T;
   // new tokens sit at positions >= C, so no cached key at or below C - window is seen
-  r.kt0 = p.window > 0 ? max(0, r.C - p.window + 1) / KT : 0;
-  r.n = static_cast<int>((static_cast<int64_t>(r.L) + KT - 1) / KT) - r.kt0;
-  r.rt = static_cast<int>((static_cast<int64_t>(r.T) * p.group + p.rows_per_tile - 1) / p.rows_per_tile);
+  r.kt0 = p.window > 0 ? static_cast<uint32_t>(max(0, r.C - p.window + 1)) / KT : 0;
+  r.n = static_cast<int>((static_cast<uint32_t>(r.L) + KT - 1) / KT) - r.kt0;
+  // (T group <= 2^30 by the checks; before them the value is not used)
+  r.rt = static_cast<int>((static_cast<uint32_t>(r.T) * p.group + p.rows_per_tile - 1) / static_cast<uint32_t>(p.rows_per_tile));
   return r;
 }
 __device__ __forceinline__ int64_t cache_cost(const CacheFwdParams& p, const CacheReq& r) {
@@ -255,9 +256,8 @@ struct CacheWalk {
     lo = r.kt0 + tile0;
     hi = lo + count;
     if (p.mask == nullptr) {
-      const int64_t last_row = min(static_cast<int64_t>(r.T) * p.group,
-                                   static_cast<int64_t>(row_tile + 1) * p.rows_per_tile) - 1;
-      const int64_t keys = static_cast<int64_t>(r.C) + last_row / p.group + 1;
+      const int last_row = min(r.T * p.group, (row_tile + 1) * p.rows_per_tile) - 1;
+      const int64_t keys = static_cast<int64_t>(r.C) + static_cast<uint32_t>(last_row) / static_cast<uint32_t>(p.group) + 1;
       hi = max(lo, static_cast<int>(min(static_cast<int64_t>(hi), (keys + KT - 1) / KT)));
     }
   }

@@ -163,8 +163,7 @@ __device__ void cc_consumer(const CacheFwdParams& p, uint8_t* smem, CcShared<MT,
     const CacheReq& r = w.r;
     int lo, hi;
     w.template tiles<kCKeys>(p, lo, hi);
-    const int n_rows = min(static_cast<int64_t>(kRows), static_cast<int64_t>(r.T) * p.group -
-                                                            static_cast<int64_t>(w.row_tile) * kRows);
+    const int n_rows = min(kRows, r.T * p.group - w.row_tile * kRows);
     CcRow rows[2];  // lane / 4 and lane / 4 + 8 of the warp's 16, of the item's first head
     const __nv_bfloat16* qrow[2];
     float far_bias[HP][2];
@@ -174,8 +173,9 @@ __device__ void cc_consumer(const CacheFwdParams& p, uint8_t* smem, CcShared<MT,
       const int lr = 16 * grp + (lane >> 2) + 8 * i;
       const int flat = w.row_tile * kRows + lr;
       CcRow& q = rows[i];
-      q.t = lr < n_rows ? flat / p.group : -1;
-      q.head = w.h * HP * p.group + (lr < n_rows ? flat % p.group : 0);
+      const int t = static_cast<uint32_t>(flat) / static_cast<uint32_t>(p.group);
+      q.t = lr < n_rows ? t : -1;
+      q.head = w.h * HP * p.group + (lr < n_rows ? flat - t * p.group : 0);
       q.pos = r.C;
       q.far_bias = 0.f;
       qrow[i] = nullptr;
@@ -414,8 +414,9 @@ __device__ void cc_consumer(const CacheFwdParams& p, uint8_t* smem, CcShared<MT,
     const int g = lr & 15, w0 = (lr >> 4) * kCGroupWarps;
     const bool live = lr < n_rows;
     const int flat = w.row_tile * kRows + lr;
-    const int64_t token = r.q0 + (live ? flat / p.group : 0);
-    const int head0 = w.h * HP * p.group + (live ? flat % p.group : 0);
+    const int t_out = static_cast<uint32_t>(flat) / static_cast<uint32_t>(p.group);
+    const int64_t token = r.q0 + (live ? t_out : 0);
+    const int head0 = w.h * HP * p.group + (live ? flat - t_out * p.group : 0);
     const int64_t part0 = (2 * static_cast<int64_t>(blockIdx.x) + (w.first ? 0 : 1)) * (HP * kRows) + lr;
     float M = -INFINITY, L = 0.f, inv = 1.f, f[kCGroupWarps] = {1.f, 1.f, 1.f, 1.f};
     float* slot = reinterpret_cast<float*>(smem + C::kOOff + warp * C::kSlotBytes);
@@ -502,8 +503,9 @@ __global__ void __launch_bounds__((CcCfg<D * HP, MT, HP>::kThreads), (CcCfg<D * 
 // ------------------------------------------------------------------ joining
 // Joins the parts of the items that range borders cut, and the CTAs' status
 // words.  Block (i, y): border i + 1, rows 2 y and 2 y + 1 of the item, whose
-// heads have at most tile_rows live rows each; four warps share a row's parts (every fourth part each, then the four sums in
-// order: the same bits on every run).
+// heads have at most tile_rows live rows each; four warps share a row's parts
+// (every fourth part each, then the four sums in order: the same bits on every
+// run).
 constexpr int kJoinRows = 2;
 
 template <int D, bool SOFTMAX>
@@ -535,8 +537,8 @@ __global__ void __launch_bounds__(kJoinRows * 128) cache_join_kernel(const __gri
   const int R = p.rows_per_tile, quarter = warp & 3;
   const int row = kJoinRows * blockIdx.y + (warp >> 2);
   const int hh = row / tile_rows, lr = row - hh * tile_rows;  // head of the item's, row of its tile
-  const int64_t flat = static_cast<int64_t>(j.rt) * R + lr;
-  const bool live = hh < p.heads_per_item && flat < static_cast<int64_t>(T) * p.group;
+  const int flat = j.rt * R + lr;
+  const bool live = hh < p.heads_per_item && flat < T * p.group;
   // (the first range that holds one of the item's tiles, the last)
   const int c0 = static_cast<int>(cache_range_of(j.t0 + p.item_cost, j.per)), c1 = static_cast<int>(cache_range_of(j.t1 - 1, j.per));
   // range c's part lies in its first slot when the range starts inside the item (or at its start)
@@ -579,7 +581,7 @@ __global__ void __launch_bounds__(kJoinRows * 128) cache_join_kernel(const __gri
     L += ml[warp >> 2][i].y;
   }
   const int64_t token = q0 + flat / p.group;
-  const int head = (j.h * p.heads_per_item + hh) * p.group + static_cast<int>(flat % p.group);
+  const int head = (j.h * p.heads_per_item + hh) * p.group + flat % p.group;
   if constexpr (SOFTMAX) {
     const float inv = L > 0.f ? 1.f / L : (L == 0.f ? 0.f : L);
 #pragma unroll

@@ -96,9 +96,7 @@ struct CwPart {
     w.tiles<kTile>(p, lo, hi);
     n = hi - lo;
     tile_rows = kTile / p.group * p.group;
-    rows = static_cast<int>(min(static_cast<int64_t>(p.rows_per_tile),
-                                static_cast<int64_t>(w.r.T) * p.group -
-                                    static_cast<int64_t>(w.row_tile) * p.rows_per_tile));
+    rows = min(p.rows_per_tile, w.r.T * p.group - w.row_tile * p.rows_per_tile);
     pair = rows > tile_rows;
     first_token = w.row_tile * (p.rows_per_tile / p.group);
     const int C = w.r.C, last_token = first_token + (rows - 1) / p.group;

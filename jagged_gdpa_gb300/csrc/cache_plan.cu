@@ -167,8 +167,10 @@ cudaError_t launch_cache_plan(const CachePlanParams& p, int sms, cudaStream_t st
   cudaError_t e = smem_attr_once(cache_plan_kernel, 3 * (kCacheMaxBatch + 1) * static_cast<int>(sizeof(int32_t)), attr_set);
   if (e != cudaSuccess) return e;
   const int64_t work = p.total > p.batch ? p.total : p.batch;
-  const int64_t ctas = (work + 4 * kPlanThreads - 1) / (4 * kPlanThreads);
-  cache_plan_kernel<<<static_cast<unsigned>(ctas < 1 ? 1 : (ctas > sms ? sms : ctas)), kPlanThreads, smem, stream>>>(p);
+  // one token per thread as far as four CTAs per SM go: a token is a chain of
+  // loads (its request, its page), and four in a row took twice the time
+  const int64_t ctas = (work + kPlanThreads - 1) / kPlanThreads, most = 4 * static_cast<int64_t>(sms);
+  cache_plan_kernel<<<static_cast<unsigned>(ctas < 1 ? 1 : (ctas > most ? most : ctas)), kPlanThreads, smem, stream>>>(p);
   return cudaGetLastError();
 }
 
