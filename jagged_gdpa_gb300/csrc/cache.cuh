@@ -54,12 +54,11 @@ struct CacheAppendParams {
   int32_t slot_end;            // num_pages * page_size
 };
 
-// The item that a range of key tiles starts inside of, written for the joining
-// kernel: valid only from the first range that continues an item.
+// The item that a range starts inside of, written for the joining kernel: valid
+// only from the second of the ranges that share it.
 struct CacheJoin {
   int32_t valid, b, h, rt;
-  int64_t t0, t1;  // the item's place in the global order
-  int64_t per;     // length of a range
+  int32_t c0, c1;  // its ranges
 };
 
 struct CacheFwdParams {
@@ -79,8 +78,8 @@ struct CacheFwdParams {
   const int32_t* depth;      // [total_q] or nullptr
   __nv_bfloat16* out;        // [total_q][heads][D]
   float* lse;                // [heads][total_q] or nullptr
-  // parts of items that other ranges share, two per range: the one its range
-  // starts with, and its last
+  // parts of items that several ranges share, two per range: the end (or the
+  // middle) of an item that its range starts with, and the start of its last
   float* part_o;             // [2 ranges][heads per item][rows per tile][D]
   float2* part_ml;           // [2 ranges][heads per item][rows per tile]: maximum (log2 units) and sum
   CacheJoin* join;           // [ranges]
@@ -93,6 +92,7 @@ struct CacheFwdParams {
   int32_t rows_per_tile;     // query rows (token, head of the group) of one item
   int32_t heads_per_item;    // key/value heads of one item
   int32_t item_cost;         // tiles that an item's start and end are worth
+  int32_t min_part;          // tiles below which a part of an item is not worth a cut
   float scale;               // s (GELU / SiLU) or s log2(e) (softmax)
   unsigned long long wait_limit_ns;
 };
@@ -132,19 +132,32 @@ __device__ __forceinline__ bool cache_req_ok(const CacheFwdParams& p, const Cach
 // beside them; laid end to end (request by request, row tiles of one head next
 // to each other so that they meet in L2) they form one line that is cut into
 // equal ranges, one per CTA, whatever the lengths.  (Without the lead, ranges
-// that fall on many short requests took half as long again as the others.)  An
-// item cut by a range border is finished by the joining kernel.
+// that fall on many short requests took half as long again as the others.)  A
+// border inside an item cuts it, and the joining kernel puts the parts together;
+// a border that would leave a part of fewer than min_part tiles moves to the
+// item's start or end.
 struct CacheRange {
   int64_t per, begin, end;
-  int b;        // request that `begin` lies in
+  int b;        // request that `begin` lies in (or at the end of)
   int64_t rem;  // begin minus the request's start
   bool ok;
 };
 struct CacheRangeShared {
   int64_t warp_sum[16];
-  int64_t rem;
+  int64_t border[2], rem;
   int b;
 };
+
+// Whether a border `from` after the start of an item of n key tiles stays there.
+__device__ __forceinline__ bool cache_cuts(const CacheFwdParams& p, int64_t from, int n) {
+  return from >= p.item_cost + p.min_part && from <= p.item_cost + n - p.min_part;
+}
+// Where it goes otherwise, from the item's start (the borders keep their order).
+__device__ __forceinline__ int cache_moves(const CacheFwdParams& p, int from, int n) {
+  const int len = p.item_cost + n;
+  const bool to_start = n >= 2 * p.min_part ? from < p.item_cost + p.min_part : 2 * from < len;
+  return to_start ? 0 : len;
+}
 
 // a / b for a >= 0: the 64-bit division, some 100 instructions, only where it is needed.
 __device__ __forceinline__ int64_t cache_div(int64_t a, int b) {
@@ -186,20 +199,39 @@ __device__ CacheRange cache_range(const CacheFwdParams& p, CacheRangeShared* sh,
   R.per = max(cache_div(total + g - 1, g), static_cast<int64_t>(min_range));
   R.begin = min(R.per * blockIdx.x, total);
   R.end = min(R.begin + R.per, total);
-  int64_t at = base + incl - sum;
-  if (all_ok && R.begin < total && at <= R.begin && R.begin < at + sum) {
-    int b = b0;
-    for (;; ++b) {
-      const int64_t c = cache_cost(p, cache_req<KT>(p, b));
-      if (R.begin < at + c) break;
-      at += c;
+  // the thread whose requests hold a border moves it, if need be
+  const int64_t mine = base + incl - sum;
+#pragma unroll 1
+  for (int side = 0; side < 2; ++side) {
+    const int64_t x = side == 0 ? R.begin : R.end;
+    if (!all_ok || x >= total || x < mine || x >= mine + sum) continue;
+    int64_t at = mine;
+    for (int b = b0;; ++b) {
+      const CacheReq r = cache_req<KT>(p, b);
+      const int64_t c = cache_cost(p, r);
+      if (x >= at + c) {
+        at += c;
+        continue;
+      }
+      const int len = r.n + p.item_cost;
+      const int64_t from_req = x - at;
+      const int from = static_cast<int>(from_req - cache_div(from_req, len) * len);
+      const int64_t moved = from_req - from + (cache_cuts(p, from, r.n) ? from : cache_moves(p, from, r.n));
+      sh->border[side] = at + moved;
+      if (side == 0) {
+        sh->b = b;
+        sh->rem = moved;
+      }
+      break;
     }
-    sh->b = b;
-    sh->rem = R.begin - at;
   }
   __syncthreads();
-  R.b = sh->b;
-  R.rem = sh->rem;
+  if (R.begin < total) {
+    R.begin = sh->border[0];
+    R.b = sh->b;
+    R.rem = sh->rem;
+  }
+  if (R.end < total) R.end = sh->border[1];
   return R;
 }
 
@@ -209,7 +241,6 @@ struct CacheWalk {
   int64_t left;  // length left in the range
   int64_t rem;   // place in the request's length
   int b;
-  bool first;    // the part starts at the range's start
   // the current part
   CacheReq r;
   int h, row_tile, tile0, count;  // count tiles from the item's tile0
@@ -220,7 +251,6 @@ struct CacheWalk {
     left = R.ok ? R.end - R.begin : 0;
     rem = R.rem;
     b = R.b;
-    first = true;
   }
   template <int KT>
   __device__ __forceinline__ bool next(const CacheFwdParams& p) {
@@ -235,9 +265,8 @@ struct CacheWalk {
     const int64_t item = cache_div(rem, len);
     const int from = static_cast<int>(rem - item * len);
     step = static_cast<int>(min(static_cast<int64_t>(len - from), left));
-    tile0 = max(0, from - p.item_cost);
-    count = max(0, from + step - p.item_cost) - tile0;
-    if (count == 0) return false;  // the range ends inside the lead
+    tile0 = max(0, from - p.item_cost);  // (a border never lies in the lead)
+    count = from + step - p.item_cost - tile0;
     h = static_cast<int>(cache_div(item, r.rt));
     row_tile = static_cast<int>(item - static_cast<int64_t>(h) * r.rt);
     whole = count == r.n;
@@ -246,8 +275,9 @@ struct CacheWalk {
   __device__ __forceinline__ void advance() {
     rem += step;
     left -= step;
-    first = false;
   }
+  // The range's place for a part that is not a whole item.
+  __device__ __forceinline__ int slot() const { return tile0 > 0 ? 0 : 1; }
   // Keys of tiles [lo, hi) (of the request's) in this part that any row of the
   // row tile can see: without a mask, rows of tokens up to t see keys up to
   // C + t, so later tiles are neither loaded nor computed.
@@ -285,11 +315,6 @@ inline cudaError_t cache_launch(void (*kern)(Params...), dim3 grid, int threads,
   return cudaLaunchKernelEx(&cfg, kern, args...);
 }
 
-// The range that a place on the line lies in.
-__device__ __forceinline__ int64_t cache_range_of(int64_t at, int64_t per) {
-  return (at | per) <= 0xFFFFFFFFll ? static_cast<uint32_t>(at) / static_cast<uint32_t>(per) : at / per;
-}
-
 // Writes a range's join record (one thread).
 template <int KT>
 __device__ __forceinline__ void cache_open(const CacheFwdParams& p, const CacheRange& R) {
@@ -299,16 +324,19 @@ __device__ __forceinline__ void cache_open(const CacheFwdParams& p, const CacheR
   if (R.ok && R.begin < R.end) {
     const CacheReq r = cache_req<KT>(p, R.b);
     const int len = r.n + p.item_cost;
-    const int64_t item = cache_div(R.rem, len);
-    j.t0 = R.begin - (R.rem - item * len);
-    j.t1 = j.t0 + len;
-    j.per = R.per;
-    j.b = R.b;
-    j.h = static_cast<int>(cache_div(item, r.rt));
-    j.rt = static_cast<int>(item - static_cast<int64_t>(j.h) * r.rt);
-    // tiles in several ranges, and this is the second of them
-    const int64_t c0 = cache_range_of(j.t0 + p.item_cost, R.per);
-    j.valid = c0 + 1 == c && cache_range_of(j.t1 - 1, R.per) > c0;
+    const int64_t item = cache_div(R.rem, len), from = R.rem - item * len;  // (len at a request's end: from is 0)
+    if (from > 0) {  // the range starts at a border that cuts the item; is it the first?
+      const int64_t before = from - R.per;  // the border before it, from the item's start
+      j.valid = before <= 0 || !cache_cuts(p, before, r.n);
+      j.b = R.b;
+      j.h = static_cast<int>(cache_div(item, r.rt));
+      j.rt = static_cast<int>(item - static_cast<int64_t>(j.h) * r.rt);
+      j.c0 = c - 1;
+      j.c1 = c;
+      // the last border that cuts it
+      const int64_t last = p.item_cost + r.n - p.min_part;
+      if (last > from) j.c1 = c + static_cast<int>(cache_div(last - from, static_cast<int>(min(R.per, static_cast<int64_t>(INT32_MAX)))));
+    }
   }
   p.join[c] = j;
 }
@@ -321,6 +349,7 @@ struct CcRow {
   float far_bias;   // bias of keys at least R behind every new token
 };
 
+// act(x) for the few weights that are formed one by one.
 template <int ACT>
 __device__ __forceinline__ float cc_act(float x) {
   if constexpr (ACT == 0) return 0.5f * x * (1.0f + erff(x * 0.70710678118654752f));

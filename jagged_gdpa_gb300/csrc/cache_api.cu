@@ -318,6 +318,7 @@ jgdpa_status jgdpa_cache_fwd(const void* q, int64_t q_stride, const void* k_cach
   p.rows_per_tile = L.rows;
   p.heads_per_item = L.heads;
   p.item_cost = L.wide ? (L.pairs ? 10 : 8) : 4;
+  p.min_part = L.wide ? 2 : 1;
   p.scale = act == JGDPA_ACT_SOFTMAX ? scale * jg::kLog2e : scale;
   p.wait_limit_ns = jg::host_wait_limit_ns();
   const int tile_rows = static_cast<int>(std::min<int64_t>(L.rows, max_rows));

@@ -29,7 +29,7 @@ namespace jg {
 
 constexpr int kCKeys = 64;        // tokens per tile
 constexpr int kCGroupWarps = 4;   // warps that share a tile's keys
-constexpr int kCMinRange = 6;     // a range below this many tiles is not worth its own CTA
+constexpr int kCMinRange = 5;        // the least length of a range
 constexpr int kCChunk = 32;       // columns of O that meet at a time at an item's end
 
 // W: columns of K and V that an item streams, the head dimension times the
@@ -307,7 +307,7 @@ __device__ void cc_consumer(const CacheFwdParams& p, uint8_t* smem, CcShared<MT,
               for (int e = 0; e < 4; ++e)
                 if (!((see[e >> 1] >> (8 * i + 2 * (lane & 3) + (e & 1))) & 1)) s[i][e] = ACT == 2 ? -INFINITY : 0.f;  // act(0) = 0
           }
-          float pv[2][4];
+          float(&pv)[2][4] = s;  // in place
           if constexpr (ACT == 2) {
             float mx[2];
 #pragma unroll
@@ -342,11 +342,16 @@ __device__ void cc_consumer(const CacheFwdParams& p, uint8_t* smem, CcShared<MT,
 #pragma unroll
             for (int i = 0; i < 2; ++i)
 #pragma unroll
-              for (int e = 0; e < 4; ++e) pv[i][e] = cc_act<ACT>(s[i][e]);
+              for (int e = 0; e < 4; e += 2) {
+                const float2 y = act2_route<ACT, 0>(make_float2(0.5f * s[i][e], 0.5f * s[i][e + 1]));
+                pv[i][e] = y.x;
+                pv[i][e + 1] = y.y;
+              }
           }
           // P rounds to bf16 as the A operand (half a step, 2^-8 of each weight at most)
-          uint32_t pa[4] = {pack_bf16(pv[0][0], pv[0][1]), pack_bf16(pv[0][2], pv[0][3]), pack_bf16(pv[1][0], pv[1][1]),
-                            pack_bf16(pv[1][2], pv[1][3])};
+          uint32_t pa[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) pa[i] = pack_bf16(pv[i >> 1][2 * (i & 1)], pv[i >> 1][2 * (i & 1) + 1]);
 #pragma unroll
           for (int n2 = 0; n2 < NT / 2; ++n2) {
             uint32_t b[4];
@@ -417,7 +422,7 @@ __device__ void cc_consumer(const CacheFwdParams& p, uint8_t* smem, CcShared<MT,
     const int t_out = static_cast<uint32_t>(flat) / static_cast<uint32_t>(p.group);
     const int64_t token = r.q0 + (live ? t_out : 0);
     const int head0 = w.h * HP * p.group + (live ? flat - t_out * p.group : 0);
-    const int64_t part0 = (2 * static_cast<int64_t>(blockIdx.x) + (w.first ? 0 : 1)) * (HP * kRows) + lr;
+    const int64_t part0 = (2 * static_cast<int64_t>(blockIdx.x) + w.slot()) * (HP * kRows) + lr;
     float M = -INFINITY, L = 0.f, inv = 1.f, f[kCGroupWarps] = {1.f, 1.f, 1.f, 1.f};
     float* slot = reinterpret_cast<float*>(smem + C::kOOff + warp * C::kSlotBytes);
 #pragma unroll
@@ -502,30 +507,31 @@ __global__ void __launch_bounds__((CcCfg<D * HP, MT, HP>::kThreads), (CcCfg<D * 
 
 // ------------------------------------------------------------------ joining
 // Joins the parts of the items that range borders cut, and the CTAs' status
-// words.  Block (i, y): border i + 1, rows 2 y and 2 y + 1 of the item, whose
-// heads have at most tile_rows live rows each; four warps share a row's parts
-// (every fourth part each, then the four sums in order: the same bits on every
-// run).
-constexpr int kJoinRows = 2;
+// words.  Block (i, y): border i + 1, and of its item the rows (of which a head
+// has at most tile_rows that live) 8 / SPLIT y and on.  SPLIT warps share a row's
+// parts, every SPLIT-th each, then their sums in order: the same bits on every
+// run.  Few rows meet with many parts (16-row tiles on a long request: SPLIT 4),
+// many rows with few (128-row tiles: SPLIT 1).
+constexpr int kJoinWarps = 8;
 
-template <int D, bool SOFTMAX>
-__global__ void __launch_bounds__(kJoinRows * 128) cache_join_kernel(const __grid_constant__ CacheFwdParams p, int n_ctas,
+template <int D, bool SOFTMAX, int SPLIT>
+__global__ void __launch_bounds__(kJoinWarps * 32) cache_join_kernel(const __grid_constant__ CacheFwdParams p, int n_ctas,
                                                                      int tile_rows) {
-  constexpr int V = D / 32;
-  __shared__ int worst[kJoinRows * 4];
-  __shared__ float sums[kJoinRows][4][D];
-  __shared__ float2 ml[kJoinRows][4];
+  constexpr int V = D / 32, kRows = kJoinWarps / SPLIT;
+  __shared__ int worst[kJoinWarps];
+  __shared__ float sums[SPLIT > 1 ? kRows : 1][SPLIT][D];
+  __shared__ float2 ml[kRows][SPLIT];
   cache_let_next();
   cache_wait_before();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   if (blockIdx.x == 0 && blockIdx.y == 0) {
     int e = kOk;
-    for (int c = threadIdx.x; c < n_ctas; c += kJoinRows * 128) e = max(e, p.err[c]);
+    for (int c = threadIdx.x; c < n_ctas; c += kJoinWarps * 32) e = max(e, p.err[c]);
     e = __reduce_max_sync(0xffffffffu, e);
     if (lane == 0) worst[warp] = e;
     __syncthreads();
     if (threadIdx.x == 0) {
-      for (int i = 1; i < kJoinRows * 4; ++i) e = max(e, worst[i]);
+      for (int i = 1; i < kJoinWarps; ++i) e = max(e, worst[i]);
       *p.status = e;
     }
   }
@@ -534,16 +540,13 @@ __global__ void __launch_bounds__(kJoinRows * 128) cache_join_kernel(const __gri
   const CacheJoin j = p.join[border];
   if (!j.valid) return;
   const int q0 = __ldg(p.q_off + j.b), T = __ldg(p.q_off + j.b + 1) - q0;
-  const int R = p.rows_per_tile, quarter = warp & 3;
-  const int row = kJoinRows * blockIdx.y + (warp >> 2);
+  const int R = p.rows_per_tile, part = warp % SPLIT;
+  const int row = kRows * blockIdx.y + warp / SPLIT;
   const int hh = row / tile_rows, lr = row - hh * tile_rows;  // head of the item's, row of its tile
   const int flat = j.rt * R + lr;
   const bool live = hh < p.heads_per_item && flat < T * p.group;
-  // (the first range that holds one of the item's tiles, the last)
-  const int c0 = static_cast<int>(cache_range_of(j.t0 + p.item_cost, j.per)), c1 = static_cast<int>(cache_range_of(j.t1 - 1, j.per));
-  // range c's part lies in its first slot when the range starts inside the item (or at its start)
   auto row_of = [&](int c) {
-    return (2 * static_cast<int64_t>(c) + (c * j.per < j.t0 ? 1 : 0)) * (p.heads_per_item * R) + hh * R + lr;
+    return (2 * static_cast<int64_t>(c) + (c == j.c0 ? 1 : 0)) * (p.heads_per_item * R) + hh * R + lr;
   };
   float M = -INFINITY, L = 0.f;
   float acc[V];
@@ -551,13 +554,13 @@ __global__ void __launch_bounds__(kJoinRows * 128) cache_join_kernel(const __gri
   for (int e = 0; e < V; ++e) acc[e] = 0.f;
   if (live) {
     if constexpr (SOFTMAX) {
-      for (int c = c0 + lane; c <= c1; c += 32) M = fmaxf(M, p.part_ml[row_of(c)].x);
+      for (int c = j.c0 + lane; c <= j.c1; c += 32) M = fmaxf(M, p.part_ml[row_of(c)].x);
 #pragma unroll
       for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
     }
     const float ref = M == -INFINITY ? 0.f : M;
-#pragma unroll 8
-    for (int c = c0 + quarter; c <= c1; c += 4) {
+#pragma unroll 4
+    for (int c = j.c0 + part; c <= j.c1; c += SPLIT) {
       const int64_t at = row_of(c);
       float f = 1.f;
       if constexpr (SOFTMAX) {
@@ -569,16 +572,18 @@ __global__ void __launch_bounds__(kJoinRows * 128) cache_join_kernel(const __gri
       for (int e = 0; e < V; ++e) acc[e] = __fmaf_rn(p.part_o[at * D + lane * V + e], f, acc[e]);
     }
   }
+  if constexpr (SPLIT > 1) {
 #pragma unroll
-  for (int e = 0; e < V; ++e) sums[warp >> 2][quarter][lane * V + e] = acc[e];
-  if (lane == 0) ml[warp >> 2][quarter] = make_float2(M, L);
-  __syncthreads();
-  if (!live || quarter != 0) return;
+    for (int e = 0; e < V; ++e) sums[warp / SPLIT][part][lane * V + e] = acc[e];
+    if (lane == 0) ml[warp / SPLIT][part] = make_float2(M, L);
+    __syncthreads();
+  }
+  if (!live || part != 0) return;
 #pragma unroll
-  for (int i = 1; i < 4; ++i) {
+  for (int i = 1; i < SPLIT; ++i) {
 #pragma unroll
-    for (int e = 0; e < V; ++e) acc[e] += sums[warp >> 2][i][lane * V + e];
-    L += ml[warp >> 2][i].y;
+    for (int e = 0; e < V; ++e) acc[e] += sums[warp / SPLIT][i][lane * V + e];
+    L += ml[warp / SPLIT][i].y;
   }
   const int64_t token = q0 + flat / p.group;
   const int head = (j.h * p.heads_per_item + hh) * p.group + flat % p.group;
@@ -627,11 +632,16 @@ cudaError_t launch_cache_fwd_d(const CacheFwdParams& p, int act, int grid, cudaS
   return launch_cc_act<D, 2>(p, grid, stream);
 }
 
+template <int D, bool SOFTMAX>
+static cudaError_t launch_join(const CacheFwdParams& p, int n_ctas, int tile_rows, cudaStream_t stream) {
+  const int split = p.rows_per_tile <= 32 ? 4 : 1, rows = kJoinWarps / split;
+  const dim3 grid(n_ctas > 1 ? n_ctas - 1 : 1, (p.heads_per_item * tile_rows + rows - 1) / rows, 1);
+  return cache_launch(split == 4 ? cache_join_kernel<D, SOFTMAX, 4> : cache_join_kernel<D, SOFTMAX, 1>, grid,
+                      kJoinWarps * 32, 0, stream, p, n_ctas, tile_rows);
+}
 template <int D>
 cudaError_t launch_cache_join_d(const CacheFwdParams& p, int act, int n_ctas, int tile_rows, cudaStream_t stream) {
-  const dim3 grid(n_ctas > 1 ? n_ctas - 1 : 1, (p.heads_per_item * tile_rows + kJoinRows - 1) / kJoinRows, 1);
-  return cache_launch(act == 2 ? cache_join_kernel<D, true> : cache_join_kernel<D, false>, grid, kJoinRows * 128, 0, stream,
-                      p, n_ctas, tile_rows);
+  return act == 2 ? launch_join<D, true>(p, n_ctas, tile_rows, stream) : launch_join<D, false>(p, n_ctas, tile_rows, stream);
 }
 
 template cudaError_t launch_cache_fwd_d<JGDPA_HEAD_DIM>(const CacheFwdParams&, int, int, cudaStream_t);

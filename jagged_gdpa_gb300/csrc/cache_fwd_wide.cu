@@ -32,7 +32,7 @@
 
 namespace jg {
 
-constexpr int kWideMinRange = 6;  // a range below this many tiles is not worth its own CTA
+constexpr int kWideMinRange = 6;  // the least length of a range
 constexpr int kWideThreads = 384;
 
 // PAIR: items of more than 128 rows.
@@ -364,13 +364,14 @@ static __device__ __noinline__ uint4 cw_visible(const CacheFwdParams& p, CacheRe
 // new tokens, where the bias varies from key to key or some rows do not see
 // some keys (-inf for softmax, else 0, as act(0) = 0).
 template <int ACT>
-__device__ __noinline__ void cw_near_tile(const CacheFwdParams& p, CacheReq r, CcRow q, bool far, uint4 see, int key0,
-                                          uint32_t t_s) {
+__device__ __noinline__ void cw_near_tile(const CacheFwdParams& p, CacheReq r, CcRow q, uint4 see, int key0, uint32_t t_s) {
   const int lane = threadIdx.x & 31, reach = (p.bias_len - 1) / 2;
 #pragma unroll 1
   for (int c0 = 0; c0 < kTile; c0 += 32) {
     uint32_t v[32];
     tmem_ld32(t_s + c0, v);
+    // keys R or more behind every new token: one bias for all
+    const bool far = p.bias_len == 0 || key0 + c0 + 31 <= r.C - max(reach, 1);
     const int my_pos = far ? 0 : cc_pos(p, r, key0 + c0 + lane);  // lane c: the position of key c0 + c
     tmem_ld_wait(v);
     if (far) {
@@ -645,7 +646,7 @@ __device__ void cw_consumer(const CacheFwdParams& p, CwShared* sh, uint32_t tmem
       if (warp_live) {
         float scale = p.scale, bias = q.far_bias;
         if (!far || !plain) {
-          cw_near_tile<ACT>(p, r, q, far, see, tile * kTile, t_s);
+          cw_near_tile<ACT>(p, r, q, see, tile * kTile, t_s);
           scale = 1.f;
           bias = 0.f;
         }
@@ -695,7 +696,7 @@ __device__ void cw_consumer(const CacheFwdParams& p, CwShared* sh, uint32_t tmem
     const bool odd = part.n > 0 && *const_cast<volatile int*>(&sh->odd[number & 15]) == number;
     const float inv = ACT != 2 || !w.whole ? 1.f : (l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l));
     const int64_t token = r.q0 + (row_ok ? q.t : 0);
-    const int64_t prow = (2 * static_cast<int64_t>(blockIdx.x) + (w.first ? 0 : 1)) * p.rows_per_tile + (flat - block_row0);
+    const int64_t prow = (2 * static_cast<int64_t>(blockIdx.x) + w.slot()) * p.rows_per_tile + (flat - block_row0);
     __nv_bfloat16* out = w.whole ? p.out + (token * p.heads + q.head) * D : nullptr;
     float* part_o = p.part_o + prow * D;
     tc_fence_after();
