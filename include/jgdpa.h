@@ -324,7 +324,8 @@ JGDPA_API jgdpa_status jgdpa_bwd_shared_q(const void* q, int32_t n_shared, const
  * ctx_lens, q_offsets is all 0 and slots all -1, so that an append and an
  * attention call that follow on the stream do nothing.  A page id outside
  * [0, num_pages) gives slot -1.
- * The workspace (jgdpa_cache_plan_workspace_bytes()) holds the status word.
+ * The workspace (jgdpa_cache_plan_workspace_bytes()) holds the status word;
+ * NULL if it will not be read.
  */
 JGDPA_API size_t jgdpa_cache_plan_workspace_bytes(void);
 JGDPA_API jgdpa_status jgdpa_cache_plan(const int32_t* ctx_lens, const int32_t* new_lens, const int32_t* held_pages,

@@ -549,7 +549,8 @@ def jgdpa_cache_plan(ctx_lens, new_lens, held_pages, block_table, free_pages, fr
     """Pages and slots for a step's tokens (jgdpa_cache_plan); returns (slots,
     q_offsets, kv_lens, held_pages, free_count), the last two being the new
     counts to pass to the next plan.  block_table and free_pages are updated in
-    place.  total_new: rows of slots, at least the sum of new_lens."""
+    place.  total_new: rows of slots, at least the sum of new_lens.  workspace:
+    where a device-detected error (out of pages) is to be read from."""
     lib = lib or load()
     try:
         index, shape = ctx_lens.get_device(), ctx_lens.shape
@@ -571,18 +572,20 @@ def jgdpa_cache_plan(ctx_lens, new_lens, held_pages, block_table, free_pages, fr
         return _on_other_device(jgdpa_cache_plan, ctx_lens.device, (ctx_lens, new_lens, held_pages, block_table, free_pages,
                                 free_count, page_size, total_new, workspace, stream, lib), {})
     raw, alloc = _launch_on(stream, ctx_lens.device)
-    # one allocation: 256 bytes of workspace (unless the caller has one), then the results
-    n = 64 + total_new + 3 * batch + 2
-    ints = torch.empty(n, dtype=_i32, device=ctx_lens.device) if alloc is None else alloc(n, _i32)
-    _, slots, q_offsets, kv_lens, held, count = torch.split_with_sizes(ints, (64, total_new, batch + 1, batch, batch, 1))
-    base = ints.data_ptr()
-    at = base + 256
-    off, kv = at + 4 * total_new, at + 4 * (total_new + batch + 1)
-    held_at = kv + 4 * batch
-    ws, ws_bytes = (base, 256) if workspace is None else (workspace.data_ptr(), workspace.numel())
+    if alloc is None:
+        device = ctx_lens.device
+        slots = torch.empty(total_new, dtype=_i32, device=device)
+        q_offsets = torch.empty(batch + 1, dtype=_i32, device=device)
+        kv_lens = torch.empty(batch, dtype=_i32, device=device)
+        held = torch.empty(batch, dtype=_i32, device=device)
+        count = torch.empty(1, dtype=_i32, device=device)
+    else:
+        slots, q_offsets, kv_lens, held, count = (alloc(n, _i32) for n in (total_new, batch + 1, batch, batch, 1))
+    ws, ws_bytes = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel())
     rc = lib.jgdpa_cache_plan(ctx_lens.data_ptr(), new_lens.data_ptr(), held_pages.data_ptr(), batch, int(page_size),
                               block_table.data_ptr(), width, free_pages.data_ptr(), pages, free_count.data_ptr(),
-                              total_new, held_at, held_at + 4 * batch, off, kv, at, ws, ws_bytes, raw)
+                              total_new, held.data_ptr(), count.data_ptr(), q_offsets.data_ptr(), kv_lens.data_ptr(),
+                              slots.data_ptr(), ws, ws_bytes, raw)
     if rc:
         raise JgdpaError(rc, "jgdpa_cache_plan")
     return slots, q_offsets, kv_lens, held, count

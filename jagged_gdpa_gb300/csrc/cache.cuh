@@ -38,7 +38,7 @@ struct CachePlanParams {
   int32_t* q_off;
   int32_t* kv_lens;
   int32_t* slots;
-  int* status;
+  int* status;  // or nullptr
 };
 
 struct CacheAppendParams {

@@ -171,7 +171,7 @@ jgdpa_status jgdpa_cache_plan(const int32_t* ctx_lens, const int32_t* new_lens, 
                         static_cast<const void*>(q_offsets), static_cast<const void*>(kv_lens),
                         static_cast<const void*>(slots)})
     if (!aligned(a, 4)) return JGDPA_ERR_MISALIGNED;
-  if (workspace == nullptr || workspace_bytes < kAlign) return JGDPA_ERR_WORKSPACE_TOO_SMALL;
+  if (workspace != nullptr && workspace_bytes < kAlign) return JGDPA_ERR_WORKSPACE_TOO_SMALL;
   if (!aligned(workspace, kAlign)) return JGDPA_ERR_MISALIGNED;
   const int sms = jg::host_sm_count();
   if (sms <= 0) return JGDPA_ERR_CUDA;

@@ -102,7 +102,7 @@ __global__ void __launch_bounds__(kPlanThreads) cache_plan_kernel(const CachePla
   else if (total[1] > n + total[2]) status = kErrOutOfPages;
   const int64_t at = static_cast<int64_t>(blockIdx.x) * kPlanThreads + tid;
   const int64_t step = static_cast<int64_t>(gridDim.x) * kPlanThreads;
-  if (at == 0) *p.status = status;
+  if (at == 0 && p.status != nullptr) *p.status = status;
   if (status != kOk) {  // nothing is handed out: no new tokens, no slots, the pages as they were
     for (int64_t b = at; b < p.batch; b += step) {
       p.held_out[b] = __ldg(p.held + b);
