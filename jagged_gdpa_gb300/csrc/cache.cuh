@@ -90,6 +90,7 @@ struct CacheFwdParams {
   int32_t page_shift, width, num_pages;
   int32_t mask_words, bias_len, window;
   int32_t rows_per_tile;     // query rows (token, head of the group) of one item
+  int32_t tile_tokens;       // tokens of a 128-row tile (128-row kernel; 0 otherwise)
   int32_t heads_per_item;    // key/value heads of one item
   int32_t item_cost;         // tiles that an item's start and end are worth
   int32_t min_part;          // tiles below which a part of an item is not worth a cut

@@ -56,6 +56,7 @@ struct CacheLayout {
   size_t err, join, part_ml, part_o, total;
   int rows, grid;  // query rows of one item per key/value head, CTAs
   int heads;       // key/value heads of one item
+  int tokens;      // of a 128-row tile
   bool wide;       // 128-row tiles through tensor memory
   bool pairs;      // of them, two at a time
 };
@@ -67,9 +68,9 @@ bool cache_layout(int32_t heads, int32_t kv_heads, int32_t head_dim, int32_t max
   // (a tile of the wide kernel holds whole tokens, so at most 128 heads share a key/value head there)
   L->wide = max_rows > 32 && group <= jg::kTile;
   if (L->wide) {
-    const int tile = jg::kTile / group * group;
-    L->pairs = max_rows > tile;
-    L->rows = L->pairs ? 2 * tile : tile;
+    L->tokens = std::min(jg::kTile / group, max_q);
+    L->pairs = max_q > L->tokens;
+    L->rows = group * L->tokens * (L->pairs ? 2 : 1);
     L->grid = sms;
     L->heads = 1;
   } else {
@@ -77,6 +78,7 @@ bool cache_layout(int32_t heads, int32_t kv_heads, int32_t head_dim, int32_t max
     L->heads = kv_heads % (128 / head_dim) == 0 ? 128 / head_dim : 1;
     L->rows = max_rows <= 16 ? 16 : 32;
     L->pairs = false;
+    L->tokens = 0;
     L->grid = sms * jg::cache_ctas(head_dim * L->heads, L->rows / 16);
   }
   const size_t parts = 2 * static_cast<size_t>(L->grid) * L->rows * L->heads;
@@ -114,18 +116,18 @@ bool cache_map(CUtensorMap* m, const void* ptr, int64_t page_stride, int32_t num
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// The queries: (column, head, token), a box one 64-column half of a tile's
-// tokens and the heads of one group.
+// The queries: (column, token, head), a box one 64-column half of a tile's
+// tokens, head by head.
 bool query_map(CUtensorMap* m, const void* ptr, int64_t q_stride, int64_t total_q, int32_t heads, int32_t head_dim,
-               int32_t group) {
+               int32_t group, int32_t tokens) {
   std::memset(m, 0, sizeof(*m));
   const jg::EncodeFn enc = jg::host_encode_fn();
   if (!enc) return false;
   const cuuint32_t cols = std::min(head_dim, 64);
-  cuuint64_t dims[3] = {static_cast<cuuint64_t>(head_dim), static_cast<cuuint64_t>(heads),
-                        static_cast<cuuint64_t>(total_q)};
-  cuuint64_t strides[2] = {static_cast<cuuint64_t>(head_dim) * 2, static_cast<cuuint64_t>(q_stride) * 2};
-  cuuint32_t box[3] = {cols, static_cast<cuuint32_t>(group), static_cast<cuuint32_t>(jg::kTile / group)};
+  cuuint64_t dims[3] = {static_cast<cuuint64_t>(head_dim), static_cast<cuuint64_t>(total_q),
+                        static_cast<cuuint64_t>(heads)};
+  cuuint64_t strides[2] = {static_cast<cuuint64_t>(q_stride) * 2, static_cast<cuuint64_t>(head_dim) * 2};
+  cuuint32_t box[3] = {cols, static_cast<cuuint32_t>(tokens), static_cast<cuuint32_t>(group)};
   cuuint32_t es[3] = {1, 1, 1};
   return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(ptr), dims, strides, box, es,
              CU_TENSOR_MAP_INTERLEAVE_NONE, cols == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
@@ -282,7 +284,7 @@ jgdpa_status jgdpa_cache_fwd(const void* q, int64_t q_stride, const void* k_cach
   const int32_t map_heads = kv_heads / L.heads, map_dim = head_dim * L.heads;  // heads that go together as one
   if (!cache_map(&p.tm_k, k_cache, k_page_stride, num_pages, page_size, map_heads, map_dim, box, !L.wide) ||
       !cache_map(&p.tm_v, v_cache, v_page_stride, num_pages, page_size, map_heads, map_dim, box, !L.wide) ||
-      (L.wide && !query_map(&p.tm_q, q, q_stride, total_q, heads, head_dim, heads / kv_heads)))
+      (L.wide && !query_map(&p.tm_q, q, q_stride, total_q, heads, head_dim, heads / kv_heads, L.tokens)))
     return JGDPA_ERR_CUDA;
   p.k_cache = static_cast<const __nv_bfloat16*>(k_cache);
   p.v_cache = static_cast<const __nv_bfloat16*>(v_cache);
@@ -316,12 +318,13 @@ jgdpa_status jgdpa_cache_fwd(const void* q, int64_t q_stride, const void* k_cach
   p.bias_len = bias_len;
   p.window = window;
   p.rows_per_tile = L.rows;
+  p.tile_tokens = L.tokens;
   p.heads_per_item = L.heads;
   p.item_cost = L.wide ? (L.pairs ? 10 : 8) : 4;
   p.min_part = L.wide ? 2 : 1;
   p.scale = act == JGDPA_ACT_SOFTMAX ? scale * jg::kLog2e : scale;
   p.wait_limit_ns = jg::host_wait_limit_ns();
-  const int tile_rows = static_cast<int>(std::min<int64_t>(L.rows, max_rows));
+  const int tile_rows = L.wide ? L.rows : static_cast<int>(std::min<int64_t>(L.rows, max_rows));  // that may live
   auto launch = [&](auto dim) -> cudaError_t {
     constexpr int D = decltype(dim)::value;
     cudaError_t e = L.wide ? jg::launch_cache_fwd_wide_d<D>(p, act, L.pairs, L.grid, stream)

@@ -543,8 +543,17 @@ __global__ void __launch_bounds__(kJoinWarps * 32) cache_join_kernel(const __gri
   const int R = p.rows_per_tile, part = warp % SPLIT;
   const int row = kRows * blockIdx.y + warp / SPLIT;
   const int hh = row / tile_rows, lr = row - hh * tile_rows;  // head of the item's, row of its tile
-  const int flat = j.rt * R + lr;
-  const bool live = hh < p.heads_per_item && flat < T * p.group;
+  int token_at, g;  // of the request, of the group
+  if (p.tile_tokens) {  // 128-row tiles: head by head
+    const int tile = p.tile_tokens * p.group, s = lr / tile, r = lr - s * tile;
+    g = r / p.tile_tokens;
+    token_at = j.rt * (R / p.group) + s * p.tile_tokens + r - g * p.tile_tokens;
+  } else {  // token by token
+    const int flat = j.rt * R + lr;
+    token_at = flat / p.group;
+    g = flat - token_at * p.group;
+  }
+  const bool live = hh < p.heads_per_item && token_at < T;
   auto row_of = [&](int c) {
     return (2 * static_cast<int64_t>(c) + (c == j.c0 ? 1 : 0)) * (p.heads_per_item * R) + hh * R + lr;
   };
@@ -585,8 +594,8 @@ __global__ void __launch_bounds__(kJoinWarps * 32) cache_join_kernel(const __gri
     for (int e = 0; e < V; ++e) acc[e] += sums[warp / SPLIT][i][lane * V + e];
     L += ml[warp / SPLIT][i].y;
   }
-  const int64_t token = q0 + flat / p.group;
-  const int head = (j.h * p.heads_per_item + hh) * p.group + flat % p.group;
+  const int64_t token = q0 + token_at;
+  const int head = (j.h * p.heads_per_item + hh) * p.group + g;
   if constexpr (SOFTMAX) {
     const float inv = L > 0.f ? 1.f / L : (L == 0.f ? 0.f : L);
 #pragma unroll

@@ -82,10 +82,9 @@ static_assert(sizeof(CwShared) <= 2048, "shared block");
 // What every role works out about a part.
 struct CwPart {
   int lo, n;        // key tiles [lo, lo + n)
-  int tile_rows;    // rows of one 128-row tile: a whole number of tokens
-  int rows;         // rows of the part
-  bool pair;        // two tiles of rows; otherwise one
   int first_token;  // of the part's rows
+  int tokens;       // of them
+  bool pair;        // two tiles of rows; otherwise one
   int plain_lo, plain_hi;  // tiles in which every row sees every key
   int far_hi;              // tiles below it are plain in the bias: R or more behind every row
 
@@ -95,11 +94,11 @@ struct CwPart {
     int hi;
     w.tiles<kTile>(p, lo, hi);
     n = hi - lo;
-    tile_rows = kTile / p.group * p.group;
-    rows = min(p.rows_per_tile, w.r.T * p.group - w.row_tile * p.rows_per_tile);
-    pair = rows > tile_rows;
-    first_token = w.row_tile * (p.rows_per_tile / p.group);
-    const int C = w.r.C, last_token = first_token + (rows - 1) / p.group;
+    const int most = p.rows_per_tile / p.group;
+    first_token = w.row_tile * most;
+    tokens = min(most, w.r.T - first_token);
+    pair = tokens > p.tile_tokens;
+    const int C = w.r.C, last_token = first_token + tokens - 1;
     plain_lo = 0;
     plain_hi = (p.window <= 0 && p.mask == nullptr ? min(w.r.L, C + first_token + 1) : C) / kTile;
     if (p.window > 0) {
@@ -144,11 +143,11 @@ struct CwProducer {
     const int slot = q_n % C::kSlots;
     if (!mbar_wait_warp(&sh->q_empty[slot], ((q_n / C::kSlots) & 1) ^ 1, fail)) return false;
     if ((threadIdx.x & 31) == 0) {
-      mbar_arrive_tx(&sh->q_full[slot], kTile / p.group * p.group * D * 2);
+      mbar_arrive_tx(&sh->q_full[slot], p.tile_tokens * p.group * D * 2);
 #pragma unroll
       for (int b = 0; b < C::kBlocks; ++b)
         tma_load_3d(smem + C::kQOff + slot * C::kTileBytes + b * C::kBlockBytes, &p.tm_q, &sh->q_full[slot],
-                    b * C::kBlockCols, w.h * p.group, w.r.q0 + token);
+                    b * C::kBlockCols, w.r.q0 + token, w.h * p.group);
     }
     __syncwarp();
     ++q_n;
@@ -211,7 +210,7 @@ __device__ void cw_producer(const CacheFwdParams& p, uint8_t* smem, CwShared* sh
     const CwPart part(p, w);
     if (part.n == 0) continue;
     ok = load.query(w, part.first_token);
-    if (PAIR && part.pair && ok) ok = load.query(w, part.first_token + part.tile_rows / p.group);
+    if (PAIR && part.pair && ok) ok = load.query(w, part.first_token + p.tile_tokens);
     for (int t = part.lo; t < part.lo + part.n && ok; ++t) ok = load.tile(w, t);
   }
   if (!ok || !load.value()) load.drain();
@@ -618,19 +617,20 @@ __device__ void cw_consumer(const CacheFwdParams& p, CwShared* sh, uint32_t tmem
     const CacheReq& r = w.r;
     if (part.n > 0) ++number;  // (the ring lets no more than 8 later parts be loaded, let alone made safe)
     __syncwarp();
-    const int block_row0 = w.row_tile * p.rows_per_tile;
     const bool pair = PAIR && part.pair;
-    const int my_rows = pair ? (stream == 0 ? part.tile_rows : part.rows - part.tile_rows) : part.rows;
-    const bool row_ok = row < my_rows;
-    const int flat = block_row0 + (pair ? stream * part.tile_rows : 0) + row;
+    // a tile's rows go head by head, so that the lanes of a warp are neighbours
+    // in their mask words and bias entries
+    const int before = pair && stream == 1 ? p.tile_tokens : 0;  // tokens of the part
+    const int g = static_cast<uint32_t>(row) / static_cast<uint32_t>(p.tile_tokens), at = row - g * p.tile_tokens;
+    const bool row_ok = g < p.group && before + at < part.tokens;
     CcRow q;
-    q.t = row_ok ? flat / p.group : -1;
-    q.head = w.h * p.group + (row_ok ? flat % p.group : 0);
+    q.t = row_ok ? part.first_token + before + at : -1;
+    q.head = w.h * p.group + (row_ok ? g : 0);
     q.pos = r.C + (row_ok ? (p.depth != nullptr ? __ldg(p.depth + r.q0 + q.t) : q.t) : 0);
     q.far_bias = 0.f;
     if (row_ok && p.bias_len)
       q.far_bias = __ldg(p.bias + static_cast<int64_t>(q.head) * p.bias_len + 2 * reach) * cc_bias_unit<ACT>();
-    const bool warp_live = (warp & 3) * 32 < my_rows;
+    const bool warp_live = __any_sync(0xffffffffu, row_ok);
     const int count = part.count(stream);
     float m = -INFINITY, l = 0.f;
     for (int i = 0; i < count; ++i) {
@@ -696,7 +696,7 @@ __device__ void cw_consumer(const CacheFwdParams& p, CwShared* sh, uint32_t tmem
     const bool odd = part.n > 0 && *const_cast<volatile int*>(&sh->odd[number & 15]) == number;
     const float inv = ACT != 2 || !w.whole ? 1.f : (l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l));
     const int64_t token = r.q0 + (row_ok ? q.t : 0);
-    const int64_t prow = (2 * static_cast<int64_t>(blockIdx.x) + w.slot()) * p.rows_per_tile + (flat - block_row0);
+    const int64_t prow = (2 * static_cast<int64_t>(blockIdx.x) + w.slot()) * p.rows_per_tile + before * p.group + row;
     __nv_bfloat16* out = w.whole ? p.out + (token * p.heads + q.head) * D : nullptr;
     float* part_o = p.part_o + prow * D;
     tc_fence_after();

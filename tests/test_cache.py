@@ -382,11 +382,13 @@ def test_prompts_longer_than_a_row_tile(jg, act):
 
 @gpu
 @pytest.mark.parametrize("act", ["gelu", "softmax"])
-@pytest.mark.parametrize("new", [1, 3])
-def test_long_contexts_are_cut_between_ctas(jg, act, new):
+@pytest.mark.parametrize("new,group,length", [(1, 4, 20000), (3, 4, 20000), (6, 5, 9000), (20, 3, 6000), (40, 4, 5000), (50, 5, 4000)])
+def test_long_contexts_are_cut_between_ctas(jg, act, new, group, length):
     """One long and some short requests: the long one's keys are split."""
-    c = Case(9, [20000, 3, 700], [new, 1, 2], 1, 4, 64, 64, act, bias=129, nan=False)
-    compare(c, *jg.jgdpa_cache_fwd(**c.kwargs()))
+    c = Case(9, [length, 3, 700], [new, 1, 2], 1, group, 64, 64, act, bias=129, nan=False)
+    kw = c.kwargs()
+    out = torch.full_like(kw["q"], float("nan"))  # every row is written
+    compare(c, *jg.jgdpa_cache_fwd(**kw, out=out))
 
 
 @gpu
