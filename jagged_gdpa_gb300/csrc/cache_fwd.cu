@@ -127,10 +127,9 @@ __device__ void cc_producer(const CacheFwdParams& p, uint8_t* smem, CcShared<MT,
       ++it;
     }
   }
-  if (!ok) {  // let the copies already issued land before the CTA exits
-    for (uint32_t i = it > C::kStages ? it - C::kStages : 0; i < it; ++i)
-      mbar_wait_drain(&sh->full[i % C::kStages], (i / C::kStages) & 1);
-  }
+  // the copies issued land before the CTA exits, also when the consumers gave up
+  for (uint32_t i = it > C::kStages ? it - C::kStages : 0; i < it; ++i)
+    mbar_wait_drain(&sh->full[i % C::kStages], (i / C::kStages) & 1);
 }
 
 // ------------------------------------------------------------- consumers
@@ -398,7 +397,9 @@ __device__ void cc_consumer(const CacheFwdParams& p, uint8_t* smem, CcShared<MT,
           }
         }
       }
-      mbar_arrive_warp(&sh->empty[st]);
+      // (a warp that gave up releases nothing: what it did not wait for may
+      // still be on its way)
+      if (!dead) mbar_arrive_warp(&sh->empty[st]);
     }
 
     // the item's end: the warps' O, maxima and sums meet in shared memory

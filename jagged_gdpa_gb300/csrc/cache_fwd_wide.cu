@@ -191,12 +191,13 @@ struct CwProducer {
   __device__ __forceinline__ bool value() {
     return it == 0 || load(C::entry_v(it - 1), &p.tm_v, held.mine, held.bytes, held.y, held.h, held.page);
   }
-  // After a failure: lets the copies already issued land before the CTA exits.
+  // The copies issued land before the CTA exits, also when the others gave up.
   __device__ void drain() {
     for (uint32_t i = q_n > C::kSlots ? q_n - C::kSlots : 0; i < q_n; ++i)
       mbar_wait_drain(&sh->q_full[i % C::kSlots], (i / C::kSlots) & 1);
     for (uint32_t e = entries > C::kStages ? entries - C::kStages : 0; e < entries; ++e)
-      mbar_wait_drain(&sh->full[C::stage(e)], C::parity(e));
+      if (e != C::entry_k(it) || entries <= e + 1)  // (the skipped one has the last V behind it)
+        mbar_wait_drain(&sh->full[C::stage(e)], C::parity(e));
   }
 };
 
@@ -213,7 +214,8 @@ __device__ void cw_producer(const CacheFwdParams& p, uint8_t* smem, CwShared* sh
     if (PAIR && part.pair && ok) ok = load.query(w, part.first_token + p.tile_tokens);
     for (int t = part.lo; t < part.lo + part.n && ok; ++t) ok = load.tile(w, t);
   }
-  if (!ok || !load.value()) load.drain();
+  if (ok) load.value();
+  load.drain();
 }
 
 // ------------------------------------------------------------- MMA issuer
@@ -718,7 +720,7 @@ __device__ void cw_consumer(const CacheFwdParams& p, CwShared* sh, uint32_t tmem
       if (row_ok && !dead) cw_store16(x, inv, out, part_o, c0);
       __syncwarp();
     }
-    if (part.n > 0) {
+    if (part.n > 0 && !dead) {
       tc_fence_before();
       mbar_arrive_warp(&sh->o_empty);
     }

@@ -346,6 +346,26 @@ def test_attention(jg, act, d, group, new):
 
 
 @gpu
+@pytest.mark.parametrize("act", ["gelu", "silu", "softmax"])
+@pytest.mark.parametrize("d,kv_heads", [(32, 4), (32, 8), (32, 3), (64, 4), (64, 3)])
+@pytest.mark.parametrize("group,new", [(1, 1), (3, 2), (4, 7)])
+def test_small_heads_side_by_side(jg, act, d, kv_heads, group, new):
+    c = Case(d + new, [0, 700, 64, 3000], [new, 1, new, new], kv_heads, group, d, 16, act, bias=65, window=0 if new < 7 else 200,
+             mask=True)
+    kw = c.kwargs()
+    out = torch.full_like(kw["q"], float("nan"))
+    compare(c, *jg.jgdpa_cache_fwd(**kw, out=out))
+
+
+@gpu
+@pytest.mark.parametrize("act", ["silu", "softmax"])
+@pytest.mark.parametrize("group", [100, 128, 130])
+def test_very_many_heads_per_group(jg, act, group):
+    c = Case(group, [70, 5], [3, 1], 1, group, 32, 16, act, bias=9)
+    compare(c, *jg.jgdpa_cache_fwd(**c.kwargs()))
+
+
+@gpu
 @pytest.mark.parametrize("act", ["silu", "softmax"])
 @pytest.mark.parametrize("new,group,bias,window,page", [
     (1, 1, 257, 0, 16), (9, 2, 33, 0, 64), (33, 1, 5, 100, 32), (64, 4, 0, 1, 128), (20, 3, 1, 64, 256), (40, 1, 129, 7, 1024),
@@ -510,6 +530,24 @@ def test_mask_narrower_than_a_request_is_refused(jg):
     ws = torch.empty(jg.jgdpa_cache_fwd_workspace_bytes(1, 1, 64, 33), dtype=torch.uint8, device="cuda")
     jg.jgdpa_cache_fwd(**{**kw, "tree_mask": kw["tree_mask"][:, :1].contiguous()}, workspace=ws)
     assert jg.jgdpa_read_device_status(ws) == 6
+
+
+@gpu
+@pytest.mark.parametrize("act", ["gelu", "softmax"])
+@pytest.mark.parametrize("d,new,group", [(128, 1, 4), (64, 6, 4), (32, 1, 2), (128, 30, 2), (64, 60, 4)])
+def test_a_wait_that_gives_up_is_reported_and_recovered_from(jg, act, d, new, group):
+    c = Case(3, [3000, 900], [new, new], 4, group, d, 64, act, nan=False)
+    kw = c.kwargs()
+    ws = torch.empty(jg.jgdpa_cache_fwd_workspace_bytes(c.heads, 4, d, new), dtype=torch.uint8, device="cuda")
+    good, _ = jg.jgdpa_cache_fwd(**kw, workspace=ws)
+    jg.jgdpa_set_wait_limit_ns(1)
+    try:
+        jg.jgdpa_cache_fwd(**kw, workspace=ws)
+        assert jg.jgdpa_read_device_status(ws) in (0, 7)  # (0: every wait was shorter than its first test)
+    finally:
+        jg.jgdpa_set_wait_limit_ns(0)
+    out, _ = jg.jgdpa_cache_fwd(**kw, workspace=ws)
+    assert jg.jgdpa_read_device_status(ws) == 0 and torch.equal(out, good)
 
 
 @gpu
