@@ -57,8 +57,10 @@ struct CacheAppendParams {
 // The item that a range starts inside of, written for the joining kernel: valid
 // only from the second of the ranges that share it.
 struct CacheJoin {
-  int32_t valid, b, h, rt;
+  int32_t valid, h, rt;
   int32_t c0, c1;  // its ranges
+  int32_t q0, T;   // its request's first query row, its tokens
+  int32_t pad;
 };
 
 struct CacheFwdParams {
@@ -160,9 +162,11 @@ __device__ __forceinline__ int cache_moves(const CacheFwdParams& p, int from, in
   return to_start ? 0 : len;
 }
 
-// a / b for a >= 0: the 64-bit division, some 100 instructions, only where it is needed.
+// a / b for a >= 0: the 64-bit division, some 100 instructions, only where it is
+// needed, and out of the way.
+static __device__ __noinline__ int64_t cache_div64(int64_t a, int64_t b) { return a / b; }
 __device__ __forceinline__ int64_t cache_div(int64_t a, int b) {
-  return a <= 0xFFFFFFFFll ? static_cast<int64_t>(static_cast<uint32_t>(a) / static_cast<uint32_t>(b)) : a / b;
+  return a <= 0xFFFFFFFFll ? static_cast<int64_t>(static_cast<uint32_t>(a) / static_cast<uint32_t>(b)) : cache_div64(a, b);
 }
 
 // This CTA's range.  Run by every thread of the CTA (a whole number of warps, at
@@ -329,7 +333,8 @@ __device__ __forceinline__ void cache_open(const CacheFwdParams& p, const CacheR
     if (from > 0) {  // the range starts at a border that cuts the item; is it the first?
       const int64_t before = from - R.per;  // the border before it, from the item's start
       j.valid = before <= 0 || !cache_cuts(p, before, r.n);
-      j.b = R.b;
+      j.q0 = r.q0;
+      j.T = r.T;
       j.h = static_cast<int>(cache_div(item, r.rt));
       j.rt = static_cast<int>(item - static_cast<int64_t>(j.h) * r.rt);
       j.c0 = c - 1;

@@ -540,7 +540,6 @@ __global__ void __launch_bounds__(kJoinWarps * 32) cache_join_kernel(const __gri
   if (border >= n_ctas) return;
   const CacheJoin j = p.join[border];
   if (!j.valid) return;
-  const int q0 = __ldg(p.q_off + j.b), T = __ldg(p.q_off + j.b + 1) - q0;
   const int R = p.rows_per_tile, part = warp % SPLIT;
   const int row = kRows * blockIdx.y + warp / SPLIT;
   const int hh = row / tile_rows, lr = row - hh * tile_rows;  // head of the item's, row of its tile
@@ -554,7 +553,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) cache_join_kernel(const __gri
     token_at = flat / p.group;
     g = flat - token_at * p.group;
   }
-  const bool live = hh < p.heads_per_item && token_at < T;
+  const bool live = hh < p.heads_per_item && token_at < j.T;
   auto row_of = [&](int c) {
     return (2 * static_cast<int64_t>(c) + (c == j.c0 ? 1 : 0)) * (p.heads_per_item * R) + hh * R + lr;
   };
@@ -595,7 +594,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) cache_join_kernel(const __gri
     for (int e = 0; e < V; ++e) acc[e] += sums[warp / SPLIT][i][lane * V + e];
     L += ml[warp / SPLIT][i].y;
   }
-  const int64_t token = q0 + token_at;
+  const int64_t token = j.q0 + token_at;
   const int head = (j.h * p.heads_per_item + hh) * p.group + g;
   if constexpr (SOFTMAX) {
     const float inv = L > 0.f ? 1.f / L : (L == 0.f ? 0.f : L);
