@@ -94,7 +94,7 @@ struct CacheFwdParams {
   int32_t rows_per_tile;     // query rows (token, head of the group) of one item
   int32_t tile_tokens;       // tokens of a 128-row tile (128-row kernel; 0 otherwise)
   int32_t heads_per_item;    // key/value heads of one item
-  int32_t item_cost;         // tiles that an item's start and end are worth
+  int32_t item_cost;         // what an item's start and end are worth, in lengths of the work division
   int32_t min_part;          // tiles below which a part of an item is not worth a cut
   float scale;               // s (GELU / SiLU) or s log2(e) (softmax)
   unsigned long long wait_limit_ns;
@@ -105,6 +105,7 @@ struct CacheReq {
   int q0, T, L, C;
   int kt0, n;  // first key tile and tiles of every item
   int rt;      // row tiles
+  int u;       // length of a key tile on the line
 };
 
 template <int KT>
@@ -119,10 +120,15 @@ __device__ __forceinline__ CacheReq cache_req(const CacheFwdParams& p, int b) {
   r.n = static_cast<int>((static_cast<uint32_t>(r.L) + KT - 1) / KT) - r.kt0;
   // (T group <= 2^30 by the checks; before them the value is not used)
   r.rt = static_cast<int>((static_cast<uint32_t>(r.T) * p.group + p.rows_per_tile - 1) / static_cast<uint32_t>(p.rows_per_tile));
+  // (128-row kernel: two tiles of rows take about 1.4 times as long as one)
+  r.u = p.tile_tokens == 0 ? 1 : (r.T > p.tile_tokens ? 3 : 2);
   return r;
 }
+// The length of one of its items on the line.
+__device__ __forceinline__ int cache_len(const CacheFwdParams& p, const CacheReq& r) { return p.item_cost + r.n * r.u; }
 __device__ __forceinline__ int64_t cache_cost(const CacheFwdParams& p, const CacheReq& r) {
-  return r.T <= 0 ? 0 : static_cast<int64_t>(p.kv_heads / p.heads_per_item) * r.rt * (r.n + p.item_cost);
+  return r.T <= 0 ? 0 : static_cast<int64_t>(p.kv_heads / p.heads_per_item) * r.rt *
+                             cache_len(p, r);
 }
 __device__ __forceinline__ bool cache_req_ok(const CacheFwdParams& p, const CacheReq& r) {
   return r.T >= 0 && r.T <= p.max_q && r.L >= r.T &&
@@ -130,9 +136,8 @@ __device__ __forceinline__ bool cache_req_ok(const CacheFwdParams& p, const Cach
          (p.mask == nullptr || r.T <= 32 * p.mask_words);
 }
 
-// Work division.  The items are (request, kv head, row tile), each of n key
-// tiles and a lead of item_cost tiles' length, what its start and end take
-// beside them; laid end to end (request by request, row tiles of one head next
+// Work division.  The items are (request, kv head, row tile), each a lead of
+// item_cost, what its start and end take, and n key tiles of length u; laid end to end (request by request, row tiles of one head next
 // to each other so that they meet in L2) they form one line that is cut into
 // equal ranges, one per CTA, whatever the lengths.  (Without the lead, ranges
 // that fall on many short requests took half as long again as the others.)  A
@@ -151,22 +156,21 @@ struct CacheRangeShared {
   int b;
 };
 
-// Whether a border `from` after the start of an item of n key tiles stays there.
-__device__ __forceinline__ bool cache_cuts(const CacheFwdParams& p, int64_t from, int n) {
-  return from >= p.item_cost + p.min_part && from <= p.item_cost + n - p.min_part;
-}
-// Where it goes otherwise, from the item's start (the borders keep their order).
-__device__ __forceinline__ int cache_moves(const CacheFwdParams& p, int from, int n) {
-  const int len = p.item_cost + n;
-  const bool to_start = n >= 2 * p.min_part ? from < p.item_cost + p.min_part : 2 * from < len;
-  return to_start ? 0 : len;
-}
-
 // a / b for a >= 0: the 64-bit division, some 100 instructions, only where it is
 // needed, and out of the way.
 static __device__ __noinline__ int64_t cache_div64(int64_t a, int64_t b) { return a / b; }
 __device__ __forceinline__ int64_t cache_div(int64_t a, int b) {
   return a <= 0xFFFFFFFFll ? static_cast<int64_t>(static_cast<uint32_t>(a) / static_cast<uint32_t>(b)) : cache_div64(a, b);
+}
+
+// The key tile of an item that a border `from` after the item's start cuts
+// before, or 0 if it goes to the item's start, or n to its end.  (The borders
+// keep their order.)
+__device__ __forceinline__ int cache_cut(const CacheFwdParams& p, int64_t from, const CacheReq& r) {
+  const int t = static_cast<int>(from < p.item_cost ? 0 : cache_div(from - p.item_cost, r.u));
+  if (t >= p.min_part && t <= r.n - p.min_part) return t;
+  const bool to_start = r.n >= 2 * p.min_part ? t < p.min_part : 2 * from < cache_len(p, r);
+  return to_start ? 0 : r.n;
 }
 
 // This CTA's range.  Run by every thread of the CTA (a whole number of warps, at
@@ -218,10 +222,10 @@ __device__ CacheRange cache_range(const CacheFwdParams& p, CacheRangeShared* sh,
         at += c;
         continue;
       }
-      const int len = r.n + p.item_cost;
-      const int64_t from_req = x - at;
-      const int from = static_cast<int>(from_req - cache_div(from_req, len) * len);
-      const int64_t moved = from_req - from + (cache_cuts(p, from, r.n) ? from : cache_moves(p, from, r.n));
+      const int len = cache_len(p, r);
+      const int64_t from_req = x - at, item0 = cache_div(from_req, len) * len;
+      const int cut = cache_cut(p, from_req - item0, r);
+      const int64_t moved = item0 + (cut == 0 ? 0 : p.item_cost + cut * r.u);
       sh->border[side] = at + moved;
       if (side == 0) {
         sh->b = b;
@@ -266,12 +270,13 @@ struct CacheWalk {
       cost = cache_cost(p, r);
       if (rem < cost) break;
     }
-    const int len = r.n + p.item_cost;
+    const int len = cache_len(p, r);
     const int64_t item = cache_div(rem, len);
     const int from = static_cast<int>(rem - item * len);
     step = static_cast<int>(min(static_cast<int64_t>(len - from), left));
-    tile0 = max(0, from - p.item_cost);  // (a border never lies in the lead)
-    count = from + step - p.item_cost - tile0;
+    // (a border lies between two tiles or items, never in the lead)
+    tile0 = static_cast<uint32_t>(max(0, from - p.item_cost)) / static_cast<uint32_t>(r.u);
+    count = static_cast<uint32_t>(from + step - p.item_cost) / static_cast<uint32_t>(r.u) - tile0;
     h = static_cast<int>(cache_div(item, r.rt));
     row_tile = static_cast<int>(item - static_cast<int64_t>(h) * r.rt);
     whole = count == r.n;
@@ -328,11 +333,13 @@ __device__ __forceinline__ void cache_open(const CacheFwdParams& p, const CacheR
   CacheJoin j{};
   if (R.ok && R.begin < R.end) {
     const CacheReq r = cache_req<KT>(p, R.b);
-    const int len = r.n + p.item_cost;
-    const int64_t item = cache_div(R.rem, len), from = R.rem - item * len;  // (len at a request's end: from is 0)
+    const int len = cache_len(p, r);
+    const int64_t item = cache_div(R.rem, len), from = R.rem - item * len;  // (at a request's end: from is 0)
     if (from > 0) {  // the range starts at a border that cuts the item; is it the first?
-      const int64_t before = from - R.per;  // the border before it, from the item's start
-      j.valid = before <= 0 || !cache_cuts(p, before, r.n);
+      const int64_t at = from + R.per * c - R.begin;  // the border before it was moved
+      const int64_t before = at - R.per;
+      const int cut = before <= 0 ? 0 : cache_cut(p, before, r);
+      j.valid = cut == 0;
       j.q0 = r.q0;
       j.T = r.T;
       j.h = static_cast<int>(cache_div(item, r.rt));
@@ -340,8 +347,8 @@ __device__ __forceinline__ void cache_open(const CacheFwdParams& p, const CacheR
       j.c0 = c - 1;
       j.c1 = c;
       // the last border that cuts it
-      const int64_t last = p.item_cost + r.n - p.min_part;
-      if (last > from) j.c1 = c + static_cast<int>(cache_div(last - from, static_cast<int>(min(R.per, static_cast<int64_t>(INT32_MAX)))));
+      const int64_t last = p.item_cost + static_cast<int64_t>(r.n - p.min_part + 1) * r.u - 1;
+      if (last > at) j.c1 = c + static_cast<int>(cache_div(last - at, static_cast<int>(min(R.per, static_cast<int64_t>(INT32_MAX)))));
     }
   }
   p.join[c] = j;

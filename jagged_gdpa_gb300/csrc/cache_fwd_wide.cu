@@ -32,7 +32,7 @@
 
 namespace jg {
 
-constexpr int kWideMinRange = 6;  // the least length of a range
+constexpr int kWideMinRange = 12;  // the least length of a range
 constexpr int kWideThreads = 384;
 
 // PAIR: items of more than 128 rows.
