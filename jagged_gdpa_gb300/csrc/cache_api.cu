@@ -321,9 +321,11 @@ jgdpa_status jgdpa_cache_fwd(const void* q, int64_t q_stride, const void* k_cach
   p.rows_per_tile = L.rows;
   p.tile_tokens = L.tokens;
   p.heads_per_item = L.heads;
-  // measured: an item's start and end take the time of about 8 tiles of 128 keys
-  // (two lengths each; 6 and 12: 10% more on ragged lengths), or of 4 tiles of 64
-  p.item_cost = L.wide ? 16 : 4;
+  // what an item's start and end take, measured: about 4 tiles of 64 keys, or in
+  // the 128-row kernel 14 half tiles of 128 keys, 24 with a bias table, whose
+  // tiles near the new tokens take longer (8 lengths off cost 5 to 10% on ragged
+  // lengths)
+  p.item_cost = L.wide ? (bias_len ? 24 : 14) : 4;
   p.min_part = L.wide ? 2 : 1;
   p.scale = act == JGDPA_ACT_SOFTMAX ? scale * jg::kLog2e : scale;
   p.wait_limit_ns = jg::host_wait_limit_ns();

@@ -342,53 +342,67 @@ __device__ void cw_mma(const CacheFwdParams& p, uint8_t* smem, CwShared* sh, uin
 // few times per item, and instructions fetched for the first time cost more
 // than the work (a fully unrolled tile took 2.1 us on its first run, 0.9 after).
 
-// Which of a tile's 128 keys a row sees (bit c of word k: key0 + 32 k + c).
-static __device__ __noinline__ uint4 cw_visible(const CacheFwdParams& p, CacheReq r, CcRow q, int key0) {
+// What a row needs to know of a tile's 128 keys, fetched before S is waited for:
+// which of them it sees (bit c of see[k]: key0 + 32 k + c), and in lane c the
+// positions of the keys key0 + 32 k + c (pos[k]; where the bias varies only).
+struct CwNear {
   uint32_t see[4];
+  int pos[4];
+};
+static __device__ __noinline__ CwNear cw_near(const CacheFwdParams& p, CacheReq r, CcRow q, bool plain, int key0) {
+  CwNear t;
+  const int lane = threadIdx.x & 31;
 #pragma unroll
-  for (int k = 0; k < 4; ++k) see[k] = cc_vis32(p, r, q, key0 + 32 * k);
-  if (p.window > 0) {
-    const int lane = threadIdx.x & 31;
+  for (int k = 0; k < 4; ++k) t.pos[k] = cc_pos(p, r, key0 + 32 * k + lane);
+#pragma unroll
+  for (int k = 0; k < 4; ++k) t.see[k] = plain ? 0xFFFFFFFFu : cc_vis32(p, r, q, key0 + 32 * k);
+  if (p.window > 0 && !plain) {
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      const int my_pos = cc_pos(p, r, key0 + 32 * k + lane);  // lane c: of key c
       uint32_t near = 0;
 #pragma unroll 4
-      for (int c = 0; c < 32; ++c) near |= (cc_near(p, q.pos, __shfl_sync(0xffffffffu, my_pos, c)) ? 1u : 0u) << c;
-      see[k] &= near;
+      for (int c = 0; c < 32; ++c) near |= (cc_near(p, q.pos, __shfl_sync(0xffffffffu, t.pos[k], c)) ? 1u : 0u) << c;
+      t.see[k] &= near;
     }
   }
-  return make_uint4(see[0], see[1], see[2], see[3]);
+  return t;
 }
 
 // S -> s S + bias (in log2 units for softmax) in place, for the tiles near the
 // new tokens, where the bias varies from key to key or some rows do not see
 // some keys (-inf for softmax, else 0, as act(0) = 0).
 template <int ACT>
-__device__ __noinline__ void cw_near_tile(const CacheFwdParams& p, CacheReq r, CcRow q, uint4 see, int key0, uint32_t t_s) {
-  const int lane = threadIdx.x & 31, reach = (p.bias_len - 1) / 2;
+__device__ __noinline__ void cw_near_tile(const CacheFwdParams& p, int C, CcRow q, CwNear t, int key0, uint32_t t_s) {
+  const int reach = (p.bias_len - 1) / 2;
+  const float* bias_row = p.bias + static_cast<int64_t>(q.head) * p.bias_len + reach;
 #pragma unroll 1
   for (int c0 = 0; c0 < kTile; c0 += 32) {
     uint32_t v[32];
     tmem_ld32(t_s + c0, v);
     // keys R or more behind every new token: one bias for all
-    const bool far = p.bias_len == 0 || key0 + c0 + 31 <= r.C - max(reach, 1);
-    const int my_pos = far ? 0 : cc_pos(p, r, key0 + c0 + lane);  // lane c: the position of key c0 + c
-    tmem_ld_wait(v);
+    const bool far = p.bias_len == 0 || key0 + c0 + 31 <= C - max(reach, 1);
     if (far) {
+      tmem_ld_wait(v);
 #pragma unroll
       for (int c = 0; c < 32; ++c) v[c] = __float_as_uint(__fmaf_rn(__uint_as_float(v[c]), p.scale, q.far_bias));
     } else {
+      float bias[32];
 #pragma unroll
-      for (int c = 0; c < 32; ++c) {
-        const float bias = cc_bias(p, q, reach, __shfl_sync(0xffffffffu, my_pos, c)) * cc_bias_unit<ACT>();
-        v[c] = __float_as_uint(__fmaf_rn(__uint_as_float(v[c]), p.scale, bias));
-      }
+      for (int c = 0; c < 32; ++c)
+        bias[c] = __ldg(bias_row + min(max(q.pos - __shfl_sync(0xffffffffu, t.pos[0], c), -reach), reach));
+      tmem_ld_wait(v);
+#pragma unroll
+      for (int c = 0; c < 32; ++c)
+        v[c] = __float_as_uint(__fmaf_rn(__uint_as_float(v[c]), p.scale, bias[c] * cc_bias_unit<ACT>()));
     }
 #pragma unroll
     for (int c = 0; c < 32; ++c)
-      if (!((see.x >> c) & 1)) v[c] = ACT == 2 ? 0xFF800000u : 0u;
-    see = make_uint4(see.y, see.z, see.w, 0u);
+      if (!((t.see[0] >> c) & 1)) v[c] = ACT == 2 ? 0xFF800000u : 0u;
+#pragma unroll
+    for (int k = 0; k < 3; ++k) {  // the next chunk's words come to the front
+      t.see[k] = t.see[k + 1];
+      t.pos[k] = t.pos[k + 1];
+    }
     tmem_st32(t_s + c0, v);
   }
   tmem_st_wait();
@@ -638,8 +652,8 @@ __device__ void cw_consumer(const CacheFwdParams& p, CwShared* sh, uint32_t tmem
     for (int i = 0; i < count; ++i) {
       const int tile = part.lo + part.at(stream, i);
       const bool far = tile < part.far_hi, plain = part.plain(tile);
-      uint4 see = make_uint4(0xFFFFFFFFu, 0xFFFFFFFFu, 0xFFFFFFFFu, 0xFFFFFFFFu);
-      if (!plain && warp_live) see = cw_visible(p, r, q, tile * kTile);  // (its loads before S is waited for)
+      CwNear near;
+      if ((!plain || !far) && warp_live) near = cw_near(p, r, q, plain, tile * kTile);
       if (!dead && !mbar_wait(&sh->s_full[stream], s_n & 1, fail)) dead = true;
       dead = __any_sync(0xffffffffu, dead);
       ++s_n;
@@ -648,7 +662,7 @@ __device__ void cw_consumer(const CacheFwdParams& p, CwShared* sh, uint32_t tmem
       if (warp_live) {
         float scale = p.scale, bias = q.far_bias;
         if (!far || !plain) {
-          cw_near_tile<ACT>(p, r, q, see, tile * kTile, t_s);
+          cw_near_tile<ACT>(p, r.C, q, near, tile * kTile, t_s);
           scale = 1.f;
           bias = 0.f;
         }
