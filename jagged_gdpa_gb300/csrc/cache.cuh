@@ -137,13 +137,18 @@ __device__ __forceinline__ bool cache_req_ok(const CacheFwdParams& p, const Cach
 }
 
 // Work division.  The items are (request, kv head, row tile), each a lead of
-// item_cost, what its start and end take, and n key tiles of length u; laid end to end (request by request, row tiles of one head next
-// to each other so that they meet in L2) they form one line that is cut into
-// equal ranges, one per CTA, whatever the lengths.  (Without the lead, ranges
-// that fall on many short requests took half as long again as the others.)  A
-// border inside an item cuts it, and the joining kernel puts the parts together;
-// a border that would leave a part of fewer than min_part tiles moves to the
-// item's start or end.
+// item_cost, what its start and end take, and n key tiles of length u.  Laid end
+// to end (request by request, row tiles of a head next to each other) they form
+// one line that is cut into equal ranges, one per CTA, whatever the lengths.
+// (Without the lead, ranges that fall on many short requests took half as long
+// again as the others.)  A border inside an item cuts it, and the joining kernel
+// puts the parts together; a border that would leave a part of fewer than
+// min_part tiles moves to the item's start or end.
+//
+// A CTA that gets several row tiles of one head reads its keys from HBM for
+// each.  Laying the row tiles of 512-row requests out in two passes over the
+// batch, so that two CTAs read them at once, left the time as it was: those
+// items are bound by their products.
 struct CacheRange {
   int64_t per, begin, end;
   int b;        // request that `begin` lies in (or at the end of)
