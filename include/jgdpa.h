@@ -315,8 +315,10 @@ JGDPA_API jgdpa_status jgdpa_bwd_shared_q(const void* q, int32_t n_shared, const
  *                  jgdpa_cache_fwd
  *   slots          int32 [total_new], the slot of each new token in request
  *                  order; -1 in rows behind the last
- * held_out, kv_lens and free_count_out must not overlap the inputs.  The same
- * call on the same inputs may be repeated: it writes the same values.
+ * The outputs that are not updated in place must not overlap the inputs or one
+ * another, and a page must stand at most once in the stack and the rows' held
+ * entries.  The same call on the same inputs may be repeated: it writes the same
+ * values.
  * Device-detected errors: BAD_OFFSETS (negative lengths, more tokens than
  * table_width pages or total_new rows hold, counts beyond num_pages),
  * OUT_OF_PAGES.  Such a call hands out nothing: table and stack are not
@@ -366,6 +368,7 @@ JGDPA_API jgdpa_status jgdpa_cache_append(const void* k_new, const void* v_new, 
  *                index is clamp(pos_i - pos_j, -R, R) + R and a window w > 0
  *                keeps pairs with |pos_i - pos_j| < w
  *   act, scale, bias_table, bias_len   as in jgdpa_fwd, bias_table [heads]
+ *                [bias_len]; a softmax bias of -inf hides a key
  *   out          bf16 [total_q][heads][head_dim]
  *   lse          fp32 [heads][total_q] in SOFTMAX mode, or NULL; NULL otherwise
  * Every token sees the whole context (within the window).  A token that sees
@@ -373,10 +376,10 @@ JGDPA_API jgdpa_status jgdpa_cache_append(const void* k_new, const void* v_new, 
  * the rows that see their token; places of a page behind kv_lens[b] may hold
  * anything.  Same bits on every run, whatever else runs beside it.
  * Device-detected errors: BAD_OFFSETS (offsets not monotone from 0, beyond
- * total_q, T_b > max_q, kv_lens[b] < T_b or beyond the table), in which case
- * nothing is written; BAD_PAGE (a table entry of a live token outside
- * [0, num_pages)): no such page is read, and its request's outputs are
- * unspecified.
+ * total_q, T_b > max_q or more than the tree mask's columns, kv_lens[b] < T_b or
+ * beyond the table), in which case nothing is written; BAD_PAGE (a table entry
+ * of a live token outside [0, num_pages)): no such page is read, and its
+ * request's outputs are unspecified.
  */
 JGDPA_API size_t jgdpa_cache_fwd_workspace_bytes(int32_t heads, int32_t kv_heads, int32_t head_dim, int32_t max_q);
 JGDPA_API jgdpa_status jgdpa_cache_fwd(const void* q, int64_t q_stride, const void* k_cache, const void* v_cache,

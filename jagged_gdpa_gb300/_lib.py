@@ -658,6 +658,9 @@ def _refuse_fwd(q, k_cache, v_cache, block_table, q_offsets, kv_lens, softmax, b
         raise ValueError("lse is written in softmax mode only; pass None")
     _check(lse, "lse", torch.float32, (heads, total_q), device, optional=True)
     _check_bytes(workspace, "workspace", device)
+    for t, name in ((bias_table, "bias_table"), (tree_mask, "tree_mask")):
+        if t is not None and t.shape[1] == 0:
+            raise ValueError(f"{name} must have columns; pass None for none")
     _refuse_rows(q, "q", heads, d)
     _contiguous(block_table=block_table, q_offsets=q_offsets, kv_lens=kv_lens, bias_table=bias_table,
                 tree_mask=tree_mask, depths=depths, out=out, lse=lse, workspace=workspace)
@@ -687,10 +690,10 @@ def jgdpa_cache_fwd(q, k_cache, v_cache, block_table, q_offsets, kv_lens, act, s
               and _is(kv_lens, _i32, (batch,), index))
         if ok and bias_table is not None:
             bias, bias_len = bias_table.data_ptr(), bias_table.shape[1]
-            ok = _is(bias_table, _f32, (heads, bias_len), index)
+            ok = bias_len > 0 and _is(bias_table, _f32, (heads, bias_len), index)
         if ok and tree_mask is not None:
             mask, words = tree_mask.data_ptr(), tree_mask.shape[1]
-            ok = _is(tree_mask, _i32, (total_q, words), index)
+            ok = words > 0 and _is(tree_mask, _i32, (total_q, words), index)
         if ok and depths is not None:
             depth = depths.data_ptr()
             ok = _is(depths, _i32, (total_q,), index)

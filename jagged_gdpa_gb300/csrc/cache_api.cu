@@ -75,7 +75,7 @@ bool cache_layout(int32_t heads, int32_t kv_heads, int32_t head_dim, int32_t max
     L->grid = sms;
     L->heads = 1;
   } else {
-    // small heads side by side; measured at d = 32, 16 heads, 8 tokens: see the kernel
+    // small heads side by side (measured: see the kernel's CcCfg)
     L->heads = kv_heads % (128 / head_dim) == 0 ? 128 / head_dim : 1;
     L->rows = max_rows <= 16 ? 16 : 32;
     L->pairs = false;
@@ -256,7 +256,7 @@ jgdpa_status jgdpa_cache_fwd(const void* q, int64_t q_stride, const void* k_cach
   if (bias_len < 0 || (bias_len > 0) != (bias_table != nullptr) || (bias_len > 0 && bias_len % 2 == 0))
     return JGDPA_ERR_INVALID_ARGUMENT;
   if (bias_len > jg::kMaxBiasLen) return JGDPA_ERR_UNSUPPORTED;
-  if ((mask_words > 0) != (tree_mask != nullptr)) return JGDPA_ERR_INVALID_ARGUMENT;
+  if (total_q > 0 && (mask_words > 0) != (tree_mask != nullptr)) return JGDPA_ERR_INVALID_ARGUMENT;
   if (act != JGDPA_ACT_SOFTMAX && lse != nullptr) return JGDPA_ERR_INVALID_ARGUMENT;
   const int64_t max_rows = static_cast<int64_t>(max_q) * (heads / kv_heads);
   if (total_q > INT32_MAX || batch > jg::kCacheMaxBatch || max_rows > INT32_MAX / 2 ||

@@ -202,6 +202,15 @@ def test_wrapper_rejects_bad_tensors(jg, field, change, match):
         jg.jgdpa_cache_fwd(**kw)
 
 
+@pytest.mark.parametrize("field", ["tree_mask", "bias_table"])
+def test_wrapper_rejects_tables_without_columns(jg, field):
+    """They would reach the library as no mask, or no bias."""
+    kw = Case(0, [40, 20], [3, 4], 2, 2, 64, 16, bias=5, mask=True).kwargs("cpu")
+    kw[field] = kw[field][:, :0]
+    with pytest.raises(ValueError, match=f"{field} must have columns"):
+        jg.jgdpa_cache_fwd(**kw)
+
+
 def test_wrappers_reject_other_bad_calls(jg):
     c = Case(0, [40], [3], 2, 2, 64, 16)
     kw = c.kwargs("cpu")
@@ -449,6 +458,21 @@ def test_rows_that_see_nothing(jg, act, new):
 
 
 @gpu
+@pytest.mark.parametrize("new", [1, 20, 70])
+@pytest.mark.parametrize("value", [-float("inf"), torch.finfo(torch.float32).min])
+def test_bias_entries_that_hide_keys(jg, new, value):
+    """Softmax with bias entries of -inf or the lowest fp32: keys 12 and more
+    behind get no weight, whole tiles of them among the others."""
+    c = Case(17, [700, 0, 129, 64], [new] * 4, 2, 2, 64, 32, "softmax", bias=33)
+    c.bias[:, 28:] = value
+    out, lse = jg.jgdpa_cache_fwd(**c.kwargs())
+    compare(c, out, lse)
+    c.bias[1] = -float("inf")  # a head that sees nothing
+    out, lse = jg.jgdpa_cache_fwd(**c.kwargs())
+    assert not out[:, 1].any() and torch.isneginf(lse[1]).all() and torch.isfinite(lse[0]).all()
+
+
+@gpu
 @pytest.mark.parametrize("act", ["gelu", "silu", "softmax"])
 @pytest.mark.parametrize("new,group", [(6, 2), (30, 4), (40, 8)])
 def test_infinities_reach_only_the_rows_that_see_them(jg, act, new, group):
@@ -562,6 +586,37 @@ def test_empty_calls(jg):
     kw = c.kwargs()
     kw.update(block_table=kw["block_table"][:0], q_offsets=i32([0], "cuda"), kv_lens=i32([], "cuda"))
     jg.jgdpa_cache_fwd(**kw)
+
+
+@gpu
+def test_empty_call_with_a_mask(jg):
+    kw = Case(1, [5, 40], [3, 2], 1, 1, 64, 16, "softmax", mask=True).kwargs()
+    for k in ("q", "tree_mask", "depths"):
+        kw[k] = kw[k][:0]
+    kw["q_offsets"] = torch.zeros_like(kw["q_offsets"])
+    out, lse = jg.jgdpa_cache_fwd(**kw)
+    assert out.shape[0] == 0 and lse.shape[1] == 0
+
+
+@gpu
+@pytest.mark.parametrize("ended", [0.0, 0.6])
+def test_plan_with_many_pages_back(jg, ended):
+    """Far more pages come back than tokens are added."""
+    rng = np.random.default_rng(31)
+    batch, width = 300, 400
+    held = rng.integers(0, width + 1, batch)
+    ctx = np.where(rng.random(batch) < ended, 0, np.maximum(0, held * 16 - rng.integers(0, 40, batch)))
+    new = np.where(ctx > 0, rng.integers(0, 3, batch), 0)
+    new = np.minimum(new, width * 16 - ctx)
+    pages = int(held.sum()) + 50
+    ids = rng.permutation(pages)
+    table = np.full((batch, width), -5)
+    at = np.concatenate([[0], np.cumsum(held)])
+    for b in range(batch):
+        table[b, :held[b]] = ids[at[b]:at[b + 1]]
+    free = np.full(pages, -9)
+    free[:50] = ids[at[-1]:]
+    check_plan(jg, ctx, new, held, table, free, 50, 16, int(new.sum()) + 5)
 
 
 @gpu
