@@ -19,6 +19,14 @@ enum : int { kErrOutOfPages = 8, kErrBadPage = 9 };
 
 constexpr int kCacheMaxBatch = 16384;  // requests per call (the plan's prefix sums live in shared memory)
 
+// Query rows per key/value head up to which the kernel for few rows
+// (cache_fwd.cu) runs, and the 128-row one (cache_fwd_wide.cu) from there on.
+// At 24 rows, 64 requests of 4,100 tokens, 32-row tiles of the former took 264 us
+// against 183 at d = 128 and 172 against 153 at d = 64 (76 against 87 on 256
+// requests of 100 to 800 tokens), but 240 against 240 at d = 32, and 180 against
+// 288 on the short requests.
+__host__ __device__ constexpr int cache_narrow_rows(int d) { return d == 32 ? 32 : 16; }
+
 // CTAs per SM of the attention kernel for up to 16 mt rows and w columns of K
 // and V per item (cache_fwd.cu).
 __host__ __device__ constexpr int cache_ctas(int w, int mt) {

@@ -67,7 +67,7 @@ bool cache_layout(int32_t heads, int32_t kv_heads, int32_t head_dim, int32_t max
   const int group = heads / kv_heads;
   const int64_t max_rows = static_cast<int64_t>(max_q) * group;
   // (a tile of the wide kernel holds whole tokens, so at most 128 heads share a key/value head there)
-  L->wide = max_rows > 32 && group <= jg::kTile;
+  L->wide = max_rows > jg::cache_narrow_rows(head_dim) && group <= jg::kTile;
   if (L->wide) {
     L->tokens = std::min(jg::kTile / group, max_q);
     L->pairs = max_q > L->tokens;
@@ -77,7 +77,7 @@ bool cache_layout(int32_t heads, int32_t kv_heads, int32_t head_dim, int32_t max
   } else {
     // small heads side by side (measured: see the kernel's CcCfg)
     L->heads = kv_heads % (128 / head_dim) == 0 ? 128 / head_dim : 1;
-    L->rows = max_rows <= 16 ? 16 : 32;
+    L->rows = max_rows <= 16 ? 16 : jg::cache_narrow_rows(head_dim);
     L->pairs = false;
     L->tokens = 0;
     L->grid = sms * jg::cache_ctas(head_dim * L->heads, L->rows / 16);

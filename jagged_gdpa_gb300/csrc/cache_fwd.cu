@@ -43,7 +43,7 @@ struct CcCfg {
   // SM (at d = 128, 64 KB reached 0.67 of the copy bandwidth on one long
   // request, 128 KB 0.82)
   static constexpr int kCtas = cache_ctas(W, MT);
-  static constexpr int kStages = MT == 1 ? (W == 128 ? 3 : W == 64 ? 4 : 5) : (W == 128 ? 6 : W == 64 ? 5 : 10);
+  static constexpr int kStages = MT == 1 ? (W == 128 ? 3 : W == 64 ? 4 : 5) : (W == 128 ? 6 : 10);
   static constexpr int kSlotBytes = 16 * kCChunk * 4;  // one warp's chunk of O
   static constexpr int kOOff = kStages * 2 * kTileBytes;
   static constexpr int kBarOff = kOOff + kWarps * kSlotBytes;
@@ -308,17 +308,17 @@ __device__ void cc_consumer(const CacheFwdParams& p, uint8_t* smem, CcShared<MT,
           }
           float(&pv)[2][4] = s;  // in place
           if constexpr (ACT == 2) {
+            // m need not be the maximum, only within 8 (in log2 units) of it or
+            // above: weights up to 2^8, and a step, with the exchange between the
+            // lanes of a row, that most tiles skip (5% at d = 32)
             float mx[2];
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              mx[i] = fmaxf(fmaxf(s[0][2 * i], s[0][2 * i + 1]), fmaxf(s[1][2 * i], s[1][2 * i + 1]));
-              mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], 1));
-              mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], 2));
-            }
-            if (__any_sync(0xffffffffu, mx[0] > m[hh][0] || mx[1] > m[hh][1])) {
+            for (int i = 0; i < 2; ++i) mx[i] = fmaxf(fmaxf(s[0][2 * i], s[0][2 * i + 1]), fmaxf(s[1][2 * i], s[1][2 * i + 1]));
+            if (__any_sync(0xffffffffu, mx[0] > m[hh][0] + 8.f || mx[1] > m[hh][1] + 8.f)) {
 #pragma unroll
               for (int i = 0; i < 2; ++i) {
-                const float mn = fmaxf(m[hh][i], mx[i]);
+                mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], 1));
+                const float mn = fmaxf(m[hh][i], fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], 2)));
                 const float f = mn == -INFINITY ? 1.f : ex2_sfu(m[hh][i] - mn);
                 m[hh][i] = mn;
                 l[hh][i] *= f;
@@ -624,14 +624,18 @@ static cudaError_t launch_cc(const CacheFwdParams& p, int grid, cudaStream_t str
   return cache_launch(kern, dim3(grid), C::kThreads, C::kSmemBytes, stream, p);
 }
 
+template <int D, int ACT, int HP>
+static cudaError_t launch_cc_rows(const CacheFwdParams& p, int grid, cudaStream_t stream) {
+  if constexpr (cache_narrow_rows(D) > 16)
+    if (p.rows_per_tile > 16) return launch_cc<D, ACT, 2, HP>(p, grid, stream);
+  return launch_cc<D, ACT, 1, HP>(p, grid, stream);
+}
+
 template <int D, int ACT>
 static cudaError_t launch_cc_act(const CacheFwdParams& p, int grid, cudaStream_t stream) {
-  if constexpr (D < 128) {
-    if (p.heads_per_item > 1)
-      return p.rows_per_tile == 16 ? launch_cc<D, ACT, 1, 128 / D>(p, grid, stream)
-                                   : launch_cc<D, ACT, 2, 128 / D>(p, grid, stream);
-  }
-  return p.rows_per_tile == 16 ? launch_cc<D, ACT, 1, 1>(p, grid, stream) : launch_cc<D, ACT, 2, 1>(p, grid, stream);
+  if constexpr (D < 128)
+    if (p.heads_per_item > 1) return launch_cc_rows<D, ACT, 128 / D>(p, grid, stream);
+  return launch_cc_rows<D, ACT, 1>(p, grid, stream);
 }
 
 template <int D>

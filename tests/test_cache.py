@@ -458,6 +458,21 @@ def test_rows_that_see_nothing(jg, act, new):
 
 
 @gpu
+@pytest.mark.parametrize("up", [True, False])
+@pytest.mark.parametrize("d,new", [(32, 3), (128, 1), (64, 8), (32, 30), (64, 24), (128, 50)])
+def test_scores_that_rise_and_fall(jg, d, new, up):
+    """Softmax whose scores grow (or shrink) along the keys, a little per tile
+    and by jumps: the running maximum has to follow."""
+    c = Case(23, [900, 77], [new, new], 4, 2, d, 64, "softmax", nan=False)
+    for b, n in enumerate(c.kv):
+        for j in range(n):
+            at = j / n if up else 1 - j / n
+            c.k[c.table[b, j // 64], j % 64] *= 8.0 * at ** 2 + (12.0 if at > 0.8 else 0.0)
+    out, lse = jg.jgdpa_cache_fwd(**c.kwargs())
+    compare(c, out, lse)
+
+
+@gpu
 @pytest.mark.parametrize("new", [1, 20, 70])
 @pytest.mark.parametrize("value", [-float("inf"), torch.finfo(torch.float32).min])
 def test_bias_entries_that_hide_keys(jg, new, value):
