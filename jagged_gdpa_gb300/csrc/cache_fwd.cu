@@ -47,16 +47,18 @@ struct CcCfg {
   static constexpr int kSlotBytes = 16 * kCChunk * 4;  // one warp's chunk of O
   static constexpr int kOOff = kStages * 2 * kTileBytes;
   static constexpr int kBarOff = kOOff + kWarps * kSlotBytes;
-  static constexpr int kSmemBytes = kBarOff + 768 + kWarps * HP * 16 * 8 + 1024;
+  static constexpr int kSmemBytes = kBarOff + 768 + kWarps * 16 * 8 + 1024;
+  // A group's warps: a head each, or a head's keys shared by several
+  static constexpr int kKeyGroups = kCGroupWarps / HP;
   static_assert(kSmemBytes <= 233472 / kCtas - 1024, "shared memory per CTA");
 };
 
-template <int MT, int HP>
+template <int MT>
 struct CcShared {
   uint64_t full[16], empty[16];
   CacheRangeShared range;
   int abort;
-  float2 ml[MT * kCGroupWarps][HP][16];  // a warp's maxima and sums
+  float2 ml[MT * kCGroupWarps][16];  // a warp's maxima and sums
 };
 
 __device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
@@ -89,7 +91,7 @@ __device__ __forceinline__ uint32_t cc_offset(int n, int c, int pr) {
 
 // ------------------------------------------------------------- producer
 template <int W, int MT, int HP>
-__device__ void cc_producer(const CacheFwdParams& p, uint8_t* smem, CcShared<MT, HP>* sh, const CacheRange& R, Fail fail) {
+__device__ void cc_producer(const CacheFwdParams& p, uint8_t* smem, CcShared<MT>* sh, const CacheRange& R, Fail fail) {
   using C = CcCfg<W, MT, HP>;
   const int lane = threadIdx.x & 31;
   const uint32_t base = smem_u32(smem);
@@ -134,25 +136,35 @@ __device__ void cc_producer(const CacheFwdParams& p, uint8_t* smem, CcShared<MT,
 
 // ------------------------------------------------------------- consumers
 template <int D, int ACT, int MT, int HP>
-__device__ void cc_consumer(const CacheFwdParams& p, uint8_t* smem, CcShared<MT, HP>* sh, const CacheRange& R, Fail fail) {
+__device__ void cc_consumer(const CacheFwdParams& p, uint8_t* smem, CcShared<MT>* sh, const CacheRange& R, Fail fail) {
   constexpr int W = D * HP;
   using C = CcCfg<W, MT, HP>;
   constexpr int KS = D / 16;  // k steps of S = Q K^T
   constexpr int NT = D / 8;   // n tiles of O
   constexpr int kRows = 16 * MT;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int grp = warp / kCGroupWarps, kw = warp % kCGroupWarps;
+  constexpr int KG = C::kKeyGroups, KB = HP;  // warps that share a head's keys, blocks of 16 keys of a warp
+  static_assert(KB * KG * 16 == kCKeys, "keys of a tile");
+  const int grp = warp / kCGroupWarps, hw = warp % kCGroupWarps / KG, kg = warp % KG;  // which rows, head, keys
   const int pr = min(1 << p.page_shift, kCKeys);
   const uint32_t base = smem_u32(smem);
-  // this warp's 16 keys: piece addresses for ldmatrix (the four 8x8 blocks of
-  // a load are keys 0-7 / 8-15 by 16-byte piece for K, and transposed for V);
-  // the lane's part of an address is fixed, a piece comes in by exclusive or
+  // this warp's keys: piece addresses for ldmatrix (the four 8x8 blocks of a
+  // load are keys 0-7 / 8-15 by 16-byte piece for K, and transposed for V); the
+  // lane's part of an address is fixed, a piece comes in by exclusive or, a
+  // block of 16 keys by addition
   const int half = W >= 64 ? pr * 128 : 0;  // bytes of a box's column half
-  const uint32_t kl = cc_offset<W>(16 * kw + (lane & 7) + ((lane & 16) ? 8 : 0), (lane >> 3) & 1, pr);
-  const uint32_t vl = cc_offset<W>(16 * kw + (lane & 7) + ((lane & 8) ? 8 : 0), lane >> 4, pr);
-  auto piece = [&](uint32_t at, int c) {  // of the even piece c
+  auto head_at = [&](uint32_t at) {         // the warp's head's first piece
+    return W >= 64 ? (at ^ ((hw * (D / 8) & 7) << 4)) + (hw * D >= 64 ? half : 0) : at;
+  };
+  const int first = 16 * KB * kg;
+  const uint32_t kl = head_at(cc_offset<W>(first + (lane & 7) + ((lane & 16) ? 8 : 0), (lane >> 3) & 1, pr));
+  const uint32_t vl = head_at(cc_offset<W>(first + (lane & 7) + ((lane & 8) ? 8 : 0), lane >> 4, pr));
+  auto piece = [&](uint32_t at, int c) {  // of the head's even piece c
     return (at ^ ((c & (W >= 64 ? 6 : 2)) << 4)) + (W >= 64 && c >= 8 ? half : 0);
   };
+  const uint32_t row_bytes = W >= 64 ? 128 : 64;
+  const uint32_t step1 = 16 * (pr >= 32 ? row_bytes : 2 * W), step2 = 32 * (pr >= 64 ? row_bytes : 2 * W);
+  auto block = [&](int kb) { return (kb & 1) * step1 + (kb >> 1) * step2; };
   const int reach = (p.bias_len - 1) / 2;
   uint32_t it = 0;
   bool dead = false;
@@ -163,9 +175,9 @@ __device__ void cc_consumer(const CacheFwdParams& p, uint8_t* smem, CcShared<MT,
     int lo, hi;
     w.template tiles<kCKeys>(p, lo, hi);
     const int n_rows = min(kRows, r.T * p.group - w.row_tile * kRows);
-    CcRow rows[2];  // lane / 4 and lane / 4 + 8 of the warp's 16, of the item's first head
+    CcRow rows[2];  // lane / 4 and lane / 4 + 8 of the warp's 16
     const __nv_bfloat16* qrow[2];
-    float far_bias[HP][2];
+    float far_bias[2];
     int pos_min = INT32_MAX;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
@@ -174,7 +186,7 @@ __device__ void cc_consumer(const CacheFwdParams& p, uint8_t* smem, CcShared<MT,
       CcRow& q = rows[i];
       const int t = static_cast<uint32_t>(flat) / static_cast<uint32_t>(p.group);
       q.t = lr < n_rows ? t : -1;
-      q.head = w.h * HP * p.group + (lr < n_rows ? flat - t * p.group : 0);
+      q.head = (w.h * HP + hw) * p.group + (lr < n_rows ? flat - t * p.group : 0);
       q.pos = r.C;
       q.far_bias = 0.f;
       qrow[i] = nullptr;
@@ -183,214 +195,224 @@ __device__ void cc_consumer(const CacheFwdParams& p, uint8_t* smem, CcShared<MT,
         qrow[i] = p.q + static_cast<int64_t>(r.q0 + q.t) * p.q_stride + static_cast<int64_t>(q.head) * D;
         pos_min = min(pos_min, q.pos);
       }
-#pragma unroll
-      for (int hh = 0; hh < HP; ++hh)
-        far_bias[hh][i] = q.t >= 0 && p.bias_len ? __ldg(p.bias + static_cast<int64_t>(q.head + hh * p.group) * p.bias_len +
-                                                         2 * reach) * cc_bias_unit<ACT>()
-                                                 : 0.f;
+      far_bias[i] = q.t >= 0 && p.bias_len
+                        ? __ldg(p.bias + static_cast<int64_t>(q.head) * p.bias_len + 2 * reach) * cc_bias_unit<ACT>()
+                        : 0.f;
     }
     pos_min = __reduce_min_sync(0xffffffffu, pos_min);
     const int pos_max = __reduce_max_sync(0xffffffffu, max(rows[0].t >= 0 ? rows[0].pos : 0, rows[1].t >= 0 ? rows[1].pos : 0));
     // Q fragments: rows lane / 4 (+ 8), columns 16 ks + 2 (lane % 4) (+ 8)
-    uint32_t qa[HP][KS][4];
+    uint32_t qa[KS][4];
 #pragma unroll
-    for (int hh = 0; hh < HP; ++hh)
+    for (int ks = 0; ks < KS; ++ks)
 #pragma unroll
-      for (int ks = 0; ks < KS; ++ks)
+      for (int e = 0; e < 4; ++e) {
+        const __nv_bfloat16* src = qrow[e & 1];
+        qa[ks][e] = src != nullptr ? __ldg(reinterpret_cast<const uint32_t*>(src + 16 * ks + 2 * (lane & 3) + ((e & 2) ? 8 : 0))) : 0u;
+      }
+    float o[NT][4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const __nv_bfloat16* src = qrow[e & 1];
-          const int64_t at = static_cast<int64_t>(hh) * p.group * D + 16 * ks + 2 * (lane & 3) + ((e & 2) ? 8 : 0);
-          qa[hh][ks][e] = src != nullptr ? __ldg(reinterpret_cast<const uint32_t*>(src + at)) : 0u;
-        }
-    float o[HP][NT][4];
-    float m[HP][2], l[HP][2];
+    for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-    for (int hh = 0; hh < HP; ++hh) {
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) o[hh][nt][e] = 0.f;
-      m[hh][0] = m[hh][1] = -INFINITY;
-      l[hh][0] = l[hh][1] = 0.f;
-    }
+      for (int e = 0; e < 4; ++e) o[nt][e] = 0.f;
+    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
 
     for (int t = lo; t < hi; ++t, ++it) {
       const int st = it % C::kStages;
       if (!dead && !mbar_wait(&sh->full[st], (it / C::kStages) & 1, fail)) dead = true;
       dead = __any_sync(0xffffffffu, dead);
-      const int key0 = t * kCKeys + 16 * kw;  // this warp's first key
+      const int key0 = t * kCKeys + first;  // this warp's first key
       if (!dead && key0 < r.L) {
-        const uint32_t kb = base + st * 2 * C::kTileBytes, vb = kb + C::kTileBytes;
-        // plain: every key of these 16 is seen by every row; far: R or more behind
-        const int last = key0 + 15;
+        const uint32_t kt = base + st * 2 * C::kTileBytes, vt = kt + C::kTileBytes;
+        // plain: every key of the warp's is seen by every row; far: R or more behind
+        const int last = key0 + 16 * KB - 1;
         const bool plain = last < r.C && (p.window <= 0 || pos_max - key0 < p.window);
         const bool far = p.bias_len == 0 || (last < r.C && pos_min - last >= reach);
-        uint32_t see[2] = {0xFFFFu, 0xFFFFu}, keep[2] = {0xFFFFFFFFu, 0xFFFFFFFFu};
+        uint32_t see[(KB + 1) / 2][2];  // by 32 keys
         bool odd = false;
         if (!plain) {
           // Some rows do not see some of these keys, and 0 * NaN = NaN: rows of
-          // V past the request's end (whatever the page held) count as zeros
-          // (`keep`), and where others hold an infinity or NaN (`odd`) those
-          // are left out of the product and added to the rows that see them.
-#pragma unroll 1
-          for (int h = 0; h < 2; ++h) {
-            uint32_t bits = cc_vis32(p, r, h == 0 ? rows[0] : rows[1], key0);
-            if (p.window > 0) {
-              uint32_t near = 0;
-#pragma unroll 1
-              for (int c = 0; c < 4; ++c) {
-                const int col = 8 * (c >> 1) + 2 * (lane & 3) + (c & 1);
-                near |= (cc_near(p, h == 0 ? rows[0].pos : rows[1].pos, cc_pos(p, r, key0 + col)) ? 1u : 0u) << col;
-              }
-              bits &= near;  // (only this lane's columns are kept)
-            }
-            if (h == 0) see[0] = bits;
-            else see[1] = bits;
-          }
+          // V past the request's end (whatever the page held) count as zeros,
+          // and where others hold an infinity or NaN (`odd`) those are left out
+          // of the product and added to the rows that see them.
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const int j = key0 + 8 * i + 2 * (lane & 3);
-            keep[i] = j + 1 < r.L ? 0xFFFFFFFFu : (j < r.L ? 0xFFFFu : 0u);
-          }
+          for (int j = 0; j < (KB + 1) / 2; ++j)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              uint32_t bits = cc_vis32(p, r, rows[h], key0 + 32 * j);
+              if (p.window > 0) {
+                uint32_t near = 0;
+#pragma unroll 1
+                for (int c = 0; c < (KB > 1 ? 8 : 4); ++c) {
+                  const int col = 8 * (c >> 1) + 2 * (lane & 3) + (c & 1);
+                  near |= (cc_near(p, rows[h].pos, cc_pos(p, r, key0 + 32 * j + col)) ? 1u : 0u) << col;
+                }
+                bits &= near;  // (only this lane's columns are kept)
+              }
+              see[j][h] = bits;
+            }
           const __nv_bfloat162 zero = __float2bfloat162_rn(0.f);
           __nv_bfloat162 sum = zero;  // of 0 * v
-          if (key0 + (lane & 15) < r.L) {
 #pragma unroll 1
-            for (int c = lane >> 4; c < W / 8; c += 2) {
+          for (int k = lane & 15; k < 16 * KB && key0 + k < r.L; k += 16)
+#pragma unroll 1
+            for (int c = lane >> 4; c < D / 8; c += 2) {
               uint32_t x[4];
-              ld_shared_v4(vb + cc_offset<W>(16 * kw + (lane & 15), c, pr), x[0], x[1], x[2], x[3]);
+              ld_shared_v4(vt + cc_offset<W>(first + k, hw * (D / 8) + c, pr), x[0], x[1], x[2], x[3]);
 #pragma unroll
               for (int e = 0; e < 4; ++e) sum = __hfma2(*reinterpret_cast<__nv_bfloat162*>(&x[e]), zero, sum);
             }
-          }
           odd = __any_sync(0xffffffffu, !(__low2float(sum) == 0.f && __high2float(sum) == 0.f));
         }
+        float s[KB][2][4];
 #pragma unroll
-        for (int hh = 0; hh < HP; ++hh) {
-          float s[2][4];
+        for (int kb = 0; kb < KB; ++kb)
 #pragma unroll
           for (int i = 0; i < 2; ++i)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) s[i][e] = 0.f;
+            for (int e = 0; e < 4; ++e) s[kb][i][e] = 0.f;
 #pragma unroll
-          for (int ks = 0; ks < KS; ++ks) {
+        for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+          for (int kb = 0; kb < KB; ++kb) {
             uint32_t b[4];
-            ldsm4(piece(kb + kl, hh * (D / 8) + 2 * ks), b);
-            mma16816(s[0], qa[hh][ks], b[0], b[1]);
-            mma16816(s[1], qa[hh][ks], b[2], b[3]);
+            ldsm4(piece(kt + block(kb) + kl, 2 * ks), b);
+            mma16816(s[kb][0], qa[ks], b[0], b[1]);
+            mma16816(s[kb][1], qa[ks], b[2], b[3]);
           }
-          if (far) {
+        if (far) {
+#pragma unroll
+          for (int kb = 0; kb < KB; ++kb)
 #pragma unroll
             for (int i = 0; i < 2; ++i)
 #pragma unroll
-              for (int e = 0; e < 4; ++e) s[i][e] = __fmaf_rn(s[i][e], p.scale, far_bias[hh][e >> 1]);
-          } else {
+              for (int e = 0; e < 4; ++e) s[kb][i][e] = __fmaf_rn(s[kb][i][e], p.scale, far_bias[e >> 1]);
+        } else {
+#pragma unroll
+          for (int kb = 0; kb < KB; ++kb)
 #pragma unroll
             for (int i = 0; i < 2; ++i)
 #pragma unroll
               for (int c = 0; c < 2; ++c) {
-                const int key_pos = cc_pos(p, r, key0 + 8 * i + 2 * (lane & 3) + c);
+                const int key_pos = cc_pos(p, r, key0 + 16 * kb + 8 * i + 2 * (lane & 3) + c);
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                  CcRow q = rows[h];
-                  q.head += hh * p.group;
-                  s[i][2 * h + c] = __fmaf_rn(s[i][2 * h + c], p.scale, cc_bias(p, q, reach, key_pos) * cc_bias_unit<ACT>());
-                }
+                for (int h = 0; h < 2; ++h)
+                  s[kb][i][2 * h + c] =
+                      __fmaf_rn(s[kb][i][2 * h + c], p.scale, cc_bias(p, rows[h], reach, key_pos) * cc_bias_unit<ACT>());
               }
-          }
-          if (!plain) {
+        }
+        if (!plain) {
+#pragma unroll
+          for (int kb = 0; kb < KB; ++kb)
 #pragma unroll
             for (int i = 0; i < 2; ++i)
 #pragma unroll
               for (int e = 0; e < 4; ++e)
-                if (!((see[e >> 1] >> (8 * i + 2 * (lane & 3) + (e & 1))) & 1)) s[i][e] = ACT == 2 ? -INFINITY : 0.f;  // act(0) = 0
-          }
-          float(&pv)[2][4] = s;  // in place
-          if constexpr (ACT == 2) {
-            // m need not be the maximum, only within 8 (in log2 units) of it or
-            // above: weights up to 2^8, and a step, with the exchange between the
-            // lanes of a row, that most tiles skip (5% at d = 32)
-            float mx[2];
+                if (!((see[kb >> 1][e >> 1] >> (16 * (kb & 1) + 8 * i + 2 * (lane & 3) + (e & 1))) & 1))
+                  s[kb][i][e] = ACT == 2 ? -INFINITY : 0.f;  // act(0) = 0
+        }
+        float(&pv)[KB][2][4] = s;  // in place
+        if constexpr (ACT == 2) {
+          // m need not be the maximum, only within 8 (in log2 units) of it or
+          // above: weights up to 2^8, and a step, with the exchange between the
+          // lanes of a row, that most tiles skip (5% at d = 32)
+          float mx[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-            for (int i = 0; i < 2; ++i) mx[i] = fmaxf(fmaxf(s[0][2 * i], s[0][2 * i + 1]), fmaxf(s[1][2 * i], s[1][2 * i + 1]));
-            if (__any_sync(0xffffffffu, mx[0] > m[hh][0] + 8.f || mx[1] > m[hh][1] + 8.f)) {
+          for (int kb = 0; kb < KB; ++kb)
 #pragma unroll
-              for (int i = 0; i < 2; ++i) {
-                mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], 1));
-                const float mn = fmaxf(m[hh][i], fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], 2)));
-                const float f = mn == -INFINITY ? 1.f : ex2_sfu(m[hh][i] - mn);
-                m[hh][i] = mn;
-                l[hh][i] *= f;
+            for (int i = 0; i < 2; ++i)
+              mx[i] = fmaxf(mx[i], fmaxf(fmaxf(s[kb][0][2 * i], s[kb][0][2 * i + 1]), fmaxf(s[kb][1][2 * i], s[kb][1][2 * i + 1])));
+          if (__any_sync(0xffffffffu, mx[0] > m[0] + 8.f || mx[1] > m[1] + 8.f)) {
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                  o[hh][nt][2 * i] *= f;
-                  o[hh][nt][2 * i + 1] *= f;
-                }
+            for (int i = 0; i < 2; ++i) {
+              mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], 1));
+              const float mn = fmaxf(m[i], fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], 2)));
+              const float f = mn == -INFINITY ? 1.f : ex2_sfu(m[i] - mn);
+              m[i] = mn;
+              l[i] *= f;
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) {
+                o[nt][2 * i] *= f;
+                o[nt][2 * i + 1] *= f;
               }
             }
-            const float ref[2] = {m[hh][0] == -INFINITY ? 0.f : m[hh][0], m[hh][1] == -INFINITY ? 0.f : m[hh][1]};
+          }
+          const float ref[2] = {m[0] == -INFINITY ? 0.f : m[0], m[1] == -INFINITY ? 0.f : m[1]};
+#pragma unroll
+          for (int kb = 0; kb < KB; ++kb)
 #pragma unroll
             for (int i = 0; i < 2; ++i)
 #pragma unroll
               for (int e = 0; e < 4; ++e) {
-                pv[i][e] = ex2_sfu(s[i][e] - ref[e >> 1]);
-                l[hh][e >> 1] += pv[i][e];
+                pv[kb][i][e] = ex2_sfu(s[kb][i][e] - ref[e >> 1]);
+                l[e >> 1] += pv[kb][i][e];
               }
-          } else {
+        } else {
+#pragma unroll
+          for (int kb = 0; kb < KB; ++kb)
 #pragma unroll
             for (int i = 0; i < 2; ++i)
 #pragma unroll
               for (int e = 0; e < 4; e += 2) {
-                const float2 y = act2_route<ACT, 0>(make_float2(0.5f * s[i][e], 0.5f * s[i][e + 1]));
-                pv[i][e] = y.x;
-                pv[i][e + 1] = y.y;
+                const float2 y = act2_route<ACT, 0>(make_float2(0.5f * s[kb][i][e], 0.5f * s[kb][i][e + 1]));
+                pv[kb][i][e] = y.x;
+                pv[kb][i][e + 1] = y.y;
               }
-          }
-          // P rounds to bf16 as the A operand (half a step, 2^-8 of each weight at most)
-          uint32_t pa[4];
+        }
 #pragma unroll
-          for (int i = 0; i < 4; ++i) pa[i] = pack_bf16(pv[i >> 1][2 * (i & 1)], pv[i >> 1][2 * (i & 1) + 1]);
+        for (int kb = 0; kb < KB; ++kb) {
+          // P rounds to bf16 as the A operand (half a step, 2^-8 of each weight at most)
+          uint32_t pa[4], keep[2] = {0xFFFFFFFFu, 0xFFFFFFFFu};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) pa[i] = pack_bf16(pv[kb][i >> 1][2 * (i & 1)], pv[kb][i >> 1][2 * (i & 1) + 1]);
+          if (!plain) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const int j = key0 + 16 * kb + 8 * i + 2 * (lane & 3);
+              keep[i] = j + 1 < r.L ? 0xFFFFFFFFu : (j < r.L ? 0xFFFFu : 0u);
+            }
+          }
 #pragma unroll
           for (int n2 = 0; n2 < NT / 2; ++n2) {
             uint32_t b[4];
-            ldsm4_t(piece(vb + vl, hh * (D / 8) + 2 * n2), b);
+            ldsm4_t(piece(vt + block(kb) + vl, 2 * n2), b);
 #pragma unroll
             for (int e = 0; e < 4; ++e) b[e] &= keep[e & 1];
             if (odd) {
 #pragma unroll
               for (int e = 0; e < 4; ++e) b[e] &= ~cc_nonfinite(b[e]);
             }
-            mma16816(o[hh][2 * n2], pa, b[0], b[1]);
-            mma16816(o[hh][2 * n2 + 1], pa, b[2], b[3]);
+            mma16816(o[2 * n2], pa, b[0], b[1]);
+            mma16816(o[2 * n2 + 1], pa, b[2], b[3]);
           }
           if (odd) {
 #pragma unroll 1
-            for (int kk = 0; kk < 16 && key0 + kk < r.L; ++kk) {
+            for (int kk = 0; kk < 16 && key0 + 16 * kb + kk < r.L; ++kk) {
               // the lane with this key's weights for the same rows, and what the rows see
-              const int from = (lane & ~3) | ((kk & 7) >> 1);
-              const uint32_t see0 = __shfl_sync(0xffffffffu, see[0], from) >> kk, see1 = __shfl_sync(0xffffffffu, see[1], from) >> kk;
-              const float w0 = __shfl_sync(0xffffffffu, kk < 8 ? ((kk & 1) ? pv[0][1] : pv[0][0])
-                                                               : ((kk & 1) ? pv[1][1] : pv[1][0]), from);
-              const float w1 = __shfl_sync(0xffffffffu, kk < 8 ? ((kk & 1) ? pv[0][3] : pv[0][2])
-                                                               : ((kk & 1) ? pv[1][3] : pv[1][2]), from);
+              const int from = (lane & ~3) | ((kk & 7) >> 1), bit = 16 * (kb & 1) + kk;
+              const uint32_t see0 = __shfl_sync(0xffffffffu, see[kb >> 1][0], from) >> bit;
+              const uint32_t see1 = __shfl_sync(0xffffffffu, see[kb >> 1][1], from) >> bit;
+              const float w0 = __shfl_sync(0xffffffffu, kk < 8 ? ((kk & 1) ? pv[kb][0][1] : pv[kb][0][0])
+                                                               : ((kk & 1) ? pv[kb][1][1] : pv[kb][1][0]), from);
+              const float w1 = __shfl_sync(0xffffffffu, kk < 8 ? ((kk & 1) ? pv[kb][0][3] : pv[kb][0][2])
+                                                               : ((kk & 1) ? pv[kb][1][3] : pv[kb][1][2]), from);
 #pragma unroll
               for (int nt = 0; nt < NT; ++nt) {
                 uint32_t v;
                 asm volatile("ld.shared.b32 %0, [%1];"
                              : "=r"(v)
-                             : "r"(vb + cc_offset<W>(16 * kw + kk, hh * (D / 8) + nt, pr) + 4 * (lane & 3))
+                             : "r"(vt + cc_offset<W>(first + 16 * kb + kk, hw * (D / 8) + nt, pr) + 4 * (lane & 3))
                              : "memory");
                 v &= cc_nonfinite(v);
                 if (v == 0) continue;
                 const float x = __uint_as_float(v << 16), y = __uint_as_float(v & 0xFFFF0000u);
                 if (see0 & 1) {
-                  if (x != 0.f) o[hh][nt][0] += w0 * x;
-                  if (y != 0.f) o[hh][nt][1] += w0 * y;
+                  if (x != 0.f) o[nt][0] += w0 * x;
+                  if (y != 0.f) o[nt][1] += w0 * y;
                 }
                 if (see1 & 1) {
-                  if (x != 0.f) o[hh][nt][2] += w1 * x;
-                  if (y != 0.f) o[hh][nt][3] += w1 * y;
+                  if (x != 0.f) o[nt][2] += w1 * x;
+                  if (y != 0.f) o[nt][3] += w1 * y;
                 }
               }
             }
@@ -404,17 +426,15 @@ __device__ void cc_consumer(const CacheFwdParams& p, uint8_t* smem, CcShared<MT,
 
     // the item's end: the warps' O, maxima and sums meet in shared memory
 #pragma unroll
-    for (int hh = 0; hh < HP; ++hh)
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        if constexpr (ACT != 2) continue;
-        l[hh][i] += __shfl_xor_sync(0xffffffffu, l[hh][i], 1);
-        l[hh][i] += __shfl_xor_sync(0xffffffffu, l[hh][i], 2);
-        if ((lane & 3) == 0) sh->ml[warp][hh][(lane >> 2) + 8 * i] = make_float2(m[hh][i], l[hh][i]);
-      }
-    // O by chunks of 32 columns: a warp's slot holds its 16 rows, row g's
-    // column pair c at pair c ^ 4 (g % 4) (no bank conflicts); a thread sums 4
-    // columns of a row over the group's four slots
+    for (int i = 0; i < 2; ++i) {
+      if constexpr (ACT != 2) continue;
+      l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
+      l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
+      if ((lane & 3) == 0) sh->ml[warp][(lane >> 2) + 8 * i] = make_float2(m[i], l[i]);
+    }
+    // O by chunks of 32 columns of every head: a warp's slot holds its 16 rows,
+    // row g's column pair c at pair c ^ 4 (g % 4) (no bank conflicts); a thread
+    // sums 4 columns of a row over the slots of each head in turn
     constexpr int kPerRow = kCChunk / 4;  // threads per row
     const int lr = tid / kPerRow, cc = (tid % kPerRow) * 4;
     const int g = lr & 15, w0 = (lr >> 4) * kCGroupWarps;
@@ -424,36 +444,37 @@ __device__ void cc_consumer(const CacheFwdParams& p, uint8_t* smem, CcShared<MT,
     const int64_t token = r.q0 + (live ? t_out : 0);
     const int head0 = w.h * HP * p.group + (live ? flat - t_out * p.group : 0);
     const int64_t part0 = (2 * static_cast<int64_t>(blockIdx.x) + w.slot()) * (HP * kRows) + lr;
-    float M = -INFINITY, L = 0.f, inv = 1.f, f[kCGroupWarps] = {1.f, 1.f, 1.f, 1.f};
     float* slot = reinterpret_cast<float*>(smem + C::kOOff + warp * C::kSlotBytes);
 #pragma unroll
-    for (int c0 = 0; c0 < W; c0 += kCChunk) {
-      const int hh = c0 / D;
+    for (int c0 = 0; c0 < D; c0 += kCChunk) {
 #pragma unroll
       for (int nt = 0; nt < kCChunk / 8; ++nt)
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           const int gr = (lane >> 2) + 8 * i, c2 = (4 * nt + (lane & 3)) ^ ((gr & 3) << 2);
-          *reinterpret_cast<float2*>(slot + gr * kCChunk + 2 * c2) =
-              make_float2(o[hh][(c0 % D) / 8 + nt][2 * i], o[hh][(c0 % D) / 8 + nt][2 * i + 1]);
+          *reinterpret_cast<float2*>(slot + gr * kCChunk + 2 * c2) = make_float2(o[c0 / 8 + nt][2 * i], o[c0 / 8 + nt][2 * i + 1]);
         }
       named_bar(1, C::kWarps * 32);
-      if (live) {
-        const int head = head0 + hh * p.group;
-        const int64_t prow = part0 + hh * kRows;
-        if (ACT == 2 && c0 % D == 0) {
-          M = -INFINITY;
-          L = 0.f;
 #pragma unroll
-          for (int i = 0; i < kCGroupWarps; ++i) M = fmaxf(M, sh->ml[w0 + i][hh][g].x);
+      for (int hh = 0; hh < HP; ++hh) {
+        if (!live) break;
+        const int head = head0 + hh * p.group, from = w0 + hh * KG;
+        const int64_t prow = part0 + hh * kRows;
+        float inv = 1.f, f[KG];
+#pragma unroll
+        for (int i = 0; i < KG; ++i) f[i] = 1.f;
+        if constexpr (ACT == 2) {
+          float M = -INFINITY, L = 0.f;
+#pragma unroll
+          for (int i = 0; i < KG; ++i) M = fmaxf(M, sh->ml[from + i][g].x);
           const float ref = M == -INFINITY ? 0.f : M;
 #pragma unroll
-          for (int i = 0; i < kCGroupWarps; ++i) {
-            f[i] = ex2_sfu(sh->ml[w0 + i][hh][g].x - ref);
-            L = __fmaf_rn(sh->ml[w0 + i][hh][g].y, f[i], L);
+          for (int i = 0; i < KG; ++i) {
+            f[i] = ex2_sfu(sh->ml[from + i][g].x - ref);
+            L = __fmaf_rn(sh->ml[from + i][g].y, f[i], L);
           }
           if (w.whole) inv = L > 0.f ? 1.f / L : (L == 0.f ? 0.f : L);  // no key seen: 0 (a NaN sum stays NaN)
-          if (cc == 0) {
+          if (c0 == 0 && cc == 0) {
             if (!w.whole) p.part_ml[prow] = make_float2(M, L);
             else if (p.lse != nullptr)
               p.lse[static_cast<int64_t>(head) * p.total_q + token] = L == 0.f ? -INFINITY : (M + log2f(L)) * kLn2;
@@ -461,8 +482,8 @@ __device__ void cc_consumer(const CacheFwdParams& p, uint8_t* smem, CcShared<MT,
         }
         float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-        for (int i = 0; i < kCGroupWarps; ++i) {
-          const float4 v = *reinterpret_cast<const float4*>(smem + C::kOOff + (w0 + i) * C::kSlotBytes +
+        for (int i = 0; i < KG; ++i) {
+          const float4 v = *reinterpret_cast<const float4*>(smem + C::kOOff + (from + i) * C::kSlotBytes +
                                                             (g * kCChunk + (cc ^ ((g & 3) << 3))) * 4);
           a.x = __fmaf_rn(v.x, f[i], a.x);
           a.y = __fmaf_rn(v.y, f[i], a.y);
@@ -470,10 +491,10 @@ __device__ void cc_consumer(const CacheFwdParams& p, uint8_t* smem, CcShared<MT,
           a.w = __fmaf_rn(v.w, f[i], a.w);
         }
         if (w.whole)
-          *reinterpret_cast<uint2*>(p.out + (token * p.heads + head) * D + c0 % D + cc) =
+          *reinterpret_cast<uint2*>(p.out + (token * p.heads + head) * D + c0 + cc) =
               make_uint2(pack_bf16(a.x * inv, a.y * inv), pack_bf16(a.z * inv, a.w * inv));
         else
-          *reinterpret_cast<float4*>(p.part_o + prow * D + c0 % D + cc) = a;
+          *reinterpret_cast<float4*>(p.part_o + prow * D + c0 + cc) = a;
       }
       named_bar(1, C::kWarps * 32);  // the slots are free again
     }
@@ -484,10 +505,10 @@ template <int D, int ACT, int MT, int HP>
 __global__ void __launch_bounds__((CcCfg<D * HP, MT, HP>::kThreads), (CcCfg<D * HP, MT, HP>::kCtas))
     cache_fwd_kernel(const __grid_constant__ CacheFwdParams p) {
   using C = CcCfg<D * HP, MT, HP>;
-  static_assert(sizeof(CcShared<MT, HP>) <= C::kSmemBytes - 1024 - C::kBarOff, "shared block");
+  static_assert(sizeof(CcShared<MT>) <= C::kSmemBytes - 1024 - C::kBarOff, "shared block");
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  CcShared<MT, HP>* sh = reinterpret_cast<CcShared<MT, HP>*>(smem + C::kBarOff);
+  CcShared<MT>* sh = reinterpret_cast<CcShared<MT>*>(smem + C::kBarOff);
   cache_let_next();
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::kStages; ++s) {
