@@ -21,11 +21,12 @@ constexpr int kCacheMaxBatch = 16384;  // requests per call (the plan's prefix s
 
 // Query rows per key/value head up to which the kernel for few rows
 // (cache_fwd.cu) runs, and the 128-row one (cache_fwd_wide.cu) from there on.
-// At 24 rows, 64 requests of 4,100 tokens, 32-row tiles of the former took 264 us
-// against 183 at d = 128 and 172 against 153 at d = 64 (76 against 87 on 256
-// requests of 100 to 800 tokens), but 240 against 240 at d = 32, and 180 against
-// 288 on the short requests.
-__host__ __device__ constexpr int cache_narrow_rows(int d) { return d == 32 ? 32 : 16; }
+// At 24 rows, 64 requests of 4,100 tokens, tiles of 32 rows of the former took
+// 264 us against 183 at d = 128, but 140 against 149 at d = 64 and 170 against 230
+// at d = 32; on 256 requests of 100 to 800 tokens 195 against 171, 60 against 87
+// and 126 against 288; on one of 100,000 tokens 105 against 77, 40 against 33 and
+// 75 against 79.
+__host__ __device__ constexpr int cache_narrow_rows(int d) { return d < 128 ? 32 : 16; }
 
 // CTAs per SM of the attention kernel for up to 16 mt rows and w columns of K
 // and V per item (cache_fwd.cu).
@@ -423,6 +424,18 @@ static __device__ __noinline__ uint32_t cc_vis32(const CacheFwdParams& p, CacheR
 __device__ __forceinline__ bool cc_near(const CacheFwdParams& p, int pos, int key_pos) {
   const int apart = pos - key_pos;
   return p.window <= 0 || (apart < p.window && apart > -p.window);
+}
+// Whether the keys key0 .. key0 + 31 are at the positions of their numbers (the
+// context's are, and the new tokens' without depths), and which of them the
+// window then joins with a row: those in (pos - w, pos + w).
+__device__ __forceinline__ bool cc_in_order(const CacheFwdParams& p, const CacheReq& r, int key0) {
+  return p.depth == nullptr || key0 + 31 < r.C;
+}
+__device__ __forceinline__ uint32_t cc_near32(const CacheFwdParams& p, int pos, int key0) {
+  const int64_t at = static_cast<int64_t>(pos) - key0;
+  const int lo = static_cast<int>(min(max(at - p.window + 1, int64_t{0}), int64_t{32}));
+  const int hi = static_cast<int>(min(max(at + p.window, int64_t{0}), int64_t{32}));
+  return cc_ones(hi) & ~cc_ones(lo);
 }
 // The bias table's entry of a row for a key position (any position: the index is clamped).
 __device__ __forceinline__ float cc_bias(const CacheFwdParams& p, const CcRow& q, int reach, int key_pos) {

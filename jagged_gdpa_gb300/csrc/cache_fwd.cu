@@ -43,7 +43,7 @@ struct CcCfg {
   // SM (at d = 128, 64 KB reached 0.67 of the copy bandwidth on one long
   // request, 128 KB 0.82)
   static constexpr int kCtas = cache_ctas(W, MT);
-  static constexpr int kStages = MT == 1 ? (W == 128 ? 3 : W == 64 ? 4 : 5) : (W == 128 ? 6 : 10);
+  static constexpr int kStages = MT == 1 ? (W == 128 ? 3 : W == 64 ? 4 : 5) : (W == 128 ? 6 : W == 64 ? 5 : 10);
   static constexpr int kSlotBytes = 16 * kCChunk * 4;  // one warp's chunk of O
   static constexpr int kOOff = kStages * 2 * kTileBytes;
   static constexpr int kBarOff = kOOff + kWarps * kSlotBytes;
@@ -242,10 +242,14 @@ __device__ void cc_consumer(const CacheFwdParams& p, uint8_t* smem, CcShared<MT>
               uint32_t bits = cc_vis32(p, r, rows[h], key0 + 32 * j);
               if (p.window > 0) {
                 uint32_t near = 0;
+                if (cc_in_order(p, r, key0 + 32 * j)) {
+                  near = cc_near32(p, rows[h].pos, key0 + 32 * j);
+                } else {
 #pragma unroll 1
-                for (int c = 0; c < (KB > 1 ? 8 : 4); ++c) {
-                  const int col = 8 * (c >> 1) + 2 * (lane & 3) + (c & 1);
-                  near |= (cc_near(p, rows[h].pos, cc_pos(p, r, key0 + 32 * j + col)) ? 1u : 0u) << col;
+                  for (int c = 0; c < (KB > 1 ? 8 : 4); ++c) {
+                    const int col = 8 * (c >> 1) + 2 * (lane & 3) + (c & 1);
+                    near |= (cc_near(p, rows[h].pos, cc_pos(p, r, key0 + 32 * j + col)) ? 1u : 0u) << col;
+                  }
                 }
                 bits &= near;  // (only this lane's columns are kept)
               }

@@ -360,8 +360,12 @@ static __device__ __noinline__ CwNear cw_near(const CacheFwdParams& p, CacheReq 
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       uint32_t near = 0;
+      if (cc_in_order(p, r, key0 + 32 * k)) {
+        near = cc_near32(p, q.pos, key0 + 32 * k);
+      } else {
 #pragma unroll 4
-      for (int c = 0; c < 32; ++c) near |= (cc_near(p, q.pos, __shfl_sync(0xffffffffu, t.pos[k], c)) ? 1u : 0u) << c;
+        for (int c = 0; c < 32; ++c) near |= (cc_near(p, q.pos, __shfl_sync(0xffffffffu, t.pos[k], c)) ? 1u : 0u) << c;
+      }
       t.see[k] &= near;
     }
   }
