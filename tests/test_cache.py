@@ -393,6 +393,61 @@ def test_trees_bias_and_window(jg, act, new, group, bias, window, page):
 
 
 @gpu
+@pytest.mark.parametrize("act", ["silu", "softmax"])
+@pytest.mark.parametrize("d,kv_heads,new,group", [(32, 4, 3, 2), (32, 3, 20, 1), (32, 4, 40, 1), (64, 2, 5, 3), (64, 2, 10, 3),
+                                                  (64, 3, 70, 1), (128, 2, 2, 2), (128, 1, 90, 2)])
+@pytest.mark.parametrize("window", [1, 30, 190, 2 ** 31 - 1])
+def test_windows_of_tokens_in_order(jg, act, d, kv_heads, new, group, window):
+    """Without a mask and depths."""
+    c = Case(d + window % 97, [0, 450, 131, 1], [new, new, 1, new], kv_heads, group, d, 32, act, bias=17, window=window)
+    compare(c, *jg.jgdpa_cache_fwd(**c.kwargs()))
+
+
+@gpu
+@pytest.mark.parametrize("d,new,group", [(32, 5, 2), (64, 20, 1), (128, 33, 2)])
+@pytest.mark.parametrize("drop", ["mask", "depth"])
+def test_a_mask_or_depths_alone(jg, d, new, group, drop):
+    c = Case(29, [70, 0, 300], [new, new, 2], 4, group, d, 16, "softmax", bias=33, window=60, mask=True)
+    setattr(c, drop, None)
+    compare(c, *jg.jgdpa_cache_fwd(**c.kwargs()))
+
+
+@gpu
+@pytest.mark.parametrize("d,group", [(64, 130), (128, 129), (128, 200)])
+def test_more_heads_per_group_than_a_tile_has_rows(jg, d, group):
+    c = Case(group, [70, 5, 600], [3, 1, 1], 1, group, d, 16, "gelu", bias=9)
+    compare(c, *jg.jgdpa_cache_fwd(**c.kwargs()))
+
+
+@gpu
+@pytest.mark.parametrize("act", ["gelu", "softmax"])
+@pytest.mark.parametrize("d,kv_heads,new,group", [(32, 4, 6, 1), (32, 4, 25, 1), (32, 3, 5, 2), (64, 2, 9, 3), (128, 2, 6, 2),
+                                                  (128, 2, 30, 2)])
+def test_infinities_in_any_place(jg, act, d, kv_heads, new, group):
+    """An infinity in one column of one head's value of a drafted token, and NaN
+    in values out of every window: only that column of the rows that see it changes."""
+    c = Case(41, [150, 40], [new, new], kv_heads, group, d, 16, act, window=60, mask=True)
+    kw = c.kwargs()
+    clean, _ = jg.jgdpa_cache_fwd(**kw)
+    rng = np.random.default_rng(d + new)
+    n = int(c.off[1])
+    for u in {0, new // 2, new - 1}:
+        sees = torch.tensor([(int(c.mask[t, u // 32]) >> (u % 32)) & 1 for t in range(n)], dtype=torch.bool)
+        head, col = int(rng.integers(kv_heads)), int(rng.integers(d))
+        v = kw["v_cache"].clone()
+        j = 150 + u
+        v[int(c.table[0, j // 16]), j % 16, head, col] = float("inf")
+        v[int(c.table[0, 17 // 16]), 17 % 16] = float("nan")
+        got = jg.jgdpa_cache_fwd(**{**kw, "v_cache": v})[0].cpu()
+        same = torch.ones_like(got, dtype=torch.bool)
+        rows = torch.nonzero(sees).flatten()
+        for h in range(head * group, (head + 1) * group):
+            same[rows, h, col] = False
+            assert not torch.isfinite(got[rows, h, col]).any()
+        assert torch.equal(got[same], clean.cpu()[same])
+
+
+@gpu
 @pytest.mark.parametrize("act", ["gelu", "softmax"])
 @pytest.mark.parametrize("length", [1, 15, 16, 17, 63, 64, 65, 127, 128, 129, 255, 256, 257])
 def test_lengths_at_tile_and_page_borders(jg, act, length):
