@@ -112,9 +112,14 @@ bool cache_map(CUtensorMap* m, const void* ptr, int64_t page_stride, int32_t num
   cuuint32_t box[5] = {static_cast<cuuint32_t>(cols), static_cast<cuuint32_t>(std::min(page_size, box_tokens)),
                        static_cast<cuuint32_t>(both_halves ? halves : 1), 1, 1};
   cuuint32_t es[5] = {1, 1, 1, 1, 1};
+  // what L2 fetches at a time: no more than a head's piece of a token, as its
+  // neighbours are other heads', read at another time
+  const CUtensorMapL2promotion promotion = head_dim >= 128 ? CU_TENSOR_MAP_L2_PROMOTION_L2_256B
+                                           : head_dim == 64 ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B
+                                                            : CU_TENSOR_MAP_L2_PROMOTION_L2_64B;
   return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<void*>(ptr), dims, strides, box, es,
              CU_TENSOR_MAP_INTERLEAVE_NONE, cols == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
-             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+             promotion, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 // The queries: (column, token, head), a box one 64-column half of a tile's
