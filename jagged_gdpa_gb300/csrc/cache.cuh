@@ -22,10 +22,11 @@ constexpr int kCacheMaxBatch = 16384;  // requests per call (the plan's prefix s
 // Query rows per key/value head up to which the kernel for few rows
 // (cache_fwd.cu) runs, and the 128-row one (cache_fwd_wide.cu) from there on.
 // At 24 rows, 64 requests of 4,100 tokens, tiles of 32 rows of the former took
-// 264 us against 183 at d = 128, but 140 against 149 at d = 64 and 170 against 230
+// 264 us against 183 at d = 128, but 140 against 121 at d = 64 and 170 against 208
 // at d = 32; on 256 requests of 100 to 800 tokens 195 against 171, 60 against 87
-// and 126 against 288; on one of 100,000 tokens 105 against 77, 40 against 33 and
-// 75 against 79.
+// and 127 against 284; on one of 100,000 tokens 105 against 77, 40 against 34 and
+// 75 against 78.  (Lengths are not known to the host; at d = 64 the short ones
+// have more to lose.)
 __host__ __device__ constexpr int cache_narrow_rows(int d) { return d < 128 ? 32 : 16; }
 
 // CTAs per SM of the attention kernel for up to 16 mt rows and w columns of K

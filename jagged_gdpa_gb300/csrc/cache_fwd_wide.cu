@@ -31,9 +31,10 @@
 // 177 to 13,900 tokens: 74 us, 0.61 (the longest requests' parts and the items'
 // starts and ends); 64 trees of 64 tokens, 512 rows, GELU with a bias over 134 to
 // 8,066 tokens: 283 us, 0.52 of the products at cuBLAS's burst rate.  At d = 64
-// the same 64 requests take 151 us, 0.53 of the copy bandwidth: a tile's weights
-// (128 x 128 exponentials, 1,024 cycles of the special-function units) and its
-// products (1,000) no longer hide behind half the bytes.
+// the same 64 requests take 114 us, 0.71 of the copy bandwidth, at d = 32 (16
+// heads) 192 us: a tile's 128 x 128 weights (1,024 cycles of the special-function
+// units, a warpgroup's way from S to P some 1,400) no longer hide behind half or a
+// quarter of the bytes.
 #include "act.cuh"
 #include "cache.cuh"
 #include "common.cuh"
@@ -444,10 +445,46 @@ __device__ __forceinline__ void cw_act_tile(uint32_t t_s, float scale, float bia
 }
 
 // P = 2^(x - m) with a running maximum that moves only when it grows by more
-// than 8 (P stays below 2^8, O and l in fp32): O is rescaled then.
+// than 8 (P stays below 2^8, O and l in fp32): O is rescaled then.  At d < 128,
+// where HBM does not hide a second pass over S, most tiles do without a look at
+// their maximum: the weights by the m so far add up to no more than 2^8, so none
+// is above it (64 requests of 4,100 tokens, 64 rows: 121 -> 114 us at d = 64, 211
+// -> 192 at d = 32; at d = 128 it would change nothing there, 453 -> 441 at 512
+// rows, but 209 -> 217 on short trees, whose few tiles have more to fetch).
 template <int D>
-__device__ __forceinline__ void cw_softmax_tile(uint32_t t_s, uint32_t t_o, float scale, float bias, bool first,
+__device__ __forceinline__ void cw_softmax_tile(uint32_t t_s, uint32_t t_o, float scale, float bias, bool live, bool first,
                                                 float& m, float& l) {
+  constexpr bool kTry = D < 128;
+  if (kTry && !__any_sync(0xffffffffu, live && m == -INFINITY)) {
+    const float2 off = f2(bias - m);
+    float2 sum = f2(0.f);
+    uint32_t pk[64];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      uint32_t a[32];
+      tmem_ld32(t_s + 32 * q, a);
+      tmem_ld_wait(a);
+#pragma unroll
+      for (int c = 0; c < 16; ++c) {
+        const float2 z = __ffma2_rn(make_float2(__uint_as_float(a[2 * c]), __uint_as_float(a[2 * c + 1])), f2(scale), off);
+        const float2 e = make_float2(ex2_sfu(z.x), ex2_sfu(z.y));
+        sum = __fadd2_rn(sum, e);
+        pk[16 * q + c] = pack_bf16(e.x, e.y);
+      }
+    }
+    const float total = sum.x + sum.y;
+    if (!__any_sync(0xffffffffu, live && !(total <= 256.f))) {
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        uint32_t x[32];
+#pragma unroll
+        for (int c = 0; c < 32; ++c) x[c] = pk[32 * q + c];
+        tmem_st32(t_s + 32 * q, x);
+      }
+      l += total;
+      return;
+    }
+  }
   float mx = -INFINITY;
 #pragma unroll 1
   for (int q = 0; q < 4; q += 2) {
@@ -462,7 +499,7 @@ __device__ __forceinline__ void cw_softmax_tile(uint32_t t_s, uint32_t t_o, floa
       mx = fmaxf(fmaxf(mx, fmaxf(x.x, x.y)), fmaxf(y.x, y.y));
     }
   }
-  const bool grow = mx > m + 8.0f;
+  const bool grow = mx > m + (kTry ? 1.0f : 8.0f);  // (128 weights of up to 2 pass the test above)
   const float factor = grow ? ex2_sfu(m - mx) : 1.0f;  // 0 on the first tile
   if (grow) m = mx;
   l *= factor;
@@ -679,7 +716,7 @@ __device__ void cw_consumer(const CacheFwdParams& p, CwShared* sh, uint32_t tmem
           scale = 1.f;
           bias = 0.f;
         }
-        if constexpr (ACT == 2) cw_softmax_tile<D>(t_s, t_o + 128 * stream, scale, bias, i == 0, m, l);
+        if constexpr (ACT == 2) cw_softmax_tile<D>(t_s, t_o + 128 * stream, scale, bias, row_ok, i == 0, m, l);
         else cw_act_tile<ACT>(t_s, scale, bias);
         tmem_st_wait();
       }
