@@ -3,11 +3,11 @@
 // One item is (request, key/value head, tile of 16 or 32 query rows); a row is
 // (new token, query head of the group), so the heads that share a key/value
 // head share its loads.  Of small heads (d < 128) an item takes 128 / d side by
-// side where their number allows: their columns are one contiguous 256-byte
-// piece per token, and an item's start and end are paid once for all of them
-// (d = 32, 16 heads, 64 requests of 4,100 tokens: 126 us against 216 one by one).
-// Its keys stream through shared memory once, in tiles of 64 tokens gathered
-// from the pages by TMA.
+// side where their number allows and the work is large enough: their columns are
+// one contiguous 256-byte piece per token, and an item's start and end are paid
+// once for all of them (d = 32, 16 heads, 64 requests of 4,100 tokens: 96 us
+// against 190 one by one).  Its keys stream through shared memory once, in tiles
+// of 64 tokens gathered from the pages by TMA.
 //
 //   S = Q K^T, P = act(S) or exp2(S - m), O += P V
 //
@@ -19,7 +19,7 @@
 // side, each takes one head (d = 32) or half the keys of one (d = 64), each with
 // its own running maximum, sum and O; those of a head meet once per item.  (With
 // every warp at all four heads of a quarter of the keys the d = 32 case above
-// took 120 us against 95: a step with few independent instructions per head,
+// took 120 us: a step with few independent instructions per head,
 // four times.)  With 32-row tiles (d < 128) a second group of four warps takes
 // the second 16 rows of the same keys.
 //

@@ -83,10 +83,11 @@ class Case:
         return oracle.attend(f(self.q), f(self.k), f(self.v), self.table, self.off, self.kv, self.act, self.scale,
                              None if self.bias is None else f(self.bias), self.window, self.mask, self.depth)
 
-    def kwargs(self, device="cuda"):
+    def kwargs(self, device="cuda", room=0):
+        """room: columns of the table beyond the longest request's pages."""
         mask = None if self.mask is None else torch.from_numpy(self.mask.astype(np.uint32).view(np.int32)).to(device)
         return dict(q=self.q.to(device), k_cache=self.k.to(device), v_cache=self.v.to(device),
-                    block_table=i32(self.table, device), q_offsets=i32(self.off, device),
+                    block_table=i32(np.pad(self.table, ((0, 0), (0, room)), constant_values=-3), device), q_offsets=i32(self.off, device),
                     kv_lens=i32(self.kv, device), act=self.act, scale=self.scale,
                     max_q=int(max(1, self.new.max())), bias_table=None if self.bias is None else self.bias.to(device),
                     window=self.window, tree_mask=mask, depths=None if self.depth is None else i32(self.depth, device))
@@ -358,10 +359,12 @@ def test_attention(jg, act, d, group, new):
 @pytest.mark.parametrize("act", ["gelu", "silu", "softmax"])
 @pytest.mark.parametrize("d,kv_heads", [(32, 4), (32, 8), (32, 3), (64, 4), (64, 3)])
 @pytest.mark.parametrize("group,new", [(1, 1), (3, 2), (4, 7)])
-def test_small_heads_side_by_side(jg, act, d, kv_heads, group, new):
+@pytest.mark.parametrize("room", [0, 1 << 16])
+def test_small_heads_side_by_side(jg, act, d, kv_heads, group, new, room):
+    """One by one in a table of few tokens, side by side in one with room for many."""
     c = Case(d + new, [0, 700, 64, 3000], [new, 1, new, new], kv_heads, group, d, 16, act, bias=65, window=0 if new < 7 else 200,
              mask=True)
-    kw = c.kwargs()
+    kw = c.kwargs(room=room)
     out = torch.full_like(kw["q"], float("nan"))
     compare(c, *jg.jgdpa_cache_fwd(**kw, out=out))
 
@@ -397,19 +400,21 @@ def test_trees_bias_and_window(jg, act, new, group, bias, window, page):
 @pytest.mark.parametrize("d,kv_heads,new,group", [(32, 4, 3, 2), (32, 3, 20, 1), (32, 4, 40, 1), (64, 2, 5, 3), (64, 2, 10, 3),
                                                   (64, 3, 70, 1), (128, 2, 2, 2), (128, 1, 90, 2)])
 @pytest.mark.parametrize("window", [1, 30, 190, 2 ** 31 - 1])
-def test_windows_of_tokens_in_order(jg, act, d, kv_heads, new, group, window):
+@pytest.mark.parametrize("room", [0, 1 << 16])
+def test_windows_of_tokens_in_order(jg, act, d, kv_heads, new, group, window, room):
     """Without a mask and depths."""
     c = Case(d + window % 97, [0, 450, 131, 1], [new, new, 1, new], kv_heads, group, d, 32, act, bias=17, window=window)
-    compare(c, *jg.jgdpa_cache_fwd(**c.kwargs()))
+    compare(c, *jg.jgdpa_cache_fwd(**c.kwargs(room=room)))
 
 
 @gpu
 @pytest.mark.parametrize("d,new,group", [(32, 5, 2), (64, 20, 1), (128, 33, 2)])
 @pytest.mark.parametrize("drop", ["mask", "depth"])
-def test_a_mask_or_depths_alone(jg, d, new, group, drop):
+@pytest.mark.parametrize("room", [0, 1 << 16])
+def test_a_mask_or_depths_alone(jg, d, new, group, drop, room):
     c = Case(29, [70, 0, 300], [new, new, 2], 4, group, d, 16, "softmax", bias=33, window=60, mask=True)
     setattr(c, drop, None)
-    compare(c, *jg.jgdpa_cache_fwd(**c.kwargs()))
+    compare(c, *jg.jgdpa_cache_fwd(**c.kwargs(room=room)))
 
 
 @gpu
@@ -423,11 +428,12 @@ def test_more_heads_per_group_than_a_tile_has_rows(jg, d, group):
 @pytest.mark.parametrize("act", ["gelu", "softmax"])
 @pytest.mark.parametrize("d,kv_heads,new,group", [(32, 4, 6, 1), (32, 4, 25, 1), (32, 3, 5, 2), (64, 2, 9, 3), (128, 2, 6, 2),
                                                   (128, 2, 30, 2)])
-def test_infinities_in_any_place(jg, act, d, kv_heads, new, group):
+@pytest.mark.parametrize("room", [0, 1 << 16])
+def test_infinities_in_any_place(jg, act, d, kv_heads, new, group, room):
     """An infinity in one column of one head's value of a drafted token, and NaN
     in values out of every window: only that column of the rows that see it changes."""
     c = Case(41, [150, 40], [new, new], kv_heads, group, d, 16, act, window=60, mask=True)
-    kw = c.kwargs()
+    kw = c.kwargs(room=room)
     clean, _ = jg.jgdpa_cache_fwd(**kw)
     rng = np.random.default_rng(d + new)
     n = int(c.off[1])
@@ -515,7 +521,8 @@ def test_rows_that_see_nothing(jg, act, new):
 @gpu
 @pytest.mark.parametrize("up", [True, False])
 @pytest.mark.parametrize("d,new", [(32, 3), (128, 1), (64, 8), (32, 30), (64, 24), (128, 50)])
-def test_scores_that_rise_and_fall(jg, d, new, up):
+@pytest.mark.parametrize("room", [0, 1 << 16])
+def test_scores_that_rise_and_fall(jg, d, new, up, room):
     """Softmax whose scores grow (or shrink) along the keys, a little per tile
     and by jumps: the running maximum has to follow."""
     c = Case(23, [900, 77], [new, new], 4, 2, d, 64, "softmax", nan=False)
@@ -523,7 +530,7 @@ def test_scores_that_rise_and_fall(jg, d, new, up):
         for j in range(n):
             at = j / n if up else 1 - j / n
             c.k[c.table[b, j // 64], j % 64] *= 8.0 * at ** 2 + (12.0 if at > 0.8 else 0.0)
-    out, lse = jg.jgdpa_cache_fwd(**c.kwargs())
+    out, lse = jg.jgdpa_cache_fwd(**c.kwargs(room=room))
     compare(c, out, lse)
 
 
