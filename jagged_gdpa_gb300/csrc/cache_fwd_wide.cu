@@ -28,13 +28,12 @@
 //
 // Measured, d = 128: 64 requests of 4,100 tokens, 8 key/value heads, 64 rows: 186
 // us, 0.87 of the copy bandwidth; 32 trees of 8 to 33 tokens, 32 to 132 rows, over
-// 177 to 13,900 tokens: 74 us, 0.61 (the longest requests' parts and the items'
-// starts and ends); 64 trees of 64 tokens, 512 rows, GELU with a bias over 134 to
-// 8,066 tokens: 283 us, 0.52 of the products at cuBLAS's burst rate.  At d = 64
-// the same 64 requests take 114 us, 0.71 of the copy bandwidth, at d = 32 (16
-// heads) 192 us: a tile's 128 x 128 weights (1,024 cycles of the special-function
-// units, a warpgroup's way from S to P some 1,400) no longer hide behind half or a
-// quarter of the bytes.
+// 177 to 13,900 tokens: 75 us, 0.60 (the items' starts and ends); 64 trees of 64
+// tokens, 512 rows, GELU with a bias over 134 to 8,066 tokens: 284 us, 0.52 of the
+// products at cuBLAS's burst rate.  At d = 64 the same 64 requests take 114 us,
+// 0.71 of the copy bandwidth, at d = 32 (16 heads) 192 us: a tile's 128 x 128
+// weights (1,024 cycles of the special-function units, a warpgroup's way from S to
+// P some 1,400) no longer hide behind half or a quarter of the bytes.
 #include "act.cuh"
 #include "cache.cuh"
 #include "common.cuh"
