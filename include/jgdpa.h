@@ -374,7 +374,9 @@ JGDPA_API jgdpa_status jgdpa_cache_append(const void* k_new, const void* v_new, 
  * Every token sees the whole context (within the window).  A token that sees
  * nothing gets O = 0 (LSE = -inf).  Infinities and NaN in the cache reach only
  * the rows that see their token; places of a page behind kv_lens[b] may hold
- * anything.  Same bits on every run, whatever else runs beside it.
+ * anything.  Same bits on every run, whatever else runs beside it.  Weights are
+ * rounded to bf16 before the product with V; GELU and SiLU are right to bf16's
+ * last place relative to themselves, far below zero, too.
  * Device-detected errors: BAD_OFFSETS (offsets not monotone from 0, beyond
  * total_q, T_b > max_q or more than the tree mask's columns, kv_lens[b] < T_b or
  * beyond the table), in which case nothing is written; BAD_PAGE (a table entry

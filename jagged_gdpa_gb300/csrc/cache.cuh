@@ -377,12 +377,50 @@ struct CcRow {
   float far_bias;   // bias of keys at least R behind every new token
 };
 
-// act(x) for the few weights that are formed one by one.
-template <int ACT>
-__device__ __forceinline__ float cc_act(float x) {
-  if constexpr (ACT == 0) return 0.5f * x * (1.0f + erff(x * 0.70710678118654752f));
-  else return __fdividef(x, 1.0f + __expf(-x));
+// GELU(x) or SiLU(x) of two scores from hx = x / 2, each right to bf16's last
+// place relative to itself.  (The packed kernels' hx + hx tanh(u) is a difference
+// of nearly equal numbers below zero, whose error of some 1e-3 is as large as the
+// weight itself from about -3 on: a long context whose bias pushes most scores
+// there would add up noise.)
+//   GELU(x) = max(x, 0) - a Phi(-a), a = |x|, with log2 Phi(-a) as a polynomial
+//     on [0, 13] (Phi within 1.9e-3, csrc/fit_constants.py; beyond it a Phi(-a) is
+//     below 2^-122; degree 7, within 5.2e-4, took 2% more time in the 128-row kernel)
+//   SiLU(x) = x / (1 + 2^(-x log2 e))
+// NaN stays NaN.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float y;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+  return y;
 }
+__device__ __forceinline__ float rcp_sfu(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+template <int ACT>
+__device__ __forceinline__ float2 cc_act2(float2 hx) {
+  if constexpr (ACT == 0) {
+    constexpr float c[7] = {-1.00261784f,  -1.1279366f,     -0.492554843f, -0.0349358097f,
+                            0.0033006093f, -0.000168592655f, 3.53243581e-06f};
+    // n = -a / 2: 2 Phi(-a) = 2^(1 + c0 - 2 c1 n + 4 c2 n^2 ..), and hx + |hx| = max(x, 0)
+    const float2 n = make_float2(max_nan(-fabsf(hx.x), -6.5f), max_nan(-fabsf(hx.y), -6.5f));
+    float2 w = f2(64.f * c[6]);
+    w = __ffma2_rn(w, n, f2(-32.f * c[5]));
+    w = __ffma2_rn(w, n, f2(16.f * c[4]));
+    w = __ffma2_rn(w, n, f2(-8.f * c[3]));
+    w = __ffma2_rn(w, n, f2(4.f * c[2]));
+    w = __ffma2_rn(w, n, f2(-2.f * c[1]));
+    w = __ffma2_rn(w, n, f2(1.f + c[0]));
+    return __ffma2_rn(n, make_float2(ex2_sfu(w.x), ex2_sfu(w.y)), make_float2(hx.x + fabsf(hx.x), hx.y + fabsf(hx.y)));
+  } else {
+    const float2 w = __fmul2_rn(hx, f2(-2.f * kLog2e));
+    const float2 a = __ffma2_rn(make_float2(ex2_sfu(w.x), ex2_sfu(w.y)), f2(0.5f), f2(0.5f));
+    return __fmul2_rn(hx, make_float2(rcp_sfu(a.x), rcp_sfu(a.y)));
+  }
+}
+// act(x) of the few weights that are formed one by one.
+template <int ACT>
+__device__ __forceinline__ float cc_act(float x) { return cc_act2<ACT>(f2(0.5f * x)).x; }
 
 template <int ACT>
 __device__ __forceinline__ float cc_bias_unit() { return ACT == 2 ? kLog2e : 1.0f; }

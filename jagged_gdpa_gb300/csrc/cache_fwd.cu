@@ -177,6 +177,9 @@ __device__ void cc_consumer(const CacheFwdParams& p, uint8_t* smem, CcShared<MT>
   const uint32_t step1 = 16 * (pr >= 32 ? row_bytes : 2 * W), step2 = 32 * (pr >= 64 ? row_bytes : 2 * W);
   auto block = [&](int kb) { return (kb & 1) * step1 + (kb >> 1) * step2; };
   const int reach = (p.bias_len - 1) / 2;
+  // scores in log2 units, or halved as cc_act2 takes them
+  constexpr float kUnit = ACT == 2 ? kLog2e : 0.5f;
+  const float scale = ACT == 2 ? p.scale : 0.5f * p.scale;
   uint32_t it = 0;
   bool dead = false;
   CacheWalk w;
@@ -207,7 +210,7 @@ __device__ void cc_consumer(const CacheFwdParams& p, uint8_t* smem, CcShared<MT>
         pos_min = min(pos_min, q.pos);
       }
       far_bias[i] = q.t >= 0 && p.bias_len
-                        ? __ldg(p.bias + static_cast<int64_t>(q.head) * p.bias_len + 2 * reach) * cc_bias_unit<ACT>()
+                        ? __ldg(p.bias + static_cast<int64_t>(q.head) * p.bias_len + 2 * reach) * kUnit
                         : 0.f;
     }
     pos_min = __reduce_min_sync(0xffffffffu, pos_min);
@@ -301,7 +304,7 @@ __device__ void cc_consumer(const CacheFwdParams& p, uint8_t* smem, CcShared<MT>
 #pragma unroll
             for (int i = 0; i < 2; ++i)
 #pragma unroll
-              for (int e = 0; e < 4; ++e) s[kb][i][e] = __fmaf_rn(s[kb][i][e], p.scale, far_bias[e >> 1]);
+              for (int e = 0; e < 4; ++e) s[kb][i][e] = __fmaf_rn(s[kb][i][e], scale, far_bias[e >> 1]);
         } else {
 #pragma unroll
           for (int kb = 0; kb < KB; ++kb)
@@ -313,7 +316,7 @@ __device__ void cc_consumer(const CacheFwdParams& p, uint8_t* smem, CcShared<MT>
 #pragma unroll
                 for (int h = 0; h < 2; ++h)
                   s[kb][i][2 * h + c] =
-                      __fmaf_rn(s[kb][i][2 * h + c], p.scale, cc_bias(p, rows[h], reach, key_pos) * cc_bias_unit<ACT>());
+                      __fmaf_rn(s[kb][i][2 * h + c], scale, cc_bias(p, rows[h], reach, key_pos) * kUnit);
               }
         }
         if (!plain) {
@@ -369,7 +372,7 @@ __device__ void cc_consumer(const CacheFwdParams& p, uint8_t* smem, CcShared<MT>
             for (int i = 0; i < 2; ++i)
 #pragma unroll
               for (int e = 0; e < 4; e += 2) {
-                const float2 y = act2_route<ACT, 0>(make_float2(0.5f * s[kb][i][e], 0.5f * s[kb][i][e + 1]));
+                const float2 y = cc_act2<ACT>(make_float2(s[kb][i][e], s[kb][i][e + 1]));
                 pv[kb][i][e] = y.x;
                 pv[kb][i][e + 1] = y.y;
               }

@@ -436,7 +436,7 @@ __device__ __forceinline__ void cw_act_tile(uint32_t t_s, float scale, float bia
     for (int c = 0; c < 32; ++c) {
       const uint32_t(&v)[32] = c < 16 ? a : b;
       const float2 hx = __ffma2_rn(make_float2(__uint_as_float(v[2 * (c % 16)]), __uint_as_float(v[2 * (c % 16) + 1])), hs, hb);
-      const float2 y = act2_route<ACT, 0>(hx);
+      const float2 y = cc_act2<ACT>(hx);
       pk[c] = pack_bf16(y.x, y.y);
     }
     tmem_st32(t_s + 16 * q, pk);  // columns [16 q, 16 q + 32) are read already

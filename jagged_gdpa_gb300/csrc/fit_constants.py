@@ -13,13 +13,18 @@ there can be re-derived from mathematics alone:
    grid, which converges to the minimax fit).
 3. The integer seed K for 1/a: as_float(K - as_int(a)) minimising the maximum
    relative error over one binade (the error is periodic in the exponent).
+4. Phi(-a) = 2^p(a) for a in [0, 13] (2^-127 at its end; cache.cuh): p of
+   degree LOG_PHI_DEG minimising the maximum absolute error of the exponent,
+   so that the relative error of Phi is the same however small it is.
 """
 
 import numpy as np
-from scipy.optimize import minimize
-from scipy.special import erf, expit
+from scipy.optimize import linprog, minimize
+from scipy.special import erf, expit, log_ndtr
 
 DEG = 3
+LOG_PHI_DEG = 6
+LOG_PHI_END = 13.0
 
 
 def fit_gelu_sigmoid():
@@ -71,6 +76,23 @@ def fit_rcp_seed():
     return best
 
 
+def fit_log2_phi(deg=LOG_PHI_DEG, end=LOG_PHI_END, n=2000):
+    a = end / 2 * (1.0 - np.cos(np.pi * np.arange(n) / (n - 1)))
+    y = log_ndtr(-a) / np.log(2.0)
+    V = np.vander(a / end, deg + 1, increasing=True)
+    one = np.ones((n, 1))
+    # minimise e subject to |V c - y| <= e
+    r = linprog(np.r_[np.zeros(deg + 1), 1.0], A_ub=np.block([[V, -one], [-V, -one]]), b_ub=np.r_[y, -y],
+                bounds=[(None, None)] * (deg + 1) + [(0, None)], method="highs")
+    c = (r.x[:-1] / end ** np.arange(deg + 1)).astype(np.float32)
+    # the error of the evaluation in fp32, Horner's scheme
+    x = np.linspace(0.0, end, 400001).astype(np.float32)
+    p = np.full_like(x, c[deg])
+    for k in range(deg - 1, -1, -1):
+        p = (p * x + c[k]).astype(np.float32)
+    return c, np.max(np.abs(np.exp2(p.astype(np.float64)) / np.exp(log_ndtr(-x.astype(np.float64))) - 1.0)), p[-1]
+
+
 if __name__ == "__main__":
     (a, b), e0, e1 = fit_gelu_sigmoid()
     print(f"GELU sigmoid form: a = {a:.9g}, b = {b:.9g}  (max abs err {e1:.3e}; tanh-form start {e0:.3e})")
@@ -78,3 +100,6 @@ if __name__ == "__main__":
     print(f"exp2 degree {DEG} on [-1/2, 1/2]: " + ", ".join(f"{v:.9g}" for v in c) + f"  (max rel err {e:.3e})")
     k, e = fit_rcp_seed()
     print(f"reciprocal seed K = 0x{k:08X}  (max rel err {e:.3e}; two Newton steps: {e**4:.3e})")
+    c, e, last = fit_log2_phi()
+    print(f"log2 Phi(-a) degree {LOG_PHI_DEG} on [0, {LOG_PHI_END:g}]: " + ", ".join(f"{v:.9g}" for v in c) +
+          f"  (max rel err of Phi {e:.3e}; exponent {last:.2f} at the end)")

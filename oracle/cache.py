@@ -47,7 +47,7 @@ def plan(ctx, new, held, table, free, count, page_size, total):
 
 def act(name, x):
     if name == "gelu":
-        return x * 0.5 * (1 + np.vectorize(math.erf)(x / math.sqrt(2)))
+        return x * 0.5 * np.vectorize(math.erfc)(-x / math.sqrt(2))  # (1 + erf has no digit left below -8)
     return x / (1 + np.exp(-x))
 
 

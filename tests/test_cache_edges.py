@@ -1,0 +1,58 @@
+"""The paged key/value cache at its edges."""
+
+import numpy as np
+import pytest
+import torch
+
+from tests.test_cache import Case, jg  # noqa: F401  (jg: the fixture)
+
+gpu = pytest.mark.gpu
+
+U = 2.0 ** -8  # half a bf16 step, relative
+
+
+# ------------------------------------------------------------ small weights (GPU)
+@gpu
+@pytest.mark.parametrize("act", ["gelu", "silu"])
+@pytest.mark.parametrize("d", [32, 64, 128])
+@pytest.mark.parametrize("group,new,window", [(1, 1, 0), (4, 6, 0), (2, 20, 0), (2, 40, 90), (8, 40, 0)])
+def test_scores_far_below_zero(jg, act, d, group, new, window):  # noqa: F811
+    """A bias that pushes every score to -4 and below: the weights are small, and
+    each is right relative to itself.  Roundings of an output, relative to
+    sum |P||V| (u = 2^-8):
+      P: u for its rounding to bf16, at most 2^-8 for the device's act, and the
+        score's error times |act'/act|: at most |x| + 1/|x| + 1 <= 16 for the
+        scores from -14 on (weights below that are 1e-30 of the others)
+      O: 2^-12 for the fp32 sums, u for the final rounding"""
+    rng = np.random.default_rng(new + d)
+    c = Case(d + new, [700, 0, 130, 61], [new, new, 1, new], 4, group, d, 16, act, bias=33, window=window, mask=new > 1)
+    c.bias = torch.from_numpy(rng.uniform(-9.0, -8.0, c.bias.shape).astype(np.float32))
+    out, _ = jg.jgdpa_cache_fwd(**c.kwargs())
+    want, _, size, dot, _ = c.oracle()
+    # scores: fp32 sums of d products, the bias, the fused rounding
+    score = d * 2.0 ** -23 * dot + 2.0 ** -19
+    tol = size * (2 * U + 2.0 ** -12 + 16 * score.T[..., None])
+    tol = tol + U * (np.abs(want) + tol)
+    got = out.double().cpu().numpy()
+    assert np.all(np.abs(got - want) <= tol), f"worst {np.nanmax(np.abs(got - want) / (tol + 1e-300)):.1f} tolerances"
+
+
+@gpu
+@pytest.mark.parametrize("act,lo", [("gelu", -12.5), ("silu", -80.0)])
+@pytest.mark.parametrize("d", [32, 64, 128])
+@pytest.mark.parametrize("kv_heads,group", [(256, 16), (32, 128)])
+def test_one_weight(jg, act, lo, d, kv_heads, group):  # noqa: F811
+    """One token that sees itself, q = 0, v = 1 and a bias of one entry per head:
+    out = act(bias), rounded to bf16 as a weight and as an output (u each), the
+    device's act within 2^-10 of itself, from where bf16 holds it on."""
+    c = Case(0, [0], [1], kv_heads, group, d, 16, act, bias=1, nan=False)
+    x = torch.linspace(lo, 16.0, c.heads - 2, dtype=torch.float32)
+    c.bias = torch.cat([x, torch.zeros(2)])[:, None].contiguous()
+    c.q.zero_()
+    c.v.fill_(1.0)
+    out, _ = jg.jgdpa_cache_fwd(**c.kwargs())
+    y = c.bias.double()
+    want = 0.5 * y * torch.erfc(-y * 0.5 ** 0.5) if act == "gelu" else y * torch.sigmoid(y)
+    got = out[0].double().cpu()
+    assert torch.all((got - want).abs() <= want.abs() * (2 * U + U * U + 2.0 ** -10))
+    assert not out[0, -2:].any()
