@@ -301,9 +301,16 @@ jgdpa_status jgdpa_cache_fwd(const void* q, int64_t q_stride, const void* k_cach
   if (!aligned(workspace, kAlign)) return JGDPA_ERR_MISALIGNED;
   put_together(&L, batch, kv_heads, max_rows, static_cast<int64_t>(table_width) * page_size);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
-  if (batch == 0 || total_q == 0 || max_q == 0) {
+  if (batch == 0) {
     JG_CUDA(cudaMemsetAsync(ws, 0, sizeof(int), stream));
     return JGDPA_OK;
+  }
+  if (total_q == 0 || max_q == 0) {  // no row is allowed: one CTA sees that the offsets hold none
+    max_q = 0;
+    L.wide = L.pairs = false;
+    L.rows = 16;
+    L.heads = L.grid = 1;
+    L.tokens = 0;
   }
   jg::CacheFwdParams p{};
   const int32_t box = L.wide ? jg::kTile : 64;
@@ -354,7 +361,7 @@ jgdpa_status jgdpa_cache_fwd(const void* q, int64_t q_stride, const void* k_cach
   p.min_part = L.wide ? 2 : 1;
   p.scale = act == JGDPA_ACT_SOFTMAX ? scale * jg::kLog2e : scale;
   p.wait_limit_ns = jg::host_wait_limit_ns();
-  const int tile_rows = L.wide ? L.rows : static_cast<int>(std::min<int64_t>(L.rows, max_rows));  // that may live
+  const int tile_rows = L.wide ? L.rows : static_cast<int>(std::clamp<int64_t>(max_rows, 1, L.rows));  // that may live
   auto launch = [&](auto dim) -> cudaError_t {
     constexpr int D = decltype(dim)::value;
     cudaError_t e = L.wide ? jg::launch_cache_fwd_wide_d<D>(p, act, L.pairs, L.grid, stream)

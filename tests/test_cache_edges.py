@@ -4,11 +4,19 @@ import numpy as np
 import pytest
 import torch
 
-from tests.test_cache import Case, jg  # noqa: F401  (jg: the fixture)
+from tests.test_cache import Case, i32, jg  # noqa: F401  (jg: the fixture)
 
 gpu = pytest.mark.gpu
 
 U = 2.0 ** -8  # half a bf16 step, relative
+
+
+def status_of(jg, case, **kw):  # noqa: F811
+    """(out, lse, status) of a call with a workspace of its own."""
+    ws = torch.empty(max(256, jg.jgdpa_cache_fwd_workspace_bytes(case.heads, case.kv_heads, case.d, kw["max_q"])),
+                     dtype=torch.uint8, device="cuda")
+    out, lse = jg.jgdpa_cache_fwd(**kw, workspace=ws)
+    return out, lse, jg.jgdpa_read_device_status(ws)
 
 
 # ------------------------------------------------------------ small weights (GPU)
@@ -56,3 +64,26 @@ def test_one_weight(jg, act, lo, d, kv_heads, group):  # noqa: F811
     got = out[0].double().cpu()
     assert torch.all((got - want).abs() <= want.abs() * (2 * U + U * U + 2.0 ** -10))
     assert not out[0, -2:].any()
+
+
+# ------------------------------------------------------------ refusals and reports
+
+
+@gpu
+@pytest.mark.parametrize("act", ["gelu", "softmax"])
+@pytest.mark.parametrize("d,kv_heads", [(32, 4), (64, 2), (128, 1)])
+@pytest.mark.parametrize("most", [0, 1, 40])
+def test_calls_without_rows_report_bad_offsets(jg, act, d, kv_heads, most):  # noqa: F811
+    """max_q = 0, or a q without rows, where the offsets hold new tokens."""
+    c = Case(1, [5, 40], [3, 2], kv_heads, 2, d, 16, act)
+    kw = c.kwargs()
+    out = torch.full_like(kw["q"], 7.0)
+    if most == 0:  # rows, but no token allowed
+        got, _, status = status_of(jg, c, **{**kw, "max_q": 0, "out": out})
+        assert status == 6 and torch.all(got == 7.0)
+    assert status_of(jg, c, **{**kw, "max_q": most, "q": kw["q"][:0]})[2] == 6
+    none = {**kw, "max_q": most, "q_offsets": torch.zeros_like(kw["q_offsets"])}
+    got, _, status = status_of(jg, c, **{**none, "out": out})
+    assert status == 0 and torch.all(got == 7.0)  # padding rows alone
+    assert status_of(jg, c, **{**none, "q": kw["q"][:0]})[2] == 0
+    assert status_of(jg, c, **{**none, "q": kw["q"][:0], "kv_lens": i32([5, -1], "cuda")})[2] == 6
