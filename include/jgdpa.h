@@ -363,7 +363,7 @@ JGDPA_API jgdpa_status jgdpa_cache_append(const void* k_new, const void* v_new, 
  *                [total_q][mask_words]: bit u % 32 of word u / 32 of its row
  *                says whether it sees new token u of its request (itself
  *                included); T_b must be at most 32 mask_words
- *   depths       NULL or int32 [total_q], >= 0: new token t is at position
+ *   depths       NULL or int32 [total_q], >= 0: new token t is at position (an int32)
  *                C + depths (C + t without), and context token j at j; the bias
  *                index is clamp(pos_i - pos_j, -R, R) + R and a window w > 0
  *                keeps pairs with |pos_i - pos_j| < w
@@ -379,9 +379,11 @@ JGDPA_API jgdpa_status jgdpa_cache_append(const void* k_new, const void* v_new, 
  * last place relative to themselves, far below zero, too.
  * Device-detected errors: BAD_OFFSETS (offsets not monotone from 0, beyond
  * total_q, T_b > max_q or more than the tree mask's columns, kv_lens[b] < T_b or
- * beyond the table), in which case nothing is written; BAD_PAGE (a table entry
- * of a live token outside [0, num_pages)): no such page is read, and its
- * request's outputs are unspecified.
+ * beyond the table), in which case nothing is written; BAD_OFFSETS also for a
+ * depth that is negative or leads beyond position 2^31 - 1, and BAD_PAGE (a table
+ * entry of a live token outside [0, num_pages)): no such page is read.  After
+ * these two the outputs of the request concerned are unspecified, the others as
+ * without it.
  */
 JGDPA_API size_t jgdpa_cache_fwd_workspace_bytes(int32_t heads, int32_t kv_heads, int32_t head_dim, int32_t max_q);
 JGDPA_API jgdpa_status jgdpa_cache_fwd(const void* q, int64_t q_stride, const void* k_cache, const void* v_cache,

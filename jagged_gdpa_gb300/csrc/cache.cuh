@@ -430,15 +430,25 @@ __device__ __forceinline__ uint32_t cc_nonfinite(uint32_t v) {
   return ((v & 0x7F80u) == 0x7F80u ? 0xFFFFu : 0u) | ((v & 0x7F800000u) == 0x7F800000u ? 0xFFFF0000u : 0u);
 }
 
-// The depth of key j's token (0 for the context).
-__device__ __forceinline__ int cc_depth(const CacheFwdParams& p, const CacheReq& r, int j) {
-  const int u = j - r.C;
-  if (u < 0 || j >= r.L) return 0;
-  return p.depth != nullptr ? __ldg(p.depth + r.q0 + u) : u;
+// The position of new token u: C + depth, a negative depth taken as 0 and a
+// position beyond 2^31 - 1 as that, which keeps what follows from positions (keys
+// behind the window or the bias table's reach, in 32 bits) true of any input.
+__device__ __forceinline__ int cc_new_pos(const CacheFwdParams& p, const CacheReq& r, int u) {
+  if (p.depth == nullptr) return r.C + u;
+  const int depth = max(__ldg(p.depth + r.q0 + u), 0);
+  return static_cast<int>(min(static_cast<uint32_t>(r.C) + static_cast<uint32_t>(depth), 0x7FFFFFFFu));
 }
-// Its position.
+// The same for the token of a query row; depths out of range are reported.
+__device__ __forceinline__ int cc_row_pos(const CacheFwdParams& p, const CacheReq& r, int t, int* status) {
+  if (p.depth != nullptr) {
+    const int depth = __ldg(p.depth + r.q0 + t);
+    if (depth < 0 || depth > INT32_MAX - r.C) atomicCAS(status, kOk, kErrBadOffsets);
+  }
+  return cc_new_pos(p, r, t);
+}
+// The position of key j (C for places behind the last token).
 __device__ __forceinline__ int cc_pos(const CacheFwdParams& p, const CacheReq& r, int j) {
-  return j < r.C ? j : r.C + cc_depth(p, r, j);
+  return j < r.C ? j : (j < r.L ? cc_new_pos(p, r, j - r.C) : r.C);
 }
 
 __device__ __forceinline__ uint32_t cc_ones(int n) { return n >= 32 ? 0xFFFFFFFFu : (n <= 0 ? 0u : (1u << n) - 1u); }

@@ -205,7 +205,7 @@ __device__ void cc_consumer(const CacheFwdParams& p, uint8_t* smem, CcShared<MT>
       q.far_bias = 0.f;
       qrow[i] = nullptr;
       if (q.t >= 0) {
-        q.pos = r.C + (p.depth != nullptr ? __ldg(p.depth + r.q0 + q.t) : q.t);
+        q.pos = cc_row_pos(p, r, q.t, fail.status);
         qrow[i] = p.q + static_cast<int64_t>(r.q0 + q.t) * p.q_stride + static_cast<int64_t>(q.head) * D;
         pos_min = min(pos_min, q.pos);
       }

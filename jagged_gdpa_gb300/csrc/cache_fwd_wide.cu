@@ -691,7 +691,7 @@ __device__ void cw_consumer(const CacheFwdParams& p, CwShared* sh, uint32_t tmem
     CcRow q;
     q.t = row_ok ? part.first_token + before + at : -1;
     q.head = w.h * p.group + (row_ok ? g : 0);
-    q.pos = r.C + (row_ok ? (p.depth != nullptr ? __ldg(p.depth + r.q0 + q.t) : q.t) : 0);
+    q.pos = row_ok ? cc_row_pos(p, r, q.t, fail.status) : r.C;
     q.far_bias = 0.f;
     if (row_ok && p.bias_len)
       q.far_bias = __ldg(p.bias + static_cast<int64_t>(q.head) * p.bias_len + 2 * reach) * cc_bias_unit<ACT>();

@@ -4,7 +4,7 @@ import numpy as np
 import pytest
 import torch
 
-from tests.test_cache import Case, i32, jg  # noqa: F401  (jg: the fixture)
+from tests.test_cache import Case, compare, i32, jg  # noqa: F401  (jg: the fixture)
 
 gpu = pytest.mark.gpu
 
@@ -87,3 +87,39 @@ def test_calls_without_rows_report_bad_offsets(jg, act, d, kv_heads, most):  # n
     assert status == 0 and torch.all(got == 7.0)  # padding rows alone
     assert status_of(jg, c, **{**none, "q": kw["q"][:0]})[2] == 0
     assert status_of(jg, c, **{**none, "q": kw["q"][:0], "kv_lens": i32([5, -1], "cuda")})[2] == 6
+
+
+@gpu
+@pytest.mark.parametrize("act", ["gelu", "softmax"])
+@pytest.mark.parametrize("new,window", [(3, 0), (3, 50), (40, 0), (40, 50)])
+@pytest.mark.parametrize("depth", [-1, -2 ** 31, 2 ** 31 - 70, 2 ** 31 - 1])
+def test_depths_out_of_range_are_reported(jg, act, new, window, depth):  # noqa: F811
+    """A negative depth, or one that leads beyond position 2^31 - 1: status
+    BAD_OFFSETS, and the other request is as without it."""
+    c = Case(13, [100, 30], [new, new], 2, 2, 64, 16, act, bias=33, window=window, mask=True, nan=False)
+    kw = c.kwargs()
+    good, good_lse, status = status_of(jg, c, **kw)
+    assert status == 0
+    depths = kw["depths"].clone()
+    depths[1] = depth
+    out, lse, status = status_of(jg, c, **{**kw, "depths": depths})
+    assert status == 6
+    n = int(c.off[1])
+    assert torch.equal(out[n:], good[n:])
+    if lse is not None:
+        assert torch.equal(lse[:, n:], good_lse[:, n:])
+
+
+@gpu
+@pytest.mark.parametrize("act", ["gelu", "softmax"])
+@pytest.mark.parametrize("new,window", [(3, 0), (3, 50), (40, 50)])
+def test_the_largest_depths(jg, act, new, window):  # noqa: F811
+    """Positions up to 2^31 - 1."""
+    c = Case(14, [100, 30], [new, new], 2, 2, 64, 16, act, bias=33, window=window, mask=True)
+    for b in range(2):
+        lo, hi = int(c.off[b]), int(c.off[b + 1])
+        top = 2 ** 31 - 1 - int(c.kv[b] - c.new[b])
+        c.depth[lo + 1:hi] = top - np.arange(hi - lo - 1)[::-1]
+    out, lse, status = status_of(jg, c, **c.kwargs())
+    assert status == 0
+    compare(c, out, lse)
