@@ -101,6 +101,7 @@ struct CacheFwdParams {
   int32_t batch, max_q, heads, kv_heads, group;
   int32_t page_shift, width, num_pages;
   int32_t mask_words, bias_len, window;
+  int32_t bias_hides;        // softmax with a bias table, whose entries of -inf hide keys
   int32_t rows_per_tile;     // query rows (token, head of the group) of one item
   int32_t tile_tokens;       // tokens of a 128-row tile (128-row kernel; 0 otherwise)
   int32_t heads_per_item;    // key/value heads of one item

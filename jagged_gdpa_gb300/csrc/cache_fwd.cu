@@ -213,6 +213,8 @@ __device__ void cc_consumer(const CacheFwdParams& p, uint8_t* smem, CcShared<MT>
                         ? __ldg(p.bias + static_cast<int64_t>(q.head) * p.bias_len + 2 * reach) * kUnit
                         : 0.f;
     }
+    // a softmax bias of -inf hides keys as the mask does; some row's for all far ones
+    const bool hides = ACT == 2 && __any_sync(0xffffffffu, far_bias[0] == -INFINITY || far_bias[1] == -INFINITY);
     pos_min = __reduce_min_sync(0xffffffffu, pos_min);
     const int pos_max = __reduce_max_sync(0xffffffffu, max(rows[0].t >= 0 ? rows[0].pos : 0, rows[1].t >= 0 ? rows[1].pos : 0));
     // Q fragments: rows lane / 4 (+ 8), columns 16 ks + 2 (lane % 4) (+ 8)
@@ -239,9 +241,10 @@ __device__ void cc_consumer(const CacheFwdParams& p, uint8_t* smem, CcShared<MT>
       if (!dead && key0 < r.L) {
         const uint32_t kt = base + st * 2 * C::kTileBytes, vt = kt + C::kTileBytes;
         // plain: every key of the warp's is seen by every row; far: R or more behind
+        // (of nearer ones only the bias table's entries say which are hidden)
         const int last = key0 + 16 * KB - 1;
-        const bool plain = last < r.C && (p.window <= 0 || pos_max - key0 < p.window);
         const bool far = p.bias_len == 0 || (last < r.C && pos_min - last >= reach);
+        const bool plain = last < r.C && (p.window <= 0 || pos_max - key0 < p.window) && (ACT != 2 || (far && !hides));
         uint32_t see[(KB + 1) / 2][2];  // by 32 keys
         bool odd = false;
         if (!plain) {
@@ -267,6 +270,7 @@ __device__ void cc_consumer(const CacheFwdParams& p, uint8_t* smem, CcShared<MT>
                 }
                 bits &= near;  // (only this lane's columns are kept)
               }
+              if (ACT == 2 && far && far_bias[h] == -INFINITY) bits = 0;
               see[j][h] = bits;
             }
           const __nv_bfloat162 zero = __float2bfloat162_rn(0.f);
@@ -314,9 +318,12 @@ __device__ void cc_consumer(const CacheFwdParams& p, uint8_t* smem, CcShared<MT>
               for (int c = 0; c < 2; ++c) {
                 const int key_pos = cc_pos(p, r, key0 + 16 * kb + 8 * i + 2 * (lane & 3) + c);
 #pragma unroll
-                for (int h = 0; h < 2; ++h)
-                  s[kb][i][2 * h + c] =
-                      __fmaf_rn(s[kb][i][2 * h + c], scale, cc_bias(p, rows[h], reach, key_pos) * kUnit);
+                for (int h = 0; h < 2; ++h) {
+                  const float bias = cc_bias(p, rows[h], reach, key_pos) * kUnit;
+                  s[kb][i][2 * h + c] = __fmaf_rn(s[kb][i][2 * h + c], scale, bias);
+                  if (ACT == 2 && bias == -INFINITY)
+                    see[kb >> 1][h] &= ~(1u << (16 * (kb & 1) + 8 * i + 2 * (lane & 3) + c));
+                }
               }
         }
         if (!plain) {

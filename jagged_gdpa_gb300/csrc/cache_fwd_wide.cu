@@ -94,7 +94,7 @@ struct CwPart {
   int first_token;  // of the part's rows
   int tokens;       // of them
   bool pair;        // two tiles of rows; otherwise one
-  int plain_lo, plain_hi;  // tiles in which every row sees every key
+  int plain_lo, plain_hi;  // tiles in which every row sees every key, whatever the bias table's entries
   int far_hi;              // tiles below it are plain in the bias: R or more behind every row
 
   __device__ __forceinline__ CwPart() {}
@@ -122,6 +122,12 @@ struct CwPart {
     }
     const int reach = max((p.bias_len - 1) / 2, 1);
     far_hi = p.bias_len == 0 ? INT32_MAX : (C >= reach ? (C - reach + 1) / kTile : 0);
+    if (p.bias_hides) {  // -inf as the bias of some row's far keys; of nearer ones only the table's entries say
+      bool hides = false;
+      for (int g = threadIdx.x & 31; g < p.group; g += 32)
+        hides = hides || __ldg(p.bias + static_cast<int64_t>(w.h * p.group + g + 1) * p.bias_len - 1) == -INFINITY;
+      plain_hi = __any_sync(0xffffffffu, hides) ? 0 : min(plain_hi, far_hi);
+    }
   }
   __device__ __forceinline__ bool plain(int tile) const { return tile >= plain_lo && tile < plain_hi; }
   // The tiles of stream s, and the one it takes as its i-th.
@@ -383,7 +389,8 @@ static __device__ __noinline__ CwNear cw_near(const CacheFwdParams& p, CacheReq 
 
 // S -> s S + bias (in log2 units for softmax) in place, for the tiles near the
 // new tokens, where the bias varies from key to key or some rows do not see
-// some keys (-inf for softmax, else 0, as act(0) = 0).
+// some keys (-inf for softmax, else 0, as act(0) = 0), those that a softmax
+// bias of -inf hides among them.
 template <int ACT>
 __device__ __noinline__ void cw_near_tile(const CacheFwdParams& p, int C, CcRow q, CwNear t, int key0, uint32_t t_s) {
   const int reach = (p.bias_len - 1) / 2;
@@ -398,6 +405,7 @@ __device__ __noinline__ void cw_near_tile(const CacheFwdParams& p, int C, CcRow 
       tmem_ld_wait(v);
 #pragma unroll
       for (int c = 0; c < 32; ++c) v[c] = __float_as_uint(__fmaf_rn(__uint_as_float(v[c]), p.scale, q.far_bias));
+      if (ACT == 2 && q.far_bias == -INFINITY) t.see[0] = 0;
     } else {
       float bias[32];
 #pragma unroll
@@ -407,6 +415,11 @@ __device__ __noinline__ void cw_near_tile(const CacheFwdParams& p, int C, CcRow 
 #pragma unroll
       for (int c = 0; c < 32; ++c)
         v[c] = __float_as_uint(__fmaf_rn(__uint_as_float(v[c]), p.scale, bias[c] * cc_bias_unit<ACT>()));
+      if constexpr (ACT == 2) {
+#pragma unroll
+        for (int c = 0; c < 32; ++c)
+          if (bias[c] == -INFINITY) t.see[0] &= ~(1u << c);
+      }
     }
 #pragma unroll
     for (int c = 0; c < 32; ++c)
@@ -552,6 +565,7 @@ __device__ __noinline__ void cw_add_odd(const CacheFwdParams& p, CacheWalk w, Cw
       if (static_cast<uint32_t>(page) >= static_cast<uint32_t>(p.num_pages)) continue;
       const int key_pos = cc_pos(p, r, key);
       if (!(cc_vis32(p, r, q, key) & 1) || !cc_near(p, q.pos, key_pos)) continue;
+      if (p.bias_hides && cc_bias(p, q, (p.bias_len - 1) / 2, key_pos) == -INFINITY) continue;
       const int64_t place = static_cast<int64_t>(key & ((1 << p.page_shift) - 1)) * p.kv_heads * D + w.h * D;
       const __nv_bfloat16* v = p.v_cache + page * p.v_page_stride + place;
       bool any = false;

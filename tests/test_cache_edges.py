@@ -123,3 +123,36 @@ def test_the_largest_depths(jg, act, new, window):  # noqa: F811
     out, lse, status = status_of(jg, c, **c.kwargs())
     assert status == 0
     compare(c, out, lse)
+
+
+# ------------------------------------------------------------ keys hidden by the bias (GPU)
+@gpu
+@pytest.mark.parametrize("d,kv_heads,new,group", [(32, 4, 3, 1), (32, 3, 20, 1), (64, 2, 1, 4), (64, 2, 12, 2), (128, 2, 1, 2),
+                                                  (32, 4, 40, 1), (64, 2, 30, 4), (128, 2, 70, 2)])
+@pytest.mark.parametrize("room", [0, 1 << 16])
+@pytest.mark.parametrize("where", ["far", "near", "one head"])
+def test_keys_hidden_by_the_bias_hold_anything(jg, d, kv_heads, new, group, room, where):  # noqa: F811
+    """Softmax with bias entries of -inf: NaN and infinities in keys and values
+    that they hide change nothing."""
+    c = Case(19, [900, 0, 300, 64], [new] * 4, kv_heads, group, d, 32, "softmax", bias=257, mask=new > 1)
+    kw = c.kwargs(room=room)
+    bias = kw["bias_table"]
+    # distances to hide (the index is distance + 128, the last entry all from 128 on)
+    hide = {"far": slice(128 + 100, None), "near": slice(128 + 70, 128 + 90), "one head": slice(128 + 100, None)}[where]
+    heads = slice(0, group) if where == "one head" else slice(None)  # the query heads of key/value head 0
+    bias[heads, hide] = -float("inf")
+    clean, clean_lse = jg.jgdpa_cache_fwd(**kw)
+    # key j of request 0 is 900 + depth - j away from its tokens: hidden from all of them
+    top = 0 if c.depth is None else int(np.max(c.depth[:new]))
+    keys = range(900 - 90 + top + 1, 900 - 70) if where == "near" else range(0, 900 - 100 + 1)
+    kv = slice(0, 1) if where == "one head" else slice(None)
+    assert len(keys) > 0 and top < 19
+    for value in (float("nan"), float("inf"), -float("inf")):
+        k, v = kw["k_cache"].clone(), kw["v_cache"].clone()
+        for j in list(keys)[::5]:
+            page, at = int(c.table[0, j // 32]), j % 32
+            v[page, at, kv] = value
+            if j % 2:
+                k[page, at, kv, 3] = value
+        out, lse = jg.jgdpa_cache_fwd(**{**kw, "k_cache": k, "v_cache": v})
+        assert torch.equal(out, clean) and torch.equal(lse, clean_lse)
