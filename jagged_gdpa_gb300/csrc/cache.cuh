@@ -423,8 +423,21 @@ __device__ __forceinline__ float2 cc_act2(float2 hx) {
 template <int ACT>
 __device__ __forceinline__ float cc_act(float x) { return cc_act2<ACT>(f2(0.5f * x)).x; }
 
+// A bias table's entry in the units of the scores, log2 units for softmax.
+// Finite entries that leave fp32 there (the type's lowest value as a mask) stay
+// finite: where nothing else is seen, their keys weigh the same.
+constexpr float kFltMax = 3.402823466e38f;
 template <int ACT>
-__device__ __forceinline__ float cc_bias_unit() { return ACT == 2 ? kLog2e : 1.0f; }
+__device__ __forceinline__ float cc_bias_in_units(float b) {
+  if constexpr (ACT != 2) return b;
+  const float x = b * kLog2e, a = fabsf(b);
+  return a > 2.358e38f && a <= kFltMax ? copysignf(kFltMax, b) : x;  // (2.358e38 log2 e is still finite)
+}
+// The LSE of a row from its maximum (log2 units) and sum.
+__device__ __forceinline__ float cc_lse(float m, float l) {
+  if (l == 0.f) return -INFINITY;
+  return fabsf(m) == kFltMax ? m : (m + log2f(l)) * kLn2;  // (such a bias is its row's LSE)
+}
 
 // The halves of a packed bf16 pair that are infinite or NaN, as a mask.
 __device__ __forceinline__ uint32_t cc_nonfinite(uint32_t v) {

@@ -177,9 +177,9 @@ __device__ void cc_consumer(const CacheFwdParams& p, uint8_t* smem, CcShared<MT>
   const uint32_t step1 = 16 * (pr >= 32 ? row_bytes : 2 * W), step2 = 32 * (pr >= 64 ? row_bytes : 2 * W);
   auto block = [&](int kb) { return (kb & 1) * step1 + (kb >> 1) * step2; };
   const int reach = (p.bias_len - 1) / 2;
-  // scores in log2 units, or halved as cc_act2 takes them
-  constexpr float kUnit = ACT == 2 ? kLog2e : 0.5f;
-  const float scale = ACT == 2 ? p.scale : 0.5f * p.scale;
+  // (GELU and SiLU scores are halved, as cc_act2 takes them)
+  constexpr float kHalf = ACT == 2 ? 1.f : 0.5f;
+  const float scale = kHalf * p.scale;
   uint32_t it = 0;
   bool dead = false;
   CacheWalk w;
@@ -209,9 +209,9 @@ __device__ void cc_consumer(const CacheFwdParams& p, uint8_t* smem, CcShared<MT>
         qrow[i] = p.q + static_cast<int64_t>(r.q0 + q.t) * p.q_stride + static_cast<int64_t>(q.head) * D;
         pos_min = min(pos_min, q.pos);
       }
-      far_bias[i] = q.t >= 0 && p.bias_len
-                        ? __ldg(p.bias + static_cast<int64_t>(q.head) * p.bias_len + 2 * reach) * kUnit
-                        : 0.f;
+      far_bias[i] = 0.f;
+      if (q.t >= 0 && p.bias_len)
+        far_bias[i] = kHalf * cc_bias_in_units<ACT>(__ldg(p.bias + static_cast<int64_t>(q.head) * p.bias_len + 2 * reach));
     }
     // a softmax bias of -inf hides keys as the mask does; some row's for all far ones
     const bool hides = ACT == 2 && __any_sync(0xffffffffu, far_bias[0] == -INFINITY || far_bias[1] == -INFINITY);
@@ -319,7 +319,7 @@ __device__ void cc_consumer(const CacheFwdParams& p, uint8_t* smem, CcShared<MT>
                 const int key_pos = cc_pos(p, r, key0 + 16 * kb + 8 * i + 2 * (lane & 3) + c);
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                  const float bias = cc_bias(p, rows[h], reach, key_pos) * kUnit;
+                  const float bias = kHalf * cc_bias_in_units<ACT>(cc_bias(p, rows[h], reach, key_pos));
                   s[kb][i][2 * h + c] = __fmaf_rn(s[kb][i][2 * h + c], scale, bias);
                   if (ACT == 2 && bias == -INFINITY)
                     see[kb >> 1][h] &= ~(1u << (16 * (kb & 1) + 8 * i + 2 * (lane & 3) + c));
@@ -502,7 +502,7 @@ __device__ void cc_consumer(const CacheFwdParams& p, uint8_t* smem, CcShared<MT>
           if (c0 == 0 && cc == 0) {
             if (!w.whole) p.part_ml[prow] = make_float2(M, L);
             else if (p.lse != nullptr)
-              p.lse[static_cast<int64_t>(head) * p.total_q + token] = L == 0.f ? -INFINITY : (M + log2f(L)) * kLn2;
+              p.lse[static_cast<int64_t>(head) * p.total_q + token] = cc_lse(M, L);
           }
         }
         float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -648,7 +648,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) cache_join_kernel(const __gri
 #pragma unroll
     for (int e = 0; e < V; ++e) acc[e] *= inv;
     if (lane == 0 && p.lse != nullptr)
-      p.lse[static_cast<int64_t>(head) * p.total_q + token] = L == 0.f ? -INFINITY : (M + log2f(L)) * kLn2;
+      p.lse[static_cast<int64_t>(head) * p.total_q + token] = cc_lse(M, L);
   }
   __nv_bfloat16* dst = p.out + (token * p.heads + head) * D + lane * V;
   if constexpr (V == 4) *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16(acc[0], acc[1]), pack_bf16(acc[2], acc[3]));

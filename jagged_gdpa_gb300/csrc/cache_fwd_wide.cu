@@ -410,11 +410,11 @@ __device__ __noinline__ void cw_near_tile(const CacheFwdParams& p, int C, CcRow 
       float bias[32];
 #pragma unroll
       for (int c = 0; c < 32; ++c)
-        bias[c] = __ldg(bias_row + min(max(q.pos - __shfl_sync(0xffffffffu, t.pos[0], c), -reach), reach));
+        bias[c] = cc_bias_in_units<ACT>(__ldg(bias_row + min(max(q.pos - __shfl_sync(0xffffffffu, t.pos[0], c), -reach), reach)));
       tmem_ld_wait(v);
 #pragma unroll
       for (int c = 0; c < 32; ++c)
-        v[c] = __float_as_uint(__fmaf_rn(__uint_as_float(v[c]), p.scale, bias[c] * cc_bias_unit<ACT>()));
+        v[c] = __float_as_uint(__fmaf_rn(__uint_as_float(v[c]), p.scale, bias[c]));
       if constexpr (ACT == 2) {
 #pragma unroll
         for (int c = 0; c < 32; ++c)
@@ -708,13 +708,15 @@ __device__ void cw_consumer(const CacheFwdParams& p, CwShared* sh, uint32_t tmem
     q.pos = row_ok ? cc_row_pos(p, r, q.t, fail.status) : r.C;
     q.far_bias = 0.f;
     if (row_ok && p.bias_len)
-      q.far_bias = __ldg(p.bias + static_cast<int64_t>(q.head) * p.bias_len + 2 * reach) * cc_bias_unit<ACT>();
+      q.far_bias = cc_bias_in_units<ACT>(__ldg(p.bias + static_cast<int64_t>(q.head) * p.bias_len + 2 * reach));
     const bool warp_live = __any_sync(0xffffffffu, row_ok);
     const int count = part.count(stream);
     float m = -INFINITY, l = 0.f;
     for (int i = 0; i < count; ++i) {
       const int tile = part.lo + part.at(stream, i);
-      const bool far = tile < part.far_hi, plain = part.plain(tile);
+      // (a bias beside which scores are lost takes the near tiles' way for all keys, where it is added to them first)
+      const bool huge = ACT == 2 && __any_sync(0xffffffffu, fabsf(q.far_bias) > 1e18f);
+      const bool far = tile < part.far_hi && !huge, plain = part.plain(tile);
       CwNear near;
       if ((!plain || !far) && warp_live) near = cw_near(p, r, q, plain, tile * kTile);
       if (!dead && !mbar_wait(&sh->s_full[stream], s_n & 1, fail)) dead = true;
@@ -806,7 +808,7 @@ __device__ void cw_consumer(const CacheFwdParams& p, CwShared* sh, uint32_t tmem
     if (ACT == 2 && o_col == 0) {
       if (!w.whole) p.part_ml[prow] = make_float2(m, l);
       else if (p.lse != nullptr)
-        p.lse[static_cast<int64_t>(q.head) * p.total_q + token] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+        p.lse[static_cast<int64_t>(q.head) * p.total_q + token] = cc_lse(m, l);
     }
   }
 }

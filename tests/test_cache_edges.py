@@ -156,3 +156,22 @@ def test_keys_hidden_by_the_bias_hold_anything(jg, d, kv_heads, new, group, room
                 k[page, at, kv, 3] = value
         out, lse = jg.jgdpa_cache_fwd(**{**kw, "k_cache": k, "v_cache": v})
         assert torch.equal(out, clean) and torch.equal(lse, clean_lse)
+
+
+@gpu
+@pytest.mark.parametrize("d,kv_heads,new,group", [(32, 4, 3, 1), (64, 2, 12, 2), (128, 2, 1, 2), (64, 2, 40, 2), (128, 2, 70, 2)])
+@pytest.mark.parametrize("value", [torch.finfo(torch.float32).min, torch.finfo(torch.float32).max])
+def test_biases_of_the_largest_finite_size(jg, d, kv_heads, new, group, value):  # noqa: F811
+    """Softmax whose every score is the lowest (or highest) fp32: the scores
+    are lost beside it, so that all seen keys weigh the same, and the LSE is
+    that value."""
+    c = Case(27, [900, 0, 300, 64], [new] * 4, kv_heads, group, d, 32, "softmax", bias=257, mask=new > 1)
+    c.bias[:] = value
+    out, lse = jg.jgdpa_cache_fwd(**c.kwargs())
+    want, want_lse, size, _, _ = c.oracle()
+    # weights 1 / n: 2^-12 for fp32 sums, u for O (a weight of 1 is exact in bf16)
+    got = out.double().cpu().numpy()
+    tol = size * 2.0 ** -12
+    tol = tol + U * (np.abs(want) + tol)
+    assert np.all(np.abs(got - want) <= tol)
+    assert np.all(np.abs(lse.double().cpu().numpy() / want_lse - 1) <= 2.0 ** -22)
