@@ -428,6 +428,7 @@ def jgdpa_bwd_shared_q(q, k, v, out, lse, dout, kv_offsets, act, scale: float, b
 # These calls belong to a serving step, where some tens of microseconds of
 # Python per call would be what the step waits for: each wrapper first tests
 # everything in one pass, and names what is wrong (`_refuse_*`) only if a test fails.
+_I32_MAX = (1 << 31) - 1
 _i32, _f32, _bf16, _u8 = torch.int32, torch.float32, torch.bfloat16, torch.uint8
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
@@ -479,6 +480,13 @@ def _contiguous(**tensors):
     for name, t in tensors.items():
         if t is not None and not t.is_contiguous():
             raise ValueError(f"{name} must be contiguous")
+
+
+def _refuse_wide(**numbers):
+    """ctypes would cut them to 32 bits without a word."""
+    for name, n in numbers.items():
+        if not -(1 << 31) <= n < 1 << 31:
+            raise ValueError(f"{name} must fit in 32 bits, got {n}")
 
 
 def _need_cuda(t: torch.Tensor):
@@ -552,6 +560,9 @@ def jgdpa_cache_plan(ctx_lens, new_lens, held_pages, block_table, free_pages, fr
     place.  total_new: rows of slots, at least the sum of new_lens.  workspace:
     where a device-detected error (out of pages) is to be read from."""
     lib = lib or load()
+    page_size, total_new = int(page_size), int(total_new)
+    if max(page_size, total_new) > _I32_MAX or page_size < -_I32_MAX:
+        _refuse_wide(page_size=page_size, total_new=total_new)
     try:
         index, shape = ctx_lens.get_device(), ctx_lens.shape
         batch, width = block_table.shape
@@ -565,9 +576,10 @@ def jgdpa_cache_plan(ctx_lens, new_lens, held_pages, block_table, free_pages, fr
     if not ok:
         _refuse_plan(ctx_lens, new_lens, held_pages, block_table, free_pages, free_count, workspace)
         raise ValueError("jgdpa_cache_plan: unusable tensors")
-    total_new = int(total_new)
     if total_new < 0:
         raise ValueError("total_new must not be negative")
+    if max(width, pages) > _I32_MAX:
+        _refuse_wide(**{"block_table's width": width, "free_pages' length": pages})
     if index != torch.cuda.current_device():
         return _on_other_device(jgdpa_cache_plan, ctx_lens.device, (ctx_lens, new_lens, held_pages, block_table, free_pages,
                                 free_count, page_size, total_new, workspace, stream, lib), {})
@@ -582,7 +594,7 @@ def jgdpa_cache_plan(ctx_lens, new_lens, held_pages, block_table, free_pages, fr
     else:
         slots, q_offsets, kv_lens, held, count = (alloc(n, _i32) for n in (total_new, batch + 1, batch, batch, 1))
     ws, ws_bytes = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel())
-    rc = lib.jgdpa_cache_plan(ctx_lens.data_ptr(), new_lens.data_ptr(), held_pages.data_ptr(), batch, int(page_size),
+    rc = lib.jgdpa_cache_plan(ctx_lens.data_ptr(), new_lens.data_ptr(), held_pages.data_ptr(), batch, page_size,
                               block_table.data_ptr(), width, free_pages.data_ptr(), pages, free_count.data_ptr(),
                               total_new, held.data_ptr(), count.data_ptr(), q_offsets.data_ptr(), kv_lens.data_ptr(),
                               slots.data_ptr(), ws, ws_bytes, raw)
@@ -626,6 +638,8 @@ def jgdpa_cache_append(k_new, v_new, slots, k_cache, v_cache, stream=None, lib=N
     if not (ks and vs and kps and vps):
         _refuse_append(k_new, v_new, slots, k_cache, v_cache)
         raise ValueError("jgdpa_cache_append: unusable tensors")
+    if max(rows, n) > _I32_MAX:
+        _refuse_wide(**{"k_new's rows": rows, "k_cache's pages": n})
     if index != torch.cuda.current_device():
         return _on_other_device(jgdpa_cache_append, k_cache.device, (k_new, v_new, slots, k_cache, v_cache, stream, lib), {})
     rc = lib.jgdpa_cache_append(k_new.data_ptr(), v_new.data_ptr(), ks, vs, slots.data_ptr(), rows, k_cache.data_ptr(),
@@ -637,6 +651,7 @@ def jgdpa_cache_append(k_new, v_new, slots, k_cache, v_cache, stream=None, lib=N
 
 
 def jgdpa_cache_fwd_workspace_bytes(heads: int, kv_heads: int, head_dim: int, max_q: int, lib=None) -> int:
+    _refuse_wide(heads=heads, kv_heads=kv_heads, head_dim=head_dim, max_q=max_q)
     return int((lib or load()).jgdpa_cache_fwd_workspace_bytes(heads, kv_heads, head_dim, max_q))
 
 
@@ -675,6 +690,9 @@ def jgdpa_cache_fwd(q, k_cache, v_cache, block_table, q_offsets, kv_lens, act, s
     act == 'softmax'.  max_q: an upper bound of the new tokens per request."""
     lib = lib or load()
     a = _act(act)
+    max_q, window = int(max_q), int(window)
+    if max(max_q, window) > _I32_MAX or min(max_q, window) < -_I32_MAX:
+        _refuse_wide(max_q=max_q, window=window)
     softmax = a == 2
     qs = kps = vps = 0
     bias = mask = depth = None
@@ -712,7 +730,8 @@ def jgdpa_cache_fwd(q, k_cache, v_cache, block_table, q_offsets, kv_lens, act, s
         _refuse_fwd(q, k_cache, v_cache, block_table, q_offsets, kv_lens, softmax, bias_table, tree_mask, depths, out, lse,
                     workspace)
         raise ValueError("jgdpa_cache_fwd: unusable tensors")
-    max_q, window = int(max_q), int(window)
+    if max(n, width, bias_len) > _I32_MAX:
+        _refuse_wide(**{"k_cache's pages": n, "block_table's width": width, "bias_table's length": bias_len})
     if index != torch.cuda.current_device():
         return _on_other_device(jgdpa_cache_fwd, k_cache.device, (q, k_cache, v_cache, block_table, q_offsets, kv_lens, act,
                                 scale, max_q, bias_table, window, tree_mask, depths, out, lse, workspace, stream, lib), {})

@@ -175,3 +175,22 @@ def test_biases_of_the_largest_finite_size(jg, d, kv_heads, new, group, value): 
     tol = tol + U * (np.abs(want) + tol)
     assert np.all(np.abs(got - want) <= tol)
     assert np.all(np.abs(lse.double().cpu().numpy() / want_lse - 1) <= 2.0 ** -22)
+
+
+# ------------------------------------------------------------ refusals and reports
+@pytest.mark.parametrize("field,value", [("max_q", 2 ** 32 + 4), ("window", 2 ** 32 + 5), ("max_q", 2 ** 31), ("window", -2 ** 32)])
+def test_attention_refuses_numbers_beyond_32_bits(jg, field, value):  # noqa: F811
+    """They would reach the library as other numbers."""
+    kw = Case(0, [40, 20], [3, 4], 2, 2, 64, 16).kwargs("cpu")
+    kw[field] = value
+    with pytest.raises(ValueError, match=f"{field} must fit in 32 bits"):
+        jg.jgdpa_cache_fwd(**kw)
+
+
+@pytest.mark.parametrize("field,value", [("page_size", 2 ** 32 + 16), ("total_new", 2 ** 32 + 1), ("total_new", 2 ** 31)])
+def test_plan_refuses_numbers_beyond_32_bits(jg, field, value):  # noqa: F811
+    kw = dict(ctx_lens=i32([1]), new_lens=i32([1]), held_pages=i32([0]), block_table=i32([[0]]), free_pages=i32([0]),
+              free_count=i32([1]), page_size=16, total_new=1)
+    kw[field] = value
+    with pytest.raises(ValueError, match=f"{field} must fit in 32 bits"):
+        jg.jgdpa_cache_plan(**kw)
