@@ -217,14 +217,16 @@ __device__ void cc_consumer(const CacheFwdParams& p, uint8_t* smem, CcShared<MT>
     const bool hides = ACT == 2 && __any_sync(0xffffffffu, far_bias[0] == -INFINITY || far_bias[1] == -INFINITY);
     pos_min = __reduce_min_sync(0xffffffffu, pos_min);
     const int pos_max = __reduce_max_sync(0xffffffffu, max(rows[0].t >= 0 ? rows[0].pos : 0, rows[1].t >= 0 ? rows[1].pos : 0));
-    // Q fragments: rows lane / 4 (+ 8), columns 16 ks + 2 (lane % 4) (+ 8)
+    // Q fragments: rows lane / 4 (+ 8), columns 16 ks + 2 (lane % 4) (+ 8).  By
+    // ordinary loads: Q may be what the call before wrote while this block was
+    // being set up, and so is not constant over the kernel's life.
     uint32_t qa[KS][4];
 #pragma unroll
     for (int ks = 0; ks < KS; ++ks)
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const __nv_bfloat16* src = qrow[e & 1];
-        qa[ks][e] = src != nullptr ? __ldg(reinterpret_cast<const uint32_t*>(src + 16 * ks + 2 * (lane & 3) + ((e & 2) ? 8 : 0))) : 0u;
+        qa[ks][e] = src != nullptr ? *reinterpret_cast<const uint32_t*>(src + 16 * ks + 2 * (lane & 3) + ((e & 2) ? 8 : 0)) : 0u;
       }
     float o[NT][4];
 #pragma unroll

@@ -4,7 +4,7 @@ import numpy as np
 import pytest
 import torch
 
-from tests.test_cache import Case, compare, i32, jg  # noqa: F401  (jg: the fixture)
+from tests.test_cache import Case, compare, i32, jg, sizes  # noqa: F401  (jg: the fixture)
 
 gpu = pytest.mark.gpu
 
@@ -194,3 +194,32 @@ def test_plan_refuses_numbers_beyond_32_bits(jg, field, value):  # noqa: F811
     kw[field] = value
     with pytest.raises(ValueError, match=f"{field} must fit in 32 bits"):
         jg.jgdpa_cache_plan(**kw)
+
+
+# ------------------------------------------------------------ calls that follow one another (GPU)
+@gpu
+@pytest.mark.parametrize("d,new,group", [(32, 2, 2), (64, 3, 4), (128, 1, 8), (128, 40, 2)])
+def test_outputs_as_the_next_queries(jg, d, new, group):  # noqa: F811
+    """Attention calls back to back, each on the rows that the one before wrote,
+    into two buffers in turn."""
+    rng = np.random.default_rng(d)
+    batch = 24
+    c = Case(51, sizes(rng, batch, 900), np.full(batch, new), 2, group, d, 16, "softmax", nan=False)
+    kw = c.kwargs()
+    kw["k_cache"] = kw["k_cache"] * 4  # so that the rows stay apart from one another
+    steps = 30
+
+    def chain(wait):
+        buffers = [kw["q"].clone(), torch.full_like(kw["q"], float("nan"))]
+        torch.cuda.synchronize()
+        for i in range(steps):
+            jg.jgdpa_cache_fwd(**{**kw, "q": buffers[i % 2], "out": buffers[(i + 1) % 2]})
+            if wait:
+                torch.cuda.synchronize()
+        torch.cuda.synchronize()
+        return [b.clone() for b in buffers]
+
+    want = chain(True)
+    for _ in range(10):
+        for a, b in zip(chain(False), want):
+            assert torch.equal(a, b)
