@@ -176,7 +176,7 @@ cudaError_t launch_cache_plan(const CachePlanParams& p, int sms, cudaStream_t st
   // alone (256 requests, 62,000 pages back; 1,024 requests, 271,000 pages back:
   // 10.8 against 17.2), and nothing more where none come back (1,024 requests:
   // 6.2).  Four CTAs per SM for them: 9.3, but 7.8 where none come back.
-  const int64_t tokens = (std::max(p.total, p.batch) + kPlanThreads - 1) / kPlanThreads;
+  const int64_t tokens = (static_cast<int64_t>(std::max(p.total, p.batch)) + kPlanThreads - 1) / kPlanThreads;
   const int64_t pages = (std::min<int64_t>(static_cast<int64_t>(p.batch) * p.width, p.pool) + kPlanThreads - 1) / kPlanThreads;
   const int64_t ctas = std::max<int64_t>({1, std::min<int64_t>(tokens, 4 * sms), std::min<int64_t>(pages, sms)});
   cache_plan_kernel<<<static_cast<unsigned>(ctas), kPlanThreads, smem, stream>>>(p);
