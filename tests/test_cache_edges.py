@@ -1,4 +1,5 @@
-"""The paged key/value cache at its edges."""
+"""The paged key/value cache at its edges: scores far below zero, keys hidden by
+the bias, contexts cut between CTAs, and what the calls refuse or report."""
 
 import numpy as np
 import pytest
@@ -17,6 +18,21 @@ def status_of(jg, case, **kw):  # noqa: F811
                      dtype=torch.uint8, device="cuda")
     out, lse = jg.jgdpa_cache_fwd(**kw, workspace=ws)
     return out, lse, jg.jgdpa_read_device_status(ws)
+
+
+def seen(case, b):
+    """Which of its tokens the new tokens of request b see, [new, length]."""
+    lo, n, length = int(case.off[b]), int(case.new[b]), int(case.kv[b])
+    ctx = length - n
+    depth = np.arange(n) if case.depth is None else np.asarray(case.depth[lo:lo + n])
+    sees = np.ones((n, length), bool)
+    for t in range(n):
+        for u in range(n):
+            sees[t, ctx + u] = u <= t if case.mask is None else bool((int(case.mask[lo + t][u // 32]) >> (u % 32)) & 1)
+    if case.window:
+        pos = np.concatenate([np.arange(ctx), ctx + depth])
+        sees &= np.abs((ctx + depth)[:, None] - pos) < case.window
+    return sees
 
 
 # ------------------------------------------------------------ small weights (GPU)
@@ -66,9 +82,7 @@ def test_one_weight(jg, act, lo, d, kv_heads, group):  # noqa: F811
     assert not out[0, -2:].any()
 
 
-# ------------------------------------------------------------ refusals and reports
-
-
+# ------------------------------------------------------------ reports (GPU)
 @gpu
 @pytest.mark.parametrize("act", ["gelu", "softmax"])
 @pytest.mark.parametrize("d,kv_heads", [(32, 4), (64, 2), (128, 1)])
@@ -177,7 +191,7 @@ def test_biases_of_the_largest_finite_size(jg, d, kv_heads, new, group, value): 
     assert np.all(np.abs(lse.double().cpu().numpy() / want_lse - 1) <= 2.0 ** -22)
 
 
-# ------------------------------------------------------------ refusals and reports
+# ------------------------------------------------------------ refusals (CPU)
 @pytest.mark.parametrize("field,value", [("max_q", 2 ** 32 + 4), ("window", 2 ** 32 + 5), ("max_q", 2 ** 31), ("window", -2 ** 32)])
 def test_attention_refuses_numbers_beyond_32_bits(jg, field, value):  # noqa: F811
     """They would reach the library as other numbers."""
@@ -223,3 +237,159 @@ def test_outputs_as_the_next_queries(jg, d, new, group):  # noqa: F811
     for _ in range(10):
         for a, b in zip(chain(False), want):
             assert torch.equal(a, b)
+
+
+# ------------------------------------------------------------ nothing is lost (GPU)
+@gpu
+@pytest.mark.parametrize("act", ["gelu", "softmax"])
+@pytest.mark.parametrize("d,kv_heads,new,group,length", [(32, 1, 16, 1, 6000), (32, 4, 4, 4, 6000), (64, 1, 3, 5, 20000),
+                                                         (64, 1, 8, 4, 9000), (64, 2, 4, 4, 9000), (128, 1, 4, 4, 20000),
+                                                         (32, 1, 40, 2, 6000), (64, 1, 64, 2, 9000), (128, 1, 25, 5, 6000),
+                                                         (64, 1, 50, 5, 9000), (128, 1, 64, 8, 6000)])
+def test_every_block_of_a_long_context_counts(jg, act, d, kv_heads, new, group, length):  # noqa: F811
+    """Each query row looks for one key, which takes (nearly) all the weight; over
+    the calls, one key in each 16 of a long context that is cut between CTAs.
+    Keys are +-1, so a row's own key scores c d (c = 64 / d a unit of scale), any
+    other a sum of d random signs.  The reference is in 64 bits; the bound, the
+    usual roundings (see `compare` in test_cache.py), is a few hundredths of the
+    weight that a lost key would take away."""
+    rng = np.random.default_rng(length + d)
+    page, heads = 64, kv_heads * group
+    c = Case(2, [length - new, 40], [new, 1], kv_heads, group, d, page, act, nan=False)
+    kw = c.kwargs()
+    sign = torch.from_numpy(rng.choice([-1.0, 1.0], size=tuple(kw["k_cache"].shape))).to(torch.bfloat16).cuda()
+    kw["k_cache"] = sign
+    kw["scale"] = 64.0 / d
+    if act == "gelu":
+        kw["bias_table"] = torch.full((heads, 3), -60.0, device="cuda")  # the own key scores 4, another at most 0 (d = 32)
+    ids = torch.from_numpy(c.table[0, :-(-length // page)]).cuda().long()
+    k, v = (kw[x][ids].flatten(0, 1)[:length].double() for x in ("k_cache", "v_cache"))
+    blocks = -(-(length - new) // 16)
+    rows = new * group
+    for first in range(0, blocks, rows):
+        block = torch.arange(first, first + rows) % blocks
+        target = torch.minimum(block * 16 + torch.from_numpy(rng.integers(0, 16, rows)), torch.tensor(length - new - 1))
+        target = target.view(new, group).cuda()
+        q = kw["q"].clone()
+        for h in range(kv_heads):
+            q[:new, h * group:(h + 1) * group] = k[target.view(-1), h].view(new, group, d).to(torch.bfloat16)
+        out, lse = jg.jgdpa_cache_fwd(**{**kw, "q": q})
+        ahead = torch.arange(length, device="cuda")[None] > length - new + torch.arange(new, device="cuda")[:, None]
+        for h in range(heads):
+            x = q[:new, h].double() @ k[:, h // group].t() * kw["scale"]
+            if act == "gelu":
+                x = x - 60.0
+                p = (0.5 * x * torch.erfc(-x * 0.5 ** 0.5)).masked_fill(ahead, 0.0)
+            else:
+                p = torch.softmax(x.masked_fill(ahead, -torch.inf), 1)
+            own = p.gather(1, target[:, h % group, None])
+            assert torch.all(own > (0.9 if act == "softmax" else 3.5))
+            want, size = p @ v[:, h // group], p.abs() @ v[:, h // group].abs()
+            # scores are exact (sums of d signs times a power of two, less 60); the device's act: 2^-8
+            tol = size * (2 * U + 2.0 ** -12)
+            tol = tol + U * (want.abs() + tol)
+            got = out[:new, h].double()
+            assert torch.all((got - want).abs() <= tol), (first, h)
+            # the row without its key would be out of the bound in most columns
+            without = want - own * v[target[:, h % group], h // group]
+            assert torch.all(((without - want).abs() > tol).double().mean(1) > 0.8)
+
+
+@gpu
+@pytest.mark.parametrize("act", ["gelu", "softmax"])
+@pytest.mark.parametrize("d,kv_heads,new,group", [(32, 4, 4, 2), (64, 2, 8, 4), (128, 1, 4, 4), (32, 1, 40, 1), (64, 1, 30, 3),
+                                                  (128, 1, 24, 3), (64, 1, 50, 5), (128, 2, 60, 4)])
+@pytest.mark.parametrize("window", [0, 3000])
+def test_infinities_in_requests_cut_between_ctas(jg, act, d, kv_heads, new, group, window):  # noqa: F811
+    """NaN and infinities in V of drafted tokens and of context tokens at the
+    window's edge, of a request whose keys many CTAs share: the rows that see
+    them are not finite in that column, and the others keep their bits."""
+    c = Case(43, [5000, 40], [new, new], kv_heads, group, d, 16, act, window=window, mask=True, nan=False)
+    kw = c.kwargs()
+    clean, clean_lse = jg.jgdpa_cache_fwd(**kw)
+    assert torch.isfinite(clean).all()
+    sees = seen(c, 0)
+    keys = [5000, 5000 + new // 2, 5000 + new - 1] + ([5000 - window + 1, 5000 - window + 2] if window else [])
+    for i, j in enumerate(keys):
+        head, col = i % kv_heads, (7 * i + 3) % d
+        v = kw["v_cache"].clone()
+        v[int(c.table[0, j // 16]), j % 16, head, col] = (float("inf"), float("nan"), -float("inf"))[i % 3]
+        out, lse = jg.jgdpa_cache_fwd(**{**kw, "v_cache": v})
+        rows = torch.from_numpy(np.nonzero(sees[:, j])[0]).cuda()
+        same = torch.ones_like(out, dtype=torch.bool)
+        for h in range(head * group, (head + 1) * group):
+            same[rows, h, col] = False
+            assert not torch.isfinite(out[rows, h, col]).any()
+        assert torch.equal(out[same], clean[same])
+        assert lse is None or torch.equal(lse, clean_lse)
+
+
+@gpu
+@pytest.mark.parametrize("act", ["silu", "softmax"])
+@pytest.mark.parametrize("d,new,group", [(32, 40, 1), (64, 12, 4), (128, 10, 4), (128, 40, 5)])
+def test_infinities_in_many_requests_per_cta(jg, act, d, new, group):  # noqa: F811
+    """Requests by the thousand, so that each CTA walks far more than 16 parts,
+    some of which hold infinities in V of a drafted token."""
+    rng = np.random.default_rng(d + new)
+    kinds = 6
+    c = Case(47, rng.integers(1, 300, kinds), np.full(kinds, new), 2, group, d, 16, act, mask=True, nan=False)
+    kw = c.kwargs()
+    order = np.concatenate([np.arange(kinds)] * 2 + [rng.integers(0, kinds, 3000)])
+    rows = torch.from_numpy(np.concatenate([np.arange(c.off[b], c.off[b + 1]) for b in order])).cuda()
+    many = {**kw, "q_offsets": i32(np.arange(len(order) + 1) * new, "cuda"), "kv_lens": i32(c.kv[order], "cuda"),
+            "block_table": kw["block_table"][torch.from_numpy(order).cuda()].contiguous()}
+    for k in ("q", "tree_mask", "depths"):
+        many[k] = kw[k][rows].contiguous()
+    v = kw["v_cache"].clone()
+    odd = torch.zeros(c.q.shape[0], c.heads, d, dtype=torch.bool, device="cuda")
+    for b, u in ((1, 0), (4, new // 2)):
+        j = int(c.kv[b]) - new + u
+        v[int(c.table[b, j // 16]), j % 16, 1, 5] = float("inf")
+        hit = torch.from_numpy(np.nonzero(seen(c, b)[:, j])[0]).cuda() + int(c.off[b])
+        for h in range(group, 2 * group):
+            odd[hit, h, 5] = True
+    clean = jg.jgdpa_cache_fwd(**many)[0]
+    out = jg.jgdpa_cache_fwd(**{**many, "v_cache": v})[0]
+    assert torch.isfinite(clean).all()
+    odd = odd[rows]
+    assert not torch.isfinite(out[odd]).any()
+    assert torch.equal(out[~odd], clean[~odd])
+
+
+# ------------------------------------------------------------ waits, and plans of nothing (GPU)
+@gpu
+@pytest.mark.parametrize("d,new,group,act", [(128, 1, 4, "softmax"), (64, 1, 1, "softmax"), (32, 1, 2, "gelu"),
+                                             (128, 30, 2, "gelu"), (64, 60, 8, "softmax"), (32, 40, 1, "silu")])
+def test_waits_that_run_out_are_reported(jg, d, new, group, act):  # noqa: F811
+    """Under a limit of 1 ns the waits of a batch that keeps every SM waiting for
+    its loads run out, in the kernel for few rows and in the 128-row one, and
+    the next call is as before.  (A wait looks at its clock only after a
+    suspended test returns, so that a single call may end without noticing.)"""
+    rng = np.random.default_rng(d)
+    batch, pages, kv_heads = 64, 96, 4
+    c = Case(3, [1], [1], kv_heads, group, d, 64, act, nan=False)
+    g = torch.Generator("cuda").manual_seed(d)
+    k, v = (torch.randn(batch * pages, 64, kv_heads, d, generator=g, device="cuda").to(torch.bfloat16) for _ in range(2))
+    kw = dict(q=torch.randn(batch * new, c.heads, d, generator=g, device="cuda").to(torch.bfloat16), k_cache=k, v_cache=v,
+              block_table=i32(rng.permutation(batch * pages).reshape(batch, pages), "cuda"),
+              q_offsets=i32(np.arange(batch + 1) * new, "cuda"), kv_lens=i32(np.full(batch, pages * 64), "cuda"), act=act,
+              scale=c.scale, max_q=new)
+    good, _, status = status_of(jg, c, **kw)
+    assert status == 0
+    jg.jgdpa_set_wait_limit_ns(1)
+    try:
+        reports = {status_of(jg, c, **kw)[2] for _ in range(20)}
+    finally:
+        jg.jgdpa_set_wait_limit_ns(0)
+    assert 7 in reports and reports <= {0, 7}
+    out, _, status = status_of(jg, c, **kw)
+    assert status == 0 and torch.equal(out, good)
+
+
+@gpu
+def test_plan_of_no_requests(jg):  # noqa: F811
+    """Every row of slots is one behind the last token; the pool stays as it is."""
+    free, none = i32([3, 1, -1], "cuda"), i32([], "cuda")
+    slots, off, kv, held, count = jg.jgdpa_cache_plan(none, none, none, i32(np.zeros((0, 4)), "cuda"), free, i32([2], "cuda"), 16, 5)
+    assert slots.tolist() == [-1] * 5 and off.tolist() == [0] and count.tolist() == [2] and free.tolist() == [3, 1, -1]
+    assert kv.numel() == 0 and held.numel() == 0
