@@ -101,7 +101,6 @@ struct CacheFwdParams {
   int32_t batch, max_q, heads, kv_heads, group;
   int32_t page_shift, width, num_pages;
   int32_t mask_words, bias_len, window;
-  int32_t bias_hides;        // softmax with a bias table, whose entries of -inf hide keys
   int32_t rows_per_tile;     // query rows (token, head of the group) of one item
   int32_t tile_tokens;       // tokens of a 128-row tile (128-row kernel; 0 otherwise)
   int32_t heads_per_item;    // key/value heads of one item
@@ -424,19 +423,21 @@ template <int ACT>
 __device__ __forceinline__ float cc_act(float x) { return cc_act2<ACT>(f2(0.5f * x)).x; }
 
 // A bias table's entry in the units of the scores, log2 units for softmax.
-// Finite entries that leave fp32 there (the type's lowest value as a mask) stay
-// finite: where nothing else is seen, their keys weigh the same.
-constexpr float kFltMax = 3.402823466e38f;
 template <int ACT>
-__device__ __forceinline__ float cc_bias_in_units(float b) {
-  if constexpr (ACT != 2) return b;
-  const float x = b * kLog2e, a = fabsf(b);
-  return a > 2.358e38f && a <= kFltMax ? copysignf(kFltMax, b) : x;  // (2.358e38 log2 e is still finite)
+__device__ __forceinline__ float cc_bias_unit() { return ACT == 2 ? kLog2e : 1.0f; }
+// Of a softmax bias, -inf hides its key as a mask would (an infinity or NaN there
+// as well), and a finite entry that would leave fp32 in log2 units (the type's
+// lowest value as a mask) counts as the largest that does not: where nothing else
+// is seen, such keys weigh the same.  Both are rare: the kernels look for entries
+// beyond kHugeBias and put things right afterwards, if there are any.
+constexpr float kHugeBias = 2.358e38f, kHugeScore = kHugeBias * kLog2e;
+__device__ __forceinline__ float cc_huge(float b) {  // in log2 units
+  return fabsf(b) > kHugeBias ? copysignf(kHugeScore, b) : b * kLog2e;
 }
 // The LSE of a row from its maximum (log2 units) and sum.
 __device__ __forceinline__ float cc_lse(float m, float l) {
   if (l == 0.f) return -INFINITY;
-  return fabsf(m) == kFltMax ? m : (m + log2f(l)) * kLn2;  // (such a bias is its row's LSE)
+  return fabsf(m) == kHugeScore ? copysignf(3.402823466e38f, m) : (m + log2f(l)) * kLn2;
 }
 
 // The halves of a packed bf16 pair that are infinite or NaN, as a mask.

@@ -349,7 +349,6 @@ jgdpa_status jgdpa_cache_fwd(const void* q, int64_t q_stride, const void* k_cach
   p.num_pages = num_pages;
   p.mask_words = mask_words;
   p.bias_len = bias_len;
-  p.bias_hides = act == JGDPA_ACT_SOFTMAX && bias_len > 0;
   p.window = window;
   p.rows_per_tile = L.rows;
   p.tile_tokens = L.tokens;

@@ -177,9 +177,9 @@ __device__ void cc_consumer(const CacheFwdParams& p, uint8_t* smem, CcShared<MT>
   const uint32_t step1 = 16 * (pr >= 32 ? row_bytes : 2 * W), step2 = 32 * (pr >= 64 ? row_bytes : 2 * W);
   auto block = [&](int kb) { return (kb & 1) * step1 + (kb >> 1) * step2; };
   const int reach = (p.bias_len - 1) / 2;
-  // (GELU and SiLU scores are halved, as cc_act2 takes them)
-  constexpr float kHalf = ACT == 2 ? 1.f : 0.5f;
-  const float scale = kHalf * p.scale;
+  // scores in log2 units, or halved as cc_act2 takes them
+  constexpr float kUnit = ACT == 2 ? kLog2e : 0.5f;
+  const float scale = ACT == 2 ? p.scale : 0.5f * p.scale;
   uint32_t it = 0;
   bool dead = false;
   CacheWalk w;
@@ -211,10 +211,10 @@ __device__ void cc_consumer(const CacheFwdParams& p, uint8_t* smem, CcShared<MT>
       }
       far_bias[i] = 0.f;
       if (q.t >= 0 && p.bias_len)
-        far_bias[i] = kHalf * cc_bias_in_units<ACT>(__ldg(p.bias + static_cast<int64_t>(q.head) * p.bias_len + 2 * reach));
+        far_bias[i] = __ldg(p.bias + static_cast<int64_t>(q.head) * p.bias_len + 2 * reach) * kUnit;
     }
-    // a softmax bias of -inf hides keys as the mask does; some row's for all far ones
-    const bool hides = ACT == 2 && __any_sync(0xffffffffu, far_bias[0] == -INFINITY || far_bias[1] == -INFINITY);
+    // some row's bias hides all far keys, or is beyond what log2 units hold
+    const bool hides = ACT == 2 && __any_sync(0xffffffffu, fabsf(far_bias[0]) > kHugeScore || fabsf(far_bias[1]) > kHugeScore);
     pos_min = __reduce_min_sync(0xffffffffu, pos_min);
     const int pos_max = __reduce_max_sync(0xffffffffu, max(rows[0].t >= 0 ? rows[0].pos : 0, rows[1].t >= 0 ? rows[1].pos : 0));
     // Q fragments: rows lane / 4 (+ 8), columns 16 ks + 2 (lane % 4) (+ 8).  By
@@ -243,17 +243,11 @@ __device__ void cc_consumer(const CacheFwdParams& p, uint8_t* smem, CcShared<MT>
       if (!dead && key0 < r.L) {
         const uint32_t kt = base + st * 2 * C::kTileBytes, vt = kt + C::kTileBytes;
         // plain: every key of the warp's is seen by every row; far: R or more behind
-        // (of nearer ones only the bias table's entries say which are hidden)
         const int last = key0 + 16 * KB - 1;
-        const bool far = p.bias_len == 0 || (last < r.C && pos_min - last >= reach);
-        const bool plain = last < r.C && (p.window <= 0 || pos_max - key0 < p.window) && (ACT != 2 || (far && !hides));
+        const bool far = p.bias_len == 0 || (!hides && last < r.C && pos_min - last >= reach);
+        bool plain = last < r.C && (p.window <= 0 || pos_max - key0 < p.window);
         uint32_t see[(KB + 1) / 2][2];  // by 32 keys
-        bool odd = false;
         if (!plain) {
-          // Some rows do not see some of these keys, and 0 * NaN = NaN: rows of
-          // V past the request's end (whatever the page held) count as zeros,
-          // and where others hold an infinity or NaN (`odd`) those are left out
-          // of the product and added to the rows that see them.
 #pragma unroll
           for (int j = 0; j < (KB + 1) / 2; ++j)
 #pragma unroll
@@ -272,21 +266,8 @@ __device__ void cc_consumer(const CacheFwdParams& p, uint8_t* smem, CcShared<MT>
                 }
                 bits &= near;  // (only this lane's columns are kept)
               }
-              if (ACT == 2 && far && far_bias[h] == -INFINITY) bits = 0;
               see[j][h] = bits;
             }
-          const __nv_bfloat162 zero = __float2bfloat162_rn(0.f);
-          __nv_bfloat162 sum = zero;  // of 0 * v
-#pragma unroll 1
-          for (int k = lane & 15; k < 16 * KB && key0 + k < r.L; k += 16)
-#pragma unroll 1
-            for (int c = lane >> 4; c < D / 8; c += 2) {
-              uint32_t x[4];
-              ld_shared_v4(vt + cc_offset<W>(first + k, hw * (D / 8) + c, pr), x[0], x[1], x[2], x[3]);
-#pragma unroll
-              for (int e = 0; e < 4; ++e) sum = __hfma2(*reinterpret_cast<__nv_bfloat162*>(&x[e]), zero, sum);
-            }
-          odd = __any_sync(0xffffffffu, !(__low2float(sum) == 0.f && __high2float(sum) == 0.f));
         }
         float s[KB][2][4];
 #pragma unroll
@@ -312,6 +293,7 @@ __device__ void cc_consumer(const CacheFwdParams& p, uint8_t* smem, CcShared<MT>
 #pragma unroll
               for (int e = 0; e < 4; ++e) s[kb][i][e] = __fmaf_rn(s[kb][i][e], scale, far_bias[e >> 1]);
         } else {
+          float top = 0.f;
 #pragma unroll
           for (int kb = 0; kb < KB; ++kb)
 #pragma unroll
@@ -321,14 +303,47 @@ __device__ void cc_consumer(const CacheFwdParams& p, uint8_t* smem, CcShared<MT>
                 const int key_pos = cc_pos(p, r, key0 + 16 * kb + 8 * i + 2 * (lane & 3) + c);
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                  const float bias = kHalf * cc_bias_in_units<ACT>(cc_bias(p, rows[h], reach, key_pos));
-                  s[kb][i][2 * h + c] = __fmaf_rn(s[kb][i][2 * h + c], scale, bias);
-                  if (ACT == 2 && bias == -INFINITY)
-                    see[kb >> 1][h] &= ~(1u << (16 * (kb & 1) + 8 * i + 2 * (lane & 3) + c));
+                  const float bias = cc_bias(p, rows[h], reach, key_pos);
+                  s[kb][i][2 * h + c] = __fmaf_rn(s[kb][i][2 * h + c], scale, bias * kUnit);
+                  if constexpr (ACT == 2) top = fmaxf(top, fabsf(bias));
                 }
               }
+          if (ACT == 2 && __any_sync(0xffffffffu, top > kHugeBias)) {
+            if (plain) {
+#pragma unroll
+              for (int j = 0; j < (KB + 1) / 2; ++j) see[j][0] = see[j][1] = 0xFFFFFFFFu;
+              plain = false;
+            }
+#pragma unroll
+            for (int kb = 0; kb < KB; ++kb)
+#pragma unroll
+              for (int e = 0; e < 8; ++e) {
+                const int i = e >> 2, h = (e >> 1) & 1, col = 16 * (kb & 1) + 8 * i + 2 * (lane & 3) + (e & 1);
+                const float bias = cc_bias(p, rows[h], reach, cc_pos(p, r, key0 + 32 * (kb >> 1) + col));
+                float& x = s[kb][i][e & 3];
+                if (bias == -INFINITY) see[kb >> 1][h] &= ~(1u << col);
+                else if (fabsf(bias) > kHugeBias && x == x) x = cc_huge(bias);
+              }
+          }
         }
+        bool odd = false;
         if (!plain) {
+          // Some rows do not see some of these keys, and 0 * NaN = NaN: rows of
+          // V past the request's end (whatever the page held) count as zeros,
+          // and where others hold an infinity or NaN (`odd`) those are left out
+          // of the product and added to the rows that see them.
+          const __nv_bfloat162 zero = __float2bfloat162_rn(0.f);
+          __nv_bfloat162 sum = zero;  // of 0 * v
+#pragma unroll 1
+          for (int k = lane & 15; k < 16 * KB && key0 + k < r.L; k += 16)
+#pragma unroll 1
+            for (int c = lane >> 4; c < D / 8; c += 2) {
+              uint32_t x[4];
+              ld_shared_v4(vt + cc_offset<W>(first + k, hw * (D / 8) + c, pr), x[0], x[1], x[2], x[3]);
+#pragma unroll
+              for (int e = 0; e < 4; ++e) sum = __hfma2(*reinterpret_cast<__nv_bfloat162*>(&x[e]), zero, sum);
+            }
+          odd = __any_sync(0xffffffffu, !(__low2float(sum) == 0.f && __high2float(sum) == 0.f));
 #pragma unroll
           for (int kb = 0; kb < KB; ++kb)
 #pragma unroll

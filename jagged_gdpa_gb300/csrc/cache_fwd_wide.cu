@@ -83,6 +83,7 @@ struct CwShared {
   CacheRangeShared range;
   uint32_t tmem_base;
   int abort;
+  int hides;         // softmax with a bias table: 1, or 2 where an entry of -inf hides all far keys of some head
   int odd[16];       // number of the last part (mod 16) whose masked tiles hold a V that is not finite
   float2 ml[kTile];  // the streams' maxima and sums at the end of a part that they share
 };
@@ -99,7 +100,7 @@ struct CwPart {
 
   __device__ __forceinline__ CwPart() {}
   // (whole warp)
-  __device__ __forceinline__ CwPart(const CacheFwdParams& p, const CacheWalk& w) {
+  __device__ __forceinline__ CwPart(const CacheFwdParams& p, const CacheWalk& w, int hides) {
     int hi;
     w.tiles<kTile>(p, lo, hi);
     n = hi - lo;
@@ -122,12 +123,8 @@ struct CwPart {
     }
     const int reach = max((p.bias_len - 1) / 2, 1);
     far_hi = p.bias_len == 0 ? INT32_MAX : (C >= reach ? (C - reach + 1) / kTile : 0);
-    if (p.bias_hides) {  // -inf as the bias of some row's far keys; of nearer ones only the table's entries say
-      bool hides = false;
-      for (int g = threadIdx.x & 31; g < p.group; g += 32)
-        hides = hides || __ldg(p.bias + static_cast<int64_t>(w.h * p.group + g + 1) * p.bias_len - 1) == -INFINITY;
-      plain_hi = __any_sync(0xffffffffu, hides) ? 0 : min(plain_hi, far_hi);
-    }
+    // (a softmax bias may hide near keys: only the table's entries say which)
+    if (hides > 0) plain_hi = hides > 1 ? 0 : min(plain_hi, far_hi);
   }
   __device__ __forceinline__ bool plain(int tile) const { return tile >= plain_lo && tile < plain_hi; }
   // The tiles of stream s, and the one it takes as its i-th.
@@ -223,7 +220,7 @@ __device__ void cw_producer(const CacheFwdParams& p, uint8_t* smem, CwShared* sh
   CacheWalk w;
   w.init(R);
   for (; ok && w.next<kTile>(p); w.advance()) {
-    const CwPart part(p, w);
+    const CwPart part(p, w, sh->hides);
     if (part.n == 0) continue;
     ok = load.query(w, part.first_token);
     if (PAIR && part.pair && ok) ok = load.query(w, part.first_token + p.tile_tokens);
@@ -315,7 +312,7 @@ __device__ void cw_mma(const CacheFwdParams& p, uint8_t* smem, CwShared* sh, uin
   CacheWalk w;
   w.init(R);
   for (; ok && w.next<kTile>(p); w.advance()) {
-    const CwPart part(p, w);
+    const CwPart part(p, w, sh->hides);
     if (part.n == 0) continue;
     const bool pair = PAIR && part.pair;
     const int slot[2] = {static_cast<int>(q_n % C::kSlots), static_cast<int>(pair ? (q_n + 1) % C::kSlots : q_n % C::kSlots)};
@@ -387,49 +384,68 @@ static __device__ __noinline__ CwNear cw_near(const CacheFwdParams& p, CacheReq 
   return t;
 }
 
+// 32 scores of a row, formed with biases of which some are beyond kHugeBias, put
+// right in place (`see`: the keys that length, mask and window let it see).
+static __device__ __noinline__ void cw_huge_biases(const float* bias_row, int reach, int row_pos, int pos, uint32_t see,
+                                                   uint32_t t_s) {
+  uint32_t v[32];
+  tmem_st_wait();
+  tmem_ld32(t_s, v);
+  tmem_ld_wait(v);
+#pragma unroll
+  for (int c = 0; c < 32; ++c) {
+    const float b = __ldg(bias_row + min(max(row_pos - __shfl_sync(0xffffffffu, pos, c), -reach), reach));
+    const float x = __uint_as_float(v[c]);
+    if (((see >> c) & 1) && fabsf(b) > kHugeBias && (b == -INFINITY || x == x))
+      v[c] = b == -INFINITY ? 0xFF800000u : __float_as_uint(cc_huge(b));
+  }
+  tmem_st32(t_s, v);
+}
+
 // S -> s S + bias (in log2 units for softmax) in place, for the tiles near the
 // new tokens, where the bias varies from key to key or some rows do not see
-// some keys (-inf for softmax, else 0, as act(0) = 0), those that a softmax
-// bias of -inf hides among them.
+// some keys (-inf for softmax, else 0, as act(0) = 0).
 template <int ACT>
 __device__ __noinline__ void cw_near_tile(const CacheFwdParams& p, int C, CcRow q, CwNear t, int key0, uint32_t t_s) {
   const int reach = (p.bias_len - 1) / 2;
   const float* bias_row = p.bias + static_cast<int64_t>(q.head) * p.bias_len + reach;
+  const bool huge = ACT == 2 && __any_sync(0xffffffffu, fabsf(q.far_bias) > kHugeScore);
 #pragma unroll 1
   for (int c0 = 0; c0 < kTile; c0 += 32) {
     uint32_t v[32];
     tmem_ld32(t_s + c0, v);
     // keys R or more behind every new token: one bias for all
-    const bool far = p.bias_len == 0 || key0 + c0 + 31 <= C - max(reach, 1);
+    const bool far = p.bias_len == 0 || (!huge && key0 + c0 + 31 <= C - max(reach, 1));
+    float top = 0.f;
     if (far) {
       tmem_ld_wait(v);
 #pragma unroll
       for (int c = 0; c < 32; ++c) v[c] = __float_as_uint(__fmaf_rn(__uint_as_float(v[c]), p.scale, q.far_bias));
-      if (ACT == 2 && q.far_bias == -INFINITY) t.see[0] = 0;
     } else {
       float bias[32];
 #pragma unroll
       for (int c = 0; c < 32; ++c)
-        bias[c] = cc_bias_in_units<ACT>(__ldg(bias_row + min(max(q.pos - __shfl_sync(0xffffffffu, t.pos[0], c), -reach), reach)));
+        bias[c] = __ldg(bias_row + min(max(q.pos - __shfl_sync(0xffffffffu, t.pos[0], c), -reach), reach));
       tmem_ld_wait(v);
 #pragma unroll
       for (int c = 0; c < 32; ++c)
-        v[c] = __float_as_uint(__fmaf_rn(__uint_as_float(v[c]), p.scale, bias[c]));
+        v[c] = __float_as_uint(__fmaf_rn(__uint_as_float(v[c]), p.scale, bias[c] * cc_bias_unit<ACT>()));
       if constexpr (ACT == 2) {
 #pragma unroll
-        for (int c = 0; c < 32; ++c)
-          if (bias[c] == -INFINITY) t.see[0] &= ~(1u << c);
+        for (int c = 0; c < 32; ++c) top = fmaxf(top, fabsf(bias[c]));
       }
     }
 #pragma unroll
     for (int c = 0; c < 32; ++c)
       if (!((t.see[0] >> c) & 1)) v[c] = ACT == 2 ? 0xFF800000u : 0u;
+    tmem_st32(t_s + c0, v);
+    if (ACT == 2 && __any_sync(0xffffffffu, top > kHugeBias))
+      cw_huge_biases(bias_row, reach, q.pos, t.pos[0], t.see[0], t_s + c0);
 #pragma unroll
     for (int k = 0; k < 3; ++k) {  // the next chunk's words come to the front
       t.see[k] = t.see[k + 1];
       t.pos[k] = t.pos[k + 1];
     }
-    tmem_st32(t_s + c0, v);
   }
   tmem_st_wait();
 }
@@ -565,7 +581,7 @@ __device__ __noinline__ void cw_add_odd(const CacheFwdParams& p, CacheWalk w, Cw
       if (static_cast<uint32_t>(page) >= static_cast<uint32_t>(p.num_pages)) continue;
       const int key_pos = cc_pos(p, r, key);
       if (!(cc_vis32(p, r, q, key) & 1) || !cc_near(p, q.pos, key_pos)) continue;
-      if (p.bias_hides && cc_bias(p, q, (p.bias_len - 1) / 2, key_pos) == -INFINITY) continue;
+      if (ACT == 2 && p.bias_len && cc_bias(p, q, (p.bias_len - 1) / 2, key_pos) == -INFINITY) continue;
       const int64_t place = static_cast<int64_t>(key & ((1 << p.page_shift) - 1)) * p.kv_heads * D + w.h * D;
       const __nv_bfloat16* v = p.v_cache + page * p.v_page_stride + place;
       bool any = false;
@@ -606,7 +622,7 @@ __device__ void cw_fixer(const CacheFwdParams& p, uint8_t* smem, CwShared* sh, c
   CacheWalk w;
   w.init(R);
   for (; w.next<kTile>(p); w.advance()) {
-    const CwPart part(p, w);
+    const CwPart part(p, w, sh->hides);
     if (part.n == 0) continue;
     ++number;
     for (int t = part.lo; t < part.lo + part.n; ++t, ++it) {
@@ -692,7 +708,7 @@ __device__ void cw_consumer(const CacheFwdParams& p, CwShared* sh, uint32_t tmem
   CacheWalk w;
   w.init(R);
   for (; w.next<kTile>(p); w.advance()) {
-    const CwPart part(p, w);
+    CwPart part(p, w, sh->hides);
     const CacheReq& r = w.r;
     if (part.n > 0) ++number;  // (the ring lets no more than 8 later parts be loaded, let alone made safe)
     __syncwarp();
@@ -708,15 +724,15 @@ __device__ void cw_consumer(const CacheFwdParams& p, CwShared* sh, uint32_t tmem
     q.pos = row_ok ? cc_row_pos(p, r, q.t, fail.status) : r.C;
     q.far_bias = 0.f;
     if (row_ok && p.bias_len)
-      q.far_bias = cc_bias_in_units<ACT>(__ldg(p.bias + static_cast<int64_t>(q.head) * p.bias_len + 2 * reach));
+      q.far_bias = __ldg(p.bias + static_cast<int64_t>(q.head) * p.bias_len + 2 * reach) * cc_bias_unit<ACT>();
     const bool warp_live = __any_sync(0xffffffffu, row_ok);
+    // a far bias beside which scores are lost takes the near tiles' way, where it is added to them first
+    if (ACT == 2 && __any_sync(0xffffffffu, fabsf(q.far_bias) > 1e18f)) part.far_hi = 0;
     const int count = part.count(stream);
     float m = -INFINITY, l = 0.f;
     for (int i = 0; i < count; ++i) {
       const int tile = part.lo + part.at(stream, i);
-      // (a bias beside which scores are lost takes the near tiles' way for all keys, where it is added to them first)
-      const bool huge = ACT == 2 && __any_sync(0xffffffffu, fabsf(q.far_bias) > 1e18f);
-      const bool far = tile < part.far_hi && !huge, plain = part.plain(tile);
+      const bool far = tile < part.far_hi, plain = part.plain(tile);
       CwNear near;
       if ((!plain || !far) && warp_live) near = cw_near(p, r, q, plain, tile * kTile);
       if (!dead && !mbar_wait(&sh->s_full[stream], s_n & 1, fail)) dead = true;
@@ -848,9 +864,15 @@ __global__ void __launch_bounds__(kWideThreads, 1) cache_fwd_wide_kernel(const _
   cache_wait_before();
   if (threadIdx.x == 0) p.err[blockIdx.x] = kOk;
   const CacheRange R = cache_range<kTile>(p, &sh->range, kWideMinRange);
+  bool hides = false;
+  if (ACT == 2 && p.bias != nullptr)
+    for (int h = threadIdx.x; h < p.heads; h += kWideThreads)
+      hides = hides || __ldg(p.bias + static_cast<int64_t>(h + 1) * p.bias_len - 1) == -INFINITY;
   tc_fence_before();
-  __syncthreads();
+  hides = __syncthreads_or(hides) != 0;
   tc_fence_after();
+  if (threadIdx.x == 0) sh->hides = ACT != 2 || p.bias == nullptr ? 0 : (hides ? 2 : 1);
+  __syncthreads();
   if (threadIdx.x == 96) cache_open<kTile>(p, R);
   const uint32_t tmem = sh->tmem_base;
   Fail fail{&sh->abort, p.err + blockIdx.x, p.wait_limit_ns};
