@@ -371,7 +371,7 @@ JGDPA_API jgdpa_status jgdpa_cache_append(const void* k_new, const void* v_new, 
  *                [bias_len]; a softmax bias of -inf hides a key
  *   out          bf16 [total_q][heads][head_dim]
  *   lse          fp32 [heads][total_q] in SOFTMAX mode, or NULL; NULL otherwise
- * Every token sees the whole context (within the window).  A token that sees
+ * out and lse must not overlap the inputs.  Every token sees the whole context (within the window).  A token that sees
  * nothing gets O = 0 (LSE = -inf).  Infinities and NaN in the cache reach only
  * the rows that see their token; places of a page behind kv_lens[b] may hold
  * anything.  Same bits on every run, whatever else runs beside it.  Weights are

@@ -21,12 +21,12 @@ constexpr int kCacheMaxBatch = 16384;  // requests per call (the plan's prefix s
 
 // Query rows per key/value head up to which the kernel for few rows
 // (cache_fwd.cu) runs, and the 128-row one (cache_fwd_wide.cu) from there on.
-// At 24 rows, 64 requests of 4,100 tokens, tiles of 32 rows of the former took
-// 264 us against 183 at d = 128, but 140 against 121 at d = 64 and 170 against 208
-// at d = 32; on 256 requests of 100 to 800 tokens 195 against 171, 60 against 87
-// and 127 against 284; on one of 100,000 tokens 105 against 77, 40 against 34 and
-// 75 against 78.  (Lengths are not known to the host; at d = 64 the short ones
-// have more to lose.)
+// At 24 rows, softmax, 64 requests of 4,100 tokens, 32-row tiles of the former took
+// 264 us against 183 at d = 128 (8 key/value heads), but 140 against 114 at d = 64
+// (8) and 169 against 192 at d = 32 (16); on 256 requests of 100 to 800 tokens 100
+// against 177 at d = 64 and 124 against 321 at d = 32; on one of 100,000 tokens 62
+// against 55 and 72 against 80.  (Lengths are not known to the host; at d = 64 the
+// short ones have more to lose.)
 __host__ __device__ constexpr int cache_narrow_rows(int d) { return d < 128 ? 32 : 16; }
 
 // CTAs per SM of the attention kernel for up to 16 mt rows and w columns of K
@@ -149,11 +149,18 @@ __device__ __forceinline__ bool cache_req_ok(const CacheFwdParams& p, const Cach
 // Work division.  The items are (request, kv head, row tile), each a lead of
 // item_cost, what its start and end take, and n key tiles of length u.  Laid end
 // to end (request by request, row tiles of a head next to each other) they form
-// one line that is cut into equal ranges, one per CTA, whatever the lengths.
+// one line that is cut into ranges of equal length, one per CTA.
 // (Without the lead, ranges that fall on many short requests took half as long
 // again as the others.)  A border inside an item cuts it, and the joining kernel
 // puts the parts together; a border that would leave a part of fewer than
 // min_part tiles moves to the item's start or end.
+//
+// n counts the request's key tiles from the first on that any of its new tokens
+// sees under the window.  What one row tile of many does not see of them is not
+// taken off: in a causal prompt the early row tiles skip the later keys (`tiles`
+// below), so that ranges over them end sooner (one prompt of 8,192 tokens: the
+// busiest CTA visits 1.9 times the mean), and under a window the late ones visit
+// tiles that their own window has left behind.
 //
 // A CTA that gets several row tiles of one head reads its keys from HBM for
 // each.  Laying the row tiles of 512-row requests out in two passes over the
@@ -303,9 +310,9 @@ struct CacheWalk {
   }
   // The range's place for a part that is not a whole item.
   __device__ __forceinline__ int slot() const { return tile0 > 0 ? 0 : 1; }
-  // Keys of tiles [lo, hi) (of the request's) in this part that any row of the
-  // row tile can see: without a mask, rows of tokens up to t see keys up to
-  // C + t, so later tiles are neither loaded nor computed.
+  // The tiles [lo, hi) (of the request's) of this part that are visited: without
+  // a mask, rows of tokens up to t see keys up to C + t, so later tiles are neither
+  // loaded nor computed.  (The window trims the request's first tile only, kt0.)
   template <int KT>
   __device__ __forceinline__ void tiles(const CacheFwdParams& p, int& lo, int& hi) const {
     lo = r.kt0 + tile0;

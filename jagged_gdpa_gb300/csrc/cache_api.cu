@@ -106,7 +106,9 @@ bool cache_layout(int32_t heads, int32_t kv_heads, int32_t head_dim, int32_t max
 // From about 12 tiles per CTA on, as far as the host can tell (the table's width
 // is its bound of the lengths), that pays: d = 32, 16 heads, 64 requests of 4,100
 // tokens 96 us against 190, of 30 to 300 tokens (8 tiles) 28 against 22; d = 64, 8
-// heads, 92 against 117, and 15 against 12.5 for 4 requests of 191 to 553.
+// heads, 92 against 117, and 15 against 12.5 for 4 requests of 191 to 553 (where a
+// table much wider than they need takes the slower way; the window, which bounds an
+// item's tiles too, is not looked at).
 void put_together(CacheLayout* L, int32_t batch, int32_t kv_heads, int64_t max_rows, int64_t table_tokens) {
   if (L->heads_together == 1) return;
   const int64_t items = static_cast<int64_t>(batch) * kv_heads * ((max_rows + L->rows - 1) / L->rows);

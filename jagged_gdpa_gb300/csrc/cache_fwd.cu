@@ -5,7 +5,7 @@
 // head share its loads.  Of small heads (d < 128) an item takes 128 / d side by
 // side where their number allows and the work is large enough: their columns are
 // one contiguous 256-byte piece per token, and an item's start and end are paid
-// once for all of them (d = 32, 16 heads, 64 requests of 4,100 tokens: 96 us
+// once for all of them (d = 32, 16 heads, 64 requests of 4,100 tokens: 98 us
 // against 190 one by one).  Its keys stream through shared memory once, in tiles
 // of 64 tokens gathered from the pages by TMA.
 //
@@ -28,9 +28,9 @@
 // stops the loads.
 //
 // Measured, d = 128: 64 requests of 118 to 8,000 tokens, 8 key/value heads, 4
-// rows each: 171 us, 0.93 of the copy bandwidth; one of 131,072 tokens: 93 us
-// with the joining, 0.85.  d = 32, 128 requests, window 1,024: 57 us, 0.66: items
-// of 17 tiles, of which two or three are masked.
+// rows each: 171 to 175 us from GPU to GPU, 0.93 to 0.91 of the copy bandwidth; one
+// of 131,072 tokens: 94 us with the joining, 0.84.  d = 32, 128 requests, SiLU,
+// window 1,024: 59 us, 0.64: items of 17 tiles, of which two or three are masked.
 #include "act.cuh"
 #include "cache.cuh"
 #include "common.cuh"

@@ -26,14 +26,15 @@
 // thread).
 // TMEM: S_s at 128 s, O_s at 256 + 128 s.
 //
-// Measured, d = 128: 64 requests of 4,100 tokens, 8 key/value heads, 64 rows: 186
+// Measured, d = 128: 64 requests of 4,100 tokens, 8 key/value heads, 64 rows: 187
 // us, 0.87 of the copy bandwidth; 32 trees of 8 to 33 tokens, 32 to 132 rows, over
-// 177 to 13,900 tokens: 75 us, 0.60 (the items' starts and ends); 64 trees of 64
-// tokens, 512 rows, GELU with a bias over 134 to 8,066 tokens: 284 us, 0.52 of the
-// products at cuBLAS's burst rate.  At d = 64 the same 64 requests take 114 us,
-// 0.71 of the copy bandwidth, at d = 32 (16 heads) 192 us: a tile's 128 x 128
-// weights (1,024 cycles of the special-function units, a warpgroup's way from S to
-// P some 1,400) no longer hide behind half or a quarter of the bytes.
+// 177 to 13,900 tokens: 74 to 77 us, 0.60 (the items' starts and ends); 64 trees of
+// 64 tokens, 512 rows, GELU with a bias over 134 to 8,066 tokens: 322 us, 0.46 of
+// the products at cuBLAS's burst rate (284 with the packed kernels' GELU, which is
+// not right far below zero, see cc_act2).  At d = 64 the same 64 requests take 112
+// to 115 us (softmax; GELU 141, SiLU 149), at d = 32 (16 heads) 185 to 194 (258,
+// 271) where the bytes take 80: the way of a tile's 128 x 128 weights from S to P no
+// longer hides behind half or a quarter of the bytes.
 #include "act.cuh"
 #include "cache.cuh"
 #include "common.cuh"
