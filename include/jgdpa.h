@@ -397,6 +397,190 @@ JGDPA_API jgdpa_status jgdpa_cache_fwd(const void* q, int64_t q_stride, const vo
                                        void* workspace, size_t workspace_bytes, jgdpa_stream_t stream);
 
 /*
+ * Norms of queries and keys for each head with the rotation by position, in one
+ * pass: what stands in front of jgdpa_fwd (and, backward, behind jgdpa_bwd) where
+ * a model has them.  Of every head's vector x of every row,
+ *
+ *     h = x w / sqrt(mean(x^2) + eps)         (norm = 1; norm = 0: h = x)
+ *     (y_a, y_b) = (h_a cos t - h_b sin t, h_b cos t + h_a sin t),  t = pos * inv_freq[i]
+ *
+ * over the pairs (a, b) = (i, i + pairs), i < pairs (interleaved = 0), or (2 i,
+ * 2 i + 1) (interleaved = 1); columns from 2 pairs on are not rotated.
+ *   q, k       bf16 rows [heads][head_dim] ([kv_heads][head_dim]), q_stride /
+ *              k_stride elements apart (multiples of 8, at least a row: they may be slices of a
+ *              fused projection's output)
+ *   q_out, k_out  the same with strides of their own; an output may be its
+ *              input itself, and must not overlap anything else.  k (with k_out
+ *              and its other arguments) may be NULL with total_kv = 0: queries alone
+ *   q_offsets, kv_offsets  int32 [batch + 1] as in jgdpa_fwd: a row's position is its
+ *              place in its segment.  Rows behind the last segment (a padded
+ *              batch) are left as they were.  Not read, and may be NULL, where
+ *   q_positions, k_positions  int32 [total_q], [total_kv] are given instead of NULL: a row's
+ *              position, any int32
+ *   q_weight, k_weight  fp32 [head_dim], the w of the norms, or NULL for 1 (norm = 0: NULL)
+ *   inv_freq   fp32 [pairs], finite; 1 <= pairs <= head_dim / 2, and a multiple of 8
+ *              unless interleaved.  The angle of any position is right to some 2^-22 of a turn
+ *   eps        finite, >= 0; not used with norm = 0
+ *   workspace  where a device-detected error is to be read from
+ *              (jgdpa_norm_rotate_workspace_bytes(head_dim, 0) bytes), or NULL
+ * Device-detected errors: BAD_OFFSETS (offsets not in order from 0, or beyond the rows); the
+ * outputs are then unspecified.  fp32 throughout, one rounding at the end.
+ *
+ * Backward, from dq_out and dk_out (rows as q and k; strides of their own):
+ *   dq, dk     the gradients of q and k; either may be its dq_out / dk_out, or its q / k
+ *   dq_weight, dk_weight  fp32 [head_dim], sums over all rows and heads, in a fixed order
+ *              (the same bits on every run); NULL where not wanted (norm = 0: NULL)
+ * With norm = 0 q and k are not read and may be NULL (their strides are not looked at).  The workspace
+ * (jgdpa_norm_rotate_workspace_bytes(head_dim, 1) bytes) holds the CTAs' sums
+ * and is required where a weight's gradient is wanted.
+ */
+JGDPA_API size_t jgdpa_norm_rotate_workspace_bytes(int32_t head_dim, int32_t for_backward);
+JGDPA_API jgdpa_status jgdpa_norm_rotate(const void* q, int64_t q_stride, void* q_out, int64_t q_out_stride,
+                                         int64_t total_q, int32_t heads, const int32_t* q_offsets,
+                                         const int32_t* q_positions, const float* q_weight, const void* k,
+                                         int64_t k_stride, void* k_out, int64_t k_out_stride, int64_t total_kv,
+                                         int32_t kv_heads, const int32_t* kv_offsets, const int32_t* k_positions,
+                                         const float* k_weight, int32_t batch, int32_t head_dim, const float* inv_freq,
+                                         int32_t pairs, int32_t interleaved, int32_t norm, float eps, void* workspace,
+                                         size_t workspace_bytes, jgdpa_stream_t stream);
+JGDPA_API jgdpa_status jgdpa_norm_rotate_bwd(const void* dq_out, int64_t dq_out_stride, const void* q,
+                                             int64_t q_stride, void* dq, int64_t dq_stride, int64_t total_q,
+                                             int32_t heads, const int32_t* q_offsets, const int32_t* q_positions,
+                                             const float* q_weight, float* dq_weight, const void* dk_out,
+                                             int64_t dk_out_stride, const void* k, int64_t k_stride, void* dk,
+                                             int64_t dk_stride, int64_t total_kv, int32_t kv_heads,
+                                             const int32_t* kv_offsets, const int32_t* k_positions,
+                                             const float* k_weight, float* dk_weight, int32_t batch, int32_t head_dim,
+                                             const float* inv_freq, int32_t pairs, int32_t interleaved, int32_t norm,
+                                             float eps, void* workspace, size_t workspace_bytes, jgdpa_stream_t stream);
+
+/*
+ * jgdpa_cache_append with the norms and the rotation of jgdpa_norm_rotate on the
+ * way, and the new tokens' queries in the same launch: stands between
+ * jgdpa_cache_plan and jgdpa_cache_fwd.
+ *   q, q_out   bf16 rows [heads][head_dim] of the new tokens (q_out may be q); q
+ *              may be NULL with heads = 0: the cache alone
+ *   k_new, v_new, slots, k_cache, v_cache, ...  as in jgdpa_cache_append, the keys with norm
+ *              and rotation, the values as they are
+ *   q_offsets, kv_lens, depths  as in jgdpa_cache_fwd: new token t of request b is at
+ *              position kv_lens[b] - T_b + t, or + depths[its row] where depths are given
+ * Rows behind q_offsets[batch] are left out.  When an accepted row moves to another slot
+ * (jgdpa_verify's keep_slots), the same call with the same q_offsets, kv_lens and depths writes it
+ * there: a token's position does not depend on its slot.
+ * Device-detected errors (workspace of jgdpa_norm_rotate_workspace_bytes(head_dim, 0) bytes, or NULL):
+ * BAD_OFFSETS (offsets not in order from 0 or beyond total_new, kv_lens[b] < T_b, a depth
+ * that is negative or leads beyond 2^31 - 1; the rows concerned are then unspecified).
+ */
+JGDPA_API jgdpa_status jgdpa_cache_append_rotated(const void* q, int64_t q_stride, void* q_out, int64_t q_out_stride,
+                                                  int32_t heads, const void* k_new, const void* v_new,
+                                                  int64_t k_stride, int64_t v_stride, const int32_t* slots,
+                                                  int32_t total_new, void* k_cache, void* v_cache,
+                                                  int64_t k_page_stride, int64_t v_page_stride, int32_t num_pages,
+                                                  int32_t page_size, int32_t kv_heads, int32_t head_dim,
+                                                  const int32_t* q_offsets, const int32_t* kv_lens,
+                                                  const int32_t* depths, int32_t batch, const float* q_weight,
+                                                  const float* k_weight, const float* inv_freq, int32_t pairs,
+                                                  int32_t interleaved, int32_t norm, float eps, void* workspace,
+                                                  size_t workspace_bytes, jgdpa_stream_t stream);
+
+/*
+ * Verification of drafted tokens against the target's probabilities, from given
+ * random numbers, and the next token.  Row 0 of a request is the token it ended with, every other
+ * row a drafted one that continues an earlier row of the request, its parent.
+ *   target       probabilities [total_q][vocab], fp32 or (target_bf16 = 1) bf16, rows target_stride
+ *                elements apart: row r's are those of the token after row r
+ *   draft        the probabilities that the drafted tokens were drawn from, row r's
+ *                those of row r's own token (a request's row 0 is not read); NULL: drafts without
+ *                probabilities.  With them parents must be NULL
+ *   tokens       int32 [total_q]
+ *   parents      int32 [total_q], the parent's row within the request (row 0's is not
+ *                looked at); NULL: chains, each row continues the one before
+ *   uniforms     fp32 [total_q] in [0, 1): row r's decides on its token, a
+ *                request's row 0's draws the next token
+ *   q_offsets    int32 [batch + 1]; at most 1024 rows per request
+ * From the root (row 0) on the children of a row are tried in order: child c with token
+ * x stays if u_c draft_c(x) < target_parent(x), or without draft probabilities if u_c (1 - g) <
+ * target_parent(x), g the target_parent of the tokens refused there before (a token that
+ * was refused there before does not stay).  The first that stays is gone on from.  Where none
+ * does, the next token is drawn from max(target - draft, 0) of the row and its refused child (each difference in fp32), or
+ * from target without the refused tokens, or from target where no row was refused (or nothing
+ * is left): the least i whose sum of entries 0 .. i exceeds u times the sum of all.  Sums
+ * are kept to some 2^-46.  Entries that are negative, infinite or NaN count nothing.
+ *   accepted     int32 [batch]: rows that stay, row 0 among them (0 of a request without rows)
+ *   next_tokens  int32 [batch], -1 of a request without rows and where the whole row holds nothing
+ *   places       int32 [total_q]: a row's place among those that stay (0: the
+ *                root), or -1
+ *   keep_lens    int32 [batch], or NULL: kv_lens[b] - T_b + accepted, the next plan's ctx_lens;
+ *                needs kv_lens [batch]
+ *   keep_slots   int32 [total_q], or NULL: where a row that stays has to move in the cache so that those
+ *                that stay lie side by side, slots[q_offsets[b] + place]; -1 for rows that go or
+ *                lie there already.  For jgdpa_cache_append, jgdpa_cache_append_rotated and
+ *                jgdpa_cache4_append; needs slots [total_q], the plan's
+ * Rows behind q_offsets[batch] get -1.  Outputs must not overlap inputs.  The same bits on every run.
+ * Device-detected errors (workspace of jgdpa_verify_workspace_bytes() bytes, or NULL): BAD_OFFSETS (offsets not in order
+ * from 0 or beyond total_q, more than 1024 rows: such a request counts as one without rows;
+ * parents that are no earlier row, tokens outside the vocabulary: such a row does not stay).
+ */
+JGDPA_API size_t jgdpa_verify_workspace_bytes(void);
+JGDPA_API jgdpa_status jgdpa_verify(const void* target, int64_t target_stride, int32_t target_bf16, const void* draft,
+                                    int64_t draft_stride, int32_t draft_bf16, const int32_t* tokens,
+                                    const int32_t* parents, const float* uniforms, const int32_t* q_offsets,
+                                    int32_t batch, int32_t total_q, int32_t vocab, const int32_t* kv_lens,
+                                    const int32_t* slots, int32_t* accepted, int32_t* next_tokens, int32_t* places,
+                                    int32_t* keep_lens, int32_t* keep_slots, void* workspace, size_t workspace_bytes,
+                                    jgdpa_stream_t stream);
+
+/*
+ * The paged cache held in 4 bits: 0.28 of the bf16 cache's bytes at head_dim 128.  Pages, slots and
+ * block tables are jgdpa_cache_plan's.  Of keys, and of values:
+ *   codes        uint8 [kv_heads][page_size][head_dim / 2] a page, code_stride bytes apart (a multiple
+ *                of 16, at least a page): columns 2 j and 2 j + 1 in the low and high bits of byte j
+ *   scales       bf16 [kv_heads][page_size][2] a page, scale_stride elements apart (a multiple of 8,
+ *                at least a page): step s and middle z of each token's head
+ * A code c stands for z + s (c - 8).
+ *
+ * jgdpa_cache4_append writes rows as jgdpa_cache_append does (rows with slots outside the cache are
+ * skipped).  With lo and hi the least and largest of a head's values, each operation rounded to fp32,
+ * halves to even:
+ *     s = bf16((hi - lo) / 15), z = bf16(lo + 8 s), c = clamp(rint((x - z) / s), -8, 7) + 8 (8 where s is 0).
+ * A head with a NaN or an infinity (or whose hi - lo leaves fp32) stands for NaN or infinities as a whole.
+ *
+ * jgdpa_cache4_read is the way back: rows slots[r] of the cache as bf16 rows (k_out and v_out, strides as
+ * k_new's), for the packed calls (the cached part of a long prompt) or another cache.  Zeros for slots
+ * outside the cache.
+ */
+JGDPA_API jgdpa_status jgdpa_cache4_append(const void* k_new, const void* v_new, int64_t k_stride, int64_t v_stride,
+                                           const int32_t* slots, int32_t total_new, void* k_codes, void* k_scales,
+                                           void* v_codes, void* v_scales, int64_t k_code_stride, int64_t k_scale_stride,
+                                           int64_t v_code_stride, int64_t v_scale_stride, int32_t num_pages,
+                                           int32_t page_size, int32_t kv_heads, int32_t head_dim,
+                                           jgdpa_stream_t stream);
+JGDPA_API jgdpa_status jgdpa_cache4_read(const void* k_codes, const void* k_scales, const void* v_codes,
+                                         const void* v_scales, int64_t k_code_stride, int64_t k_scale_stride,
+                                         int64_t v_code_stride, int64_t v_scale_stride, int32_t num_pages,
+                                         int32_t page_size, int32_t kv_heads, int32_t head_dim, const int32_t* slots,
+                                         int32_t rows, void* k_out, void* v_out, int64_t k_stride, int64_t v_stride,
+                                         jgdpa_stream_t stream);
+
+/*
+ * jgdpa_cache_fwd over a cache held in 4 bits: its arguments, its computation from the values that the
+ * codes stand for, which are not rounded again, and its errors.  Made for few rows (max_q heads / kv_heads up to
+ * some 16: the keys are read again for every 16).  NaN and infinities of steps and middles reach
+ * only the rows that see their token; a row of q with an infinity or a NaN is NaN or infinite itself.
+ */
+JGDPA_API size_t jgdpa_cache4_fwd_workspace_bytes(int32_t head_dim);
+JGDPA_API jgdpa_status jgdpa_cache4_fwd(const void* q, int64_t q_stride, const void* k_codes, const void* k_scales,
+                                        const void* v_codes, const void* v_scales, int64_t k_code_stride,
+                                        int64_t k_scale_stride, int64_t v_code_stride, int64_t v_scale_stride,
+                                        int32_t num_pages, int32_t page_size, const int32_t* block_table,
+                                        int32_t table_width, const int32_t* q_offsets, const int32_t* kv_lens,
+                                        int32_t batch, int64_t total_q, int32_t max_q, int32_t heads, int32_t kv_heads,
+                                        int32_t head_dim, jgdpa_act act, float scale, const float* bias_table,
+                                        int32_t bias_len, int32_t window, const int32_t* tree_mask, int32_t mask_words,
+                                        const int32_t* depths, void* out, float* lse, void* workspace,
+                                        size_t workspace_bytes, jgdpa_stream_t stream);
+
+/*
  * Forward pass without a caller-provided workspace: the same computation and
  * arguments as jgdpa_fwd minus (workspace, workspace_bytes).  There is no
  * counterpart on the pages; this entry point exists for callers that cannot

@@ -12,7 +12,12 @@ from ._lib import (  # noqa: F401
     JgdpaError,
     jgdpa_bwd,
     jgdpa_bwd_shared_q,
+    jgdpa_cache4_append,
+    jgdpa_cache4_fwd,
+    jgdpa_cache4_fwd_workspace_bytes,
+    jgdpa_cache4_read,
     jgdpa_cache_append,
+    jgdpa_cache_append_rotated,
     jgdpa_cache_fwd,
     jgdpa_cache_fwd_workspace_bytes,
     jgdpa_cache_plan,
@@ -23,9 +28,14 @@ from ._lib import (  # noqa: F401
     jgdpa_eval_activation,
     jgdpa_fwd,
     jgdpa_fwd_noalloc,
+    jgdpa_norm_rotate,
+    jgdpa_norm_rotate_bwd,
+    jgdpa_norm_rotate_workspace_bytes,
     jgdpa_read_device_status,
     jgdpa_set_wait_limit_ns,
     jgdpa_status_string,
+    jgdpa_verify,
+    jgdpa_verify_workspace_bytes,
     jgdpa_workspace_bytes,
     load,
 )

@@ -31,7 +31,10 @@ EXPORTS = ("jgdpa_workspace_bytes", "jgdpa_fwd", "jgdpa_fwd_ex", "jgdpa_bwd", "j
            "jgdpa_read_device_status", "jgdpa_status_string", "jgdpa_eval_activation", "jgdpa_fwd_noalloc",
            "jgdpa_set_wait_limit_ns", "jgdpa_shared_q_workspace_bytes", "jgdpa_fwd_shared_q", "jgdpa_bwd_shared_q",
            "jgdpa_cache_plan_workspace_bytes", "jgdpa_cache_plan", "jgdpa_cache_append",
-           "jgdpa_cache_fwd_workspace_bytes", "jgdpa_cache_fwd")
+           "jgdpa_cache_fwd_workspace_bytes", "jgdpa_cache_fwd",
+           "jgdpa_norm_rotate_workspace_bytes", "jgdpa_norm_rotate", "jgdpa_norm_rotate_bwd",
+           "jgdpa_cache_append_rotated", "jgdpa_verify_workspace_bytes", "jgdpa_verify",
+           "jgdpa_cache4_append", "jgdpa_cache4_read", "jgdpa_cache4_fwd_workspace_bytes", "jgdpa_cache4_fwd")
 
 
 class JgdpaError(RuntimeError):
@@ -97,6 +100,32 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.jgdpa_cache_fwd.argtypes = [P, i64, P, P, i64, i64, i32, i32, P, i32, P, P, i32, i64, i32, i32, i32, i32,
                                     ctypes.c_int, f32, P, i32, i32, P, i32, P, P, P, P, sz, P]
     lib.jgdpa_cache_fwd.restype = ctypes.c_int
+    lib.jgdpa_norm_rotate_workspace_bytes.argtypes = [i32, i32]
+    lib.jgdpa_norm_rotate_workspace_bytes.restype = sz
+    side = [P, i64, P, i64, i64, i32, P, P, P]
+    rotation = [P, i32, i32, i32, f32, P, sz, P]
+    lib.jgdpa_norm_rotate.argtypes = side + side + [i32, i32] + rotation
+    lib.jgdpa_norm_rotate.restype = ctypes.c_int
+    side = [P, i64, P, i64, P, i64, i64, i32, P, P, P, P]
+    lib.jgdpa_norm_rotate_bwd.argtypes = side + side + [i32, i32] + rotation
+    lib.jgdpa_norm_rotate_bwd.restype = ctypes.c_int
+    lib.jgdpa_cache_append_rotated.argtypes = [P, i64, P, i64, i32, P, P, i64, i64, P, i32, P, P, i64, i64, i32, i32, i32,
+                                               i32, P, P, P, i32, P, P] + rotation
+    lib.jgdpa_cache_append_rotated.restype = ctypes.c_int
+    lib.jgdpa_verify_workspace_bytes.argtypes = []
+    lib.jgdpa_verify_workspace_bytes.restype = sz
+    lib.jgdpa_verify.argtypes = [P, i64, i32, P, i64, i32, P, P, P, P, i32, i32, i32, P, P, P, P, P, P, P, P, sz, P]
+    lib.jgdpa_verify.restype = ctypes.c_int
+    cache4 = [P, P, P, P, i64, i64, i64, i64, i32, i32]
+    lib.jgdpa_cache4_append.argtypes = [P, P, i64, i64, P, i32] + cache4 + [i32, i32, P]
+    lib.jgdpa_cache4_append.restype = ctypes.c_int
+    lib.jgdpa_cache4_read.argtypes = cache4 + [i32, i32, P, i32, P, P, i64, i64, P]
+    lib.jgdpa_cache4_read.restype = ctypes.c_int
+    lib.jgdpa_cache4_fwd_workspace_bytes.argtypes = [i32]
+    lib.jgdpa_cache4_fwd_workspace_bytes.restype = sz
+    lib.jgdpa_cache4_fwd.argtypes = [P, i64] + cache4 + [P, i32, P, P, i32, i64, i32, i32, i32, i32, ctypes.c_int, f32, P,
+                                                         i32, i32, P, i32, P, P, P, P, sz, P]
+    lib.jgdpa_cache4_fwd.restype = ctypes.c_int
     _libs[path] = lib
     return lib
 
@@ -759,4 +788,668 @@ def jgdpa_cache_fwd(q, k_cache, v_cache, block_table, q_offsets, kv_lens, act, s
                              workspace.numel(), raw)
     if rc:
         raise JgdpaError(rc, "jgdpa_cache_fwd")
+    return out, lse
+
+
+# ------------------------------------------- norms of queries and keys with the rotation
+def jgdpa_norm_rotate_workspace_bytes(head_dim: int, for_backward: bool = False, lib=None) -> int:
+    _refuse_wide(head_dim=head_dim)
+    return int((lib or load()).jgdpa_norm_rotate_workspace_bytes(head_dim, int(bool(for_backward))))
+
+
+def _refuse_side(x, name, off_name, offsets, positions, weight, batch, d, device):
+    """Refuses what `_side` does not take, by name."""
+    _check(x, name, torch.bfloat16, (None, None, d), device)
+    _refuse_rows(x, name, x.shape[1], d)
+    if positions is None:
+        _check(offsets, off_name, torch.int32, (None,) if batch is None else (batch + 1,), device)
+        if offsets.shape[0] < 1:
+            raise ValueError(f"{off_name} must hold batch + 1 >= 1 entries")
+    else:
+        _check(positions, f"{name[-1] if name[0] == 'd' else name}_positions", torch.int32, (x.shape[0],), device)
+    _check(weight, f"{name}_weight", torch.float32, (d,), device, optional=True)
+    _contiguous(**{off_name: None if positions is not None else offsets, f"{name}_positions": positions,
+                   f"{name}_weight": weight})
+    if x.shape[1] < 1:
+        raise ValueError(f"{name} must have heads")
+
+
+def _refuse_rotation(inv_freq, eps, interleaved, d, device, weights):
+    if d not in (32, 64, 128):
+        raise ValueError(f"head_dim must be 32, 64 or 128, got {d}")
+    _check(inv_freq, "inv_freq", torch.float32, (None,), device)
+    _contiguous(inv_freq=inv_freq)
+    n = inv_freq.shape[0]
+    if not 1 <= n <= d // 2 or (not interleaved and n % 8):
+        raise ValueError(f"inv_freq must hold 1 to {d // 2} entries, a multiple of 8 of them unless interleaved, got {n}")
+    if eps is None and any(w is not None for w in weights):
+        raise ValueError("weights belong to a norm; eps None has none")
+
+
+def _rotation_ok(inv_freq, eps, interleaved, d, index) -> bool:
+    n = inv_freq.shape[0]
+    return _is(inv_freq, _f32, (n,), index) and 1 <= n <= d // 2 and (interleaved or n % 8 == 0) and d in (32, 64, 128)
+
+
+def _side_ok(x, offsets, positions, weight, d, index) -> int:
+    """Row stride of a tensor of a rotation call, 0 if something of it cannot be used."""
+    rows, heads, dim = x.shape
+    if not (x.dtype is _bf16 and dim == d and heads > 0 and x.get_device() == index):
+        return 0
+    if positions is None:
+        n = offsets.shape[0]
+        if n < 1 or not _is(offsets, _i32, (n,), index):
+            return 0
+    elif not _is(positions, _i32, (rows,), index):
+        return 0
+    if weight is not None and not _is(weight, _f32, (d,), index):
+        return 0
+    return _row_stride(x, heads, d)
+
+
+def _at(t):
+    return None if t is None else t.data_ptr()
+
+
+def _batch_of(pairs):
+    """The batch of the offsets in use, None if they do not agree."""
+    sizes = {o.shape[0] - 1 for o, p in pairs if p is None}
+    return None if len(sizes) > 1 else (sizes.pop() if sizes else 0)
+
+
+def _empty_rows(x, alloc, shape=None):
+    shape = x.shape if shape is None else shape
+    return torch.empty(shape, dtype=_bf16, device=x.device) if alloc is None else alloc(shape, _bf16)
+
+
+def _out_stride(t, x, index) -> int:
+    if not (t.dtype is _bf16 and t.shape == x.shape and t.get_device() == index):
+        return 0
+    return _row_stride(t, x.shape[1], x.shape[2])
+
+
+def _refuse_out(t, name, x):
+    if t is not None:
+        _check(t, name, torch.bfloat16, tuple(x.shape), x.device)
+        _refuse_rows(t, name, x.shape[1], x.shape[2])
+
+
+def jgdpa_norm_rotate(q, k, q_offsets, kv_offsets, inv_freq, q_weight=None, k_weight=None, eps=1e-6,
+                      interleaved: bool = False, q_positions=None, k_positions=None, q_out=None, k_out=None,
+                      workspace=None, stream=None, lib=None):
+    """Norms of queries and keys for each head with the rotation by position
+    (jgdpa_norm_rotate); returns (q_out, k_out).  q [total_q, heads, head_dim] and
+    k [total_kv, kv_heads, head_dim] may be slices of wider rows; k None: queries
+    alone.  eps None: the rotation without a norm.  Positions are those within
+    the segments of q_offsets / kv_offsets, or q_positions / k_positions."""
+    lib = lib or load()
+    eps_value = 0.0 if eps is None else float(eps)
+    qs = ks = qos = kos = 0
+    batch = None
+    ok = False
+    try:
+        index, d = q.get_device(), q.shape[2]
+        ok = index >= 0 and _rotation_ok(inv_freq, eps, interleaved, d, index)
+        ok = ok and (eps is not None or (q_weight is None and k_weight is None))
+        qs = _side_ok(q, q_offsets, q_positions, q_weight, d, index) if ok else 0
+        ks = 8 if k is None else (_side_ok(k, kv_offsets, k_positions, k_weight, d, index) if ok else 0)
+        qos = qs if q_out is None else _out_stride(q_out, q, index)
+        kos = ks if k is None or k_out is None else _out_stride(k_out, k, index)
+        batch = _batch_of([(q_offsets, q_positions)] + ([] if k is None else [(kv_offsets, k_positions)]))
+        ok = ok and qs and ks and qos and kos and batch is not None
+        ok = ok and (workspace is None or _is(workspace, _u8, (workspace.numel(),), index))
+        ok = ok and not (k is None and (k_out is not None or k_weight is not None))
+    except (AttributeError, ValueError, IndexError, TypeError):
+        ok = False
+    if not ok:
+        if not isinstance(q, torch.Tensor) or q.dim() != 3:
+            raise ValueError("q must be a bf16 tensor [total_q, heads, head_dim]")
+        d, device = q.shape[2], q.device
+        _refuse_rotation(inv_freq, eps, interleaved, d, device, (q_weight, k_weight))
+        _refuse_side(q, "q", "q_offsets", q_offsets, q_positions, q_weight, None, d, device)
+        if k is not None:
+            batch = None if q_positions is not None else q_offsets.shape[0] - 1
+            _refuse_side(k, "k", "kv_offsets", kv_offsets, k_positions, k_weight, batch, d, device)
+            _refuse_out(k_out, "k_out", k)
+        elif k_out is not None or k_weight is not None:
+            raise ValueError("k_out and k_weight belong to k, which is None")
+        _refuse_out(q_out, "q_out", q)
+        _check_bytes(workspace, "workspace", device)
+        _contiguous(workspace=workspace)
+        _need_cuda(q)
+        raise ValueError("jgdpa_norm_rotate: unusable tensors")
+    if index != torch.cuda.current_device():
+        return _on_other_device(jgdpa_norm_rotate, q.device, (q, k, q_offsets, kv_offsets, inv_freq, q_weight, k_weight, eps,
+                                interleaved, q_positions, k_positions, q_out, k_out, workspace, stream, lib), {})
+    raw, alloc = _launch_on(stream, q.device)
+    if q_out is None:
+        q_out = _empty_rows(q, alloc)
+        qos = q.shape[1] * d
+    k_rows = k_heads = 0
+    if k is not None:
+        k_rows, k_heads = k.shape[0], k.shape[1]
+        if k_out is None:
+            k_out = _empty_rows(k, alloc)
+            kos = k_heads * d
+    ws, ws_bytes = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel())
+    rc = lib.jgdpa_norm_rotate(q.data_ptr(), qs, q_out.data_ptr(), qos, q.shape[0], q.shape[1],
+                               None if q_positions is not None else q_offsets.data_ptr(), _at(q_positions), _at(q_weight),
+                               _at(k), ks, _at(k_out), kos, k_rows, k_heads,
+                               None if k is None or k_positions is not None else kv_offsets.data_ptr(),
+                               None if k is None else _at(k_positions), _at(k_weight), batch, d, inv_freq.data_ptr(),
+                               inv_freq.shape[0], 1 if interleaved else 0, 0 if eps is None else 1, eps_value, ws, ws_bytes, raw)
+    if rc:
+        raise JgdpaError(rc, "jgdpa_norm_rotate")
+    return q_out, k_out
+
+
+def jgdpa_norm_rotate_bwd(dq_out, dk_out, q, k, q_offsets, kv_offsets, inv_freq, q_weight=None, k_weight=None, eps=1e-6,
+                          interleaved: bool = False, q_positions=None, k_positions=None, dq=None, dk=None,
+                          dq_weight=None, dk_weight=None, workspace=None, stream=None, lib=None):
+    """Backward of jgdpa_norm_rotate; returns (dq, dk, dq_weight, dk_weight), a
+    weight's gradient (fp32, summed over rows and heads) None where there is no
+    such weight, unless a tensor for it is passed.  dk_out and k None: queries
+    alone.  eps None: q and k are not read and may be None."""
+    lib = lib or load()
+    eps_value = 0.0 if eps is None else float(eps)
+    both = dk_out is not None
+    batch = None
+    ok = False
+    gqs = gks = qs = ks = dqs = dks = 0
+    try:
+        index, d = dq_out.get_device(), dq_out.shape[2]
+        ok = index >= 0 and _rotation_ok(inv_freq, eps, interleaved, d, index)
+        ok = ok and (eps is not None or not any(w is not None for w in (q_weight, k_weight, dq_weight, dk_weight)))
+        gqs = _side_ok(dq_out, q_offsets, q_positions, q_weight, d, index) if ok else 0
+        gks = (_side_ok(dk_out, kv_offsets, k_positions, k_weight, d, index) if ok else 0) if both else 8
+        qs = gqs if eps is None else _out_stride(q, dq_out, index)
+        ks = gks if eps is None or not both else _out_stride(k, dk_out, index)
+        dqs = gqs if dq is None else _out_stride(dq, dq_out, index)
+        dks = gks if dk is None or not both else _out_stride(dk, dk_out, index)
+        batch = _batch_of([(q_offsets, q_positions)] + ([(kv_offsets, k_positions)] if both else []))
+        ok = ok and gqs and gks and qs and ks and dqs and dks and batch is not None
+        ok = ok and all(t is None or _is(t, _f32, (d,), index) for t in (dq_weight, dk_weight))
+        ok = ok and (workspace is None or _is(workspace, _u8, (workspace.numel(),), index))
+        ok = ok and (both or not any(t is not None for t in (k, dk, k_weight, dk_weight)))
+    except (AttributeError, ValueError, IndexError, TypeError):
+        ok = False
+    if not ok:
+        if not isinstance(dq_out, torch.Tensor) or dq_out.dim() != 3:
+            raise ValueError("dq_out must be a bf16 tensor [total_q, heads, head_dim]")
+        d, device = dq_out.shape[2], dq_out.device
+        _refuse_rotation(inv_freq, eps, interleaved, d, device, (q_weight, k_weight, dq_weight, dk_weight))
+        _refuse_side(dq_out, "dq_out", "q_offsets", q_offsets, q_positions, q_weight, None, d, device)
+        if both:
+            batch = None if q_positions is not None else q_offsets.shape[0] - 1
+            _refuse_side(dk_out, "dk_out", "kv_offsets", kv_offsets, k_positions, k_weight, batch, d, device)
+        elif any(t is not None for t in (k, dk, k_weight, dk_weight)):
+            raise ValueError("k, dk and their weights belong to dk_out, which is None")
+        for x, name, like in ((q, "q", dq_out), (k, "k", dk_out)):
+            if eps is not None and like is not None:
+                if x is None:
+                    raise ValueError(f"{name} is required")
+                _refuse_out(x, name, like)
+        _refuse_out(dq, "dq", dq_out)
+        if both:
+            _refuse_out(dk, "dk", dk_out)
+        for t, name in ((dq_weight, "dq_weight"), (dk_weight, "dk_weight")):
+            _check(t, name, torch.float32, (d,), device, optional=True)
+        _check_bytes(workspace, "workspace", device)
+        _contiguous(workspace=workspace, dq_weight=dq_weight, dk_weight=dk_weight)
+        _need_cuda(dq_out)
+        raise ValueError("jgdpa_norm_rotate_bwd: unusable tensors")
+    if index != torch.cuda.current_device():
+        return _on_other_device(jgdpa_norm_rotate_bwd, dq_out.device, (dq_out, dk_out, q, k, q_offsets, kv_offsets, inv_freq,
+                                q_weight, k_weight, eps, interleaved, q_positions, k_positions, dq, dk, dq_weight, dk_weight,
+                                workspace, stream, lib), {})
+    device = dq_out.device
+    raw, alloc = _launch_on(stream, device)
+    if dq is None:
+        dq = _empty_rows(dq_out, alloc)
+        dqs = dq_out.shape[1] * d
+    k_rows = k_heads = 0
+    if both:
+        k_rows, k_heads = dk_out.shape[0], dk_out.shape[1]
+        if dk is None:
+            dk = _empty_rows(dk_out, alloc)
+            dks = k_heads * d
+    if dq_weight is None and q_weight is not None:
+        dq_weight = torch.empty(d, dtype=_f32, device=device) if alloc is None else alloc((d,), _f32)
+    if dk_weight is None and k_weight is not None:
+        dk_weight = torch.empty(d, dtype=_f32, device=device) if alloc is None else alloc((d,), _f32)
+    if workspace is None and (dq_weight is not None or dk_weight is not None):
+        n = max(256, lib.jgdpa_norm_rotate_workspace_bytes(d, 1))
+        workspace = torch.empty(n, dtype=_u8, device=device) if alloc is None else alloc((n,), _u8, result=False)
+    ws, ws_bytes = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel())
+    read = eps is not None
+    rc = lib.jgdpa_norm_rotate_bwd(
+        dq_out.data_ptr(), gqs, q.data_ptr() if read else None, qs, dq.data_ptr(), dqs, dq_out.shape[0], dq_out.shape[1],
+        None if q_positions is not None else q_offsets.data_ptr(), _at(q_positions), _at(q_weight), _at(dq_weight),
+        _at(dk_out), gks, k.data_ptr() if read and both else None, ks, _at(dk), dks, k_rows, k_heads,
+        None if not both or k_positions is not None else kv_offsets.data_ptr(), _at(k_positions) if both else None,
+        _at(k_weight), _at(dk_weight), batch, d, inv_freq.data_ptr(), inv_freq.shape[0], 1 if interleaved else 0,
+        1 if read else 0, eps_value, ws, ws_bytes, raw)
+    if rc:
+        raise JgdpaError(rc, "jgdpa_norm_rotate_bwd")
+    return dq, dk, dq_weight, dk_weight
+
+
+def _refuse_append_rotated(q, k_new, v_new, slots, k_cache, v_cache, q_offsets, kv_lens, inv_freq, q_weight, k_weight,
+                           eps, interleaved, depths, q_out, workspace):
+    _refuse_append(k_new, v_new, slots, k_cache, v_cache)
+    d, device, rows = k_cache.shape[3], k_cache.device, k_new.shape[0]
+    _refuse_rotation(inv_freq, eps, interleaved, d, device, (q_weight, k_weight))
+    if q is not None:
+        _check(q, "q", torch.bfloat16, (rows, None, d), device)
+        _refuse_rows(q, "q", q.shape[1], d)
+        if q.shape[1] < 1:
+            raise ValueError("q must have heads; pass None for none")
+        _refuse_out(q_out, "q_out", q)
+    elif q_out is not None or q_weight is not None:
+        raise ValueError("q_out and q_weight belong to q, which is None")
+    _check(kv_lens, "kv_lens", torch.int32, (None,), device)
+    _check(q_offsets, "q_offsets", torch.int32, (kv_lens.shape[0] + 1,), device)
+    _check(depths, "depths", torch.int32, (rows,), device, optional=True)
+    _check(q_weight, "q_weight", torch.float32, (d,), device, optional=True)
+    _check(k_weight, "k_weight", torch.float32, (d,), device, optional=True)
+    _check_bytes(workspace, "workspace", device)
+    _contiguous(kv_lens=kv_lens, q_offsets=q_offsets, depths=depths, q_weight=q_weight, k_weight=k_weight, workspace=workspace)
+
+
+def jgdpa_cache_append_rotated(q, k_new, v_new, slots, k_cache, v_cache, q_offsets, kv_lens, inv_freq, q_weight=None,
+                               k_weight=None, eps=1e-6, interleaved: bool = False, depths=None, q_out=None,
+                               workspace=None, stream=None, lib=None):
+    """jgdpa_cache_append with the norms and the rotation on the way, and the new
+    tokens' queries [total_new, heads, head_dim] in the same launch (q None: the
+    cache alone); returns (q_out, k_cache, v_cache).  q_offsets, kv_lens and
+    depths as in jgdpa_cache_fwd; eps None: no norm."""
+    lib = lib or load()
+    eps_value = 0.0 if eps is None else float(eps)
+    qs = qos = ks = vs = kps = vps = 0
+    ok = False
+    try:
+        index = k_cache.get_device()
+        n, page, kv_heads, d = k_cache.shape
+        rows, batch = k_new.shape[0], kv_lens.shape[0]
+        shape = (rows, kv_heads, d)
+        ok = (index >= 0 and k_cache.dtype is _bf16 and v_cache.dtype is _bf16 and v_cache.shape == k_cache.shape
+              and v_cache.get_device() == index and k_new.dtype is _bf16 and v_new.dtype is _bf16
+              and k_new.shape == shape and v_new.shape == shape and k_new.get_device() == index
+              and v_new.get_device() == index and _is(slots, _i32, (rows,), index) and _is(kv_lens, _i32, (batch,), index)
+              and _is(q_offsets, _i32, (batch + 1,), index) and _rotation_ok(inv_freq, eps, interleaved, d, index)
+              and (depths is None or _is(depths, _i32, (rows,), index))
+              and (q_weight is None or (q is not None and eps is not None and _is(q_weight, _f32, (d,), index)))
+              and (k_weight is None or (eps is not None and _is(k_weight, _f32, (d,), index)))
+              and (workspace is None or _is(workspace, _u8, (workspace.numel(),), index)))
+        if ok:
+            kps, vps = _page_stride(k_cache, page, kv_heads, d), _page_stride(v_cache, page, kv_heads, d)
+            ks, vs = _row_stride(k_new, kv_heads, d), _row_stride(v_new, kv_heads, d)
+            heads = 0
+            if q is not None:
+                heads = q.shape[1]
+                ok = heads > 0 and q.dtype is _bf16 and q.shape == (rows, heads, d) and q.get_device() == index
+                qs = _row_stride(q, heads, d)
+                qos = heads * d if q_out is None else _out_stride(q_out, q, index)
+                ok = ok and qs and qos
+            else:
+                ok = q_out is None
+            ok = ok and ks and vs and kps and vps
+    except (AttributeError, ValueError, IndexError, TypeError):
+        ok = False
+    if not ok:
+        _refuse_append_rotated(q, k_new, v_new, slots, k_cache, v_cache, q_offsets, kv_lens, inv_freq, q_weight, k_weight, eps,
+                               interleaved, depths, q_out, workspace)
+        raise ValueError("jgdpa_cache_append_rotated: unusable tensors")
+    if max(rows, n) > _I32_MAX:
+        _refuse_wide(**{"k_new's rows": rows, "k_cache's pages": n})
+    if index != torch.cuda.current_device():
+        return _on_other_device(jgdpa_cache_append_rotated, k_cache.device, (q, k_new, v_new, slots, k_cache, v_cache,
+                                q_offsets, kv_lens, inv_freq, q_weight, k_weight, eps, interleaved, depths, q_out, workspace,
+                                stream, lib), {})
+    raw, alloc = _launch_on(stream, k_cache.device)
+    if q is not None and q_out is None:
+        q_out = _empty_rows(q, alloc)
+    ws, ws_bytes = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel())
+    rc = lib.jgdpa_cache_append_rotated(_at(q), qs, _at(q_out), qos, heads, k_new.data_ptr(), v_new.data_ptr(), ks, vs,
+                                        slots.data_ptr(), rows, k_cache.data_ptr(), v_cache.data_ptr(), kps, vps, n, page,
+                                        kv_heads, d, q_offsets.data_ptr(), kv_lens.data_ptr(), _at(depths), batch,
+                                        _at(q_weight), _at(k_weight), inv_freq.data_ptr(), inv_freq.shape[0],
+                                        1 if interleaved else 0, 0 if eps is None else 1, eps_value, ws, ws_bytes, raw)
+    if rc:
+        raise JgdpaError(rc, "jgdpa_cache_append_rotated")
+    return q_out, k_cache, v_cache
+
+
+# ------------------------------------------------------- verification of drafted tokens
+def jgdpa_verify_workspace_bytes(lib=None) -> int:
+    return int((lib or load()).jgdpa_verify_workspace_bytes())
+
+
+def _prob_stride(t) -> int:
+    """Elements between the rows of probabilities, 0 if a row is not contiguous or rows overlap."""
+    rows, vocab = t.shape
+    if vocab > 1 and t.stride(1) != 1:
+        return 0
+    if rows <= 1:
+        return vocab
+    return t.stride(0) if t.stride(0) >= vocab else 0
+
+
+def _refuse_verify(target_probs, tokens, q_offsets, uniforms, draft_probs, parents, kv_lens, slots, workspace):
+    if not isinstance(target_probs, torch.Tensor) or target_probs.dim() != 2:
+        raise ValueError("target_probs must be a tensor [total_q, vocab]")
+    device = target_probs.device
+    total, vocab = target_probs.shape
+    for t, name in ((target_probs, "target_probs"), (draft_probs, "draft_probs")):
+        if t is None:
+            continue
+        if not isinstance(t, torch.Tensor) or t.dtype not in (torch.float32, torch.bfloat16):
+            raise ValueError(f"{name} must be an fp32 or bf16 tensor")
+        _check(t, name, t.dtype, (total, vocab), device)
+        if not _prob_stride(t):
+            raise ValueError(f"{name}: rows must be contiguous inside and must not overlap")
+    if vocab < 1:
+        raise ValueError("target_probs must have columns")
+    if draft_probs is not None and parents is not None:
+        raise ValueError("draft_probs go with chains; parents must be None")
+    _check(tokens, "tokens", torch.int32, (total,), device)
+    _check(uniforms, "uniforms", torch.float32, (total,), device)
+    _check(q_offsets, "q_offsets", torch.int32, (None,), device)
+    if q_offsets.shape[0] < 1:
+        raise ValueError("q_offsets must hold batch + 1 >= 1 entries")
+    _check(parents, "parents", torch.int32, (total,), device, optional=True)
+    _check(kv_lens, "kv_lens", torch.int32, (q_offsets.shape[0] - 1,), device, optional=True)
+    _check(slots, "slots", torch.int32, (total,), device, optional=True)
+    _check_bytes(workspace, "workspace", device)
+    _contiguous(tokens=tokens, uniforms=uniforms, q_offsets=q_offsets, parents=parents, kv_lens=kv_lens, slots=slots,
+                workspace=workspace)
+    _need_cuda(target_probs)
+
+
+def jgdpa_verify(target_probs, tokens, q_offsets, uniforms, draft_probs=None, parents=None, kv_lens=None, slots=None,
+                 workspace=None, stream=None, lib=None):
+    """Which drafted tokens stay, and the next one (jgdpa_verify); returns
+    (accepted, next_tokens, places, keep_lens, keep_slots).  target_probs and
+    draft_probs fp32 or bf16 [total_q, vocab], tokens and parents int32 [total_q],
+    uniforms fp32 [total_q].  keep_lens, the next plan's ctx_lens, is None without kv_lens,
+    keep_slots, where the rows that stay move to, without slots."""
+    lib = lib or load()
+    ps = ds = 0
+    ok = False
+    try:
+        index = target_probs.get_device()
+        total, vocab = target_probs.shape
+        batch = q_offsets.shape[0] - 1
+        half = target_probs.dtype is _bf16
+        draft_half = False
+        ok = (index >= 0 and batch >= 0 and vocab > 0 and (half or target_probs.dtype is _f32)
+              and _is(tokens, _i32, (total,), index) and _is(uniforms, _f32, (total,), index)
+              and _is(q_offsets, _i32, (batch + 1,), index)
+              and (parents is None or (draft_probs is None and _is(parents, _i32, (total,), index)))
+              and (kv_lens is None or _is(kv_lens, _i32, (batch,), index))
+              and (slots is None or _is(slots, _i32, (total,), index))
+              and (workspace is None or _is(workspace, _u8, (workspace.numel(),), index)))
+        ps = ds = _prob_stride(target_probs)
+        if ok and draft_probs is not None:
+            draft_half = draft_probs.dtype is _bf16
+            ok = ((draft_half or draft_probs.dtype is _f32) and draft_probs.shape == (total, vocab)
+                  and draft_probs.get_device() == index)
+            ds = _prob_stride(draft_probs)
+    except (AttributeError, ValueError, IndexError, TypeError):
+        ok = False
+    if not (ok and ps and ds):
+        _refuse_verify(target_probs, tokens, q_offsets, uniforms, draft_probs, parents, kv_lens, slots, workspace)
+        raise ValueError("jgdpa_verify: unusable tensors")
+    if max(total, vocab) > _I32_MAX:
+        _refuse_wide(**{"target_probs' rows": total, "target_probs' columns": vocab})
+    if index != torch.cuda.current_device():
+        return _on_other_device(jgdpa_verify, target_probs.device, (target_probs, tokens, q_offsets, uniforms, draft_probs,
+                                parents, kv_lens, slots, workspace, stream, lib), {})
+    device = target_probs.device
+    raw, alloc = _launch_on(stream, device)
+    # the results as pieces of one tensor: batch entries, then total ones
+    n = batch * (2 if kv_lens is None else 3)
+    both = (n + total * (1 if slots is None else 2),)
+    every = torch.empty(both, dtype=_i32, device=device) if alloc is None else alloc(both, _i32)
+    accepted, next_tokens, places = every[:batch], every[batch:2 * batch], every[n:n + total]
+    keep_lens = None if kv_lens is None else every[2 * batch:n]
+    keep_slots = None if slots is None else every[n + total:]
+    ws, ws_bytes = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel())
+    at = every.data_ptr()
+    rc = lib.jgdpa_verify(target_probs.data_ptr(), ps, 1 if half else 0, _at(draft_probs), ds, 1 if draft_half else 0,
+                          tokens.data_ptr(), _at(parents), uniforms.data_ptr(), q_offsets.data_ptr(), batch, total, vocab,
+                          _at(kv_lens), _at(slots), at, at + 4 * batch, at + 4 * n,
+                          None if kv_lens is None else at + 8 * batch, None if slots is None else at + 4 * (n + total),
+                          ws, ws_bytes, raw)
+    if rc:
+        raise JgdpaError(rc, "jgdpa_verify")
+    return accepted, next_tokens, places, keep_lens, keep_slots
+
+
+# --------------------------------------------------------- the cache held in 4 bits
+def _page_stride4(t: torch.Tensor, align: int) -> int:
+    """Elements between the pages of a tensor [pages, heads, page, columns], 0 if
+    its pages are not contiguous inside, overlap, or lie no multiple of align apart."""
+    _, heads, page, columns = t.shape
+    size, stride = heads * page * columns, t.stride()
+    if any(n > 1 and a != b for n, a, b in zip((heads, page, columns), stride[1:], (page * columns, columns, 1))):
+        return 0
+    if t.shape[0] <= 1:
+        return size
+    return stride[0] if stride[0] >= size and stride[0] % align == 0 else 0
+
+
+def _cache4(k_codes, k_scales, v_codes, v_scales, index):
+    """(page strides of the four, pages, page size, heads, head dimension), None if something cannot be used."""
+    n, heads, page, half = shape = k_codes.shape
+    if not (index >= 0 and k_codes.dtype is _u8 and v_codes.dtype is _u8 and v_codes.shape == shape
+            and k_scales.dtype is _bf16 and v_scales.dtype is _bf16 and k_scales.shape == (n, heads, page, 2)
+            and v_scales.shape == k_scales.shape and v_codes.get_device() == index and k_scales.get_device() == index
+            and v_scales.get_device() == index):
+        return None
+    strides = (_page_stride4(k_codes, 16), _page_stride4(k_scales, 8), _page_stride4(v_codes, 16), _page_stride4(v_scales, 8))
+    return (strides, n, page, heads, 2 * half) if all(strides) else None
+
+
+def _refuse_cache4(k_codes, k_scales, v_codes, v_scales):
+    if not isinstance(k_codes, torch.Tensor) or k_codes.dim() != 4:
+        raise ValueError("k_codes must be a uint8 tensor [num_pages, kv_heads, page_size, head_dim / 2]")
+    device = k_codes.device
+    n, heads, page, half = k_codes.shape
+    _check(k_codes, "k_codes", torch.uint8, (None,) * 4)
+    _check(v_codes, "v_codes", torch.uint8, tuple(k_codes.shape), device)
+    _check(k_scales, "k_scales", torch.bfloat16, (n, heads, page, 2), device)
+    _check(v_scales, "v_scales", torch.bfloat16, (n, heads, page, 2), device)
+    for t, name, align in ((k_codes, "k_codes", 16), (k_scales, "k_scales", 8), (v_codes, "v_codes", 16), (v_scales, "v_scales", 8)):
+        if not _page_stride4(t, align):
+            raise ValueError(f"{name}: pages must be contiguous inside, must not overlap and lie a multiple of {align} "
+                             "elements apart")
+
+
+def _refuse_rows4(k, v, slots, names, k_codes):
+    heads, d, device = k_codes.shape[1], 2 * k_codes.shape[3], k_codes.device
+    _check(slots, "slots", torch.int32, (None,), device)
+    rows = slots.shape[0]
+    for t, name in zip((k, v), names):
+        if t is None and name.endswith("out"):
+            continue
+        _check(t, name, torch.bfloat16, (rows, heads, d), device)
+        _refuse_rows(t, name, heads, d)
+    _contiguous(slots=slots)
+    _need_cuda(k_codes)
+
+
+def jgdpa_cache4_append(k_new, v_new, slots, k_codes, k_scales, v_codes, v_scales, stream=None, lib=None):
+    """Writes rows of k_new / v_new [total_new, kv_heads, head_dim] to their slots
+    of a cache held in 4 bits: codes uint8 [num_pages, kv_heads, page_size, head_dim / 2],
+    scales bf16 [num_pages, kv_heads, page_size, 2]; returns the four."""
+    lib = lib or load()
+    got, ks, vs = None, 0, 0
+    try:
+        index = k_codes.get_device()
+        got = _cache4(k_codes, k_scales, v_codes, v_scales, index)
+        if got is not None:
+            strides, n, page, heads, d = got
+            rows = slots.shape[0]
+            shape = (rows, heads, d)
+            if (k_new.dtype is _bf16 and v_new.dtype is _bf16 and k_new.shape == shape and v_new.shape == shape
+                    and k_new.get_device() == index and v_new.get_device() == index and _is(slots, _i32, (rows,), index)):
+                ks, vs = _row_stride(k_new, heads, d), _row_stride(v_new, heads, d)
+    except (AttributeError, ValueError, IndexError, TypeError):
+        ks = 0
+    if not (ks and vs):
+        _refuse_cache4(k_codes, k_scales, v_codes, v_scales)
+        _refuse_rows4(k_new, v_new, slots, ("k_new", "v_new"), k_codes)
+        raise ValueError("jgdpa_cache4_append: unusable tensors")
+    if max(rows, n) > _I32_MAX:
+        _refuse_wide(**{"k_new's rows": rows, "k_codes' pages": n})
+    if index != torch.cuda.current_device():
+        return _on_other_device(jgdpa_cache4_append, k_codes.device, (k_new, v_new, slots, k_codes, k_scales, v_codes, v_scales,
+                                stream, lib), {})
+    rc = lib.jgdpa_cache4_append(k_new.data_ptr(), v_new.data_ptr(), ks, vs, slots.data_ptr(), rows, k_codes.data_ptr(),
+                                 k_scales.data_ptr(), v_codes.data_ptr(), v_scales.data_ptr(), *strides, n, page, heads, d,
+                                 _current_raw_stream(index) if stream is None else stream.cuda_stream)
+    if rc:
+        raise JgdpaError(rc, "jgdpa_cache4_append")
+    return k_codes, k_scales, v_codes, v_scales
+
+
+def jgdpa_cache4_read(k_codes, k_scales, v_codes, v_scales, slots, k_out=None, v_out=None, stream=None, lib=None):
+    """The rows at `slots` of a cache held in 4 bits, as bf16 (k, v)
+    [rows, kv_heads, head_dim]; zeros for slots outside the cache."""
+    lib = lib or load()
+    got, ks, vs = None, 0, 0
+    try:
+        index = k_codes.get_device()
+        got = _cache4(k_codes, k_scales, v_codes, v_scales, index)
+        if got is not None:
+            strides, n, page, heads, d = got
+            rows = slots.shape[0]
+            shape = (rows, heads, d)
+            if _is(slots, _i32, (rows,), index):
+                ks = vs = heads * d
+                if k_out is not None:
+                    ks = _row_stride(k_out, heads, d) if (k_out.dtype is _bf16 and k_out.shape == shape
+                                                          and k_out.get_device() == index) else 0
+                if v_out is not None:
+                    vs = _row_stride(v_out, heads, d) if (v_out.dtype is _bf16 and v_out.shape == shape
+                                                          and v_out.get_device() == index) else 0
+    except (AttributeError, ValueError, IndexError, TypeError):
+        ks = 0
+    if not (ks and vs):
+        _refuse_cache4(k_codes, k_scales, v_codes, v_scales)
+        _refuse_rows4(k_out, v_out, slots, ("k_out", "v_out"), k_codes)
+        raise ValueError("jgdpa_cache4_read: unusable tensors")
+    if max(rows, n) > _I32_MAX:
+        _refuse_wide(**{"slots": rows, "k_codes' pages": n})
+    if index != torch.cuda.current_device():
+        return _on_other_device(jgdpa_cache4_read, k_codes.device, (k_codes, k_scales, v_codes, v_scales, slots, k_out, v_out,
+                                stream, lib), {})
+    raw, alloc = _launch_on(stream, k_codes.device)
+    if k_out is None:
+        k_out = _empty_rows(k_codes, alloc, shape)
+    if v_out is None:
+        v_out = _empty_rows(k_codes, alloc, shape)
+    rc = lib.jgdpa_cache4_read(k_codes.data_ptr(), k_scales.data_ptr(), v_codes.data_ptr(), v_scales.data_ptr(), *strides, n,
+                               page, heads, d, slots.data_ptr(), rows, k_out.data_ptr(), v_out.data_ptr(), ks, vs, raw)
+    if rc:
+        raise JgdpaError(rc, "jgdpa_cache4_read")
+    return k_out, v_out
+
+
+def jgdpa_cache4_fwd_workspace_bytes(head_dim: int, lib=None) -> int:
+    _refuse_wide(head_dim=head_dim)
+    return int((lib or load()).jgdpa_cache4_fwd_workspace_bytes(head_dim))
+
+
+def _refuse_fwd4(q, k_codes, k_scales, v_codes, v_scales, block_table, q_offsets, kv_lens, softmax, bias_table, tree_mask,
+                 depths, out, lse, workspace):
+    _refuse_cache4(k_codes, k_scales, v_codes, v_scales)
+    d, device = 2 * k_codes.shape[3], k_codes.device
+    _check(q, "q", torch.bfloat16, (None, None, d), device)
+    total_q, heads = q.shape[0], q.shape[1]
+    _check(kv_lens, "kv_lens", torch.int32, (None,), device)
+    batch = kv_lens.shape[0]
+    _check(q_offsets, "q_offsets", torch.int32, (batch + 1,), device)
+    _check(block_table, "block_table", torch.int32, (batch, None), device)
+    _check(bias_table, "bias_table", torch.float32, (heads, None), device, optional=True)
+    _check(tree_mask, "tree_mask", torch.int32, (total_q, None), device, optional=True)
+    _check(depths, "depths", torch.int32, (total_q,), device, optional=True)
+    _check(out, "out", torch.bfloat16, (total_q, heads, d), device, optional=True)
+    if lse is not None and not softmax:
+        raise ValueError("lse is written in softmax mode only; pass None")
+    _check(lse, "lse", torch.float32, (heads, total_q), device, optional=True)
+    _check_bytes(workspace, "workspace", device)
+    for t, name in ((bias_table, "bias_table"), (tree_mask, "tree_mask")):
+        if t is not None and t.shape[1] == 0:
+            raise ValueError(f"{name} must have columns; pass None for none")
+    _refuse_rows(q, "q", heads, d)
+    _contiguous(block_table=block_table, q_offsets=q_offsets, kv_lens=kv_lens, bias_table=bias_table,
+                tree_mask=tree_mask, depths=depths, out=out, lse=lse, workspace=workspace)
+    _need_cuda(k_codes)
+
+
+def jgdpa_cache4_fwd(q, k_codes, k_scales, v_codes, v_scales, block_table, q_offsets, kv_lens, act, scale: float,
+                     max_q: int, bias_table=None, window: int = 0, tree_mask=None, depths=None, out=None, lse=None,
+                     workspace=None, stream=None, lib=None):
+    """jgdpa_cache_fwd over a cache held in 4 bits (jgdpa_cache4_fwd); returns
+    (out, lse) with lse None unless act == 'softmax'."""
+    lib = lib or load()
+    a = _act(act)
+    max_q, window = int(max_q), int(window)
+    if max(max_q, window) > _I32_MAX or min(max_q, window) < -_I32_MAX:
+        _refuse_wide(max_q=max_q, window=window)
+    softmax = a == 2
+    got, qs = None, 0
+    bias_len = words = 0
+    try:
+        index = k_codes.get_device()
+        got = _cache4(k_codes, k_scales, v_codes, v_scales, index)
+        if got is not None:
+            strides, n, page, kv_heads, d = got
+            total_q, heads, _ = shape = q.shape
+            batch, width = block_table.shape
+            ok = (q.dtype is _bf16 and shape[2] == d and q.get_device() == index
+                  and _is(block_table, _i32, (batch, width), index) and _is(q_offsets, _i32, (batch + 1,), index)
+                  and _is(kv_lens, _i32, (batch,), index))
+            if ok and bias_table is not None:
+                bias_len = bias_table.shape[1]
+                ok = bias_len > 0 and _is(bias_table, _f32, (heads, bias_len), index)
+            if ok and tree_mask is not None:
+                words = tree_mask.shape[1]
+                ok = words > 0 and _is(tree_mask, _i32, (total_q, words), index)
+            ok = ok and (depths is None or _is(depths, _i32, (total_q,), index))
+            ok = ok and (out is None or _is(out, _bf16, shape, index))
+            ok = ok and (lse is None or (softmax and _is(lse, _f32, (heads, total_q), index)))
+            ok = ok and (workspace is None or _is(workspace, _u8, (workspace.numel(),), index))
+            if ok:
+                qs = _row_stride(q, heads, d)
+    except (AttributeError, ValueError, IndexError, TypeError):
+        qs = 0
+    if not qs:
+        _refuse_fwd4(q, k_codes, k_scales, v_codes, v_scales, block_table, q_offsets, kv_lens, softmax, bias_table, tree_mask,
+                     depths, out, lse, workspace)
+        raise ValueError("jgdpa_cache4_fwd: unusable tensors")
+    if max(n, width, bias_len) > _I32_MAX:
+        _refuse_wide(**{"k_codes' pages": n, "block_table's width": width, "bias_table's length": bias_len})
+    if index != torch.cuda.current_device():
+        return _on_other_device(jgdpa_cache4_fwd, k_codes.device, (q, k_codes, k_scales, v_codes, v_scales, block_table,
+                                q_offsets, kv_lens, act, scale, max_q, bias_table, window, tree_mask, depths, out, lse,
+                                workspace, stream, lib), {})
+    device = k_codes.device
+    raw, alloc = _launch_on(stream, device)
+    if out is None:
+        out = torch.empty(shape, dtype=_bf16, device=device) if alloc is None else alloc(shape, _bf16)
+    if softmax and lse is None:
+        lse = torch.empty((heads, total_q), dtype=_f32, device=device) if alloc is None else alloc((heads, total_q), _f32)
+    if workspace is None:
+        nbytes = max(256, lib.jgdpa_cache4_fwd_workspace_bytes(d))
+        workspace = torch.empty(nbytes, dtype=_u8, device=device) if alloc is None else alloc(nbytes, _u8, result=False)
+    rc = lib.jgdpa_cache4_fwd(q.data_ptr(), qs, k_codes.data_ptr(), k_scales.data_ptr(), v_codes.data_ptr(),
+                              v_scales.data_ptr(), *strides, n, page, block_table.data_ptr(), width, q_offsets.data_ptr(),
+                              kv_lens.data_ptr(), batch, total_q, max_q, heads, kv_heads, d, a, float(scale), _at(bias_table),
+                              bias_len, window, _at(tree_mask), words, _at(depths), out.data_ptr(), _at(lse),
+                              workspace.data_ptr(), workspace.numel(), raw)
+    if rc:
+        raise JgdpaError(rc, "jgdpa_cache4_fwd")
     return out, lse

@@ -28,11 +28,12 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(BUILD, "libjgdpa.so")
 HEAD_DIMS = (32, 64, 128)
-SOURCES = ["api.cu", "sched.cu", "cache_api.cu", "cache_plan.cu"]  # compiled once
+SOURCES = ["api.cu", "sched.cu", "cache_api.cu", "cache_plan.cu", "step_api.cu", "rotate.cu", "verify.cu",
+           "cache4.cu"]  # compiled once
 # compiled once per head dimension, shared by both libraries
-PER_DIM_SHARED_SOURCES = ["cache_fwd.cu", "cache_fwd_wide.cu"]
+PER_DIM_SHARED_SOURCES = ["cache_fwd.cu", "cache_fwd_wide.cu", "cache4_fwd.cu"]
 PER_DIM_SOURCES = ["fwd.cu", "fwd_shortq.cu", "bwd.cu", "bwd_shortq.cu"]  # compiled once per head dimension and library
-HEADERS = ["act.cuh", "cache.cuh", "common.cuh", "host.h", "ptx.cuh"]
+HEADERS = ["act.cuh", "cache.cuh", "cache4.cuh", "common.cuh", "host.h", "ptx.cuh", "rotate.cuh", "verify.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
          "--expt-relaxed-constexpr"]

@@ -1,0 +1,177 @@
+// Writes rows of keys and values into a cache held in 4 bits, and reads them back.
+//
+// Of a token's head, with lo and hi its least and largest value:
+//
+//   s = bf16((hi - lo) / 15),  z = bf16(lo + 8 s),
+//   c = clamp(rint((x - z) / s), -8, 7) + 8       (s = 0: 8)
+//
+// in fp32, each operation rounded once (halves to even), so that the codes are
+// the same wherever they are formed.  A few operations per value: bound by HBM (2.5
+// bytes a value each way and 4 a head).  D / 16 lanes take a head, 16 columns each.
+#include <algorithm>
+
+#include "cache4.cuh"
+#include "common.cuh"
+#include "ptx.cuh"
+
+namespace jg {
+
+constexpr int kRows4Threads = 256;
+constexpr int kRows4Steps = 4;  // heads after one another
+
+__device__ __forceinline__ float min_nan(float a, float b) {
+  float y;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+  return y;
+}
+__device__ __forceinline__ uint4 ld_rows4(const void* p) {
+  uint4 v;
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p)
+               : "memory");
+  return v;
+}
+
+// The head of a row and where it lies in the cache.
+struct Rows4At {
+  uint32_t row, head;
+  int slot;  // or -1
+  int64_t page, place;
+  __device__ __forceinline__ Rows4At(const Cache4RowsParams& p, uint32_t vec) {
+    row = vec / static_cast<uint32_t>(p.heads);
+    head = vec - row * p.heads;
+    slot = row < static_cast<uint32_t>(p.rows) ? p.slots[row] : -1;
+    if (static_cast<uint32_t>(slot) >= static_cast<uint32_t>(p.slot_end)) slot = -1;
+    page = slot >> p.page_shift;
+    place = (static_cast<int64_t>(head) << p.page_shift) + (slot & ((1 << p.page_shift) - 1));
+  }
+};
+
+// blockIdx.y: K or V.
+template <int D>
+__global__ void __launch_bounds__(kRows4Threads) cache4_append_kernel(const __grid_constant__ Cache4RowsParams p, int steps) {
+  constexpr int L = D / 16, G = 32 / L;
+  cache_let_next();
+  cache_wait_before();
+  const int half = blockIdx.y, l = threadIdx.x % L;
+  const int64_t warp = static_cast<int64_t>(blockIdx.x) * (kRows4Threads / 32) + (threadIdx.x >> 5);
+  const uint32_t vec0 = static_cast<uint32_t>(warp) * (G * steps) + (threadIdx.x & 31) / L;
+  uint4 v[kRows4Steps][2];
+  int slot[kRows4Steps];
+#pragma unroll
+  for (int i = 0; i < kRows4Steps; ++i) {
+    slot[i] = -1;
+    v[i][0] = v[i][1] = make_uint4(0, 0, 0, 0);
+    if (i >= steps) continue;
+    const Rows4At at(p, vec0 + i * G);
+    slot[i] = at.slot;
+    if (at.row < static_cast<uint32_t>(p.rows)) {
+      const __nv_bfloat16* src = p.in[half] + at.row * p.stride[half] + at.head * D + 16 * l;
+      v[i][0] = ld_rows4(src);
+      v[i][1] = ld_rows4(src + 8);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < kRows4Steps; ++i) {
+    if (i >= steps) break;
+    float x[16];
+    const uint32_t w[8] = {v[i][0].x, v[i][0].y, v[i][0].z, v[i][0].w, v[i][1].x, v[i][1].y, v[i][1].z, v[i][1].w};
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      x[2 * e] = __uint_as_float(w[e] << 16);
+      x[2 * e + 1] = __uint_as_float(w[e] & 0xFFFF0000u);
+    }
+    float lo = x[0], hi = x[0];
+#pragma unroll
+    for (int e = 1; e < 16; ++e) {
+      lo = min_nan(lo, x[e]);
+      hi = max_nan(hi, x[e]);
+    }
+#pragma unroll
+    for (int o = L / 2; o; o >>= 1) {
+      lo = min_nan(lo, __shfl_xor_sync(0xffffffffu, lo, o));
+      hi = max_nan(hi, __shfl_xor_sync(0xffffffffu, hi, o));
+    }
+    const __nv_bfloat16 step = __float2bfloat16_rn(__fdiv_rn(__fsub_rn(hi, lo), 15.f));
+    const float s = __bfloat162float(step);
+    const __nv_bfloat16 middle = __float2bfloat16_rn(__fadd_rn(lo, 8.f * s));
+    const float z = __bfloat162float(middle);
+    uint32_t code[2] = {0, 0};
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+      const float q = s > 0.f ? __fdiv_rn(__fsub_rn(x[e], z), s) : 0.f;
+      const int c = static_cast<int>(fminf(fmaxf(rintf(q), -8.f), 7.f)) + 8;  // (NaN: the least)
+      code[e >> 3] |= static_cast<uint32_t>(c) << (4 * (e & 7));
+    }
+    if (slot[i] < 0) continue;
+    const Rows4At at(p, vec0 + i * G);
+    const Cache4& c = p.cache[half];
+    *reinterpret_cast<uint2*>(c.codes + at.page * c.code_stride + at.place * (D / 2) + 8 * l) = make_uint2(code[0], code[1]);
+    if (l == 0) {
+      __nv_bfloat162 pair;
+      pair.x = step;
+      pair.y = middle;
+      *reinterpret_cast<__nv_bfloat162*>(c.scales + at.page * c.scale_stride + at.place * 2) = pair;
+    }
+  }
+}
+
+template <int D>
+__global__ void __launch_bounds__(kRows4Threads) cache4_read_kernel(const __grid_constant__ Cache4RowsParams p, int steps) {
+  constexpr int L = D / 16, G = 32 / L;
+  cache_let_next();
+  cache_wait_before();
+  const int half = blockIdx.y, l = threadIdx.x % L;
+  const int64_t warp = static_cast<int64_t>(blockIdx.x) * (kRows4Threads / 32) + (threadIdx.x >> 5);
+  const uint32_t vec0 = static_cast<uint32_t>(warp) * (G * steps) + (threadIdx.x & 31) / L;
+  const Cache4& c = p.cache[half];
+  uint2 code[kRows4Steps];
+  uint32_t scale[kRows4Steps];
+#pragma unroll
+  for (int i = 0; i < kRows4Steps; ++i) {
+    code[i] = make_uint2(0, 0);
+    scale[i] = 0;
+    if (i >= steps) continue;
+    const Rows4At at(p, vec0 + i * G);
+    if (at.slot >= 0) {
+      code[i] = *reinterpret_cast<const uint2*>(c.codes + at.page * c.code_stride + at.place * (D / 2) + 8 * l);
+      scale[i] = *reinterpret_cast<const uint32_t*>(c.scales + at.page * c.scale_stride + at.place * 2);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < kRows4Steps; ++i) {
+    if (i >= steps) break;
+    const Rows4At at(p, vec0 + i * G);
+    if (at.row >= static_cast<uint32_t>(p.rows)) continue;
+    const float s = __uint_as_float(scale[i] << 16), z = __uint_as_float(scale[i] & 0xFFFF0000u);
+    uint32_t w[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const uint32_t two = (e < 4 ? code[i].x : code[i].y) >> (8 * (e & 3));
+      const float a = static_cast<float>(static_cast<int>(two & 15) - 8), b = static_cast<float>(static_cast<int>((two >> 4) & 15) - 8);
+      // (the product has 12 bits: the sum is rounded to fp32, then to bf16)
+      w[e] = pack_bf16(__fmaf_rn(s, a, z), __fmaf_rn(s, b, z));
+    }
+    __nv_bfloat16* dst = p.out[half] + at.row * p.stride[half] + at.head * D + 16 * l;
+    *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
+    *reinterpret_cast<uint4*>(dst + 8) = make_uint4(w[4], w[5], w[6], w[7]);
+  }
+}
+
+template <int D>
+static cudaError_t launch_rows4(const Cache4RowsParams& p, bool append, int sms, cudaStream_t stream) {
+  constexpr int G = 512 / D;  // heads side by side in a warp
+  const int64_t vecs = static_cast<int64_t>(p.rows) * p.heads;
+  const int steps = vecs >= static_cast<int64_t>(sms) * 8 * G * kRows4Steps ? kRows4Steps : 1;  // (K and V: two CTAs per SM)
+  const int64_t per_cta = static_cast<int64_t>(kRows4Threads / 32) * G * steps;
+  return cache_launch(append ? cache4_append_kernel<D> : cache4_read_kernel<D>,
+                      dim3(static_cast<unsigned>((vecs + per_cta - 1) / per_cta), 2, 1), kRows4Threads, 0, stream, p, steps);
+}
+cudaError_t launch_cache4_rows(const Cache4RowsParams& p, int head_dim, bool append, int sms, cudaStream_t stream) {
+  return head_dim == 128  ? launch_rows4<128>(p, append, sms, stream)
+         : head_dim == 64 ? launch_rows4<64>(p, append, sms, stream)
+                          : launch_rows4<32>(p, append, sms, stream);
+}
+
+}  // namespace jg

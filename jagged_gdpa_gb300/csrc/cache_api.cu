@@ -22,16 +22,7 @@ template <int D>
 cudaError_t launch_cache_join_d(const CacheFwdParams& p, int act, int n_ctas, int tile_rows, cudaStream_t stream);
 cudaError_t launch_cache_plan(const CachePlanParams& p, int sms, cudaStream_t stream);
 cudaError_t launch_cache_append(const CacheAppendParams& p, cudaStream_t stream);
-}  // namespace jg
 
-namespace {
-
-constexpr size_t kAlign = 256;
-constexpr int64_t kMaxTokens = INT32_MAX - 1024;  // so that a tile's last key is an int32, too
-size_t up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
-bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
-
-// log2 of an accepted page size (a power of two, 16 to 1024 tokens), or -1.
 int page_shift_of(int32_t page_size) {
   for (int s = 4; s <= 10; ++s)
     if (page_size == 1 << s) return s;
@@ -48,10 +39,21 @@ jgdpa_status check_cache(const void* k_cache, const void* v_cache, int64_t k_pag
   const int64_t page = static_cast<int64_t>(page_size) * kv_heads * head_dim;
   if (k_page_stride < page || v_page_stride < page) return JGDPA_ERR_INVALID_ARGUMENT;
   if (k_page_stride >= (int64_t{1} << 39) || v_page_stride >= (int64_t{1} << 39)) return JGDPA_ERR_UNSUPPORTED;
-  if (!aligned(k_cache, 16) || !aligned(v_cache, 16) || k_page_stride % 8 || v_page_stride % 8)
+  if (reinterpret_cast<uintptr_t>(k_cache) % 16 || reinterpret_cast<uintptr_t>(v_cache) % 16 || k_page_stride % 8 ||
+      v_page_stride % 8)
     return JGDPA_ERR_MISALIGNED;
   return JGDPA_OK;
 }
+}  // namespace jg
+
+namespace {
+
+constexpr size_t kAlign = 256;
+using jg::check_cache;
+using jg::kMaxTokens;
+using jg::page_shift_of;
+size_t up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
+bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
 struct CacheLayout {
   size_t err, join, part_ml, part_o, total;
