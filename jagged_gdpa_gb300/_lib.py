@@ -643,7 +643,6 @@ def _refuse_append(k_new, v_new, slots, k_cache, v_cache):
     _refuse_rows(k_new, "k_new", heads, d)
     _refuse_rows(v_new, "v_new", heads, d)
     _contiguous(slots=slots)
-    _need_cuda(k_cache)
 
 
 def jgdpa_cache_append(k_new, v_new, slots, k_cache, v_cache, stream=None, lib=None):
@@ -666,6 +665,7 @@ def jgdpa_cache_append(k_new, v_new, slots, k_cache, v_cache, stream=None, lib=N
         pass
     if not (ks and vs and kps and vps):
         _refuse_append(k_new, v_new, slots, k_cache, v_cache)
+        _need_cuda(k_cache)
         raise ValueError("jgdpa_cache_append: unusable tensors")
     if max(rows, n) > _I32_MAX:
         _refuse_wide(**{"k_new's rows": rows, "k_cache's pages": n})
@@ -1099,6 +1099,7 @@ def jgdpa_cache_append_rotated(q, k_new, v_new, slots, k_cache, v_cache, q_offse
     if not ok:
         _refuse_append_rotated(q, k_new, v_new, slots, k_cache, v_cache, q_offsets, kv_lens, inv_freq, q_weight, k_weight, eps,
                                interleaved, depths, q_out, workspace)
+        _need_cuda(k_cache)
         raise ValueError("jgdpa_cache_append_rotated: unusable tensors")
     if max(rows, n) > _I32_MAX:
         _refuse_wide(**{"k_new's rows": rows, "k_cache's pages": n})
