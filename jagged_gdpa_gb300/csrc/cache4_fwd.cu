@@ -6,24 +6,35 @@
 // joined as in the bf16 kernel (cache.cuh, cache_fwd.cu).  With a key's step s,
 // middle z and codes c,
 //
-//   x = scale (s <q, c - 8> + z sum q),   O = sum_j (P_j s_j) (c_j - 8) + sum_j P_j z_j
+//   x = scale (s <q, c> + (z - 8 s) sum q),   O = sum_j (P_j s_j) (c_j - 8) + sum_j P_j z_j
 //
-// so that the products take the codes themselves, small whole numbers that bf16
-// holds exactly, and steps and middles enter in fp32: no value of the cache is
+// so that the products take the codes themselves, small whole numbers that 16-bit
+// types hold exactly, and steps and middles enter in fp32: no value of the cache is
 // rounded again, and what a masked place holds (its codes are always finite)
 // never meets a row that does not see it.
 //
-// Bytes per key and head are D + 8 instead of the bf16 cache's 4 D, and what a
-// byte costs in instructions counts: 5 per 2 codes (a shift, a mask, a
-// subtraction, their share of the products).  Every warp works by itself, on blocks of 32 keys
+// Bytes per key and head are D + 8 instead of the bf16 cache's 4 D, so what a
+// byte costs in instructions counts.
+//   S^T = K Q^T and O^T += V^T P^T: the cache is the operand of 16 rows, the
+//     query rows the one of 8 columns, one set of them (up to 8 rows) or two; with the rows on the
+//     side of 16, as in the bf16 kernel, a single token's 4 heads took twice the
+//     products and twice the work on scores.
+//   K is fp16: a nibble in the last four bits, or the next four, of a half is
+//     2^-24 c or 2^-20 c, a subnormal that takes no instruction but a mask.  Q follows: a row
+//     times the power of two that brings its largest value to 2^14 (what falls
+//     below fp16 then is 2^-38 of that), the columns of high nibbles times 2^-4 more.
+//   V is bf16, as P has its range: 128 + c is 128's bits with c in its last four, less 136.
+// Every warp works by itself, on blocks of 32 keys
 // that it copies (cp.async) into a ring of its own, a few blocks ahead: no
 // barrier but an item's end.  The order of columns within a product and of keys within
 // a block is free, so both are chosen such that a lane's codes come in one load
 // per key and turn into operands by shifts and masks:
-//   K: key n of a product of 8 is key (n / 2) + 4 (n % 2), and lane t of a key's
+//   K: row n of 8 of a product is key (n / 2) + 4 (n % 2), and lane t of a key's
 //      four takes columns D / 4 t and on; nibbles i and i + 4 of a word side by side
 //   V: lane g of a key's eight takes columns D / 8 g and on; two keys' words are
 //      put together by halves, nibble i of both side by side.
+#include <cuda_fp16.h>
+
 #include "act.cuh"
 #include "cache4.cuh"
 #include "common.cuh"
@@ -37,18 +48,17 @@ constexpr int kC4Warps = 4;
 constexpr int kC4Rows = kCache4Rows;
 constexpr int kC4MinRange = 5;  // the least length of a range
 
-template <int D>
+template <int D, int NQ>
 struct C4Cfg {
   static constexpr int kRow = D / 2;  // bytes of a key's codes
   static constexpr int kCodes = kC4Block * kRow;
   static constexpr int kStage = 2 * kCodes + 2 * kC4Block * 4;  // codes of K and V, scales of K and V
-  static constexpr int kStages = D == 128 ? 4 : D == 64 ? 5 : 6;
+  static constexpr int kStages = D == 128 ? (NQ == 1 ? 3 : 4) : D == 64 ? 5 : 6;
   static constexpr int kRing = kStage * kStages > kC4Rows * D * 4 ? kStage * kStages : kC4Rows * D * 4;  // (O meets there)
   static constexpr int kSmem = kC4Warps * kRing;
-  static_assert(kSmem <= 233472 / cache4_ctas(D) - 2048, "shared memory per CTA");
+  static_assert(kSmem <= 233472 / cache4_ctas(D, NQ) - 2048, "shared memory per CTA");
 };
 
-template <int D>
 struct C4Shared {
   CacheRangeShared range;
   float2 ml[kC4Warps][kC4Rows];
@@ -63,14 +73,25 @@ template <int N>
 __device__ __forceinline__ void c4_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
-__device__ __forceinline__ void c4_mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+__device__ __forceinline__ void c4_mma_k(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void c4_mma_v(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm volatile(
       "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-// Nibble 0 of both halves of w as a bf16 pair, less 8: 128 + c is the bits of
-// 128 with c in its last four.
+// The warp's 8 x 8 matrix of 16-bit values, rows to columns.
+__device__ __forceinline__ uint32_t c4_transpose(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+// Nibble 0 of both halves of w as a bf16 pair, less 8.
 __device__ __forceinline__ uint32_t c4_pair(uint32_t w) {
   const uint32_t v = (w & 0x000F000Fu) | 0x43004300u;
   uint32_t y;
@@ -89,24 +110,30 @@ __device__ __forceinline__ float2 c4_scale(uint32_t addr) {  // step, middle
   asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w) : "r"(addr) : "memory");
   return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
 }
-// Where four columns of O's row lie in a warp's part of shared memory (no bank
-// conflicts, neither as the fragments are written nor as the rows are read).
+__device__ __forceinline__ uint32_t c4_half2(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+// Where four columns of O's row lie in a warp's part of shared memory: no bank
+// conflicts, neither as the fragments are written (8 lanes: 4 rows 2 apart, 2
+// places D / 32 apart) nor as rows are read.
 template <int D>
 __device__ __forceinline__ int c4_place(int row, int q4) {
-  const int x = D == 128 ? (q4 >> 3) | ((row & 1) << 2) : D == 64 ? ((q4 >> 3) & 1) | ((row & 1) << 1) : row & 1;
-  return row * (D / 4) + (q4 ^ x);
+  const int t = (row >> 1) & 3;
+  return row * (D / 4) + (q4 ^ (D == 128 ? t : D == 64 ? (t & 1) | ((t & 2) << 1) : t << 1));
 }
 
-template <int D, int ACT>
-__global__ void __launch_bounds__(kC4Warps * 32, cache4_ctas(D)) cache4_fwd_kernel(const __grid_constant__ Cache4FwdParams pp) {
-  using C = C4Cfg<D>;
+// NQ: columns of query rows, by 8.
+template <int D, int ACT, int NQ>
+__global__ void __launch_bounds__(kC4Warps * 32, cache4_ctas(D, NQ)) cache4_fwd_kernel(const __grid_constant__ Cache4FwdParams pp) {
+  using C = C4Cfg<D, NQ>;
   constexpr int WK = D / 32;      // words of K's codes of a lane and key
   constexpr int KS = D / 16;      // k steps of S
-  constexpr int NT = D / 8;       // n tiles of O
-  constexpr int kTiles = kC4Block / 8;
+  constexpr int MT = D / 16;      // tiles of 16 columns of O
+  constexpr int R2 = 2 * NQ;      // a lane's query rows: 2 tig + (i % 2) + 8 (i / 2)
   const CacheFwdParams& p = pp.f;
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ C4Shared<D> sh;
+  __shared__ C4Shared sh;
   cache_let_next();
   cache_wait_before();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, tig = lane & 3;
@@ -119,6 +146,7 @@ __global__ void __launch_bounds__(kC4Warps * 32, cache4_ctas(D)) cache4_fwd_kern
   // scores in log2 units, or halved as cc_act2 takes them
   constexpr float kUnit = ACT == 2 ? kLog2e : 0.5f;
   const float scale = ACT == 2 ? p.scale : 0.5f * p.scale;
+  const int page_mask = (1 << p.page_shift) - 1;
 
   CacheWalk w;
   w.init(R);
@@ -143,34 +171,40 @@ __global__ void __launch_bounds__(kC4Warps * 32, cache4_ctas(D)) cache4_fwd_kern
       }
       return id;
     };
+    // A block's copies: a half of 16 keys lies in one page, side by side.
+    constexpr int kPieces = C::kRow / 16;                   // of a key
+    constexpr int kHalf = 16 * kPieces;                     // of 16 keys' codes
+    constexpr int kEach = kHalf >= 32 ? kHalf / 32 : 1;     // of them a lane's
+    const int c_key = lane / kPieces, c_piece = lane % kPieces;  // (with kHalf = 16 lanes 16 and on take the second half)
     auto copy = [&](int block, int id, int stage) {  // (the whole warp)
-      const int id0 = __shfl_sync(0xffffffffu, id, 0), id1 = __shfl_sync(0xffffffffu, id, 1);
       if (block < blocks_end) {
-        const int mask = (1 << p.page_shift) - 1, first = block * kC4Block;
         const uint32_t to = ring + stage * C::kStage;
-        auto where = [&](int key, int& page) {  // place in the head's part of a page
-          page = key < 16 ? id0 : id1;
-          return (static_cast<int64_t>(w.h) << p.page_shift) + ((first + key) & mask);
-        };
-        constexpr int kPieces = C::kRow / 16;  // of a key
+        const int first = block * kC4Block;
 #pragma unroll
-        for (int i = 0; i < kPieces; ++i) {
-          const int key = (i * 32 + lane) / kPieces, c = lane % kPieces;
-          int page;
-          const int64_t at = where(key, page) * C::kRow + 16 * c;
+        for (int half = 0; half < (kHalf >= 32 ? 2 : 1); ++half) {
+          const int h = kHalf >= 32 ? half : lane >> 4;
+          const int page = __shfl_sync(0xffffffffu, id, h);
           const bool live = page >= 0;
           const int64_t pg = live ? page : 0;
-          // K's keys in the order of their products, V's pieces turned by key
-          const int n = (key & ~7) | ((key & 3) << 1) | ((key >> 2) & 1);
-          c4_copy(to + n * C::kRow + 16 * c, pp.k.codes + pg * pp.k.code_stride + at, live);
-          const int cv = D == 128 ? c ^ (key & 2) : c;
-          c4_copy(to + C::kCodes + key * C::kRow + 16 * cv, pp.v.codes + pg * pp.v.code_stride + at, live);
+          const int64_t at = ((static_cast<int64_t>(w.h) << p.page_shift) + ((first + 16 * h) & page_mask)) * C::kRow +
+                             16 * (kHalf >= 32 ? lane : lane & 15);
+          const uint8_t* ks = pp.k.codes + pg * pp.k.code_stride + at;
+          const uint8_t* vs = pp.v.codes + pg * pp.v.code_stride + at;
+#pragma unroll
+          for (int i = 0; i < kEach; ++i) {
+            const int key = (kHalf >= 32 ? 16 * half : 0) + i * (32 / kPieces) + c_key;
+            // K's keys in the order of their products, V's pieces turned by key
+            const int n = (key & ~7) | ((key & 3) << 1) | ((key >> 2) & 1);
+            const int cv = D == 128 ? c_piece ^ (key & 2) : c_piece;
+            c4_copy(to + n * C::kRow + 16 * c_piece, ks + 512 * i, live);
+            c4_copy(to + C::kCodes + key * C::kRow + 16 * cv, vs + 512 * i, live);
+          }
         }
-        if (lane < 16) {  // four keys' scales each
-          const int key = (lane & 7) * 4;
+        // four keys' scales each: lanes 0 to 7 K's, 8 to 15 V's
+        const int key = (lane & 7) * 4, page = __shfl_sync(0xffffffffu, id, (lane >> 2) & 1);
+        if (lane < 16) {
           const Cache4& c = lane < 8 ? pp.k : pp.v;
-          int page;
-          const int64_t at = where(key, page) * 2;
+          const int64_t at = ((static_cast<int64_t>(w.h) << p.page_shift) + ((first + key) & page_mask)) * 2;
           const bool live = page >= 0;
           c4_copy(to + 2 * C::kCodes + lane * 16, c.scales + (live ? page : 0) * c.scale_stride + at, live);
         }
@@ -187,62 +221,98 @@ __global__ void __launch_bounds__(kC4Warps * 32, cache4_ctas(D)) cache4_fwd_kern
     }
 
     const int n_rows = min(kC4Rows, r.T * p.group - w.row_tile * kC4Rows);
-    CcRow rows[2];  // g and g + 8
-    const __nv_bfloat16* qrow[2];
-    float far_bias[2];
-    int pos_min = INT32_MAX;
+    CcRow rows[R2];
+    float far_bias[R2];
+    int pos_min = INT32_MAX, pos_max = 0;
+    bool hides = false;  // some row's bias hides all far keys, or is beyond what log2 units hold
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int lr = g + 8 * i, flat = w.row_tile * kC4Rows + lr;
+    for (int i = 0; i < R2; ++i) {
+      const int lr = 2 * tig + (i & 1) + 8 * (i >> 1), flat = w.row_tile * kC4Rows + lr;
       CcRow& q = rows[i];
       const int t = static_cast<uint32_t>(flat) / static_cast<uint32_t>(p.group);
       q.t = lr < n_rows ? t : -1;
       q.head = w.h * p.group + (lr < n_rows ? flat - t * p.group : 0);
       q.pos = r.C;
       q.far_bias = 0.f;
-      qrow[i] = nullptr;
+      far_bias[i] = 0.f;
       if (q.t >= 0) {
         q.pos = cc_row_pos(p, r, q.t, status);
-        qrow[i] = p.q + static_cast<int64_t>(r.q0 + q.t) * p.q_stride + static_cast<int64_t>(q.head) * D;
         pos_min = min(pos_min, q.pos);
+        pos_max = max(pos_max, q.pos);
+        if (p.bias_len) far_bias[i] = __ldg(p.bias + static_cast<int64_t>(q.head) * p.bias_len + 2 * reach) * kUnit;
       }
-      far_bias[i] = 0.f;
-      if (q.t >= 0 && p.bias_len)
-        far_bias[i] = __ldg(p.bias + static_cast<int64_t>(q.head) * p.bias_len + 2 * reach) * kUnit;
+      hides = hides || (ACT == 2 && fabsf(far_bias[i]) > kHugeScore);
     }
-    // some row's bias hides all far keys, or is beyond what log2 units hold
-    const bool hides = ACT == 2 && __any_sync(0xffffffffu, fabsf(far_bias[0]) > kHugeScore || fabsf(far_bias[1]) > kHugeScore);
+    hides = __any_sync(0xffffffffu, hides);
     pos_min = __reduce_min_sync(0xffffffffu, pos_min);
-    const int pos_max = __reduce_max_sync(0xffffffffu, max(rows[0].t >= 0 ? rows[0].pos : 0, rows[1].t >= 0 ? rows[1].pos : 0));
-    // Q's fragments in the order of K's nibbles, and its sums
-    uint32_t qa[KS][4];
-    float q_sum[2] = {0.f, 0.f};
+    pos_max = __reduce_max_sync(0xffffffffu, pos_max);
+    // Q's fragments (query row g + 8 n) in the order of K's nibbles, and what a lane's rows (2 tig ..) need of it
+    uint32_t qb[NQ][KS][2];
+    float q_sum[R2], q_unit[R2];  // sum q, and what brings <q, c> back
 #pragma unroll
-    for (int j = 0; j < WK; ++j)
+    for (int n = 0; n < NQ; ++n) {
+      const int lr = g + 8 * n, flat = w.row_tile * kC4Rows + lr, t = static_cast<uint32_t>(flat) / static_cast<uint32_t>(p.group);
+      const __nv_bfloat16* src = p.q + static_cast<int64_t>(r.q0 + t) * p.q_stride +
+                                 static_cast<int64_t>(w.h * p.group + flat - t * p.group) * D + (D / 4) * tig;
+      uint4 v[WK];
+      float sum = 0.f, top = 0.f;
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        uint4 v = make_uint4(0, 0, 0, 0);
-        if (qrow[i] != nullptr) v = *reinterpret_cast<const uint4*>(qrow[i] + (D / 4) * tig + 8 * j);
-        const uint32_t x[4] = {v.x, v.y, v.z, v.w};  // columns 2 e, 2 e + 1
+      for (int j = 0; j < WK; ++j) {
+        v[j] = make_uint4(0, 0, 0, 0);
+        if (lr < n_rows) v[j] = *reinterpret_cast<const uint4*>(src + 8 * j);
+        const uint32_t x[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
 #pragma unroll
-        for (int e = 0; e < 4; ++e) q_sum[i] += __uint_as_float(x[e] << 16) + __uint_as_float(x[e] & 0xFFFF0000u);
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {  // columns 2 h and 2 h + 4, 2 h + 1 and 2 h + 5
-          qa[2 * j + h][i] = __byte_perm(x[h], x[h + 2], 0x5410);
-          qa[2 * j + h][2 + i] = __byte_perm(x[h], x[h + 2], 0x7632);
+        for (int e = 0; e < 4; ++e) {
+          const float a = __uint_as_float(x[e] << 16), b = __uint_as_float(x[e] & 0xFFFF0000u);
+          sum += a + b;
+          top = fmaxf(top, fmaxf(fabsf(a), fabsf(b)));
         }
       }
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      q_sum[i] += __shfl_xor_sync(0xffffffffu, q_sum[i], 1);
-      q_sum[i] += __shfl_xor_sync(0xffffffffu, q_sum[i], 2);
+      for (int o = 1; o < 4; o <<= 1) {
+        sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+      }
+      // 2^e <= top < 2^(e + 1): the row times 2^(14 - e), in two factors that fp32 holds
+      const int e = top > 0.f ? max(static_cast<int>(__float_as_uint(top) >> 23) - 127, -124) : 0;
+      const int up = min(14 - e, 123);
+      const float f0 = __uint_as_float(static_cast<uint32_t>(up + 127) << 23), f1 = __uint_as_float(static_cast<uint32_t>(14 - e - up + 127) << 23);
+#pragma unroll
+      for (int j = 0; j < WK; ++j) {
+        const uint32_t x[4] = {v[j].x, v[j].y, v[j].z, v[j].w};  // columns 2 e, 2 e + 1
+        float y[8];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          y[2 * c] = __uint_as_float(x[c] << 16) * f0 * f1;
+          y[2 * c + 1] = __uint_as_float(x[c] & 0xFFFF0000u) * f0 * f1 * 0.0625f;
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {  // columns 2 h and 2 h + 4, 2 h + 1 and 2 h + 5
+          qb[n][2 * j + h][0] = c4_half2(y[2 * h], y[2 * h + 4]);
+          qb[n][2 * j + h][1] = c4_half2(y[2 * h + 1], y[2 * h + 5]);
+        }
+      }
+      // 2^24 of the codes (half of it with the step) and 2^(e - 14) of the row; lane 4 (2 tig + i) has row 2 tig + i
+      const float back = __uint_as_float(static_cast<uint32_t>(12 + e - 14 + 127) << 23);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        q_sum[2 * n + i] = __shfl_sync(0xffffffffu, sum, 4 * (2 * tig + i));
+        q_unit[2 * n + i] = __shfl_sync(0xffffffffu, back, 4 * (2 * tig + i));
+      }
     }
-    float o[NT][4];
+    float o[NQ][MT][4];
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
+    for (int n = 0; n < NQ; ++n)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) o[nt][e] = 0.f;
-    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f}, pz[2] = {0.f, 0.f};  // pz: sum P z
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[n][mt][e] = 0.f;
+    float m[R2], l[R2], pz[R2];  // pz: sum P z
+#pragma unroll
+    for (int i = 0; i < R2; ++i) {
+      m[i] = -INFINITY;
+      l[i] = pz[i] = 0.f;
+    }
 
     int stage = 0;
 #pragma unroll 1
@@ -253,153 +323,177 @@ __global__ void __launch_bounds__(kC4Warps * 32, cache4_ctas(D)) cache4_fwd_kern
       const int key0 = kb * kC4Block;
       const bool far = p.bias_len == 0 || (!hides && key0 + kC4Block - 1 < r.C && pos_min - (key0 + kC4Block - 1) >= reach);
       bool plain = key0 + kC4Block - 1 < r.C && (p.window <= 0 || pos_max - key0 < p.window);
-      // lane's columns: keys key0 + col(tile, e)
-      auto col = [&](int nt, int e) { return 8 * nt + tig + 4 * e; };
-      uint32_t see[2] = {0xFFFFFFFFu, 0xFFFFFFFFu};
+      // a lane's keys: of the two of every 16, e = 0 and 1
+      const int own = (g >> 1) + 4 * (g & 1);
+      auto key_of = [&](int kk, int e) { return 16 * kk + 8 * e + own; };
+      uint32_t see[R2];
+#pragma unroll
+      for (int i = 0; i < R2; ++i) see[i] = 0xFFFFFFFFu;
       if (!plain) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          uint32_t bits = cc_vis32(p, r, rows[h], key0);
+        for (int i = 0; i < R2; ++i) {
+          uint32_t bits = cc_vis32(p, r, rows[i], key0);
           if (p.window > 0) {
             uint32_t near = 0;
             if (cc_in_order(p, r, key0)) {
-              near = cc_near32(p, rows[h].pos, key0);
+              near = cc_near32(p, rows[i].pos, key0);
             } else {
 #pragma unroll 1
-              for (int c = 0; c < 2 * kTiles; ++c) {
-                const int at = col(c >> 1, c & 1);
-                near |= (cc_near(p, rows[h].pos, cc_pos(p, r, key0 + at)) ? 1u : 0u) << at;
+              for (int c = 0; c < 4; ++c) {
+                const int at = key_of(c >> 1, c & 1);
+                near |= (cc_near(p, rows[i].pos, cc_pos(p, r, key0 + at)) ? 1u : 0u) << at;
               }
             }
-            bits &= near;  // (only this lane's columns are kept)
+            bits &= near;  // (only this lane's keys are kept)
           }
-          see[h] = bits;
+          see[i] = bits;
         }
       }
-      float s[kTiles][4];
+      // S^T: s[n][kk][2 e + i] is key_of(kk, e) with row 2 n + i
+      float s[NQ][2][4];
 #pragma unroll
-      for (int nt = 0; nt < kTiles; ++nt) {
+      for (int kk = 0; kk < 2; ++kk) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) s[nt][e] = 0.f;
-        uint32_t word[WK];
-        c4_words<WK>(kt + (8 * nt + g) * C::kRow + tig * (4 * WK), word);
+        for (int n = 0; n < NQ; ++n)
 #pragma unroll
-        for (int j = 0; j < WK; ++j) {
-          c4_mma(s[nt], qa[2 * j], c4_pair(word[j]), c4_pair(word[j] >> 4));
-          c4_mma(s[nt], qa[2 * j + 1], c4_pair(word[j] >> 8), c4_pair(word[j] >> 12));
-        }
+          for (int e = 0; e < 4; ++e) s[n][kk][e] = 0.f;
+        uint32_t word[2][WK];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) c4_words<WK>(kt + (16 * kk + 8 * e + g) * C::kRow + tig * (4 * WK), word[e]);
+#pragma unroll
+        for (int j = 0; j < WK; ++j)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const uint32_t x = word[0][j] >> (8 * h), y = word[1][j] >> (8 * h);
+            const uint32_t a[4] = {x & 0x000F000Fu, y & 0x000F000Fu, x & 0x00F000F0u, y & 0x00F000F0u};
+#pragma unroll
+            for (int n = 0; n < NQ; ++n) c4_mma_k(s[n][kk], a, qb[n][2 * j + h][0], qb[n][2 * j + h][1]);
+          }
       }
 #pragma unroll
-      for (int nt = 0; nt < kTiles; ++nt)
+      for (int kk = 0; kk < 2; ++kk)
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          const float2 k = c4_scale(ks + 4 * col(nt, c));
-          const float step = k.x * scale, middle = k.y * scale;
+        for (int e = 0; e < 2; ++e) {
+          const float2 k = c4_scale(ks + 4 * key_of(kk, e));
+          const float step = k.x * (4096.f * scale), middle = __fmaf_rn(-8.f, k.x, k.y) * scale;
 #pragma unroll
-          for (int h = 0; h < 2; ++h)
-            s[nt][2 * h + c] = __fmaf_rn(s[nt][2 * h + c], step, __fmaf_rn(middle, q_sum[h], far ? far_bias[h] : 0.f));
+          for (int i = 0; i < R2; ++i) {
+            float& x = s[i >> 1][kk][2 * e + (i & 1)];
+            x = __fmaf_rn(x * q_unit[i], step, __fmaf_rn(middle, q_sum[i], far ? far_bias[i] : 0.f));
+          }
         }
       if (!far) {
         float top = 0.f;
 #pragma unroll
-        for (int nt = 0; nt < kTiles; ++nt)
+        for (int kk = 0; kk < 2; ++kk)
 #pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            const int key_pos = cc_pos(p, r, key0 + col(nt, c));
+          for (int e = 0; e < 2; ++e) {
+            const int key_pos = cc_pos(p, r, key0 + key_of(kk, e));
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const float bias = cc_bias(p, rows[h], reach, key_pos);
-              s[nt][2 * h + c] = __fmaf_rn(bias, kUnit, s[nt][2 * h + c]);
+            for (int i = 0; i < R2; ++i) {
+              const float bias = cc_bias(p, rows[i], reach, key_pos);
+              float& x = s[i >> 1][kk][2 * e + (i & 1)];
+              x = __fmaf_rn(bias, kUnit, x);
               if constexpr (ACT == 2) top = fmaxf(top, fabsf(bias));
             }
           }
         if (ACT == 2 && __any_sync(0xffffffffu, top > kHugeBias)) {
           plain = false;
 #pragma unroll
-          for (int nt = 0; nt < kTiles; ++nt)
+          for (int kk = 0; kk < 2; ++kk)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const int h = e >> 1, at = col(nt, e & 1);
-              const float bias = cc_bias(p, rows[h], reach, cc_pos(p, r, key0 + at));
-              if (bias == -INFINITY) see[h] &= ~(1u << at);
-              else if (fabsf(bias) > kHugeBias && s[nt][e] == s[nt][e]) s[nt][e] = cc_huge(bias);
-            }
+            for (int e = 0; e < 2; ++e)
+#pragma unroll
+              for (int i = 0; i < R2; ++i) {
+                const int at = key_of(kk, e);
+                const float bias = cc_bias(p, rows[i], reach, cc_pos(p, r, key0 + at));
+                float& x = s[i >> 1][kk][2 * e + (i & 1)];
+                if (bias == -INFINITY) see[i] &= ~(1u << at);
+                else if (fabsf(bias) > kHugeBias && x == x) x = cc_huge(bias);
+              }
         }
       }
       if (!plain) {
 #pragma unroll
-        for (int nt = 0; nt < kTiles; ++nt)
+        for (int kk = 0; kk < 2; ++kk)
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            if (!((see[e >> 1] >> col(nt, e & 1)) & 1)) s[nt][e] = ACT == 2 ? -INFINITY : 0.f;  // act(0) = 0
+          for (int e = 0; e < 2; ++e)
+#pragma unroll
+            for (int i = 0; i < R2; ++i)
+              if (!((see[i] >> key_of(kk, e)) & 1)) s[i >> 1][kk][2 * e + (i & 1)] = ACT == 2 ? -INFINITY : 0.f;  // act(0) = 0
       }
       if constexpr (ACT == 2) {
         // m: within 8 (log2 units) of the maximum or above, as in the bf16 kernel
-        float mx[2] = {-INFINITY, -INFINITY};
+        float mx[R2];
+        bool over = false;
 #pragma unroll
-        for (int nt = 0; nt < kTiles; ++nt)
+        for (int i = 0; i < R2; ++i) {
+          const int n = i >> 1, c = i & 1;
+          mx[i] = fmaxf(fmaxf(s[n][0][c], s[n][0][2 + c]), fmaxf(s[n][1][c], s[n][1][2 + c]));
+          over = over || mx[i] > m[i] + 8.f;
+        }
+        if (__any_sync(0xffffffffu, over)) {
 #pragma unroll
-          for (int i = 0; i < 2; ++i) mx[i] = fmaxf(mx[i], fmaxf(s[nt][2 * i], s[nt][2 * i + 1]));
-        if (__any_sync(0xffffffffu, mx[0] > m[0] + 8.f || mx[1] > m[1] + 8.f)) {
+          for (int i = 0; i < R2; ++i) {
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], 1));
-            const float mn = fmaxf(m[i], fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], 2)));
+            for (int x = 4; x < 32; x <<= 1) mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], x));
+            const float mn = fmaxf(m[i], mx[i]);
             const float f = mn == -INFINITY ? 1.f : ex2_sfu(m[i] - mn);
             m[i] = mn;
             l[i] *= f;
             pz[i] *= f;
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-              o[nt][2 * i] *= f;
-              o[nt][2 * i + 1] *= f;
+            for (int mt = 0; mt < MT; ++mt) {
+              o[i >> 1][mt][i & 1] *= f;
+              o[i >> 1][mt][2 + (i & 1)] *= f;
             }
           }
         }
-        const float ref[2] = {m[0] == -INFINITY ? 0.f : m[0], m[1] == -INFINITY ? 0.f : m[1]};
 #pragma unroll
-        for (int nt = 0; nt < kTiles; ++nt)
+        for (int i = 0; i < R2; ++i) {
+          const float ref = m[i] == -INFINITY ? 0.f : m[i];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            s[nt][e] = ex2_sfu(s[nt][e] - ref[e >> 1]);
-            l[e >> 1] += s[nt][e];
-          }
+          for (int kk = 0; kk < 2; ++kk)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              float& x = s[i >> 1][kk][2 * e + (i & 1)];
+              x = ex2_sfu(x - ref);
+              l[i] += x;
+            }
+        }
       } else {
 #pragma unroll
-        for (int nt = 0; nt < kTiles; ++nt)
+        for (int n = 0; n < NQ; ++n)
 #pragma unroll
-          for (int e = 0; e < 4; e += 2) {
-            const float2 y = cc_act2<ACT>(make_float2(s[nt][e], s[nt][e + 1]));
-            s[nt][e] = y.x;
-            s[nt][e + 1] = y.y;
-          }
+          for (int kk = 0; kk < 2; ++kk)
+#pragma unroll
+            for (int e = 0; e < 4; e += 2) {
+              const float2 y = cc_act2<ACT>(make_float2(s[n][kk][e], s[n][kk][e + 1]));
+              s[n][kk][e] = y.x;
+              s[n][kk][e + 1] = y.y;
+            }
       }
 #pragma unroll
-      for (int kk = 0; kk < kTiles / 2; ++kk) {  // 16 keys
-        // P s rounds to bf16 as the A operand (half a step, 2^-8 of each at most)
-        uint32_t pa[4];
+      for (int kk = 0; kk < 2; ++kk) {  // 16 keys
+        // P s rounds to bf16 as an operand (half a step, 2^-8 of each at most)
+        uint32_t pb[NQ][2];
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int nt = 2 * kk + i;
-          float2 v[2];
+        for (int e = 0; e < 2; ++e) {
+          const float2 v = c4_scale(vs + 4 * key_of(kk, e));
+          float y[R2];
 #pragma unroll
-          for (int c = 0; c < 2; ++c) v[c] = c4_scale(vs + 4 * col(nt, c));
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            float y[2];
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-              const float weight = s[nt][2 * h + c];
-              // (a place that the row does not see may hold any step and middle)
-              const bool sees = plain || ((see[h] >> col(nt, c)) & 1);
-              y[c] = sees ? weight * v[c].x : 0.f;
-              if (sees) pz[h] = __fmaf_rn(weight, v[c].y, pz[h]);
-            }
-            pa[2 * i + h] = pack_bf16(y[0], y[1]);
+          for (int i = 0; i < R2; ++i) {
+            const float weight = s[i >> 1][kk][2 * e + (i & 1)];
+            // (a place that the row does not see may hold any step and middle)
+            const bool sees = plain || ((see[i] >> key_of(kk, e)) & 1);
+            y[i] = sees ? weight * v.x : 0.f;
+            if (sees) pz[i] = __fmaf_rn(weight, v.y, pz[i]);
           }
+#pragma unroll
+          for (int n = 0; n < NQ; ++n) pb[n][e] = c4_transpose(pack_bf16(y[2 * n], y[2 * n + 1]));
         }
-        // V's codes of four keys: columns NT g and on of keys tig, tig + 4, + 8, + 12
-        constexpr int WV = NT >= 8 ? NT / 8 : 1;
+        // V's codes of four keys: columns D / 8 g and on of keys tig, tig + 4, + 8, + 12
+        constexpr int WV = D >= 64 ? D / 64 : 1;
         uint32_t word[4][WV];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -416,11 +510,15 @@ __global__ void __launch_bounds__(kC4Warps * 32, cache4_ctas(D)) cache4_fwd_kern
 #pragma unroll
         for (int j = 0; j < WV; ++j)
 #pragma unroll
-          for (int u = 0; u < (NT >= 8 ? 2 : 1); ++u) {
+          for (int u = 0; u < (D >= 64 ? 2 : 1); ++u) {
             const uint32_t sel = u == 0 ? 0x5410 : 0x7632;
-            const uint32_t a = __byte_perm(word[0][j], word[1][j], sel), b = __byte_perm(word[2][j], word[3][j], sel);
+            const uint32_t x = __byte_perm(word[0][j], word[1][j], sel), y = __byte_perm(word[2][j], word[3][j], sel);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) c4_mma(o[8 * j + 4 * u + i], pa, c4_pair(a >> (4 * i)), c4_pair(b >> (4 * i)));
+            for (int i = 0; i < 2; ++i) {  // nibbles 2 i and 2 i + 1: columns D / 8 g + 2 mt and + 1
+              const uint32_t a[4] = {c4_pair(x >> (8 * i)), c4_pair(x >> (8 * i + 4)), c4_pair(y >> (8 * i)), c4_pair(y >> (8 * i + 4))};
+#pragma unroll
+              for (int n = 0; n < NQ; ++n) c4_mma_v(o[n][4 * j + 2 * u + i], a, pb[n][0], pb[n][1]);
+            }
           }
       }
       __syncwarp();  // the block has been read
@@ -435,21 +533,20 @@ __global__ void __launch_bounds__(kC4Warps * 32, cache4_ctas(D)) cache4_fwd_kern
     // the item's end: the warps' O, maxima and sums meet in shared memory
     float* mine = reinterpret_cast<float*>(smem + warp * C::kRing);
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      pz[i] += __shfl_xor_sync(0xffffffffu, pz[i], 1);
-      pz[i] += __shfl_xor_sync(0xffffffffu, pz[i], 2);
-      if constexpr (ACT == 2) {
-        l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
-        l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
-        if (tig == 0) sh.ml[warp][g + 8 * i] = make_float2(m[i], l[i]);
+    for (int i = 0; i < R2; ++i) {
+      const int row = 2 * tig + (i & 1) + 8 * (i >> 1);
+#pragma unroll
+      for (int x = 4; x < 32; x <<= 1) {
+        pz[i] += __shfl_xor_sync(0xffffffffu, pz[i], x);
+        if constexpr (ACT == 2) l[i] += __shfl_xor_sync(0xffffffffu, l[i], x);
       }
+      if (ACT == 2 && g == 0) sh.ml[warp][row] = make_float2(m[i], l[i]);
 #pragma unroll
-      for (int e = 0; e < 2; ++e)
-#pragma unroll
-        for (int c = 0; c < NT / 4; ++c)
-          *reinterpret_cast<float4*>(mine + 4 * c4_place<D>(g + 8 * i, (NT / 4) * (2 * tig + e) + c)) =
-              make_float4(o[4 * c][2 * i + e] + pz[i], o[4 * c + 1][2 * i + e] + pz[i], o[4 * c + 2][2 * i + e] + pz[i],
-                          o[4 * c + 3][2 * i + e] + pz[i]);
+      for (int c = 0; c < D / 32; ++c) {
+        const float(&a)[4] = o[i >> 1][2 * c], (&b)[4] = o[i >> 1][2 * c + 1];
+        *reinterpret_cast<float4*>(mine + 4 * c4_place<D>(row, (D / 32) * g + c)) =
+            make_float4(a[i & 1] + pz[i], a[2 + (i & 1)] + pz[i], b[i & 1] + pz[i], b[2 + (i & 1)] + pz[i]);
+      }
     }
     __syncthreads();
 #pragma unroll 1
@@ -500,19 +597,24 @@ __global__ void __launch_bounds__(kC4Warps * 32, cache4_ctas(D)) cache4_fwd_kern
 #error "compile cache4_fwd.cu with -DJGDPA_HEAD_DIM=32, 64 or 128"
 #endif
 
-template <int D, int ACT>
+template <int D, int ACT, int NQ>
 static cudaError_t launch_c4(const Cache4FwdParams& p, int grid, cudaStream_t stream) {
-  auto kern = cache4_fwd_kernel<D, ACT>;
+  auto kern = cache4_fwd_kernel<D, ACT, NQ>;
   static DeviceFlags attr_set = {};
-  cudaError_t e = smem_attr_once(kern, C4Cfg<D>::kSmem, attr_set);
+  cudaError_t e = smem_attr_once(kern, C4Cfg<D, NQ>::kSmem, attr_set);
   if (e != cudaSuccess) return e;
-  return cache_launch(kern, dim3(grid), kC4Warps * 32, C4Cfg<D>::kSmem, stream, p);
+  return cache_launch(kern, dim3(grid), kC4Warps * 32, C4Cfg<D, NQ>::kSmem, stream, p);
+}
+template <int D, int ACT>
+static cudaError_t launch_c4_rows(const Cache4FwdParams& p, int grid, cudaStream_t stream) {
+  return cache4_columns(static_cast<int64_t>(p.f.max_q) * p.f.group) == 1 ? launch_c4<D, ACT, 1>(p, grid, stream)
+                                                                           : launch_c4<D, ACT, 2>(p, grid, stream);
 }
 template <int D>
 cudaError_t launch_cache4_fwd_d(const Cache4FwdParams& p, int act, int grid, cudaStream_t stream) {
-  if (act == 0) return launch_c4<D, 0>(p, grid, stream);
-  if (act == 1) return launch_c4<D, 1>(p, grid, stream);
-  return launch_c4<D, 2>(p, grid, stream);
+  if (act == 0) return launch_c4_rows<D, 0>(p, grid, stream);
+  if (act == 1) return launch_c4_rows<D, 1>(p, grid, stream);
+  return launch_c4_rows<D, 2>(p, grid, stream);
 }
 template cudaError_t launch_cache4_fwd_d<JGDPA_HEAD_DIM>(const Cache4FwdParams&, int, int, cudaStream_t);
 

@@ -156,12 +156,13 @@ jgdpa_status cache4_rows(bool append, const void* k_in, const void* v_in, void* 
 
 struct Cache4Layout {
   size_t err, join, part_ml, part_o, total;
-  int grid;
+  int sms, grid;  // grid: CTAs at most
 };
 bool cache4_layout(int32_t head_dim, Cache4Layout* L) {
   const int sms = jg::host_sm_count();
   if (sms <= 0) return false;
-  L->grid = sms * jg::cache4_ctas(head_dim);
+  L->sms = sms;
+  L->grid = sms * std::max(jg::cache4_ctas(head_dim, 1), jg::cache4_ctas(head_dim, 2));
   const size_t parts = 2 * static_cast<size_t>(L->grid) * jg::kCache4Rows;
   size_t off = kAlign;  // the status word
   L->err = off;
@@ -455,7 +456,7 @@ jgdpa_status jgdpa_cache4_fwd(const void* q, int64_t q_stride, const void* k_cod
     JG_CUDA(cudaMemsetAsync(ws, 0, sizeof(int), stream));
     return JGDPA_OK;
   }
-  int grid = L.grid;
+  int grid = L.sms * jg::cache4_ctas(head_dim, jg::cache4_columns(max_rows));
   if (total_q == 0 || max_q == 0) {  // no row is allowed: one CTA sees that the offsets hold none
     max_q = 0;
     grid = 1;
