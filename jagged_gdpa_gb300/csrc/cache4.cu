@@ -8,6 +8,11 @@
 // in fp32, each operation rounded once (halves to even), so that the codes are
 // the same wherever they are formed.  A few operations per value: bound by HBM (2.5
 // bytes a value each way and 4 a head).  D / 16 lanes take a head, 16 columns each.
+// The quotient is q = d y with y = 1 / s rounded, corrected twice by its remainder:
+// q + (d - q s) y is the rounded quotient from a q within one last place on (P. Markstein,
+// Computation of elementary functions on the IBM RISC System/6000 processor,
+// 1990, theorem 8); halves are exact then, which values and steps of 8 bits meet
+// often.  (With 16 divisions per lane the write of 32,768 rows x 8 x 128 took 84 us.)
 #include <algorithm>
 
 #include "cache4.cuh"
@@ -19,9 +24,14 @@ namespace jg {
 constexpr int kRows4Threads = 256;
 constexpr int kRows4Steps = 4;  // heads after one another
 
-__device__ __forceinline__ float min_nan(float a, float b) {
-  float y;
-  asm("min.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+__device__ __forceinline__ uint32_t min_nan2(uint32_t a, uint32_t b) {
+  uint32_t y;
+  asm("min.NaN.bf16x2 %0, %1, %2;" : "=r"(y) : "r"(a), "r"(b));
+  return y;
+}
+__device__ __forceinline__ uint32_t max_nan2(uint32_t a, uint32_t b) {
+  uint32_t y;
+  asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(y) : "r"(a), "r"(b));
   return y;
 }
 __device__ __forceinline__ uint4 ld_rows4(const void* p) {
@@ -75,34 +85,51 @@ __global__ void __launch_bounds__(kRows4Threads) cache4_append_kernel(const __gr
 #pragma unroll
   for (int i = 0; i < kRows4Steps; ++i) {
     if (i >= steps) break;
-    float x[16];
     const uint32_t w[8] = {v[i][0].x, v[i][0].y, v[i][0].z, v[i][0].w, v[i][1].x, v[i][1].y, v[i][1].z, v[i][1].w};
+    uint32_t least = w[0], most = w[0];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      x[2 * e] = __uint_as_float(w[e] << 16);
-      x[2 * e + 1] = __uint_as_float(w[e] & 0xFFFF0000u);
+    for (int e = 1; e < 8; ++e) {
+      least = min_nan2(least, w[e]);
+      most = max_nan2(most, w[e]);
     }
-    float lo = x[0], hi = x[0];
+    // the least value and the largest's negative side by side
+    most ^= 0x80008000u;
+    uint32_t both = min_nan2(__byte_perm(least, most, 0x5410), __byte_perm(least, most, 0x7632));
 #pragma unroll
-    for (int e = 1; e < 16; ++e) {
-      lo = min_nan(lo, x[e]);
-      hi = max_nan(hi, x[e]);
-    }
-#pragma unroll
-    for (int o = L / 2; o; o >>= 1) {
-      lo = min_nan(lo, __shfl_xor_sync(0xffffffffu, lo, o));
-      hi = max_nan(hi, __shfl_xor_sync(0xffffffffu, hi, o));
-    }
+    for (int o = L / 2; o; o >>= 1) both = min_nan2(both, __shfl_xor_sync(0xffffffffu, both, o));
+    const float lo = __uint_as_float(both << 16), hi = -__uint_as_float(both & 0xFFFF0000u);
     const __nv_bfloat16 step = __float2bfloat16_rn(__fdiv_rn(__fsub_rn(hi, lo), 15.f));
     const float s = __bfloat162float(step);
     const __nv_bfloat16 middle = __float2bfloat16_rn(__fadd_rn(lo, 8.f * s));
     const float z = __bfloat162float(middle);
+    // rounded by the addition of 1.5 2^23, with c + 8 in the last bits of the sum
+    constexpr float kRound = 12582912.f + 8.f;
+    constexpr uint32_t kBits = 0x4B400000u, kRest = kBits * 0x111u;  // 16^3 kBits and on leave 32 bits
+    const float inv = __frcp_rn(s);
+    const bool usual = s >= 0x1p-100f && s <= 0x1p100f;  // (1 / s and the remainders are normal numbers)
     uint32_t code[2] = {0, 0};
 #pragma unroll
-    for (int e = 0; e < 16; ++e) {
-      const float q = s > 0.f ? __fdiv_rn(__fsub_rn(x[e], z), s) : 0.f;
-      const int c = static_cast<int>(fminf(fmaxf(rintf(q), -8.f), 7.f)) + 8;  // (NaN: the least)
-      code[e >> 3] |= static_cast<uint32_t>(c) << (4 * (e & 7));
+    for (int e = 7; e >= 0; --e) {
+      const float2 x = make_float2(__uint_as_float(w[e] << 16), __uint_as_float(w[e] & 0xFFFF0000u));
+      const float2 d = __fadd2_rn(x, make_float2(-z, -z)), y = make_float2(inv, inv), less = make_float2(-s, -s);
+      float2 q = __fmul2_rn(d, y);
+      q = __ffma2_rn(__ffma2_rn(q, less, d), y, q);
+      q = __ffma2_rn(__ffma2_rn(q, less, d), y, q);
+      q = make_float2(fminf(fmaxf(q.x, -8.f), 7.f), fminf(fmaxf(q.y, -8.f), 7.f));  // (NaN: the least)
+      const float2 t = __fadd2_rn(q, make_float2(kRound, kRound));
+      uint32_t& c = code[e >> 2];
+      c = (c * 16 + __float_as_uint(t.y)) * 16 + __float_as_uint(t.x);
+    }
+    code[0] -= kRest;
+    code[1] -= kRest;
+    if (!usual) {
+      code[0] = code[1] = 0;
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        const float x = __uint_as_float(e & 1 ? w[e >> 1] & 0xFFFF0000u : w[e >> 1] << 16);
+        const float q = s > 0.f ? __fdiv_rn(__fsub_rn(x, z), s) : 0.f;
+        code[e >> 3] |= static_cast<uint32_t>(static_cast<int>(fminf(fmaxf(rintf(q), -8.f), 7.f)) + 8) << (4 * (e & 7));
+      }
     }
     if (slot[i] < 0) continue;
     const Rows4At at(p, vec0 + i * G);

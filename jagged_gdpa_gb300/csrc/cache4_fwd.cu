@@ -62,6 +62,7 @@ struct C4Cfg {
 struct C4Shared {
   CacheRangeShared range;
   float2 ml[kC4Warps][kC4Rows];
+  CcRow row[kC4Warps][kC4Rows];  // of the item, a copy for every warp
 };
 
 __device__ __forceinline__ void c4_copy(uint32_t dst, const void* src, bool live) {
@@ -158,15 +159,19 @@ __global__ void __launch_bounds__(kC4Warps * 32, cache4_ctas(D, NQ)) cache4_fwd_
     const int32_t* table = p.table + static_cast<int64_t>(w.b) * p.width;
     const int blocks_end = min(hi * (kC4Keys / kC4Block), static_cast<int>((static_cast<uint32_t>(r.L) + kC4Block - 1) / kC4Block));
     int kb = lo * (kC4Keys / kC4Block) + warp;
-    // lane i: the page of key 16 (i % 2) of a block, or -1
-    auto page_of = [&](int block) {
-      int id = -1;
-      const int key = block * kC4Block + 16 * (lane & 1);
-      if (block < blocks_end && key < r.L) {
-        id = table[key >> p.page_shift];
-        if (static_cast<uint32_t>(id) >= static_cast<uint32_t>(p.num_pages)) {
+    // the pages of a block's keys 0 and 16 on, or -1
+    auto pages_of = [&](int block) {
+      int2 id = make_int2(-1, -1);
+      const int key = block * kC4Block;
+      if (block < blocks_end) {
+        id.x = table[key >> p.page_shift];
+        id.y = key + 16 < r.L ? (p.page_shift == 4 ? table[(key >> 4) + 1] : id.x) : -1;
+        const bool bad_x = static_cast<uint32_t>(id.x) >= static_cast<uint32_t>(p.num_pages);
+        const bool bad_y = key + 16 < r.L && static_cast<uint32_t>(id.y) >= static_cast<uint32_t>(p.num_pages);
+        if (bad_x || bad_y) {
           atomicCAS(status, kOk, kErrBadPage);
-          id = -1;
+          if (bad_x) id.x = -1;
+          if (bad_y) id.y = -1;
         }
       }
       return id;
@@ -176,20 +181,25 @@ __global__ void __launch_bounds__(kC4Warps * 32, cache4_ctas(D, NQ)) cache4_fwd_
     constexpr int kHalf = 16 * kPieces;                     // of 16 keys' codes
     constexpr int kEach = kHalf >= 32 ? kHalf / 32 : 1;     // of them a lane's
     const int c_key = lane / kPieces, c_piece = lane % kPieces;  // (with kHalf = 16 lanes 16 and on take the second half)
-    auto copy = [&](int block, int id, int stage) {  // (the whole warp)
+    // a lane's places in the head's part of page 0: codes, and (lanes 0 to 7 K's, 8 to 15 V's) scales of four keys
+    const int64_t head_at = static_cast<int64_t>(w.h) << p.page_shift;
+    const uint8_t* const k_lane = pp.k.codes + head_at * C::kRow + 16 * (kHalf >= 32 ? lane : lane & 15);
+    const uint8_t* const v_lane = pp.v.codes + head_at * C::kRow + 16 * (kHalf >= 32 ? lane : lane & 15);
+    const Cache4& s_half = lane < 8 ? pp.k : pp.v;
+    const __nv_bfloat16* const s_lane = s_half.scales + head_at * 2;
+    const int64_t s_stride = s_half.scale_stride;
+    auto copy = [&](int block, int2 id, int stage) {  // (the whole warp)
       if (block < blocks_end) {
         const uint32_t to = ring + stage * C::kStage;
         const int first = block * kC4Block;
 #pragma unroll
         for (int half = 0; half < (kHalf >= 32 ? 2 : 1); ++half) {
           const int h = kHalf >= 32 ? half : lane >> 4;
-          const int page = __shfl_sync(0xffffffffu, id, h);
+          const int page = h ? id.y : id.x;
           const bool live = page >= 0;
-          const int64_t pg = live ? page : 0;
-          const int64_t at = ((static_cast<int64_t>(w.h) << p.page_shift) + ((first + 16 * h) & page_mask)) * C::kRow +
-                             16 * (kHalf >= 32 ? lane : lane & 15);
-          const uint8_t* ks = pp.k.codes + pg * pp.k.code_stride + at;
-          const uint8_t* vs = pp.v.codes + pg * pp.v.code_stride + at;
+          const int pg = max(page, 0), at = ((first + 16 * h) & page_mask) * C::kRow;
+          const uint8_t* ks = k_lane + pg * pp.k.code_stride + at;
+          const uint8_t* vs = v_lane + pg * pp.v.code_stride + at;
 #pragma unroll
           for (int i = 0; i < kEach; ++i) {
             const int key = (kHalf >= 32 ? 16 * half : 0) + i * (32 / kPieces) + c_key;
@@ -200,52 +210,44 @@ __global__ void __launch_bounds__(kC4Warps * 32, cache4_ctas(D, NQ)) cache4_fwd_
             c4_copy(to + C::kCodes + key * C::kRow + 16 * cv, vs + 512 * i, live);
           }
         }
-        // four keys' scales each: lanes 0 to 7 K's, 8 to 15 V's
-        const int key = (lane & 7) * 4, page = __shfl_sync(0xffffffffu, id, (lane >> 2) & 1);
         if (lane < 16) {
-          const Cache4& c = lane < 8 ? pp.k : pp.v;
-          const int64_t at = ((static_cast<int64_t>(w.h) << p.page_shift) + ((first + key) & page_mask)) * 2;
-          const bool live = page >= 0;
-          c4_copy(to + 2 * C::kCodes + lane * 16, c.scales + (live ? page : 0) * c.scale_stride + at, live);
+          const int key = (lane & 7) * 4, page = key & 16 ? id.y : id.x;
+          c4_copy(to + 2 * C::kCodes + lane * 16, s_lane + max(page, 0) * s_stride + ((first + key) & page_mask) * 2, page >= 0);
         }
       }
       c4_commit();
     };
     // the first blocks are on their way before anything else of the item
-    int ids = page_of(kb);
+    int2 ids = pages_of(kb);
 #pragma unroll
     for (int i = 0; i < C::kStages; ++i) {
-      const int next_ids = page_of(kb + (i + 1) * kC4Warps);
+      const int2 next_ids = pages_of(kb + (i + 1) * kC4Warps);
       copy(kb + i * kC4Warps, ids, i);
       ids = next_ids;
     }
 
     const int n_rows = min(kC4Rows, r.T * p.group - w.row_tile * kC4Rows);
-    CcRow rows[R2];
-    float far_bias[R2];
+    // the rows, lanes 0 to 15 one each; by the loop they are only asked for where a block is not plain
     int pos_min = INT32_MAX, pos_max = 0;
     bool hides = false;  // some row's bias hides all far keys, or is beyond what log2 units hold
-#pragma unroll
-    for (int i = 0; i < R2; ++i) {
-      const int lr = 2 * tig + (i & 1) + 8 * (i >> 1), flat = w.row_tile * kC4Rows + lr;
-      CcRow& q = rows[i];
-      const int t = static_cast<uint32_t>(flat) / static_cast<uint32_t>(p.group);
-      q.t = lr < n_rows ? t : -1;
-      q.head = w.h * p.group + (lr < n_rows ? flat - t * p.group : 0);
-      q.pos = r.C;
-      q.far_bias = 0.f;
-      far_bias[i] = 0.f;
-      if (q.t >= 0) {
-        q.pos = cc_row_pos(p, r, q.t, status);
-        pos_min = min(pos_min, q.pos);
-        pos_max = max(pos_max, q.pos);
-        if (p.bias_len) far_bias[i] = __ldg(p.bias + static_cast<int64_t>(q.head) * p.bias_len + 2 * reach) * kUnit;
+    if (lane < kC4Rows) {
+      const int flat = w.row_tile * kC4Rows + lane, t = static_cast<uint32_t>(flat) / static_cast<uint32_t>(p.group);
+      CcRow q{-1, r.C, w.h * p.group, 0.f};
+      if (lane < n_rows) {
+        q.t = t;
+        q.head += flat - t * p.group;
+        q.pos = cc_row_pos(p, r, t, status);
+        pos_min = pos_max = q.pos;
+        if (p.bias_len) q.far_bias = __ldg(p.bias + static_cast<int64_t>(q.head) * p.bias_len + 2 * reach) * kUnit;
+        hides = ACT == 2 && fabsf(q.far_bias) > kHugeScore;
       }
-      hides = hides || (ACT == 2 && fabsf(far_bias[i]) > kHugeScore);
+      sh.row[warp][lane] = q;
     }
     hides = __any_sync(0xffffffffu, hides);
     pos_min = __reduce_min_sync(0xffffffffu, pos_min);
     pos_max = __reduce_max_sync(0xffffffffu, pos_max);
+    __syncwarp();
+    auto row_of = [&](int i) -> const CcRow& { return sh.row[warp][2 * tig + (i & 1) + 8 * (i >> 1)]; };
     // Q's fragments (query row g + 8 n) in the order of K's nibbles, and what a lane's rows (2 tig ..) need of it
     uint32_t qb[NQ][KS][2];
     float q_sum[R2], q_unit[R2];  // sum q, and what brings <q, c> back
@@ -323,6 +325,13 @@ __global__ void __launch_bounds__(kC4Warps * 32, cache4_ctas(D, NQ)) cache4_fwd_
       const int key0 = kb * kC4Block;
       const bool far = p.bias_len == 0 || (!hides && key0 + kC4Block - 1 < r.C && pos_min - (key0 + kC4Block - 1) >= reach);
       bool plain = key0 + kC4Block - 1 < r.C && (p.window <= 0 || pos_max - key0 < p.window);
+      float far_bias[R2];
+#pragma unroll
+      for (int i = 0; i < R2; ++i) far_bias[i] = 0.f;
+      if (p.bias_len != 0 && far) {
+#pragma unroll
+        for (int i = 0; i < R2; ++i) far_bias[i] = row_of(i).far_bias;
+      }
       // a lane's keys: of the two of every 16, e = 0 and 1
       const int own = (g >> 1) + 4 * (g & 1);
       auto key_of = [&](int kk, int e) { return 16 * kk + 8 * e + own; };
@@ -332,16 +341,16 @@ __global__ void __launch_bounds__(kC4Warps * 32, cache4_ctas(D, NQ)) cache4_fwd_
       if (!plain) {
 #pragma unroll
         for (int i = 0; i < R2; ++i) {
-          uint32_t bits = cc_vis32(p, r, rows[i], key0);
+          uint32_t bits = cc_vis32(p, r, row_of(i), key0);
           if (p.window > 0) {
             uint32_t near = 0;
             if (cc_in_order(p, r, key0)) {
-              near = cc_near32(p, rows[i].pos, key0);
+              near = cc_near32(p, row_of(i).pos, key0);
             } else {
 #pragma unroll 1
               for (int c = 0; c < 4; ++c) {
                 const int at = key_of(c >> 1, c & 1);
-                near |= (cc_near(p, rows[i].pos, cc_pos(p, r, key0 + at)) ? 1u : 0u) << at;
+                near |= (cc_near(p, row_of(i).pos, cc_pos(p, r, key0 + at)) ? 1u : 0u) << at;
               }
             }
             bits &= near;  // (only this lane's keys are kept)
@@ -379,7 +388,7 @@ __global__ void __launch_bounds__(kC4Warps * 32, cache4_ctas(D, NQ)) cache4_fwd_
 #pragma unroll
           for (int i = 0; i < R2; ++i) {
             float& x = s[i >> 1][kk][2 * e + (i & 1)];
-            x = __fmaf_rn(x * q_unit[i], step, __fmaf_rn(middle, q_sum[i], far ? far_bias[i] : 0.f));
+            x = __fmaf_rn(x * q_unit[i], step, __fmaf_rn(middle, q_sum[i], far_bias[i]));
           }
         }
       if (!far) {
@@ -391,7 +400,7 @@ __global__ void __launch_bounds__(kC4Warps * 32, cache4_ctas(D, NQ)) cache4_fwd_
             const int key_pos = cc_pos(p, r, key0 + key_of(kk, e));
 #pragma unroll
             for (int i = 0; i < R2; ++i) {
-              const float bias = cc_bias(p, rows[i], reach, key_pos);
+              const float bias = cc_bias(p, row_of(i), reach, key_pos);
               float& x = s[i >> 1][kk][2 * e + (i & 1)];
               x = __fmaf_rn(bias, kUnit, x);
               if constexpr (ACT == 2) top = fmaxf(top, fabsf(bias));
@@ -406,7 +415,7 @@ __global__ void __launch_bounds__(kC4Warps * 32, cache4_ctas(D, NQ)) cache4_fwd_
 #pragma unroll
               for (int i = 0; i < R2; ++i) {
                 const int at = key_of(kk, e);
-                const float bias = cc_bias(p, rows[i], reach, cc_pos(p, r, key0 + at));
+                const float bias = cc_bias(p, row_of(i), reach, cc_pos(p, r, key0 + at));
                 float& x = s[i >> 1][kk][2 * e + (i & 1)];
                 if (bias == -INFINITY) see[i] &= ~(1u << at);
                 else if (fabsf(bias) > kHugeBias && x == x) x = cc_huge(bias);
@@ -481,13 +490,21 @@ __global__ void __launch_bounds__(kC4Warps * 32, cache4_ctas(D, NQ)) cache4_fwd_
         for (int e = 0; e < 2; ++e) {
           const float2 v = c4_scale(vs + 4 * key_of(kk, e));
           float y[R2];
+          if (plain) {
 #pragma unroll
-          for (int i = 0; i < R2; ++i) {
-            const float weight = s[i >> 1][kk][2 * e + (i & 1)];
-            // (a place that the row does not see may hold any step and middle)
-            const bool sees = plain || ((see[i] >> key_of(kk, e)) & 1);
-            y[i] = sees ? weight * v.x : 0.f;
-            if (sees) pz[i] = __fmaf_rn(weight, v.y, pz[i]);
+            for (int i = 0; i < R2; ++i) {
+              const float weight = s[i >> 1][kk][2 * e + (i & 1)];
+              y[i] = weight * v.x;
+              pz[i] = __fmaf_rn(weight, v.y, pz[i]);
+            }
+          } else {  // (a place that the row does not see may hold any step and middle)
+#pragma unroll
+            for (int i = 0; i < R2; ++i) {
+              const float weight = s[i >> 1][kk][2 * e + (i & 1)];
+              const bool sees = (see[i] >> key_of(kk, e)) & 1;
+              y[i] = sees ? weight * v.x : 0.f;
+              if (sees) pz[i] = __fmaf_rn(weight, v.y, pz[i]);
+            }
           }
 #pragma unroll
           for (int n = 0; n < NQ; ++n) pb[n][e] = c4_transpose(pack_bf16(y[2 * n], y[2 * n + 1]));
@@ -522,7 +539,7 @@ __global__ void __launch_bounds__(kC4Warps * 32, cache4_ctas(D, NQ)) cache4_fwd_
           }
       }
       __syncwarp();  // the block has been read
-      const int next_ids = page_of(kb + (C::kStages + 1) * kC4Warps);
+      const int2 next_ids = pages_of(kb + (C::kStages + 1) * kC4Warps);
       copy(kb + C::kStages * kC4Warps, ids, stage);
       ids = next_ids;
       stage = stage + 1 == C::kStages ? 0 : stage + 1;

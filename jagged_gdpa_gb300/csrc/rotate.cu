@@ -11,9 +11,10 @@
 //
 // A few operations per value: bound by HBM.  D / 16 lanes take a vector (one
 // head of one row), each two 16-byte pieces that hold whole pairs, so the only
-// exchange between lanes is that of the norm's sum.  A warp's unit is some
-// vectors side by side, in (row, head) order whatever the number of heads, up to
-// four (backward two) after one another, which it loads before it uses the first.
+// exchange between lanes is that of the norm's sum.  Such a group of lanes walks a run of
+// vectors in (row, head) order, so that a row's angles, times the norm's weights,
+// are formed once for the heads of the run; a few vectors are loaded before the
+// first is used.  Two values at a time (fp32 pairs).
 #include <algorithm>
 
 #include "cache.cuh"
@@ -25,8 +26,9 @@ namespace jg {
 
 constexpr int kRotThreads = 256;
 constexpr int kRotWarps = kRotThreads / 32;
-constexpr int kRotSteps = 4, kRotBackSteps = 2;  // vectors after one another, at most
-constexpr int kRotCtas = 3, kRotBackCtas = 2;    // per SM
+constexpr int kRotBatch = 4, kRotBackBatch = 2;  // vectors loaded at a time
+constexpr int kRotRun = 8;                       // vectors of a run in calls that fill the GPU
+constexpr int kRotCtas = 2, kRotBackCtas = 2;    // per SM
 
 template <int D>
 struct RotShape {
@@ -90,16 +92,44 @@ struct RotLane {
   }
 };
 
-__device__ __forceinline__ void rot_unpack(const uint4& v, float* f) {
-  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+// A lane's 8 pairs (a, b), two to a register pair: halves: a's from the first
+// piece, b's from the second; interleaved: both from every word.
+struct Pairs {
+  float2 a[4], b[4];
+};
+__device__ __forceinline__ float2 rot_pair(uint32_t w) {
+  return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+}
+template <bool PAIRS>
+__device__ __forceinline__ void rot_unpack(const uint4& u, const uint4& v, Pairs& f) {
+  const uint32_t x[4] = {u.x, u.y, u.z, u.w}, y[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    f[2 * i] = __uint_as_float(w[i] << 16);
-    f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    if constexpr (PAIRS) {
+      const float2 p = rot_pair(i < 2 ? x[2 * i] : y[2 * i - 4]), q = rot_pair(i < 2 ? x[2 * i + 1] : y[2 * i - 3]);
+      f.a[i] = make_float2(p.x, q.x);
+      f.b[i] = make_float2(p.y, q.y);
+    } else {
+      f.a[i] = rot_pair(x[i]);
+      f.b[i] = rot_pair(y[i]);
+    }
   }
 }
-__device__ __forceinline__ uint4 rot_pack(const float* f) {
-  return make_uint4(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7]));
+template <bool PAIRS>
+__device__ __forceinline__ void rot_pack(const Pairs& f, uint4& u, uint4& v) {
+  uint32_t x[4], y[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (PAIRS) {
+      (i < 2 ? x[2 * i] : y[2 * i - 4]) = pack_bf16(f.a[i].x, f.b[i].x);
+      (i < 2 ? x[2 * i + 1] : y[2 * i - 3]) = pack_bf16(f.a[i].y, f.b[i].y);
+    } else {
+      x[i] = pack_bf16(f.a[i].x, f.a[i].y);
+      y[i] = pack_bf16(f.b[i].x, f.b[i].y);
+    }
+  }
+  u = make_uint4(x[0], x[1], x[2], x[3]);
+  v = make_uint4(y[0], y[1], y[2], y[3]);
 }
 // (Not by the read-only path: the output may be the input itself.)
 __device__ __forceinline__ uint4 rot_load(const __nv_bfloat16* p) {
@@ -111,23 +141,25 @@ __device__ __forceinline__ uint4 rot_load(const __nv_bfloat16* p) {
   return v;
 }
 
-__device__ __forceinline__ void rot_weight(const float* w, int a, int b, float (&out)[16]) {
+// Columns of a lane's pieces of w, in the order of its pairs.
+template <bool PAIRS>
+__device__ __forceinline__ void rot_weight(const float* w, int a, int b, Pairs& out) {
+  float x[8], y[8];
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-    *reinterpret_cast<float4*>(out + 4 * i) = *reinterpret_cast<const float4*>(w + (i < 2 ? a + 4 * i : b + 4 * i - 8));
-}
-
-// Rotates a lane's 16 columns (8 of each piece) by its 8 angles; BACK: the other way.
-template <bool PAIRS, bool BACK>
-__device__ __forceinline__ void rot_turn(float (&f)[16], const float (&s)[8], const float (&c)[8]) {
+  for (int i = 0; i < 2; ++i) {
+    *reinterpret_cast<float4*>(x + 4 * i) = *reinterpret_cast<const float4*>(w + a + 4 * i);
+    *reinterpret_cast<float4*>(y + 4 * i) = *reinterpret_cast<const float4*>(w + b + 4 * i);
+  }
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    float& x = f[PAIRS ? 2 * i : i];
-    float& y = f[PAIRS ? 2 * i + 1 : i + 8];
-    const float sn = BACK ? -s[i] : s[i];
-    const float u = x * c[i] - y * sn;
-    y = y * c[i] + x * sn;
-    x = u;
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (PAIRS) {
+      const float* z = i < 2 ? x + 4 * i : y + 4 * i - 8;
+      out.a[i] = make_float2(z[0], z[2]);
+      out.b[i] = make_float2(z[1], z[3]);
+    } else {
+      out.a[i] = make_float2(x[2 * i], x[2 * i + 1]);
+      out.b[i] = make_float2(y[2 * i], y[2 * i + 1]);
+    }
   }
 }
 
@@ -143,7 +175,6 @@ template <int D, bool PAIRS>
 struct RotRow {
   int row = -1, b = 0, start = 0, end = 0;
   bool live = false;  // not behind the last segment
-  float s[8], c[8];
 
   // At a job's first row of the warp's.
   __device__ __forceinline__ void enter(const RotateJob& j, int first_row) {
@@ -153,10 +184,10 @@ struct RotRow {
     start = j.offsets[b];
     end = j.offsets[b + 1];
   }
-  // Moves on to a row that is not before the last one (an own one for every group of lanes).
+  // Moves on to another row, one that is not before the last (an own one for
+  // every group of lanes), and forms the sines and cosines of its angles.
   __device__ __forceinline__ void to(const RotateParams& p, const RotateJob& j, const RotLane<D, PAIRS>& l,
-                                     const uint64_t* turn, int r, bool want_angles) {
-    if (r == row) return;
+                                     const uint64_t* turn, int r, float2 (&s)[4], float2 (&c)[4]) {
     row = r;
     int64_t pos;
     if (j.positions != nullptr) {
@@ -180,13 +211,14 @@ struct RotRow {
         if (p.status != nullptr && (ctx < 0 || pos > INT32_MAX)) atomicCAS(p.status, kOk, kErrBadOffsets);
       }
     }
-    if (!want_angles) return;
+    if (j.copy) return;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int at = l.first + i;
-      s[i] = 0.f;
-      c[i] = 1.f;
-      if (l.turns && at < p.pairs) sincos_turn(turn[at] * static_cast<uint64_t>(pos), s[i], c[i]);
+    for (int i = 0; i < 4; ++i) {
+      s[i] = make_float2(0.f, 0.f);
+      c[i] = make_float2(1.f, 1.f);
+      const int at = l.first + 2 * i;
+      if (l.turns && at < p.pairs) sincos_turn(turn[at] * static_cast<uint64_t>(pos), s[i].x, c[i].x);
+      if (l.turns && at + 1 < p.pairs) sincos_turn(turn[at + 1] * static_cast<uint64_t>(pos), s[i].y, c[i].y);
     }
   }
 };
@@ -234,17 +266,18 @@ struct RotShare {
   }
 };
 
-// Vector of a job -> row and head.
-struct RotVec {
+// A place among the vectors of a job.
+struct RotAt {
   uint32_t row, head;
-  bool here;
-  __device__ __forceinline__ RotVec(const RotateJob& j, uint32_t vec) {
-    const uint32_t heads = j.heads;
-    here = vec < static_cast<uint32_t>(j.rows) * heads;
-    row = vec / heads;
-    head = vec - row * heads;
+  __device__ __forceinline__ void next(uint32_t heads) {
+    if (++head == heads) {
+      head = 0;
+      ++row;
+    }
   }
 };
+
+__device__ __forceinline__ float2 neg2(float2 x) { return make_float2(-x.x, -x.y); }
 
 template <int D, bool NORM, bool PAIRS>
 __global__ void __launch_bounds__(kRotThreads, kRotCtas) rotate_kernel(const __grid_constant__ RotateParams p) {
@@ -257,6 +290,9 @@ __global__ void __launch_bounds__(kRotThreads, kRotCtas) rotate_kernel(const __g
   const int group = (threadIdx.x & 31) / S::kLanes;
   const RotLane<D, PAIRS> lane(p.pairs);
   RotRow<D, PAIRS> at;
+  // y_a = r (x_a ca - x_b sb), y_b = r (x_b cb + x_a sa): cosines and sines times
+  // the weights of their columns (without a norm: cosines and sines)
+  float2 ca[4] = {}, sa[4] = {}, cb[NORM ? 4 : 1] = {}, sb[NORM ? 4 : 1] = {};
   int k = -1;
 #pragma unroll 1
   for (RotShare share(p.units); share.at < share.end; ++share.at) {
@@ -267,52 +303,90 @@ __global__ void __launch_bounds__(kRotThreads, kRotCtas) rotate_kernel(const __g
       enter = true;
     }
     const RotateJob& j = p.job[k];
-    const uint32_t vec0 = static_cast<uint32_t>(share.at - j.unit0) * (p.steps * S::kGroups) + group;
-    uint4 v[kRotSteps][2];
+    const uint32_t heads = j.heads, vecs = static_cast<uint32_t>(j.rows) * heads;
+    const uint32_t vec = (static_cast<uint32_t>(share.at - j.unit0) * S::kGroups + group) * p.run;
+    const int n = static_cast<int>(min(vecs - min(vec, vecs), static_cast<uint32_t>(p.run)));
+    RotAt here{vec / heads, 0};
+    here.head = vec - here.row * heads;
+    if (enter) at.enter(j, __shfl_sync(0xffffffffu, here.row, 0));
+#pragma unroll 1
+    for (int i0 = 0; i0 < p.run; i0 += kRotBatch) {
+      uint4 u[kRotBatch], v[kRotBatch];
+      RotAt load = here;
 #pragma unroll
-    for (int i = 0; i < kRotSteps; ++i) {
-      const RotVec vec(j, vec0 + i * S::kGroups);
-      v[i][0] = v[i][1] = make_uint4(0, 0, 0, 0);
-      if (i < p.steps && vec.here) {
-        const __nv_bfloat16* src = j.x + vec.row * j.x_stride + vec.head * D;
-        v[i][0] = rot_load(src + lane.a);
-        v[i][1] = rot_load(src + lane.b);
-      }
-    }
-    if (enter) at.enter(j, __shfl_sync(0xffffffffu, RotVec(j, vec0).row, 0));
-#pragma unroll
-    for (int i = 0; i < kRotSteps; ++i) {
-      if (i >= p.steps) break;
-      const RotVec vec(j, vec0 + i * S::kGroups);
-      if (vec.here) at.to(p, j, lane, sh.turn, vec.row, !j.copy);
-      if (!j.copy) {
-        float f[16];
-        rot_unpack(v[i][0], f);
-        rot_unpack(v[i][1], f + 8);
-        if constexpr (NORM) {
-          float sq = 0.f;
-#pragma unroll
-          for (int e = 0; e < 16; ++e) sq = __fmaf_rn(f[e], f[e], sq);
-          const float r = rsqrtf(rot_sum<S::kLanes>(sq) * (1.f / D) + p.eps);
-          float w[16];
-          rot_weight(sh.weight[k], lane.a, lane.b, w);
-#pragma unroll
-          for (int e = 0; e < 16; ++e) f[e] = f[e] * r * w[e];
+      for (int i = 0; i < kRotBatch; ++i) {
+        u[i] = v[i] = make_uint4(0, 0, 0, 0);
+        if (i0 + i < n) {
+          const __nv_bfloat16* src = j.x + load.row * j.x_stride + load.head * D;
+          u[i] = rot_load(src + lane.a);
+          v[i] = rot_load(src + lane.b);
         }
-        rot_turn<PAIRS, false>(f, at.s, at.c);
-        v[i][0] = rot_pack(f);
-        v[i][1] = rot_pack(f + 8);
+        load.next(heads);
       }
-      if (!vec.here || !at.live) continue;
-      __nv_bfloat16* dst = j.y + vec.row * j.y_stride;
-      if (j.slots != nullptr) {
-        const int slot = j.slots[vec.row];
-        if (static_cast<uint32_t>(slot) >= static_cast<uint32_t>(p.slot_end)) continue;
-        dst = j.y + (slot >> p.page_shift) * j.page_stride + static_cast<int64_t>(slot & ((1 << p.page_shift) - 1)) * (j.heads * D);
+#pragma unroll
+      for (int i = 0; i < kRotBatch; ++i) {
+        if (i0 + i >= p.run) break;
+        if (i0 + i < n && static_cast<int>(here.row) != at.row) {
+          float2 s[4], c[4];
+          at.to(p, j, lane, sh.turn, here.row, s, c);
+          if constexpr (NORM) {
+            if (!j.copy) {
+              Pairs w;
+              rot_weight<PAIRS>(sh.weight[k], lane.a, lane.b, w);
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                ca[e] = __fmul2_rn(c[e], w.a[e]);
+                sa[e] = __fmul2_rn(s[e], w.a[e]);
+                cb[e] = __fmul2_rn(c[e], w.b[e]);
+                sb[e] = neg2(__fmul2_rn(s[e], w.b[e]));
+              }
+            }
+          } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              ca[e] = c[e];
+              sa[e] = s[e];
+            }
+          }
+        }
+        if (!j.copy) {
+          Pairs f;
+          rot_unpack<PAIRS>(u[i], v[i], f);
+          float2 r = make_float2(1.f, 1.f);
+          if constexpr (NORM) {
+            float2 sq = make_float2(0.f, 0.f);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) sq = __ffma2_rn(f.b[e], f.b[e], __ffma2_rn(f.a[e], f.a[e], sq));
+            r.x = r.y = rsqrtf(rot_sum<S::kLanes>(sq.x + sq.y) * (1.f / D) + p.eps);
+          }
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float2 a = f.a[e], b = f.b[e];
+            f.a[e] = __ffma2_rn(b, NORM ? sb[NORM ? e : 0] : neg2(sa[e]), __fmul2_rn(a, ca[e]));
+            f.b[e] = __ffma2_rn(a, sa[e], __fmul2_rn(b, NORM ? cb[NORM ? e : 0] : ca[e]));
+            if constexpr (NORM) {
+              f.a[e] = __fmul2_rn(f.a[e], r);
+              f.b[e] = __fmul2_rn(f.b[e], r);
+            }
+          }
+          rot_pack<PAIRS>(f, u[i], v[i]);
+        }
+        if (i0 + i < n && at.live) {
+          __nv_bfloat16* dst = j.y + here.row * j.y_stride;
+          bool write = true;
+          if (j.slots != nullptr) {
+            const int slot = j.slots[here.row];
+            write = static_cast<uint32_t>(slot) < static_cast<uint32_t>(p.slot_end);
+            dst = j.y + (slot >> p.page_shift) * j.page_stride + static_cast<int64_t>(slot & ((1 << p.page_shift) - 1)) * (j.heads * D);
+          }
+          if (write) {
+            dst += here.head * D;
+            *reinterpret_cast<uint4*>(dst + lane.a) = u[i];
+            *reinterpret_cast<uint4*>(dst + lane.b) = v[i];
+          }
+        }
+        here.next(heads);
       }
-      dst += vec.head * D;
-      *reinterpret_cast<uint4*>(dst + lane.a) = v[i][0];
-      *reinterpret_cast<uint4*>(dst + lane.b) = v[i][1];
     }
   }
 }
@@ -332,9 +406,10 @@ __global__ void __launch_bounds__(kRotThreads, kRotBackCtas) rotate_back_kernel(
   if (blockIdx.x == 0 && p.status != nullptr) rot_check(p);
   const int lane32 = threadIdx.x & 31, warp = threadIdx.x >> 5, group = lane32 / S::kLanes;
   const RotLane<D, PAIRS> lane(p.pairs);
-  float acc[16];
+  Pairs acc;
+  const float2 zero = make_float2(0.f, 0.f);
 #pragma unroll
-  for (int e = 0; e < 16; ++e) acc[e] = 0.f;
+  for (int e = 0; e < 4; ++e) acc.a[e] = acc.b[e] = zero;
   if constexpr (NORM) {
     for (int i = lane32; i < 2 * D; i += 32) sums[warp][i / D][i % D] = 0.f;
     __syncwarp();
@@ -343,14 +418,22 @@ __global__ void __launch_bounds__(kRotThreads, kRotBackCtas) rotate_back_kernel(
     if constexpr (NORM) {
 #pragma unroll
       for (int e = 0; e < 16; ++e) {
+        float2& two = e < 8 ? acc.a[e >> 1] : acc.b[(e >> 1) - 4];
+        float v = e & 1 ? two.y : two.x;
 #pragma unroll
-        for (int o = S::kLanes; o < 32; o <<= 1) acc[e] += __shfl_xor_sync(0xffffffffu, acc[e], o);
-        if (group == 0) sums[warp][k][(e < 8 ? lane.a : lane.b - 8) + e] = acc[e];
-        acc[e] = 0.f;
+        for (int o = S::kLanes; o < 32; o <<= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+        // pair e % 8, a's or b's
+        const int column = PAIRS ? (e % 8 < 4 ? lane.a + 2 * (e % 8) : lane.b + 2 * (e % 8) - 8) + (e >> 3) : (e < 8 ? lane.a : lane.b) + e % 8;
+        if (group == 0) sums[warp][k][column] = v;
       }
+#pragma unroll
+      for (int e = 0; e < 4; ++e) acc.a[e] = acc.b[e] = zero;
     }
   };
   RotRow<D, PAIRS> at;
+  float2 s[4], c[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) s[e] = c[e] = zero;
   int k = -1;
 #pragma unroll 1
   for (RotShare share(p.units); share.at < share.end; ++share.at) {
@@ -362,59 +445,82 @@ __global__ void __launch_bounds__(kRotThreads, kRotBackCtas) rotate_back_kernel(
       enter = true;
     }
     const RotateJob& j = p.job[k];
-    const uint32_t vec0 = static_cast<uint32_t>(share.at - j.unit0) * (p.steps * S::kGroups) + group;
-    uint4 v[kRotBackSteps][2], d[kRotBackSteps][2];
+    const uint32_t heads = j.heads, vecs = static_cast<uint32_t>(j.rows) * heads;
+    const uint32_t vec = (static_cast<uint32_t>(share.at - j.unit0) * S::kGroups + group) * p.run;
+    const int n = static_cast<int>(min(vecs - min(vec, vecs), static_cast<uint32_t>(p.run)));
+    RotAt here{vec / heads, 0};
+    here.head = vec - here.row * heads;
+    if (enter) at.enter(j, __shfl_sync(0xffffffffu, here.row, 0));
+#pragma unroll 1
+    for (int i0 = 0; i0 < p.run; i0 += kRotBackBatch) {
+      uint4 u[kRotBackBatch], v[kRotBackBatch], du[kRotBackBatch], dv[kRotBackBatch];
+      RotAt load = here;
 #pragma unroll
-    for (int i = 0; i < kRotBackSteps; ++i) {
-      const RotVec vec(j, vec0 + i * S::kGroups);
-      v[i][0] = v[i][1] = d[i][0] = d[i][1] = make_uint4(0, 0, 0, 0);
-      if (i < p.steps && vec.here) {
-        const __nv_bfloat16* dy = j.dy + vec.row * j.dy_stride + vec.head * D;
-        d[i][0] = rot_load(dy + lane.a);
-        d[i][1] = rot_load(dy + lane.b);
+      for (int i = 0; i < kRotBackBatch; ++i) {
+        u[i] = v[i] = du[i] = dv[i] = make_uint4(0, 0, 0, 0);
+        if (i0 + i < n) {
+          const __nv_bfloat16* dy = j.dy + load.row * j.dy_stride + load.head * D;
+          du[i] = rot_load(dy + lane.a);
+          dv[i] = rot_load(dy + lane.b);
+          if constexpr (NORM) {
+            const __nv_bfloat16* x = j.x + load.row * j.x_stride + load.head * D;
+            u[i] = rot_load(x + lane.a);
+            v[i] = rot_load(x + lane.b);
+          }
+        }
+        load.next(heads);
+      }
+#pragma unroll
+      for (int i = 0; i < kRotBackBatch; ++i) {
+        if (i0 + i >= p.run) break;
+        if (i0 + i < n && static_cast<int>(here.row) != at.row) at.to(p, j, lane, sh.turn, here.row, s, c);
+        const bool live = i0 + i < n && at.live;
+        Pairs g;
+        rot_unpack<PAIRS>(du[i], dv[i], g);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {  // the other way round
+          const float2 a = g.a[e], b = g.b[e];
+          g.a[e] = __ffma2_rn(b, s[e], __fmul2_rn(a, c[e]));
+          g.b[e] = __ffma2_rn(a, neg2(s[e]), __fmul2_rn(b, c[e]));
+        }
         if constexpr (NORM) {
-          const __nv_bfloat16* x = j.x + vec.row * j.x_stride + vec.head * D;
-          v[i][0] = rot_load(x + lane.a);
-          v[i][1] = rot_load(x + lane.b);
+          Pairs h, w;
+          rot_unpack<PAIRS>(u[i], v[i], h);
+          float2 sq = zero;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) sq = __ffma2_rn(h.b[e], h.b[e], __ffma2_rn(h.a[e], h.a[e], sq));
+          const float r1 = rsqrtf(rot_sum<S::kLanes>(sq.x + sq.y) * (1.f / D) + p.eps);
+          const float2 r = make_float2(r1, r1);
+          rot_weight<PAIRS>(sh.weight[k], lane.a, lane.b, w);
+          float2 dot2 = zero;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            h.a[e] = __fmul2_rn(h.a[e], r);
+            h.b[e] = __fmul2_rn(h.b[e], r);
+            if (live) {
+              acc.a[e] = __ffma2_rn(g.a[e], h.a[e], acc.a[e]);
+              acc.b[e] = __ffma2_rn(g.b[e], h.b[e], acc.b[e]);
+            }
+            g.a[e] = __fmul2_rn(g.a[e], w.a[e]);
+            g.b[e] = __fmul2_rn(g.b[e], w.b[e]);
+            dot2 = __ffma2_rn(g.b[e], h.b[e], __ffma2_rn(g.a[e], h.a[e], dot2));
+          }
+          const float dot1 = rot_sum<S::kLanes>(dot2.x + dot2.y) * (-1.f / D);
+          const float2 dot = make_float2(dot1, dot1);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            g.a[e] = __fmul2_rn(__ffma2_rn(h.a[e], dot, g.a[e]), r);
+            g.b[e] = __fmul2_rn(__ffma2_rn(h.b[e], dot, g.b[e]), r);
+          }
         }
-      }
-    }
-    if (enter) at.enter(j, __shfl_sync(0xffffffffu, RotVec(j, vec0).row, 0));
-#pragma unroll
-    for (int i = 0; i < kRotBackSteps; ++i) {
-      if (i >= p.steps) break;
-      const RotVec vec(j, vec0 + i * S::kGroups);
-      if (vec.here) at.to(p, j, lane, sh.turn, vec.row, true);
-      const bool live = vec.here && at.live;
-      float g[16];
-      rot_unpack(d[i][0], g);
-      rot_unpack(d[i][1], g + 8);
-      rot_turn<PAIRS, true>(g, at.s, at.c);
-      if constexpr (NORM) {
-        float h[16], w[16];
-        rot_unpack(v[i][0], h);
-        rot_unpack(v[i][1], h + 8);
-        float sq = 0.f;
-#pragma unroll
-        for (int e = 0; e < 16; ++e) sq = __fmaf_rn(h[e], h[e], sq);
-        const float r = rsqrtf(rot_sum<S::kLanes>(sq) * (1.f / D) + p.eps);
-        rot_weight(sh.weight[k], lane.a, lane.b, w);
-        float dot = 0.f;
-#pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          h[e] *= r;
-          if (live) acc[e] = __fmaf_rn(g[e], h[e], acc[e]);
-          g[e] *= w[e];
-          dot = __fmaf_rn(g[e], h[e], dot);
+        if (live) {
+          rot_pack<PAIRS>(g, du[i], dv[i]);
+          __nv_bfloat16* dst = j.y + here.row * j.y_stride + here.head * D;
+          *reinterpret_cast<uint4*>(dst + lane.a) = du[i];
+          *reinterpret_cast<uint4*>(dst + lane.b) = dv[i];
         }
-        dot = rot_sum<S::kLanes>(dot) * (1.f / D);
-#pragma unroll
-        for (int e = 0; e < 16; ++e) g[e] = r * __fmaf_rn(-h[e], dot, g[e]);
+        here.next(heads);
       }
-      if (!live) continue;
-      __nv_bfloat16* dst = j.y + vec.row * j.y_stride + vec.head * D;
-      *reinterpret_cast<uint4*>(dst + lane.a) = rot_pack(g);
-      *reinterpret_cast<uint4*>(dst + lane.b) = rot_pack(g + 8);
     }
   }
   if constexpr (NORM) {
@@ -453,16 +559,16 @@ __global__ void __launch_bounds__(1024) rotate_weights_kernel(const __grid_const
 }
 
 // ------------------------------------------------------------------ launch
-// The units of the call's jobs, and the CTAs for them.  Calls that would leave
-// SMs idle with full units take one vector at a time (64 single tokens of 48
-// vectors of 128: 96 CTAs instead of 24).
+// The units of the call's jobs (a run of every group of a warp), and the CTAs for
+// them.  The run gets shorter as long as warps would have none (64 single tokens of
+// 48 vectors of 128: 96 CTAs with runs of one, 12 with runs of 8).
 template <int D>
-static int rotate_units(RotateParams& p, int most, int ctas) {
-  p.steps = most;
+static int rotate_units(RotateParams& p, int ctas) {
   int64_t vecs = 0;
   for (int k = 0; k < p.jobs; ++k) vecs += static_cast<int64_t>(p.job[k].rows) * p.job[k].heads;
-  if (vecs < static_cast<int64_t>(ctas) * kRotWarps * most * RotShape<D>::kGroups) p.steps = 1;
-  const int64_t each = p.steps * RotShape<D>::kGroups;
+  p.run = kRotRun;
+  while (p.run > 1 && vecs < static_cast<int64_t>(ctas) * kRotWarps * p.run * RotShape<D>::kGroups) p.run /= 2;
+  const int64_t each = static_cast<int64_t>(p.run) * RotShape<D>::kGroups;
   p.units = 0;
   for (int k = 0; k < p.jobs; ++k) {
     p.job[k].unit0 = p.units;
@@ -473,7 +579,7 @@ static int rotate_units(RotateParams& p, int most, int ctas) {
 
 template <int D>
 static cudaError_t launch_rotate_d(RotateParams p, bool norm, bool pairs, int sms, cudaStream_t stream) {
-  const int grid = rotate_units<D>(p, kRotSteps, sms * kRotCtas);
+  const int grid = rotate_units<D>(p, sms * kRotCtas);
   return cache_launch(norm ? (pairs ? rotate_kernel<D, true, true> : rotate_kernel<D, true, false>)
                            : (pairs ? rotate_kernel<D, false, true> : rotate_kernel<D, false, false>),
                       dim3(grid), kRotThreads, 0, stream, p);
@@ -486,7 +592,7 @@ cudaError_t launch_rotate(const RotateParams& p, int head_dim, bool norm, bool p
 
 template <int D>
 static cudaError_t launch_rotate_back_d(RotateParams p, bool norm, bool pairs, int sms, cudaStream_t stream) {
-  const int grid = rotate_units<D>(p, kRotBackSteps, sms * kRotBackCtas);
+  const int grid = rotate_units<D>(p, sms * kRotBackCtas);
   const cudaError_t e =
       cache_launch(norm ? (pairs ? rotate_back_kernel<D, true, true> : rotate_back_kernel<D, true, false>)
                         : (pairs ? rotate_back_kernel<D, false, true> : rotate_back_kernel<D, false, false>),

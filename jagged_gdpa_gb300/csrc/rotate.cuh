@@ -29,7 +29,7 @@ struct RotateParams {
   int64_t units;            // of all jobs
   const float* inv_freq;    // [pairs]
   int32_t jobs, pairs;
-  int32_t steps;            // vectors of a unit after one another
+  int32_t run;              // vectors that a group of lanes takes after one another
   float eps;
   const int32_t* kv_lens;   // [batch]: the rows are their requests' last tokens; nullptr: positions from 0
   const int32_t* depths;    // [rows] or nullptr: places after the context instead of the row's own
