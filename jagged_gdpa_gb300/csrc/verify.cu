@@ -95,16 +95,113 @@ struct Rest {
   }
 };
 
+// Two sums side by side.
+struct Sums2 {
+  float2 hi, lo;
+};
+__device__ __forceinline__ float2 minus(float2 a, float2 b) { return __ffma2_rn(b, make_float2(-1.f, -1.f), a); }
+__device__ __forceinline__ void add(Sums2& a, float2 v) {
+  const float2 s = __fadd2_rn(a.hi, v), t = minus(s, a.hi);
+  a.lo = __fadd2_rn(a.lo, __fadd2_rn(minus(a.hi, minus(s, t)), minus(v, t)));
+  a.hi = s;
+}
+// 16 bytes of a row as fp32 pairs.
+template <typename T>
+struct Piece {
+  static constexpr int kValues = 16 / sizeof(T);
+  float2 v[kValues / 2];
+  __device__ __forceinline__ explicit Piece(const uint4& u) {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < kValues / 2; ++i) {
+      if constexpr (sizeof(T) == 4) v[i] = make_float2(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1]));
+      else v[i] = make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u));
+    }
+  }
+};
+
+// The sum of what is left at tokens [lo, hi), the warp's, in 16-byte pieces from the first
+// that starts one (lo, but for a row's head) on.  r0 and r1 count nothing.  Infinities are not looked for:
+// the sum is no number then.
+template <typename T>
+__device__ __forceinline__ Sum2 verify_sum_pieces(const T* p, const T* q, int lo, int hi, int r0, int r1) {
+  constexpr int kV = Piece<T>::kValues, kWays = 4;
+  const int lane = threadIdx.x & 31;
+  Sums2 part[kWays];
+#pragma unroll
+  for (int i = 0; i < kWays; ++i) part[i].hi = part[i].lo = make_float2(0.f, 0.f);
+  auto take = [&](Sums2& to, const uint4& a, const uint4& b, int at) {
+    Piece<T> x(a);
+    if (q != nullptr) {
+      const Piece<T> y(b);
+#pragma unroll
+      for (int i = 0; i < kV / 2; ++i) x.v[i] = minus(x.v[i], y.v[i]);
+    }
+    const uint32_t o0 = static_cast<uint32_t>(r0 - at), o1 = static_cast<uint32_t>(r1 - at);
+    if (o0 < kV || o1 < kV) {
+#pragma unroll
+      for (int i = 0; i < kV / 2; ++i) {
+        if (o0 == 2 * i || o1 == 2 * i) x.v[i].x = 0.f;
+        if (o0 == 2 * i + 1 || o1 == 2 * i + 1) x.v[i].y = 0.f;
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kV / 2; ++i) add(to, make_float2(fmaxf(x.v[i].x, 0.f), fmaxf(x.v[i].y, 0.f)));
+  };
+  const int head = static_cast<int>((16 - (reinterpret_cast<uintptr_t>(p + lo) & 15)) & 15) / static_cast<int>(sizeof(T));
+  const int first = min(lo + head, hi), end = first + (hi - first) / kV * kV;
+  int at = first + lane * kV;
+  const uint4 none = make_uint4(0, 0, 0, 0);
+#pragma unroll 1
+  for (; at + (kWays - 1) * 32 * kV < end; at += kWays * 32 * kV) {
+    uint4 a[kWays], b[kWays];
+#pragma unroll
+    for (int i = 0; i < kWays; ++i) {
+      a[i] = *reinterpret_cast<const uint4*>(p + at + i * 32 * kV);
+      b[i] = q != nullptr ? *reinterpret_cast<const uint4*>(q + at + i * 32 * kV) : none;
+    }
+#pragma unroll
+    for (int i = 0; i < kWays; ++i) take(part[i], a[i], b[i], at + i * 32 * kV);
+  }
+  {
+    uint4 a[kWays - 1], b[kWays - 1];
+#pragma unroll
+    for (int i = 0; i < kWays - 1; ++i) {
+      const bool in = at + i * 32 * kV < end;
+      a[i] = in ? *reinterpret_cast<const uint4*>(p + at + i * 32 * kV) : none;
+      b[i] = in && q != nullptr ? *reinterpret_cast<const uint4*>(q + at + i * 32 * kV) : none;
+    }
+#pragma unroll
+    for (int i = 0; i < kWays - 1; ++i) take(part[i], a[i], b[i], at + i * 32 * kV);
+  }
+  // the row's head and tail, a lane each (fewer than 8)
+  Sum2 sum{0.f, 0.f};
+  const int rest = lane < 8 ? lo + lane : end + lane - 8;
+  if (lane < 16 && (lane < 8 ? rest < first : rest < hi) && rest != r0 && rest != r1) {
+    float r = prob(p + rest);
+    if (q != nullptr) r = __fsub_rn(r, prob(q + rest));
+    sum.hi = fmaxf(r, 0.f);
+  }
+#pragma unroll
+  for (int i = 0; i < kWays; ++i) {
+    sum = add(sum, Sum2{part[i].hi.x, part[i].lo.x});
+    sum = add(sum, Sum2{part[i].hi.y, part[i].lo.y});
+  }
+  return sum;
+}
+
 struct VerShared {
   int token[kVerifyMaxTokens], parent[kVerifyMaxTokens];
   float p[kVerifyMaxTokens];      // the parent's probability of the row's token
+  float u[kVerifyMaxTokens];
   int child[kVerifyMaxTokens];    // the row's first accepted child; then its place
   unsigned char first[kVerifyMaxTokens], ok[kVerifyMaxTokens];
   int kept, last, n_refused;
   Sum2 piece[kVerWarps];          // sums of the CTA's pieces, read by the whole cluster
   Sum2 warp_sum[kVerWarps];
   Sum2 before, target;
-  int win, winner, last_one;
+  int win, winner, last_one, n_here;
+  int here[kVerifyMaxTokens];     // refused tokens of the piece that is searched
 };
 
 // Which rows stay; every CTA of the cluster comes to the same.
@@ -115,34 +212,42 @@ __device__ void verify_walk(const VerifyParams& p, VerShared* sh, int q0, int T)
   const TQ* draft = static_cast<const TQ*>(p.draft);
   for (int t = tid; t < T; t += kVerThreads) {
     const int x = p.tokens[q0 + t], up = t == 0 ? -1 : p.parents != nullptr ? p.parents[q0 + t] : t - 1;
+    const float u = p.uniforms[q0 + t];
     const bool valid = t > 0 && up >= 0 && up < t && x >= 0 && x < p.vocab;
     if (t > 0 && !valid && p.status != nullptr) atomicCAS(p.status, kOk, kErrBadOffsets);
+    const float pt = valid ? prob(target + (q0 + up) * p.target_stride + x) : 0.f;
+    const float qt = valid && draft != nullptr ? prob(draft + (q0 + t) * p.draft_stride + x) : 0.f;
     sh->token[t] = x;
     sh->parent[t] = valid ? up : -1;
     sh->child[t] = INT32_MAX;
     sh->first[t] = valid;
-    const float pt = valid ? prob(target + (q0 + up) * p.target_stride + x) : 0.f;
     sh->p[t] = pt;
-    if (draft != nullptr && valid)
-      sh->ok[t] = static_cast<double>(p.uniforms[q0 + t]) * prob(draft + (q0 + t) * p.draft_stride + x) < pt;
-    else
-      sh->ok[t] = 0;
+    sh->u[t] = u;
+    sh->ok[t] = draft != nullptr && valid && static_cast<double>(u) * qt < pt;
   }
   __syncthreads();
   if (draft == nullptr) {
     if (p.parents != nullptr) {  // (a chain has no siblings) of equal tokens the first counts
       for (int t = tid; t < T; t += kVerThreads)
-        for (int s = 1; s < t; ++s)
-          if (sh->parent[s] == sh->parent[t] && sh->token[s] == sh->token[t]) sh->first[t] = 0;
+      {
+        const int up = sh->parent[t], x = sh->token[t];
+        bool twin = false;
+#pragma unroll 4
+        for (int s = 1; s < t; ++s) twin = twin || (sh->parent[s] == up && sh->token[s] == x);
+        if (twin) sh->first[t] = 0;
+      }
       __syncthreads();
     }
     for (int t = tid; t < T; t += kVerThreads) {
       if (!sh->first[t]) continue;
       double gone = 0.0;
-      if (p.parents != nullptr)
+      if (p.parents != nullptr) {
+        const int up = sh->parent[t];
+#pragma unroll 4
         for (int s = 1; s < t; ++s)
-          if (sh->first[s] && sh->parent[s] == sh->parent[t]) gone += sh->p[s];
-      sh->ok[t] = p.uniforms[q0 + t] * (1.0 - gone) < sh->p[t];
+          if (sh->first[s] && sh->parent[s] == up) gone += sh->p[s];
+      }
+      sh->ok[t] = sh->u[t] * (1.0 - gone) < sh->p[t];
     }
     __syncthreads();
   }
@@ -164,6 +269,17 @@ __device__ void verify_walk(const VerifyParams& p, VerShared* sh, int q0, int T)
   __syncthreads();
 }
 
+// Rows behind the last request.
+__device__ __forceinline__ void verify_padding(const VerifyParams& p) {
+  const int last = p.q_off[p.batch];
+  if (last < 0 || last >= p.total) return;
+  for (int64_t r = last + static_cast<int64_t>(blockIdx.x) * kVerThreads + threadIdx.x; r < p.total;
+       r += static_cast<int64_t>(gridDim.x) * kVerThreads) {
+    p.places[r] = -1;
+    if (p.keep_slots != nullptr) p.keep_slots[r] = -1;
+  }
+}
+
 template <typename TP, typename TQ>
 __global__ void __launch_bounds__(kVerThreads, 2) verify_kernel(const __grid_constant__ VerifyParams p) {
   __shared__ VerShared sh;
@@ -176,25 +292,19 @@ __global__ void __launch_bounds__(kVerThreads, 2) verify_kernel(const __grid_con
   const bool valid = q0 >= 0 && q1 >= q0 && q1 <= p.total && (b > 0 || q0 == 0);
   const int T = valid && q1 - q0 <= kVerifyMaxTokens ? q1 - q0 : 0;
   if (T != q1 - q0 && tid == 0 && p.status != nullptr) atomicCAS(p.status, kOk, kErrBadOffsets);
-  // rows behind the last request
-  const int last_row = p.q_off[p.batch];
-  if (last_row >= 0 && last_row < p.total)
-    for (int64_t r = last_row + static_cast<int64_t>(blockIdx.x) * kVerThreads + tid; r < p.total;
-         r += static_cast<int64_t>(gridDim.x) * kVerThreads) {
-      p.places[r] = -1;
-      if (p.keep_slots != nullptr) p.keep_slots[r] = -1;
-    }
   if (T == 0) {  // (the whole cluster)
-    if (rank != 0) return;
-    if (tid == 0) {
-      p.accepted[b] = 0;
-      p.next[b] = -1;
-      if (p.keep_lens != nullptr) p.keep_lens[b] = p.kv_lens[b];
+    if (rank == 0) {
+      if (tid == 0) {
+        p.accepted[b] = 0;
+        p.next[b] = -1;
+        if (p.keep_lens != nullptr) p.keep_lens[b] = p.kv_lens[b];
+      }
+      for (int r = q0 + tid; valid && r < q1; r += kVerThreads) {
+        p.places[r] = -1;
+        if (p.keep_slots != nullptr) p.keep_slots[r] = -1;
+      }
     }
-    for (int r = q0 + tid; valid && r < q1; r += kVerThreads) {
-      p.places[r] = -1;
-      if (p.keep_slots != nullptr) p.keep_slots[r] = -1;
-    }
+    verify_padding(p);
     return;
   }
   verify_walk<TP, TQ>(p, &sh, q0, T);
@@ -229,38 +339,56 @@ __global__ void __launch_bounds__(kVerThreads, 2) verify_kernel(const __grid_con
     __syncthreads();
     rest.n_refused = sh.n_refused;
   }
-  // pieces of the vocabulary: warp w of CTA c takes piece 16 c + w
+  // Pieces of the vocabulary: warp w of CTA c takes piece 16 c + w.  They are cut at whole
+  // 16 bytes of the row in memory, which `shift` entries in front of it start.
+  constexpr int kV = Piece<TP>::kValues;
+  const int shift = static_cast<int>(reinterpret_cast<uintptr_t>(rest.p) & 15) / static_cast<int>(sizeof(TP));
   const int pieces = n_cta * kVerWarps;
-  const int piece = (p.vocab + pieces - 1) / pieces;
-  const int64_t from = static_cast<int64_t>(rank * kVerWarps + warp) * piece;
-  const int lo = static_cast<int>(min(from, static_cast<int64_t>(p.vocab)));
-  const int hi = static_cast<int>(min(from + piece, static_cast<int64_t>(p.vocab)));
-  int next = -1;
+  const int piece = ((p.vocab + shift + pieces - 1) / pieces + kV - 1) / kV * kV;
+  auto piece_lo = [&](int k) { return static_cast<int>(min(max(static_cast<int64_t>(k) * piece - shift, int64_t{0}), static_cast<int64_t>(p.vocab))); };
+  const int lo = piece_lo(rank * kVerWarps + warp), hi = piece_lo(rank * kVerWarps + warp + 1);
 #pragma unroll 1
   for (int attempt = 0; attempt < 2; ++attempt) {
-    Rest<TP, TQ> here = rest;
-    if (rest.n_refused > 0) {
-      bool any = false;
-      for (int k = 0; k < rest.n_refused; ++k) any = any || (sh.token[k] >= lo && sh.token[k] < hi);
-      if (!any) here.n_refused = 0;
-    }
-    constexpr int kWays = 8;
-    Sum2 part[kWays];
-#pragma unroll
-    for (int i = 0; i < kWays; ++i) part[i] = {0.f, 0.f};
-    int at = lo + lane;
-    if (here.n_refused == 0)
-      for (; at + (kWays - 1) * 32 < hi; at += kWays * 32) {
-        float v[kWays];
-#pragma unroll
-        for (int i = 0; i < kWays; ++i) v[i] = here(at + 32 * i);
-#pragma unroll
-        for (int i = 0; i < kWays; ++i) part[i] = add(part[i], v[i]);
+    int r0 = -1, r1 = -1, n_here = 0;  // the piece's refused tokens
+    for (int k0 = 0; k0 < rest.n_refused; k0 += 32) {
+      const int x = k0 + lane < rest.n_refused ? rest.refused[k0 + lane] : -1;
+      unsigned in = __ballot_sync(0xffffffffu, x >= lo && x < hi);
+      n_here += __popc(in);
+      for (; in != 0; in &= in - 1) {
+        r1 = r0;
+        r0 = __shfl_sync(0xffffffffu, x, __ffs(in) - 1);
       }
-    for (; at < hi; at += 32) part[0] = add(part[0], here(at));
-    Sum2 sum = part[0];
+    }
+    Sum2 sum{0.f, 0.f};
+    bool good = false;
+    if constexpr (sizeof(TP) == sizeof(TQ)) {
+      // (rows of a draft that lie otherwise in their 16 bytes: one by one)
+      if (n_here <= 2 && (rest.q == nullptr || ((reinterpret_cast<uintptr_t>(rest.p) ^ reinterpret_cast<uintptr_t>(rest.q)) & 15) == 0)) {
+        sum = verify_sum_pieces<TP>(rest.p, reinterpret_cast<const TP*>(rest.q), lo, hi, r0, r1);
+        good = __all_sync(0xffffffffu, sum.hi <= 3.402823466e38f);
+      }
+    }
+    if (!good) {
+      constexpr int kWays = 8;
+      Rest<TP, TQ> here = rest;
+      if (n_here == 0) here.n_refused = 0;
+      Sum2 part[kWays];
 #pragma unroll
-    for (int i = 1; i < kWays; ++i) sum = add(sum, part[i]);
+      for (int i = 0; i < kWays; ++i) part[i] = {0.f, 0.f};
+      int at = lo + lane;
+      if (here.n_refused == 0)
+        for (; at + (kWays - 1) * 32 < hi; at += kWays * 32) {
+          float v[kWays];
+#pragma unroll
+          for (int i = 0; i < kWays; ++i) v[i] = here(at + 32 * i);
+#pragma unroll
+          for (int i = 0; i < kWays; ++i) part[i] = add(part[i], v[i]);
+        }
+      for (; at < hi; at += 32) part[0] = add(part[0], here(at));
+      sum = part[0];
+#pragma unroll
+      for (int i = 1; i < kWays; ++i) sum = add(sum, part[i]);
+    }
 #pragma unroll
     for (int o = 16; o; o >>= 1)
       sum = add(sum, Sum2{__shfl_xor_sync(0xffffffffu, sum.hi, o), __shfl_xor_sync(0xffffffffu, sum.lo, o)});
@@ -312,6 +440,7 @@ __global__ void __launch_bounds__(kVerThreads, 2) verify_kernel(const __grid_con
     if (tid == 0) {
       sh.winner = INT32_MAX;
       sh.last_one = -1;
+      sh.n_here = 0;
     }
     cluster.sync();  // the sums have been read by all
     if (sh.win >= 0) break;
@@ -319,14 +448,24 @@ __global__ void __launch_bounds__(kVerThreads, 2) verify_kernel(const __grid_con
     rest.q = nullptr;
     rest.n_refused = 0;
   }
+  verify_padding(p);
   if (sh.win < 0) {
     if (rank == 0 && tid == 0) p.next[b] = -1;
     return;
   }
   if (sh.win / kVerWarps != rank) return;
   // this CTA's: each thread some tokens in a row
-  const int w0 = sh.win * piece, w1 = min(w0 + piece, p.vocab);
-  const int each = (piece + kVerThreads - 1) / kVerThreads;
+  const int w0 = piece_lo(sh.win), w1 = piece_lo(sh.win + 1);
+  if (rest.n_refused > 0) {
+    for (int k = tid; k < rest.n_refused; k += kVerThreads) {
+      const int x = rest.refused[k];
+      if (x >= w0 && x < w1) sh.here[atomicAdd(&sh.n_here, 1)] = x;
+    }
+    __syncthreads();
+    rest.refused = sh.here;
+    rest.n_refused = sh.n_here;
+  }
+  const int each = (w1 - w0 + kVerThreads - 1) / kVerThreads;
   const int i0 = min(w0 + tid * each, w1), i1 = min(i0 + each, w1);
   Sum2 sum = {0.f, 0.f};
   for (int i = i0; i < i1; ++i) sum = add(sum, rest(i));
@@ -343,19 +482,25 @@ __global__ void __launch_bounds__(kVerThreads, 2) verify_kernel(const __grid_con
     if (above(to_here, sh.target)) atomicMin(&sh.winner, tid);
   }
   __syncthreads();
+  // the winner's tokens, a lane of its warp each
   const int winner = sh.winner == INT32_MAX ? sh.last_one : sh.winner;
-  if (tid == winner) {
-    Sum2 run = start;
-    for (int i = i0; i < i1; ++i) {
-      const float r = rest(i);
-      if (r > 0.f) {
-        next = i;
-        run = add(run, Sum2{r, 0.f});
-        if (above(run, sh.target)) break;
-      }
+  if (winner >> 5 != warp) return;
+  Sum2 run = {__shfl_sync(0xffffffffu, start.hi, winner & 31), __shfl_sync(0xffffffffu, start.lo, winner & 31)};
+  const int j0 = __shfl_sync(0xffffffffu, i0, winner & 31), j1 = __shfl_sync(0xffffffffu, i1, winner & 31);
+  int next = -1;
+  for (int j = j0; j < j1; j += 32) {
+    const float r = j + lane < j1 ? rest(j + lane) : 0.f;
+    const Sum2 sums = warp_prefix(Sum2{r, 0.f});
+    const unsigned some = __ballot_sync(0xffffffffu, r > 0.f);
+    const unsigned over = __ballot_sync(0xffffffffu, r > 0.f && above(add(run, sums), sh.target));
+    if (over != 0) {
+      next = j + __ffs(over) - 1;
+      break;
     }
-    p.next[b] = next;
+    if (some != 0) next = j + 31 - __clz(some);
+    run = add(run, Sum2{__shfl_sync(0xffffffffu, sums.hi, 31), __shfl_sync(0xffffffffu, sums.lo, 31)});
   }
+  if (lane == 0) p.next[b] = next;
 }
 
 template <typename TP, typename TQ>
