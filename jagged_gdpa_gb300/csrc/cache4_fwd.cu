@@ -180,7 +180,11 @@ __global__ void __launch_bounds__(kC4Warps * 32, cache4_ctas(D, NQ)) cache4_fwd_
     constexpr int kPieces = C::kRow / 16;                   // of a key
     constexpr int kHalf = 16 * kPieces;                     // of 16 keys' codes
     constexpr int kEach = kHalf >= 32 ? kHalf / 32 : 1;     // of them a lane's
-    const int c_key = lane / kPieces, c_piece = lane % kPieces;  // (with kHalf = 16 lanes 16 and on take the second half)
+    // A lane's place in a half's codes (with kHalf = 16 lanes 16 and on take the second half): key and piece,
+    // and where they go: K's keys in the order of their products, V's pieces turned by key.
+    const int c_key = lane / kPieces, c_piece = lane % kPieces;
+    const int k_to = ((c_key & ~7) | ((c_key & 3) << 1) | ((c_key >> 2) & 1)) * C::kRow + 16 * c_piece;
+    const int v_to = C::kCodes + c_key * C::kRow + 16 * (D == 128 ? c_piece ^ (c_key & 2) : c_piece);
     // a lane's places in the head's part of page 0: codes, and (lanes 0 to 7 K's, 8 to 15 V's) scales of four keys
     const int64_t head_at = static_cast<int64_t>(w.h) << p.page_shift;
     const uint8_t* const k_lane = pp.k.codes + head_at * C::kRow + 16 * (kHalf >= 32 ? lane : lane & 15);
@@ -202,12 +206,9 @@ __global__ void __launch_bounds__(kC4Warps * 32, cache4_ctas(D, NQ)) cache4_fwd_
           const uint8_t* vs = v_lane + pg * pp.v.code_stride + at;
 #pragma unroll
           for (int i = 0; i < kEach; ++i) {
-            const int key = (kHalf >= 32 ? 16 * half : 0) + i * (32 / kPieces) + c_key;
-            // K's keys in the order of their products, V's pieces turned by key
-            const int n = (key & ~7) | ((key & 3) << 1) | ((key >> 2) & 1);
-            const int cv = D == 128 ? c_piece ^ (key & 2) : c_piece;
-            c4_copy(to + n * C::kRow + 16 * c_piece, ks + 512 * i, live);
-            c4_copy(to + C::kCodes + key * C::kRow + 16 * cv, vs + 512 * i, live);
+            const int from = ((kHalf >= 32 ? 16 * half : 0) + i * (32 / kPieces)) * C::kRow;  // (8 keys or more, in order)
+            c4_copy(to + k_to + from, ks + 512 * i, live);
+            c4_copy(to + v_to + from, vs + 512 * i, live);
           }
         }
         if (lane < 16) {
@@ -361,23 +362,24 @@ __global__ void __launch_bounds__(kC4Warps * 32, cache4_ctas(D, NQ)) cache4_fwd_
       // S^T: s[n][kk][2 e + i] is key_of(kk, e) with row 2 n + i
       float s[NQ][2][4];
 #pragma unroll
-      for (int kk = 0; kk < 2; ++kk) {
+      for (int n = 0; n < NQ; ++n)
 #pragma unroll
-        for (int n = 0; n < NQ; ++n)
+        for (int e = 0; e < 8; ++e) s[n][e >> 2][e & 3] = 0.f;
+      {
+        uint32_t word[4][WK];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) s[n][kk][e] = 0.f;
-        uint32_t word[2][WK];
-#pragma unroll
-        for (int e = 0; e < 2; ++e) c4_words<WK>(kt + (16 * kk + 8 * e + g) * C::kRow + tig * (4 * WK), word[e]);
+        for (int e = 0; e < 4; ++e) c4_words<WK>(kt + (8 * e + g) * C::kRow + tig * (4 * WK), word[e]);
 #pragma unroll
         for (int j = 0; j < WK; ++j)
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const uint32_t x = word[0][j] >> (8 * h), y = word[1][j] >> (8 * h);
-            const uint32_t a[4] = {x & 0x000F000Fu, y & 0x000F000Fu, x & 0x00F000F0u, y & 0x00F000F0u};
+          for (int h = 0; h < 2; ++h)
 #pragma unroll
-            for (int n = 0; n < NQ; ++n) c4_mma_k(s[n][kk], a, qb[n][2 * j + h][0], qb[n][2 * j + h][1]);
-          }
+            for (int kk = 0; kk < 2; ++kk) {
+              const uint32_t x = word[2 * kk][j] >> (8 * h), y = word[2 * kk + 1][j] >> (8 * h);
+              const uint32_t a[4] = {x & 0x000F000Fu, y & 0x000F000Fu, x & 0x00F000F0u, y & 0x00F000F0u};
+#pragma unroll
+              for (int n = 0; n < NQ; ++n) c4_mma_k(s[n][kk], a, qb[n][2 * j + h][0], qb[n][2 * j + h][1]);
+            }
       }
 #pragma unroll
       for (int kk = 0; kk < 2; ++kk)
