@@ -53,9 +53,11 @@ struct C4Cfg {
   static constexpr int kRow = D / 2;  // bytes of a key's codes
   static constexpr int kCodes = kC4Block * kRow;
   static constexpr int kStage = 2 * kCodes + 2 * kC4Block * 4;  // codes of K and V, scales of K and V
-  static constexpr int kStages = D == 128 ? (NQ == 1 ? 3 : 4) : D == 64 ? 5 : 6;
+  static constexpr int kStages = D == 128 ? (NQ == 1 ? 3 : 4) : D == 64 ? (NQ == 1 ? 4 : 5) : 6;
   static constexpr int kRing = kStage * kStages > kC4Rows * D * 4 ? kStage * kStages : kC4Rows * D * 4;  // (O meets there)
-  static constexpr int kSmem = kC4Warps * kRing;
+  static constexpr int kQ = NQ * D / 32 * 32 * 16;  // Q's fragments, a copy for every warp
+  static constexpr int kQOff = kC4Warps * kRing;
+  static constexpr int kSmem = kQOff + kC4Warps * kQ;
   static_assert(kSmem <= 233472 / cache4_ctas(D, NQ) - 2048, "shared memory per CTA");
 };
 
@@ -106,9 +108,12 @@ __device__ __forceinline__ void c4_words(uint32_t addr, uint32_t (&w)[N]) {
     asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(addr) : "memory");
   else asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w[0]) : "r"(addr) : "memory");
 }
-__device__ __forceinline__ float2 c4_scale(uint32_t addr) {  // step, middle
+__device__ __forceinline__ uint32_t c4_word(uint32_t addr) {
   uint32_t w;
   asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w) : "r"(addr) : "memory");
+  return w;
+}
+__device__ __forceinline__ float2 c4_scale(uint32_t w) {  // step, middle
   return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
 }
 __device__ __forceinline__ uint32_t c4_half2(float lo, float hi) {
@@ -129,7 +134,6 @@ template <int D, int ACT, int NQ>
 __global__ void __launch_bounds__(kC4Warps * 32, cache4_ctas(D, NQ)) cache4_fwd_kernel(const __grid_constant__ Cache4FwdParams pp) {
   using C = C4Cfg<D, NQ>;
   constexpr int WK = D / 32;      // words of K's codes of a lane and key
-  constexpr int KS = D / 16;      // k steps of S
   constexpr int MT = D / 16;      // tiles of 16 columns of O
   constexpr int R2 = 2 * NQ;      // a lane's query rows: 2 tig + (i % 2) + 8 (i / 2)
   const CacheFwdParams& p = pp.f;
@@ -142,7 +146,7 @@ __global__ void __launch_bounds__(kC4Warps * 32, cache4_ctas(D, NQ)) cache4_fwd_
   if (tid == 0) *status = kOk;
   const CacheRange R = cache_range<kC4Keys>(p, &sh.range, kC4MinRange);
   if (tid == 0) cache_open<kC4Keys>(p, R);
-  const uint32_t ring = smem_u32(smem) + warp * C::kRing;
+  const uint32_t ring = smem_u32(smem) + warp * C::kRing, q_at = smem_u32(smem) + C::kQOff + warp * C::kQ + lane * 16;
   const int reach = (p.bias_len - 1) / 2;
   // scores in log2 units, or halved as cc_act2 takes them
   constexpr float kUnit = ACT == 2 ? kLog2e : 0.5f;
@@ -250,7 +254,6 @@ __global__ void __launch_bounds__(kC4Warps * 32, cache4_ctas(D, NQ)) cache4_fwd_
     __syncwarp();
     auto row_of = [&](int i) -> const CcRow& { return sh.row[warp][2 * tig + (i & 1) + 8 * (i >> 1)]; };
     // Q's fragments (query row g + 8 n) in the order of K's nibbles, and what a lane's rows (2 tig ..) need of it
-    uint32_t qb[NQ][KS][2];
     float q_sum[R2], q_unit[R2];  // sum q, and what brings <q, c> back
 #pragma unroll
     for (int n = 0; n < NQ; ++n) {
@@ -289,11 +292,8 @@ __global__ void __launch_bounds__(kC4Warps * 32, cache4_ctas(D, NQ)) cache4_fwd_
           y[2 * c] = __uint_as_float(x[c] << 16) * f0 * f1;
           y[2 * c + 1] = __uint_as_float(x[c] & 0xFFFF0000u) * f0 * f1 * 0.0625f;
         }
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {  // columns 2 h and 2 h + 4, 2 h + 1 and 2 h + 5
-          qb[n][2 * j + h][0] = c4_half2(y[2 * h], y[2 * h + 4]);
-          qb[n][2 * j + h][1] = c4_half2(y[2 * h + 1], y[2 * h + 5]);
-        }
+        // columns 2 h and 2 h + 4, 2 h + 1 and 2 h + 5
+        st_shared_v4(q_at + (n * WK + j) * 512, c4_half2(y[0], y[4]), c4_half2(y[1], y[5]), c4_half2(y[2], y[6]), c4_half2(y[3], y[7]));
       }
       // 2^24 of the codes (half of it with the step) and 2^(e - 14) of the row; lane 4 (2 tig + i) has row 2 tig + i
       const float back = __uint_as_float(static_cast<uint32_t>(12 + e - 14 + 127) << 23);
@@ -323,6 +323,30 @@ __global__ void __launch_bounds__(kC4Warps * 32, cache4_ctas(D, NQ)) cache4_fwd_
       c4_wait<C::kStages - 1>();
       __syncwarp();
       const uint32_t kt = ring + stage * C::kStage, vt = kt + C::kCodes, ks = vt + C::kCodes, vs = ks + kC4Block * 4;
+      // everything of the block that is read, at once: what follows is cut by branches, across which loads do not move
+      constexpr int WV = D >= 64 ? D / 64 : 1;
+      const int own = (g >> 1) + 4 * (g & 1);  // a lane's keys: of every 16 two, e = 0 and 1
+      auto key_of = [&](int kk, int e) { return 16 * kk + 8 * e + own; };
+      uint32_t k_word[4][WK], k_scale[4], v_scale[4], v_word[8][WV];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        c4_words<WK>(kt + (8 * e + g) * C::kRow + tig * (4 * WK), k_word[e]);
+        k_scale[e] = c4_word(ks + 4 * key_of(e >> 1, e & 1));
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v_scale[e] = c4_word(vs + 4 * key_of(e >> 1, e & 1));
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {  // columns D / 8 g and on of keys tig, tig + 4 ..
+        const int key = tig + 4 * i;
+        const uint32_t at = vt + key * C::kRow;
+        if constexpr (D == 128) c4_words<2>(at + (((g >> 1) ^ (key & 2)) << 4) + ((g & 1) << 3), v_word[i]);
+        else if constexpr (D == 64) c4_words<1>(at + 4 * g, v_word[i]);
+        else {
+          unsigned short x;
+          asm volatile("ld.shared.u16 %0, [%1];" : "=h"(x) : "r"(at + 2 * g) : "memory");
+          v_word[i][0] = x;
+        }
+      }
       const int key0 = kb * kC4Block;
       const bool far = p.bias_len == 0 || (!hides && key0 + kC4Block - 1 < r.C && pos_min - (key0 + kC4Block - 1) >= reach);
       bool plain = key0 + kC4Block - 1 < r.C && (p.window <= 0 || pos_max - key0 < p.window);
@@ -333,9 +357,6 @@ __global__ void __launch_bounds__(kC4Warps * 32, cache4_ctas(D, NQ)) cache4_fwd_
 #pragma unroll
         for (int i = 0; i < R2; ++i) far_bias[i] = row_of(i).far_bias;
       }
-      // a lane's keys: of the two of every 16, e = 0 and 1
-      const int own = (g >> 1) + 4 * (g & 1);
-      auto key_of = [&](int kk, int e) { return 16 * kk + 8 * e + own; };
       uint32_t see[R2];
 #pragma unroll
       for (int i = 0; i < R2; ++i) see[i] = 0xFFFFFFFFu;
@@ -366,26 +387,28 @@ __global__ void __launch_bounds__(kC4Warps * 32, cache4_ctas(D, NQ)) cache4_fwd_
 #pragma unroll
         for (int e = 0; e < 8; ++e) s[n][e >> 2][e & 3] = 0.f;
       {
-        uint32_t word[4][WK];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) c4_words<WK>(kt + (8 * e + g) * C::kRow + tig * (4 * WK), word[e]);
 #pragma unroll
         for (int j = 0; j < WK; ++j)
+        {
+          uint32_t qb[NQ][4];
+#pragma unroll
+          for (int n = 0; n < NQ; ++n) ld_shared_v4(q_at + (n * WK + j) * 512, qb[n][0], qb[n][1], qb[n][2], qb[n][3]);
 #pragma unroll
           for (int h = 0; h < 2; ++h)
 #pragma unroll
             for (int kk = 0; kk < 2; ++kk) {
-              const uint32_t x = word[2 * kk][j] >> (8 * h), y = word[2 * kk + 1][j] >> (8 * h);
+              const uint32_t x = k_word[2 * kk][j] >> (8 * h), y = k_word[2 * kk + 1][j] >> (8 * h);
               const uint32_t a[4] = {x & 0x000F000Fu, y & 0x000F000Fu, x & 0x00F000F0u, y & 0x00F000F0u};
 #pragma unroll
-              for (int n = 0; n < NQ; ++n) c4_mma_k(s[n][kk], a, qb[n][2 * j + h][0], qb[n][2 * j + h][1]);
+              for (int n = 0; n < NQ; ++n) c4_mma_k(s[n][kk], a, qb[n][2 * h], qb[n][2 * h + 1]);
             }
+        }
       }
 #pragma unroll
       for (int kk = 0; kk < 2; ++kk)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          const float2 k = c4_scale(ks + 4 * key_of(kk, e));
+          const float2 k = c4_scale(k_scale[2 * kk + e]);
           const float step = k.x * (4096.f * scale), middle = __fmaf_rn(-8.f, k.x, k.y) * scale;
 #pragma unroll
           for (int i = 0; i < R2; ++i) {
@@ -490,7 +513,7 @@ __global__ void __launch_bounds__(kC4Warps * 32, cache4_ctas(D, NQ)) cache4_fwd_
         uint32_t pb[NQ][2];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          const float2 v = c4_scale(vs + 4 * key_of(kk, e));
+          const float2 v = c4_scale(v_scale[2 * kk + e]);
           float y[R2];
           if (plain) {
 #pragma unroll
@@ -511,27 +534,13 @@ __global__ void __launch_bounds__(kC4Warps * 32, cache4_ctas(D, NQ)) cache4_fwd_
 #pragma unroll
           for (int n = 0; n < NQ; ++n) pb[n][e] = c4_transpose(pack_bf16(y[2 * n], y[2 * n + 1]));
         }
-        // V's codes of four keys: columns D / 8 g and on of keys tig, tig + 4, + 8, + 12
-        constexpr int WV = D >= 64 ? D / 64 : 1;
-        uint32_t word[4][WV];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int key = 16 * kk + tig + 4 * i;
-          const uint32_t at = vt + key * C::kRow;
-          if constexpr (D == 128) c4_words<2>(at + (((g >> 1) ^ (key & 2)) << 4) + ((g & 1) << 3), word[i]);
-          else if constexpr (D == 64) c4_words<1>(at + 4 * g, word[i]);
-          else {
-            unsigned short x;
-            asm volatile("ld.shared.u16 %0, [%1];" : "=h"(x) : "r"(at + 2 * g) : "memory");
-            word[i][0] = x;
-          }
-        }
 #pragma unroll
         for (int j = 0; j < WV; ++j)
 #pragma unroll
           for (int u = 0; u < (D >= 64 ? 2 : 1); ++u) {
             const uint32_t sel = u == 0 ? 0x5410 : 0x7632;
-            const uint32_t x = __byte_perm(word[0][j], word[1][j], sel), y = __byte_perm(word[2][j], word[3][j], sel);
+            const uint32_t x = __byte_perm(v_word[4 * kk][j], v_word[4 * kk + 1][j], sel);
+            const uint32_t y = __byte_perm(v_word[4 * kk + 2][j], v_word[4 * kk + 3][j], sel);
 #pragma unroll
             for (int i = 0; i < 2; ++i) {  // nibbles 2 i and 2 i + 1: columns D / 8 g + 2 mt and + 1
               const uint32_t a[4] = {c4_pair(x >> (8 * i)), c4_pair(x >> (8 * i + 4)), c4_pair(y >> (8 * i)), c4_pair(y >> (8 * i + 4))};
