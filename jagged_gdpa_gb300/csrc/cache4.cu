@@ -43,19 +43,31 @@ __device__ __forceinline__ uint4 ld_rows4(const void* p) {
   return v;
 }
 
-// The head of a row and where it lies in the cache.
+// A place among the heads of the rows, and where it lies in the cache.
 struct Rows4At {
   uint32_t row, head;
-  int slot;  // or -1
-  int64_t page, place;
+  int slot = -1;         // of the row, or -1
+  int64_t page = 0;
+  int place = 0;         // of the row in its page
   __device__ __forceinline__ Rows4At(const Cache4RowsParams& p, uint32_t vec) {
     row = vec / static_cast<uint32_t>(p.heads);
     head = vec - row * p.heads;
+    find(p);
+  }
+  __device__ __forceinline__ void find(const Cache4RowsParams& p) {
     slot = row < static_cast<uint32_t>(p.rows) ? p.slots[row] : -1;
     if (static_cast<uint32_t>(slot) >= static_cast<uint32_t>(p.slot_end)) slot = -1;
     page = slot >> p.page_shift;
-    place = (static_cast<int64_t>(head) << p.page_shift) + (slot & ((1 << p.page_shift) - 1));
+    place = slot & ((1 << p.page_shift) - 1);
   }
+  __device__ __forceinline__ void next(const Cache4RowsParams& p) {
+    if (++head == static_cast<uint32_t>(p.heads)) {
+      head = 0;
+      ++row;
+      find(p);
+    }
+  }
+  __device__ __forceinline__ int64_t in_page(const Cache4RowsParams& p) const { return (static_cast<int64_t>(head) << p.page_shift) + place; }
 };
 
 // blockIdx.y: K or V.
@@ -66,20 +78,23 @@ __global__ void __launch_bounds__(kRows4Threads) cache4_append_kernel(const __gr
   cache_wait_before();
   const int half = blockIdx.y, l = threadIdx.x % L;
   const int64_t warp = static_cast<int64_t>(blockIdx.x) * (kRows4Threads / 32) + (threadIdx.x >> 5);
-  const uint32_t vec0 = static_cast<uint32_t>(warp) * (G * steps) + (threadIdx.x & 31) / L;
+  Rows4At at(p, (static_cast<uint32_t>(warp) * G + (threadIdx.x & 31) / L) * steps);
   uint4 v[kRows4Steps][2];
-  int slot[kRows4Steps];
+  {
+    uint32_t row = at.row, head = at.head;
 #pragma unroll
-  for (int i = 0; i < kRows4Steps; ++i) {
-    slot[i] = -1;
-    v[i][0] = v[i][1] = make_uint4(0, 0, 0, 0);
-    if (i >= steps) continue;
-    const Rows4At at(p, vec0 + i * G);
-    slot[i] = at.slot;
-    if (at.row < static_cast<uint32_t>(p.rows)) {
-      const __nv_bfloat16* src = p.in[half] + at.row * p.stride[half] + at.head * D + 16 * l;
-      v[i][0] = ld_rows4(src);
-      v[i][1] = ld_rows4(src + 8);
+    for (int i = 0; i < kRows4Steps; ++i) {
+      v[i][0] = v[i][1] = make_uint4(0, 0, 0, 0);
+      if (i >= steps) continue;
+      if (row < static_cast<uint32_t>(p.rows)) {
+        const __nv_bfloat16* src = p.in[half] + row * p.stride[half] + head * D + 16 * l;
+        v[i][0] = ld_rows4(src);
+        v[i][1] = ld_rows4(src + 8);
+      }
+      if (++head == static_cast<uint32_t>(p.heads)) {
+        head = 0;
+        ++row;
+      }
     }
   }
 #pragma unroll
@@ -131,16 +146,18 @@ __global__ void __launch_bounds__(kRows4Threads) cache4_append_kernel(const __gr
         code[e >> 3] |= static_cast<uint32_t>(static_cast<int>(fminf(fmaxf(rintf(q), -8.f), 7.f)) + 8) << (4 * (e & 7));
       }
     }
-    if (slot[i] < 0) continue;
-    const Rows4At at(p, vec0 + i * G);
-    const Cache4& c = p.cache[half];
-    *reinterpret_cast<uint2*>(c.codes + at.page * c.code_stride + at.place * (D / 2) + 8 * l) = make_uint2(code[0], code[1]);
-    if (l == 0) {
-      __nv_bfloat162 pair;
-      pair.x = step;
-      pair.y = middle;
-      *reinterpret_cast<__nv_bfloat162*>(c.scales + at.page * c.scale_stride + at.place * 2) = pair;
+    if (at.slot >= 0) {
+      const Cache4& c = p.cache[half];
+      const int64_t place = at.in_page(p);
+      *reinterpret_cast<uint2*>(c.codes + at.page * c.code_stride + place * (D / 2) + 8 * l) = make_uint2(code[0], code[1]);
+      if (l == 0) {
+        __nv_bfloat162 pair;
+        pair.x = step;
+        pair.y = middle;
+        *reinterpret_cast<__nv_bfloat162*>(c.scales + at.page * c.scale_stride + place * 2) = pair;
+      }
     }
+    at.next(p);
   }
 }
 
@@ -151,8 +168,9 @@ __global__ void __launch_bounds__(kRows4Threads) cache4_read_kernel(const __grid
   cache_wait_before();
   const int half = blockIdx.y, l = threadIdx.x % L;
   const int64_t warp = static_cast<int64_t>(blockIdx.x) * (kRows4Threads / 32) + (threadIdx.x >> 5);
-  const uint32_t vec0 = static_cast<uint32_t>(warp) * (G * steps) + (threadIdx.x & 31) / L;
+  Rows4At at(p, (static_cast<uint32_t>(warp) * G + (threadIdx.x & 31) / L) * steps);
   const Cache4& c = p.cache[half];
+  uint32_t row = at.row, head = at.head;
   uint2 code[kRows4Steps];
   uint32_t scale[kRows4Steps];
 #pragma unroll
@@ -160,17 +178,16 @@ __global__ void __launch_bounds__(kRows4Threads) cache4_read_kernel(const __grid
     code[i] = make_uint2(0, 0);
     scale[i] = 0;
     if (i >= steps) continue;
-    const Rows4At at(p, vec0 + i * G);
     if (at.slot >= 0) {
-      code[i] = *reinterpret_cast<const uint2*>(c.codes + at.page * c.code_stride + at.place * (D / 2) + 8 * l);
-      scale[i] = *reinterpret_cast<const uint32_t*>(c.scales + at.page * c.scale_stride + at.place * 2);
+      const int64_t place = at.in_page(p);
+      code[i] = *reinterpret_cast<const uint2*>(c.codes + at.page * c.code_stride + place * (D / 2) + 8 * l);
+      scale[i] = *reinterpret_cast<const uint32_t*>(c.scales + at.page * c.scale_stride + place * 2);
     }
+    at.next(p);
   }
 #pragma unroll
   for (int i = 0; i < kRows4Steps; ++i) {
-    if (i >= steps) break;
-    const Rows4At at(p, vec0 + i * G);
-    if (at.row >= static_cast<uint32_t>(p.rows)) continue;
+    if (i >= steps || row >= static_cast<uint32_t>(p.rows)) break;
     const float s = __uint_as_float(scale[i] << 16), z = __uint_as_float(scale[i] & 0xFFFF0000u);
     uint32_t w[8];
 #pragma unroll
@@ -180,9 +197,13 @@ __global__ void __launch_bounds__(kRows4Threads) cache4_read_kernel(const __grid
       // (the product has 12 bits: the sum is rounded to fp32, then to bf16)
       w[e] = pack_bf16(__fmaf_rn(s, a, z), __fmaf_rn(s, b, z));
     }
-    __nv_bfloat16* dst = p.out[half] + at.row * p.stride[half] + at.head * D + 16 * l;
+    __nv_bfloat16* dst = p.out[half] + row * p.stride[half] + head * D + 16 * l;
     *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
     *reinterpret_cast<uint4*>(dst + 8) = make_uint4(w[4], w[5], w[6], w[7]);
+    if (++head == static_cast<uint32_t>(p.heads)) {
+      head = 0;
+      ++row;
+    }
   }
 }
 

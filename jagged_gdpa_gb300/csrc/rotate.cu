@@ -44,9 +44,13 @@ __device__ __forceinline__ uint64_t turn_of(float f) {
   const double turns = static_cast<double>(f) * 0.15915494309189533577;  // 1 / (2 pi)
   return static_cast<uint64_t>(__double2ll_rn((turns - rint(turns)) * 18446744073709551616.0));
 }
-__device__ __forceinline__ void sincos_turn(uint64_t turn, float& s, float& c) {
+__device__ __forceinline__ void sincos_turn(uint64_t f, int pos, float& s, float& c) {
+  // bits 32 to 63 of the product, half a turn on, as a number of [1, 2)
+  const uint32_t turn = static_cast<uint32_t>(pos) * static_cast<uint32_t>(f >> 32) + __umulhi(static_cast<uint32_t>(pos), static_cast<uint32_t>(f)) -
+                        (pos < 0 ? static_cast<uint32_t>(f) : 0u);
+  const float x = __uint_as_float(((turn + 0x80000000u) >> 9) | 0x3F800000u) - 1.5f;
   // [-pi, pi), where the hardware's sine and cosine are within 2^-20.9
-  const float a = static_cast<float>(static_cast<int32_t>(turn >> 32)) * 1.46291807926715968e-9f;  // pi 2^-31
+  const float a = x * 6.283185307179586f;
   s = __sinf(a);
   c = __cosf(a);
 }
@@ -74,17 +78,14 @@ template <int D, bool PAIRS>
 struct RotLane {
   int a, b;        // first columns of the two pieces
   int first;       // the first pair's frequency
-  bool turns;      // some of the lane's columns rotate
   __device__ __forceinline__ RotLane(int n) {
     const int l = threadIdx.x % RotShape<D>::kLanes;
     if constexpr (PAIRS) {
       a = 16 * l;
       b = a + 8;
       first = 8 * l;
-      turns = first < n;
     } else {
-      const int m = n >> 3;
-      turns = l < m;
+      const bool turns = l < (n >> 3);
       a = turns ? 8 * l : 16 * l;
       b = turns ? 8 * l + n : 16 * l + 8;
       first = 8 * l;
@@ -212,13 +213,12 @@ struct RotRow {
       }
     }
     if (j.copy) return;
+    // (columns that do not rotate have frequencies of 0: sine 0, cosine 1)
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      s[i] = make_float2(0.f, 0.f);
-      c[i] = make_float2(1.f, 1.f);
-      const int at = l.first + 2 * i;
-      if (l.turns && at < p.pairs) sincos_turn(turn[at] * static_cast<uint64_t>(pos), s[i].x, c[i].x);
-      if (l.turns && at + 1 < p.pairs) sincos_turn(turn[at + 1] * static_cast<uint64_t>(pos), s[i].y, c[i].y);
+      const ulonglong2 f = *reinterpret_cast<const ulonglong2*>(turn + l.first + 2 * i);
+      sincos_turn(f.x, static_cast<int>(pos), s[i].x, c[i].x);
+      sincos_turn(f.y, static_cast<int>(pos), s[i].y, c[i].y);
     }
   }
 };
@@ -226,13 +226,13 @@ struct RotRow {
 // The call's frequencies and weights, in shared memory.
 template <int D>
 struct RotShared {
-  uint64_t turn[D / 2];
+  alignas(16) uint64_t turn[D / 2];
   alignas(16) float weight[2][D];
 };
 template <int D>
 __device__ __forceinline__ void rot_setup(const RotateParams& p, RotShared<D>* sh) {
   const int tid = threadIdx.x;
-  if (tid < p.pairs) sh->turn[tid] = turn_of(p.inv_freq[tid]);
+  if (tid < D / 2) sh->turn[tid] = tid < p.pairs ? turn_of(p.inv_freq[tid]) : 0;
   for (int i = tid; i < 2 * D; i += kRotThreads) {
     const float* w = p.job[i / D].weight;
     sh->weight[i / D][i % D] = w != nullptr ? w[i % D] : 1.f;
@@ -391,6 +391,68 @@ __global__ void __launch_bounds__(kRotThreads, kRotCtas) rotate_kernel(const __g
   }
 }
 
+// Backward of N vectors of a row, side by side (what lanes exchange and what is
+// looked up costs the latency of one):
+//   dx = r dh - x r^3 mean(dh x),  dw += (g x) r
+// u, v: x; du, dv: dy, then dx.
+template <int D, bool NORM, bool PAIRS, int N>
+__device__ __forceinline__ void rot_back(const RotLane<D, PAIRS>& lane, const float* weight, float eps, const float2 (&s)[4],
+                                         const float2 (&c)[4], const uint4* u, const uint4* v, uint4* du, uint4* dv, bool live,
+                                         Pairs& acc) {
+  Pairs g[N], x[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    rot_unpack<PAIRS>(du[i], dv[i], g[i]);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {  // the other way round
+      const float2 a = g[i].a[e], b = g[i].b[e];
+      g[i].a[e] = __ffma2_rn(b, s[e], __fmul2_rn(a, c[e]));
+      g[i].b[e] = __ffma2_rn(a, neg2(s[e]), __fmul2_rn(b, c[e]));
+    }
+  }
+  if constexpr (NORM) {
+    Pairs w;
+    rot_weight<PAIRS>(weight, lane.a, lane.b, w);
+    float sq[N], dot[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      rot_unpack<PAIRS>(u[i], v[i], x[i]);
+      float2 sq2 = make_float2(0.f, 0.f), dot2 = sq2;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        sq2 = __ffma2_rn(x[i].b[e], x[i].b[e], __ffma2_rn(x[i].a[e], x[i].a[e], sq2));
+        dot2 = __ffma2_rn(__fmul2_rn(g[i].a[e], x[i].a[e]), w.a[e], dot2);
+        dot2 = __ffma2_rn(__fmul2_rn(g[i].b[e], x[i].b[e]), w.b[e], dot2);
+      }
+      sq[i] = sq2.x + sq2.y;
+      dot[i] = dot2.x + dot2.y;
+    }
+#pragma unroll
+    for (int o = RotShape<D>::kLanes / 2; o; o >>= 1)
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        sq[i] += __shfl_xor_sync(0xffffffffu, sq[i], o);
+        dot[i] += __shfl_xor_sync(0xffffffffu, dot[i], o);
+      }
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const float r1 = rsqrtf(sq[i] * (1.f / D) + eps), m1 = (r1 * r1) * (r1 * dot[i]) * (-1.f / D);
+      const float2 r = make_float2(r1, r1), m = make_float2(m1, m1);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        if (live) {
+          acc.a[e] = __ffma2_rn(__fmul2_rn(g[i].a[e], x[i].a[e]), r, acc.a[e]);
+          acc.b[e] = __ffma2_rn(__fmul2_rn(g[i].b[e], x[i].b[e]), r, acc.b[e]);
+        }
+        g[i].a[e] = __ffma2_rn(x[i].a[e], m, __fmul2_rn(__fmul2_rn(g[i].a[e], w.a[e]), r));
+        g[i].b[e] = __ffma2_rn(x[i].b[e], m, __fmul2_rn(__fmul2_rn(g[i].b[e], w.b[e]), r));
+      }
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < N; ++i) rot_pack<PAIRS>(g[i], du[i], dv[i]);
+}
+
 // Backward.  The weights' gradients are sums over every row and head: a lane
 // keeps its 16 columns' in registers over its warp's units of a job, the warps of
 // a CTA meet in shared memory, the CTAs in `partial`, each in a fixed order (the
@@ -470,51 +532,31 @@ __global__ void __launch_bounds__(kRotThreads, kRotBackCtas) rotate_back_kernel(
         }
         load.next(heads);
       }
+      // both of one row, in every group of the warp: side by side
+      static_assert(kRotBackBatch == 2, "pairs");
+      const bool both = i0 + 1 < n && here.head + 1 < heads;
+      if (__all_sync(0xffffffffu, both)) {
+        if (static_cast<int>(here.row) != at.row) at.to(p, j, lane, sh.turn, here.row, s, c);
+        rot_back<D, NORM, PAIRS, 2>(lane, sh.weight[k], p.eps, s, c, u, v, du, dv, at.live, acc);
+        if (at.live) {
+          __nv_bfloat16* dst = j.y + here.row * j.y_stride + here.head * D;
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            *reinterpret_cast<uint4*>(dst + i * D + lane.a) = du[i];
+            *reinterpret_cast<uint4*>(dst + i * D + lane.b) = dv[i];
+          }
+        }
+        here.next(heads);
+        here.next(heads);
+        continue;
+      }
 #pragma unroll
       for (int i = 0; i < kRotBackBatch; ++i) {
         if (i0 + i >= p.run) break;
         if (i0 + i < n && static_cast<int>(here.row) != at.row) at.to(p, j, lane, sh.turn, here.row, s, c);
         const bool live = i0 + i < n && at.live;
-        Pairs g;
-        rot_unpack<PAIRS>(du[i], dv[i], g);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {  // the other way round
-          const float2 a = g.a[e], b = g.b[e];
-          g.a[e] = __ffma2_rn(b, s[e], __fmul2_rn(a, c[e]));
-          g.b[e] = __ffma2_rn(a, neg2(s[e]), __fmul2_rn(b, c[e]));
-        }
-        if constexpr (NORM) {
-          Pairs h, w;
-          rot_unpack<PAIRS>(u[i], v[i], h);
-          float2 sq = zero;
-#pragma unroll
-          for (int e = 0; e < 4; ++e) sq = __ffma2_rn(h.b[e], h.b[e], __ffma2_rn(h.a[e], h.a[e], sq));
-          const float r1 = rsqrtf(rot_sum<S::kLanes>(sq.x + sq.y) * (1.f / D) + p.eps);
-          const float2 r = make_float2(r1, r1);
-          rot_weight<PAIRS>(sh.weight[k], lane.a, lane.b, w);
-          float2 dot2 = zero;
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            h.a[e] = __fmul2_rn(h.a[e], r);
-            h.b[e] = __fmul2_rn(h.b[e], r);
-            if (live) {
-              acc.a[e] = __ffma2_rn(g.a[e], h.a[e], acc.a[e]);
-              acc.b[e] = __ffma2_rn(g.b[e], h.b[e], acc.b[e]);
-            }
-            g.a[e] = __fmul2_rn(g.a[e], w.a[e]);
-            g.b[e] = __fmul2_rn(g.b[e], w.b[e]);
-            dot2 = __ffma2_rn(g.b[e], h.b[e], __ffma2_rn(g.a[e], h.a[e], dot2));
-          }
-          const float dot1 = rot_sum<S::kLanes>(dot2.x + dot2.y) * (-1.f / D);
-          const float2 dot = make_float2(dot1, dot1);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            g.a[e] = __fmul2_rn(__ffma2_rn(h.a[e], dot, g.a[e]), r);
-            g.b[e] = __fmul2_rn(__ffma2_rn(h.b[e], dot, g.b[e]), r);
-          }
-        }
+        rot_back<D, NORM, PAIRS, 1>(lane, sh.weight[k], p.eps, s, c, u + i, v + i, du + i, dv + i, live, acc);
         if (live) {
-          rot_pack<PAIRS>(g, du[i], dv[i]);
           __nv_bfloat16* dst = j.y + here.row * j.y_stride + here.head * D;
           *reinterpret_cast<uint4*>(dst + lane.a) = du[i];
           *reinterpret_cast<uint4*>(dst + lane.b) = dv[i];
