@@ -462,6 +462,9 @@ _i32, _f32, _bf16, _u8 = torch.int32, torch.float32, torch.bfloat16, torch.uint8
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
+
 def _current_raw_stream(index: int) -> int:
     if _raw_stream is not None:
         return _raw_stream(index)
@@ -844,17 +847,20 @@ def _side_ok(x, offsets, positions, weight, d, index) -> int:
         return 0
     if weight is not None and not _is(weight, _f32, (d,), index):
         return 0
-    return _row_stride(x, heads, d)
+    return heads * d if x.is_contiguous() else _row_stride(x, heads, d)
 
 
 def _at(t):
     return None if t is None else t.data_ptr()
 
 
-def _batch_of(pairs):
+def _batch_of(q_offsets, q_positions, k_offsets, k_positions, both):
     """The batch of the offsets in use, None if they do not agree."""
-    sizes = {o.shape[0] - 1 for o, p in pairs if p is None}
-    return None if len(sizes) > 1 else (sizes.pop() if sizes else 0)
+    k = k_offsets.shape[0] if both and k_positions is None else None
+    if q_positions is not None:
+        return 0 if k is None else k - 1
+    q = q_offsets.shape[0]
+    return q - 1 if k is None or k == q else None
 
 
 def _empty_rows(x, alloc, shape=None):
@@ -863,9 +869,10 @@ def _empty_rows(x, alloc, shape=None):
 
 
 def _out_stride(t, x, index) -> int:
-    if not (t.dtype is _bf16 and t.shape == x.shape and t.get_device() == index):
+    shape = x.shape
+    if not (t.dtype is _bf16 and t.shape == shape and t.get_device() == index):
         return 0
-    return _row_stride(t, x.shape[1], x.shape[2])
+    return shape[1] * shape[2] if t.is_contiguous() else _row_stride(t, shape[1], shape[2])
 
 
 def _refuse_out(t, name, x):
@@ -895,7 +902,7 @@ def jgdpa_norm_rotate(q, k, q_offsets, kv_offsets, inv_freq, q_weight=None, k_we
         ks = 8 if k is None else (_side_ok(k, kv_offsets, k_positions, k_weight, d, index) if ok else 0)
         qos = qs if q_out is None else _out_stride(q_out, q, index)
         kos = ks if k is None or k_out is None else _out_stride(k_out, k, index)
-        batch = _batch_of([(q_offsets, q_positions)] + ([] if k is None else [(kv_offsets, k_positions)]))
+        batch = _batch_of(q_offsets, q_positions, kv_offsets, k_positions, k is not None)
         ok = ok and qs and ks and qos and kos and batch is not None
         ok = ok and (workspace is None or _is(workspace, _u8, (workspace.numel(),), index))
         ok = ok and not (k is None and (k_out is not None or k_weight is not None))
@@ -918,7 +925,7 @@ def jgdpa_norm_rotate(q, k, q_offsets, kv_offsets, inv_freq, q_weight=None, k_we
         _contiguous(workspace=workspace)
         _need_cuda(q)
         raise ValueError("jgdpa_norm_rotate: unusable tensors")
-    if index != torch.cuda.current_device():
+    if index != _current_device():
         return _on_other_device(jgdpa_norm_rotate, q.device, (q, k, q_offsets, kv_offsets, inv_freq, q_weight, k_weight, eps,
                                 interleaved, q_positions, k_positions, q_out, k_out, workspace, stream, lib), {})
     raw, alloc = _launch_on(stream, q.device)
@@ -966,7 +973,7 @@ def jgdpa_norm_rotate_bwd(dq_out, dk_out, q, k, q_offsets, kv_offsets, inv_freq,
         ks = gks if eps is None or not both else _out_stride(k, dk_out, index)
         dqs = gqs if dq is None else _out_stride(dq, dq_out, index)
         dks = gks if dk is None or not both else _out_stride(dk, dk_out, index)
-        batch = _batch_of([(q_offsets, q_positions)] + ([(kv_offsets, k_positions)] if both else []))
+        batch = _batch_of(q_offsets, q_positions, kv_offsets, k_positions, both)
         ok = ok and gqs and gks and qs and ks and dqs and dks and batch is not None
         ok = ok and all(t is None or _is(t, _f32, (d,), index) for t in (dq_weight, dk_weight))
         ok = ok and (workspace is None or _is(workspace, _u8, (workspace.numel(),), index))
@@ -998,7 +1005,7 @@ def jgdpa_norm_rotate_bwd(dq_out, dk_out, q, k, q_offsets, kv_offsets, inv_freq,
         _contiguous(workspace=workspace, dq_weight=dq_weight, dk_weight=dk_weight)
         _need_cuda(dq_out)
         raise ValueError("jgdpa_norm_rotate_bwd: unusable tensors")
-    if index != torch.cuda.current_device():
+    if index != _current_device():
         return _on_other_device(jgdpa_norm_rotate_bwd, dq_out.device, (dq_out, dk_out, q, k, q_offsets, kv_offsets, inv_freq,
                                 q_weight, k_weight, eps, interleaved, q_positions, k_positions, dq, dk, dq_weight, dk_weight,
                                 workspace, stream, lib), {})
@@ -1103,7 +1110,7 @@ def jgdpa_cache_append_rotated(q, k_new, v_new, slots, k_cache, v_cache, q_offse
         raise ValueError("jgdpa_cache_append_rotated: unusable tensors")
     if max(rows, n) > _I32_MAX:
         _refuse_wide(**{"k_new's rows": rows, "k_cache's pages": n})
-    if index != torch.cuda.current_device():
+    if index != _current_device():
         return _on_other_device(jgdpa_cache_append_rotated, k_cache.device, (q, k_new, v_new, slots, k_cache, v_cache,
                                 q_offsets, kv_lens, inv_freq, q_weight, k_weight, eps, interleaved, depths, q_out, workspace,
                                 stream, lib), {})
@@ -1203,7 +1210,7 @@ def jgdpa_verify(target_probs, tokens, q_offsets, uniforms, draft_probs=None, pa
         raise ValueError("jgdpa_verify: unusable tensors")
     if max(total, vocab) > _I32_MAX:
         _refuse_wide(**{"target_probs' rows": total, "target_probs' columns": vocab})
-    if index != torch.cuda.current_device():
+    if index != _current_device():
         return _on_other_device(jgdpa_verify, target_probs.device, (target_probs, tokens, q_offsets, uniforms, draft_probs,
                                 parents, kv_lens, slots, workspace, stream, lib), {})
     device = target_probs.device
@@ -1212,9 +1219,12 @@ def jgdpa_verify(target_probs, tokens, q_offsets, uniforms, draft_probs=None, pa
     n = batch * (2 if kv_lens is None else 3)
     both = (n + total * (1 if slots is None else 2),)
     every = torch.empty(both, dtype=_i32, device=device) if alloc is None else alloc(both, _i32)
-    accepted, next_tokens, places = every[:batch], every[batch:2 * batch], every[n:n + total]
-    keep_lens = None if kv_lens is None else every[2 * batch:n]
-    keep_slots = None if slots is None else every[n + total:]
+    sizes = [batch, batch, n - 2 * batch, total, both[0] - n - total]
+    accepted, next_tokens, keep_lens, places, keep_slots = every.split(sizes)
+    if kv_lens is None:
+        keep_lens = None
+    if slots is None:
+        keep_slots = None
     ws, ws_bytes = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel())
     at = every.data_ptr()
     rc = lib.jgdpa_verify(target_probs.data_ptr(), ps, 1 if half else 0, _at(draft_probs), ds, 1 if draft_half else 0,
@@ -1231,11 +1241,12 @@ def jgdpa_verify(target_probs, tokens, q_offsets, uniforms, draft_probs=None, pa
 def _page_stride4(t: torch.Tensor, align: int) -> int:
     """Elements between the pages of a tensor [pages, heads, page, columns], 0 if
     its pages are not contiguous inside, overlap, or lie no multiple of align apart."""
-    _, heads, page, columns = t.shape
+    n, heads, page, columns = t.shape
     size, stride = heads * page * columns, t.stride()
-    if any(n > 1 and a != b for n, a, b in zip((heads, page, columns), stride[1:], (page * columns, columns, 1))):
+    if stride[1:] != (page * columns, columns, 1) and any(
+            k > 1 and a != b for k, a, b in zip((heads, page, columns), stride[1:], (page * columns, columns, 1))):
         return 0
-    if t.shape[0] <= 1:
+    if n <= 1:
         return size
     return stride[0] if stride[0] >= size and stride[0] % align == 0 else 0
 
@@ -1304,7 +1315,7 @@ def jgdpa_cache4_append(k_new, v_new, slots, k_codes, k_scales, v_codes, v_scale
         raise ValueError("jgdpa_cache4_append: unusable tensors")
     if max(rows, n) > _I32_MAX:
         _refuse_wide(**{"k_new's rows": rows, "k_codes' pages": n})
-    if index != torch.cuda.current_device():
+    if index != _current_device():
         return _on_other_device(jgdpa_cache4_append, k_codes.device, (k_new, v_new, slots, k_codes, k_scales, v_codes, v_scales,
                                 stream, lib), {})
     rc = lib.jgdpa_cache4_append(k_new.data_ptr(), v_new.data_ptr(), ks, vs, slots.data_ptr(), rows, k_codes.data_ptr(),
@@ -1343,7 +1354,7 @@ def jgdpa_cache4_read(k_codes, k_scales, v_codes, v_scales, slots, k_out=None, v
         raise ValueError("jgdpa_cache4_read: unusable tensors")
     if max(rows, n) > _I32_MAX:
         _refuse_wide(**{"slots": rows, "k_codes' pages": n})
-    if index != torch.cuda.current_device():
+    if index != _current_device():
         return _on_other_device(jgdpa_cache4_read, k_codes.device, (k_codes, k_scales, v_codes, v_scales, slots, k_out, v_out,
                                 stream, lib), {})
     raw, alloc = _launch_on(stream, k_codes.device)
@@ -1433,7 +1444,7 @@ def jgdpa_cache4_fwd(q, k_codes, k_scales, v_codes, v_scales, block_table, q_off
         raise ValueError("jgdpa_cache4_fwd: unusable tensors")
     if max(n, width, bias_len) > _I32_MAX:
         _refuse_wide(**{"k_codes' pages": n, "block_table's width": width, "bias_table's length": bias_len})
-    if index != torch.cuda.current_device():
+    if index != _current_device():
         return _on_other_device(jgdpa_cache4_fwd, k_codes.device, (q, k_codes, k_scales, v_codes, v_scales, block_table,
                                 q_offsets, kv_lens, act, scale, max_q, bias_table, window, tree_mask, depths, out, lse,
                                 workspace, stream, lib), {})

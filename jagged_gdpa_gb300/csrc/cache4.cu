@@ -8,12 +8,15 @@
 // in fp32, each operation rounded once (halves to even), so that the codes are
 // the same wherever they are formed.  A few operations per value: bound by HBM (2.5
 // bytes a value each way and 4 a head).  D / 16 lanes take a head, 16 columns each.
-// The quotient is q = d y with y = 1 / s rounded, corrected twice by its remainder:
-// q + (d - q s) y is the rounded quotient from a q within one last place on (P. Markstein,
-// Computation of elementary functions on the IBM RISC System/6000 processor,
-// 1990, theorem 8); halves are exact then, which values and steps of 8 bits meet
-// often.  (With 16 divisions per lane the write of 32,768 rows x 8 x 128 took 84 us.)
+// The quotient is q = d y, y = 1 / s rounded, corrected by its remainder, q + (d -
+// q s) y (after P. Markstein, Computation of elementary functions on the IBM RISC
+// System/6000 processor, 1990): the remainder is exact, as s has 8 bits, so that a quotient that is a half is met
+// exactly, which values of 8 bits often are; any other differs from a half by
+// more than the correction leaves (d - (k + 1/2) s is a multiple of d's last place, which
+// is more than s 2^-24 of the quotient's power of two), so that the code is that of the divided
+// quotient.  (With 16 divisions per lane the write of 32,768 rows x 8 x 128 took 84 us.)
 #include <algorithm>
+#include <type_traits>
 
 #include "cache4.cuh"
 #include "common.cuh"
@@ -123,20 +126,24 @@ __global__ void __launch_bounds__(kRows4Threads) cache4_append_kernel(const __gr
     const float inv = __frcp_rn(s);
     const bool usual = s >= 0x1p-100f && s <= 0x1p100f;  // (1 / s and the remainders are normal numbers)
     uint32_t code[2] = {0, 0};
+    auto form = [&](auto clamp) {
 #pragma unroll
-    for (int e = 7; e >= 0; --e) {
-      const float2 x = make_float2(__uint_as_float(w[e] << 16), __uint_as_float(w[e] & 0xFFFF0000u));
-      const float2 d = __fadd2_rn(x, make_float2(-z, -z)), y = make_float2(inv, inv), less = make_float2(-s, -s);
-      float2 q = __fmul2_rn(d, y);
-      q = __ffma2_rn(__ffma2_rn(q, less, d), y, q);
-      q = __ffma2_rn(__ffma2_rn(q, less, d), y, q);
-      q = make_float2(fminf(fmaxf(q.x, -8.f), 7.f), fminf(fmaxf(q.y, -8.f), 7.f));  // (NaN: the least)
-      const float2 t = __fadd2_rn(q, make_float2(kRound, kRound));
-      uint32_t& c = code[e >> 2];
-      c = (c * 16 + __float_as_uint(t.y)) * 16 + __float_as_uint(t.x);
-    }
-    code[0] -= kRest;
-    code[1] -= kRest;
+      for (int e = 7; e >= 0; --e) {
+        const float2 x = make_float2(__uint_as_float(w[e] << 16), __uint_as_float(w[e] & 0xFFFF0000u));
+        const float2 d = __fadd2_rn(x, make_float2(-z, -z)), y = make_float2(inv, inv);
+        float2 q = __fmul2_rn(d, y);
+        q = __ffma2_rn(__ffma2_rn(q, make_float2(-s, -s), d), y, q);
+        if (decltype(clamp)::value) q = make_float2(fminf(fmaxf(q.x, -8.f), 7.f), fminf(fmaxf(q.y, -8.f), 7.f));
+        const float2 t = __fadd2_rn(q, make_float2(kRound, kRound));
+        uint32_t& c = code[e >> 2];
+        c = (c * 16 + __float_as_uint(t.y)) * 16 + __float_as_uint(t.x);
+      }
+      code[0] -= kRest;
+      code[1] -= kRest;
+    };
+    // (the roundings of s and z take q beyond -8 - 1/2 or 7 + 1/2 only if the middle is far from zero)
+    if (__all_sync(0xffffffffu, usual && fabsf(z) < 64.f * s)) form(std::false_type{});
+    else form(std::true_type{});
     if (!usual) {
       code[0] = code[1] = 0;
 #pragma unroll
