@@ -461,7 +461,7 @@ JGDPA_API jgdpa_status jgdpa_norm_rotate_bwd(const void* dq_out, int64_t dq_out_
  *   q, q_out   bf16 rows [heads][head_dim] of the new tokens (q_out may be q); q
  *              may be NULL with heads = 0: the cache alone
  *   k_new, v_new, slots, k_cache, v_cache, ...  as in jgdpa_cache_append, the keys with norm
- *              and rotation, the values as they are
+ *              and rotation, the values as they are (of rows with the same slot, parts of either may stay)
  *   q_offsets, kv_lens, depths  as in jgdpa_cache_fwd: new token t of request b is at
  *              position kv_lens[b] - T_b + t, or + depths[its row] where depths are given
  * Rows behind q_offsets[batch] are left out.  When an accepted row moves to another slot
@@ -531,7 +531,7 @@ JGDPA_API jgdpa_status jgdpa_verify(const void* target, int64_t target_stride, i
                                     jgdpa_stream_t stream);
 
 /*
- * The paged cache held in 4 bits: 0.28 of the bf16 cache's bytes at head_dim 128.  Pages, slots and
+ * The paged cache held in 4 bits: 0.27 of the bf16 cache's bytes at head_dim 128.  Pages, slots and
  * block tables are jgdpa_cache_plan's.  Of keys, and of values:
  *   codes        uint8 [kv_heads][page_size][head_dim / 2] a page, code_stride bytes apart (a multiple
  *                of 16, at least a page): columns 2 j and 2 j + 1 in the low and high bits of byte j
@@ -540,7 +540,7 @@ JGDPA_API jgdpa_status jgdpa_verify(const void* target, int64_t target_stride, i
  * A code c stands for z + s (c - 8).
  *
  * jgdpa_cache4_append writes rows as jgdpa_cache_append does (rows with slots outside the cache are
- * skipped).  With lo and hi the least and largest of a head's values, each operation rounded to fp32,
+ * skipped; of rows with the same slot, parts of either may stay).  With lo and hi the least and largest of a head's values, each operation rounded to fp32,
  * halves to even:
  *     s = bf16((hi - lo) / 15), z = bf16(lo + 8 s), c = clamp(rint((x - z) / s), -8, 7) + 8 (8 where s is 0).
  * A head with a NaN or an infinity (or whose hi - lo leaves fp32) stands for NaN or infinities as a whole.

@@ -801,7 +801,8 @@ def jgdpa_norm_rotate_workspace_bytes(head_dim: int, for_backward: bool = False,
 
 
 def _refuse_side(x, name, off_name, offsets, positions, weight, batch, d, device):
-    """Refuses what `_side` does not take, by name."""
+    """Refuses what `_side_ok` does not take, by name."""
+    side = name.removeprefix("d").removesuffix("_out")  # q or k
     _check(x, name, torch.bfloat16, (None, None, d), device)
     _refuse_rows(x, name, x.shape[1], d)
     if positions is None:
@@ -809,10 +810,10 @@ def _refuse_side(x, name, off_name, offsets, positions, weight, batch, d, device
         if offsets.shape[0] < 1:
             raise ValueError(f"{off_name} must hold batch + 1 >= 1 entries")
     else:
-        _check(positions, f"{name[-1] if name[0] == 'd' else name}_positions", torch.int32, (x.shape[0],), device)
-    _check(weight, f"{name}_weight", torch.float32, (d,), device, optional=True)
-    _contiguous(**{off_name: None if positions is not None else offsets, f"{name}_positions": positions,
-                   f"{name}_weight": weight})
+        _check(positions, f"{side}_positions", torch.int32, (x.shape[0],), device)
+    _check(weight, f"{side}_weight", torch.float32, (d,), device, optional=True)
+    _contiguous(**{off_name: None if positions is not None else offsets, f"{side}_positions": positions,
+                   f"{side}_weight": weight})
     if x.shape[1] < 1:
         raise ValueError(f"{name} must have heads")
 
@@ -1220,7 +1221,7 @@ def jgdpa_verify(target_probs, tokens, q_offsets, uniforms, draft_probs=None, pa
     both = (n + total * (1 if slots is None else 2),)
     every = torch.empty(both, dtype=_i32, device=device) if alloc is None else alloc(both, _i32)
     sizes = [batch, batch, n - 2 * batch, total, both[0] - n - total]
-    accepted, next_tokens, keep_lens, places, keep_slots = every.split(sizes)
+    accepted, next_tokens, keep_lens, places, keep_slots = torch.split_with_sizes(every, sizes)
     if kv_lens is None:
         keep_lens = None
     if slots is None:

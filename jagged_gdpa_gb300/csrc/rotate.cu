@@ -45,10 +45,10 @@ __device__ __forceinline__ uint64_t turn_of(float f) {
   return static_cast<uint64_t>(__double2ll_rn((turns - rint(turns)) * 18446744073709551616.0));
 }
 __device__ __forceinline__ void sincos_turn(uint64_t f, int pos, float& s, float& c) {
-  // bits 32 to 63 of the product, half a turn on, as a number of [1, 2)
+  // bits 32 to 63 of the product, half a turn on, to 23 bits as a number of [1, 2)
   const uint32_t turn = static_cast<uint32_t>(pos) * static_cast<uint32_t>(f >> 32) + __umulhi(static_cast<uint32_t>(pos), static_cast<uint32_t>(f)) -
                         (pos < 0 ? static_cast<uint32_t>(f) : 0u);
-  const float x = __uint_as_float(((turn + 0x80000000u) >> 9) | 0x3F800000u) - 1.5f;
+  const float x = __uint_as_float(((turn + 0x80000100u) >> 9) | 0x3F800000u) - 1.5f;
   // [-pi, pi), where the hardware's sine and cosine are within 2^-20.9
   const float a = x * 6.283185307179586f;
   s = __sinf(a);
@@ -245,7 +245,11 @@ __device__ __forceinline__ void rot_check(const RotateParams& p) {
   bool ok = true;
   for (int k = 0; k < p.jobs; ++k) {
     const RotateJob& j = p.job[k];
-    if (j.positions != nullptr || (k > 0 && j.offsets == p.job[k - 1].offsets)) continue;
+    if (j.positions != nullptr) continue;
+    if (k > 0) {  // (the same offsets of as many rows have been looked at)
+      const RotateJob& i = p.job[k - 1];
+      if (i.positions == nullptr && i.offsets == j.offsets && i.rows == j.rows) continue;
+    }
     for (int i = threadIdx.x; i <= j.batch; i += kRotThreads) {
       const int v = j.offsets[i];
       ok = ok && (i == 0 ? v == 0 : v >= j.offsets[i - 1]) && v <= j.rows;

@@ -31,6 +31,7 @@ namespace {
 
 constexpr size_t kAlign = 256;
 constexpr int64_t kMaxStride = int64_t{1} << 39;
+constexpr int32_t kMaxBatch = 1 << 30;  // (its offsets are searched and counted in 32 bits)
 size_t up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 bool head_dim_ok(int32_t d) { return d == 32 || d == 64 || d == 128; }
@@ -75,7 +76,7 @@ jgdpa_status check_rotation(const float* inv_freq, int32_t pairs, int32_t interl
 
 jgdpa_status check_segments(int64_t rows, int32_t heads, int32_t batch, const int32_t* offsets, const int32_t* positions) {
   if (rows < 0 || batch < 0 || heads < 0 || (rows > 0 && heads < 1)) return JGDPA_ERR_INVALID_ARGUMENT;
-  if (rows > INT32_MAX || rows * std::max<int64_t>(heads, 1) > INT32_MAX) return JGDPA_ERR_UNSUPPORTED;
+  if (rows > INT32_MAX || rows * std::max<int64_t>(heads, 1) > INT32_MAX || batch > kMaxBatch) return JGDPA_ERR_UNSUPPORTED;
   if (rows > 0 && offsets == nullptr && positions == nullptr) return JGDPA_ERR_INVALID_ARGUMENT;
   if (!aligned(offsets, 4) || !aligned(positions, 4)) return JGDPA_ERR_MISALIGNED;
   return JGDPA_OK;
@@ -297,7 +298,7 @@ jgdpa_status jgdpa_cache_append_rotated(const void* q, int64_t q_stride, void* q
   }
   JG_CHECK(check_rows(k_new, k_stride, total_new, kv_heads, head_dim));
   JG_CHECK(check_rows(v_new, v_stride, total_new, kv_heads, head_dim));
-  if (static_cast<int64_t>(total_new) * std::max(heads, kv_heads) > INT32_MAX) return JGDPA_ERR_UNSUPPORTED;
+  if (static_cast<int64_t>(total_new) * std::max(heads, kv_heads) > INT32_MAX || batch > kMaxBatch) return JGDPA_ERR_UNSUPPORTED;
   if (total_new > 0 && (slots == nullptr || q_offsets == nullptr || (batch > 0 && kv_lens == nullptr)))
     return JGDPA_ERR_INVALID_ARGUMENT;
   if (!aligned(slots, 4) || !aligned(q_offsets, 4) || !aligned(kv_lens, 4) || !aligned(depths, 4))
@@ -341,7 +342,7 @@ jgdpa_status jgdpa_verify(const void* target, int64_t target_stride, int32_t tar
   if (draft != nullptr && parents != nullptr) return JGDPA_ERR_INVALID_ARGUMENT;
   if (batch > jg::kCacheMaxBatch || vocab > (1 << 30)) return JGDPA_ERR_UNSUPPORTED;
   if (target_stride < vocab || (draft != nullptr && draft_stride < vocab)) return JGDPA_ERR_INVALID_ARGUMENT;
-  if (target_stride >= kMaxStride || draft_stride >= kMaxStride) return JGDPA_ERR_UNSUPPORTED;
+  if (target_stride >= kMaxStride || (draft != nullptr && draft_stride >= kMaxStride)) return JGDPA_ERR_UNSUPPORTED;
   if (batch > 0 && (q_offsets == nullptr || accepted == nullptr || next_tokens == nullptr)) return JGDPA_ERR_INVALID_ARGUMENT;
   if (total_q > 0 && (target == nullptr || tokens == nullptr || uniforms == nullptr || places == nullptr))
     return JGDPA_ERR_INVALID_ARGUMENT;
@@ -494,8 +495,10 @@ jgdpa_status jgdpa_cache4_fwd(const void* q, int64_t q_stride, const void* k_cod
   p.window = window;
   p.rows_per_tile = jg::kCache4Rows;
   p.heads_per_item = 1;
-  p.item_cost = 8;
-  p.min_part = 2;
+  // what an item's start and end take, in tiles of 64 keys, measured (half or
+  // twice as many: up to 10% more on ragged lengths)
+  p.item_cost = head_dim == 32 ? 16 : 8;
+  p.min_part = 1;
   p.scale = act == JGDPA_ACT_SOFTMAX ? scale * jg::kLog2e : scale;
   p.wait_limit_ns = jg::host_wait_limit_ns();
   const int tile_rows = static_cast<int>(std::clamp<int64_t>(max_rows, 1, jg::kCache4Rows));  // that may live

@@ -291,7 +291,7 @@ __global__ void __launch_bounds__(kVerThreads, 2) verify_kernel(const __grid_con
   const int q0 = p.q_off[b], q1 = p.q_off[b + 1];
   const bool valid = q0 >= 0 && q1 >= q0 && q1 <= p.total && (b > 0 || q0 == 0);
   const int T = valid && q1 - q0 <= kVerifyMaxTokens ? q1 - q0 : 0;
-  if (T != q1 - q0 && tid == 0 && p.status != nullptr) atomicCAS(p.status, kOk, kErrBadOffsets);
+  if ((!valid || T != q1 - q0) && tid == 0 && p.status != nullptr) atomicCAS(p.status, kOk, kErrBadOffsets);
   if (T == 0) {  // (the whole cluster)
     if (rank == 0) {
       if (tid == 0) {

@@ -117,6 +117,7 @@ def _args(**kw):
     (dict(ko=None), 1), (dict(qs=248), 1), (dict(kos=132), 3), (dict(q=(1 << 20) + 8), 3), (dict(q_off=None), 1),
     (dict(tq=-1), 1), (dict(heads=0), 1), (dict(batch=-1), 1), (dict(tq=1 << 31), 2), (dict(tq=1 << 30), 2),
     (dict(ws=1 << 20, wsb=16), 4), (dict(ws=(1 << 20) + 16, wsb=256), 3), (dict(q_off=(1 << 20) + 2), 3), (dict(ks=1 << 40), 2),
+    (dict(batch=2 ** 31 - 1), 2),
 ])
 def test_rejects_bad_arguments_without_a_launch(jg, kw, code):
     assert jg.load().jgdpa_norm_rotate(*_args(**kw)) == code
@@ -193,6 +194,8 @@ def test_wrappers_reject_other_bad_calls(jg):
         jg.jgdpa_norm_rotate_bwd(kw["q"], kw["k"], kw["k"], kw["k"], *list(kw.values())[2:])
     with pytest.raises(ValueError, match="q is required"):
         jg.jgdpa_norm_rotate_bwd(kw["q"], kw["k"], None, None, *list(kw.values())[2:])
+    with pytest.raises(ValueError, match="^k_positions must have shape"):
+        jg.jgdpa_norm_rotate_bwd(kw["q"], kw["k"], kw["q"], kw["k"], *list(kw.values())[2:], k_positions=i32([0], "cpu"))
     cache = normal(np.random.default_rng(0), 2, 16, 2, 64, device="cpu")
     with pytest.raises(ValueError, match="depths must have dtype"):
         jg.jgdpa_cache_append_rotated(kw["q"], kw["k"], kw["k"], i32(range(5), "cpu"), cache, cache, i32([0, 5], "cpu"),
@@ -316,6 +319,18 @@ def test_bad_offsets_are_reported(jg):
             assert jg.jgdpa_read_device_status(ws) == status, off
             jg.jgdpa_norm_rotate_bwd(q, k, q, k, *offs, freq, workspace=ws)
             assert jg.jgdpa_read_device_status(ws) == status, off
+
+
+@gpu
+def test_offsets_of_queries_that_are_beyond_the_keys_are_reported(jg):
+    rng = np.random.default_rng(6)
+    x, freq, off = normal(rng, 20, 2, 64), freqs(32), i32([0, 5, 20])
+    ws = torch.empty(jg.jgdpa_norm_rotate_workspace_bytes(64, True), dtype=torch.uint8, device="cuda")
+    for q, k in ((x, x[:19]), (x[:19], x)):
+        jg.jgdpa_norm_rotate(q, k, off, off, freq, workspace=ws)
+        assert jg.jgdpa_read_device_status(ws) == 6
+        jg.jgdpa_norm_rotate_bwd(q, k, q, k, off, off, freq, workspace=ws)
+        assert jg.jgdpa_read_device_status(ws) == 6
 
 
 @gpu

@@ -291,6 +291,14 @@ def test_device_detected_errors(jg):
 
 
 @gpu
+def test_offsets_that_do_not_start_at_0_are_reported(jg):
+    p, u = torch.full((3, 10), 0.1, device="cuda"), torch.zeros(3, device="cuda")
+    ws = torch.empty(jg.jgdpa_verify_workspace_bytes(), dtype=torch.uint8, device="cuda")
+    got = jg.jgdpa_verify(p, i32([0, 0, 0]), i32([3, 3]), u, workspace=ws)  # a request without rows
+    assert jg.jgdpa_read_device_status(ws) == 6 and got[0].tolist() == [0]
+
+
+@gpu
 def test_empty_calls(jg):
     p, u = torch.full((3, 10), 0.1, device="cuda"), torch.zeros(3, device="cuda")
     got = jg.jgdpa_verify(p, i32([0, 0, 0]), i32([0]), u, kv_lens=i32([]), slots=i32([1, 2, 3]))
