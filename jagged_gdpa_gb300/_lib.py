@@ -1216,23 +1216,26 @@ def jgdpa_verify(target_probs, tokens, q_offsets, uniforms, draft_probs=None, pa
                                 parents, kv_lens, slots, workspace, stream, lib), {})
     device = target_probs.device
     raw, alloc = _launch_on(stream, device)
-    # the results as pieces of one tensor: batch entries, then total ones
-    n = batch * (2 if kv_lens is None else 3)
-    both = (n + total * (1 if slots is None else 2),)
-    every = torch.empty(both, dtype=_i32, device=device) if alloc is None else alloc(both, _i32)
-    sizes = [batch, batch, n - 2 * batch, total, both[0] - n - total]
-    accepted, next_tokens, keep_lens, places, keep_slots = torch.split_with_sizes(every, sizes)
-    if kv_lens is None:
-        keep_lens = None
-    if slots is None:
-        keep_slots = None
+    keep_lens = keep_slots = None
+    if alloc is None:  # (empty_like of a contiguous tensor: less work for the host than empty, or than pieces of one tensor)
+        like = torch.empty_like
+        accepted = torch.empty((batch,), dtype=_i32, device=device)
+        next_tokens, places = like(accepted), like(tokens)
+        if kv_lens is not None:
+            keep_lens = like(accepted)
+        if slots is not None:
+            keep_slots = like(places)
+    else:
+        accepted, next_tokens, places = alloc((batch,), _i32), alloc((batch,), _i32), alloc((total,), _i32)
+        if kv_lens is not None:
+            keep_lens = alloc((batch,), _i32)
+        if slots is not None:
+            keep_slots = alloc((total,), _i32)
     ws, ws_bytes = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel())
-    at = every.data_ptr()
     rc = lib.jgdpa_verify(target_probs.data_ptr(), ps, 1 if half else 0, _at(draft_probs), ds, 1 if draft_half else 0,
                           tokens.data_ptr(), _at(parents), uniforms.data_ptr(), q_offsets.data_ptr(), batch, total, vocab,
-                          _at(kv_lens), _at(slots), at, at + 4 * batch, at + 4 * n,
-                          None if kv_lens is None else at + 8 * batch, None if slots is None else at + 4 * (n + total),
-                          ws, ws_bytes, raw)
+                          _at(kv_lens), _at(slots), accepted.data_ptr(), next_tokens.data_ptr(), places.data_ptr(),
+                          _at(keep_lens), _at(keep_slots), ws, ws_bytes, raw)
     if rc:
         raise JgdpaError(rc, "jgdpa_verify")
     return accepted, next_tokens, places, keep_lens, keep_slots
@@ -1260,6 +1263,10 @@ def _cache4(k_codes, k_scales, v_codes, v_scales, index):
             and v_scales.shape == k_scales.shape and v_codes.get_device() == index and k_scales.get_device() == index
             and v_scales.get_device() == index):
         return None
+    if k_codes.is_contiguous() and k_scales.is_contiguous() and v_codes.is_contiguous() and v_scales.is_contiguous():
+        size = heads * page
+        strides = (size * half, 2 * size, size * half, 2 * size)
+        return (strides, n, page, heads, 2 * half) if size > 0 and size % 4 == 0 and size * half % 16 == 0 else None
     strides = (_page_stride4(k_codes, 16), _page_stride4(k_scales, 8), _page_stride4(v_codes, 16), _page_stride4(v_scales, 8))
     return (strides, n, page, heads, 2 * half) if all(strides) else None
 
@@ -1362,7 +1369,7 @@ def jgdpa_cache4_read(k_codes, k_scales, v_codes, v_scales, slots, k_out=None, v
     if k_out is None:
         k_out = _empty_rows(k_codes, alloc, shape)
     if v_out is None:
-        v_out = _empty_rows(k_codes, alloc, shape)
+        v_out = torch.empty_like(k_out) if alloc is None and k_out.is_contiguous() else _empty_rows(k_codes, alloc, shape)
     rc = lib.jgdpa_cache4_read(k_codes.data_ptr(), k_scales.data_ptr(), v_codes.data_ptr(), v_scales.data_ptr(), *strides, n,
                                page, heads, d, slots.data_ptr(), rows, k_out.data_ptr(), v_out.data_ptr(), ks, vs, raw)
     if rc:
