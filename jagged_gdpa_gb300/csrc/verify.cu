@@ -18,6 +18,12 @@
 // in the prefix sums draws another token with probability V e: in fp32 (2^-24)
 // one row in some hundred, so the sums are held as unevaluated pairs of fp32
 // (some 2^-46; FP64 runs at a sixtieth of the rate here).
+//
+// Chains of 2 to 6 with drafts' probabilities, fp32, 128,000 tokens: 64 requests 19 us
+// (the two rows 9.7 at the copy bandwidth), 256 requests 47 us, 0.81 of it.  What few
+// requests take is latency: gathers along the chain, two meetings of the cluster
+// and the second reading of a piece, some 8 to 9 us.  With one value at a time
+// instead of 16 bytes in paired sums: 28 and 79 us.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 
