@@ -9,6 +9,7 @@ import fails loudly -- there is no fallback implementation.
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
 from typing import Optional
 
@@ -794,6 +795,40 @@ def jgdpa_cache_fwd(q, k_cache, v_cache, block_table, q_offsets, kv_lens, act, s
     return out, lse
 
 
+# The calls from here on have a short way: where nothing is out of the ordinary, csrc/native.cpp
+# checks, makes the results and enters the library in one call.  It answers None to whatever
+# it does not take, and the wrapper goes on; both do the same.
+NATIVE_PATH = os.path.join(_HERE, "_build", f"_native-{torch.__version__}.so")
+_native = None
+
+
+class _NoNative:
+    def __getattr__(self, name):
+        return lambda *args: None
+
+
+def _native_calls():
+    """The native calls, loaded at the first use (none of them where they were not built)."""
+    global _native
+    lib = load()
+    if os.path.exists(NATIVE_PATH):
+        spec = importlib.util.spec_from_file_location("jagged_gdpa_gb300._native", NATIVE_PATH)
+        module = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(module)
+        if not module.use({name: ctypes.cast(getattr(lib, name), ctypes.c_void_p).value for name in EXPORTS}):
+            raise RuntimeError("the native calls do not belong to this library: build again")
+        _native = module
+    else:
+        _native = _NoNative()
+    return _native
+
+
+def _answer(got, name):
+    if type(got) is tuple:
+        return got
+    raise JgdpaError(got, name)
+
+
 # ------------------------------------------- norms of queries and keys with the rotation
 def jgdpa_norm_rotate_workspace_bytes(head_dim: int, for_backward: bool = False, lib=None) -> int:
     _refuse_wide(head_dim=head_dim)
@@ -890,6 +925,11 @@ def jgdpa_norm_rotate(q, k, q_offsets, kv_offsets, inv_freq, q_weight=None, k_we
     k [total_kv, kv_heads, head_dim] may be slices of wider rows; k None: queries
     alone.  eps None: the rotation without a norm.  Positions are those within
     the segments of q_offsets / kv_offsets, or q_positions / k_positions."""
+    if stream is None and lib is None:
+        got = (_native or _native_calls()).norm_rotate(q, k, q_offsets, kv_offsets, inv_freq, q_weight, k_weight, eps, interleaved,
+                                                       q_positions, k_positions, q_out, k_out, workspace)
+        if got is not None:
+            return _answer(got, "jgdpa_norm_rotate")
     lib = lib or load()
     eps_value = 0.0 if eps is None else float(eps)
     qs = ks = qos = kos = 0
@@ -958,6 +998,12 @@ def jgdpa_norm_rotate_bwd(dq_out, dk_out, q, k, q_offsets, kv_offsets, inv_freq,
     weight's gradient (fp32, summed over rows and heads) None where there is no
     such weight, unless a tensor for it is passed.  dk_out and k None: queries
     alone.  eps None: q and k are not read and may be None."""
+    if stream is None and lib is None:
+        got = (_native or _native_calls()).norm_rotate_bwd(dq_out, dk_out, q, k, q_offsets, kv_offsets, inv_freq, q_weight, k_weight,
+                                                           eps, interleaved, q_positions, k_positions, dq, dk, dq_weight, dk_weight,
+                                                           workspace)
+        if got is not None:
+            return _answer(got, "jgdpa_norm_rotate_bwd")
     lib = lib or load()
     eps_value = 0.0 if eps is None else float(eps)
     both = dk_out is not None
@@ -1071,6 +1117,11 @@ def jgdpa_cache_append_rotated(q, k_new, v_new, slots, k_cache, v_cache, q_offse
     tokens' queries [total_new, heads, head_dim] in the same launch (q None: the
     cache alone); returns (q_out, k_cache, v_cache).  q_offsets, kv_lens and
     depths as in jgdpa_cache_fwd; eps None: no norm."""
+    if stream is None and lib is None:
+        got = (_native or _native_calls()).cache_append_rotated(q, k_new, v_new, slots, k_cache, v_cache, q_offsets, kv_lens, inv_freq,
+                                                                q_weight, k_weight, eps, interleaved, depths, q_out, workspace)
+        if got is not None:
+            return _answer(got, "jgdpa_cache_append_rotated")
     lib = lib or load()
     eps_value = 0.0 if eps is None else float(eps)
     qs = qos = ks = vs = kps = vps = 0
@@ -1182,6 +1233,10 @@ def jgdpa_verify(target_probs, tokens, q_offsets, uniforms, draft_probs=None, pa
     draft_probs fp32 or bf16 [total_q, vocab], tokens and parents int32 [total_q],
     uniforms fp32 [total_q].  keep_lens, the next plan's ctx_lens, is None without kv_lens,
     keep_slots, where the rows that stay move to, without slots."""
+    if stream is None and lib is None:
+        got = (_native or _native_calls()).verify(target_probs, tokens, q_offsets, uniforms, draft_probs, parents, kv_lens, slots, workspace)
+        if got is not None:
+            return _answer(got, "jgdpa_verify")
     lib = lib or load()
     ps = ds = 0
     ok = False
@@ -1303,6 +1358,10 @@ def jgdpa_cache4_append(k_new, v_new, slots, k_codes, k_scales, v_codes, v_scale
     """Writes rows of k_new / v_new [total_new, kv_heads, head_dim] to their slots
     of a cache held in 4 bits: codes uint8 [num_pages, kv_heads, page_size, head_dim / 2],
     scales bf16 [num_pages, kv_heads, page_size, 2]; returns the four."""
+    if stream is None and lib is None:
+        got = (_native or _native_calls()).cache4_append(k_new, v_new, slots, k_codes, k_scales, v_codes, v_scales)
+        if got is not None:
+            return _answer(got, "jgdpa_cache4_append")
     lib = lib or load()
     got, ks, vs = None, 0, 0
     try:
@@ -1337,6 +1396,10 @@ def jgdpa_cache4_append(k_new, v_new, slots, k_codes, k_scales, v_codes, v_scale
 def jgdpa_cache4_read(k_codes, k_scales, v_codes, v_scales, slots, k_out=None, v_out=None, stream=None, lib=None):
     """The rows at `slots` of a cache held in 4 bits, as bf16 (k, v)
     [rows, kv_heads, head_dim]; zeros for slots outside the cache."""
+    if stream is None and lib is None:
+        got = (_native or _native_calls()).cache4_read(k_codes, k_scales, v_codes, v_scales, slots, k_out, v_out)
+        if got is not None:
+            return _answer(got, "jgdpa_cache4_read")
     lib = lib or load()
     got, ks, vs = None, 0, 0
     try:
@@ -1414,9 +1477,14 @@ def jgdpa_cache4_fwd(q, k_codes, k_scales, v_codes, v_scales, block_table, q_off
                      workspace=None, stream=None, lib=None):
     """jgdpa_cache_fwd over a cache held in 4 bits (jgdpa_cache4_fwd); returns
     (out, lse) with lse None unless act == 'softmax'."""
-    lib = lib or load()
     a = _act(act)
     max_q, window = int(max_q), int(window)
+    if stream is None and lib is None:
+        got = (_native or _native_calls()).cache4_fwd(q, k_codes, k_scales, v_codes, v_scales, block_table, q_offsets, kv_lens, a, scale,
+                                                      max_q, bias_table, window, tree_mask, depths, out, lse, workspace)
+        if got is not None:
+            return _answer(got, "jgdpa_cache4_fwd")
+    lib = lib or load()
     if max(max_q, window) > _I32_MAX or min(max_q, window) < -_I32_MAX:
         _refuse_wide(max_q=max_q, window=window)
     softmax = a == 2

@@ -13,6 +13,9 @@ Two libraries are built:
                             polynomial route (JGDPA_FWD_ALU_CHUNKS=4,
                             JGDPA_BWD_ALU_GROUPS=4), so that route's kernel
                             instantiations are compiled and parity-tested
+and, by g++, the Python module that makes the plain calls of csrc/native.cpp,
+one per torch version (its headers and Python's are needed; where they are
+missing there is none, and the wrappers do all calls).
 """
 
 from __future__ import annotations
@@ -22,11 +25,15 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
+
+import torch
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(BUILD, "libjgdpa.so")
+NATIVE = os.path.join(BUILD, f"_native-{torch.__version__}.so")
 HEAD_DIMS = (32, 64, 128)
 SOURCES = ["api.cu", "sched.cu", "cache_api.cu", "cache_plan.cu", "step_api.cu", "rotate.cu", "verify.cu",
            "cache4.cu"]  # compiled once
@@ -94,12 +101,32 @@ def _compile_jobs(cc: str, force: bool):
     return jobs, objs
 
 
+def _native_job(cc: str, force: bool):
+    """The command that builds the Python module, None if it is there or cannot be built."""
+    src = os.path.join(CSRC, "native.cpp")
+    top = os.path.dirname(torch.__file__)
+    include = [sysconfig.get_paths()["include"], os.path.join(top, "include"),
+               os.path.join(top, "include", "torch", "csrc", "api", "include"),
+               os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(cc))), "include")]
+    cxx = shutil.which("g++")
+    needed = [os.path.join(include[0], "Python.h"), os.path.join(include[1], "torch", "csrc", "autograd", "python_variable.h"),
+              os.path.join(include[1], "c10", "cuda", "CUDAStream.h"), os.path.join(include[3], "cuda_runtime_api.h")]
+    if cxx is None or not all(os.path.exists(p) for p in needed) or not (force or _stale(NATIVE, src)):
+        return None
+    return [cxx, "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+            *[f"-I{p}" for p in include], src, "-L" + os.path.join(top, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_cuda",
+            "-ltorch", "-ltorch_python", "-o", NATIVE + f".tmp{os.getpid()}"]
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
     """Compiles every object that is out of date (in parallel) and links both
     libraries; returns the product library's path."""
     os.makedirs(BUILD, exist_ok=True)
     cc = nvcc()
     jobs, objs = _compile_jobs(cc, force)
+    native = _native_job(cc, force)
+    if native is not None:
+        jobs.insert(0, native)
     if jobs:
         workers = max(1, min(len(jobs), os.cpu_count() or 1))
         with concurrent.futures.ThreadPoolExecutor(max_workers=workers) as ex:
@@ -108,7 +135,9 @@ def build(force: bool = False, verbose: bool = False) -> str:
             if verbose and r.stderr:
                 sys.stderr.write(r.stderr)
             if r.returncode != 0:
-                raise RuntimeError(f"nvcc failed: {' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
+                raise RuntimeError(f"compilation failed: {' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
+    if native is not None:
+        os.replace(native[-1], NATIVE)
     for v in VARIANTS:
         out = lib_path(v)
         if force or jobs or not os.path.exists(out):
