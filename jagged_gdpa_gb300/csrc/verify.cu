@@ -20,10 +20,11 @@
 // (some 2^-46; FP64 runs at a sixtieth of the rate here).
 //
 // Chains of 2 to 6 with drafts' probabilities, fp32, 128,000 tokens: 64 requests 19 us
-// (the two rows 9.7 at the copy bandwidth), 256 requests 47 us, 0.81 of it.  What few
+// (the two rows 9.7 at the copy bandwidth), 256 requests 48 us, 0.80 of it.  What few
 // requests take is latency: gathers along the chain, two meetings of the cluster
 // and the second reading of a piece, some 8 to 9 us.  With one value at a time
-// instead of 16 bytes in paired sums: 28 and 79 us.
+// instead of 16 bytes in paired sums: 28 and 79 us.  8 trees of 8 to 33 over 50,001
+// tokens: 11 us (14 with a thread per row that went through the rows before it in FP64).
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 
@@ -79,6 +80,13 @@ __device__ __forceinline__ Sum2 warp_prefix(Sum2 a) {
     const Sum2 b = shfl_up(a, o);
     if ((threadIdx.x & 31) >= o) a = add(b, a);
   }
+  return a;
+}
+
+__device__ __forceinline__ Sum2 warp_sum(Sum2 a) {
+#pragma unroll
+  for (int o = 16; o; o >>= 1)
+    a = add(a, Sum2{__shfl_xor_sync(0xffffffffu, a.hi, o), __shfl_xor_sync(0xffffffffu, a.lo, o)});
   return a;
 }
 
@@ -156,6 +164,13 @@ __device__ __forceinline__ Sum2 verify_sum_pieces(const T* p, const T* q, int lo
   };
   const int head = static_cast<int>((16 - (reinterpret_cast<uintptr_t>(p + lo) & 15)) & 15) / static_cast<int>(sizeof(T));
   const int first = min(lo + head, hi), end = first + (hi - first) / kV * kV;
+  // the row's head and tail, a lane each (fewer than 8)
+  const int rest = lane < 8 ? lo + lane : end + lane - 8;
+  float edge = 0.f;
+  if (lane < 16 && (lane < 8 ? rest < first : rest < hi) && rest != r0 && rest != r1) {
+    edge = prob(p + rest);
+    if (q != nullptr) edge = __fsub_rn(edge, prob(q + rest));
+  }
   int at = first + lane * kV;
   const uint4 none = make_uint4(0, 0, 0, 0);
 #pragma unroll 1
@@ -180,14 +195,7 @@ __device__ __forceinline__ Sum2 verify_sum_pieces(const T* p, const T* q, int lo
 #pragma unroll
     for (int i = 0; i < kWays - 1; ++i) take(part[i], a[i], b[i], at + i * 32 * kV);
   }
-  // the row's head and tail, a lane each (fewer than 8)
-  Sum2 sum{0.f, 0.f};
-  const int rest = lane < 8 ? lo + lane : end + lane - 8;
-  if (lane < 16 && (lane < 8 ? rest < first : rest < hi) && rest != r0 && rest != r1) {
-    float r = prob(p + rest);
-    if (q != nullptr) r = __fsub_rn(r, prob(q + rest));
-    sum.hi = fmaxf(r, 0.f);
-  }
+  Sum2 sum{fmaxf(edge, 0.f), 0.f};
 #pragma unroll
   for (int i = 0; i < kWays; ++i) {
     sum = add(sum, Sum2{part[i].hi.x, part[i].lo.x});
@@ -201,6 +209,7 @@ struct VerShared {
   float p[kVerifyMaxTokens];      // the parent's probability of the row's token
   float u[kVerifyMaxTokens];
   int child[kVerifyMaxTokens];    // the row's first accepted child; then its place
+  Sum2 gone[kVerifyMaxTokens];    // the probabilities of its earlier siblings
   unsigned char first[kVerifyMaxTokens], ok[kVerifyMaxTokens];
   int kept, last, n_refused;
   Sum2 piece[kVerWarps];          // sums of the CTA's pieces, read by the whole cluster
@@ -233,27 +242,36 @@ __device__ void verify_walk(const VerifyParams& p, VerShared* sh, int q0, int T)
   }
   __syncthreads();
   if (draft == nullptr) {
-    if (p.parents != nullptr) {  // (a chain has no siblings) of equal tokens the first counts
-      for (int t = tid; t < T; t += kVerThreads)
-      {
+    if (p.parents != nullptr) {  // (a chain has no siblings)
+      // a warp per row, its lanes over the earlier ones: of equal siblings the first counts
+      const int lane = tid & 31, warp = tid >> 5;
+      for (int t = 1 + warp; t < T; t += kVerWarps) {
         const int up = sh->parent[t], x = sh->token[t];
         bool twin = false;
-#pragma unroll 4
-        for (int s = 1; s < t; ++s) twin = twin || (sh->parent[s] == up && sh->token[s] == x);
-        if (twin) sh->first[t] = 0;
+        for (int s = 1 + lane; s < t; s += 32) twin = twin || (sh->parent[s] == up && sh->token[s] == x);
+        if (__any_sync(0xffffffffu, twin) && lane == 0) sh->first[t] = 0;
+      }
+      __syncthreads();
+      for (int t = 1 + warp; t < T; t += kVerWarps) {
+        if (!sh->first[t]) continue;
+        const int up = sh->parent[t];
+        Sum2 sum{0.f, 0.f};
+        bool some = false;
+        for (int s = 1 + lane; s < t; s += 32)
+          if (sh->parent[s] == up && sh->first[s]) {
+            sum = add(sum, sh->p[s]);
+            some = true;
+          }
+        if (__any_sync(0xffffffffu, some)) sum = warp_sum(sum);
+        if (lane == 0) sh->gone[t] = sum;
       }
       __syncthreads();
     }
     for (int t = tid; t < T; t += kVerThreads) {
       if (!sh->first[t]) continue;
-      double gone = 0.0;
-      if (p.parents != nullptr) {
-        const int up = sh->parent[t];
-#pragma unroll 4
-        for (int s = 1; s < t; ++s)
-          if (sh->first[s] && sh->parent[s] == up) gone += sh->p[s];
-      }
-      sh->ok[t] = sh->u[t] * (1.0 - gone) < sh->p[t];
+      double left = 1.0;
+      if (p.parents != nullptr && sh->gone[t].hi != 0.f) left -= static_cast<double>(sh->gone[t].hi) + sh->gone[t].lo;
+      sh->ok[t] = sh->u[t] * left < sh->p[t];
     }
     __syncthreads();
   }
@@ -275,6 +293,19 @@ __device__ void verify_walk(const VerifyParams& p, VerShared* sh, int q0, int T)
   __syncthreads();
 }
 
+// The rows that stay, written out.
+__device__ __forceinline__ void verify_kept(const VerifyParams& p, const VerShared* sh, int b, int q0, int T) {
+  if (threadIdx.x == 0) {
+    p.accepted[b] = sh->kept;
+    if (p.keep_lens != nullptr) p.keep_lens[b] = p.kv_lens[b] - T + sh->kept;
+  }
+  for (int t = threadIdx.x; t < T; t += kVerThreads) {
+    const int place = sh->child[t] < 0 ? -1 - sh->child[t] : -1;
+    p.places[q0 + t] = place;
+    if (p.keep_slots != nullptr) p.keep_slots[q0 + t] = place >= 0 && place != t ? p.slots[q0 + place] : -1;
+  }
+}
+
 // Rows behind the last request.
 __device__ __forceinline__ void verify_padding(const VerifyParams& p) {
   const int last = p.q_off[p.batch];
@@ -284,6 +315,57 @@ __device__ __forceinline__ void verify_padding(const VerifyParams& p) {
     p.places[r] = -1;
     if (p.keep_slots != nullptr) p.keep_slots[r] = -1;
   }
+}
+
+// The token the number falls into, of [w0, w1), by one CTA: each thread some tokens in a row.
+template <typename TP, typename TQ>
+__device__ __forceinline__ void verify_next(const VerifyParams& p, VerShared* sh, Rest<TP, TQ> rest, int b, int w0, int w1) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (rest.n_refused > 0) {
+    for (int k = tid; k < rest.n_refused; k += kVerThreads) {
+      const int x = rest.refused[k];
+      if (x >= w0 && x < w1) sh->here[atomicAdd(&sh->n_here, 1)] = x;
+    }
+    __syncthreads();
+    rest.refused = sh->here;
+    rest.n_refused = sh->n_here;
+  }
+  const int each = (w1 - w0 + kVerThreads - 1) / kVerThreads;
+  const int i0 = min(w0 + tid * each, w1), i1 = min(i0 + each, w1);
+  Sum2 sum = {0.f, 0.f};
+  for (int i = i0; i < i1; ++i) sum = add(sum, rest(i));
+  const Sum2 prefix = warp_prefix(add(sum, Sum2{0.f, 0.f}));
+  if (lane == 31) sh->warp_sum[warp] = prefix;
+  __syncthreads();
+  Sum2 before = sh->before;
+  for (int w = 0; w < warp; ++w) before = add(before, sh->warp_sum[w]);
+  const Sum2 to_here = add(before, prefix);
+  Sum2 start = shfl_up(prefix, 1);
+  start = lane == 0 ? before : add(before, start);
+  if (sum.hi > 0.f) {
+    atomicMax(&sh->last_one, tid);
+    if (above(to_here, sh->target)) atomicMin(&sh->winner, tid);
+  }
+  __syncthreads();
+  // the winner's tokens, a lane of its warp each
+  const int winner = sh->winner == INT32_MAX ? sh->last_one : sh->winner;
+  if (winner >> 5 != warp) return;
+  Sum2 run = {__shfl_sync(0xffffffffu, start.hi, winner & 31), __shfl_sync(0xffffffffu, start.lo, winner & 31)};
+  const int j0 = __shfl_sync(0xffffffffu, i0, winner & 31), j1 = __shfl_sync(0xffffffffu, i1, winner & 31);
+  int next = -1;
+  for (int j = j0; j < j1; j += 32) {
+    const float r = j + lane < j1 ? rest(j + lane) : 0.f;
+    const Sum2 sums = warp_prefix(Sum2{r, 0.f});
+    const unsigned some = __ballot_sync(0xffffffffu, r > 0.f);
+    const unsigned over = __ballot_sync(0xffffffffu, r > 0.f && above(add(run, sums), sh->target));
+    if (over != 0) {
+      next = j + __ffs(over) - 1;
+      break;
+    }
+    if (some != 0) next = j + 31 - __clz(some);
+    run = add(run, Sum2{__shfl_sync(0xffffffffu, sums.hi, 31), __shfl_sync(0xffffffffu, sums.lo, 31)});
+  }
+  if (lane == 0) p.next[b] = next;
 }
 
 template <typename TP, typename TQ>
@@ -314,18 +396,7 @@ __global__ void __launch_bounds__(kVerThreads, 2) verify_kernel(const __grid_con
     return;
   }
   verify_walk<TP, TQ>(p, &sh, q0, T);
-  const int kept = sh.kept, last = sh.last;
-  if (rank == 0) {
-    if (tid == 0) {
-      p.accepted[b] = kept;
-      if (p.keep_lens != nullptr) p.keep_lens[b] = p.kv_lens[b] - T + kept;
-    }
-    for (int t = tid; t < T; t += kVerThreads) {
-      const int place = sh.child[t] < 0 ? -1 - sh.child[t] : -1;
-      p.places[q0 + t] = place;
-      if (p.keep_slots != nullptr) p.keep_slots[q0 + t] = place >= 0 && place != t ? p.slots[q0 + place] : -1;
-    }
-  }
+  const int last = sh.last;
   Rest<TP, TQ> rest{static_cast<const TP*>(p.target) + (q0 + last) * p.target_stride, nullptr, sh.token, 0};
   if (p.draft != nullptr) {
     if (last + 1 < T) rest.q = static_cast<const TQ*>(p.draft) + (q0 + last + 1) * p.draft_stride;
@@ -395,11 +466,13 @@ __global__ void __launch_bounds__(kVerThreads, 2) verify_kernel(const __grid_con
 #pragma unroll
       for (int i = 1; i < kWays; ++i) sum = add(sum, part[i]);
     }
-#pragma unroll
-    for (int o = 16; o; o >>= 1)
-      sum = add(sum, Sum2{__shfl_xor_sync(0xffffffffu, sum.hi, o), __shfl_xor_sync(0xffffffffu, sum.lo, o)});
+    sum = warp_sum(sum);
     if (lane == 0) sh.piece[warp] = sum;
-    cluster.sync();
+    __syncwarp();
+    cluster.barrier_arrive();
+    if (rank == 0 && attempt == 0) verify_kept(p, &sh, b, q0, T);  // (while the others arrive)
+    __syncwarp();
+    cluster.barrier_wait();
     if (warp == 0) {  // the piece that the number falls into
       constexpr int kEach = kVerMaxCluster * kVerWarps / 32;
       Sum2 own[kEach], run[kEach];
@@ -448,65 +521,24 @@ __global__ void __launch_bounds__(kVerThreads, 2) verify_kernel(const __grid_con
       sh.last_one = -1;
       sh.n_here = 0;
     }
-    cluster.sync();  // the sums have been read by all
-    if (sh.win >= 0) break;
+    __syncwarp();
+    cluster.barrier_arrive();  // (the sums have been read)
+    __syncthreads();
+    if (sh.win >= 0 || attempt == 1) break;
+    cluster.barrier_wait();
     // nothing left to draw from: the row itself
     rest.q = nullptr;
     rest.n_refused = 0;
   }
+  // the CTA that the number falls into looks on; the others wait until all have read their sums
+  if (sh.win < 0 || sh.win / kVerWarps != rank) {
+    if (sh.win < 0 && rank == 0 && tid == 0) p.next[b] = -1;
+  } else {
+    verify_next<TP, TQ>(p, &sh, rest, b, piece_lo(sh.win), piece_lo(sh.win + 1));
+  }
   verify_padding(p);
-  if (sh.win < 0) {
-    if (rank == 0 && tid == 0) p.next[b] = -1;
-    return;
-  }
-  if (sh.win / kVerWarps != rank) return;
-  // this CTA's: each thread some tokens in a row
-  const int w0 = piece_lo(sh.win), w1 = piece_lo(sh.win + 1);
-  if (rest.n_refused > 0) {
-    for (int k = tid; k < rest.n_refused; k += kVerThreads) {
-      const int x = rest.refused[k];
-      if (x >= w0 && x < w1) sh.here[atomicAdd(&sh.n_here, 1)] = x;
-    }
-    __syncthreads();
-    rest.refused = sh.here;
-    rest.n_refused = sh.n_here;
-  }
-  const int each = (w1 - w0 + kVerThreads - 1) / kVerThreads;
-  const int i0 = min(w0 + tid * each, w1), i1 = min(i0 + each, w1);
-  Sum2 sum = {0.f, 0.f};
-  for (int i = i0; i < i1; ++i) sum = add(sum, rest(i));
-  const Sum2 prefix = warp_prefix(add(sum, Sum2{0.f, 0.f}));
-  if (lane == 31) sh.warp_sum[warp] = prefix;
-  __syncthreads();
-  Sum2 before = sh.before;
-  for (int w = 0; w < warp; ++w) before = add(before, sh.warp_sum[w]);
-  const Sum2 to_here = add(before, prefix);
-  Sum2 start = shfl_up(prefix, 1);
-  start = lane == 0 ? before : add(before, start);
-  if (sum.hi > 0.f) {
-    atomicMax(&sh.last_one, tid);
-    if (above(to_here, sh.target)) atomicMin(&sh.winner, tid);
-  }
-  __syncthreads();
-  // the winner's tokens, a lane of its warp each
-  const int winner = sh.winner == INT32_MAX ? sh.last_one : sh.winner;
-  if (winner >> 5 != warp) return;
-  Sum2 run = {__shfl_sync(0xffffffffu, start.hi, winner & 31), __shfl_sync(0xffffffffu, start.lo, winner & 31)};
-  const int j0 = __shfl_sync(0xffffffffu, i0, winner & 31), j1 = __shfl_sync(0xffffffffu, i1, winner & 31);
-  int next = -1;
-  for (int j = j0; j < j1; j += 32) {
-    const float r = j + lane < j1 ? rest(j + lane) : 0.f;
-    const Sum2 sums = warp_prefix(Sum2{r, 0.f});
-    const unsigned some = __ballot_sync(0xffffffffu, r > 0.f);
-    const unsigned over = __ballot_sync(0xffffffffu, r > 0.f && above(add(run, sums), sh.target));
-    if (over != 0) {
-      next = j + __ffs(over) - 1;
-      break;
-    }
-    if (some != 0) next = j + 31 - __clz(some);
-    run = add(run, Sum2{__shfl_sync(0xffffffffu, sums.hi, 31), __shfl_sync(0xffffffffu, sums.lo, 31)});
-  }
-  if (lane == 0) p.next[b] = next;
+  __syncwarp();
+  cluster.barrier_wait();
 }
 
 template <typename TP, typename TQ>
