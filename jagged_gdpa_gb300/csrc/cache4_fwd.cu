@@ -26,15 +26,14 @@
 //   V is bf16, as P has its range: 128 + c is 128's bits with c in its last four, less 136.
 // Every warp works by itself, on blocks of 32 keys
 // that it copies (cp.async) into a ring of its own, a few blocks ahead: no
-// barrier but an item's end.  The order of columns within a product and of keys within
-// a block is free, so both are chosen such that a lane's codes come in one load
-// per key and turn into operands by shifts and masks:
-//   K: row n of 8 of a product is key (n / 2) + 4 (n % 2), and lane t of a key's
-//      four takes columns D / 4 t and on; nibbles i and i + 4 of a word side by side
-//   V: lane g of a key's eight takes columns D / 8 g and on; two keys' words are
-//      put together by halves, nibble i of both side by side.
+// barrier but an item's end.
+//   K: lane t of a key's four takes columns D / 4 t and on, in one load; the order of columns within a
+//      product is free, so nibbles i and i + 4 of a word go side by side, masked where they stand.
+//   V: a transposing matrix load gives a lane the same four columns of two keys side by side; what is
+//      left is a shift and a mask per nibble (with loads key by key and a
+//      permutation of bytes: 82 us for 79, 95 for 88 at D = 32).
 //
-// 64 single tokens over up to 8,192 tokens each (8 x 4 heads, D = 128, softmax): 82 us, 0.47
+// 64 single tokens over up to 8,192 tokens each (8 x 4 heads, D = 128, softmax): 79 us, 0.48
 // of the copy bandwidth (the bf16 cache's bytes alone would take 145).  Bound by instructions:
 // some 680 per block and warp, of them about 190 for V's operands, 110 for K's, 32 products,
 // and what a score takes.  Parts alone: copies 52 us, without V's products 62, without K's 72.  Measured slower:
@@ -129,11 +128,18 @@ __device__ __forceinline__ uint32_t c4_half2(float lo, float hi) {
 }
 // Where four columns of O's row lie in a warp's part of shared memory: no bank
 // conflicts, neither as the fragments are written (8 lanes: 4 rows 2 apart, 2
-// places D / 32 apart) nor as rows are read.
+// places side by side) nor as rows are read.
 template <int D>
 __device__ __forceinline__ int c4_place(int row, int q4) {
-  const int t = (row >> 1) & 3;
-  return row * (D / 4) + (q4 ^ (D == 128 ? t : D == 64 ? (t & 1) | ((t & 2) << 1) : t << 1));
+  return row * (D / 4) + (q4 ^ (row & 6));
+}
+// Four 8 x 8 matrices of 16-bit values: a lane's two of each are column lane / 4 of rows
+// 2 (lane % 4) and the next; lanes 8 i to 8 i + 7 name matrix i's rows.
+__device__ __forceinline__ void c4_matrices(uint32_t addr, uint32_t (&x)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3])
+               : "r"(addr)
+               : "memory");
 }
 
 // NQ: columns of query rows, by 8.
@@ -188,14 +194,15 @@ __global__ void __launch_bounds__(kC4Warps * 32, cache4_ctas(D, NQ)) cache4_fwd_
       return id;
     };
     // A block's copies: a half of 16 keys lies in one page, side by side.
+    auto v_turn = [](int key) { return D == 128 ? (key >> 1) & 3 : D == 64 ? (key >> 2) & 1 : 0; };
     constexpr int kPieces = C::kRow / 16;                   // of a key
     constexpr int kHalf = 16 * kPieces;                     // of 16 keys' codes
     constexpr int kEach = kHalf >= 32 ? kHalf / 32 : 1;     // of them a lane's
     // A lane's place in a half's codes (with kHalf = 16 lanes 16 and on take the second half): key and piece,
-    // and where they go: K's keys in the order of their products, V's pieces turned by key.
+    // and where they go: V's pieces turned by key, so that one piece of 8 keys is read without bank conflicts.
     const int c_key = lane / kPieces, c_piece = lane % kPieces;
-    const int k_to = ((c_key & ~7) | ((c_key & 3) << 1) | ((c_key >> 2) & 1)) * C::kRow + 16 * c_piece;
-    const int v_to = C::kCodes + c_key * C::kRow + 16 * (D == 128 ? c_piece ^ (c_key & 2) : c_piece);
+    const int k_to = c_key * C::kRow + 16 * c_piece;
+    const int v_to = C::kCodes + c_key * C::kRow + 16 * (c_piece ^ v_turn(c_key));
     // a lane's places in the head's part of page 0: codes, and (lanes 0 to 7 K's, 8 to 15 V's) scales of four keys
     const int64_t head_at = static_cast<int64_t>(w.h) << p.page_shift;
     const uint8_t* const k_lane = pp.k.codes + head_at * C::kRow + 16 * (kHalf >= 32 ? lane : lane & 15);
@@ -325,16 +332,16 @@ __global__ void __launch_bounds__(kC4Warps * 32, cache4_ctas(D, NQ)) cache4_fwd_
     }
 
     int stage = 0;
+    const int v_key = (lane & 7) + 8 * (lane / 8 / kPieces);
+    const int v_lane_at = v_key * C::kRow + 16 * ((lane / 8) % kPieces ^ v_turn(v_key));
 #pragma unroll 1
     for (; kb < blocks_end; kb += kC4Warps) {
       c4_wait<C::kStages - 1>();
       __syncwarp();
       const uint32_t kt = ring + stage * C::kStage, vt = kt + C::kCodes, ks = vt + C::kCodes, vs = ks + kC4Block * 4;
       // everything of the block that is read, at once: what follows is cut by branches, across which loads do not move
-      constexpr int WV = D >= 64 ? D / 64 : 1;
-      const int own = (g >> 1) + 4 * (g & 1);  // a lane's keys: of every 16 two, e = 0 and 1
-      auto key_of = [&](int kk, int e) { return 16 * kk + 8 * e + own; };
-      uint32_t k_word[4][WK], k_scale[4], v_scale[4], v_word[8][WV];
+      auto key_of = [&](int kk, int e) { return 16 * kk + 8 * e + g; };  // a lane's keys
+      uint32_t k_word[4][WK], k_scale[4], v_scale[4], v_word[kPieces][4];
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         c4_words<WK>(kt + (8 * e + g) * C::kRow + tig * (4 * WK), k_word[e]);
@@ -342,18 +349,9 @@ __global__ void __launch_bounds__(kC4Warps * 32, cache4_ctas(D, NQ)) cache4_fwd_
       }
 #pragma unroll
       for (int e = 0; e < 4; ++e) v_scale[e] = c4_word(vs + 4 * key_of(e >> 1, e & 1));
+      // matrix i of a read: piece i % kPieces of the 8 keys 8 (i / kPieces) and on
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {  // columns D / 8 g and on of keys tig, tig + 4 ..
-        const int key = tig + 4 * i;
-        const uint32_t at = vt + key * C::kRow;
-        if constexpr (D == 128) c4_words<2>(at + (((g >> 1) ^ (key & 2)) << 4) + ((g & 1) << 3), v_word[i]);
-        else if constexpr (D == 64) c4_words<1>(at + 4 * g, v_word[i]);
-        else {
-          unsigned short x;
-          asm volatile("ld.shared.u16 %0, [%1];" : "=h"(x) : "r"(at + 2 * g) : "memory");
-          v_word[i][0] = x;
-        }
-      }
+      for (int i = 0; i < kPieces; ++i) c4_matrices(vt + v_lane_at + i * (4 / kPieces) * 8 * C::kRow, v_word[i]);
       const int key0 = kb * kC4Block;
       const bool far = p.bias_len == 0 || (!hides && key0 + kC4Block - 1 < r.C && pos_min - (key0 + kC4Block - 1) >= reach);
       bool plain = key0 + kC4Block - 1 < r.C && (p.window <= 0 || pos_max - key0 < p.window);
@@ -542,19 +540,17 @@ __global__ void __launch_bounds__(kC4Warps * 32, cache4_ctas(D, NQ)) cache4_fwd_
           for (int n = 0; n < NQ; ++n) pb[n][e] = c4_transpose(pack_bf16(y[2 * n], y[2 * n + 1]));
         }
 #pragma unroll
-        for (int j = 0; j < WV; ++j)
+        for (int c = 0; c < kPieces; ++c) {  // 32 columns
+          // (8 keys' piece c is number kPieces (2 kk) + c of the matrices read)
+          constexpr int kP = kPieces;
+          const uint32_t x = v_word[(kP * 2 * kk + c) / 4][(kP * 2 * kk + c) % 4], y = v_word[(kP * (2 * kk + 1) + c) / 4][(kP * (2 * kk + 1) + c) % 4];
 #pragma unroll
-          for (int u = 0; u < (D >= 64 ? 2 : 1); ++u) {
-            const uint32_t sel = u == 0 ? 0x5410 : 0x7632;
-            const uint32_t x = __byte_perm(v_word[4 * kk][j], v_word[4 * kk + 1][j], sel);
-            const uint32_t y = __byte_perm(v_word[4 * kk + 2][j], v_word[4 * kk + 3][j], sel);
+          for (int i = 0; i < 2; ++i) {  // nibbles 2 i and 2 i + 1: columns 32 c + 4 g + 2 i and + 1
+            const uint32_t a[4] = {c4_pair(x >> (8 * i)), c4_pair(x >> (8 * i + 4)), c4_pair(y >> (8 * i)), c4_pair(y >> (8 * i + 4))};
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {  // nibbles 2 i and 2 i + 1: columns D / 8 g + 2 mt and + 1
-              const uint32_t a[4] = {c4_pair(x >> (8 * i)), c4_pair(x >> (8 * i + 4)), c4_pair(y >> (8 * i)), c4_pair(y >> (8 * i + 4))};
-#pragma unroll
-              for (int n = 0; n < NQ; ++n) c4_mma_v(o[n][4 * j + 2 * u + i], a, pb[n][0], pb[n][1]);
-            }
+            for (int n = 0; n < NQ; ++n) c4_mma_v(o[n][2 * c + i], a, pb[n][0], pb[n][1]);
           }
+        }
       }
       __syncwarp();  // the block has been read
       const int2 next_ids = pages_of(kb + (C::kStages + 1) * kC4Warps);
@@ -579,7 +575,7 @@ __global__ void __launch_bounds__(kC4Warps * 32, cache4_ctas(D, NQ)) cache4_fwd_
 #pragma unroll
       for (int c = 0; c < D / 32; ++c) {
         const float(&a)[4] = o[i >> 1][2 * c], (&b)[4] = o[i >> 1][2 * c + 1];
-        *reinterpret_cast<float4*>(mine + 4 * c4_place<D>(row, (D / 32) * g + c)) =
+        *reinterpret_cast<float4*>(mine + 4 * c4_place<D>(row, 8 * c + g)) =
             make_float4(a[i & 1] + pz[i], a[2 + (i & 1)] + pz[i], b[i & 1] + pz[i], b[2 + (i & 1)] + pz[i]);
       }
     }
