@@ -33,12 +33,14 @@
 //      left is a shift and a mask per nibble (with loads key by key and a
 //      permutation of bytes: 82 us for 79, 95 for 88 at D = 32).
 //
-// 64 single tokens over up to 8,192 tokens each (8 x 4 heads, D = 128, softmax): 79 us, 0.48
+// 64 single tokens over up to 8,192 tokens each (8 x 4 heads, D = 128, softmax): 78 us, 0.49
 // of the copy bandwidth (the bf16 cache's bytes alone would take 145).  Bound by instructions:
-// some 680 per block and warp, of them about 190 for V's operands, 110 for K's, 32 products,
-// and what a score takes.  Parts alone: copies 52 us, without V's products 62, without K's 72.  Measured slower:
+// some 630 per block and warp, of them about 180 for V's operands, 110 for K's, 32 products,
+// and what a score takes (in fp32 pairs; one by one 1.5% more).  Copies alone take 52 us.  Measured slower:
+// four chains of K's products for two (84 for 82),
 // a fifth CTA per SM at the price of spills (127), V's shifts by multiplication
-// (86 for 83), blocks of 64 keys (77 here, but 74 for 64 on short contexts and 115 for 104 at D = 32).
+// (86 for 83), blocks of 64 keys (before the last two steps: 77 for 82 here, but 74 for 64 on short
+// contexts and 115 for 104 at D = 32).
 #include <cuda_fp16.h>
 
 #include "act.cuh"
@@ -415,10 +417,15 @@ __global__ void __launch_bounds__(kC4Warps * 32, cache4_ctas(D, NQ)) cache4_fwd_
         for (int e = 0; e < 2; ++e) {
           const float2 k = c4_scale(k_scale[2 * kk + e]);
           const float step = k.x * (4096.f * scale), middle = __fmaf_rn(-8.f, k.x, k.y) * scale;
+          const float2 step2 = make_float2(step, step), middle2 = make_float2(middle, middle);
 #pragma unroll
-          for (int i = 0; i < R2; ++i) {
-            float& x = s[i >> 1][kk][2 * e + (i & 1)];
-            x = __fmaf_rn(x * q_unit[i], step, __fmaf_rn(middle, q_sum[i], far_bias[i]));
+          for (int n = 0; n < NQ; ++n) {
+            float* x = &s[n][kk][2 * e];
+            const float2 y = __ffma2_rn(__fmul2_rn(make_float2(x[0], x[1]), make_float2(q_unit[2 * n], q_unit[2 * n + 1])), step2,
+                                        __ffma2_rn(middle2, make_float2(q_sum[2 * n], q_sum[2 * n + 1]),
+                                                   make_float2(far_bias[2 * n], far_bias[2 * n + 1])));
+            x[0] = y.x;
+            x[1] = y.y;
           }
         }
       if (!far) {
@@ -489,16 +496,21 @@ __global__ void __launch_bounds__(kC4Warps * 32, cache4_ctas(D, NQ)) cache4_fwd_
           }
         }
 #pragma unroll
-        for (int i = 0; i < R2; ++i) {
-          const float ref = m[i] == -INFINITY ? 0.f : m[i];
+        for (int n = 0; n < NQ; ++n) {
+          const float2 ref = make_float2(m[2 * n] == -INFINITY ? 0.f : -m[2 * n], m[2 * n + 1] == -INFINITY ? 0.f : -m[2 * n + 1]);
+          float2 sum = make_float2(l[2 * n], l[2 * n + 1]);
 #pragma unroll
           for (int kk = 0; kk < 2; ++kk)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              float& x = s[i >> 1][kk][2 * e + (i & 1)];
-              x = ex2_sfu(x - ref);
-              l[i] += x;
+              float* x = &s[n][kk][2 * e];
+              const float2 y = __fadd2_rn(make_float2(x[0], x[1]), ref);
+              x[0] = ex2_sfu(y.x);
+              x[1] = ex2_sfu(y.y);
+              sum = __fadd2_rn(sum, make_float2(x[0], x[1]));
             }
+          l[2 * n] = sum.x;
+          l[2 * n + 1] = sum.y;
         }
       } else {
 #pragma unroll
@@ -522,10 +534,14 @@ __global__ void __launch_bounds__(kC4Warps * 32, cache4_ctas(D, NQ)) cache4_fwd_
           float y[R2];
           if (plain) {
 #pragma unroll
-            for (int i = 0; i < R2; ++i) {
-              const float weight = s[i >> 1][kk][2 * e + (i & 1)];
-              y[i] = weight * v.x;
-              pz[i] = __fmaf_rn(weight, v.y, pz[i]);
+            for (int n = 0; n < NQ; ++n) {
+              const float2 weight = make_float2(s[n][kk][2 * e], s[n][kk][2 * e + 1]);
+              const float2 a = __fmul2_rn(weight, make_float2(v.x, v.x));
+              const float2 b = __ffma2_rn(weight, make_float2(v.y, v.y), make_float2(pz[2 * n], pz[2 * n + 1]));
+              y[2 * n] = a.x;
+              y[2 * n + 1] = a.y;
+              pz[2 * n] = b.x;
+              pz[2 * n + 1] = b.y;
             }
           } else {  // (a place that the row does not see may hold any step and middle)
 #pragma unroll
