@@ -33,7 +33,7 @@
 //      left is a shift and a mask per nibble (with loads key by key and a
 //      permutation of bytes: 82 us for 79, 95 for 88 at D = 32).
 //
-// 64 single tokens over up to 8,192 tokens each (8 x 4 heads, D = 128, softmax): 78 us, 0.49
+// 64 single tokens over up to 8,192 tokens each (8 x 4 heads, D = 128, softmax): 81 us, 0.48
 // of the copy bandwidth (the bf16 cache's bytes alone would take 145).  Bound by instructions:
 // some 630 per block and warp, of them about 180 for V's operands, 110 for K's, 32 products,
 // and what a score takes (in fp32 pairs; one by one 1.5% more).  Copies alone take 52 us.  Measured slower:
@@ -41,7 +41,10 @@
 // a fifth CTA per SM at the price of spills (127), V's shifts by multiplication
 // (86 for 83), blocks of 64 keys (before the last two steps: 77 for 82 here, but 74 for 64 on short
 // contexts and 115 for 104 at D = 32).
+#include <cuda_bf16.h>
 #include <cuda_fp16.h>
+
+#include <cfloat>
 
 #include "act.cuh"
 #include "cache4.cuh"
@@ -54,6 +57,10 @@ constexpr int kC4Keys = 64;    // tokens per tile of the work division
 constexpr int kC4Block = 32;   // keys of a warp's step
 constexpr int kC4Warps = 4;
 constexpr int kC4Rows = kCache4Rows;
+// With up to so many keys (GELU and SiLU, whose sums nothing divides: four times) P s is held in two
+// operands (one key: errors of 1.3 to 1.6 roundings of the result otherwise).  The branches cost long
+// contexts 2 us in 81, one for all 32 keys in place of two 2 more.
+constexpr int kC4Fine = 64;
 constexpr int kC4MinRange = 5;  // the least length of a range
 
 template <int D, int NQ>
@@ -333,6 +340,7 @@ __global__ void __launch_bounds__(kC4Warps * 32, cache4_ctas(D, NQ)) cache4_fwd_
       l[i] = pz[i] = 0.f;
     }
 
+    const bool fine = min(r.L, p.window > 0 ? p.window : r.L) <= (ACT == 2 ? kC4Fine : 4 * kC4Fine);
     int stage = 0;
     const int v_key = (lane & 7) + 8 * (lane / 8 / kPieces);
     const int v_lane_at = v_key * C::kRow + 16 * ((lane / 8) % kPieces ^ v_turn(v_key));
@@ -526,7 +534,8 @@ __global__ void __launch_bounds__(kC4Warps * 32, cache4_ctas(D, NQ)) cache4_fwd_
       }
 #pragma unroll
       for (int kk = 0; kk < 2; ++kk) {  // 16 keys
-        // P s rounds to bf16 as an operand (half a step, 2^-8 of each at most)
+        // P s rounds to bf16 as an operand (half a step, 2^-8 of each at most); where few
+        // keys count these do not average out, and a second operand holds the rest
         uint32_t pb[NQ][2];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
@@ -565,6 +574,34 @@ __global__ void __launch_bounds__(kC4Warps * 32, cache4_ctas(D, NQ)) cache4_fwd_
             const uint32_t a[4] = {c4_pair(x >> (8 * i)), c4_pair(x >> (8 * i + 4)), c4_pair(y >> (8 * i)), c4_pair(y >> (8 * i + 4))};
 #pragma unroll
             for (int n = 0; n < NQ; ++n) c4_mma_v(o[n][2 * c + i], a, pb[n][0], pb[n][1]);
+          }
+        }
+        if (fine) {  // what P s lost by rounding
+          uint32_t pl[NQ][2];
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const float step = c4_scale(v_scale[2 * kk + e]).x;
+#pragma unroll
+            for (int n = 0; n < NQ; ++n) {
+              float rest[2];
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {
+                const float y = s[n][kk][2 * e + i] * step, d = y - __bfloat162float(__float2bfloat16_rn(y));
+                rest[i] = ((see[2 * n + i] >> key_of(kk, e)) & 1) && fabsf(d) <= FLT_MAX ? d : 0.f;  // (none of an infinity)
+              }
+              pl[n][e] = c4_transpose(pack_bf16(rest[0], rest[1]));
+            }
+          }
+#pragma unroll
+          for (int c = 0; c < kPieces; ++c) {
+            constexpr int kP = kPieces;
+            const uint32_t x = v_word[(kP * 2 * kk + c) / 4][(kP * 2 * kk + c) % 4], y = v_word[(kP * (2 * kk + 1) + c) / 4][(kP * (2 * kk + 1) + c) % 4];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const uint32_t a[4] = {c4_pair(x >> (8 * i)), c4_pair(x >> (8 * i + 4)), c4_pair(y >> (8 * i)), c4_pair(y >> (8 * i + 4))};
+#pragma unroll
+              for (int n = 0; n < NQ; ++n) c4_mma_v(o[n][2 * c + i], a, pl[n][0], pl[n][1]);
+            }
           }
         }
       }

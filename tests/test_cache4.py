@@ -514,3 +514,20 @@ def test_same_bits_in_graphs_and_on_other_streams(jg):
         graph.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(o, a) for o, a in zip(outs, alone))
+
+
+@gpu
+@pytest.mark.parametrize("d", [32, 64, 128])
+def test_a_single_key_loses_no_more_than_its_rounding(jg, d):
+    """With one key a softmax gives the value that its codes stand for, rounded to bf16 once (half a step, 2^-8 of
+    it); of the codes' part, 8 s at most, two bf16 operands lose 2^-16, and fp32 steps less than that again."""
+    rng = np.random.default_rng(d)
+    n, heads = 40, 2
+    pages = [torch.from_numpy(rng.integers(0, 256, (n, heads, 16, d // 2), dtype=np.uint8)).cuda() for _ in range(2)]
+    scales = [normal(rng, n, heads, 16, 2) for _ in range(2)]
+    out, _ = jg.jgdpa_cache4_fwd(normal(rng, n, heads, d), pages[0], scales[0], pages[1], scales[1], i32(np.arange(n)[:, None]),
+                                 i32(np.arange(n + 1)), i32(np.ones(n)), "softmax", 1.0, max_q=1)
+    c, sz = pages[1].cpu().numpy()[:, :, 0].astype(np.int64), scales[1].double().cpu().numpy()[:, :, 0]
+    v = sz[..., 1:] + sz[..., :1] * (np.stack([c & 15, c >> 4], -1).reshape(n, heads, d) - 8)
+    bad = ~(np.abs(out.double().cpu().numpy() - v) <= U * np.abs(v) + 2.0 ** -15 * 8 * np.abs(sz[..., :1]))
+    assert not bad.any(), f"{bad.sum()} of {bad.size}"
