@@ -35,7 +35,7 @@
 //
 // 64 single tokens over up to 8,192 tokens each (8 x 4 heads, D = 128, softmax): 81 us, 0.48
 // of the copy bandwidth (the bf16 cache's bytes alone would take 145).  Bound by instructions:
-// some 630 per block and warp, of them about 180 for V's operands, 110 for K's, 32 products,
+// some 655 per block and warp, of them about 180 for V's operands, 110 for K's, 32 products,
 // and what a score takes (in fp32 pairs; one by one 1.5% more).  Copies alone take 52 us.  Measured slower:
 // four chains of K's products for two (84 for 82),
 // a fifth CTA per SM at the price of spills (127), V's shifts by multiplication
