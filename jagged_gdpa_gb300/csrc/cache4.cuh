@@ -18,6 +18,7 @@ namespace jg {
 // Query rows per item of the attention kernel, and its CTAs per SM with 8 nq of
 // them (at D = 128 two sets of columns take 168 registers a thread).
 constexpr int kCache4Rows = 16;
+constexpr int kCache4MinRange = 5;  // the least length of a CTA's range on the line of items
 __host__ __device__ constexpr int cache4_ctas(int d, int nq) { return d == 128 ? 4 - nq : nq == 2 ? 3 : d == 64 ? 4 : 5; }
 inline int cache4_columns(int64_t rows) { return rows <= 8 ? 1 : 2; }
 

@@ -61,7 +61,6 @@ constexpr int kC4Rows = kCache4Rows;
 // operands (one key: errors of 1.3 to 1.6 roundings of the result otherwise).  The branches cost long
 // contexts 2 us in 81, one for all 32 keys in place of two 2 more.
 constexpr int kC4Fine = 64;
-constexpr int kC4MinRange = 5;  // the least length of a range
 
 template <int D, int NQ>
 struct C4Cfg {
@@ -166,7 +165,7 @@ __global__ void __launch_bounds__(kC4Warps * 32, cache4_ctas(D, NQ)) cache4_fwd_
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, tig = lane & 3;
   int* status = p.err + blockIdx.x;
   if (tid == 0) *status = kOk;
-  const CacheRange R = cache_range<kC4Keys>(p, &sh.range, kC4MinRange);
+  const CacheRange R = cache_range<kC4Keys>(p, &sh.range, kCache4MinRange);
   if (tid == 0) cache_open<kC4Keys>(p, R);
   const uint32_t ring = smem_u32(smem) + warp * C::kRing, q_at = smem_u32(smem) + C::kQOff + warp * C::kQ + lane * 16;
   const int reach = (p.bias_len - 1) / 2;

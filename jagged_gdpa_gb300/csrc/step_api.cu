@@ -501,6 +501,11 @@ jgdpa_status jgdpa_cache4_fwd(const void* q, int64_t q_stride, const void* k_cod
   p.min_part = 1;
   p.scale = act == JGDPA_ACT_SOFTMAX ? scale * jg::kLog2e : scale;
   p.wait_limit_ns = jg::host_wait_limit_ns();
+  // no more CTAs than the longest line that these sizes allow has ranges
+  const double tiles = std::ceil(static_cast<double>(table_width) * page_size / 64);
+  const double row_tiles = std::ceil(static_cast<double>(max_rows) / jg::kCache4Rows);
+  const double ranges = std::ceil(static_cast<double>(batch) * kv_heads * row_tiles * (p.item_cost + tiles) / jg::kCache4MinRange);
+  if (ranges < grid) grid = std::max(1, static_cast<int>(ranges));
   const int tile_rows = static_cast<int>(std::clamp<int64_t>(max_rows, 1, jg::kCache4Rows));  // that may live
   auto launch = [&](auto dim) -> cudaError_t {
     constexpr int D = decltype(dim)::value;
