@@ -24,6 +24,11 @@
 //     times the power of two that brings its largest value to 2^14 (what falls
 //     below fp16 then is 2^-38 of that), the columns of high nibbles times 2^-4 more.
 //   V is bf16, as P has its range: 128 + c is 128's bits with c in its last four, less 136.
+//   P s goes in two bf16 operands, its rounding and what that leaves: in one (2^-8 of each term) errors
+//      average out over many keys that count alike, but where few carry the weight (a peaked softmax of
+//      any length, a prompt's first rows) results had 1.05 to 1.4 times the error of one rounding, and
+//      by the number of keys such rows cannot be told.  With both 1.00 times; 85 us for 81, 35 for 32 on trees of
+//      up to 32 rows (d = 64, GELU), 224 for 199 on trees of 64 rows (d = 128).
 // Every warp works by itself, on blocks of 32 keys
 // that it copies (cp.async) into a ring of its own, a few blocks ahead: no
 // barrier but an item's end.
@@ -33,18 +38,14 @@
 //      left is a shift and a mask per nibble (with loads key by key and a
 //      permutation of bytes: 82 us for 79, 95 for 88 at D = 32).
 //
-// 64 single tokens over up to 8,192 tokens each (8 x 4 heads, D = 128, softmax): 81 us, 0.48
-// of the copy bandwidth (the bf16 cache's bytes alone would take 145).  Bound by instructions:
-// some 655 per block and warp, of them about 180 for V's operands, 110 for K's, 32 products,
-// and what a score takes (in fp32 pairs; one by one 1.5% more).  Copies alone take 52 us.  Measured slower:
-// four chains of K's products for two (84 for 82),
+// 64 single tokens over up to 8,192 tokens each (8 x 4 heads, D = 128, softmax): 85 us, 0.45
+// of the copy bandwidth (the bf16 cache's bytes alone would take 145).  Copies alone take 52 us.  Measured slower
+// (before the second operand): four chains of K's products for two (84 for 82),
 // a fifth CTA per SM at the price of spills (127), V's shifts by multiplication
 // (86 for 83), blocks of 64 keys (before the last two steps: 77 for 82 here, but 74 for 64 on short
 // contexts and 115 for 104 at D = 32).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
-
-#include <cfloat>
 
 #include "act.cuh"
 #include "cache4.cuh"
@@ -57,10 +58,6 @@ constexpr int kC4Keys = 64;    // tokens per tile of the work division
 constexpr int kC4Block = 32;   // keys of a warp's step
 constexpr int kC4Warps = 4;
 constexpr int kC4Rows = kCache4Rows;
-// With up to so many keys (GELU and SiLU, whose sums nothing divides: four times) P s is held in two
-// operands (one key: errors of 1.3 to 1.6 roundings of the result otherwise).  The branches cost long
-// contexts 2 us in 81, one for all 32 keys in place of two 2 more.
-constexpr int kC4Fine = 64;
 
 template <int D, int NQ>
 struct C4Cfg {
@@ -339,7 +336,6 @@ __global__ void __launch_bounds__(kC4Warps * 32, cache4_ctas(D, NQ)) cache4_fwd_
       l[i] = pz[i] = 0.f;
     }
 
-    const bool fine = min(r.L, p.window > 0 ? p.window : r.L) <= (ACT == 2 ? kC4Fine : 4 * kC4Fine);
     int stage = 0;
     const int v_key = (lane & 7) + 8 * (lane / 8 / kPieces);
     const int v_lane_at = v_key * C::kRow + 16 * ((lane / 8) % kPieces ^ v_turn(v_key));
@@ -533,21 +529,18 @@ __global__ void __launch_bounds__(kC4Warps * 32, cache4_ctas(D, NQ)) cache4_fwd_
       }
 #pragma unroll
       for (int kk = 0; kk < 2; ++kk) {  // 16 keys
-        // P s rounds to bf16 as an operand (half a step, 2^-8 of each at most); where few
-        // keys count these do not average out, and a second operand holds the rest
-        uint32_t pb[NQ][2];
+        // P s as two bf16 operands, its rounding and what that leaves (2^-16 of it at most)
+        uint32_t pb[NQ][2], pl[NQ][2];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           const float2 v = c4_scale(v_scale[2 * kk + e]);
-          float y[R2];
+          float2 y[NQ];
           if (plain) {
 #pragma unroll
             for (int n = 0; n < NQ; ++n) {
               const float2 weight = make_float2(s[n][kk][2 * e], s[n][kk][2 * e + 1]);
-              const float2 a = __fmul2_rn(weight, make_float2(v.x, v.x));
+              y[n] = __fmul2_rn(weight, make_float2(v.x, v.x));
               const float2 b = __ffma2_rn(weight, make_float2(v.y, v.y), make_float2(pz[2 * n], pz[2 * n + 1]));
-              y[2 * n] = a.x;
-              y[2 * n + 1] = a.y;
               pz[2 * n] = b.x;
               pz[2 * n + 1] = b.y;
             }
@@ -556,52 +549,35 @@ __global__ void __launch_bounds__(kC4Warps * 32, cache4_ctas(D, NQ)) cache4_fwd_
             for (int i = 0; i < R2; ++i) {
               const float weight = s[i >> 1][kk][2 * e + (i & 1)];
               const bool sees = (see[i] >> key_of(kk, e)) & 1;
-              y[i] = sees ? weight * v.x : 0.f;
+              (i & 1 ? y[i >> 1].y : y[i >> 1].x) = sees ? weight * v.x : 0.f;
               if (sees) pz[i] = __fmaf_rn(weight, v.y, pz[i]);
             }
           }
 #pragma unroll
-          for (int n = 0; n < NQ; ++n) pb[n][e] = c4_transpose(pack_bf16(y[2 * n], y[2 * n + 1]));
+          for (int n = 0; n < NQ; ++n) {
+            const uint32_t top = pack_bf16(y[n].x, y[n].y);
+            const float2 rest = __ffma2_rn(c4_scale(top), make_float2(-1.f, -1.f), y[n]);  // (of an infinity: NaN)
+            pb[n][e] = c4_transpose(top);
+            pl[n][e] = c4_transpose(pack_bf16(rest.x, rest.y));
+          }
         }
 #pragma unroll
         for (int c = 0; c < kPieces; ++c) {  // 32 columns
           // (8 keys' piece c is number kPieces (2 kk) + c of the matrices read)
           constexpr int kP = kPieces;
           const uint32_t x = v_word[(kP * 2 * kk + c) / 4][(kP * 2 * kk + c) % 4], y = v_word[(kP * (2 * kk + 1) + c) / 4][(kP * (2 * kk + 1) + c) % 4];
+          uint32_t a[2][4];  // nibbles 2 i and 2 i + 1: columns 32 c + 4 g + 2 i and + 1
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {  // nibbles 2 i and 2 i + 1: columns 32 c + 4 g + 2 i and + 1
-            const uint32_t a[4] = {c4_pair(x >> (8 * i)), c4_pair(x >> (8 * i + 4)), c4_pair(y >> (8 * i)), c4_pair(y >> (8 * i + 4))};
+          for (int i = 0; i < 2; ++i) {
+            a[i][0] = c4_pair(x >> (8 * i)), a[i][1] = c4_pair(x >> (8 * i + 4));
+            a[i][2] = c4_pair(y >> (8 * i)), a[i][3] = c4_pair(y >> (8 * i + 4));
 #pragma unroll
-            for (int n = 0; n < NQ; ++n) c4_mma_v(o[n][2 * c + i], a, pb[n][0], pb[n][1]);
-          }
-        }
-        if (fine) {  // what P s lost by rounding
-          uint32_t pl[NQ][2];
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const float step = c4_scale(v_scale[2 * kk + e]).x;
-#pragma unroll
-            for (int n = 0; n < NQ; ++n) {
-              float rest[2];
-#pragma unroll
-              for (int i = 0; i < 2; ++i) {
-                const float y = s[n][kk][2 * e + i] * step, d = y - __bfloat162float(__float2bfloat16_rn(y));
-                rest[i] = ((see[2 * n + i] >> key_of(kk, e)) & 1) && fabsf(d) <= FLT_MAX ? d : 0.f;  // (none of an infinity)
-              }
-              pl[n][e] = c4_transpose(pack_bf16(rest[0], rest[1]));
-            }
+            for (int n = 0; n < NQ; ++n) c4_mma_v(o[n][2 * c + i], a[i], pb[n][0], pb[n][1]);
           }
 #pragma unroll
-          for (int c = 0; c < kPieces; ++c) {
-            constexpr int kP = kPieces;
-            const uint32_t x = v_word[(kP * 2 * kk + c) / 4][(kP * 2 * kk + c) % 4], y = v_word[(kP * (2 * kk + 1) + c) / 4][(kP * (2 * kk + 1) + c) % 4];
+          for (int i = 0; i < 2; ++i)
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              const uint32_t a[4] = {c4_pair(x >> (8 * i)), c4_pair(x >> (8 * i + 4)), c4_pair(y >> (8 * i)), c4_pair(y >> (8 * i + 4))};
-#pragma unroll
-              for (int n = 0; n < NQ; ++n) c4_mma_v(o[n][2 * c + i], a, pl[n][0], pl[n][1]);
-            }
-          }
+            for (int n = 0; n < NQ; ++n) c4_mma_v(o[n][2 * c + i], a[i], pl[n][0], pl[n][1]);
         }
       }
       __syncwarp();  // the block has been read
