@@ -11,6 +11,7 @@ from __future__ import annotations
 import ctypes
 import importlib.util
 import os
+import warnings
 from typing import Optional
 
 import torch
@@ -798,7 +799,6 @@ def jgdpa_cache_fwd(q, k_cache, v_cache, block_table, q_offsets, kv_lens, act, s
 # The calls from here on have a short way: where nothing is out of the ordinary, csrc/native.cpp
 # checks, makes the results and enters the library in one call.  It answers None to whatever
 # it does not take, and the wrapper goes on; both do the same.
-NATIVE_PATH = os.path.join(_HERE, "_build", f"_native-{torch.__version__}.so")
 _native = None
 
 
@@ -808,18 +808,24 @@ class _NoNative:
 
 
 def _native_calls():
-    """The native calls, loaded at the first use (none of them where they were not built)."""
+    """The native calls, loaded at the first use (none of them where there is no module that fits)."""
     global _native
-    lib = load()
-    if os.path.exists(NATIVE_PATH):
-        spec = importlib.util.spec_from_file_location("jagged_gdpa_gb300._native", NATIVE_PATH)
-        module = importlib.util.module_from_spec(spec)
-        spec.loader.exec_module(module)
-        if not module.use({name: ctypes.cast(getattr(lib, name), ctypes.c_void_p).value for name in EXPORTS}):
-            raise RuntimeError("the native calls do not belong to this library: build again")
-        _native = module
-    else:
-        _native = _NoNative()
+    from . import build
+    lib, path, why = load(), build.native_path(), None
+    _native = _NoNative()
+    if os.path.exists(path):
+        try:
+            spec = importlib.util.spec_from_file_location("jagged_gdpa_gb300._native", path)
+            module = importlib.util.module_from_spec(spec)
+            spec.loader.exec_module(module)
+            if module.use({name: ctypes.cast(getattr(lib, name), ctypes.c_void_p).value for name in EXPORTS}):
+                _native = module
+            else:
+                why = "it does not know this library"
+        except (ImportError, OSError) as e:
+            why = e
+        if why is not None:
+            warnings.warn(f"the wrappers do the native calls of {path}: {why}", RuntimeWarning, stacklevel=3)
     return _native
 
 

@@ -14,26 +14,27 @@ Two libraries are built:
                             JGDPA_BWD_ALU_GROUPS=4), so that route's kernel
                             instantiations are compiled and parity-tested
 and, by g++, the Python module that makes the plain calls of csrc/native.cpp,
-one per torch version (its headers and Python's are needed; where they are
-missing there is none, and the wrappers do all calls).
+one per torch version, interpreter and text of the sources (its name holds them).
+It is extra: without torch's and Python's headers, or where they do not compile,
+there is none, and the wrappers do all calls.
 """
 
 from __future__ import annotations
 
 import concurrent.futures
+import hashlib
 import os
 import shutil
 import subprocess
 import sys
 import sysconfig
-
-import torch
+import warnings
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(BUILD, "libjgdpa.so")
-NATIVE = os.path.join(BUILD, f"_native-{torch.__version__}.so")
+HEADER = os.path.join(os.path.dirname(HERE), "include", "jgdpa.h")
 HEAD_DIMS = (32, 64, 128)
 SOURCES = ["api.cu", "sched.cu", "cache_api.cu", "cache_plan.cu", "step_api.cu", "rotate.cu", "verify.cu",
            "cache4.cu"]  # compiled once
@@ -65,8 +66,7 @@ def _stale(obj: str, src: str) -> bool:
     if not os.path.exists(obj):
         return True
     t = os.path.getmtime(obj)
-    deps = [src, __file__] + [os.path.join(CSRC, h) for h in HEADERS] + \
-        [os.path.join(HERE, "..", "include", "jgdpa.h")]
+    deps = [src, __file__, HEADER] + [os.path.join(CSRC, h) for h in HEADERS]
     return any(os.path.getmtime(d) > t for d in deps if os.path.exists(d))
 
 
@@ -101,8 +101,23 @@ def _compile_jobs(cc: str, force: bool):
     return jobs, objs
 
 
+def native_path() -> str:
+    """Where the module of the plain calls lies that fits this interpreter, its torch and these sources."""
+    import torch
+    text = hashlib.sha256()
+    for path in (HEADER, os.path.join(CSRC, "native.cpp")):
+        if os.path.exists(path):
+            with open(path, "rb") as f:
+                text.update(f.read())
+    return os.path.join(BUILD, f"_native-{torch.__version__}-{sysconfig.get_config_var('SOABI')}-{text.hexdigest()[:12]}.so")
+
+
 def _native_job(cc: str, force: bool):
-    """The command that builds the Python module, None if it is there or cannot be built."""
+    """The command that builds the module (its last word is the file), None if it is there or cannot be built."""
+    try:
+        import torch
+    except ImportError:
+        return None
     src = os.path.join(CSRC, "native.cpp")
     top = os.path.dirname(torch.__file__)
     include = [sysconfig.get_paths()["include"], os.path.join(top, "include"),
@@ -111,11 +126,12 @@ def _native_job(cc: str, force: bool):
     cxx = shutil.which("g++")
     needed = [os.path.join(include[0], "Python.h"), os.path.join(include[1], "torch", "csrc", "autograd", "python_variable.h"),
               os.path.join(include[1], "c10", "cuda", "CUDAStream.h"), os.path.join(include[3], "cuda_runtime_api.h")]
-    if cxx is None or not all(os.path.exists(p) for p in needed) or not (force or _stale(NATIVE, src)):
+    out = native_path()
+    if cxx is None or not all(os.path.exists(p) for p in needed) or (os.path.exists(out) and not force):
         return None
     return [cxx, "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
             *[f"-I{p}" for p in include], src, "-L" + os.path.join(top, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_cuda",
-            "-ltorch", "-ltorch_python", "-o", NATIVE + f".tmp{os.getpid()}"]
+            "-ltorch", "-ltorch_python", "-o", out + f".tmp{os.getpid()}"]
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
@@ -125,19 +141,22 @@ def build(force: bool = False, verbose: bool = False) -> str:
     cc = nvcc()
     jobs, objs = _compile_jobs(cc, force)
     native = _native_job(cc, force)
-    if native is not None:
-        jobs.insert(0, native)
-    if jobs:
-        workers = max(1, min(len(jobs), os.cpu_count() or 1))
+    if jobs or native is not None:
+        workers = max(1, min(len(jobs) + 1, os.cpu_count() or 1))
         with concurrent.futures.ThreadPoolExecutor(max_workers=workers) as ex:
-            results = list(ex.map(lambda c: subprocess.run(c, capture_output=True, text=True), jobs))
+            results = list(ex.map(lambda c: subprocess.run(c, capture_output=True, text=True),
+                                  ([] if native is None else [native]) + jobs))
+        if native is not None:
+            r = results.pop(0)
+            if r.returncode == 0:
+                os.replace(native[-1], native_path())
+            else:
+                warnings.warn(f"no native calls, the wrappers do them: {' '.join(native)}\n{r.stdout}\n{r.stderr}", RuntimeWarning, stacklevel=2)
         for cmd, r in zip(jobs, results):
             if verbose and r.stderr:
                 sys.stderr.write(r.stderr)
             if r.returncode != 0:
-                raise RuntimeError(f"compilation failed: {' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
-    if native is not None:
-        os.replace(native[-1], NATIVE)
+                raise RuntimeError(f"nvcc failed: {' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
     for v in VARIANTS:
         out = lib_path(v)
         if force or jobs or not os.path.exists(out):
