@@ -505,7 +505,8 @@ JGDPA_API jgdpa_status jgdpa_cache_append_rotated(const void* q, int64_t q_strid
  * does, the next token is drawn from max(target - draft, 0) of the row and its refused child (each difference in fp32), or
  * from target without the refused tokens, or from target where no row was refused (or nothing
  * is left): the least i whose sum of entries 0 .. i exceeds u times the sum of all.  Sums
- * are kept to some 2^-46.  Entries that are negative, infinite or NaN count nothing.
+ * are kept to some 2^-46.  Entries of target that are negative, infinite or NaN count as 0, in what stays and
+ * in what is drawn, and so do such differences.  A token whose draft entry is NaN or +infinity does not stay.
  *   accepted     int32 [batch]: rows that stay, row 0 among them (0 of a request without rows)
  *   next_tokens  int32 [batch], -1 of a request without rows and where the whole row holds nothing
  *   places       int32 [total_q]: a row's place among those that stay (0: the

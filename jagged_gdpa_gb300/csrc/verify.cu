@@ -93,6 +93,9 @@ __device__ __forceinline__ Sum2 warp_sum(Sum2 a) {
 __device__ __forceinline__ float prob(const float* p) { return *p; }
 __device__ __forceinline__ float prob(const __nv_bfloat16* p) { return __bfloat162float(*p); }
 
+// (An entry that is negative, infinite or NaN counts nothing.)
+__device__ __forceinline__ float counted(float r) { return r > 0.f && r <= 3.402823466e38f ? r : 0.f; }
+
 // What is left of a row's distribution at token i.
 template <typename TP, typename TQ>
 struct Rest {
@@ -105,7 +108,7 @@ struct Rest {
     if (q != nullptr) r = __fsub_rn(r, prob(q + i));
     for (int k = 0; k < n_refused; ++k)
       if (refused[k] == i) return 0.f;
-    return r > 0.f && r <= 3.402823466e38f ? r : 0.f;  // (a NaN or an infinity counts nothing)
+    return counted(r);
   }
 };
 
@@ -230,7 +233,7 @@ __device__ void verify_walk(const VerifyParams& p, VerShared* sh, int q0, int T)
     const float u = p.uniforms[q0 + t];
     const bool valid = t > 0 && up >= 0 && up < t && x >= 0 && x < p.vocab;
     if (t > 0 && !valid && p.status != nullptr) atomicCAS(p.status, kOk, kErrBadOffsets);
-    const float pt = valid ? prob(target + (q0 + up) * p.target_stride + x) : 0.f;
+    const float pt = valid ? counted(prob(target + (q0 + up) * p.target_stride + x)) : 0.f;
     const float qt = valid && draft != nullptr ? prob(draft + (q0 + t) * p.draft_stride + x) : 0.f;
     sh->token[t] = x;
     sh->parent[t] = valid ? up : -1;
@@ -238,7 +241,7 @@ __device__ void verify_walk(const VerifyParams& p, VerShared* sh, int q0, int T)
     sh->first[t] = valid;
     sh->p[t] = pt;
     sh->u[t] = u;
-    sh->ok[t] = draft != nullptr && valid && static_cast<double>(u) * qt < pt;
+    sh->ok[t] = draft != nullptr && pt > 0.f && static_cast<double>(u) * qt < pt;
   }
   __syncthreads();
   if (draft == nullptr) {

@@ -56,7 +56,7 @@ def positions(offsets, rows):
 
 def verify(target, tokens, offsets, uniforms, draft=None, parents=None):
     """(accepted, next, places), a request at a time.  target and draft hold
-    fp32 values as float64."""
+    fp32 values as float64.  Entries of target below zero, infinite or NaN count as 0."""
     accepted, following, places = [], [], np.full(len(tokens), -1, np.int64)
     for lo, hi in zip(offsets[:-1], offsets[1:]):
         if lo == hi:
@@ -73,12 +73,13 @@ def verify(target, tokens, offsets, uniforms, draft=None, parents=None):
             places[lo + at] = n
             n += 1
             p, gone, step = target[lo + at], set(), None
+            counts = lambda x: float(p[x]) if 0 < p[x] < math.inf else 0.0  # noqa: E731
             for t in children[at]:
-                x, u = tokens[lo + t], uniforms[lo + t]
+                x, u = tokens[lo + t], float(uniforms[lo + t])
                 if draft is not None:
-                    stays = u * draft[lo + t][x] < p[x]
+                    stays = u * float(draft[lo + t][x]) < counts(x) > 0
                 else:
-                    stays = x not in gone and u * (1 - math.fsum(p[g] for g in gone)) < p[x]
+                    stays = x not in gone and u * (1 - math.fsum(counts(g) for g in gone)) < counts(x)
                 if stays:
                     step = t
                     break
