@@ -519,7 +519,8 @@ JGDPA_API jgdpa_status jgdpa_cache_append_rotated(const void* q, int64_t q_strid
  *                jgdpa_cache4_append; needs slots [total_q], the plan's
  * Rows behind q_offsets[batch] get -1.  Outputs must not overlap inputs.  The same bits on every run.
  * Device-detected errors (workspace of jgdpa_verify_workspace_bytes() bytes, or NULL): BAD_OFFSETS (offsets not in order
- * from 0 or beyond total_q, more than 1024 rows: such a request counts as one without rows;
+ * from 0 or beyond total_q, more than 1024 rows: such a request counts as one without rows; a row that several
+ * requests then claim holds -1 or what one of them makes of it;
  * parents that are no earlier row, tokens outside the vocabulary: such a row does not stay).
  */
 JGDPA_API size_t jgdpa_verify_workspace_bytes(void);

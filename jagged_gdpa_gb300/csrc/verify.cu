@@ -309,10 +309,11 @@ __device__ __forceinline__ void verify_kept(const VerifyParams& p, const VerShar
   }
 }
 
-// Rows behind the last request.
+// Rows behind the last request.  (Offsets that are out of order lead from row 0 to here in steps of which
+// the forward ones are some request's rows and the rest these, so that every row is written.)
 __device__ __forceinline__ void verify_padding(const VerifyParams& p) {
-  const int last = p.q_off[p.batch];
-  if (last < 0 || last >= p.total) return;
+  const int last = max(p.q_off[p.batch], 0);
+  if (last >= p.total) return;
   for (int64_t r = last + static_cast<int64_t>(blockIdx.x) * kVerThreads + threadIdx.x; r < p.total;
        r += static_cast<int64_t>(gridDim.x) * kVerThreads) {
     p.places[r] = -1;
@@ -390,7 +391,8 @@ __global__ void __launch_bounds__(kVerThreads, 2) verify_kernel(const __grid_con
         p.next[b] = -1;
         if (p.keep_lens != nullptr) p.keep_lens[b] = p.kv_lens[b];
       }
-      for (int r = q0 + tid; valid && r < q1; r += kVerThreads) {
+      const int64_t begin = b == 0 ? 0 : max(q0, 0), end = min(q1, p.total);  // (64 bits: offsets of 2^31 - 1)
+      for (int64_t r = begin + tid; r < end; r += kVerThreads) {
         p.places[r] = -1;
         if (p.keep_slots != nullptr) p.keep_slots[r] = -1;
       }
