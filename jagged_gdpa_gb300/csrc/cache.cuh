@@ -390,8 +390,8 @@ struct CcRow {
 // weight itself from about -3 on: a long context whose bias pushes most scores
 // there would add up noise.)
 //   GELU(x) = max(x, 0) - a Phi(-a), a = |x|, with log2 Phi(-a) as a polynomial
-//     on [0, 13] (Phi within 1.9e-3, csrc/fit_constants.py; beyond it a Phi(-a) is
-//     below 2^-122; degree 7, within 5.2e-4, took 2% more time in the 128-row kernel)
+//     on [0, 13] (csrc/fit_constants.py; beyond it a Phi(-a) is below 2^-122): of degree 6, Phi within
+//     1.9e-3 (degree 7, within 5.2e-4, took 2% more time in the 128-row kernel), or 8, within 1.5e-4
 //   SiLU(x) = x / (1 + 2^(-x log2 e))
 // NaN stays NaN.
 __device__ __forceinline__ float max_nan(float a, float b) {
@@ -404,20 +404,22 @@ __device__ __forceinline__ float rcp_sfu(float x) {
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-template <int ACT>
+template <int ACT, int DEG = 6>
 __device__ __forceinline__ float2 cc_act2(float2 hx) {
   if constexpr (ACT == 0) {
-    constexpr float c[7] = {-1.00261784f,  -1.1279366f,     -0.492554843f, -0.0349358097f,
-                            0.0033006093f, -0.000168592655f, 3.53243581e-06f};
+    constexpr float c6[7] = {-1.00261784f,  -1.1279366f,     -0.492554843f, -0.0349358097f,
+                             0.0033006093f, -0.000168592655f, 3.53243581e-06f};
+    constexpr float c8[9] = {-1.00016737f,    -1.14921916f,    -0.462455243f,    -0.0510253534f, 0.00749332923f,
+                             -0.00075733976f, 4.89184131e-05f, -1.80116172e-06f, 2.86048483e-08f};
+    static_assert(DEG == 6 || DEG == 8, "degrees with constants");
     // n = -a / 2: 2 Phi(-a) = 2^(1 + c0 - 2 c1 n + 4 c2 n^2 ..), and hx + |hx| = max(x, 0)
     const float2 n = make_float2(max_nan(-fabsf(hx.x), -6.5f), max_nan(-fabsf(hx.y), -6.5f));
-    float2 w = f2(64.f * c[6]);
-    w = __ffma2_rn(w, n, f2(-32.f * c[5]));
-    w = __ffma2_rn(w, n, f2(16.f * c[4]));
-    w = __ffma2_rn(w, n, f2(-8.f * c[3]));
-    w = __ffma2_rn(w, n, f2(4.f * c[2]));
-    w = __ffma2_rn(w, n, f2(-2.f * c[1]));
-    w = __ffma2_rn(w, n, f2(1.f + c[0]));
+    float2 w = f2(0.f);
+#pragma unroll
+    for (int k = DEG; k >= 0; --k) {
+      const float ck = (k % 2 ? -1.f : 1.f) * static_cast<float>(1 << k) * (DEG == 6 ? c6[k % 7] : c8[k]) + (k == 0 ? 1.f : 0.f);
+      w = k == DEG ? f2(ck) : __ffma2_rn(w, n, f2(ck));
+    }
     return __ffma2_rn(n, make_float2(ex2_sfu(w.x), ex2_sfu(w.y)), make_float2(hx.x + fabsf(hx.x), hx.y + fabsf(hx.y)));
   } else {
     const float2 w = __fmul2_rn(hx, f2(-2.f * kLog2e));

@@ -26,9 +26,11 @@
 //   V is bf16, as P has its range: 128 + c is 128's bits with c in its last four, less 136.
 //   P s goes in two bf16 operands, its rounding and what that leaves: in one (2^-8 of each term) errors
 //      average out over many keys that count alike, but where few carry the weight (a peaked softmax of
-//      any length, a prompt's first rows) results had 1.05 to 1.4 times the error of one rounding, and
+//      any length, a prompt's first rows) results had up to 1.25 times the error of one rounding, and
 //      by the number of keys such rows cannot be told.  With both 1.00 times; 85 us for 81, 35 for 32 on trees of
 //      up to 32 rows (d = 64, GELU), 224 for 199 on trees of 64 rows (d = 128).
+//   GELU's Phi is right to 1.5e-4 (1.9e-3, as in the bf16 kernels, is as much as the result's own rounding:
+//      1.45 to 1.65 times its error at scores near -2 and -4.5; trees 34.6 us for 35.3).
 // Every warp works by itself, on blocks of 32 keys
 // that it copies (cp.async) into a ring of its own, a few blocks ahead: no
 // barrier but an item's end.
@@ -522,7 +524,7 @@ __global__ void __launch_bounds__(kC4Warps * 32, cache4_ctas(D, NQ)) cache4_fwd_
           for (int kk = 0; kk < 2; ++kk)
 #pragma unroll
             for (int e = 0; e < 4; e += 2) {
-              const float2 y = cc_act2<ACT>(make_float2(s[n][kk][e], s[n][kk][e + 1]));
+              const float2 y = cc_act2<ACT, 8>(make_float2(s[n][kk][e], s[n][kk][e + 1]));
               s[n][kk][e] = y.x;
               s[n][kk][e + 1] = y.y;
             }

@@ -23,7 +23,7 @@ from scipy.optimize import linprog, minimize
 from scipy.special import erf, expit, log_ndtr
 
 DEG = 3
-LOG_PHI_DEG = 6
+LOG_PHI_DEGS = (6, 8)
 LOG_PHI_END = 13.0
 
 
@@ -76,7 +76,7 @@ def fit_rcp_seed():
     return best
 
 
-def fit_log2_phi(deg=LOG_PHI_DEG, end=LOG_PHI_END, n=2000):
+def fit_log2_phi(deg, end=LOG_PHI_END, n=2000):
     a = end / 2 * (1.0 - np.cos(np.pi * np.arange(n) / (n - 1)))
     y = log_ndtr(-a) / np.log(2.0)
     V = np.vander(a / end, deg + 1, increasing=True)
@@ -100,6 +100,7 @@ if __name__ == "__main__":
     print(f"exp2 degree {DEG} on [-1/2, 1/2]: " + ", ".join(f"{v:.9g}" for v in c) + f"  (max rel err {e:.3e})")
     k, e = fit_rcp_seed()
     print(f"reciprocal seed K = 0x{k:08X}  (max rel err {e:.3e}; two Newton steps: {e**4:.3e})")
-    c, e, last = fit_log2_phi()
-    print(f"log2 Phi(-a) degree {LOG_PHI_DEG} on [0, {LOG_PHI_END:g}]: " + ", ".join(f"{v:.9g}" for v in c) +
-          f"  (max rel err of Phi {e:.3e}; exponent {last:.2f} at the end)")
+    for deg in LOG_PHI_DEGS:
+        c, e, last = fit_log2_phi(deg)
+        print(f"log2 Phi(-a) degree {deg} on [0, {LOG_PHI_END:g}]: " + ", ".join(f"{v:.9g}" for v in c) +
+              f"  (max rel err of Phi {e:.3e}; exponent {last:.2f} at the end)")
