@@ -424,7 +424,9 @@ JGDPA_API jgdpa_status jgdpa_cache_fwd(const void* q, int64_t q_stride, const vo
  *   workspace  where a device-detected error is to be read from
  *              (jgdpa_norm_rotate_workspace_bytes(head_dim, 0) bytes), or NULL
  * Device-detected errors: BAD_OFFSETS (offsets not in order from 0, or beyond the rows); the
- * outputs are then unspecified.  fp32 throughout, one rounding at the end.
+ * outputs are then unspecified.  fp32 throughout, one rounding at the end.  (So a head's sum of squares has to be
+ * an fp32 number: heads with values of some 2^60 and more, or with eps = 0 of nothing but values below 2^-60, are
+ * unspecified, gradients included.)
  *
  * Backward, from dq_out and dk_out (rows as q and k; strides of their own):
  *   dq, dk     the gradients of q and k; either may be its dq_out / dk_out, or its q / k

@@ -16,7 +16,9 @@
 namespace jg {
 
 // Query rows per item of the attention kernel, and its CTAs per SM with 8 nq of
-// them (at D = 128 two sets of columns take 168 registers a thread).
+// them: as many as registers allow (D = 128: 157 to 160 a thread with one set of columns, 226 to
+// 241 with two, whose 84 KB of shared memory a third CTA would not find either; D = 64: 114 to 125
+// and 165 to 168; D = 32: 91 to 96 and 141 to 160).
 constexpr int kCache4Rows = 16;
 constexpr int kCache4MinRange = 5;  // the least length of a CTA's range on the line of items
 __host__ __device__ constexpr int cache4_ctas(int d, int nq) { return d == 128 ? 4 - nq : nq == 2 ? 3 : d == 64 ? 4 : 5; }

@@ -41,7 +41,11 @@
 //      permutation of bytes: 82 us for 79, 95 for 88 at D = 32).
 //
 // 64 single tokens over up to 8,192 tokens each (8 x 4 heads, D = 128, softmax): 85 us, 0.45
-// of the copy bandwidth (the bf16 cache's bytes alone would take 145).  Copies alone take 52 us.  Measured slower
+// of the copy bandwidth (the bf16 cache's bytes alone would take 145).  Bound by latency at few warps: 12 per
+// SM by registers, 0.83 of them ready per scheduler and cycle, each taking one block after the other.  Of the 5.3
+// cycles per instruction 1.5 are fixed latencies, 0.6 another warp's turn, 0.5 each the integer unit and copies
+// and tables; nothing is full (issue slots 52%, integer unit 49%, DRAM 42%, matrix unit 27%).  Some 740 instructions
+// per block and warp; copies alone take 52 us.  Measured slower
 // (before the second operand): four chains of K's products for two (84 for 82),
 // a fifth CTA per SM at the price of spills (127), V's shifts by multiplication
 // (86 for 83), blocks of 64 keys (before the last two steps: 77 for 82 here, but 74 for 64 on short

@@ -23,7 +23,10 @@
 // (the two rows 9.7 at the copy bandwidth), 256 requests 48 us, 0.80 of it.  What few
 // requests take is latency: gathers along the chain, two meetings of the cluster
 // and the second reading of a piece, some 8 to 9 us.  With one value at a time
-// instead of 16 bytes in paired sums: 28 and 79 us.  8 trees of 8 to 33 over 50,001
+// instead of 16 bytes in paired sums: 28 and 79 us.  That (with 8 loads at once) is still the way of rows of
+// target and draft that lie otherwise in their 16 bytes, which contiguous rows do unless the vocabulary is a
+// multiple of 4 (fp32) or 8 (bf16), and of types that differ: 23 and 55 us at 128,001 tokens in fp32; in bf16 20
+// and 48 us, where 128,000 tokens take 16 and 34.  8 trees of 8 to 33 over 50,001
 // tokens: 11 us (14 with a thread per row that went through the rows before it in FP64).
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
