@@ -822,7 +822,7 @@ def _native_calls():
                 _native = module
             else:
                 why = "it does not know this library"
-        except (ImportError, OSError) as e:
+        except (ImportError, OSError, SystemError) as e:
             why = e
         if why is not None:
             warnings.warn(f"the wrappers do the native calls of {path}: {why}", RuntimeWarning, stacklevel=3)

@@ -105,7 +105,7 @@ def native_path() -> str:
     """Where the module of the plain calls lies that fits this interpreter, its torch and these sources."""
     import torch
     text = hashlib.sha256()
-    for path in (HEADER, os.path.join(CSRC, "native.cpp")):
+    for path in (HEADER, os.path.join(CSRC, "native.cpp"), __file__):  # (and the flags it is built with)
         if os.path.exists(path):
             with open(path, "rb") as f:
                 text.update(f.read())
